@@ -15,6 +15,10 @@ AF_Q4_0, AF_Q8_0, AF_Q4_K, AF_Q5_K, AF_Q6_K = 2, 8, 12, 13, 14
 AF_F32, AF_F16, AF_KV_Q8_0, AF_KV_Q4_0 = 0, 1, 2, 3
 WTYPE = {"q4_0": AF_Q4_0, "q8_0": AF_Q8_0, "q4_k": AF_Q4_K, "q5_k": AF_Q5_K, "q6_k": AF_Q6_K}
 KVTYPE = {"f32": AF_F32, "f16": AF_F16, "q8_0": AF_KV_Q8_0, "q4_0": AF_KV_Q4_0}
+AF_ROPE_INTERLEAVED, AF_ROPE_HALF = 0, 1
+AF_ROPE_NONE, AF_ROPE_LINEAR, AF_ROPE_NTK, AF_ROPE_YARN = range(4)
+ROPE_LAYOUT = {"interleaved": AF_ROPE_INTERLEAVED, "half": AF_ROPE_HALF}
+ROPE_SCALING = {"none": AF_ROPE_NONE, "linear": AF_ROPE_LINEAR, "ntk": AF_ROPE_NTK, "yarn": AF_ROPE_YARN}
 STATUS_NAMES = {0: "AF_OK", 1: "AF_EINVAL", 2: "AF_ERANGE", 3: "AF_ENOMEM", 4: "AF_ECUDA", 5: "AF_ETIMEOUT",
                 6: "AF_ENOTIMPL"}
 
@@ -36,6 +40,11 @@ class af_config(ctypes.Structure):
 class af_weights(ctypes.Structure):
     _fields_ = [("layer_blob", ctypes.POINTER(ctypes.c_void_p)), ("token_embd", ctypes.c_void_p),
                 ("output_norm", ctypes.c_void_p), ("output", ctypes.c_void_p)]
+
+
+class af_rope_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("head_dim", "rot_dim", "layout", "scaling", "native_ctx")] + \
+               [(n, ctypes.c_float) for n in ("base", "factor", "turns_low", "turns_high", "magnitude")]
 
 
 _lib = None
@@ -87,6 +96,14 @@ def lib():
         f32 = ctypes.c_float
         L.af_sample.argtypes = [vp, i32, vp, i32, f32, f32, f32, f32, vp, vp]
         L.af_model_sample.argtypes = [vp, vp, vp, i32, f32, f32, f32, f32, vp]
+        i64 = ctypes.c_int64
+        L.af_rope.argtypes = [P(af_rope_config), vp, i64, vp, i64, i32, i32, i32, vp, i32, vp]
+        L.af_kv_write.argtypes = [vp, vp, i64, i32, vp, i32, vp, vp, vp, vp, i32, i32, i32, i32, vp]
+        L.af_kv_read.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, i32, vp, vp, i64, vp]
+        L.af_tree_mask.argtypes = [vp, i32, i32, vp, vp, vp]
+        L.af_attention_tree_workspace.argtypes = [i32] * 6
+        L.af_attention_tree_workspace.restype = u64
+        L.af_attention_tree.argtypes = [vp, i64, vp, vp, vp, vp] + [i32] * 7 + [vp, vp, u64, vp, i64, vp]
         _lib = L
     return _lib
 
@@ -274,6 +291,50 @@ def af_model_sample(m, logits_dev, recent_dev, n_recent: int, repeat_penalty: fl
     check(lib().af_model_sample(m, _ptr(logits_dev), _ptr(recent_dev), n_recent, repeat_penalty, temperature, top_p,
                                 u, ctypes.byref(out) if want_token else None))
     return out.value if want_token else None
+
+
+def rope_config(head_dim: int, rot_dim: int, layout: str = "interleaved", base: float = 10000.0, scaling: str = "none",
+                factor: float = 1.0, native_ctx: int = 0, turns_low: float = 1.0, turns_high: float = 32.0,
+                magnitude: float = 1.0) -> af_rope_config:
+    return af_rope_config(head_dim, rot_dim, ROPE_LAYOUT[layout], ROPE_SCALING[scaling], native_ctx, base, factor,
+                          turns_low, turns_high, magnitude)
+
+
+def af_rope(cfg: af_rope_config, x_dev, ldx: int, y_dev, ldy: int, dtype: int, n: int, n_heads: int, pos_dev,
+            pos0: int = 0, stream=None):
+    return check(lib().af_rope(ctypes.byref(cfg), _ptr(x_dev), ldx, _ptr(y_dev), ldy, dtype, n, n_heads, _ptr(pos_dev),
+                               pos0, _stream(stream)))
+
+
+def af_kv_write(k_dev, v_dev, ld: int, n: int, slots_dev, slot0: int, k_cache, k_scales, v_cache, v_scales,
+                kv_dtype: int, n_kv_heads: int, head_dim: int, ctx: int, stream=None):
+    return check(lib().af_kv_write(_ptr(k_dev), _ptr(v_dev), ld, n, _ptr(slots_dev), slot0, _ptr(k_cache),
+                                   _ptr(k_scales), _ptr(v_cache), _ptr(v_scales), kv_dtype, n_kv_heads, head_dim, ctx,
+                                   _stream(stream)))
+
+
+def af_kv_read(k_cache, k_scales, v_cache, v_scales, kv_dtype: int, n_kv_heads: int, head_dim: int, ctx: int, n: int,
+               slots_dev, slot0: int, k_dev, v_dev, ld: int, stream=None):
+    return check(lib().af_kv_read(_ptr(k_cache), _ptr(k_scales), _ptr(v_cache), _ptr(v_scales), kv_dtype, n_kv_heads,
+                                  head_dim, ctx, n, _ptr(slots_dev), slot0, _ptr(k_dev), _ptr(v_dev), ld,
+                                  _stream(stream)))
+
+
+def af_tree_mask(parent_dev, n: int, pos0: int, mask_dev, pos_dev=None, stream=None):
+    return check(lib().af_tree_mask(_ptr(parent_dev), n, pos0, _ptr(mask_dev), _ptr(pos_dev), _stream(stream)))
+
+
+def af_attention_tree_workspace(kv_dtype: int, n_heads: int, n_kv_heads: int, head_dim: int, n_past: int,
+                                n: int) -> int:
+    return int(lib().af_attention_tree_workspace(kv_dtype, n_heads, n_kv_heads, head_dim, n_past, n))
+
+
+def af_attention_tree(q_dev, ldq: int, k_cache, k_scales, v_cache, v_scales, kv_dtype: int, n_heads: int,
+                      n_kv_heads: int, head_dim: int, ctx: int, n_past: int, n: int, mask_dev, ws_dev, ws_bytes: int,
+                      out_dev, ldo: int, stream=None):
+    return check(lib().af_attention_tree(_ptr(q_dev), ldq, _ptr(k_cache), _ptr(k_scales), _ptr(v_cache),
+                                         _ptr(v_scales), kv_dtype, n_heads, n_kv_heads, head_dim, ctx, n_past, n,
+                                         _ptr(mask_dev), _ptr(ws_dev), ws_bytes, _ptr(out_dev), ldo, _stream(stream)))
 
 
 def af_last_error() -> str:

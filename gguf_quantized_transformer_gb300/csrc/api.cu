@@ -13,6 +13,7 @@
 // The decode step after its first kernel is captured once into a CUDA graph
 // (position and token are read from device memory, so the graph is reused).
 #include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <new>
 #include <cstdio>
@@ -21,6 +22,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "draft.cuh"
 
 using namespace af;
 
@@ -1039,6 +1041,198 @@ int af_model_sample(af_model* m, const float* logits_dev, const int32_t* recent_
         CK(cudaMemcpyAsync(token_host, &m->st->next_token, 4, cudaMemcpyDeviceToHost, m->s));
         CK(cudaStreamSynchronize(m->s));
     }
+    return AF_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- drafted tokens: positions, cache rows, tree attention
+
+namespace {
+
+bool finite_pos(float x) { return x > 0.f && x <= 3.4e38f; }
+
+int check_rope(const af_rope_config* c) {
+    if (c->head_dim <= 0 || c->head_dim % 2) return fail(AF_EINVAL, "head_dim %d must be even", c->head_dim);
+    if (c->head_dim > 2 * kRopeMaxPairs) return fail(AF_ENOTIMPL, "head_dim %d above %d", c->head_dim, 2 * kRopeMaxPairs);
+    if (c->rot_dim < 2 || c->rot_dim > c->head_dim || c->rot_dim % 2)
+        return fail(AF_EINVAL, "rot_dim %d must be even and in [2, head_dim]", c->rot_dim);
+    if (c->layout != AF_ROPE_INTERLEAVED && c->layout != AF_ROPE_HALF) return fail(AF_EINVAL, "bad layout");
+    if (c->scaling < AF_ROPE_NONE || c->scaling > AF_ROPE_YARN) return fail(AF_EINVAL, "bad scaling");
+    if (!finite_pos(c->base) || c->base <= 1.f) return fail(AF_EINVAL, "base must be a finite number above 1");
+    if (c->scaling != AF_ROPE_NONE && !finite_pos(c->factor)) return fail(AF_EINVAL, "factor must be finite and > 0");
+    if (c->scaling == AF_ROPE_NTK && c->rot_dim < 4) return fail(AF_EINVAL, "AF_ROPE_NTK needs rot_dim >= 4");
+    if (c->scaling == AF_ROPE_YARN &&
+        (c->native_ctx <= 0 || !(c->turns_low >= 0.f) || !finite_pos(c->turns_high) || c->turns_high <= c->turns_low))
+        return fail(AF_EINVAL, "AF_ROPE_YARN needs native_ctx > 0 and 0 <= turns_low < turns_high");
+    if (c->magnitude != 0.f && !finite_pos(c->magnitude)) return fail(AF_EINVAL, "magnitude must be finite and > 0 (0 = 1)");
+    return AF_OK;
+}
+
+// Fractions of a turn per position, 64-bit fixed point.
+void rope_turns(const af_rope_config* c, RopeTurns& t) {
+    const double two_pi = 6.283185307179586476925286766559, R = c->rot_dim, s = c->factor;
+    double base = c->base;
+    if (c->scaling == AF_ROPE_NTK) base *= std::pow(s, R / (R - 2));
+    const double ratio = std::pow(base, -2.0 / R);
+    double f = 1.0;  // base^(-2i / R)
+    for (int i = 0; i < c->rot_dim / 2; i++, f *= ratio) {
+        double g = f;
+        if (c->scaling == AF_ROPE_LINEAR) g = f / s;
+        if (c->scaling == AF_ROPE_YARN) {
+            const double lo = c->turns_low, hi = c->turns_high;
+            const double w = std::min(1.0, std::max(0.0, (c->native_ctx * f / two_pi - lo) / (hi - lo)));
+            g = f * w + f / s * (1.0 - w);
+        }
+        g /= two_pi;
+        g -= std::floor(g);  // whole turns per position (factor < 1) change nothing
+        t.turn[i] = (uint64_t)std::ldexp(g, 64 - 1) << 1;
+    }
+}
+
+// The cache arguments shared by af_kv_write, af_kv_read and af_attention_tree.
+int check_cache(const void* k, const void* ks, const void* v, const void* vs, int32_t type, int32_t KVH, int32_t D,
+                int32_t ctx, KvRows& c) {
+    if (!k || !v) return fail(AF_EINVAL, "null cache");
+    if (type != AF_F32 && type != AF_F16 && type != AF_KV_Q8_0 && type != AF_KV_Q4_0)
+        return fail(AF_EINVAL, "kv_dtype must be AF_F32, AF_F16, AF_KV_Q8_0 or AF_KV_Q4_0");
+    const bool quant = type == AF_KV_Q8_0 || type == AF_KV_Q4_0;
+    if (quant && (!ks || !vs)) return fail(AF_EINVAL, "a quantized cache needs its scales");
+    if (!quant && (ks || vs)) return fail(AF_EINVAL, "an fp32 or fp16 cache has no scales");
+    if (KVH <= 0 || D <= 0 || ctx <= 0) return fail(AF_EINVAL, "sizes must be positive");
+    if (D % 32 || D > 256) return fail(AF_ENOTIMPL, "head_dim %d must be a multiple of 32 up to 256", D);
+    if ((int64_t)KVH * D > (1 << 20)) return fail(AF_ENOTIMPL, "n_kv_heads * head_dim above 2^20");
+    if (((uintptr_t)k | (uintptr_t)v | (uintptr_t)ks | (uintptr_t)vs) & 15) return fail(AF_EINVAL, "unaligned cache");
+    c.k = const_cast<void*>(k);
+    c.v = const_cast<void*>(v);
+    c.ks = (__half*)const_cast<void*>(ks);
+    c.vs = (__half*)const_cast<void*>(vs);
+    c.type = type;
+    c.KVH = KVH;
+    c.D = D;
+    c.ctx = ctx;
+    return AF_OK;
+}
+
+int check_rows(const void* k, const void* v, int64_t ld, int32_t n, const void* slots, int32_t slot0, const KvRows& c) {
+    if (!k || !v) return fail(AF_EINVAL, "null rows");
+    if (((uintptr_t)k | (uintptr_t)v) & 15) return fail(AF_EINVAL, "unaligned rows");
+    if ((uintptr_t)slots & 3) return fail(AF_EINVAL, "unaligned slots");
+    if (ld < (int64_t)c.KVH * c.D || ld % 4) return fail(AF_EINVAL, "ld must be a multiple of 4 >= n_kv_heads * head_dim");
+    if (n < 0) return fail(AF_ERANGE, "n=%d", n);
+    if (!slots && (slot0 < 0 || (int64_t)slot0 + n > c.ctx))
+        return fail(AF_ERANGE, "slots %d..%lld outside the cache (%d slots)", slot0, (long long)slot0 + n - 1, c.ctx);
+    return AF_OK;
+}
+
+int check_tree(int32_t type, int32_t H, int32_t KVH, int32_t D, int32_t past, int32_t n) {
+    if (type != AF_F32 && type != AF_F16 && type != AF_KV_Q8_0 && type != AF_KV_Q4_0) return fail(AF_EINVAL, "bad kv_dtype");
+    if (H <= 0 || KVH <= 0 || D <= 0) return fail(AF_EINVAL, "sizes must be positive");
+    if (H % KVH) return fail(AF_EINVAL, "n_heads must be a multiple of n_kv_heads");
+    if ((D != 64 && D != 128) || H / KVH > 64 || H > 65535)
+        return fail(AF_ENOTIMPL, "tree attention supports head_dim 64 / 128 and groups up to 64");
+    if (n < 1 || n > kTreeMax) return fail(AF_ERANGE, "n=%d outside [1, %d]", n, kTreeMax);
+    if (past < 0 || past > INT32_MAX - kTreeMax) return fail(AF_ERANGE, "n_past=%d", past);
+    return AF_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int af_rope(const af_rope_config* cfg, const void* x_dev, int64_t ldx, void* y_dev, int64_t ldy, int32_t dtype,
+            int32_t n, int32_t n_heads, const int32_t* pos_dev, int32_t pos0, void* stream) {
+    if (!cfg || !x_dev || !y_dev) return fail(AF_EINVAL, "null argument");
+    if (int rc = check_rope(cfg)) return rc;
+    if (dtype != AF_F32 && dtype != AF_F16) return fail(AF_EINVAL, "dtype must be AF_F32 or AF_F16");
+    if (n_heads <= 0 || n_heads > (1 << 20)) return fail(AF_EINVAL, "n_heads %d", n_heads);
+    if (n < 0) return fail(AF_ERANGE, "n=%d", n);
+    const int64_t w = (int64_t)n_heads * cfg->head_dim;
+    if (ldx < w || ldy < w) return fail(AF_EINVAL, "ldx and ldy must be at least n_heads * head_dim");
+    const uintptr_t es = dtype == AF_F32 ? 4 : 2;
+    if (((uintptr_t)x_dev | (uintptr_t)y_dev) & (es - 1) || (uintptr_t)pos_dev & 3) return fail(AF_EINVAL, "unaligned pointer");
+    if (x_dev == y_dev && ldx != ldy) return fail(AF_EINVAL, "in place needs ldx == ldy");
+    if (!pos_dev && n > 0 && (int64_t)pos0 + n - 1 > INT32_MAX) return fail(AF_ERANGE, "positions past 2^31");
+    if (!n) return AF_OK;
+    RopeTurns t;
+    rope_turns(cfg, t);
+    RopeArgs a;
+    a.x = x_dev;
+    a.y = y_dev;
+    a.ldx = ldx;
+    a.ldy = ldy;
+    a.f16 = dtype == AF_F16;
+    a.n = n;
+    a.heads = n_heads;
+    a.D = cfg->head_dim;
+    a.R = cfg->rot_dim;
+    a.half = cfg->layout == AF_ROPE_HALF;
+    a.pos = pos_dev;
+    a.pos0 = pos0;
+    a.mag = cfg->magnitude != 0.f ? cfg->magnitude : 1.f;
+    CK(launch_rope(a, t, (cudaStream_t)stream));
+    return AF_OK;
+}
+
+int af_kv_write(const float* k_dev, const float* v_dev, int64_t ld, int32_t n, const int32_t* slots_dev, int32_t slot0,
+                void* k_cache, void* k_scales, void* v_cache, void* v_scales, int32_t kv_dtype, int32_t KVH, int32_t D,
+                int32_t ctx, void* stream) {
+    KvRows c;
+    if (int rc = check_cache(k_cache, k_scales, v_cache, v_scales, kv_dtype, KVH, D, ctx, c)) return rc;
+    if (int rc = check_rows(k_dev, v_dev, ld, n, slots_dev, slot0, c)) return rc;
+    if (n) CK(launch_kv_write(c, k_dev, v_dev, ld, n, slots_dev, slot0, (cudaStream_t)stream));
+    return AF_OK;
+}
+
+int af_kv_read(const void* k_cache, const void* k_scales, const void* v_cache, const void* v_scales, int32_t kv_dtype,
+               int32_t KVH, int32_t D, int32_t ctx, int32_t n, const int32_t* slots_dev, int32_t slot0, float* k_dev,
+               float* v_dev, int64_t ld, void* stream) {
+    KvRows c;
+    if (int rc = check_cache(k_cache, k_scales, v_cache, v_scales, kv_dtype, KVH, D, ctx, c)) return rc;
+    if (int rc = check_rows(k_dev, v_dev, ld, n, slots_dev, slot0, c)) return rc;
+    if (n) CK(launch_kv_read(c, n, slots_dev, slot0, k_dev, v_dev, ld, (cudaStream_t)stream));
+    return AF_OK;
+}
+
+int af_tree_mask(const int32_t* parent_dev, int32_t n, int32_t pos0, uint32_t* mask_dev, int32_t* pos_dev, void* stream) {
+    if (!parent_dev || !mask_dev) return fail(AF_EINVAL, "null argument");
+    if (((uintptr_t)parent_dev | (uintptr_t)mask_dev | (uintptr_t)pos_dev) & 3) return fail(AF_EINVAL, "unaligned pointer");
+    if (n < 1 || n > kTreeMax) return fail(AF_ERANGE, "n=%d outside [1, %d]", n, kTreeMax);
+    if (pos0 < 0 || pos0 > INT32_MAX - kTreeMax) return fail(AF_ERANGE, "pos0=%d", pos0);
+    CK(launch_tree_mask(parent_dev, n, pos0, mask_dev, pos_dev, (cudaStream_t)stream));
+    return AF_OK;
+}
+
+uint64_t af_attention_tree_workspace(int32_t kv_dtype, int32_t H, int32_t KVH, int32_t D, int32_t past, int32_t n) {
+    if (check_tree(kv_dtype, H, KVH, D, past, n)) return 0;
+    return attn_tree_ws_bytes(H, KVH, D, kv_dtype, past, n);
+}
+
+int af_attention_tree(const float* q_dev, int64_t ldq, const void* k_cache, const void* k_scales, const void* v_cache,
+                      const void* v_scales, int32_t kv_dtype, int32_t H, int32_t KVH, int32_t D, int32_t ctx,
+                      int32_t past, int32_t n, const uint32_t* mask_dev, void* ws_dev, uint64_t ws_bytes, float* out_dev,
+                      int64_t ldo, void* stream) {
+    if (!q_dev || !mask_dev || !out_dev) return fail(AF_EINVAL, "null argument");
+    if (int rc = check_tree(kv_dtype, H, KVH, D, past, n)) return rc;
+    TreeArgs a;
+    if (int rc = check_cache(k_cache, k_scales, v_cache, v_scales, kv_dtype, KVH, D, ctx, a.c)) return rc;
+    if ((int64_t)past + n > ctx) return fail(AF_ERANGE, "slots 0..%lld outside the cache (%d slots)", (long long)past + n - 1, ctx);
+    if (((uintptr_t)q_dev | (uintptr_t)out_dev) & 15 || (uintptr_t)mask_dev & 3) return fail(AF_EINVAL, "unaligned pointer");
+    if (ldq < (int64_t)H * D || ldo < (int64_t)H * D || ldq % 4 || ldo % 4)
+        return fail(AF_EINVAL, "ldq and ldo must be multiples of 4 >= n_heads * head_dim");
+    const size_t need = attn_tree_ws_bytes(H, KVH, D, kv_dtype, past, n);
+    if (need && (!ws_dev || (uintptr_t)ws_dev & 255 || ws_bytes < need))
+        return fail(AF_EINVAL, "needs a 256-byte aligned workspace of %zu bytes", need);
+    a.q = q_dev;
+    a.ldq = ldq;
+    a.H = H;
+    a.past = past;
+    a.n = n;
+    a.mask = mask_dev;
+    a.out = out_dev;
+    a.ldo = ldo;
+    a.ws = (float*)ws_dev;
+    CK(launch_attn_tree(a, (cudaStream_t)stream));
     return AF_OK;
 }
 

@@ -1,0 +1,57 @@
+// Launchers of the drafted-tree operators (rotary positions, cache write and read, tree attention).
+#pragma once
+#include "common.cuh"
+
+namespace af {
+
+// ---- rotary positions (rope.cu)
+constexpr int kRopeMaxPairs = 128;  // head_dim <= 256
+
+// Angle per position of each pair as a fraction of a turn in 64-bit fixed point: position times turn, wrapped
+// to 64 bits, is the angle modulo one turn, for any int32 position and without fp64 on the device.
+struct RopeTurns {
+    uint64_t turn[kRopeMaxPairs];
+};
+struct RopeArgs {
+    const void* x = nullptr;
+    void* y = nullptr;
+    int64_t ldx = 0, ldy = 0;
+    int f16 = 0, n = 0, heads = 0, D = 0, R = 0, half = 0;
+    const int* pos = nullptr;  // nullable: position of row r is pos0 + r
+    int pos0 = 0;
+    float mag = 1.f;
+};
+cudaError_t launch_rope(const RopeArgs& a, const RopeTurns& t, cudaStream_t s);
+
+// ---- cache rows (kv_rows.cu)
+struct KvRows {
+    void* k = nullptr;  // [KVH][ctx][D] values, or codes (kv_code_bytes per slot)
+    void* v = nullptr;
+    __half* ks = nullptr;  // [KVH][ctx][D / 32] scales of a quantized cache
+    __half* vs = nullptr;
+    int type = 0;  // af_dtype
+    int KVH = 0, D = 0, ctx = 0;
+};
+cudaError_t launch_kv_write(const KvRows& c, const float* k, const float* v, int64_t ld, int n, const int* slots,
+                            int slot0, cudaStream_t s);
+cudaError_t launch_kv_read(const KvRows& c, int n, const int* slots, int slot0, float* k, float* v, int64_t ld,
+                           cudaStream_t s);
+
+// ---- tree attention (attn_tree.cu)
+constexpr int kTreeMax = 1024;  // nodes
+cudaError_t launch_tree_mask(const int* parent, int n, int pos0, unsigned* mask, int* pos, cudaStream_t s);
+
+struct TreeArgs {
+    const float* q = nullptr;
+    int64_t ldq = 0;
+    KvRows c;
+    int H = 0, past = 0, n = 0;
+    const unsigned* mask = nullptr;
+    float* out = nullptr;
+    int64_t ldo = 0;
+    float* ws = nullptr;
+};
+size_t attn_tree_ws_bytes(int H, int KVH, int D, int type, int past, int n);
+cudaError_t launch_attn_tree(const TreeArgs& a, cudaStream_t s);
+
+}  // namespace af

@@ -371,6 +371,105 @@ int af_sample(const float* logits_dev, int32_t n_vocab, const int32_t* recent_de
 int af_model_sample(af_model* m, const float* logits_dev, const int32_t* recent_dev, int32_t n_recent,
                     float repeat_penalty, float temperature, float top_p, float u, int32_t* token_host);
 
+/*
+ * Rotary positions on rows of heads, for queries and keys that are rotated outside af_model (drafted tokens at the
+ * position of their depth, cached keys that move).  Pairs (a, b) of a head's first rot_dim values,
+ *   y_a = m (x_a cos t - x_b sin t),  y_b = m (x_a sin t + x_b cos t),  t = pos * f_i,  i = 0 .. rot_dim / 2 - 1,
+ * (a, b) = (2i, 2i + 1) (AF_ROPE_INTERLEAVED, as in af_model) or (i, i + rot_dim / 2) (AF_ROPE_HALF); the values from
+ * rot_dim on are copied unchanged.  f_i = base^(-2i / rot_dim), for a context `factor` times native_ctx:
+ *   AF_ROPE_LINEAR  f_i / factor (af_model's yarn_scale, Shimmy v2.0 Architecture, "Extended Context")
+ *   AF_ROPE_NTK     the base becomes base * factor^(rot_dim / (rot_dim - 2)) (rot_dim >= 4)
+ *   AF_ROPE_YARN    by parts: with r = native_ctx f_i / 2 pi turns over the native context and
+ *                   w = clamp((r - turns_low) / (turns_high - turns_low), 0, 1), f_i (w + (1 - w) / factor)
+ */
+typedef enum af_rope_layout { AF_ROPE_INTERLEAVED = 0, AF_ROPE_HALF = 1 } af_rope_layout;
+typedef enum af_rope_scaling { AF_ROPE_NONE = 0, AF_ROPE_LINEAR = 1, AF_ROPE_NTK = 2, AF_ROPE_YARN = 3 } af_rope_scaling;
+typedef struct af_rope_config {
+    int32_t head_dim;   /* even, <= 256 */
+    int32_t rot_dim;    /* even, 2 .. head_dim */
+    int32_t layout;     /* af_rope_layout */
+    int32_t scaling;    /* af_rope_scaling */
+    int32_t native_ctx; /* AF_ROPE_YARN */
+    float base;         /* > 1 */
+    float factor;       /* > 0 (ignored by AF_ROPE_NONE) */
+    float turns_low;    /* AF_ROPE_YARN: 0 <= turns_low < turns_high (1 and 32 in the method's paper) */
+    float turns_high;
+    float magnitude;    /* m; 0 = 1 (AF_ROPE_YARN's paper: 0.1 ln(factor) + 1) */
+} af_rope_config;
+
+/*
+ *   x_dev   [n] rows of n_heads * head_dim values of dtype (AF_F32, or AF_F16 computed in fp32 and rounded once),
+ *           consecutive rows ldx values apart (ldx >= n_heads * head_dim: the q and k heads of a fused projection
+ *           are one call; the heads of a cache are one row each with n_heads = 1)
+ *   y_dev   the result, rows ldy values apart; may be x_dev itself with ldy == ldx, and overlaps it in no other way
+ *   pos_dev int32 [n], any value (a negative one rotates back); NULL: row r is at pos0 + r (pos0 + n - 1 < 2^31)
+ * The angle is exact modulo a turn to 2^-33 of a turn at a million positions (2^-22 at 2^31).  Asynchronous on `stream`, allocates
+ * nothing, can be captured.  Vectors of 16 bytes are moved where rows, rot_dim and pointers allow it.
+ * n = 0 does nothing.  Errors: AF_EINVAL, AF_ERANGE, AF_ENOTIMPL (head_dim > 256), AF_ECUDA.
+ */
+int af_rope(const af_rope_config* cfg, const void* x_dev, int64_t ldx, void* y_dev, int64_t ldy, int32_t dtype,
+            int32_t n, int32_t n_heads, const int32_t* pos_dev, int32_t pos0, void* stream);
+
+/*
+ * Rows of keys and values into a caller's cache of any type, quantized as they are written, and slots of it back
+ * as fp32 rows.  The cache of one layer, K and V each:
+ *   AF_F32, AF_F16          [n_kv_heads][ctx][head_dim] values; k_scales = v_scales = NULL
+ *   AF_KV_Q8_0, AF_KV_Q4_0  codes [n_kv_heads][ctx][head_dim or head_dim / 2 bytes] and fp16 scales
+ *                           [n_kv_heads][ctx][head_dim / 32], as af_model_kv_store's: every slot is quantized at
+ *                           once from the fp32 values given here (no fp16 window)
+ * The decisions of the quantizers are those of exact arithmetic on the fp32 values.  A block of 32 that holds a NaN,
+ * or whose scale overflows fp16, reads back as NaN.  Slots written from values that af_kv_read returned hold the same
+ * values again (scales below fp16's normal range excepted), so a read and a write move slots.
+ *   k_dev, v_dev  fp32 rows [n] of n_kv_heads * head_dim values, ld apart (16-byte aligned, ld a multiple of 4)
+ *   slots_dev     int32 [n]: the slot of each row; a row whose slot is outside [0, ctx) is skipped (af_kv_read
+ *                 leaves its output row as it was).  Of rows with the same slot the last is written.  NULL: row r
+ *                 is slot slot0 + r, inside the cache (AF_ERANGE)
+ * head_dim: a multiple of 32 up to 256.  All device pointers but slots_dev are 16-byte aligned.  Asynchronous on
+ * `stream`, allocate nothing, can be captured.  n = 0 does nothing.
+ * Errors: AF_EINVAL, AF_ERANGE, AF_ENOTIMPL (head_dim), AF_ECUDA.
+ */
+int af_kv_write(const float* k_dev, const float* v_dev, int64_t ld, int32_t n, const int32_t* slots_dev, int32_t slot0,
+                void* k_cache, void* k_scales, void* v_cache, void* v_scales, int32_t kv_dtype, int32_t n_kv_heads,
+                int32_t head_dim, int32_t ctx, void* stream);
+int af_kv_read(const void* k_cache, const void* k_scales, const void* v_cache, const void* v_scales, int32_t kv_dtype,
+               int32_t n_kv_heads, int32_t head_dim, int32_t ctx, int32_t n, const int32_t* slots_dev, int32_t slot0,
+               float* k_dev, float* v_dev, int64_t ld, void* stream);
+
+/*
+ * The mask and the positions of a tree of n drafted tokens (1 <= n <= 1024), once per tree for all layers:
+ *   parent_dev  int32 [n]: the node a node follows, an earlier one, or -1 for the last accepted token (a value that
+ *               is not an earlier node counts as -1)
+ *   mask_dev    uint32 [n][(n + 31) / 32]: bit j % 32 of word j / 32 of row i is set where j is i or an ancestor
+ *   pos_dev     int32 [n] (nullable): pos0 + the node's depth (0 for a child of the last accepted token)
+ * Asynchronous on `stream`, allocates nothing, can be captured.  Errors: AF_EINVAL, AF_ERANGE, AF_ECUDA.
+ */
+int af_tree_mask(const int32_t* parent_dev, int32_t n, int32_t pos0, uint32_t* mask_dev, int32_t* pos_dev,
+                 void* stream);
+
+/*
+ * Attention for a tree of drafted tokens over a caller's cache: every node sees slots 0..n_past-1, and of the slots
+ * n_past..n_past+n-1, where node j's key and value are (af_kv_write with slot0 = n_past), those whose bit its mask
+ * row has set; softmax(q K^T / sqrt(head_dim)) V over what it sees, GQA group = n_heads / n_kv_heads.
+ *   q_dev     fp32 [n] rows of n_heads * head_dim values (rotated), ldq apart
+ *   cache     as af_kv_write's; slots from n_past + n on are not read
+ *   mask_dev  uint32 [n][(n + 31) / 32] as af_tree_mask writes it, or any other: a row that sees nothing (n_past = 0
+ *             and no bit set) gives zeros, and what a hidden slot holds (NaN, infinities) reaches no row it is
+ *             hidden from
+ *   ws_dev    scratch of at least af_attention_tree_workspace bytes (NULL where that is 0), 256-byte aligned, of any
+ *             contents; calls that may overlap in time need scratch of their own
+ *   out_dev   fp32 [n] rows, ldo apart
+ * 1 <= n <= 1024, 0 <= n_past, n_past + n <= ctx; head_dim 64 or 128, any whole group up to 64.  Pointers are 16-byte
+ * aligned (mask_dev: 4), ldq and ldo multiples of 4.  Asynchronous on `stream`, allocates nothing, can be captured
+ * (the first call on a device loads the kernels: make it before a capture).
+ * Errors: AF_EINVAL, AF_ERANGE, AF_ENOTIMPL, AF_ECUDA.
+ */
+uint64_t af_attention_tree_workspace(int32_t kv_dtype, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                                     int32_t n_past, int32_t n);
+int af_attention_tree(const float* q_dev, int64_t ldq, const void* k_cache, const void* k_scales, const void* v_cache,
+                      const void* v_scales, int32_t kv_dtype, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                      int32_t ctx, int32_t n_past, int32_t n, const uint32_t* mask_dev, void* ws_dev, uint64_t ws_bytes,
+                      float* out_dev, int64_t ldo, void* stream);
+
 /* Thread-local message for the last failed call on this thread ("" if none). */
 const char* af_last_error(void);
 

@@ -1,0 +1,111 @@
+"""Refusals of the drafted-tree operators (af_rope, af_kv_write, af_kv_read, af_tree_mask, af_attention_tree): every
+check runs on the host before anything is launched, so no GPU is needed.  Pointers are dummies, never dereferenced."""
+import ctypes
+
+import pytest
+
+P = 4096  # an aligned address nothing reads
+
+
+def _af():
+    import gguf_quantized_transformer_gb300 as af
+    af.build()
+    return af
+
+
+def _rope(L, af, cfg=None, x=P, y=P, ldx=1024, ldy=1024, dtype=0, n=4, heads=8, pos=P, pos0=0, **kw):
+    base = dict(head_dim=128, rot_dim=128, layout="interleaved", base=10000.0)
+    base.update(kw)
+    c = cfg or af.rope_config(**base)
+    return L.af_rope(ctypes.byref(c), x, ldx, y, ldy, dtype, n, heads, pos, pos0, None)
+
+
+def test_rope_refusals():
+    af = _af()
+    L = af.lib()
+    E, R, N = af.AF_EINVAL, af.AF_ERANGE, af.AF_ENOTIMPL
+    assert L.af_rope(None, P, 1024, P, 1024, 0, 4, 8, P, 0, None) == E
+    assert _rope(L, af, x=None) == E and _rope(L, af, y=None) == E
+    assert _rope(L, af, head_dim=127) == E and _rope(L, af, head_dim=258, rot_dim=2) == N
+    assert _rope(L, af, rot_dim=0) == E and _rope(L, af, rot_dim=130) == E and _rope(L, af, rot_dim=63) == E
+    assert _rope(L, af, base=1.0) == E and _rope(L, af, base=float("nan")) == E and _rope(L, af, base=float("inf")) == E
+    assert _rope(L, af, scaling="linear", factor=0.0) == E and _rope(L, af, scaling="linear", factor=float("inf")) == E
+    assert _rope(L, af, scaling="ntk", rot_dim=2, factor=2.0) == E
+    assert _rope(L, af, scaling="yarn", factor=2.0, native_ctx=0) == E
+    assert _rope(L, af, scaling="yarn", factor=2.0, native_ctx=64, turns_low=32.0, turns_high=32.0) == E
+    assert _rope(L, af, magnitude=-1.0) == E and _rope(L, af, magnitude=float("nan")) == E
+    c = af.rope_config(128, 128)
+    c.layout = 2
+    assert _rope(L, af, cfg=c) == E
+    c = af.rope_config(128, 128)
+    c.scaling = 4
+    assert _rope(L, af, cfg=c) == E
+    assert _rope(L, af, dtype=2) == E and _rope(L, af, heads=0) == E and _rope(L, af, n=-1) == R
+    assert _rope(L, af, ldx=1023) == E and _rope(L, af, ldy=1000) == E
+    assert _rope(L, af, x=P + 2) == E and _rope(L, af, pos=P + 1) == E and _rope(L, af, dtype=1, y=P + 1) == E
+    assert _rope(L, af, ldy=2048) == E  # in place with another stride
+    assert _rope(L, af, pos=None, pos0=2 ** 31 - 4, n=5) == R
+    assert _rope(L, af, n=0) == af.AF_OK
+
+
+def _rows(L, af, write, k=P, v=P, ld=1024, n=4, slots=None, slot0=0, kc=P, ks=None, vc=P, vs=None, t=0, kvh=8, d=128,
+          ctx=64):
+    if write:
+        return L.af_kv_write(k, v, ld, n, slots, slot0, kc, ks, vc, vs, t, kvh, d, ctx, None)
+    return L.af_kv_read(kc, ks, vc, vs, t, kvh, d, ctx, n, slots, slot0, k, v, ld, None)
+
+
+@pytest.mark.parametrize("write", [True, False])
+def test_kv_rows_refusals(write):
+    af = _af()
+    L = af.lib()
+    E, R, N = af.AF_EINVAL, af.AF_ERANGE, af.AF_ENOTIMPL
+    def call(**kw):
+        return _rows(L, af, write, **kw)
+    assert call(k=None) == E and call(v=None) == E and call(kc=None) == E and call(vc=None) == E
+    assert call(t=7) == E and call(t=-1) == E
+    assert call(t=af.AF_KV_Q8_0) == E and call(t=af.AF_KV_Q8_0, ks=P) == E and call(t=0, ks=P, vs=P) == E
+    assert call(kvh=0) == E and call(d=0) == E and call(ctx=0) == E
+    assert call(d=48) == N and call(d=288, ld=4096) == N and call(kvh=1 << 14, ld=1 << 30) == N
+    assert call(ld=1023) == E and call(ld=1026) == E and call(ld=1020) == E
+    assert call(k=P + 4) == E and call(vc=P + 8) == E and call(t=af.AF_KV_Q4_0, ks=P + 2, vs=P) == E
+    assert call(slots=P + 2) == E
+    assert call(n=-1) == R and call(n=65) == R and call(slot0=-1) == R and call(slot0=61) == R
+    assert call(slot0=2 ** 31 - 1) == R
+    assert call(n=0) == af.AF_OK and call(n=0, slots=P) == af.AF_OK
+
+
+def test_tree_refusals():
+    af = _af()
+    L = af.lib()
+    E, R, N = af.AF_EINVAL, af.AF_ERANGE, af.AF_ENOTIMPL
+    assert L.af_tree_mask(None, 4, 0, P, P, None) == E and L.af_tree_mask(P, 4, 0, None, P, None) == E
+    assert L.af_tree_mask(P, 0, 0, P, P, None) == R and L.af_tree_mask(P, 1025, 0, P, P, None) == R
+    assert L.af_tree_mask(P, 4, -1, P, P, None) == R and L.af_tree_mask(P, 4, 2 ** 31 - 1, P, P, None) == R
+    assert L.af_tree_mask(P + 2, 4, 0, P, P, None) == E
+
+    def call(q=P, ldq=4096, kc=P, ks=None, vc=P, vs=None, t=1, h=32, kvh=8, d=128, ctx=64, past=10, n=4, mask=P, ws=P,
+             wsb=1 << 40, out=P, ldo=4096):
+        return L.af_attention_tree(q, ldq, kc, ks, vc, vs, t, h, kvh, d, ctx, past, n, mask, ws, wsb, out, ldo, None)
+    assert call(q=None) == E and call(mask=None) == E and call(out=None) == E and call(kc=None) == E
+    assert call(t=5) == E and call(t=2) == E and call(t=2, ks=P) == E and call(t=1, ks=P, vs=P) == E
+    assert call(h=0) == E and call(kvh=0) == E and call(h=30) == E and call(d=-1) == E
+    assert call(d=96) == N and call(d=256) == N and call(h=520, kvh=8, ldq=1 << 20, ldo=1 << 20) == N
+    assert call(n=0) == R and call(n=1025) == R and call(past=-1) == R and call(past=61) == R
+    assert call(past=2 ** 31 - 1) == R
+    assert call(q=P + 4) == E and call(out=P + 8) == E and call(mask=P + 1) == E and call(vc=P + 4) == E
+    assert call(ldq=4095) == E and call(ldq=4098) == E and call(ldo=4092) == E
+    ws = af.af_attention_tree_workspace(af.AF_F16, 32, 8, 128, 4096, 64)
+    if ws:
+        assert call(ctx=8192, past=4096, n=64, wsb=ws - 1) == E and "workspace" in af.af_last_error()
+        assert call(ctx=8192, past=4096, n=64, ws=None) == E and call(ctx=8192, past=4096, n=64, ws=P + 16) == E
+    assert af.af_attention_tree_workspace(af.AF_F16, 32, 8, 96, 4096, 64) == 0
+
+
+def test_workspace_covers_the_documented_range():
+    af = _af()
+    for t in (af.AF_F32, af.AF_F16, af.AF_KV_Q8_0, af.AF_KV_Q4_0):
+        for h, kvh, d in ((1, 1, 64), (8, 4, 64), (32, 8, 128), (64, 1, 128), (40, 5, 128)):
+            for past in (0, 1, 31, 4096, 30720, 1 << 20):
+                for n in (1, 4, 64, 1024):
+                    assert 0 <= af.af_attention_tree_workspace(t, h, kvh, d, past, n) <= 256 << 20

@@ -1,0 +1,586 @@
+"""The drafted-tree operators against plain implementations in 64 bits: rotary positions, cache rows of every type,
+the mask of a tree and attention over it, and a run of them together."""
+import decimal
+
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+KV = ["f32", "f16", "q8_0", "q4_0"]
+
+
+@pytest.fixture(scope="module")
+def af():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import gguf_quantized_transformer_gb300 as af
+    af.build()
+    af.lib()
+    return af
+
+
+def _dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+# ---------------------------------------------------------------- rotary positions
+
+def turns(rot, base, scaling, factor, native, low=1, high=32):
+    """Turns per position of each pair as exact fractions (50 digits): (numerator, 10^40)."""
+    D = decimal.Decimal
+    decimal.getcontext().prec = 60
+    pi = D("3.14159265358979323846264338327950288419716939937510582097494")
+    b, s = D(float(np.float32(base))), D(float(np.float32(factor)))
+    if scaling == "ntk":
+        b *= (s.ln() * rot / (rot - 2)).exp()
+    out = []
+    for i in range(rot // 2):
+        f = (b.ln() * (-2 * i) / rot).exp()
+        if scaling == "linear":
+            f /= s
+        if scaling == "yarn":
+            w = min(D(1), max(D(0), (native * f / (2 * pi) - low) / (high - low)))
+            f = f * w + f / s * (1 - w)
+        out.append(int(f / (2 * pi) * 10 ** 40))
+    return out
+
+
+def rope_ref(x, pos, rot, layout, tn, mag):
+    """x [n, h, D] float64, pos python ints."""
+    one = 10 ** 40
+    y = x.copy()
+    for r, p in enumerate(pos):
+        for i, t in enumerate(tn):
+            a, b = (2 * i, 2 * i + 1) if layout == "interleaved" else (i, i + rot // 2)
+            th = 2 * np.pi * (((p * t) % one) / one)
+            c, s = mag * np.cos(th), mag * np.sin(th)
+            y[r, :, a] = x[r, :, a] * c - x[r, :, b] * s
+            y[r, :, b] = x[r, :, a] * s + x[r, :, b] * c
+    return y
+
+
+ROPE_CASES = [  # n, heads, D, rot, layout, scaling, positions
+    (1, 8, 64, 64, "interleaved", "none", [0]),
+    (3, 40, 128, 128, "interleaved", "none", [4096, 4097, 4097]),
+    (5, 3, 128, 96, "half", "yarn", [-512, 0, 1, 30720, 131071]),
+    (4, 2, 80, 32, "half", "linear", [7, 8, 9, 10]),
+    (4, 2, 80, 20, "half", "ntk", [1 << 20, -(1 << 20), 2 ** 31 - 1, -2 ** 31]),
+    (7, 1, 96, 94, "interleaved", "yarn", list(range(100, 107))),
+    (2, 5, 256, 256, "half", "none", [12345, 54321]),
+    (2, 1, 6, 2, "interleaved", "linear", [3, 1000003]),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("n,heads,D,rot,layout,scaling,pos", ROPE_CASES)
+@pytest.mark.parametrize("pad", [0, 3])
+def test_rope(af, n, heads, D, rot, layout, scaling, pos, dtype, pad):
+    rng = np.random.default_rng(n * D + rot)
+    ld = heads * D + pad
+    x = rng.standard_normal((n, ld)).astype(np.float32 if dtype == "f32" else np.float16)
+    mag = 1.25 if scaling == "yarn" else 1.0
+    cfg = af.rope_config(D, rot, layout, 500000.0, scaling, 4.5, 8192, magnitude=mag)
+    xd, pd = _dev(x), _dev(np.array(pos, np.int64).astype(np.int32))
+    y = torch.full((n, ld), 7.0, dtype=xd.dtype, device="cuda")
+    af.af_rope(cfg, xd, ld, y, ld, af.AF_F32 if dtype == "f32" else af.AF_F16, n, heads, pd)
+    got = y.cpu().numpy().astype(np.float64)
+    xr = x[:, :heads * D].astype(np.float64).reshape(n, heads, D)
+    ref = rope_ref(xr, pos, rot, layout, turns(rot, 500000.0, scaling, 4.5, 8192), mag)
+    # sin and cos: the argument's rounding (2^-24 of at most pi / 4) and at most two steps of the function's value,
+    # under 2^-22 together, the angle's |pos| 2^-53 turns, and three roundings of products and their sum
+    size = np.abs(xr).max(-1, keepdims=True) * mag
+    tol = 2 * size * (2.0 ** -22 + 2.0 ** -22 + 2 * np.pi * np.abs(np.array(pos, float))[:, None, None] * 2.0 ** -53)
+    if dtype == "f16":
+        tol = tol + np.abs(ref) * 2.0 ** -11 + 2.0 ** -25
+    g = got[:, :heads * D].reshape(n, heads, D)
+    assert np.all(np.abs(g - ref) <= tol), np.max(np.abs(g - ref) / tol)
+    assert np.array_equal(g[..., rot:], xr[..., rot:])   # the rest of the head is copied
+    assert np.all(got[:, heads * D:] == 7.0)             # and nothing behind the heads is written
+    # in place, and without positions in memory
+    af.af_rope(cfg, xd, ld, xd, ld, af.AF_F32 if dtype == "f32" else af.AF_F16, n, heads, pd)
+    assert torch.equal(xd[:, :heads * D], y[:, :heads * D])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_rope_counted_positions_and_inverse(af, dtype):
+    n, heads, D = 700, 8, 128
+    x = torch.randn(n, heads * D, device="cuda").to(torch.float32 if dtype == "f32" else torch.float16)
+    t = af.AF_F32 if dtype == "f32" else af.AF_F16
+    cfg = af.rope_config(D, D, "half", 10000.0)
+    y, z = torch.empty_like(x), torch.empty_like(x)
+    pos = torch.arange(50, 50 + n, dtype=torch.int32, device="cuda")
+    af.af_rope(cfg, x, heads * D, y, heads * D, t, n, heads, None, 50)
+    af.af_rope(cfg, x, heads * D, z, heads * D, t, n, heads, pos)
+    assert torch.equal(y, z)
+    af.af_rope(cfg, y, heads * D, z, heads * D, t, n, heads, -pos)
+    # two rotations, each off by at most 2^-20 of the pair's size (and a half-step of fp16)
+    tol = 4 * x.abs().max().item() * (2.0 ** -20 + (2.0 ** -11 if dtype == "f16" else 0))
+    assert (z.float() - x.float()).abs().max().item() <= tol
+
+
+def test_rope_equals_the_models_rotation(af):
+    """AF_ROPE_INTERLEAVED with linear scaling is the rotation the model's QKV epilogue applies."""
+    import oracle
+    D, base, scale = 128, 500000.0, 4.0
+    x = np.random.default_rng(3).standard_normal((1, D)).astype(np.float32)
+    for p in (0, 1, 4095, 30720):
+        cfg = af.rope_config(D, D, "interleaved", base, "linear", scale)
+        y = torch.empty(1, D, device="cuda")
+        af.af_rope(cfg, _dev(x), D, y, D, af.AF_F32, 1, 1, None, p)
+        th = np.array([p / scale / base ** (2 * i / D) for i in range(D // 2)])
+        a, b = x[0, 0::2].astype(np.float64), x[0, 1::2].astype(np.float64)
+        ref = np.empty(D)
+        ref[0::2], ref[1::2] = a * np.cos(th) - b * np.sin(th), a * np.sin(th) + b * np.cos(th)
+        assert np.max(np.abs(y.cpu().numpy()[0] - ref)) <= 2 * np.abs(x).max() * 2.0 ** -20
+    assert oracle is not None
+
+
+# ---------------------------------------------------------------- cache rows
+
+def quantize(x, t):
+    """Codes (integers) and fp16 scales of float32 blocks [..., 32], decided in float64."""
+    b = x.astype(np.float64)
+    if t == "q8_0":
+        d = (np.abs(b).max(-1) / 127).astype(np.float32).astype(np.float16)
+        with np.errstate(divide="ignore", invalid="ignore"):
+            r = b / d.astype(np.float64)[..., None]
+        q = np.sign(r) * np.floor(np.abs(r) + 0.5)
+        q = np.clip(q, -127, 127)
+    else:
+        m = np.take_along_axis(b, np.abs(b).argmax(-1)[..., None], -1)[..., 0]
+        d = (m / -8).astype(np.float32).astype(np.float16)
+        with np.errstate(divide="ignore", invalid="ignore"):
+            q = np.clip(np.floor(b / d.astype(np.float64)[..., None] + 8.5), 0, 15) - 8
+    return np.where(d[..., None] == 0, 0, q), d
+
+
+def held(x, t):
+    """What a cache of type t holds of float32 rows [..., D], as float64."""
+    if t == "f32":
+        return x.astype(np.float64)
+    if t == "f16":
+        return x.astype(np.float16).astype(np.float64)
+    q, d = quantize(x.reshape(*x.shape[:-1], -1, 32), t)
+    return (q * d.astype(np.float64)[..., None]).reshape(x.shape)
+
+
+def new_cache(t, kvh, ctx, d, fill=0):
+    """k, k_scales, v, v_scales filled with a byte value."""
+    def plane(*shape, dtype):
+        nbytes = int(np.prod(shape)) * np.dtype(dtype).itemsize
+        return torch.full((nbytes,), fill, dtype=torch.uint8, device="cuda").view(
+            {"f": torch.float32, "e": torch.float16, "B": torch.uint8}[np.dtype(dtype).char]).view(*shape)
+    if t in ("f32", "f16"):
+        dt = np.float32 if t == "f32" else np.float16
+        return [plane(kvh, ctx, d, dtype=dt), None, plane(kvh, ctx, d, dtype=dt), None]
+    cb = d if t == "q8_0" else d // 2
+    return [x for _ in range(2) for x in (plane(kvh, ctx, cb, dtype=np.uint8), plane(kvh, ctx, d // 32, dtype=np.float16))]
+
+
+def write(af, t, cache, k, v, kvh, d, ctx, slots=None, slot0=0, stream=None):
+    n, ld = k.shape
+    af.af_kv_write(k, v, ld, n, slots, slot0, *cache, af.KVTYPE[t], kvh, d, ctx, stream)
+
+
+def read(af, t, cache, n, kvh, d, ctx, slots=None, slot0=0, fill=0.0):
+    k = torch.full((n, kvh * d), fill, device="cuda")
+    v = torch.full((n, kvh * d), fill, device="cuda")
+    af.af_kv_read(*cache, af.KVTYPE[t], kvh, d, ctx, n, slots, slot0, k, v, kvh * d)
+    return k.cpu().numpy(), v.cpu().numpy()
+
+
+def hard_rows(rng, n, w):
+    """Rows with ordinary values, and blocks that sit on the quantizers' borders."""
+    x = rng.standard_normal((n, w)).astype(np.float32)
+    b = x.reshape(-1, 32)
+    for i in range(0, len(b), 7):
+        if i % 3 == 0:
+            b[i] = 0
+        elif i % 3 == 1:  # exact halves of a scale that is a power of two, and their neighbours in fp32
+            h = (rng.integers(-8, 8, 32) + 0.5).astype(np.float32) / 64
+            b[i] = np.nextafter(h, rng.choice([-9, 9], 32).astype(np.float32))
+            b[i, ::3] = h[::3]
+            b[i, 5] = -8 / 64
+        else:  # ties of the largest magnitude with both signs, tiny and huge scales
+            b[i] *= rng.choice([1e-6, 1e-3, 1e3])
+            b[i, 3], b[i, 17] = -np.abs(b[i]).max() - 1e-6, np.abs(b[i]).max() + 1e-6
+            b[i, 17] = -b[i, 3]
+    return x
+
+
+@pytest.mark.parametrize("t", KV)
+@pytest.mark.parametrize("n,kvh,d,listed", [(1, 1, 32, False), (1, 4, 64, True), (16, 8, 128, True), (37, 5, 96, False),
+                                            (300, 8, 128, False), (257, 3, 64, True), (9, 2, 256, True)])
+def test_kv_rows_bit_exact(af, t, n, kvh, d, listed):
+    rng = np.random.default_rng(n + d)
+    ctx, w = n + 21, kvh * d
+    k, v = hard_rows(rng, n, w), hard_rows(rng, n, w)
+    kd = torch.full((n, w + 4), float("nan"), device="cuda")  # rows of a wider buffer
+    vd = torch.full((n, w + 4), float("nan"), device="cuda")
+    kd[:, :w], vd[:, :w] = _dev(k), _dev(v)
+    cache = new_cache(t, kvh, ctx, d, 0x2A)
+    before = [None if c is None else c.clone() for c in cache]
+    if listed:
+        slots = rng.permutation(ctx)[:n].astype(np.int32)
+        if n > 4:
+            slots[1], slots[n // 2] = -1, ctx
+        live = np.flatnonzero((slots >= 0) & (slots < ctx))
+        write(af, t, cache, kd, vd, kvh, d, ctx, _dev(slots))
+        gk, gv = read(af, t, cache, n, kvh, d, ctx, _dev(slots), fill=5.0)
+        assert np.all(gk[np.setdiff1d(np.arange(n), live)] == 5.0)
+    else:
+        slots = np.arange(n, dtype=np.int32) + 13
+        live = np.arange(n)
+        write(af, t, cache, kd, vd, kvh, d, ctx, slot0=13)
+        gk, gv = read(af, t, cache, n, kvh, d, ctx, slot0=13)
+    assert np.array_equal(gk[live].astype(np.float64).reshape(-1, kvh, d), held(k.reshape(n, kvh, d), t)[live])
+    assert np.array_equal(gv[live].astype(np.float64).reshape(-1, kvh, d), held(v.reshape(n, kvh, d), t)[live])
+    other = np.setdiff1d(np.arange(ctx), slots[live])  # every other slot is as it was
+    for a, b in zip(cache, before):
+        if a is not None:
+            assert torch.equal(a[:, other].view(torch.uint8), b[:, other].view(torch.uint8))
+
+
+@pytest.mark.parametrize("t", ["q8_0", "q4_0"])
+def test_kv_codes_are_the_models_store_format(af, t):
+    """Code bytes and scales as af_model_kv_store's: Q8_0 int8 in element order, Q4_0 nibble pairs of n = q + 8."""
+    rng = np.random.default_rng(5)
+    k = rng.standard_normal((2, 64)).astype(np.float32)
+    cache = new_cache(t, 1, 4, 64)
+    write(af, t, cache, _dev(k), _dev(k), 1, 64, 4, slot0=1)
+    q, d = quantize(k.reshape(2, 2, 32), t)
+    codes = cache[0].cpu().numpy()[0, 1:3]
+    got = codes.view(np.int8).astype(int) if t == "q8_0" else np.stack((codes & 15, codes >> 4), -1).reshape(2, 64).astype(int) - 8
+    assert np.array_equal(got, q.reshape(2, 64))
+    assert np.array_equal(cache[1].cpu().numpy()[0, 1:3], d)
+
+
+@pytest.mark.parametrize("t", KV)
+def test_kv_same_slot_twice_last_row_wins(af, t):
+    rng = np.random.default_rng(6)
+    n, kvh, d, ctx = 700, 2, 64, 50
+    k = rng.standard_normal((n, kvh * d)).astype(np.float32)
+    slots = rng.integers(-1, ctx, n).astype(np.int32)
+    cache = new_cache(t, kvh, ctx, d)
+    write(af, t, cache, _dev(k), _dev(-k), kvh, d, ctx, _dev(slots))
+    gk, gv = read(af, t, cache, ctx, kvh, d, ctx)
+    for s in range(ctx):
+        rows = np.flatnonzero(slots == s)
+        if len(rows):
+            assert np.array_equal(gk[s].astype(np.float64), held(k[rows[-1]].reshape(kvh, d), t).reshape(-1)), s
+            assert np.array_equal(gv[s].astype(np.float64), held(-k[rows[-1]].reshape(kvh, d), t).reshape(-1)), s
+
+
+@pytest.mark.parametrize("t", ["q8_0", "q4_0"])
+def test_kv_non_finite_blocks_read_back_as_nan(af, t):
+    k = np.random.default_rng(7).standard_normal((1, 128)).astype(np.float32)
+    v = k.copy()
+    k[0, 3], k[0, 40], k[0, 70] = np.nan, np.inf, -np.inf
+    v[0, 100] = 3e38  # the scale overflows fp16
+    cache = new_cache(t, 1, 2, 128)
+    write(af, t, cache, _dev(k), _dev(v), 1, 128, 2)
+    gk, gv = read(af, t, cache, 1, 1, 128, 2)
+    assert np.all(np.isnan(gk[0, :96])) and np.array_equal(gk[0, 96:].astype(np.float64), held(k[0, 96:], t))
+    assert np.all(np.isnan(gv[0, 96:])) and np.array_equal(gv[0, :96].astype(np.float64), held(v[0, :96], t))
+
+
+@pytest.mark.parametrize("t", KV)
+def test_kv_read_then_write_moves_slots(af, t):
+    rng = np.random.default_rng(8)
+    kvh, d, ctx, n = 8, 128, 64, 40
+    k, v = rng.standard_normal((n, kvh * d)).astype(np.float32), rng.standard_normal((n, kvh * d)).astype(np.float32)
+    cache = new_cache(t, kvh, ctx, d)
+    write(af, t, cache, _dev(k), _dev(v), kvh, d, ctx)
+    path = np.array([3, 4, 9, 17, 39], np.int32)
+    before = [None if c is None else c[:, path.astype(np.int64)].clone() for c in cache]
+    gk, gv = read(af, t, cache, 5, kvh, d, ctx, _dev(path))
+    write(af, t, cache, _dev(gk), _dev(gv), kvh, d, ctx, slot0=50)
+    for a, b in zip(cache, before):
+        if a is not None:
+            assert torch.equal(a[:, 50:55].contiguous().view(torch.uint8), b.view(torch.uint8))
+
+
+# ---------------------------------------------------------------- trees
+
+def closure(parent):
+    n = len(parent)
+    see, depth = np.zeros((n, n), bool), np.zeros(n, int)
+    for i, p in enumerate(parent):
+        if 0 <= p < i:
+            see[i], depth[i] = see[p], depth[p] + 1
+        see[i, i] = True
+    return see, depth
+
+
+def pack(see):
+    n = see.shape[0]
+    w = (n + 31) // 32
+    bits = np.zeros((n, w * 32), np.uint64)
+    bits[:, :n] = see
+    words = (bits.reshape(n, w, 32) << np.arange(32, dtype=np.uint64)).sum(-1)
+    return words.astype(np.uint32).view(np.int32)
+
+
+def random_parents(rng, n):
+    return np.array([max(-1, i - 1 - int(rng.random() ** 2 * 8)) for i in range(n)], np.int32)
+
+
+@pytest.mark.parametrize("n", [1, 2, 31, 32, 33, 64, 100, 1000, 1024])
+@pytest.mark.parametrize("kind", ["random", "chain", "star", "wild"])
+def test_tree_mask(af, n, kind):
+    rng = np.random.default_rng(n)
+    parent = {"random": random_parents(rng, n), "chain": np.arange(n) - 1, "star": np.full(n, -1),
+              "wild": rng.integers(-5, n + 5, n)}[kind].astype(np.int32)
+    see, depth = closure(parent)
+    mask = torch.full((n + 1, (n + 31) // 32), 0x55, dtype=torch.int32, device="cuda")
+    pos = torch.full((n + 1,), -7, dtype=torch.int32, device="cuda")
+    af.af_tree_mask(_dev(parent), n, 1000, mask, pos)
+    assert np.array_equal(mask[:n].cpu().numpy(), pack(see))
+    assert np.array_equal(pos[:n].cpu().numpy(), 1000 + depth)
+    assert int(pos[n]) == -7 and bool((mask[n] == 0x55).all())
+    again = torch.empty_like(mask)
+    af.af_tree_mask(_dev(parent), n, 0, again)  # without positions
+    assert torch.equal(again[:n], mask[:n])
+
+
+def attn_ref(q, k, v, see, past):
+    """q [n, H, D], k, v [KVH, past + n, D] float64, see [n, n]: row by row over what the row sees."""
+    n, H, D = q.shape
+    G = H // k.shape[0]
+    out = np.zeros((n, H, D))
+    for i in range(n):
+        at = np.concatenate([np.arange(past), past + np.flatnonzero(see[i])])
+        if not len(at):
+            continue
+        for g in range(k.shape[0]):
+            s = q[i, g * G:(g + 1) * G] @ k[g, at].T / np.sqrt(D)
+            p = np.exp(s - s.max(-1, keepdims=True))
+            out[i, g * G:(g + 1) * G] = p @ v[g, at] / p.sum(-1, keepdims=True)
+    return out
+
+
+def attn_tol(q, k, v):
+    """Scores in fp32 or from parts that keep 22 bits: |ds| <= 2^-20 sum |q||k| / sqrt(D) (the parts' 2^-21 and the sum's
+    roundings); p then moves by ds relative, the average of v by at most twice that times max |v|, and the parts of
+    p and v, the exponential and the sums add 2^-19 max |v|."""
+    D = q.shape[-1]
+    qa, ka = np.abs(q).max(0).max(0), np.abs(k).max(0).max(0)
+    return float(np.abs(v).max() * (2 * 2.0 ** -20 * (qa * ka).sum() / np.sqrt(D) + 2.0 ** -19))
+
+
+def attend(af, t, cache, q, H, kvh, d, ctx, past, see, pad=0, stream=None, ws=None, out=None):
+    n = q.shape[0]
+    qd = torch.full((n, H * d + pad), float("nan"), device="cuda")
+    qd[:, :H * d] = _dev(q.reshape(n, H * d).astype(np.float32))
+    out = torch.full((n, H * d + pad), 9.0, device="cuda") if out is None else out
+    need = af.af_attention_tree_workspace(af.KVTYPE[t], H, kvh, d, past, n)
+    if ws is None:
+        ws = torch.full((max(need, 256),), 0xFF, dtype=torch.uint8, device="cuda")  # any contents: NaN patterns
+    af.af_attention_tree(qd, H * d + pad, *cache, af.KVTYPE[t], H, kvh, d, ctx, past, n, _dev(pack(see)), ws, need, out,
+                         H * d + pad, stream)
+    return out
+
+
+def filled(af, t, rng, kvh, d, ctx, m, spread=1.0):
+    """A cache whose first m slots hold random rows (written by af_kv_write), the rest 0xFF bytes (NaN)."""
+    k = (rng.standard_normal((m, kvh * d)) * spread).astype(np.float32)
+    v = rng.standard_normal((m, kvh * d)).astype(np.float32)
+    cache = new_cache(t, kvh, ctx, d, 0xFF)
+    write(af, t, cache, _dev(k), _dev(v), kvh, d, ctx)
+    return cache, held(k.reshape(m, kvh, d), t).transpose(1, 0, 2), held(v.reshape(m, kvh, d), t).transpose(1, 0, 2)
+
+
+ATTN = [  # H, KVH, D, past, n
+    (8, 4, 64, 0, 1), (8, 4, 64, 31, 1), (1, 1, 64, 1, 1), (32, 8, 128, 300, 16), (32, 8, 64, 1024, 17),
+    (12, 4, 128, 77, 5), (5, 1, 64, 129, 33), (64, 1, 128, 500, 3), (32, 8, 128, 4097, 64), (8, 8, 128, 0, 100),
+    (32, 4, 64, 15, 31), (16, 2, 128, 255, 128), (7, 7, 64, 63, 9), (2, 2, 128, 3, 700), (4, 1, 64, 1, 1024),
+]
+
+
+@pytest.mark.parametrize("t", KV)
+@pytest.mark.parametrize("H,KVH,D,past,n", ATTN)
+def test_attention_tree(af, t, H, KVH, D, past, n):
+    rng = np.random.default_rng(past * 7 + n)
+    ctx = past + n + (n % 3) * 5
+    cache, k, v = filled(af, t, rng, KVH, D, ctx, past + n)
+    q = rng.standard_normal((n, H, D)).astype(np.float32)
+    see, _ = closure(random_parents(rng, n))
+    out = attend(af, t, cache, q, H, KVH, D, ctx, past, see, pad=4)
+    got = out.cpu().numpy().astype(np.float64)
+    assert np.all(got[:, H * D:] == 9.0)
+    ref = attn_ref(q.astype(np.float64), k, v, see, past)
+    err, tol = np.abs(got[:, :H * D].reshape(n, H, D) - ref).max(), attn_tol(q, k, v)
+    print(f"err {err:.2e} tol {tol:.2e} rel {np.linalg.norm(got[:, :H * D].ravel() - ref.ravel()) / np.linalg.norm(ref):.2e}")
+    assert err <= tol
+
+
+@pytest.mark.parametrize("t", KV)
+@pytest.mark.parametrize("past,n", [(0, 40), (70, 40), (33, 300)])
+def test_attention_tree_masks(af, t, past, n):
+    """Rows that see nothing, everything, one slot, later slots (any mask goes, not only a tree's)."""
+    H, KVH, D = 8, 2, 128
+    rng = np.random.default_rng(n)
+    cache, k, v = filled(af, t, rng, KVH, D, past + n, past + n)
+    q = rng.standard_normal((n, H, D)).astype(np.float32)
+    see = rng.random((n, n)) < 0.3
+    see[0], see[1], see[2] = False, True, False
+    see[2, n - 1] = True
+    see[5:25] = False
+    got = attend(af, t, cache, q, H, KVH, D, past + n, past, see).cpu().numpy().astype(np.float64).reshape(n, H, D)
+    ref = attn_ref(q.astype(np.float64), k, v, see, past)
+    assert np.abs(got - ref).max() <= attn_tol(q, k, v)
+    if past == 0:
+        assert np.all(got[5:25] == 0.0) and np.all(got[0] == 0.0)
+
+
+@pytest.mark.parametrize("t", KV)
+@pytest.mark.parametrize("what", ["nan", "inf", "-inf"])
+@pytest.mark.parametrize("past,n", [(50, 20), (0, 130)])
+def test_attention_tree_hidden_slots_reach_no_row(af, t, what, past, n):
+    """A slot that holds NaN or infinities changes the rows that see it and no other."""
+    H, KVH, D = 8, 2, 64
+    rng = np.random.default_rng(11)
+    cache, k, v = filled(af, t, rng, KVH, D, past + n, past + n)
+    q = rng.standard_normal((n, H, D)).astype(np.float32)
+    see, _ = closure(random_parents(rng, n))
+    see[:, 3] = False
+    see[7, 3] = True
+    clean = attend(af, t, cache, q, H, KVH, D, past + n, past, see).cpu().numpy()
+    bad = torch.full((1, KVH * D), float(what), device="cuda")
+    write(af, t, cache, bad, bad, KVH, D, past + n, slot0=past + 3)
+    got = attend(af, t, cache, q, H, KVH, D, past + n, past, see).cpu().numpy()
+    rest = np.arange(n) != 7
+    assert np.abs(got[rest] - clean[rest]).max() <= attn_tol(q.astype(np.float64), k, v)  # (False for a NaN)
+    assert not np.array_equal(got[7], clean[7])
+
+
+@pytest.mark.parametrize("t", KV)
+def test_attention_tree_wide_scores_and_small_values(af, t):
+    """Scores far apart (one slot takes nearly all the weight), and values whose sizes differ by blocks and slots."""
+    H, KVH, D, past, n = 8, 2, 128, 700, 24
+    rng = np.random.default_rng(12)
+    m = past + n
+    k = (rng.standard_normal((m, KVH * D)) * 6).astype(np.float32)
+    v = (rng.standard_normal((m, KVH * D)) * np.exp(rng.uniform(-6, 3, (m, 1)))).astype(np.float32)
+    cache = new_cache(t, KVH, m, D)
+    write(af, t, cache, _dev(k), _dev(v), KVH, D, m)
+    q = (rng.standard_normal((n, H, D)) * 4).astype(np.float32)
+    see, _ = closure(random_parents(rng, n))
+    got = attend(af, t, cache, q, H, KVH, D, m, past, see).cpu().numpy().astype(np.float64).reshape(n, H, D)
+    kh, vh = held(k.reshape(m, KVH, D), t).transpose(1, 0, 2), held(v.reshape(m, KVH, D), t).transpose(1, 0, 2)
+    assert np.abs(got - attn_ref(q.astype(np.float64), kh, vh, see, past)).max() <= attn_tol(q, kh, vh)
+
+
+@pytest.mark.parametrize("t,scale", [("f32", 1e-4), ("f32", 3e4), ("f16", 1e-4), ("f16", 1e4), ("q8_0", 1e-3), ("q8_0", 1e4),
+                                     ("q4_0", 1e-3), ("q4_0", 1e4)])
+@pytest.mark.parametrize("n", [3, 70])
+def test_attention_tree_scale_of_values(af, t, scale, n):
+    """The result scales with the values: nothing under- or overflows on the way, at small row counts or large."""
+    H, KVH, D, past = 8, 2, 64, 200
+    rng = np.random.default_rng(13)
+    m = past + n
+    k = rng.standard_normal((m, KVH * D)).astype(np.float32)
+    v = (rng.standard_normal((m, KVH * D)) * scale).astype(np.float32)
+    cache = new_cache(t, KVH, m, D)
+    write(af, t, cache, _dev(k), _dev(v), KVH, D, m)
+    q = rng.standard_normal((n, H, D)).astype(np.float32)
+    see, _ = closure(random_parents(rng, n))
+    got = attend(af, t, cache, q, H, KVH, D, m, past, see).cpu().numpy().astype(np.float64).reshape(n, H, D)
+    kh, vh = held(k.reshape(m, KVH, D), t).transpose(1, 0, 2), held(v.reshape(m, KVH, D), t).transpose(1, 0, 2)
+    assert np.abs(got - attn_ref(q.astype(np.float64), kh, vh, see, past)).max() <= attn_tol(q, kh, vh)
+
+
+@pytest.mark.parametrize("t", ["f32", "f16"])
+def test_attention_tree_of_one_node_is_decode_attention(af, t):
+    H, KVH, D, past = 32, 8, 128, 1000
+    rng = np.random.default_rng(14)
+    cache, k, v = filled(af, t, rng, KVH, D, past + 1, past + 1)
+    q = rng.standard_normal((1, H, D)).astype(np.float32)
+    got = attend(af, t, cache, q, H, KVH, D, past + 1, past, np.ones((1, 1), bool)).cpu().numpy()
+    dec = torch.empty(H * D, device="cuda")
+    af.af_attention_decode(_dev(q.reshape(-1)), cache[0], cache[2], af.KVTYPE[t], H, KVH, D, past + 1, past, dec)
+    assert np.abs(got.reshape(-1) - dec.cpu().numpy()).max() <= 2 * 1e-3 * np.abs(got).max()  # both within 1e-3 normwise
+
+
+@pytest.mark.parametrize("t", KV)
+@pytest.mark.parametrize("past,n", [(2000, 8), (900, 96)])
+def test_attention_tree_repeats_captures_and_streams(af, t, past, n):
+    """The same bits from call to call, from a replayed graph over new inputs, and from two streams at once."""
+    H, KVH, D = 32, 8, 128
+    rng = np.random.default_rng(15)
+    ctx = past + n
+    cache, k, v = filled(af, t, rng, KVH, D, ctx, ctx)
+    qs = [rng.standard_normal((n, H * D)).astype(np.float32) for _ in range(2)]
+    see, _ = closure(random_parents(rng, n))
+    want = [attend(af, t, cache, q, H, KVH, D, ctx, past, see) for q in qs]
+    assert torch.equal(want[0], attend(af, t, cache, qs[0], H, KVH, D, ctx, past, see))
+    need = max(256, af.af_attention_tree_workspace(af.KVTYPE[t], H, KVH, D, past, n))
+    q, out, mask = _dev(qs[0]), torch.zeros(n, H * D, device="cuda"), _dev(pack(see))
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        af.af_attention_tree(q, H * D, *cache, af.KVTYPE[t], H, KVH, D, ctx, past, n, mask, ws, need, out, H * D)
+    for i in (1, 0, 1):
+        q.copy_(_dev(qs[i]))
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[i])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    bufs = [(_dev(qs[i]), torch.empty(need, dtype=torch.uint8, device="cuda"), torch.zeros(n, H * D, device="cuda"))
+            for i in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, (qd, w, o) in zip(streams, bufs):
+            af.af_attention_tree(qd, H * D, *cache, af.KVTYPE[t], H, KVH, D, ctx, past, n, mask, w, need, o, H * D, s)
+    torch.cuda.synchronize()
+    assert torch.equal(bufs[0][2], want[0]) and torch.equal(bufs[1][2], want[1])
+
+
+# ---------------------------------------------------------------- together
+
+@pytest.mark.parametrize("t", KV)
+def test_draft_verify_and_move(af, t):
+    """A drafted tree through rotary positions, cache write, mask and attention equals, node by node, the definition
+    on the node's own path; the accepted branch, moved with a read and a write, serves the next call."""
+    H, KVH, D, past, n, ctx = 16, 4, 128, 90, 23, 160
+    rng = np.random.default_rng(16)
+    parent = random_parents(rng, n)
+    see, depth = closure(parent)
+    cache, k0, v0 = filled(af, t, rng, KVH, D, ctx, past)
+    fused = rng.standard_normal((n, (H + 2 * KVH) * D)).astype(np.float32)
+    w = fused.shape[1]
+    rows, rot = _dev(fused), torch.empty(n, w, device="cuda")
+    mask = torch.empty(n, 1, dtype=torch.int32, device="cuda")
+    pos = torch.empty(n, dtype=torch.int32, device="cuda")
+    cfg = af.rope_config(D, D, "interleaved", 500000.0)
+    af.af_tree_mask(_dev(parent), n, past, mask, pos)
+    af.af_rope(cfg, rows, w, rot, w, af.AF_F32, n, H + KVH, pos)          # q and k heads in one call
+    kd, vd = rot[:, H * D:], rows[:, (H + KVH) * D:]
+    af.af_kv_write(kd, vd, w, n, None, past, *cache, af.KVTYPE[t], KVH, D, ctx)
+    need = af.af_attention_tree_workspace(af.KVTYPE[t], H, KVH, D, past, n)
+    ws = torch.empty(max(need, 256), dtype=torch.uint8, device="cuda")
+    out = torch.empty(n, H * D, device="cuda")
+    af.af_attention_tree(rot, w, *cache, af.KVTYPE[t], H, KVH, D, ctx, past, n, mask, ws, need, out, H * D)
+    r = rot.cpu().numpy()
+    th = rope_ref(fused[:, :(H + KVH) * D].astype(np.float64).reshape(n, H + KVH, D), [past + int(x) for x in depth], D,
+                  "interleaved", turns(D, 500000.0, "none", 1, 1), 1.0)
+    assert np.abs(r[:, :(H + KVH) * D].reshape(n, H + KVH, D) - th).max() <= 2 * np.abs(fused).max() * 2.0 ** -20
+    q = r[:, :H * D].reshape(n, H, D).astype(np.float64)
+    kn = held(r[:, H * D:(H + KVH) * D].reshape(n, KVH, D), t).transpose(1, 0, 2)
+    vn = held(fused[:, (H + KVH) * D:].reshape(n, KVH, D), t).transpose(1, 0, 2)
+    k, v = np.concatenate([k0, kn], 1), np.concatenate([v0, vn], 1)
+    assert np.abs(out.cpu().numpy().reshape(n, H, D) - attn_ref(q, k, v, see, past)).max() <= attn_tol(q, k, v)
+    # the accepted branch: the path to the last node, moved to the slots after the past
+    path = np.flatnonzero(see[n - 1])
+    m = len(path)
+    slots = _dev((past + path).astype(np.int32))
+    kr, vr = torch.empty(m, KVH * D, device="cuda"), torch.empty(m, KVH * D, device="cuda")
+    af.af_kv_read(*cache, af.KVTYPE[t], KVH, D, ctx, m, slots, 0, kr, vr, KVH * D)
+    af.af_kv_write(kr, vr, KVH * D, m, None, past, *cache, af.KVTYPE[t], KVH, D, ctx)
+    got = attend(af, t, cache, q[n - 1:], H, KVH, D, ctx, past + m - 1, np.ones((1, 1), bool))
+    # the same slots in another order of summation
+    assert np.abs(got.cpu().numpy().reshape(H, D) - out[n - 1].cpu().numpy().reshape(H, D)).max() <= 2 * attn_tol(q, k, v)
