@@ -2,9 +2,32 @@
 // past..past+n-1 that hold the nodes' own keys and values, those whose bit its mask row has:
 //   out_i = sum_j p_ij v_j / sum_j p_ij,   p_ij = exp(q_i . k_j / sqrt(D)).
 // A row that sees no slot gives zeros.
+//
+// The rows of a kv head are its n nodes times the G heads of its group (row = node G + head), so that every cached
+// byte is read once for all of them.  Split-KV: CTA (split, kv head, row tile of 16 MT rows) walks its range of
+// slots once; inside it every warp takes its own stages of KS slots through a private cp.async ring, with its own
+// running maximum, sum and output (mma.sync fragments in registers), no CTA barrier in the loop, and the warps'
+// states are joined at the end.  With several splits the partials are joined by a second kernel in split order.
+//
+// Scores and output on the tensor cores at fp32-level precision:
+//  - q (scaled by log2 e / sqrt(D): p = 2^(s - m)) is split into two parts of 11 bits, fp16 (scaled by a power of
+//    two per row, so no magnitude overflows) or tf32; so is p.
+//  - fp16 cache: K and V are operands as they are; two products each (hi and lo).
+//  - Q8_0 / Q4_0: the integer codes are exact fp16 operands.  A key's scale multiplies its fp32 partial score of
+//    each 32-value block; a value's scale multiplies p, per block, before p is split (with a power of two that
+//    follows the largest scale seen, so that p d stays in fp16's range).
+//  - fp32 cache: tf32 parts of K and V too, three products (the dropped lo lo product is 2^-22 relative).
+// The reference maximum of the softmax moves only when a score exceeds it by more than 4 (in powers of two); p
+// carries a factor 2^8 so that small p keep their low part above fp16's subnormal step.  Sums are fp32.
+//
+// Hidden slots: a masked score is -inf (a select, so NaN does not survive); in the groups of slots that hold nodes,
+// non-finite values are taken out of the product and added element by element to the rows that see them.
 #include <math_constants.h>
 
+#include <algorithm>
+
 #include "draft.cuh"
+#include "tma.cuh"
 
 namespace af {
 
@@ -30,72 +53,776 @@ __global__ void __launch_bounds__(256)
     if (pos && lane == 0) pos[i] = pos0 + depth;
 }
 
-template <int TYPE>
-__device__ __forceinline__ float cell_value(const void* base, const __half* scales, int64_t cell, int D, int d) {
-    if (TYPE == AF_F32) return ((const float*)base)[cell * D + d];
-    if (TYPE == AF_F16) return __half2float(((const __half*)base)[cell * D + d]);
-    const float s = __half2float(scales[cell * (D / 32) + d / 32]);
-    if (TYPE == AF_KV_Q8_0) return s * (float)((const int8_t*)base)[cell * D + d];
-    const int b = ((const uint8_t*)base)[cell * (D / 2) + d / 2];
-    return s * (float)((d & 1 ? b >> 4 : b & 15) - 8);
+// ---------------------------------------------------------------- building blocks
+
+constexpr float kLog2eT = 1.4426950408889634f;
+constexpr float kLazyT = 4.f;  // powers of two by which a score may exceed the reference maximum
+constexpr float kBiasT = 8.f;  // p = 2^(s - m + kBiasT): at most 2^12
+
+__device__ __forceinline__ float ex2t(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+template <int B>
+__device__ __forceinline__ void cp_small(uint32_t dst, const void* src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(B), "r"(in ? B : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+    unsigned short v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint4 ldsm4t(uint32_t a) {
+    uint4 v;
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(a));
+    return v;
+}
+__device__ __forceinline__ void mma16(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma8(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t tf32_of(float x) {
+    uint32_t r;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+    return r;
+}
+// x = hi + lo in two tf32 parts
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+    hi = tf32_of(x);
+    lo = tf32_of(x - __uint_as_float(hi));
+}
+// (a, b) = hi + lo in two fp16 parts each
+__device__ __forceinline__ void split_h2(float a, float b, uint32_t& hi, uint32_t& lo) {
+    const __half2 h = __floats2half2_rn(a, b);
+    const float2 back = __half22float2(h);
+    const __half2 l = __floats2half2_rn(a - back.x, b - back.y);
+    hi = *reinterpret_cast<const uint32_t*>(&h);
+    lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+// two halves of `magic + code` minus `off`: the codes as fp16
+__device__ __forceinline__ uint32_t hsub2u(uint32_t x, uint32_t off) {
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&off));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+// non-finite halves of x become 0; `bad` is set if there were any
+__device__ __forceinline__ uint32_t finite_h2(uint32_t x, bool& bad) {
+    const bool lo = (x & 0x7C00u) == 0x7C00u, hi = (x & 0x7C000000u) == 0x7C000000u;
+    bad |= lo | hi;
+    return x & ((lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u));
 }
 
-constexpr int kWarps = 8;
-
-// One CTA per (node, head); the warps take the slots in turn, a lane owns D / 32 dims.
 template <int TYPE, int D>
-__global__ void __launch_bounds__(kWarps * 32) attn_tree_kernel(TreeArgs a) {
-    constexpr int E = D / 32;
-    __shared__ float sm_o[kWarps][D], sm_m[kWarps], sm_l[kWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int i = blockIdx.x / a.H, h = blockIdx.x % a.H, g = h / (a.H / a.c.KVH);
-    const int words = (a.n + 31) / 32;
-    float q[E], o[E] = {};
+struct TreeCfg {
+    static constexpr bool QUANT = TYPE == AF_KV_Q8_0 || TYPE == AF_KV_Q4_0;
+    static constexpr int NB = D / 32;                                             // 32-value blocks of a head
+    static constexpr int RB = TYPE == AF_F32 ? 4 * D : TYPE == AF_F16 ? 2 * D : TYPE == AF_KV_Q8_0 ? D : D / 2;  // row bytes
+    static constexpr int SB = QUANT ? 2 * NB : 0;                                 // scale bytes of a row
+    static constexpr int KS = QUANT ? 32 : 16;                                    // slots per stage
+    static constexpr int NW = TYPE == AF_F32 && D == 128 ? 6 : 8;                 // warps
+    static constexpr int OV = KS * RB, OKS = 2 * KS * RB, OVS = OKS + KS * SB;    // V, K scales, V scales in a stage
+    static constexpr int STAGE = 2 * KS * (RB + SB);
+    static constexpr int NST = 192 * 1024 / (NW * STAGE) < 4 ? 192 * 1024 / (NW * STAGE) : 4;  // stages of a warp
+    static constexpr int KQ = TYPE == AF_F32 ? D / 8 : D / 16;                    // mma steps along a head
+    // 16-byte chunk permutation of row `key`, so that the fragment loads of a warp meet all banks
+    static __device__ __forceinline__ int swk(int key) {
+        if (TYPE == AF_F32) return key & 1;
+        if (TYPE == AF_F16) return (key & 1) << 2;
+        if (TYPE == AF_KV_Q8_0) return D == 128 ? (key & 3) << 1 : (key & 2);
+        return D == 128 ? (key >> 1) & 3 : (key >> 2) & 1;
+    }
+    static __device__ __forceinline__ int swv(int key) {
+        if (TYPE == AF_F32) return ((key >> 1) & 3) << 1;
+        if (TYPE == AF_F16) return key & 7;
+        if (TYPE == AF_KV_Q8_0) return D == 128 ? ((key >> 1) & 3) << 1 : (key & 2);
+        return D == 128 ? (key >> 1) & 3 : (key >> 2) & 1;
+    }
+    // dim of the output fragment's column m (0..7) of n-tile t
+    static __device__ __forceinline__ int odim(int t, int m) {
+        return TYPE == AF_F16 ? 8 * t + m : 32 * (t >> 2) + 4 * m + (t & 3);
+    }
+};
+template <int TYPE, int D, int MT>
+constexpr int tree_q_bytes() {
+    return TreeCfg<TYPE, D>::KQ * MT * 32 * 16 * 2;
+}
+template <int TYPE, int D, int MT>
+constexpr int tree_smem() {
+    using C = TreeCfg<TYPE, D>;
+    constexpr int ring = C::NW * C::NST * C::STAGE, join = C::NW * 16 * MT * (D + 2) * 4;
+    return tree_q_bytes<TYPE, D, MT>() + (ring > join ? ring : join);
+}
+
+// One stage of a warp: slots [key0, key0 + KS), of which those below `end` are read.
+template <int TYPE, int D>
+__device__ __forceinline__ void tree_issue(const KvRows& c, int64_t row0, int key0, int end, uint32_t dst, int lane) {
+    using C = TreeCfg<TYPE, D>;
+    constexpr int CPR = C::RB / 16;
+    const uint8_t* k = (const uint8_t*)c.k + row0 * C::RB;
+    const uint8_t* v = (const uint8_t*)c.v + row0 * C::RB;
 #pragma unroll
-    for (int e = 0; e < E; e++) q[e] = a.q[i * a.ldq + h * D + lane + 32 * e] * rsqrtf((float)D);
-    float m = -CUDART_INF_F, l = 0.f;
-    for (int j = warp; j < a.past + a.n; j += kWarps) {
-        const int t = j - a.past;
-        if (t >= 0 && !(a.mask[(int64_t)i * words + (t >> 5)] >> (t & 31) & 1)) continue;
-        const int64_t cell = (int64_t)g * a.c.ctx + j;
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; e++) s += q[e] * cell_value<TYPE>(a.c.k, a.c.ks, cell, D, lane + 32 * e);
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        const float mn = fmaxf(m, s), f = expf(m - mn), p = expf(s - mn);
-        l = l * f + p;
-#pragma unroll
-        for (int e = 0; e < E; e++) o[e] = o[e] * f + p * cell_value<TYPE>(a.c.v, a.c.vs, cell, D, lane + 32 * e);
-        m = mn;
+    for (int i = 0; i < C::KS * CPR / 32; i++) {
+        const int idx = i * 32 + lane, key = idx / CPR, ch = idx % CPR;
+        const bool in = key0 + key < end;
+        const int64_t off = in ? (int64_t)(key0 + key) * C::RB + ch * 16 : 0;
+        cp16(dst + key * C::RB + ((ch ^ C::swk(key)) << 4), k + off, in);
+        cp16(dst + C::OV + key * C::RB + ((ch ^ C::swv(key)) << 4), v + off, in);
+    }
+    if (C::QUANT) {
+        static_assert(!C::QUANT || C::KS == 32, "a lane per slot");
+        const bool in = key0 + lane < end;
+        const int64_t off = row0 + (in ? key0 + lane : 0);
+        cp_small<C::QUANT ? C::SB : 4>(dst + C::OKS + lane * C::SB, (const uint8_t*)c.ks + off * C::SB, in);
+        cp_small<C::QUANT ? C::SB : 4>(dst + C::OVS + lane * C::SB, (const uint8_t*)c.vs + off * C::SB, in);
+    }
+}
+
+// fp32 scales of slots key and key + 1 (key even) of a stage, [slot][block]
+template <int NB>
+__device__ __forceinline__ void load_scales(uint32_t a, float (&d)[2][NB]) {
+    uint32_t w[NB];
+    if (NB == 4) {
+        const uint4 r = lds128(a);
+        w[0] = r.x, w[1] = r.y, w[NB - 2] = r.z, w[NB - 1] = r.w;
+    } else {
+        const uint2 r = lds64(a);
+        w[0] = r.x, w[NB - 1] = r.y;
     }
 #pragma unroll
-    for (int e = 0; e < E; e++) sm_o[warp][lane + 32 * e] = o[e];
-    if (lane == 0) {
-        sm_m[warp] = m;
-        sm_l[warp] = l;
+    for (int s = 0; s < 2; s++)
+#pragma unroll
+        for (int b = 0; b < NB; b += 2) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[(s * NB + b) / 2]));
+            d[s][b] = f.x;
+            d[s][b + 1] = f.y;
+        }
+}
+
+// The value of (key, dim) of a stage's V, for the element-by-element path.
+template <int TYPE, int D>
+__device__ __forceinline__ float stage_value(uint32_t st, int key, int d) {
+    using C = TreeCfg<TYPE, D>;
+    const uint32_t row = st + C::OV + key * C::RB;
+    auto at = [&](int byte) { return row + ((((byte >> 4) ^ C::swv(key)) << 4) | (byte & 15)); };
+    if (TYPE == AF_F32) return __uint_as_float(lds32(at(4 * d)));
+    if (TYPE == AF_F16) return __half2float(__ushort_as_half((unsigned short)lds16(at(2 * d))));
+    const float s = __half2float(__ushort_as_half((unsigned short)lds16(st + C::OVS + key * C::SB + 2 * (d >> 5))));
+    if (TYPE == AF_KV_Q8_0) {
+        const uint32_t w = lds16(at(d & ~1));
+        return s * (float)(int8_t)(d & 1 ? w >> 8 : w & 255);
+    }
+    const uint32_t w = lds16(at((d >> 1) & ~1));
+    return s * (float)((int)(w >> (4 * (d & 3)) & 15) - 8);
+}
+
+template <int TYPE, int D, int MT>
+__global__ void __launch_bounds__(TreeCfg<TYPE, D>::NW * 32, 1) attn_tree_kernel(TreeArgs a, int splits) {
+    using C = TreeCfg<TYPE, D>;
+    constexpr int NW = C::NW, NT = D / 8, KS = C::KS, NB = C::NB, ROWS = 16 * MT;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float sm_rowf[ROWS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 3, j = lane >> 2;
+    const int G = a.H / a.c.KVH, R = a.n * G, keys = a.past + a.n;
+    const int split = blockIdx.x, g = blockIdx.y, r0 = blockIdx.z * ROWS;
+    const int stages = (keys + KS - 1) / KS;
+    const int st0 = (int)((int64_t)stages * split / splits), st1 = (int)((int64_t)stages * (split + 1) / splits);
+    const int64_t row0 = (int64_t)g * a.c.ctx;
+    const uint32_t sq = smem_u32(smem), ring = sq + tree_q_bytes<TYPE, D, MT>() + warp * C::NST * C::STAGE;
+
+    pdl_launch_dependents();
+    // ---- the first stages are on their way while q is prepared
+#pragma unroll
+    for (int i = 0; i < C::NST - 1; i++) {
+        const int st = st0 + warp + i * NW;
+        if (st < st1) tree_issue<TYPE, D>(a.c, row0, st * KS, keys, ring + i * C::STAGE, lane);
+        cp_commit();
+    }
+
+    // ---- q fragments: a warp scales and splits a row; lane l holds dims 4l..4l+3
+    for (int r = warp; r < ROWS; r += NW) {
+        float x[4] = {};
+        if (r0 + r < R && lane < D / 4) {
+            const int node = (r0 + r) / G, head = g * G + (r0 + r) % G;
+            const float4 f = *reinterpret_cast<const float4*>(a.q + (int64_t)node * a.ldq + (int64_t)head * D + 4 * lane);
+            const float sc = rsqrtf((float)D) * kLog2eT;
+            x[0] = f.x * sc, x[1] = f.y * sc, x[2] = f.z * sc, x[3] = f.w * sc;
+        }
+        if (TYPE != AF_F32) {  // a power of two brings the row's largest value to [1, 2)
+            float mx = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            int e = (int)(__float_as_uint(mx) >> 23) - 127;
+            e = e < -100 ? -100 : (e > 126 ? 126 : e);  // (0, subnormal; infinite: the row becomes NaN either way)
+            const float down = __uint_as_float((unsigned)(127 - e) << 23);
+#pragma unroll
+            for (int i = 0; i < 4; i++) x[i] *= down;
+            if (lane == 0) sm_rowf[r] = __uint_as_float((unsigned)(127 + e) << 23);
+        }
+        if (lane < D / 4) {
+            const int mt = r >> 4, rr = r & 15, b = lane >> 3, cc = (lane & 7) >> 1, par = lane & 1;
+            const uint32_t lane_off = (uint32_t)((rr & 7) * 4 + cc) * 16, hi8 = (uint32_t)(rr >> 3);
+            auto frag = [&](int step, int part) { return sq + (uint32_t)((step * MT + mt) * 2 + part) * 512 + lane_off; };
+            if (TYPE == AF_F32) {
+#pragma unroll
+                for (int i = 0; i < 4; i++) {  // dim 8 cc + 2 s + h: register 2 h + (row >= 8) of step 4 b + s
+                    uint32_t hi, lo;
+                    split_tf32(x[i], hi, lo);
+                    const int step = 4 * b + 2 * par + (i >> 1);
+                    const uint32_t reg = (2 * (i & 1) + hi8) * 4;
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(frag(step, 0) + reg), "r"(hi) : "memory");
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(frag(step, 1) + reg), "r"(lo) : "memory");
+                }
+            } else {
+                uint32_t hi[2], lo[2];
+                split_h2(x[0], x[1], hi[0], lo[0]);
+                split_h2(x[2], x[3], hi[1], lo[1]);
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    // dim 8 cc + i of its half: Q4_0 pairs dims 4 apart (their nibbles share a mask), else neighbours
+                    const int dd = 4 * par + i;
+                    const int s = TYPE == AF_KV_Q4_0 ? (dd & 3) >> 1 : dd >> 2, h = TYPE == AF_KV_Q4_0 ? dd & 1 : (dd >> 1) & 1;
+                    const int e = TYPE == AF_KV_Q4_0 ? dd >> 2 : dd & 1;
+                    const uint32_t reg = (2 * h + hi8) * 4 + 2 * e;
+                    const unsigned short vh = (unsigned short)(hi[i >> 1] >> (16 * (i & 1)));
+                    const unsigned short vl = (unsigned short)(lo[i >> 1] >> (16 * (i & 1)));
+                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(frag(2 * b + s, 0) + reg), "h"(vh) : "memory");
+                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(frag(2 * b + s, 1) + reg), "h"(vl) : "memory");
+                }
+            }
+        }
     }
     __syncthreads();
-    for (int d = threadIdx.x; d < D; d += kWarps * 32) {
-        float mx = -CUDART_INF_F, num = 0.f, den = 0.f;
-        for (int w = 0; w < kWarps; w++) mx = fmaxf(mx, sm_m[w]);
-        for (int w = 0; w < kWarps; w++) {
-            if (sm_l[w] == 0.f) continue;
-            const float f = expf(sm_m[w] - mx);
-            num += f * sm_o[w][d];
-            den += f * sm_l[w];
+    float rowf[MT][2];
+    const unsigned* mrow[MT][2];  // mask words of this thread's rows
+#pragma unroll
+    for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const int r = mt * 16 + h * 8 + j;
+            rowf[mt][h] = TYPE == AF_F32 ? 1.f : sm_rowf[r];
+            mrow[mt][h] = r0 + r < R ? a.mask + (int64_t)((r0 + r) / G) * ((a.n + 31) / 32) : nullptr;
         }
-        a.out[i * a.ldo + h * D + d] = den == 0.f ? 0.f : num / den;
+    auto sees = [&](int mt, int h, int key) {  // slot key of the cache
+        if (key < a.past) return true;
+        const int t = key - a.past;
+        return t < a.n && mrow[mt][h] && (mrow[mt][h][t >> 5] >> (t & 31) & 1);
+    };
+
+    float o[MT][NT][4] = {}, m_ref[MT][2], l[MT][2] = {};
+#pragma unroll
+    for (int mt = 0; mt < MT; mt++) m_ref[mt][0] = m_ref[mt][1] = -CUDART_INF_F;
+    float vinv = 1.f, vlim = 0.f;  // quantized: V's scales are taken times vinv, a power of two
+
+    int slot = 0;
+    for (int st = st0 + warp; st < st1; st += NW) {
+        cp_wait<C::NST - 2>();
+        __syncwarp();  // every lane's copies of this stage have landed, and every lane is done with the previous one
+        asm volatile("" ::: "memory");
+        {  // the previous stage's slot takes the stage NST - 1 ahead
+            const int nx = st + (C::NST - 1) * NW, ns = slot == 0 ? C::NST - 1 : slot - 1;
+            if (nx < st1) tree_issue<TYPE, D>(a.c, row0, nx * KS, keys, ring + ns * C::STAGE, lane);
+            cp_commit();
+        }
+        const uint32_t base = ring + slot * C::STAGE;
+#pragma unroll 1
+        for (int grp = 0; grp < KS / 16; grp++) {
+            const int key0 = st * KS + grp * 16;
+            if (key0 >= keys) break;
+            const uint32_t kb = base + grp * 16 * C::RB, vb = kb + C::OV;
+            // ---- scores of 16 slots
+            float s[MT][2][4] = {};
+            if constexpr (C::QUANT) {
+                float dk[2][2][NB];
+#pragma unroll
+                for (int t = 0; t < 2; t++) load_scales<NB>(base + C::OKS + (grp * 16 + t * 8 + 2 * c) * C::SB, dk[t]);
+#pragma unroll
+                for (int b = 0; b < NB; b++) {
+                    uint32_t kw[2][4];
+#pragma unroll
+                    for (int t = 0; t < 2; t++) {
+                        const int key = t * 8 + j;
+                        if (TYPE == AF_KV_Q8_0) {
+                            const int byte = 32 * b + 8 * c;
+                            uint2 w = lds64(kb + key * C::RB + ((((byte >> 4) ^ C::swk(key)) << 4) | (byte & 15)));
+                            w.x ^= 0x80808080u, w.y ^= 0x80808080u;
+                            kw[t][0] = hsub2u(__byte_perm(w.x, 0x64646464u, 0x4140), 0x64806480u);
+                            kw[t][1] = hsub2u(__byte_perm(w.x, 0x64646464u, 0x4342), 0x64806480u);
+                            kw[t][2] = hsub2u(__byte_perm(w.y, 0x64646464u, 0x4140), 0x64806480u);
+                            kw[t][3] = hsub2u(__byte_perm(w.y, 0x64646464u, 0x4342), 0x64806480u);
+                        } else {
+                            const uint32_t w = lds32(kb + key * C::RB + ((b ^ C::swk(key)) << 4) + 4 * c);
+#pragma unroll
+                            for (int i = 0; i < 4; i++) kw[t][i] = hsub2u(((w >> (4 * i)) & 0x000F000Fu) | 0x64006400u, 0x64086408u);
+                        }
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < MT; mt++) {
+                        float p[2][4] = {};
+#pragma unroll
+                        for (int e = 0; e < 2; e++) {
+                            const uint4 qh = lds128(sq + ((2 * b + e) * MT + mt) * 1024 + lane * 16);
+                            const uint4 ql = lds128(sq + ((2 * b + e) * MT + mt) * 1024 + 512 + lane * 16);
+#pragma unroll
+                            for (int t = 0; t < 2; t++) {
+                                mma16(p[t], qh, kw[t][2 * e], kw[t][2 * e + 1]);
+                                mma16(p[t], ql, kw[t][2 * e], kw[t][2 * e + 1]);
+                            }
+                        }
+#pragma unroll
+                        for (int t = 0; t < 2; t++)
+#pragma unroll
+                            for (int i = 0; i < 4; i++) s[mt][t][i] += dk[t][i & 1][b] * p[t][i];
+                    }
+                }
+            } else if constexpr (TYPE == AF_F16) {
+#pragma unroll
+                for (int b = 0; b < NB; b++) {
+                    uint4 kw[2];
+#pragma unroll
+                    for (int t = 0; t < 2; t++) {
+                        const int key = t * 8 + j;
+                        kw[t] = lds128(kb + key * C::RB + (((4 * b + c) ^ C::swk(key)) << 4));
+                    }
+#pragma unroll
+                    for (int e = 0; e < 2; e++)
+#pragma unroll
+                        for (int mt = 0; mt < MT; mt++) {
+                            const uint4 qh = lds128(sq + ((2 * b + e) * MT + mt) * 1024 + lane * 16);
+                            const uint4 ql = lds128(sq + ((2 * b + e) * MT + mt) * 1024 + 512 + lane * 16);
+#pragma unroll
+                            for (int t = 0; t < 2; t++) {
+                                mma16(s[mt][t], qh, e ? kw[t].z : kw[t].x, e ? kw[t].w : kw[t].y);
+                                mma16(s[mt][t], ql, e ? kw[t].z : kw[t].x, e ? kw[t].w : kw[t].y);
+                            }
+                        }
+                }
+            } else {
+#pragma unroll
+                for (int b = 0; b < NB; b++) {
+                    uint32_t kh[2][8], kl[2][8];
+#pragma unroll
+                    for (int t = 0; t < 2; t++) {
+                        const int key = t * 8 + j;
+#pragma unroll
+                        for (int u = 0; u < 2; u++) {
+                            const uint4 w = lds128(kb + key * C::RB + (((8 * b + 2 * c + u) ^ C::swk(key)) << 4));
+                            split_tf32(__uint_as_float(w.x), kh[t][4 * u], kl[t][4 * u]);
+                            split_tf32(__uint_as_float(w.y), kh[t][4 * u + 1], kl[t][4 * u + 1]);
+                            split_tf32(__uint_as_float(w.z), kh[t][4 * u + 2], kl[t][4 * u + 2]);
+                            split_tf32(__uint_as_float(w.w), kh[t][4 * u + 3], kl[t][4 * u + 3]);
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+#pragma unroll
+                        for (int mt = 0; mt < MT; mt++) {
+                            const uint4 qh = lds128(sq + ((4 * b + e) * MT + mt) * 1024 + lane * 16);
+                            const uint4 ql = lds128(sq + ((4 * b + e) * MT + mt) * 1024 + 512 + lane * 16);
+#pragma unroll
+                            for (int t = 0; t < 2; t++) {
+                                mma8(s[mt][t], qh, kh[t][2 * e], kh[t][2 * e + 1]);
+                                mma8(s[mt][t], ql, kh[t][2 * e], kh[t][2 * e + 1]);
+                                mma8(s[mt][t], qh, kl[t][2 * e], kl[t][2 * e + 1]);
+                            }
+                        }
+                }
+            }
+            // ---- mask and softmax
+            const bool nodes = key0 + 16 > a.past;  // slots of nodes, or behind the last one
+#pragma unroll
+            for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+                for (int t = 0; t < 2; t++)
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        if (TYPE != AF_F32) s[mt][t][i] *= rowf[mt][i >> 1];
+                        if (nodes && !sees(mt, i >> 1, key0 + t * 8 + 2 * c + (i & 1))) s[mt][t][i] = -CUDART_INF_F;
+                    }
+            float mx[MT][2];
+            bool move = false;
+#pragma unroll
+            for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    float x = fmaxf(fmaxf(s[mt][0][2 * h], s[mt][0][2 * h + 1]), fmaxf(s[mt][1][2 * h], s[mt][1][2 * h + 1]));
+                    mx[mt][h] = x;
+                    move |= x > m_ref[mt][h] + kLazyT;
+                }
+            if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+                for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        float x = mx[mt][h];
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                        if (x > m_ref[mt][h]) {
+                            const float f = ex2t(m_ref[mt][h] - x);
+                            m_ref[mt][h] = x;
+                            l[mt][h] *= f;
+#pragma unroll
+                            for (int t = 0; t < NT; t++) {
+                                o[mt][t][2 * h] *= f;
+                                o[mt][t][2 * h + 1] *= f;
+                            }
+                        }
+                    }
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const float mb = m_ref[mt][h] == -CUDART_INF_F ? 0.f : m_ref[mt][h] - kBiasT;
+#pragma unroll
+                    for (int t = 0; t < 2; t++)
+#pragma unroll
+                        for (int i = 0; i < 2; i++) {
+                            const float p = ex2t(s[mt][t][2 * h + i] - mb);
+                            s[mt][t][2 * h + i] = p;
+                            l[mt][h] += p;
+                        }
+                }
+            // ---- output
+            bool bad = false;  // non-finite values among the nodes' slots, taken out of the product
+            if constexpr (C::QUANT) {
+                float dv[2][2][NB];
+                float big = 0.f;
+#pragma unroll
+                for (int t = 0; t < 2; t++) {
+                    load_scales<NB>(base + C::OVS + (grp * 16 + t * 8 + 2 * c) * C::SB, dv[t]);
+#pragma unroll
+                    for (int i = 0; i < 2; i++)
+#pragma unroll
+                        for (int b = 0; b < NB; b++) {
+                            if (nodes && !(fabsf(dv[t][i][b]) <= 65504.f)) {
+                                dv[t][i][b] = 0.f;
+                                bad = true;
+                            }
+                            big = fmaxf(big, fabsf(dv[t][i][b]));
+                        }
+                }
+                if (__any_sync(0xffffffffu, big > vlim)) {
+                    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+                    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+                    if (big <= 65504.f) {  // (an infinite scale of the past makes its rows infinite or NaN as it is)
+                        const unsigned e = __float_as_uint(big) >> 23;
+                        const float up = __uint_as_float((254u - e) << 23);  // 2^-exponent(big)
+                        const float f = up / vinv;
+                        vinv = up;
+                        vlim = 4.f * __uint_as_float(e << 23);
+#pragma unroll
+                        for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+                            for (int t = 0; t < NT; t++)
+#pragma unroll
+                                for (int i = 0; i < 4; i++) o[mt][t][i] *= f;
+                    }
+                }
+#pragma unroll
+                for (int b = 0; b < NB; b++) {
+                    uint32_t vw[4][2];
+                    if (TYPE == AF_KV_Q8_0) {
+#pragma unroll
+                        for (int h = 0; h < 2; h++) {
+                            uint32_t w[2];
+#pragma unroll
+                            for (int i = 0; i < 2; i++) {
+                                const int key = h * 8 + 2 * c + i, byte = 32 * b + 4 * j;
+                                w[i] = lds32(vb + key * C::RB + ((((byte >> 4) ^ C::swv(key)) << 4) | (byte & 15))) ^ 0x80808080u;
+                            }
+                            const uint32_t x = __byte_perm(w[0], w[1], 0x5140), y = __byte_perm(w[0], w[1], 0x7362);
+                            vw[0][h] = hsub2u(__byte_perm(x, 0x64646464u, 0x4140), 0x64806480u);
+                            vw[1][h] = hsub2u(__byte_perm(x, 0x64646464u, 0x4342), 0x64806480u);
+                            vw[2][h] = hsub2u(__byte_perm(y, 0x64646464u, 0x4140), 0x64806480u);
+                            vw[3][h] = hsub2u(__byte_perm(y, 0x64646464u, 0x4342), 0x64806480u);
+                        }
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < 2; h++) {
+                            const int k0 = h * 8 + 2 * c, k1 = k0 + 1;
+                            const uint32_t w = lds16(vb + k0 * C::RB + ((b ^ C::swv(k0)) << 4) + 2 * j) |
+                                               lds16(vb + k1 * C::RB + ((b ^ C::swv(k1)) << 4) + 2 * j) << 16;
+#pragma unroll
+                            for (int i = 0; i < 4; i++) vw[i][h] = hsub2u(((w >> (4 * i)) & 0x000F000Fu) | 0x64006400u, 0x64086408u);
+                        }
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < MT; mt++) {
+                        uint4 ph, pl;
+                        float x[2][2];
+#pragma unroll
+                        for (int t = 0; t < 2; t++)
+#pragma unroll
+                            for (int i = 0; i < 2; i++) x[t][i] = dv[t][i][b] * vinv;
+                        split_h2(s[mt][0][0] * x[0][0], s[mt][0][1] * x[0][1], ph.x, pl.x);
+                        split_h2(s[mt][0][2] * x[0][0], s[mt][0][3] * x[0][1], ph.y, pl.y);
+                        split_h2(s[mt][1][0] * x[1][0], s[mt][1][1] * x[1][1], ph.z, pl.z);
+                        split_h2(s[mt][1][2] * x[1][0], s[mt][1][3] * x[1][1], ph.w, pl.w);
+#pragma unroll
+                        for (int t = 0; t < 4; t++) {
+                            mma16(o[mt][4 * b + t], ph, vw[t][0], vw[t][1]);
+                            mma16(o[mt][4 * b + t], pl, vw[t][0], vw[t][1]);
+                        }
+                    }
+                }
+            } else if constexpr (TYPE == AF_F16) {
+                uint4 ph[MT], pl[MT];
+#pragma unroll
+                for (int mt = 0; mt < MT; mt++) {
+                    split_h2(s[mt][0][0], s[mt][0][1], ph[mt].x, pl[mt].x);
+                    split_h2(s[mt][0][2], s[mt][0][3], ph[mt].y, pl[mt].y);
+                    split_h2(s[mt][1][0], s[mt][1][1], ph[mt].z, pl[mt].z);
+                    split_h2(s[mt][1][2], s[mt][1][3], ph[mt].w, pl[mt].w);
+                }
+                // lane: row lane & 15 of the 16 slots, chunk (lane >> 4) of the pair
+                const int key = lane & 15;
+#pragma unroll
+                for (int t = 0; t < NT; t += 2) {
+                    uint4 v = ldsm4t(vb + key * C::RB + (((t + (lane >> 4)) ^ C::swv(key)) << 4));
+                    if (nodes) {
+                        v.x = finite_h2(v.x, bad), v.y = finite_h2(v.y, bad);
+                        v.z = finite_h2(v.z, bad), v.w = finite_h2(v.w, bad);
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < MT; mt++) {
+                        mma16(o[mt][t], ph[mt], v.x, v.y);
+                        mma16(o[mt][t], pl[mt], v.x, v.y);
+                        mma16(o[mt][t + 1], ph[mt], v.z, v.w);
+                        mma16(o[mt][t + 1], pl[mt], v.z, v.w);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int t = 0; t < 2; t++) {
+                    uint4 ph[MT], pl[MT];
+#pragma unroll
+                    for (int mt = 0; mt < MT; mt++) {  // slot 2c is k = c, slot 2c + 1 is k = c + 4
+                        split_tf32(s[mt][t][0], ph[mt].x, pl[mt].x);
+                        split_tf32(s[mt][t][2], ph[mt].y, pl[mt].y);
+                        split_tf32(s[mt][t][1], ph[mt].z, pl[mt].z);
+                        split_tf32(s[mt][t][3], ph[mt].w, pl[mt].w);
+                    }
+                    const int k0 = t * 8 + 2 * c, k1 = k0 + 1;
+#pragma unroll
+                    for (int b = 0; b < NB; b++) {
+                        const uint4 x = lds128(vb + k0 * C::RB + (((8 * b + j) ^ C::swv(k0)) << 4));
+                        const uint4 y = lds128(vb + k1 * C::RB + (((8 * b + j) ^ C::swv(k1)) << 4));
+                        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            float fx = __uint_as_float(xs[i]), fy = __uint_as_float(ys[i]);
+                            if (nodes) {
+                                if (!(fabsf(fx) < CUDART_INF_F)) fx = 0.f, bad = true;
+                                if (!(fabsf(fy) < CUDART_INF_F)) fy = 0.f, bad = true;
+                            }
+                            uint32_t xh, xl, yh, yl;
+                            split_tf32(fx, xh, xl);
+                            split_tf32(fy, yh, yl);
+#pragma unroll
+                            for (int mt = 0; mt < MT; mt++) {
+                                mma8(o[mt][4 * b + i], ph[mt], xh, yh);
+                                mma8(o[mt][4 * b + i], pl[mt], xh, yh);
+                                mma8(o[mt][4 * b + i], ph[mt], xl, yl);
+                            }
+                        }
+                    }
+                }
+            }
+            if (nodes && __any_sync(0xffffffffu, bad)) {
+                // rare: add p v of the non-finite values to the rows that see the slot
+#pragma unroll 1
+                for (int key = 0; key < 16; key++) {
+                    const int src = (lane & ~3) | ((key & 7) >> 1);
+                    const float scale = C::QUANT ? vinv : 1.f;
+#pragma unroll
+                    for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+                        for (int h = 0; h < 2; h++) {
+                            const float p0 = key < 8 ? s[mt][0][2 * h] : s[mt][1][2 * h];
+                            const float p1 = key < 8 ? s[mt][0][2 * h + 1] : s[mt][1][2 * h + 1];
+                            const float p = __shfl_sync(0xffffffffu, (key & 1) ? p1 : p0, src);
+                            if (!sees(mt, h, key0 + key)) continue;
+#pragma unroll
+                            for (int t = 0; t < NT; t++)
+#pragma unroll
+                                for (int i = 0; i < 2; i++) {
+                                    const float v = stage_value<TYPE, D>(base, grp * 16 + key, C::odim(t, 2 * c + i));
+                                    if (!(fabsf(v) < CUDART_INF_F)) o[mt][t][2 * h + i] += p * (v * scale);
+                                }
+                        }
+                }
+            }
+        }
+        slot = slot + 1 == C::NST ? 0 : slot + 1;
+    }
+    cp_wait<0>();
+    __syncthreads();
+
+    // ---- join the warps: [warp][row][D] outputs, then [warp][row] (m, l)
+    float* so = reinterpret_cast<float*>(smem + tree_q_bytes<TYPE, D, MT>());
+    float2* sml = reinterpret_cast<float2*>(so + NW * ROWS * D);
+    const float back = C::QUANT ? 1.f / vinv : 1.f;
+#pragma unroll
+    for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const int r = mt * 16 + h * 8 + j;
+            float x = l[mt][h];
+            x += __shfl_xor_sync(0xffffffffu, x, 1);
+            x += __shfl_xor_sync(0xffffffffu, x, 2);
+            if (c == 0) sml[warp * ROWS + r] = make_float2(m_ref[mt][h], x);
+            float* dst = so + (warp * ROWS + r) * D;
+#pragma unroll
+            for (int t = 0; t < NT; t++)
+#pragma unroll
+                for (int i = 0; i < 2; i++) dst[C::odim(t, 2 * c + i)] = o[mt][t][2 * h + i] * back;
+        }
+    __syncthreads();
+    float* part = a.ws;
+    float2* part_ml = reinterpret_cast<float2*>(a.ws + (int64_t)splits * a.c.KVH * R * D);
+    for (int i = threadIdx.x; i < ROWS * (D / 4); i += NW * 32) {
+        const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+        if (r0 + r >= R) break;
+        float m = -CUDART_INF_F;
+#pragma unroll
+        for (int w = 0; w < NW; w++) m = fmaxf(m, sml[w * ROWS + r].x);
+        float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+        float den = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; w++) {
+            const float2 ml = sml[w * ROWS + r];
+            if (ml.x == -CUDART_INF_F && ml.y == 0.f) continue;  // this warp saw nothing
+            const float f = ex2t(ml.x - m);
+            const float4 v = *reinterpret_cast<const float4*>(so + (w * ROWS + r) * D + d);
+            num.x += f * v.x, num.y += f * v.y, num.z += f * v.z, num.w += f * v.w;
+            den += f * ml.y;
+        }
+        if (splits == 1) {
+            const float inv = den == 0.f ? 0.f : 1.f / den;
+            const int node = (r0 + r) / G, head = g * G + (r0 + r) % G;
+            *reinterpret_cast<float4*>(a.out + (int64_t)node * a.ldo + (int64_t)head * D + d) =
+                make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
+        } else {
+            const int64_t row = ((int64_t)split * a.c.KVH + g) * R + r0 + r;
+            *reinterpret_cast<float4*>(part + row * D + d) = num;
+            if (d == 0) part_ml[row] = make_float2(m, den);
+        }
     }
 }
 
+// Joins the splits in their order: a warp per row.
+template <int D>
+__global__ void __launch_bounds__(256) tree_merge_kernel(TreeArgs a, int splits) {
+    const int lane = threadIdx.x & 31, G = a.H / a.c.KVH, R = a.n * G;
+    const int row = blockIdx.x * 8 + (threadIdx.x >> 5), rows = a.c.KVH * R;
+    pdl_wait();
+    if (row >= rows) return;
+    const float2* ml = reinterpret_cast<const float2*>(a.ws + (int64_t)splits * rows * D);
+    float m = -CUDART_INF_F;
+    for (int s = lane; s < splits; s += 32) {
+        const float2 x = __ldcg(ml + (int64_t)s * rows + row);
+        m = fmaxf(m, x.x);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+    float den = 0.f;
+    const int d = 4 * lane;
+#pragma unroll 8
+    for (int s = 0; s < splits; s++) {
+        const float2 x = __ldcg(ml + (int64_t)s * rows + row);
+        const float4 v = d < D ? __ldcg(reinterpret_cast<const float4*>(a.ws + ((int64_t)s * rows + row) * D + d))
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float f = x.x == -CUDART_INF_F && x.y == 0.f ? 0.f : ex2t(x.x - m);
+        num.x += f * v.x, num.y += f * v.y, num.z += f * v.z, num.w += f * v.w;
+        den += f * x.y;
+    }
+    if (d >= D) return;
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    const int g = row / R, node = (row % R) / G, head = g * G + row % R % G;
+    *reinterpret_cast<float4*>(a.out + (int64_t)node * a.ldo + (int64_t)head * D + d) =
+        make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
+}
+
+struct TreePlan {
+    int mt = 1, splits = 1;
+};
+
+// Row tiles of 32 where there are more than 16 rows; splits fill the SMs, as long as every warp has a stage.
+TreePlan tree_plan(int H, int KVH, int D, int type, int past, int n) {
+    TreePlan p;
+    const int R = n * (H / KVH);
+    p.mt = R > 16 ? 2 : 1;
+    const bool quant = type == AF_KV_Q8_0 || type == AF_KV_Q4_0;
+    const int ks = quant ? 32 : 16, nw = type == AF_F32 && D == 128 ? 6 : 8;
+    const int64_t tiles = (int64_t)KVH * ((R + 16 * p.mt - 1) / (16 * p.mt));
+    const int stages = (past + n + ks - 1) / ks;
+    int64_t s = num_sms() / tiles;
+    s = std::min<int64_t>(s, (stages + nw - 1) / nw);
+    p.splits = (int)std::max<int64_t>(1, s);
+    return p;
+}
+
+template <int TYPE, int D, int MT>
+cudaError_t go(const TreeArgs& a, int splits, cudaStream_t s) {
+    constexpr int smem = tree_smem<TYPE, D, MT>();
+    auto k = attn_tree_kernel<TYPE, D, MT>;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e) return e;
+    const int R = a.n * (a.H / a.c.KVH);
+    k<<<dim3(splits, a.c.KVH, (R + 16 * MT - 1) / (16 * MT)), TreeCfg<TYPE, D>::NW * 32, smem, s>>>(a, splits);
+    e = cudaGetLastError();
+    if (e || splits == 1) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((a.c.KVH * R + 7) / 8);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, a, splits);
+}
+
 template <int TYPE>
-cudaError_t go(const TreeArgs& a, cudaStream_t s) {
-    if (a.c.D == 64)
-        attn_tree_kernel<TYPE, 64><<<a.n * a.H, kWarps * 32, 0, s>>>(a);
-    else
-        attn_tree_kernel<TYPE, 128><<<a.n * a.H, kWarps * 32, 0, s>>>(a);
-    return cudaGetLastError();
+cudaError_t go_type(const TreeArgs& a, cudaStream_t s) {
+    const TreePlan p = tree_plan(a.H, a.c.KVH, a.c.D, TYPE, a.past, a.n);
+    if (a.c.D == 64) return p.mt == 1 ? go<TYPE, 64, 1>(a, p.splits, s) : go<TYPE, 64, 2>(a, p.splits, s);
+    return p.mt == 1 ? go<TYPE, 128, 1>(a, p.splits, s) : go<TYPE, 128, 2>(a, p.splits, s);
 }
 
 }  // namespace
@@ -105,14 +832,18 @@ cudaError_t launch_tree_mask(const int* parent, int n, int pos0, unsigned* mask,
     return cudaGetLastError();
 }
 
-size_t attn_tree_ws_bytes(int, int, int, int, int, int) { return 0; }
+size_t attn_tree_ws_bytes(int H, int KVH, int D, int type, int past, int n) {
+    const TreePlan p = tree_plan(H, KVH, D, type, past, n);
+    if (p.splits == 1) return 0;
+    return ((size_t)p.splits * n * H * (D + 2) * sizeof(float) + 255) & ~(size_t)255;
+}
 
 cudaError_t launch_attn_tree(const TreeArgs& a, cudaStream_t s) {
     switch (a.c.type) {
-        case AF_F32: return go<AF_F32>(a, s);
-        case AF_F16: return go<AF_F16>(a, s);
-        case AF_KV_Q8_0: return go<AF_KV_Q8_0>(a, s);
-        default: return go<AF_KV_Q4_0>(a, s);
+        case AF_F32: return go_type<AF_F32>(a, s);
+        case AF_F16: return go_type<AF_F16>(a, s);
+        case AF_KV_Q8_0: return go_type<AF_KV_Q8_0>(a, s);
+        default: return go_type<AF_KV_Q4_0>(a, s);
     }
 }
 
