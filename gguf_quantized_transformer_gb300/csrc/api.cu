@@ -1216,6 +1216,7 @@ int af_attention_tree(const float* q_dev, int64_t ldq, const void* k_cache, cons
     if (int rc = check_tree(kv_dtype, H, KVH, D, past, n)) return rc;
     TreeArgs a;
     if (int rc = check_cache(k_cache, k_scales, v_cache, v_scales, kv_dtype, KVH, D, ctx, a.c)) return rc;
+    if ((int64_t)KVH * ctx > INT32_MAX) return fail(AF_ENOTIMPL, "n_kv_heads * ctx above 2^31 - 1");
     if ((int64_t)past + n > ctx) return fail(AF_ERANGE, "slots 0..%lld outside the cache (%d slots)", (long long)past + n - 1, ctx);
     if (((uintptr_t)q_dev | (uintptr_t)out_dev) & 15 || (uintptr_t)mask_dev & 3) return fail(AF_EINVAL, "unaligned pointer");
     if (ldq < (int64_t)H * D || ldo < (int64_t)H * D || ldq % 4 || ldo % 4)

@@ -249,7 +249,7 @@ __device__ __forceinline__ float stage_value(uint32_t st, int key, int d) {
 }
 
 template <int TYPE, int D, int MT>
-__global__ void __launch_bounds__(TreeCfg<TYPE, D>::NW * 32, 1) attn_tree_kernel(TreeArgs a, int splits) {
+__global__ void __launch_bounds__(TreeCfg<TYPE, D>::NW * 32, 1) attn_tree_kernel(TreeArgs a, int key_begin, int splits, int part0, int parts) {
     using C = TreeCfg<TYPE, D>;
     constexpr int NW = C::NW, NT = D / 8, KS = C::KS, NB = C::NB, ROWS = 16 * MT;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -257,8 +257,10 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D>::NW * 32, 1) attn_tree_kernel
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 3, j = lane >> 2;
     const int G = a.H / a.c.KVH, R = a.n * G, keys = a.past + a.n;
     const int split = blockIdx.x, g = blockIdx.y, r0 = blockIdx.z * ROWS;
-    const int stages = (keys + KS - 1) / KS;
-    const int st0 = (int)((int64_t)stages * split / splits), st1 = (int)((int64_t)stages * (split + 1) / splits);
+    // this split's stages; key_begin is a whole number of stages
+    const int first = key_begin / KS, stages = (keys + KS - 1) / KS - first;
+    const int st0 = first + (int)((int64_t)stages * split / splits);
+    const int st1 = first + (int)((int64_t)stages * (split + 1) / splits);
     const int64_t row0 = (int64_t)g * a.c.ctx;
     const uint32_t sq = smem_u32(smem), ring = sq + tree_q_bytes<TYPE, D, MT>() + warp * C::NST * C::STAGE;
 
@@ -712,7 +714,7 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D>::NW * 32, 1) attn_tree_kernel
         }
     __syncthreads();
     float* part = a.ws;
-    float2* part_ml = reinterpret_cast<float2*>(a.ws + (int64_t)splits * a.c.KVH * R * D);
+    float2* part_ml = reinterpret_cast<float2*>(a.ws + (int64_t)parts * a.c.KVH * R * D);
     for (int i = threadIdx.x; i < ROWS * (D / 4); i += NW * 32) {
         const int r = i / (D / 4), d = (i % (D / 4)) * 4;
         if (r0 + r >= R) break;
@@ -730,13 +732,13 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D>::NW * 32, 1) attn_tree_kernel
             num.x += f * v.x, num.y += f * v.y, num.z += f * v.z, num.w += f * v.w;
             den += f * ml.y;
         }
-        if (splits == 1) {
+        if (parts == 1) {
             const float inv = den == 0.f ? 0.f : 1.f / den;
             const int node = (r0 + r) / G, head = g * G + (r0 + r) % G;
             *reinterpret_cast<float4*>(a.out + (int64_t)node * a.ldo + (int64_t)head * D + d) =
                 make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
         } else {
-            const int64_t row = ((int64_t)split * a.c.KVH + g) * R + r0 + r;
+            const int64_t row = ((int64_t)(part0 + split) * a.c.KVH + g) * R + r0 + r;
             *reinterpret_cast<float4*>(part + row * D + d) = num;
             if (d == 0) part_ml[row] = make_float2(m, den);
         }
@@ -777,19 +779,24 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(TreeArgs a, int splits)
         make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
 }
 
+// How a call is split: the tcgen05 kernel's part, then the mma.sync kernel's over the slots from key_begin on.
 struct TreePlan {
-    int mt = 1, splits = 1;
+    TreeTcPlan tc;
+    int key_begin = 0, mt = 1, splits = 1;
+    int parts() const { return tc.splits + splits; }
 };
 
 // Row tiles of 32 where there are more than 16 rows; splits fill the SMs, as long as every warp has a stage.
 TreePlan tree_plan(int H, int KVH, int D, int type, int past, int n) {
     TreePlan p;
+    p.tc = tree_tc_plan(H, KVH, past, n);
+    p.key_begin = p.tc.tiles * 64;
     const int R = n * (H / KVH);
     p.mt = R > 16 ? 2 : 1;
     const bool quant = type == AF_KV_Q8_0 || type == AF_KV_Q4_0;
     const int ks = quant ? 32 : 16, nw = type == AF_F32 && D == 128 ? 6 : 8;
     const int64_t tiles = (int64_t)KVH * ((R + 16 * p.mt - 1) / (16 * p.mt));
-    const int stages = (past + n + ks - 1) / ks;
+    const int stages = (past + n - p.key_begin + ks - 1) / ks;
     int64_t s = num_sms() / tiles;
     s = std::min<int64_t>(s, (stages + nw - 1) / nw);
     p.splits = (int)std::max<int64_t>(1, s);
@@ -797,15 +804,17 @@ TreePlan tree_plan(int H, int KVH, int D, int type, int past, int n) {
 }
 
 template <int TYPE, int D, int MT>
-cudaError_t go(const TreeArgs& a, int splits, cudaStream_t s) {
+cudaError_t go(const TreeArgs& a, const TreePlan& p, cudaStream_t s) {
     constexpr int smem = tree_smem<TYPE, D, MT>();
     auto k = attn_tree_kernel<TYPE, D, MT>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e) return e;
-    const int R = a.n * (a.H / a.c.KVH);
-    k<<<dim3(splits, a.c.KVH, (R + 16 * MT - 1) / (16 * MT)), TreeCfg<TYPE, D>::NW * 32, smem, s>>>(a, splits);
+    const int R = a.n * (a.H / a.c.KVH), parts = p.parts();
+    k<<<dim3(p.splits, a.c.KVH, (R + 16 * MT - 1) / (16 * MT)), TreeCfg<TYPE, D>::NW * 32, smem, s>>>(
+        a, p.key_begin, p.splits, p.tc.splits, parts);
     e = cudaGetLastError();
-    if (e || splits == 1) return e;
+    if (!e && p.tc.splits) e = launch_attn_tree_tc(a, p.tc, parts, s);
+    if (e || parts == 1) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((a.c.KVH * R + 7) / 8);
     cfg.blockDim = dim3(256);
@@ -815,14 +824,14 @@ cudaError_t go(const TreeArgs& a, int splits, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, a, splits);
+    return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, a, parts);
 }
 
 template <int TYPE>
 cudaError_t go_type(const TreeArgs& a, cudaStream_t s) {
     const TreePlan p = tree_plan(a.H, a.c.KVH, a.c.D, TYPE, a.past, a.n);
-    if (a.c.D == 64) return p.mt == 1 ? go<TYPE, 64, 1>(a, p.splits, s) : go<TYPE, 64, 2>(a, p.splits, s);
-    return p.mt == 1 ? go<TYPE, 128, 1>(a, p.splits, s) : go<TYPE, 128, 2>(a, p.splits, s);
+    if (a.c.D == 64) return p.mt == 1 ? go<TYPE, 64, 1>(a, p, s) : go<TYPE, 64, 2>(a, p, s);
+    return p.mt == 1 ? go<TYPE, 128, 1>(a, p, s) : go<TYPE, 128, 2>(a, p, s);
 }
 
 }  // namespace
@@ -834,8 +843,8 @@ cudaError_t launch_tree_mask(const int* parent, int n, int pos0, unsigned* mask,
 
 size_t attn_tree_ws_bytes(int H, int KVH, int D, int type, int past, int n) {
     const TreePlan p = tree_plan(H, KVH, D, type, past, n);
-    if (p.splits == 1) return 0;
-    return ((size_t)p.splits * n * H * (D + 2) * sizeof(float) + 255) & ~(size_t)255;
+    if (p.parts() == 1) return 0;
+    return ((size_t)p.parts() * n * H * (D + 2) * sizeof(float) + 255) & ~(size_t)255;
 }
 
 cudaError_t launch_attn_tree(const TreeArgs& a, cudaStream_t s) {

@@ -1,0 +1,649 @@
+// Tree attention over the whole 64-slot tiles of the past on the 5th-generation tensor cores, for calls with many
+// rows: nothing is masked there, every node sees every slot.  The slots after the last whole tile and the nodes' own
+// go to the mma.sync kernel (attn_tree.cu), and the partial results are joined by its merge kernel.
+//
+// CTA (split, kv head g, row tile): 128 rows (row = node G + head of the group) are the 128 TMEM lanes.  With
+// everything that belongs to a row in tensor memory (q, scores, p and the output: 512 columns), shared memory holds
+// only K and V operands, and an MMA reads nothing else from it:
+//   columns [0, D)            output accumulator, fp32
+//   columns [128, 128 + D)    q, scaled by log2 e / sqrt(D) and a power of two per row, as fp16 hi and lo parts
+//   columns [256 + 64 b, ..)  b < 4: scores of a tile (64 fp32 columns), overwritten by p as fp16 hi and lo parts
+// Both products take their A operand (q, p) from tensor memory and B from shared memory: K rows [slot][dim] are
+// K-major, V rows [slot][dim] MN-major, so neither is transposed and both have the cache's own order:
+//   fp16 cache    TMA copies 64 slots x 64 dims boxes into the SWIZZLE_128B layout; two products (hi, lo of q or p)
+//   fp32, Q8_0, Q4_0  eight warps read the tile through registers (two tiles ahead) and write it as fp16 hi and lo
+//                 parts in the same layout; three products (the dropped lo lo is 2^-22 relative).  A tile is scaled
+//                 by a power of two that brings its largest value (or scale) near 1, so fp16's range never binds:
+//                 K's goes into the score's factor, V's follows the tiles through a running exponent whose moves
+//                 rescale the output like the softmax's maximum.
+// Warps 0-3 are the softmax (a thread owns a row: the whole tile of its scores in registers, maximum, p, sum), one
+// warp issues the MMAs, scores of up to three tiles ahead of the outputs, so the tensor pipe always has a queue.
+// The reference maximum moves lazily, as in attn_tree.cu, with the same factor 2^8 in p.
+// Every wait is bounded: a CTA that gives up lets what it issued finish, frees its TMEM and marks its rows NaN.
+#include <math_constants.h>
+
+#include <algorithm>
+
+#include "draft.cuh"
+#include "tcgen05.cuh"
+
+namespace af {
+
+namespace {
+
+constexpr int BK = 64;         // slots per tile
+constexpr int kAhead = 3;      // tiles whose scores are issued ahead of the outputs
+constexpr int kQCol = 128, kSCol = 256, kTmem = 512;
+constexpr int kRows = 128;
+constexpr float kLazy2 = 4.f, kBias2 = 8.f;  // as attn_tree.cu's
+constexpr int kConvWarps = 8;
+
+template <int TYPE, int D>
+struct TcCfgT {
+    static constexpr bool SPLIT = TYPE != AF_F16;
+    static constexpr int PART = BK * D * 2;                  // one fp16 operand of a tile
+    static constexpr int SLOT = PART * (SPLIT ? 2 : 1);      // hi (and lo)
+    static constexpr int NS = SPLIT ? (D == 128 ? 7 : 8) : (D == 128 ? 12 : 16);
+    static constexpr int WARPS = 4 + (SPLIT ? kConvWarps : 1) + 1;
+    static constexpr int MMA_WARP = WARPS - 1;
+    // at least more than half of an SM's shared memory: a CTA takes all of its tensor memory
+    static constexpr int SMEM = (NS * SLOT > 120 * 1024 ? NS * SLOT : 120 * 1024) + 1024;
+};
+
+struct TcState {
+    uint64_t full[16], empty[16];  // operand slots
+    uint64_t s_full[4], p_full[4], pv_done[4];
+    uint64_t q_ready, done;
+    uint64_t max_bar;
+    uint32_t tmem_base;
+    int fills;
+    volatile int abort;
+    float ek[8];      // 2^exponent of K tiles
+    int ev[8];        // exponent of V tiles
+    float wmax[2][kConvWarps];
+};
+
+__device__ __forceinline__ bool twait(uint64_t* bar, unsigned parity, TcState& sm) {  // whole warp
+    bool ok = false;
+    for (unsigned i = 0; i < kWaitLimit && !ok; i++) {
+        ok = mbar_try_wait(bar, parity);
+        if (!ok && sm.abort) break;
+    }
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) sm.abort = 1;
+    return ok;
+}
+__device__ __forceinline__ bool twait1(uint64_t* bar, unsigned parity, TcState& sm) {  // one thread
+    for (unsigned i = 0; i < kWaitLimit; i++) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (sm.abort) return false;
+    }
+    sm.abort = 1;
+    return false;
+}
+
+// The order in which operand tiles are filled and consumed: K0 K1 K2 V0 K3 V1 K4 ...: index of K and V of tile t.
+__device__ __forceinline__ int fill_k(int t) { return t + max(0, t - kAhead + 1); }
+__device__ __forceinline__ int fill_v(int t, int T) { return t + min(T, t + kAhead); }
+// its inverse
+__device__ __forceinline__ void fill_item(int f, int T, bool& isv, int& t) {
+    if (f < min(kAhead, T)) {
+        isv = false;
+        t = f;
+    } else if (T > kAhead && f < kAhead + 2 * (T - kAhead)) {
+        isv = ((f - kAhead) & 1) == 0;
+        t = (f - kAhead) / 2 + (isv ? 0 : kAhead);
+    } else {
+        isv = true;
+        t = f - T;
+    }
+}
+
+__device__ __forceinline__ float ex2u(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((unsigned)(min(max(e, -126), 127) + 127) << 23); }
+__device__ __forceinline__ int exponent_of(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }  // x >= 0
+
+// fp16 MN-major B operand: rows of 64 dims (128 B) per slot, 8-slot groups 1024 B apart, 64-dim chunks `chunk` apart.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t chunk) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr >> 4) & 0x3FFF);
+    d |= (uint64_t)(chunk >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+// 32 lanes x 64 columns, waited for
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
+    uint32_t r[64];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]),
+          "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]),
+          "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
+          "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]),
+          "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 64; i++) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+    const __half2 h = __floats2half2_rn(a, b);
+    const float2 back = __half22float2(h);
+    const __half2 l = __floats2half2_rn(a - back.x, b - back.y);
+    hi = *reinterpret_cast<const uint32_t*>(&h);
+    lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+
+// ---------------------------------------------------------------- tile loads of the converted cache types
+
+// 8 values of a row as they lie in the cache
+template <int TYPE>
+struct Raw8;
+template <>
+struct Raw8<AF_F32> {
+    uint4 a, b;
+};
+template <>
+struct Raw8<AF_KV_Q8_0> {
+    uint2 a;
+    unsigned short d;
+};
+template <>
+struct Raw8<AF_KV_Q4_0> {
+    uint32_t a;
+    unsigned short d;
+};
+
+template <int TYPE, int D>
+struct RawTile {
+    static constexpr int N = BK * D / 8 / (kConvWarps * 32);  // chunks of 8 values per thread
+    static constexpr int W = TYPE == AF_F32 ? 1 : BK * (D / 32) / 2 / 32;  // scale words per lane (the whole tile's)
+    Raw8<TYPE> c[N];
+    uint32_t sc[W];
+};
+
+template <int TYPE, int D>
+__device__ __forceinline__ void load_tile(const void* base, const __half* scales, int64_t row, int ct, int lane,
+                                          RawTile<TYPE, D>& r) {
+    constexpr int CPR = D / 8;
+#pragma unroll
+    for (int i = 0; i < RawTile<TYPE, D>::N; i++) {
+        const int idx = i * kConvWarps * 32 + ct;  // row idx / CPR, chunk idx % CPR: consecutive in memory
+        if constexpr (TYPE == AF_F32) {
+            const uint4* p = reinterpret_cast<const uint4*>((const float*)base + row * D + (int64_t)idx * 8);
+            r.c[i].a = __ldcg(p);
+            r.c[i].b = __ldcg(p + 1);
+        } else {
+            if constexpr (TYPE == AF_KV_Q8_0)
+                r.c[i].a = __ldcg(reinterpret_cast<const uint2*>((const uint8_t*)base + row * D + (int64_t)idx * 8));
+            else
+                r.c[i].a = __ldcg(reinterpret_cast<const uint32_t*>((const uint8_t*)base + row * (D / 2) + (int64_t)idx * 4));
+            r.c[i].d = __ldcg(reinterpret_cast<const unsigned short*>(scales) + (row + idx / CPR) * (D / 32) + (idx % CPR) / 4);
+        }
+    }
+    if constexpr (TYPE != AF_F32) {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(scales + row * (D / 32));
+#pragma unroll
+        for (int i = 0; i < RawTile<TYPE, D>::W; i++) r.sc[i] = __ldcg(w + i * 32 + lane);
+    }
+}
+
+// Largest magnitude among this thread's values (fp32) or this lane's scales.
+template <int TYPE, int D>
+__device__ __forceinline__ float raw_max(const RawTile<TYPE, D>& r) {
+    float m = 0.f;
+    if constexpr (TYPE == AF_F32) {
+#pragma unroll
+        for (int i = 0; i < RawTile<TYPE, D>::N; i++) {
+            const uint32_t w[8] = {r.c[i].a.x, r.c[i].a.y, r.c[i].a.z, r.c[i].a.w, r.c[i].b.x, r.c[i].b.y, r.c[i].b.z, r.c[i].b.w};
+#pragma unroll
+            for (int e = 0; e < 8; e++) m = fmaxf(m, fabsf(__uint_as_float(w[e])));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < RawTile<TYPE, D>::W; i++) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r.sc[i]));
+            m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+    }
+    return m;
+}
+
+__device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+__device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
+
+// The tile's fp16 hi and lo parts, times 2^-e, into a slot (SWIZZLE_128B atoms of 64 dims, [64 slots][128 B] each).
+template <int TYPE, int D>
+__device__ __forceinline__ void store_tile(uint8_t* dst, const RawTile<TYPE, D>& r, int e, int ct) {
+    constexpr int CPR = D / 8, PART = BK * D * 2;
+    const float down = pow2i(-e);
+#pragma unroll
+    for (int i = 0; i < RawTile<TYPE, D>::N; i++) {
+        const int idx = i * kConvWarps * 32 + ct, key = idx / CPR, ch = idx % CPR;
+        uint32_t hi[4], lo[4];
+        if constexpr (TYPE == AF_F32) {
+            const uint32_t w[8] = {r.c[i].a.x, r.c[i].a.y, r.c[i].a.z, r.c[i].a.w, r.c[i].b.x, r.c[i].b.y, r.c[i].b.z, r.c[i].b.w};
+#pragma unroll
+            for (int p = 0; p < 4; p++) split2(__uint_as_float(w[2 * p]) * down, __uint_as_float(w[2 * p + 1]) * down, hi[p], lo[p]);
+        } else {
+            // codes q are exact in fp16, and so is d 2^-e (11 bits); hi = fp16(q d), lo = q d - hi by a fused
+            // multiply-add, exact as long as it is not below fp16's smallest step 2^-24
+            const __half2 d2 = __float2half2_rn(__half2float(__ushort_as_half(r.c[i].d)) * down);
+            __half2 q[4];
+            if constexpr (TYPE == AF_KV_Q8_0) {
+                const uint32_t x = r.c[i].a.x ^ 0x80808080u, y = r.c[i].a.y ^ 0x80808080u;
+                const __half2 off = u2h(0x64806480u);
+                q[0] = __hsub2(u2h(__byte_perm(x, 0x64646464u, 0x4140)), off);
+                q[1] = __hsub2(u2h(__byte_perm(x, 0x64646464u, 0x4342)), off);
+                q[2] = __hsub2(u2h(__byte_perm(y, 0x64646464u, 0x4140)), off);
+                q[3] = __hsub2(u2h(__byte_perm(y, 0x64646464u, 0x4342)), off);
+            } else {
+                const __half2 off = u2h(0x64086408u);
+                const uint32_t x = r.c[i].a;
+                __half2 n[4];  // dims (p, p + 4)
+#pragma unroll
+                for (int p = 0; p < 4; p++) n[p] = __hsub2(u2h(((x >> (4 * p)) & 0x000F000Fu) | 0x64006400u), off);
+                q[0] = __lows2half2(n[0], n[1]);
+                q[1] = __lows2half2(n[2], n[3]);
+                q[2] = __highs2half2(n[0], n[1]);
+                q[3] = __highs2half2(n[2], n[3]);
+            }
+#pragma unroll
+            for (int p = 0; p < 4; p++) {
+                const __half2 h = __hmul2_rn(q[p], d2);
+                hi[p] = h2u(h);
+                lo[p] = h2u(__hfma2(q[p], d2, __hneg2(h)));
+            }
+        }
+        const uint32_t off = (uint32_t)((ch >> 3) * BK * 128) + sw128(key, ch & 7);
+        *reinterpret_cast<uint4*>(dst + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(dst + PART + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+}
+
+// ---------------------------------------------------------------- the kernel
+
+template <int TYPE, int D>
+__global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
+    attn_tree_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, TreeArgs a,
+                        int tiles, int splits, int parts) {
+    using C = TcCfgT<TYPE, D>;
+    constexpr uint32_t kIdS = idesc_f16(kRows, BK);                  // scores: N = slots, B K-major
+    constexpr uint32_t kIdO = idesc_f16(kRows, D) | (1u << 16);      // output: N = dims, B MN-major
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ TcState sm;
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = a.H / a.c.KVH, R = a.n * G;
+    const int split = blockIdx.x, g = blockIdx.y, r0 = blockIdx.z * kRows;
+    const int t0 = (int)((int64_t)tiles * split / splits), T = (int)((int64_t)tiles * (split + 1) / splits) - t0;
+    const int64_t row0 = (int64_t)g * a.c.ctx + (int64_t)t0 * BK;  // first slot row of the split
+
+    pdl_launch_dependents();
+    if (tid == 0) {
+        for (int i = 0; i < C::NS; i++) {
+            mbar_init(&sm.full[i], C::SPLIT ? kConvWarps : 1);
+            mbar_init(&sm.empty[i], 1);
+        }
+        for (int i = 0; i < 4; i++) {
+            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.p_full[i], 4);
+            mbar_init(&sm.pv_done[i], 1);
+        }
+        mbar_init(&sm.q_ready, 4);
+        mbar_init(&sm.done, 1);
+        mbar_init(&sm.max_bar, kConvWarps);
+        sm.fills = 0;
+        sm.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == C::MMA_WARP) tmem_alloc(&sm.tmem_base, kTmem);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+
+    if (warp == C::MMA_WARP) {
+        // ---------------- MMA issuer
+        if (lane == 0) {
+            const uint32_t sbase = smem_u32(smem);
+            bool ok = twait1(&sm.q_ready, 0, sm);
+            tc_fence_after();
+            auto scores = [&](int t) {
+                if (t >= 4 && !twait1(&sm.pv_done[t & 3], ((t - 4) >> 2) & 1, sm)) return false;
+                const int f = fill_k(t), slot = f % C::NS;
+                if (!twait1(&sm.full[slot], (f / C::NS) & 1, sm)) return false;
+                tc_fence_after();
+                const uint32_t k = sbase + slot * C::SLOT, d = tmem + kSCol + (t & 3) * BK;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; kk++) {
+                    const uint64_t b = umma_desc_sw128(k + (kk >> 2) * BK * 128 + (kk & 3) * 32);
+                    mma_f16_ts(d, tmem + kQCol + kk * 8, b, kIdS, kk > 0);
+                    mma_f16_ts(d, tmem + kQCol + D / 2 + kk * 8, b, kIdS, 1);
+                    if (C::SPLIT)
+                        mma_f16_ts(d, tmem + kQCol + kk * 8, umma_desc_sw128(k + C::PART + (kk >> 2) * BK * 128 + (kk & 3) * 32),
+                                   kIdS, 1);
+                }
+                mma_commit(&sm.s_full[t & 3]);
+                mma_commit(&sm.empty[slot]);
+                return true;
+            };
+            for (int t = 0; ok && t < min(kAhead, T); t++) ok = scores(t);
+            for (int t = 0; ok && t < T; t++) {
+                const int f = fill_v(t, T), slot = f % C::NS;
+                ok = twait1(&sm.full[slot], (f / C::NS) & 1, sm) && twait1(&sm.p_full[t & 3], (t >> 2) & 1, sm);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t v = sbase + slot * C::SLOT, p = tmem + kSCol + (t & 3) * BK;
+#pragma unroll
+                for (int kk = 0; kk < BK / 16; kk++) {
+                    const uint64_t b = desc_mn(v + kk * 2048, BK * 128);
+                    mma_f16_ts(tmem, p + kk * 8, b, kIdO, t > 0 || kk > 0);
+                    mma_f16_ts(tmem, p + BK / 2 + kk * 8, b, kIdO, 1);
+                    if (C::SPLIT) mma_f16_ts(tmem, p + kk * 8, desc_mn(v + C::PART + kk * 2048, BK * 128), kIdO, 1);
+                }
+                mma_commit(&sm.pv_done[t & 3]);
+                mma_commit(&sm.empty[slot]);
+                if (t + kAhead < T) ok = scores(t + kAhead);
+            }
+            mma_commit(&sm.done);  // always: the drain waits on it
+        }
+    } else if (warp >= 4) {
+        const int total = 2 * T;
+        if constexpr (!C::SPLIT) {
+            // ---------------- fp16: TMA straight into the operand layout
+            if (lane == 0) {
+                for (int f = 0; f < total; f++) {
+                    const int slot = f % C::NS;
+                    if (f >= C::NS && !twait1(&sm.empty[slot], (f / C::NS - 1) & 1, sm)) break;
+                    bool isv;
+                    int t;
+                    fill_item(f, T, isv, t);
+                    mbar_arrive_expect_tx(&sm.full[slot], C::PART);
+                    for (int x = 0; x < D; x += 64)
+                        tma_load_2d(smem + slot * C::SLOT + x * BK * 2, isv ? &map_v : &map_k, x, (int)(row0 + t * BK),
+                                    &sm.full[slot]);
+                    sm.fills = f + 1;
+                }
+            }
+        } else {
+            // ---------------- fp32, Q8_0, Q4_0: registers -> fp16 parts
+            const int ct = tid - 128;
+            RawTile<TYPE, D> raw[2];
+            auto fetch = [&](int f, RawTile<TYPE, D>& r) {
+                if (f >= total) return;
+                bool isv;
+                int t;
+                fill_item(f, T, isv, t);
+                load_tile<TYPE, D>(isv ? a.c.v : a.c.k, isv ? a.c.vs : a.c.ks, row0 + (int64_t)t * BK, ct, lane, r);
+            };
+            fetch(0, raw[0]);
+            fetch(1, raw[1]);
+            int ev_max = -126;
+            bool ok = true;
+            auto fill = [&](int f, RawTile<TYPE, D>& r) {
+                bool isv;
+                int t;
+                fill_item(f, T, isv, t);
+                float m = raw_max<TYPE, D>(r);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                if (TYPE == AF_F32) {  // the warps hold different rows: exchange their maxima
+                    if (lane == 0) {
+                        sm.wmax[f & 1][warp - 4] = m;
+                        mbar_arrive(&sm.max_bar);
+                    }
+                    if (!twait(&sm.max_bar, f & 1, sm)) return false;
+#pragma unroll
+                    for (int w = 0; w < kConvWarps; w++) m = fmaxf(m, sm.wmax[f & 1][w]);
+                }
+                // largest value in [1, 2), or largest scale times its largest code in [1, 4)
+                int e = max(exponent_of(m), -126);
+                if (TYPE == AF_KV_Q8_0) e = min(e + 6, 127);
+                if (TYPE == AF_KV_Q4_0) e = min(e + 2, 127);
+                e = min(e, 126);
+                if (isv) {  // follows the largest tile seen; smaller ones come at most 2^-8 below it
+                    ev_max = max(ev_max, e);
+                    e = max(e, ev_max - 8);
+                }
+                const int slot = f % C::NS;
+                if (f >= C::NS && !twait(&sm.empty[slot], (f / C::NS - 1) & 1, sm)) return false;
+                store_tile<TYPE, D>(smem + slot * C::SLOT, r, e, ct);
+                if (ct == 0) {
+                    if (isv)
+                        sm.ev[t & 7] = e;
+                    else
+                        sm.ek[t & 7] = pow2i(e);
+                }
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.full[slot]);
+                return true;
+            };
+            for (int f = 0; ok && f < total; f += 2) {
+                ok = fill(f, raw[0]);
+                fetch(f + 2, raw[0]);
+                if (ok && f + 1 < total) ok = fill(f + 1, raw[1]);
+                fetch(f + 3, raw[1]);
+            }
+        }
+    } else {
+        // ---------------- softmax: thread = row
+        const int r = r0 + tid;
+        const bool live = r < R;
+        const uint32_t lane_addr = tmem + ((uint32_t)(warp * 32) << 16);
+        float rowf = 1.f;
+        {  // q: scaled to [1, 2), split, into tensor memory
+            const float* q = a.q + (live ? (int64_t)(r / G) * a.ldq + (int64_t)(g * G + r % G) * D : 0);
+            const float sc = live ? rsqrtf((float)D) * 1.4426950408889634f : 0.f;
+            float mx = 0.f;
+#pragma unroll 8
+            for (int i = 0; i < D; i += 4) {
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(q + i));
+                mx = fmaxf(mx, fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))));
+            }
+            const int e = min(max(exponent_of(mx * sc), -100), 126);
+            rowf = pow2i(e);
+            const float k = pow2i(-e);
+#pragma unroll 1
+            for (int h = 0; h < D / 64; h++) {
+                uint32_t hi[32], lo[32];
+#pragma unroll
+                for (int i = 0; i < 64; i += 4) {
+                    const float4 x = __ldcg(reinterpret_cast<const float4*>(q + h * 64 + i));
+                    const float z = live ? 1.f : 0.f;  // (a select: what a dead row reads may be anything)
+                    split2(live ? x.x * sc * k : z, live ? x.y * sc * k : z, hi[i / 2], lo[i / 2]);
+                    split2(live ? x.z * sc * k : z, live ? x.w * sc * k : z, hi[i / 2 + 1], lo[i / 2 + 1]);
+                }
+                tmem_st32(lane_addr + kQCol + h * 32, hi);
+                tmem_st32(lane_addr + kQCol + D / 2 + h * 32, lo);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.q_ready);
+        }
+        float m_ref = -CUDART_INF_F, l = 0.f;
+        int ev_ref = 0;
+        bool ok = true;
+        for (int t = 0; t < T; t++) {
+            const int b = t & 3;
+            ok = twait(&sm.s_full[b], (t >> 2) & 1, sm);
+            if (!ok) break;
+            float f = rowf;
+            int ev = 0;
+            if (C::SPLIT) {
+                const int fk = fill_k(t), fv = fill_v(t, T);
+                ok = twait(&sm.full[fv % C::NS], (fv / C::NS) & 1, sm);
+                if (!ok) break;
+                (void)fk;
+                f *= sm.ek[t & 7];
+                ev = sm.ev[t & 7];
+                if (t == 0) ev_ref = ev;
+            }
+            tc_fence_after();
+            const uint32_t s_addr = lane_addr + kSCol + b * BK;
+            float s[BK];
+            tmem_ld64(s_addr, s);
+            float mx[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) mx[i] = fmaxf(s[i], s[i + 4]);
+#pragma unroll
+            for (int i = 8; i < BK; i++) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
+            const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
+            const bool move = mt > m_ref + kLazy2;
+            if (__any_sync(0xffffffffu, move || ev - ev_ref > 2)) {
+                float up = 1.f;
+                if (mt > m_ref) {
+                    up = ex2u(m_ref - mt);
+                    m_ref = mt;
+                    l *= up;
+                }
+                if (ev > ev_ref) {
+                    up *= ex2u((float)(ev_ref - ev));
+                    ev_ref = ev;
+                }
+                if (t > 0) {  // the output holds the tiles before t: wait for them, rescale this warp's rows
+                    ok = twait(&sm.pv_done[(t - 1) & 3], ((t - 1) >> 2) & 1, sm);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        float o[32];
+                        uint32_t u[32];
+                        tmem_ld32(lane_addr + c, o);
+#pragma unroll
+                        for (int i = 0; i < 32; i++) u[i] = __float_as_uint(o[i] * up);
+                        tmem_st32(lane_addr + c, u);
+                    }
+                    tmem_st_wait();
+                }
+            }
+            const float shift = C::SPLIT ? (float)(ev - ev_ref) : 0.f;
+            const float mb = (m_ref == -CUDART_INF_F ? 0.f : m_ref) - kBias2 - shift;
+            float sum[4] = {};
+            uint32_t hi[32], lo[32];
+#pragma unroll
+            for (int i = 0; i < BK; i += 2) {
+                const float p0 = ex2u(s[i] * f - mb), p1 = ex2u(s[i + 1] * f - mb);
+                sum[(i >> 1) & 1] += p0;
+                sum[2 + ((i >> 1) & 1)] += p1;
+                split2(p0, p1, hi[i / 2], lo[i / 2]);
+            }
+            const float add = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            l += C::SPLIT ? add * ex2u(-shift) : add;
+            tmem_st32(s_addr, hi);
+            tmem_st32(s_addr + BK / 2, lo);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.p_full[b]);
+        }
+        // ---- this split's part of the row
+        ok = ok && twait(&sm.done, 0, sm);
+        const int64_t rows = (int64_t)a.c.KVH * R;
+        const int64_t row = (int64_t)split * rows + (int64_t)g * R + r;
+        float2* ml = reinterpret_cast<float2*>(a.ws + parts * rows * D);
+        if (ok) {
+            tc_fence_after();
+            const float up = C::SPLIT ? pow2i(ev_ref) : 1.f;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                float o[32];
+                tmem_ld32(lane_addr + c, o);
+                if (live) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        *reinterpret_cast<float4*>(a.ws + row * D + c + i) =
+                            make_float4(o[i] * up, o[i + 1] * up, o[i + 2] * up, o[i + 3] * up);
+                }
+            }
+        }
+        if (live) ml[row] = ok ? make_float2(m_ref, l) : make_float2(CUDART_NAN_F, CUDART_NAN_F);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (sm.abort && tid == 0) {  // let what was issued finish before leaving
+        mbar_wait_bounded(&sm.done, 0);
+        if (!C::SPLIT)
+            for (int f = max(0, sm.fills - C::NS); f < sm.fills; f++) mbar_wait_bounded(&sm.full[f % C::NS], (f / C::NS) & 1);
+    }
+    __syncthreads();
+    if (warp == C::MMA_WARP) {
+        tc_fence_after();
+        tmem_free(tmem, kTmem);
+    }
+    pdl_wait();  // the kernel that does the other slots: the merge waits for this one alone
+}
+
+template <int TYPE, int D>
+cudaError_t go(const TreeArgs& a, const TreeTcPlan& p, int parts, cudaStream_t s) {
+    using C = TcCfgT<TYPE, D>;
+    auto k = attn_tree_tc_kernel<TYPE, D>;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e) return e;
+    CUtensorMap mk = {}, mv = {};
+    if (TYPE == AF_F16) {
+        const uint64_t rows = (uint64_t)a.c.KVH * a.c.ctx;
+        if (!make_tmap_f16(&mk, a.c.k, rows, D, D, 64, BK) || !make_tmap_f16(&mv, a.c.v, rows, D, D, 64, BK))
+            return cudaErrorInvalidValue;
+    }
+    cudaLaunchConfig_t cfg = {};
+    const int R = a.n * (a.H / a.c.KVH);
+    cfg.gridDim = dim3(p.splits, a.c.KVH, (R + kRows - 1) / kRows);
+    cfg.blockDim = dim3(C::WARPS * 32);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, mk, mv, a, p.tiles, p.splits, parts);
+}
+
+template <int TYPE>
+cudaError_t go_type(const TreeArgs& a, const TreeTcPlan& p, int parts, cudaStream_t s) {
+    return a.c.D == 64 ? go<TYPE, 64>(a, p, parts, s) : go<TYPE, 128>(a, p, parts, s);
+}
+
+}  // namespace
+
+TreeTcPlan tree_tc_plan(int H, int KVH, int past, int n) {
+    TreeTcPlan p;
+    const int R = n * (H / KVH);
+    const int tiles = past / BK;
+    if (R <= 32 || tiles < 4) return p;
+    p.tiles = tiles;
+    const int64_t ctas = (int64_t)KVH * ((R + kRows - 1) / kRows);
+    // one CTA per SM; at least four tiles each
+    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(num_sms() / ctas, tiles / 4));
+    return p;
+}
+
+cudaError_t launch_attn_tree_tc(const TreeArgs& a, const TreeTcPlan& p, int parts, cudaStream_t s) {
+    switch (a.c.type) {
+        case AF_F32: return go_type<AF_F32>(a, p, parts, s);
+        case AF_F16: return go_type<AF_F16>(a, p, parts, s);
+        case AF_KV_Q8_0: return go_type<AF_KV_Q8_0>(a, p, parts, s);
+        default: return go_type<AF_KV_Q4_0>(a, p, parts, s);
+    }
+}
+
+}  // namespace af

@@ -51,6 +51,14 @@ struct TreeArgs {
     int64_t ldo = 0;
     float* ws = nullptr;
 };
+// The part of a call that the tcgen05 kernel takes (attn_tree_tc.cu): whole 64-slot tiles of the past; splits = 0: none.
+struct TreeTcPlan {
+    int tiles = 0, splits = 0;
+};
+TreeTcPlan tree_tc_plan(int H, int KVH, int past, int n);
+// Writes parts [0, splits) of the workspace's `parts`, and completes after the kernel launched before it has.
+cudaError_t launch_attn_tree_tc(const TreeArgs& a, const TreeTcPlan& p, int parts, cudaStream_t s);
+
 size_t attn_tree_ws_bytes(int H, int KVH, int D, int type, int past, int n);
 cudaError_t launch_attn_tree(const TreeArgs& a, cudaStream_t s);
 

@@ -305,14 +305,6 @@ __device__ __forceinline__ void deq_blk(const RawBlk<AF_Q6_K>& b, uint4 (&hi)[4]
     }
 }
 
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
-            "r"(smem_u32(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
-        : "memory");
-}
-
 struct TcSmem {
     uint64_t xfull[kMaxStages];  // X tiles landed (TMA transaction bytes)
     uint64_t afull[kMaxStages];  // W tile stored in TMEM (one arrival per quadrant warp)

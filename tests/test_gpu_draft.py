@@ -395,6 +395,7 @@ def filled(af, t, rng, kvh, d, ctx, m, spread=1.0):
 ATTN = [  # H, KVH, D, past, n
     (8, 4, 64, 0, 1), (8, 4, 64, 31, 1), (1, 1, 64, 1, 1), (32, 8, 128, 300, 16), (32, 8, 64, 1024, 17),
     (12, 4, 128, 77, 5), (5, 1, 64, 129, 33), (64, 1, 128, 500, 3), (32, 8, 128, 4097, 64), (8, 8, 128, 0, 100),
+    (32, 4, 64, 640, 100), (8, 8, 128, 257, 200), (3, 1, 128, 3000, 40), (24, 8, 64, 2111, 300), (64, 1, 64, 320, 2),
     (32, 4, 64, 15, 31), (16, 2, 128, 255, 128), (7, 7, 64, 63, 9), (2, 2, 128, 3, 700), (4, 1, 64, 1, 1024),
 ]
 
@@ -475,10 +476,10 @@ def test_attention_tree_wide_scores_and_small_values(af, t):
 
 @pytest.mark.parametrize("t,scale", [("f32", 1e-4), ("f32", 3e4), ("f16", 1e-4), ("f16", 1e4), ("q8_0", 1e-3), ("q8_0", 1e4),
                                      ("q4_0", 1e-3), ("q4_0", 1e4)])
-@pytest.mark.parametrize("n", [3, 70])
-def test_attention_tree_scale_of_values(af, t, scale, n):
+@pytest.mark.parametrize("past,n", [(200, 3), (200, 70), (900, 70)])
+def test_attention_tree_scale_of_values(af, t, scale, past, n):
     """The result scales with the values: nothing under- or overflows on the way, at small row counts or large."""
-    H, KVH, D, past = 8, 2, 64, 200
+    H, KVH, D = 8, 2, 64
     rng = np.random.default_rng(13)
     m = past + n
     k = rng.standard_normal((m, KVH * D)).astype(np.float32)
