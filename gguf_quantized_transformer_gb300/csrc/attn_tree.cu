@@ -156,6 +156,7 @@ struct TreeCfg {
     static constexpr int OV = KS * RB, OKS = 2 * KS * RB, OVS = OKS + KS * SB;    // V, K scales, V scales in a stage
     static constexpr int STAGE = 2 * KS * (RB + SB);
     static constexpr int NST = 192 * 1024 / (NW * STAGE) < 4 ? 192 * 1024 / (NW * STAGE) : 4;  // stages of a warp
+    static constexpr int DP = D + (TYPE == AF_F16 ? 8 : 4);                       // padded output row of the join
     static constexpr int KQ = TYPE == AF_F32 ? D / 8 : D / 16;                    // mma steps along a head
     // 16-byte chunk permutation of row `key`, so that the fragment loads of a warp meet all banks
     static __device__ __forceinline__ int swk(int key) {
@@ -182,7 +183,7 @@ constexpr int tree_q_bytes() {
 template <int TYPE, int D, int MT>
 constexpr int tree_smem() {
     using C = TreeCfg<TYPE, D>;
-    constexpr int ring = C::NW * C::NST * C::STAGE, join = C::NW * 16 * MT * (D + 2) * 4;
+    constexpr int ring = C::NW * C::NST * C::STAGE, join = C::NW * 16 * MT * (C::DP + 2) * 4;
     return tree_q_bytes<TYPE, D, MT>() + (ring > join ? ring : join);
 }
 
@@ -274,14 +275,23 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D>::NW * 32, 1) attn_tree_kernel
     }
 
     // ---- q fragments: a warp scales and splits a row; lane l holds dims 4l..4l+3
-    for (int r = warp; r < ROWS; r += NW) {
-        float x[4] = {};
-        if (r0 + r < R && lane < D / 4) {
+    constexpr int RPW = (ROWS + NW - 1) / NW;
+    float4 qin[RPW];
+#pragma unroll
+    for (int i = 0; i < RPW; i++) {
+        const int r = warp + i * NW;
+        qin[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < ROWS && r0 + r < R && lane < D / 4) {
             const int node = (r0 + r) / G, head = g * G + (r0 + r) % G;
-            const float4 f = *reinterpret_cast<const float4*>(a.q + (int64_t)node * a.ldq + (int64_t)head * D + 4 * lane);
-            const float sc = rsqrtf((float)D) * kLog2eT;
-            x[0] = f.x * sc, x[1] = f.y * sc, x[2] = f.z * sc, x[3] = f.w * sc;
+            qin[i] = *reinterpret_cast<const float4*>(a.q + (int64_t)node * a.ldq + (int64_t)head * D + 4 * lane);
         }
+    }
+#pragma unroll
+    for (int ri = 0; ri < RPW; ri++) {
+        const int r = warp + ri * NW;
+        if (r >= ROWS) break;
+        const float sc = rsqrtf((float)D) * kLog2eT;
+        float x[4] = {qin[ri].x * sc, qin[ri].y * sc, qin[ri].z * sc, qin[ri].w * sc};
         if (TYPE != AF_F32) {  // a power of two brings the row's largest value to [1, 2)
             float mx = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
 #pragma unroll
@@ -329,18 +339,23 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D>::NW * 32, 1) attn_tree_kernel
     __syncthreads();
     float rowf[MT][2];
     const unsigned* mrow[MT][2];  // mask words of this thread's rows
+    const int words = (a.n + 31) / 32;
 #pragma unroll
     for (int mt = 0; mt < MT; mt++)
 #pragma unroll
         for (int h = 0; h < 2; h++) {
             const int r = mt * 16 + h * 8 + j;
             rowf[mt][h] = TYPE == AF_F32 ? 1.f : sm_rowf[r];
-            mrow[mt][h] = r0 + r < R ? a.mask + (int64_t)((r0 + r) / G) * ((a.n + 31) / 32) : nullptr;
+            mrow[mt][h] = r0 + r < R ? a.mask + (int64_t)((r0 + r) / G) * words : nullptr;
         }
-    auto sees = [&](int mt, int h, int key) {  // slot key of the cache
-        if (key < a.past) return true;
-        const int t = key - a.past;
-        return t < a.n && mrow[mt][h] && (mrow[mt][h][t >> 5] >> (t & 31) & 1);
+    // bit i: the row sees slot key0 + i of the cache (i < 16)
+    auto window = [&](int mt, int h, int key0) {
+        const int t = key0 - a.past, w = t >> 5;  // t < 0: slots of the past, which every row sees
+        const unsigned* m = mrow[mt][h];
+        const unsigned lo = w < 0 ? ~0u : (m && w < words ? m[w] : 0u);
+        const unsigned hi = w + 1 < 0 ? ~0u : (m && w + 1 < words ? m[w + 1] : 0u);
+        const unsigned x = __funnelshift_r(lo, hi, t & 31);
+        return t + 16 <= a.n ? x : x & ((1u << max(a.n - t, 0)) - 1u);  // nothing behind the last node
     };
 
     float o[MT][NT][4] = {}, m_ref[MT][2], l[MT][2] = {};
@@ -364,6 +379,13 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D>::NW * 32, 1) attn_tree_kernel
             const int key0 = st * KS + grp * 16;
             if (key0 >= keys) break;
             const uint32_t kb = base + grp * 16 * C::RB, vb = kb + C::OV;
+            const bool nodes = key0 + 16 > a.past;  // slots of nodes, or behind the last one
+            unsigned see[MT][2] = {};
+            if (nodes)
+#pragma unroll
+                for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+                    for (int h = 0; h < 2; h++) see[mt][h] = window(mt, h, key0);
             // ---- scores of 16 slots
             float s[MT][2][4] = {};
             if constexpr (C::QUANT) {
@@ -463,7 +485,6 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D>::NW * 32, 1) attn_tree_kernel
                 }
             }
             // ---- mask and softmax
-            const bool nodes = key0 + 16 > a.past;  // slots of nodes, or behind the last one
 #pragma unroll
             for (int mt = 0; mt < MT; mt++)
 #pragma unroll
@@ -471,7 +492,7 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D>::NW * 32, 1) attn_tree_kernel
 #pragma unroll
                     for (int i = 0; i < 4; i++) {
                         if (TYPE != AF_F32) s[mt][t][i] *= rowf[mt][i >> 1];
-                        if (nodes && !sees(mt, i >> 1, key0 + t * 8 + 2 * c + (i & 1))) s[mt][t][i] = -CUDART_INF_F;
+                        if (nodes && !(see[mt][i >> 1] >> (t * 8 + 2 * c + (i & 1)) & 1)) s[mt][t][i] = -CUDART_INF_F;
                     }
             float mx[MT][2];
             bool move = false;
@@ -676,7 +697,7 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D>::NW * 32, 1) attn_tree_kernel
                             const float p0 = key < 8 ? s[mt][0][2 * h] : s[mt][1][2 * h];
                             const float p1 = key < 8 ? s[mt][0][2 * h + 1] : s[mt][1][2 * h + 1];
                             const float p = __shfl_sync(0xffffffffu, (key & 1) ? p1 : p0, src);
-                            if (!sees(mt, h, key0 + key)) continue;
+                            if (!(see[mt][h] >> key & 1)) continue;
 #pragma unroll
                             for (int t = 0; t < NT; t++)
 #pragma unroll
@@ -695,7 +716,7 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D>::NW * 32, 1) attn_tree_kernel
 
     // ---- join the warps: [warp][row][D] outputs, then [warp][row] (m, l)
     float* so = reinterpret_cast<float*>(smem + tree_q_bytes<TYPE, D, MT>());
-    float2* sml = reinterpret_cast<float2*>(so + NW * ROWS * D);
+    float2* sml = reinterpret_cast<float2*>(so + NW * ROWS * C::DP);
     const float back = C::QUANT ? 1.f / vinv : 1.f;
 #pragma unroll
     for (int mt = 0; mt < MT; mt++)
@@ -706,11 +727,20 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D>::NW * 32, 1) attn_tree_kernel
             x += __shfl_xor_sync(0xffffffffu, x, 1);
             x += __shfl_xor_sync(0xffffffffu, x, 2);
             if (c == 0) sml[warp * ROWS + r] = make_float2(m_ref[mt][h], x);
-            float* dst = so + (warp * ROWS + r) * D;
+            float* dst = so + (warp * ROWS + r) * C::DP;
+            if (TYPE == AF_F16) {
 #pragma unroll
-            for (int t = 0; t < NT; t++)
+                for (int t = 0; t < NT; t++)
+                    *reinterpret_cast<float2*>(dst + C::odim(t, 2 * c)) = make_float2(o[mt][t][2 * h], o[mt][t][2 * h + 1]);
+            } else {  // tiles t..t+3 are neighbouring dims
 #pragma unroll
-                for (int i = 0; i < 2; i++) dst[C::odim(t, 2 * c + i)] = o[mt][t][2 * h + i] * back;
+                for (int t = 0; t < NT; t += 4)
+#pragma unroll
+                    for (int i = 0; i < 2; i++)
+                        *reinterpret_cast<float4*>(dst + C::odim(t, 2 * c + i)) =
+                            make_float4(o[mt][t][2 * h + i] * back, o[mt][t + 1][2 * h + i] * back,
+                                        o[mt][t + 2][2 * h + i] * back, o[mt][t + 3][2 * h + i] * back);
+            }
         }
     __syncthreads();
     float* part = a.ws;
@@ -728,7 +758,7 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D>::NW * 32, 1) attn_tree_kernel
             const float2 ml = sml[w * ROWS + r];
             if (ml.x == -CUDART_INF_F && ml.y == 0.f) continue;  // this warp saw nothing
             const float f = ex2t(ml.x - m);
-            const float4 v = *reinterpret_cast<const float4*>(so + (w * ROWS + r) * D + d);
+            const float4 v = *reinterpret_cast<const float4*>(so + (w * ROWS + r) * C::DP + d);
             num.x += f * v.x, num.y += f * v.y, num.z += f * v.z, num.w += f * v.w;
             den += f * ml.y;
         }
@@ -763,15 +793,27 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(TreeArgs a, int splits)
     float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
     float den = 0.f;
     const int d = 4 * lane;
-#pragma unroll 8
-    for (int s = 0; s < splits; s++) {
-        const float2 x = __ldcg(ml + (int64_t)s * rows + row);
-        const float4 v = d < D ? __ldcg(reinterpret_cast<const float4*>(a.ws + ((int64_t)s * rows + row) * D + d))
-                               : make_float4(0.f, 0.f, 0.f, 0.f);
-        const float f = x.x == -CUDART_INF_F && x.y == 0.f ? 0.f : ex2t(x.x - m);
-        num.x += f * v.x, num.y += f * v.y, num.z += f * v.z, num.w += f * v.w;
-        den += f * x.y;
+    const float* part = a.ws + (int64_t)row * D + (d < D ? d : 0);
+    for (int s0 = 0; s0 < splits; s0 += 32) {
+        float2 x = make_float2(-CUDART_INF_F, 0.f);
+        if (s0 + lane < splits) x = __ldcg(ml + (int64_t)(s0 + lane) * rows + row);
+        const float w = x.x == -CUDART_INF_F && x.y == 0.f ? 0.f : ex2t(x.x - m);
+        den += w * x.y;
+        for (int s1 = s0; s1 < min(splits, s0 + 32); s1 += 8) {
+            float4 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                v[i] = s1 + i < splits ? __ldcg(reinterpret_cast<const float4*>(part + (int64_t)(s1 + i) * rows * D))
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const float f = __shfl_sync(0xffffffffu, w, (s1 - s0 + i) & 31);
+                num.x += f * v[i].x, num.y += f * v[i].y, num.z += f * v[i].z, num.w += f * v[i].w;
+            }
+        }
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
     if (d >= D) return;
     const float inv = den == 0.f ? 0.f : 1.f / den;
     const int g = row / R, node = (row % R) / G, head = g * G + row % R % G;

@@ -11,7 +11,7 @@
 // Both products take their A operand (q, p) from tensor memory and B from shared memory: K rows [slot][dim] are
 // K-major, V rows [slot][dim] MN-major, so neither is transposed and both have the cache's own order:
 //   fp16 cache    TMA copies 64 slots x 64 dims boxes into the SWIZZLE_128B layout; two products (hi, lo of q or p)
-//   fp32, Q8_0, Q4_0  eight warps read the tile through registers (two tiles ahead) and write it as fp16 hi and lo
+//   fp32, Q8_0, Q4_0  eight warps read the tile through registers (three or four tiles ahead) and write it as fp16 hi and lo
 //                 parts in the same layout; three products (the dropped lo lo is 2^-22 relative).  A tile is scaled
 //                 by a power of two that brings its largest value (or scale) near 1, so fp16's range never binds:
 //                 K's goes into the score's factor, V's follows the tiles through a running exponent whose moves
@@ -44,6 +44,7 @@ struct TcCfgT {
     static constexpr int PART = BK * D * 2;                  // one fp16 operand of a tile
     static constexpr int SLOT = PART * (SPLIT ? 2 : 1);      // hi (and lo)
     static constexpr int NS = SPLIT ? (D == 128 ? 7 : 8) : (D == 128 ? 12 : 16);
+    static constexpr int QS = kRows * D * 4 / SLOT;          // the last slots, through which q and the output pass
     static constexpr int WARPS = 4 + (SPLIT ? kConvWarps : 1) + 1;
     static constexpr int MMA_WARP = WARPS - 1;
     // at least more than half of an SM's shared memory: a CTA takes all of its tensor memory
@@ -97,6 +98,12 @@ __device__ __forceinline__ void fill_item(int f, int T, bool& isv, int& t) {
         isv = true;
         t = f - T;
     }
+}
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 __device__ __forceinline__ float ex2u(float x) {
@@ -186,9 +193,10 @@ __device__ __forceinline__ void load_tile(const void* base, const __half* scales
     for (int i = 0; i < RawTile<TYPE, D>::N; i++) {
         const int idx = i * kConvWarps * 32 + ct;  // row idx / CPR, chunk idx % CPR: consecutive in memory
         if constexpr (TYPE == AF_F32) {
-            const uint4* p = reinterpret_cast<const uint4*>((const float*)base + row * D + (int64_t)idx * 8);
-            r.c[i].a = __ldcg(p);
-            r.c[i].b = __ldcg(p + 1);
+            asm volatile("ld.global.cg.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=r"(r.c[i].a.x), "=r"(r.c[i].a.y), "=r"(r.c[i].a.z), "=r"(r.c[i].a.w), "=r"(r.c[i].b.x),
+                           "=r"(r.c[i].b.y), "=r"(r.c[i].b.z), "=r"(r.c[i].b.w)
+                         : "l"((const float*)base + row * D + (int64_t)idx * 8));
         } else {
             if constexpr (TYPE == AF_KV_Q8_0)
                 r.c[i].a = __ldcg(reinterpret_cast<const uint2*>((const uint8_t*)base + row * D + (int64_t)idx * 8));
@@ -289,7 +297,7 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
     extern __shared__ uint8_t smem_raw[];
     __shared__ TcState sm;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int G = a.H / a.c.KVH, R = a.n * G;
     const int split = blockIdx.x, g = blockIdx.y, r0 = blockIdx.z * kRows;
     const int t0 = (int)((int64_t)tiles * split / splits), T = (int)((int64_t)tiles * (split + 1) / splits) - t0;
@@ -320,50 +328,59 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
     const uint32_t tmem = sm.tmem_base;
 
     if (warp == C::MMA_WARP) {
-        // ---------------- MMA issuer
-        if (lane == 0) {
-            const uint32_t sbase = smem_u32(smem);
-            bool ok = twait1(&sm.q_ready, 0, sm);
+        // ---------------- MMA issuer: the whole warp walks the tiles (so that descriptors stay in uniform
+        // registers), one elected lane issues
+        const bool lead = elect_one();
+        const uint32_t sbase = smem_u32(smem);
+        const uint64_t kd0 = umma_desc_sw128(sbase), vd0 = desc_mn(sbase, BK * 128);
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        int slot = 0;
+        unsigned ph = 0;
+        bool ok = twait(&sm.q_ready, 0, sm);
+        auto scores = [&](int t) {
+            if (t >= 4 && !twait(&sm.pv_done[t & 3], ((t - 4) >> 2) & 1, sm)) return false;
+            if (!twait(&sm.full[slot], ph, sm)) return false;
             tc_fence_after();
-            auto scores = [&](int t) {
-                if (t >= 4 && !twait1(&sm.pv_done[t & 3], ((t - 4) >> 2) & 1, sm)) return false;
-                const int f = fill_k(t), slot = f % C::NS;
-                if (!twait1(&sm.full[slot], (f / C::NS) & 1, sm)) return false;
-                tc_fence_after();
-                const uint32_t k = sbase + slot * C::SLOT, d = tmem + kSCol + (t & 3) * BK;
+            if (lead) {
+                const uint64_t kd = kd0 + (uint32_t)(slot * (C::SLOT >> 4));
+                const uint32_t d = tm + kSCol + (t & 3) * BK;
 #pragma unroll
                 for (int kk = 0; kk < D / 16; kk++) {
-                    const uint64_t b = umma_desc_sw128(k + (kk >> 2) * BK * 128 + (kk & 3) * 32);
-                    mma_f16_ts(d, tmem + kQCol + kk * 8, b, kIdS, kk > 0);
-                    mma_f16_ts(d, tmem + kQCol + D / 2 + kk * 8, b, kIdS, 1);
-                    if (C::SPLIT)
-                        mma_f16_ts(d, tmem + kQCol + kk * 8, umma_desc_sw128(k + C::PART + (kk >> 2) * BK * 128 + (kk & 3) * 32),
-                                   kIdS, 1);
+                    const uint64_t b = kd + (((kk >> 2) * BK * 128 + (kk & 3) * 32) >> 4);
+                    mma_f16_ts(d, tm + kQCol + kk * 8, b, kIdS, kk > 0);
+                    mma_f16_ts(d, tm + kQCol + D / 2 + kk * 8, b, kIdS, 1);
+                    if (C::SPLIT) mma_f16_ts(d, tm + kQCol + kk * 8, b + (C::PART >> 4), kIdS, 1);
                 }
                 mma_commit(&sm.s_full[t & 3]);
                 mma_commit(&sm.empty[slot]);
-                return true;
-            };
-            for (int t = 0; ok && t < min(kAhead, T); t++) ok = scores(t);
-            for (int t = 0; ok && t < T; t++) {
-                const int f = fill_v(t, T), slot = f % C::NS;
-                ok = twait1(&sm.full[slot], (f / C::NS) & 1, sm) && twait1(&sm.p_full[t & 3], (t >> 2) & 1, sm);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t v = sbase + slot * C::SLOT, p = tmem + kSCol + (t & 3) * BK;
+            }
+            __syncwarp();
+            if (++slot == C::NS) slot = 0, ph ^= 1;
+            return true;
+        };
+        for (int t = 0; ok && t < min(kAhead, T); t++) ok = scores(t);
+        for (int t = 0; ok && t < T; t++) {
+            ok = twait(&sm.full[slot], ph, sm) && twait(&sm.p_full[t & 3], (t >> 2) & 1, sm);
+            if (!ok) break;
+            tc_fence_after();
+            if (lead) {
+                const uint64_t vd = vd0 + (uint32_t)(slot * (C::SLOT >> 4));
+                const uint32_t p = tm + kSCol + (t & 3) * BK;
 #pragma unroll
                 for (int kk = 0; kk < BK / 16; kk++) {
-                    const uint64_t b = desc_mn(v + kk * 2048, BK * 128);
-                    mma_f16_ts(tmem, p + kk * 8, b, kIdO, t > 0 || kk > 0);
-                    mma_f16_ts(tmem, p + BK / 2 + kk * 8, b, kIdO, 1);
-                    if (C::SPLIT) mma_f16_ts(tmem, p + kk * 8, desc_mn(v + C::PART + kk * 2048, BK * 128), kIdO, 1);
+                    const uint64_t b = vd + ((kk * 2048) >> 4);
+                    mma_f16_ts(tm, p + kk * 8, b, kIdO, t > 0 || kk > 0);
+                    mma_f16_ts(tm, p + BK / 2 + kk * 8, b, kIdO, 1);
+                    if (C::SPLIT) mma_f16_ts(tm, p + kk * 8, b + (C::PART >> 4), kIdO, 1);
                 }
                 mma_commit(&sm.pv_done[t & 3]);
                 mma_commit(&sm.empty[slot]);
-                if (t + kAhead < T) ok = scores(t + kAhead);
             }
-            mma_commit(&sm.done);  // always: the drain waits on it
+            __syncwarp();
+            if (++slot == C::NS) slot = 0, ph ^= 1;
+            if (t + kAhead < T) ok = scores(t + kAhead);
         }
+        if (lead) mma_commit(&sm.done);  // always: the drain waits on it
     } else if (warp >= 4) {
         const int total = 2 * T;
         if constexpr (!C::SPLIT) {
@@ -372,6 +389,7 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                 for (int f = 0; f < total; f++) {
                     const int slot = f % C::NS;
                     if (f >= C::NS && !twait1(&sm.empty[slot], (f / C::NS - 1) & 1, sm)) break;
+                    if (f == C::NS - C::QS && !twait1(&sm.q_ready, 0, sm)) break;
                     bool isv;
                     int t;
                     fill_item(f, T, isv, t);
@@ -385,7 +403,8 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
         } else {
             // ---------------- fp32, Q8_0, Q4_0: registers -> fp16 parts
             const int ct = tid - 128;
-            RawTile<TYPE, D> raw[2];
+            constexpr int DEP = TYPE == AF_F32 ? 3 : 4;  // tiles in flight
+            RawTile<TYPE, D> raw[DEP];
             auto fetch = [&](int f, RawTile<TYPE, D>& r) {
                 if (f >= total) return;
                 bool isv;
@@ -393,8 +412,8 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                 fill_item(f, T, isv, t);
                 load_tile<TYPE, D>(isv ? a.c.v : a.c.k, isv ? a.c.vs : a.c.ks, row0 + (int64_t)t * BK, ct, lane, r);
             };
-            fetch(0, raw[0]);
-            fetch(1, raw[1]);
+#pragma unroll
+            for (int i = 0; i < DEP; i++) fetch(i, raw[i]);
             int ev_max = -126;
             bool ok = true;
             auto fill = [&](int f, RawTile<TYPE, D>& r) {
@@ -424,6 +443,7 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                 }
                 const int slot = f % C::NS;
                 if (f >= C::NS && !twait(&sm.empty[slot], (f / C::NS - 1) & 1, sm)) return false;
+                if (f == C::NS - C::QS && !twait(&sm.q_ready, 0, sm)) return false;
                 store_tile<TYPE, D>(smem + slot * C::SLOT, r, e, ct);
                 if (ct == 0) {
                     if (isv)
@@ -436,11 +456,12 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                 if (lane == 0) mbar_arrive(&sm.full[slot]);
                 return true;
             };
-            for (int f = 0; ok && f < total; f += 2) {
-                ok = fill(f, raw[0]);
-                fetch(f + 2, raw[0]);
-                if (ok && f + 1 < total) ok = fill(f + 1, raw[1]);
-                fetch(f + 3, raw[1]);
+            for (int f = 0; ok && f < total; f += DEP) {
+#pragma unroll
+                for (int i = 0; i < DEP; i++) {
+                    if (ok && f + i < total) ok = fill(f + i, raw[i]);
+                    fetch(f + i + DEP, raw[i]);
+                }
             }
         }
     } else {
@@ -449,13 +470,31 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
         const bool live = r < R;
         const uint32_t lane_addr = tmem + ((uint32_t)(warp * 32) << 16);
         float rowf = 1.f;
+        // Rows pass through shared memory, so that global accesses are whole rows: chunk c (16 bytes) of row r sits at
+        // c ^ (r & 7).
+        constexpr int CPR = D / 4, RPI = 32 / CPR;  // chunks per row, rows per warp access
+        auto stage = [&](uint8_t* base, int rr, int c) { return reinterpret_cast<float4*>(base + rr * D * 4 + ((c ^ (rr & 7)) << 4)); };
         {  // q: scaled to [1, 2), split, into tensor memory
-            const float* q = a.q + (live ? (int64_t)(r / G) * a.ldq + (int64_t)(g * G + r % G) * D : 0);
+            uint8_t* st = smem + (C::NS - C::QS) * C::SLOT + warp * 32 * D * 4;
+            const int64_t off = live ? (int64_t)(r / G) * a.ldq + (int64_t)(g * G + r % G) * D : 0;
+            const int c = lane % CPR;
+#pragma unroll
+            for (int i0 = 0; i0 < 32; i0 += 16) {
+                float4 x[16 / RPI];
+#pragma unroll
+                for (int i = 0; i < 16 / RPI; i++) {
+                    const int64_t o = __shfl_sync(0xffffffffu, off, i0 + i * RPI + lane / CPR);
+                    x[i] = __ldcg(reinterpret_cast<const float4*>(a.q + o) + c);
+                }
+#pragma unroll
+                for (int i = 0; i < 16 / RPI; i++) *stage(st, i0 + i * RPI + lane / CPR, c) = x[i];
+            }
+            __syncwarp();
             const float sc = live ? rsqrtf((float)D) * 1.4426950408889634f : 0.f;
             float mx = 0.f;
 #pragma unroll 8
-            for (int i = 0; i < D; i += 4) {
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(q + i));
+            for (int i = 0; i < CPR; i++) {
+                const float4 x = *stage(st, lane, i);
                 mx = fmaxf(mx, fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))));
             }
             const int e = min(max(exponent_of(mx * sc), -100), 126);
@@ -465,17 +504,17 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
             for (int h = 0; h < D / 64; h++) {
                 uint32_t hi[32], lo[32];
 #pragma unroll
-                for (int i = 0; i < 64; i += 4) {
-                    const float4 x = __ldcg(reinterpret_cast<const float4*>(q + h * 64 + i));
-                    const float z = live ? 1.f : 0.f;  // (a select: what a dead row reads may be anything)
-                    split2(live ? x.x * sc * k : z, live ? x.y * sc * k : z, hi[i / 2], lo[i / 2]);
-                    split2(live ? x.z * sc * k : z, live ? x.w * sc * k : z, hi[i / 2 + 1], lo[i / 2 + 1]);
-                }
+                for (int i = 0; i < 16; i++) {
+                    const float4 x = *stage(st, lane, h * 16 + i);
+                    split2(live ? x.x * sc * k : 0.f, live ? x.y * sc * k : 0.f, hi[2 * i], lo[2 * i]);  // (what a dead
+                    split2(live ? x.z * sc * k : 0.f, live ? x.w * sc * k : 0.f, hi[2 * i + 1], lo[2 * i + 1]);  // row reads
+                }                                                                                          // may be anything)
                 tmem_st32(lane_addr + kQCol + h * 32, hi);
                 tmem_st32(lane_addr + kQCol + D / 2 + h * 32, lo);
             }
             tmem_st_wait();
             tc_fence_before();
+            fence_proxy_async_shared();  // the slots may be filled
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.q_ready);
         }
@@ -560,20 +599,24 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
         const int64_t rows = (int64_t)a.c.KVH * R;
         const int64_t row = (int64_t)split * rows + (int64_t)g * R + r;
         float2* ml = reinterpret_cast<float2*>(a.ws + parts * rows * D);
-        if (ok) {
+        if (ok) {  // every operand has been read: the ring is free
             tc_fence_after();
             const float up = C::SPLIT ? pow2i(ev_ref) : 1.f;
+            uint8_t* st = smem + warp * 32 * D * 4;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 float o[32];
                 tmem_ld32(lane_addr + c, o);
-                if (live) {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        *reinterpret_cast<float4*>(a.ws + row * D + c + i) =
-                            make_float4(o[i] * up, o[i + 1] * up, o[i + 2] * up, o[i + 3] * up);
-                }
+                for (int i = 0; i < 32; i += 4)
+                    *stage(st, lane, (c + i) / 4) = make_float4(o[i] * up, o[i + 1] * up, o[i + 2] * up, o[i + 3] * up);
             }
+            __syncwarp();
+            const int rw = r0 + warp * 32;  // the warp's first row
+            float4* dst = reinterpret_cast<float4*>(a.ws + ((int64_t)split * rows + (int64_t)g * R + rw) * D);
+#pragma unroll 4
+            for (int i = lane / CPR; i < 32; i += RPI)
+                if (rw + i < R) dst[i * CPR + lane % CPR] = *stage(st, i, lane % CPR);
         }
         if (live) ml[row] = ok ? make_float2(m_ref, l) : make_float2(CUDART_NAN_F, CUDART_NAN_F);
     }
