@@ -11,11 +11,13 @@
 // Both products take their A operand (q, p) from tensor memory and B from shared memory: K rows [slot][dim] are
 // K-major, V rows [slot][dim] MN-major, so neither is transposed and both have the cache's own order:
 //   fp16 cache    TMA copies 64 slots x 64 dims boxes into the SWIZZLE_128B layout; two products (hi, lo of q or p)
-//   fp32, Q8_0, Q4_0  eight warps read the tile through registers (three or four tiles ahead) and write it as fp16 hi and lo
-//                 parts in the same layout; three products (the dropped lo lo is 2^-22 relative).  A tile is scaled
-//                 by a power of two that brings its largest value (or scale) near 1, so fp16's range never binds:
-//                 K's goes into the score's factor, V's follows the tiles through a running exponent whose moves
-//                 rescale the output like the softmax's maximum.
+//   fp32, Q8_0, Q4_0  bulk copies bring the raw rows into a staging ring, four warps for K and four for V write them
+//                 as fp16 hi and lo parts in the same layout; three products (the dropped lo lo is 2^-22 relative).
+//                 A tile is scaled by a power of two that brings its largest value (or scale) near 1, so fp16's
+//                 range never binds: K's goes into the score's factor, V's follows the tiles through a running
+//                 exponent whose moves rescale the output like the softmax's maximum.
+//                 (Rows read through registers instead, three tiles ahead: 192 us where this takes 108 at 64 nodes
+//                 over 30720 fp32 slots; the warp's loads of several tiles share its few scoreboards.)
 // Warps 0-3 are the softmax (a thread owns a row: the whole tile of its scores in registers, maximum, p, sum), one
 // warp issues the MMAs, scores of up to three tiles ahead of the outputs, so the tensor pipe always has a queue.
 // The reference maximum moves lazily, as in attn_tree.cu, with the same factor 2^8 in p.
@@ -36,32 +38,53 @@ constexpr int kAhead = 3;      // tiles whose scores are issued ahead of the out
 constexpr int kQCol = 128, kSCol = 256, kTmem = 512;
 constexpr int kRows = 128;
 constexpr float kLazy2 = 4.f, kBias2 = 8.f;  // as attn_tree.cu's
-constexpr int kConvWarps = 8;
+constexpr int kConvWarps = 4;  // for K, and as many for V
 
 template <int TYPE, int D>
 struct TcCfgT {
     static constexpr bool SPLIT = TYPE != AF_F16;
     static constexpr int PART = BK * D * 2;                  // one fp16 operand of a tile
     static constexpr int SLOT = PART * (SPLIT ? 2 : 1);      // hi (and lo)
-    static constexpr int NS = SPLIT ? (D == 128 ? 7 : 8) : (D == 128 ? 12 : 16);
-    static constexpr int QS = kRows * D * 4 / SLOT;          // the last slots, through which q and the output pass
-    static constexpr int WARPS = 4 + (SPLIT ? kConvWarps : 1) + 1;
-    static constexpr int MMA_WARP = WARPS - 1;
+    static constexpr int NS = SPLIT ? (D == 128 ? 2 : 4) : 6;  // operand slots of K, and of V
+    // staging of raw rows: RR rows a slot, NR slots for K and for V
+    static constexpr int RB = TYPE == AF_F32 ? 4 * D : TYPE == AF_KV_Q8_0 ? D : D / 2;
+    static constexpr int SB = TYPE == AF_F32 ? 0 : D / 16;   // scale bytes of a row
+    static constexpr int RR = TYPE == AF_F32 ? BK / 2 : BK;
+    static constexpr int RAW = RR * (RB + SB);
+    static constexpr int NR = !SPLIT ? 0 : TYPE == AF_F32 ? (D == 128 ? 3 : 6) : 5;
+    static constexpr int OFF_V = NS * SLOT, OFF_RAW = 2 * NS * SLOT;
+    static constexpr int QS = kRows * D * 4 / SLOT;          // the last V slots, through which q and the output pass
+    static_assert(QS <= NS, "q fits the V slots");
+    static constexpr int MMA_WARP = 4 + (SPLIT ? 2 * kConvWarps : 0), COPY_WARP = MMA_WARP + 1;  // + 1: V's copies
+    static constexpr int WARPS = COPY_WARP + 2;
     // at least more than half of an SM's shared memory: a CTA takes all of its tensor memory
-    static constexpr int SMEM = (NS * SLOT > 120 * 1024 ? NS * SLOT : 120 * 1024) + 1024;
+    static constexpr int USED = OFF_RAW + 2 * NR * RAW;
+    static constexpr int SMEM = (USED > 120 * 1024 ? USED : 120 * 1024) + 1024;
 };
 
+// Of pairs, [0] is K's and [1] V's.
 struct TcState {
-    uint64_t full[16], empty[16];  // operand slots
+    uint64_t full[2][6], empty[2][6];          // operand slots
+    uint64_t raw_full[2][6], raw_empty[2][6];  // staging slots
     uint64_t s_full[4], p_full[4], pv_done[4];
     uint64_t q_ready, done;
-    uint64_t max_bar;
+    uint64_t max_bar[2];
     uint32_t tmem_base;
-    int fills;
+    int copies[2];    // bulk copies issued, for the drain
     volatile int abort;
     float ek[8];      // 2^exponent of K tiles
     int ev[8];        // exponent of V tiles
-    float wmax[2][kConvWarps];
+    float wmax[2][2][kConvWarps];
+};
+
+// A position in a ring of N slots: its index and the parity of its round.
+template <int N>
+struct Ring {
+    int i = 0;
+    unsigned ph = 0;
+    __device__ __forceinline__ void next() {
+        if (++i == N) i = 0, ph ^= 1;
+    }
 };
 
 __device__ __forceinline__ bool twait(uint64_t* bar, unsigned parity, TcState& sm) {  // whole warp
@@ -81,23 +104,6 @@ __device__ __forceinline__ bool twait1(uint64_t* bar, unsigned parity, TcState& 
     }
     sm.abort = 1;
     return false;
-}
-
-// The order in which operand tiles are filled and consumed: K0 K1 K2 V0 K3 V1 K4 ...: index of K and V of tile t.
-__device__ __forceinline__ int fill_k(int t) { return t + max(0, t - kAhead + 1); }
-__device__ __forceinline__ int fill_v(int t, int T) { return t + min(T, t + kAhead); }
-// its inverse
-__device__ __forceinline__ void fill_item(int f, int T, bool& isv, int& t) {
-    if (f < min(kAhead, T)) {
-        isv = false;
-        t = f;
-    } else if (T > kAhead && f < kAhead + 2 * (T - kAhead)) {
-        isv = ((f - kAhead) & 1) == 0;
-        t = (f - kAhead) / 2 + (isv ? 0 : kAhead);
-    } else {
-        isv = true;
-        t = f - T;
-    }
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -157,7 +163,7 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
     lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
-// ---------------------------------------------------------------- tile loads of the converted cache types
+// ---------------------------------------------------------------- tiles of the converted cache types
 
 // 8 values of a row as they lie in the cache
 template <int TYPE>
@@ -169,52 +175,51 @@ struct Raw8<AF_F32> {
 template <>
 struct Raw8<AF_KV_Q8_0> {
     uint2 a;
-    unsigned short d;
+    __half d;
 };
 template <>
 struct Raw8<AF_KV_Q4_0> {
     uint32_t a;
-    unsigned short d;
+    __half d;
 };
 
+// A thread's chunks of 8 values of a tile: chunk i of thread ct is chunk i * 128 + ct of the rows in order.
 template <int TYPE, int D>
 struct RawTile {
-    static constexpr int N = BK * D / 8 / (kConvWarps * 32);  // chunks of 8 values per thread
-    static constexpr int W = TYPE == AF_F32 ? 1 : BK * (D / 32) / 2 / 32;  // scale words per lane (the whole tile's)
+    static constexpr int N = BK * D / 8 / (kConvWarps * 32);
     Raw8<TYPE> c[N];
-    uint32_t sc[W];
 };
 
-template <int TYPE, int D>
-__device__ __forceinline__ void load_tile(const void* base, const __half* scales, int64_t row, int ct, int lane,
-                                          RawTile<TYPE, D>& r) {
-    constexpr int CPR = D / 8;
+// Chunks [I0, I0 + N / PARTS) from the staged rows.
+template <int TYPE, int D, int PARTS>
+__device__ __forceinline__ void load_raw(const uint8_t* st, int part, int ct, RawTile<TYPE, D>& r) {
+    using C = TcCfgT<TYPE, D>;
+    constexpr int N = RawTile<TYPE, D>::N / PARTS;
 #pragma unroll
-    for (int i = 0; i < RawTile<TYPE, D>::N; i++) {
-        const int idx = i * kConvWarps * 32 + ct;  // row idx / CPR, chunk idx % CPR: consecutive in memory
+    for (int i = 0; i < N; i++) {
+        const int idx = i * kConvWarps * 32 + ct;
+        Raw8<TYPE>& c = r.c[part * N + i];
         if constexpr (TYPE == AF_F32) {
-            asm volatile("ld.global.cg.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                         : "=r"(r.c[i].a.x), "=r"(r.c[i].a.y), "=r"(r.c[i].a.z), "=r"(r.c[i].a.w), "=r"(r.c[i].b.x),
-                           "=r"(r.c[i].b.y), "=r"(r.c[i].b.z), "=r"(r.c[i].b.w)
-                         : "l"((const float*)base + row * D + (int64_t)idx * 8));
+            // the two halves in an order that differs between groups of four lanes: every bank once per access
+            const uint4* p = reinterpret_cast<const uint4*>(st) + idx * 2;
+            const int sw = (ct >> 2) & 1;
+            const uint4 x = p[sw], y = p[sw ^ 1];
+            c.a = sw ? y : x;
+            c.b = sw ? x : y;
         } else {
             if constexpr (TYPE == AF_KV_Q8_0)
-                r.c[i].a = __ldcg(reinterpret_cast<const uint2*>((const uint8_t*)base + row * D + (int64_t)idx * 8));
+                c.a = reinterpret_cast<const uint2*>(st)[idx];
             else
-                r.c[i].a = __ldcg(reinterpret_cast<const uint32_t*>((const uint8_t*)base + row * (D / 2) + (int64_t)idx * 4));
-            r.c[i].d = __ldcg(reinterpret_cast<const unsigned short*>(scales) + (row + idx / CPR) * (D / 32) + (idx % CPR) / 4);
+                c.a = reinterpret_cast<const uint32_t*>(st)[idx];
+            c.d = reinterpret_cast<const __half*>(st + C::RR * C::RB)[idx / 4];
         }
-    }
-    if constexpr (TYPE != AF_F32) {
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(scales + row * (D / 32));
-#pragma unroll
-        for (int i = 0; i < RawTile<TYPE, D>::W; i++) r.sc[i] = __ldcg(w + i * 32 + lane);
     }
 }
 
-// Largest magnitude among this thread's values (fp32) or this lane's scales.
+// Largest magnitude among this thread's values (fp32), or this lane's share of the tile's scales.
 template <int TYPE, int D>
-__device__ __forceinline__ float raw_max(const RawTile<TYPE, D>& r) {
+__device__ __forceinline__ float raw_max(const RawTile<TYPE, D>& r, const uint8_t* st, int lane) {
+    using C = TcCfgT<TYPE, D>;
     float m = 0.f;
     if constexpr (TYPE == AF_F32) {
 #pragma unroll
@@ -224,9 +229,10 @@ __device__ __forceinline__ float raw_max(const RawTile<TYPE, D>& r) {
             for (int e = 0; e < 8; e++) m = fmaxf(m, fabsf(__uint_as_float(w[e])));
         }
     } else {
+        const __half2* w = reinterpret_cast<const __half2*>(st + C::RR * C::RB);
 #pragma unroll
-        for (int i = 0; i < RawTile<TYPE, D>::W; i++) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r.sc[i]));
+        for (int i = 0; i < BK * (D / 32) / 2 / 32; i++) {
+            const float2 f = __half22float2(w[i * 32 + lane]);
             m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
         }
     }
@@ -252,7 +258,7 @@ __device__ __forceinline__ void store_tile(uint8_t* dst, const RawTile<TYPE, D>&
         } else {
             // codes q are exact in fp16, and so is d 2^-e (11 bits); hi = fp16(q d), lo = q d - hi by a fused
             // multiply-add, exact as long as it is not below fp16's smallest step 2^-24
-            const __half2 d2 = __float2half2_rn(__half2float(__ushort_as_half(r.c[i].d)) * down);
+            const __half2 d2 = __float2half2_rn(__half2float(r.c[i].d) * down);
             __half2 q[4];
             if constexpr (TYPE == AF_KV_Q8_0) {
                 const uint32_t x = r.c[i].a.x ^ 0x80808080u, y = r.c[i].a.y ^ 0x80808080u;
@@ -305,19 +311,25 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
 
     pdl_launch_dependents();
     if (tid == 0) {
-        for (int i = 0; i < C::NS; i++) {
-            mbar_init(&sm.full[i], C::SPLIT ? kConvWarps : 1);
-            mbar_init(&sm.empty[i], 1);
+        for (int x = 0; x < 2; x++) {
+            for (int i = 0; i < C::NS; i++) {
+                mbar_init(&sm.full[x][i], C::SPLIT ? kConvWarps : 1);
+                mbar_init(&sm.empty[x][i], 1);
+            }
+            for (int i = 0; i < C::NR; i++) {
+                mbar_init(&sm.raw_full[x][i], C::SB ? 33 : 1);  // the copy's bytes, and each lane's scales
+                mbar_init(&sm.raw_empty[x][i], kConvWarps);
+            }
+            mbar_init(&sm.max_bar[x], kConvWarps);
+            sm.copies[x] = 0;
         }
         for (int i = 0; i < 4; i++) {
-            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.s_full[i], C::SPLIT ? 2 : 1);  // the commit, and the issuer for K's exponent
             mbar_init(&sm.p_full[i], 4);
             mbar_init(&sm.pv_done[i], 1);
         }
         mbar_init(&sm.q_ready, 4);
         mbar_init(&sm.done, 1);
-        mbar_init(&sm.max_bar, kConvWarps);
-        sm.fills = 0;
         sm.abort = 0;
         fence_mbar_init();
     }
@@ -332,17 +344,16 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
         // registers), one elected lane issues
         const bool lead = elect_one();
         const uint32_t sbase = smem_u32(smem);
-        const uint64_t kd0 = umma_desc_sw128(sbase), vd0 = desc_mn(sbase, BK * 128);
+        const uint64_t kd0 = umma_desc_sw128(sbase), vd0 = desc_mn(sbase + C::OFF_V, BK * 128);
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-        int slot = 0;
-        unsigned ph = 0;
+        Ring<C::NS> rk, rv;
         bool ok = twait(&sm.q_ready, 0, sm);
         auto scores = [&](int t) {
             if (t >= 4 && !twait(&sm.pv_done[t & 3], ((t - 4) >> 2) & 1, sm)) return false;
-            if (!twait(&sm.full[slot], ph, sm)) return false;
+            if (!twait(&sm.full[0][rk.i], rk.ph, sm)) return false;
             tc_fence_after();
             if (lead) {
-                const uint64_t kd = kd0 + (uint32_t)(slot * (C::SLOT >> 4));
+                const uint64_t kd = kd0 + (uint32_t)(rk.i * (C::SLOT >> 4));
                 const uint32_t d = tm + kSCol + (t & 3) * BK;
 #pragma unroll
                 for (int kk = 0; kk < D / 16; kk++) {
@@ -352,19 +363,20 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                     if (C::SPLIT) mma_f16_ts(d, tm + kQCol + kk * 8, b + (C::PART >> 4), kIdS, 1);
                 }
                 mma_commit(&sm.s_full[t & 3]);
-                mma_commit(&sm.empty[slot]);
+                mma_commit(&sm.empty[0][rk.i]);
+                if (C::SPLIT) mbar_arrive(&sm.s_full[t & 3]);
             }
             __syncwarp();
-            if (++slot == C::NS) slot = 0, ph ^= 1;
+            rk.next();
             return true;
         };
         for (int t = 0; ok && t < min(kAhead, T); t++) ok = scores(t);
         for (int t = 0; ok && t < T; t++) {
-            ok = twait(&sm.full[slot], ph, sm) && twait(&sm.p_full[t & 3], (t >> 2) & 1, sm);
+            ok = twait(&sm.full[1][rv.i], rv.ph, sm) && twait(&sm.p_full[t & 3], (t >> 2) & 1, sm);
             if (!ok) break;
             tc_fence_after();
             if (lead) {
-                const uint64_t vd = vd0 + (uint32_t)(slot * (C::SLOT >> 4));
+                const uint64_t vd = vd0 + (uint32_t)(rv.i * (C::SLOT >> 4));
                 const uint32_t p = tm + kSCol + (t & 3) * BK;
 #pragma unroll
                 for (int kk = 0; kk < BK / 16; kk++) {
@@ -374,94 +386,114 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                     if (C::SPLIT) mma_f16_ts(tm, p + kk * 8, b + (C::PART >> 4), kIdO, 1);
                 }
                 mma_commit(&sm.pv_done[t & 3]);
-                mma_commit(&sm.empty[slot]);
+                mma_commit(&sm.empty[1][rv.i]);
             }
             __syncwarp();
-            if (++slot == C::NS) slot = 0, ph ^= 1;
+            rv.next();
             if (t + kAhead < T) ok = scores(t + kAhead);
         }
         if (lead) mma_commit(&sm.done);  // always: the drain waits on it
-    } else if (warp >= 4) {
-        const int total = 2 * T;
+    } else if (warp >= C::COPY_WARP) {
+        const int x = warp - C::COPY_WARP;  // 0: K, 1: V
         if constexpr (!C::SPLIT) {
             // ---------------- fp16: TMA straight into the operand layout
             if (lane == 0) {
-                for (int f = 0; f < total; f++) {
-                    const int slot = f % C::NS;
-                    if (f >= C::NS && !twait1(&sm.empty[slot], (f / C::NS - 1) & 1, sm)) break;
-                    if (f == C::NS - C::QS && !twait1(&sm.q_ready, 0, sm)) break;
-                    bool isv;
-                    int t;
-                    fill_item(f, T, isv, t);
-                    mbar_arrive_expect_tx(&sm.full[slot], C::PART);
-                    for (int x = 0; x < D; x += 64)
-                        tma_load_2d(smem + slot * C::SLOT + x * BK * 2, isv ? &map_v : &map_k, x, (int)(row0 + t * BK),
-                                    &sm.full[slot]);
-                    sm.fills = f + 1;
+                Ring<C::NS> r;
+                for (int t = 0; t < T; t++, r.next()) {
+                    if (t >= C::NS && !twait1(&sm.empty[x][r.i], r.ph ^ 1, sm)) break;
+                    if (x == 1 && t == C::NS - C::QS && !twait1(&sm.q_ready, 0, sm)) break;
+                    mbar_arrive_expect_tx(&sm.full[x][r.i], C::PART);
+                    for (int d = 0; d < D; d += 64)
+                        tma_load_2d(smem + (x ? C::OFF_V : 0) + r.i * C::SLOT + d * BK * 2, x ? &map_v : &map_k, d,
+                                    (int)(row0 + t * BK), &sm.full[x][r.i]);
+                    sm.copies[x] = t + 1;
                 }
             }
         } else {
-            // ---------------- fp32, Q8_0, Q4_0: registers -> fp16 parts
-            const int ct = tid - 128;
-            constexpr int DEP = TYPE == AF_F32 ? 3 : 4;  // tiles in flight
-            RawTile<TYPE, D> raw[DEP];
-            auto fetch = [&](int f, RawTile<TYPE, D>& r) {
-                if (f >= total) return;
-                bool isv;
-                int t;
-                fill_item(f, T, isv, t);
-                load_tile<TYPE, D>(isv ? a.c.v : a.c.k, isv ? a.c.vs : a.c.ks, row0 + (int64_t)t * BK, ct, lane, r);
-            };
+            // ---------------- raw rows into the staging ring: one bulk copy, and the scales by the lanes
+            const uint8_t* src = (const uint8_t*)(x ? a.c.v : a.c.k) + row0 * C::RB;
+            const uint8_t* sc = (const uint8_t*)(x ? a.c.vs : a.c.ks) + row0 * C::SB;
+            Ring<C::NR> r;
+            for (int i = 0; i < T * (BK / C::RR); i++, r.next()) {
+                if (i >= C::NR && !twait(&sm.raw_empty[x][r.i], r.ph ^ 1, sm)) break;
+                uint8_t* dst = smem + C::OFF_RAW + (x * C::NR + r.i) * C::RAW;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&sm.raw_full[x][r.i], C::RR * C::RB);
+                    bulk_g2s(dst, src + (int64_t)i * C::RR * C::RB, C::RR * C::RB, &sm.raw_full[x][r.i]);
+                    sm.copies[x] = i + 1;
+                }
+                if (C::SB) {  // rows may start off 16 bytes: 8- or 4-byte copies
+                    constexpr int B = C::SB ? C::SB : 4;
 #pragma unroll
-            for (int i = 0; i < DEP; i++) fetch(i, raw[i]);
+                    for (int k = 0; k < C::RR; k += 32)
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst) + C::RR * C::RB + (k + lane) * B),
+                                     "l"(sc + ((int64_t)i * C::RR + k + lane) * B), "n"(B)
+                                     : "memory");
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sm.raw_full[x][r.i]))
+                                 : "memory");
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+        }
+    } else if (warp >= 4) {
+        if constexpr (C::SPLIT) {
+            // ---------------- fp32, Q8_0, Q4_0: staged rows -> fp16 parts
+            const int x = (warp - 4) / kConvWarps, w = (warp - 4) % kConvWarps, ct = w * 32 + lane;
+            constexpr int PARTS = BK / C::RR;
+            Ring<C::NR> rr;
+            Ring<C::NS> ro;
             int ev_max = -126;
             bool ok = true;
-            auto fill = [&](int f, RawTile<TYPE, D>& r) {
-                bool isv;
-                int t;
-                fill_item(f, T, isv, t);
-                float m = raw_max<TYPE, D>(r);
+            for (int t = 0; t < T; t++, ro.next()) {
+                RawTile<TYPE, D> raw;
+                float m = 0.f;
+#pragma unroll
+                for (int p = 0; p < PARTS; p++) {
+                    ok = ok && twait(&sm.raw_full[x][rr.i], rr.ph, sm);
+                    if (!ok) break;
+                    const uint8_t* st = smem + C::OFF_RAW + (x * C::NR + rr.i) * C::RAW;
+                    load_raw<TYPE, D, PARTS>(st, p, ct, raw);
+                    if (TYPE != AF_F32) m = raw_max<TYPE, D>(raw, st, lane);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.raw_empty[x][rr.i]);
+                    rr.next();
+                }
+                if (!ok) break;
+                if (TYPE == AF_F32) m = raw_max<TYPE, D>(raw, nullptr, lane);
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
                 if (TYPE == AF_F32) {  // the warps hold different rows: exchange their maxima
                     if (lane == 0) {
-                        sm.wmax[f & 1][warp - 4] = m;
-                        mbar_arrive(&sm.max_bar);
+                        sm.wmax[x][t & 1][w] = m;
+                        mbar_arrive(&sm.max_bar[x]);
                     }
-                    if (!twait(&sm.max_bar, f & 1, sm)) return false;
+                    ok = twait(&sm.max_bar[x], t & 1, sm);
+                    if (!ok) break;
 #pragma unroll
-                    for (int w = 0; w < kConvWarps; w++) m = fmaxf(m, sm.wmax[f & 1][w]);
+                    for (int i = 0; i < kConvWarps; i++) m = fmaxf(m, sm.wmax[x][t & 1][i]);
                 }
                 // largest value in [1, 2), or largest scale times its largest code in [1, 4)
                 int e = max(exponent_of(m), -126);
-                if (TYPE == AF_KV_Q8_0) e = min(e + 6, 127);
-                if (TYPE == AF_KV_Q4_0) e = min(e + 2, 127);
+                if (TYPE == AF_KV_Q8_0) e += 6;
+                if (TYPE == AF_KV_Q4_0) e += 2;
                 e = min(e, 126);
-                if (isv) {  // follows the largest tile seen; smaller ones come at most 2^-8 below it
+                if (x == 1) {  // follows the largest tile seen; smaller ones come at most 2^-8 below it
                     ev_max = max(ev_max, e);
                     e = max(e, ev_max - 8);
                 }
-                const int slot = f % C::NS;
-                if (f >= C::NS && !twait(&sm.empty[slot], (f / C::NS - 1) & 1, sm)) return false;
-                if (f == C::NS - C::QS && !twait(&sm.q_ready, 0, sm)) return false;
-                store_tile<TYPE, D>(smem + slot * C::SLOT, r, e, ct);
+                if (t >= C::NS) ok = twait(&sm.empty[x][ro.i], ro.ph ^ 1, sm);
+                if (x == 1 && t == C::NS - C::QS) ok = ok && twait(&sm.q_ready, 0, sm);
+                if (!ok) break;
+                store_tile<TYPE, D>(smem + (x ? C::OFF_V : 0) + ro.i * C::SLOT, raw, e, ct);
                 if (ct == 0) {
-                    if (isv)
+                    if (x == 1)
                         sm.ev[t & 7] = e;
                     else
                         sm.ek[t & 7] = pow2i(e);
                 }
                 fence_proxy_async_shared();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.full[slot]);
-                return true;
-            };
-            for (int f = 0; ok && f < total; f += DEP) {
-#pragma unroll
-                for (int i = 0; i < DEP; i++) {
-                    if (ok && f + i < total) ok = fill(f + i, raw[i]);
-                    fetch(f + i + DEP, raw[i]);
-                }
+                if (lane == 0) mbar_arrive(&sm.full[x][ro.i]);
             }
         }
     } else {
@@ -475,7 +507,7 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
         constexpr int CPR = D / 4, RPI = 32 / CPR;  // chunks per row, rows per warp access
         auto stage = [&](uint8_t* base, int rr, int c) { return reinterpret_cast<float4*>(base + rr * D * 4 + ((c ^ (rr & 7)) << 4)); };
         {  // q: scaled to [1, 2), split, into tensor memory
-            uint8_t* st = smem + (C::NS - C::QS) * C::SLOT + warp * 32 * D * 4;
+            uint8_t* st = smem + C::OFF_V + (C::NS - C::QS) * C::SLOT + warp * 32 * D * 4;
             const int64_t off = live ? (int64_t)(r / G) * a.ldq + (int64_t)(g * G + r % G) * D : 0;
             const int c = lane % CPR;
 #pragma unroll
@@ -521,6 +553,7 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
         float m_ref = -CUDART_INF_F, l = 0.f;
         int ev_ref = 0;
         bool ok = true;
+        Ring<C::NS> rv;
         for (int t = 0; t < T; t++) {
             const int b = t & 3;
             ok = twait(&sm.s_full[b], (t >> 2) & 1, sm);
@@ -528,10 +561,9 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
             float f = rowf;
             int ev = 0;
             if (C::SPLIT) {
-                const int fk = fill_k(t), fv = fill_v(t, T);
-                ok = twait(&sm.full[fv % C::NS], (fv / C::NS) & 1, sm);
+                ok = twait(&sm.full[1][rv.i], rv.ph, sm);  // V's exponent is there (K's since its scores were issued)
                 if (!ok) break;
-                (void)fk;
+                rv.next();
                 f *= sm.ek[t & 7];
                 ev = sm.ev[t & 7];
                 if (t == 0) ev_ref = ev;
@@ -602,7 +634,7 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
         if (ok) {  // every operand has been read: the ring is free
             tc_fence_after();
             const float up = C::SPLIT ? pow2i(ev_ref) : 1.f;
-            uint8_t* st = smem + warp * 32 * D * 4;
+            uint8_t* st = smem + C::OFF_V + (C::NS - C::QS) * C::SLOT + warp * 32 * D * 4;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 float o[32];
@@ -614,7 +646,7 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
             __syncwarp();
             const int rw = r0 + warp * 32;  // the warp's first row
             float4* dst = reinterpret_cast<float4*>(a.ws + ((int64_t)split * rows + (int64_t)g * R + rw) * D);
-#pragma unroll 4
+#pragma unroll 8
             for (int i = lane / CPR; i < 32; i += RPI)
                 if (rw + i < R) dst[i * CPR + lane % CPR] = *stage(st, i, lane % CPR);
         }
@@ -624,8 +656,11 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
     __syncthreads();
     if (sm.abort && tid == 0) {  // let what was issued finish before leaving
         mbar_wait_bounded(&sm.done, 0);
-        if (!C::SPLIT)
-            for (int f = max(0, sm.fills - C::NS); f < sm.fills; f++) mbar_wait_bounded(&sm.full[f % C::NS], (f / C::NS) & 1);
+        for (int x = 0; x < 2; x++) {
+            constexpr int N = C::SPLIT ? C::NR : C::NS;
+            for (int i = max(0, sm.copies[x] - N); i < sm.copies[x]; i++)
+                mbar_wait_bounded(C::SPLIT ? &sm.raw_full[x][i % N] : &sm.full[x][i % N], (i / N) & 1);
+        }
     }
     __syncthreads();
     if (warp == C::MMA_WARP) {
