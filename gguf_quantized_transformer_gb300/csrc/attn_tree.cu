@@ -250,7 +250,7 @@ __device__ __forceinline__ float stage_value(uint32_t st, int key, int d) {
 }
 
 template <int TYPE, int D, int MT>
-__global__ void __launch_bounds__(TreeCfg<TYPE, D>::NW * 32, 1) attn_tree_kernel(TreeArgs a, int key_begin, int splits, int part0, int parts) {
+__global__ void __launch_bounds__(TreeCfg<TYPE, D>::NW * 32, 1) attn_tree_kernel(TreeArgs a, int splits) {
     using C = TreeCfg<TYPE, D>;
     constexpr int NW = C::NW, NT = D / 8, KS = C::KS, NB = C::NB, ROWS = 16 * MT;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -258,14 +258,13 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D>::NW * 32, 1) attn_tree_kernel
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 3, j = lane >> 2;
     const int G = a.H / a.c.KVH, R = a.n * G, keys = a.past + a.n;
     const int split = blockIdx.x, g = blockIdx.y, r0 = blockIdx.z * ROWS;
-    // this split's stages; key_begin is a whole number of stages
-    const int first = key_begin / KS, stages = (keys + KS - 1) / KS - first;
-    const int st0 = first + (int)((int64_t)stages * split / splits);
-    const int st1 = first + (int)((int64_t)stages * (split + 1) / splits);
+    const int stages = (keys + KS - 1) / KS;
+    const int st0 = (int)((int64_t)stages * split / splits), st1 = (int)((int64_t)stages * (split + 1) / splits);
     const int64_t row0 = (int64_t)g * a.c.ctx;
     const uint32_t sq = smem_u32(smem), ring = sq + tree_q_bytes<TYPE, D, MT>() + warp * C::NST * C::STAGE;
 
     pdl_launch_dependents();
+    pdl_wait();  // q, the mask and the cache are written by earlier kernels
     // ---- the first stages are on their way while q is prepared
 #pragma unroll
     for (int i = 0; i < C::NST - 1; i++) {
@@ -283,7 +282,7 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D>::NW * 32, 1) attn_tree_kernel
         qin[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (r < ROWS && r0 + r < R && lane < D / 4) {
             const int node = (r0 + r) / G, head = g * G + (r0 + r) % G;
-            qin[i] = *reinterpret_cast<const float4*>(a.q + (int64_t)node * a.ldq + (int64_t)head * D + 4 * lane);
+            qin[i] = __ldcg(reinterpret_cast<const float4*>(a.q + (int64_t)node * a.ldq + (int64_t)head * D + 4 * lane));
         }
     }
 #pragma unroll
@@ -352,8 +351,8 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D>::NW * 32, 1) attn_tree_kernel
     auto window = [&](int mt, int h, int key0) {
         const int t = key0 - a.past, w = t >> 5;  // t < 0: slots of the past, which every row sees
         const unsigned* m = mrow[mt][h];
-        const unsigned lo = w < 0 ? ~0u : (m && w < words ? m[w] : 0u);
-        const unsigned hi = w + 1 < 0 ? ~0u : (m && w + 1 < words ? m[w + 1] : 0u);
+        const unsigned lo = w < 0 ? ~0u : (m && w < words ? __ldcg(m + w) : 0u);
+        const unsigned hi = w + 1 < 0 ? ~0u : (m && w + 1 < words ? __ldcg(m + w + 1) : 0u);
         const unsigned x = __funnelshift_r(lo, hi, t & 31);
         return t + 16 <= a.n ? x : x & ((1u << max(a.n - t, 0)) - 1u);  // nothing behind the last node
     };
@@ -744,7 +743,7 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D>::NW * 32, 1) attn_tree_kernel
         }
     __syncthreads();
     float* part = a.ws;
-    float2* part_ml = reinterpret_cast<float2*>(a.ws + (int64_t)parts * a.c.KVH * R * D);
+    float2* part_ml = reinterpret_cast<float2*>(a.ws + (int64_t)splits * a.c.KVH * R * D);
     for (int i = threadIdx.x; i < ROWS * (D / 4); i += NW * 32) {
         const int r = i / (D / 4), d = (i % (D / 4)) * 4;
         if (r0 + r >= R) break;
@@ -762,13 +761,13 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D>::NW * 32, 1) attn_tree_kernel
             num.x += f * v.x, num.y += f * v.y, num.z += f * v.z, num.w += f * v.w;
             den += f * ml.y;
         }
-        if (parts == 1) {
+        if (splits == 1) {
             const float inv = den == 0.f ? 0.f : 1.f / den;
             const int node = (r0 + r) / G, head = g * G + (r0 + r) % G;
             *reinterpret_cast<float4*>(a.out + (int64_t)node * a.ldo + (int64_t)head * D + d) =
                 make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
         } else {
-            const int64_t row = ((int64_t)(part0 + split) * a.c.KVH + g) * R + r0 + r;
+            const int64_t row = ((int64_t)split * a.c.KVH + g) * R + r0 + r;
             *reinterpret_cast<float4*>(part + row * D + d) = num;
             if (d == 0) part_ml[row] = make_float2(m, den);
         }
@@ -780,6 +779,7 @@ template <int D>
 __global__ void __launch_bounds__(256) tree_merge_kernel(TreeArgs a, int splits) {
     const int lane = threadIdx.x & 31, G = a.H / a.c.KVH, R = a.n * G;
     const int row = blockIdx.x * 8 + (threadIdx.x >> 5), rows = a.c.KVH * R;
+    pdl_launch_dependents();
     pdl_wait();
     if (row >= rows) return;
     const float2* ml = reinterpret_cast<const float2*>(a.ws + (int64_t)splits * rows * D);
@@ -821,24 +821,24 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(TreeArgs a, int splits)
         make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
 }
 
-// How a call is split: the tcgen05 kernel's part, then the mma.sync kernel's over the slots from key_begin on.
+// The tcgen05 kernel, or this file's over row tiles of 32 (16 where there are no more) and so many splits that they fill
+// the SMs, as long as every warp has a stage.
 struct TreePlan {
     TreeTcPlan tc;
-    int key_begin = 0, mt = 1, splits = 1;
-    int parts() const { return tc.splits + splits; }
+    int mt = 1, splits = 1;
 };
 
-// Row tiles of 32 where there are more than 16 rows; splits fill the SMs, as long as every warp has a stage.
 TreePlan tree_plan(int H, int KVH, int D, int type, int past, int n) {
     TreePlan p;
     p.tc = tree_tc_plan(H, KVH, past, n);
-    p.key_begin = p.tc.tiles * 64;
+    p.splits = p.tc.splits;
+    if (p.splits) return p;
     const int R = n * (H / KVH);
     p.mt = R > 16 ? 2 : 1;
     const bool quant = type == AF_KV_Q8_0 || type == AF_KV_Q4_0;
     const int ks = quant ? 32 : 16, nw = type == AF_F32 && D == 128 ? 6 : 8;
     const int64_t tiles = (int64_t)KVH * ((R + 16 * p.mt - 1) / (16 * p.mt));
-    const int stages = (past + n - p.key_begin + ks - 1) / ks;
+    const int stages = (past + n + ks - 1) / ks;
     int64_t s = num_sms() / tiles;
     s = std::min<int64_t>(s, (stages + nw - 1) / nw);
     p.splits = (int)std::max<int64_t>(1, s);
@@ -849,31 +849,28 @@ template <int TYPE, int D, int MT>
 cudaError_t go(const TreeArgs& a, const TreePlan& p, cudaStream_t s) {
     constexpr int smem = tree_smem<TYPE, D, MT>();
     auto k = attn_tree_kernel<TYPE, D, MT>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static SmemOptIn opt;
+    cudaError_t e = opt((const void*)k, smem);
     if (e) return e;
-    const int R = a.n * (a.H / a.c.KVH), parts = p.parts();
-    k<<<dim3(p.splits, a.c.KVH, (R + 16 * MT - 1) / (16 * MT)), TreeCfg<TYPE, D>::NW * 32, smem, s>>>(
-        a, p.key_begin, p.splits, p.tc.splits, parts);
-    e = cudaGetLastError();
-    if (!e && p.tc.splits) e = launch_attn_tree_tc(a, p.tc, parts, s);
-    if (e || parts == 1) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((a.c.KVH * R + 7) / 8);
-    cfg.blockDim = dim3(256);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, a, parts);
+    const int R = a.n * (a.H / a.c.KVH);
+    return launch_chained(k, dim3(p.splits, a.c.KVH, (R + 16 * MT - 1) / (16 * MT)), TreeCfg<TYPE, D>::NW * 32, smem, s, a,
+                          p.splits);
 }
 
 template <int TYPE>
 cudaError_t go_type(const TreeArgs& a, cudaStream_t s) {
     const TreePlan p = tree_plan(a.H, a.c.KVH, a.c.D, TYPE, a.past, a.n);
-    if (a.c.D == 64) return p.mt == 1 ? go<TYPE, 64, 1>(a, p, s) : go<TYPE, 64, 2>(a, p, s);
-    return p.mt == 1 ? go<TYPE, 128, 1>(a, p, s) : go<TYPE, 128, 2>(a, p, s);
+    cudaError_t e;
+    if (p.tc.splits)
+        e = launch_attn_tree_tc(a, p.tc, s);
+    else if (a.c.D == 64)
+        e = p.mt == 1 ? go<TYPE, 64, 1>(a, p, s) : go<TYPE, 64, 2>(a, p, s);
+    else
+        e = p.mt == 1 ? go<TYPE, 128, 1>(a, p, s) : go<TYPE, 128, 2>(a, p, s);
+    if (e || p.splits == 1) return e;
+    const dim3 grid((a.H * a.n + 7) / 8);
+    return a.c.D == 64 ? launch_chained(tree_merge_kernel<64>, grid, 256, 0, s, a, p.splits)
+                       : launch_chained(tree_merge_kernel<128>, grid, 256, 0, s, a, p.splits);
 }
 
 }  // namespace
@@ -885,8 +882,8 @@ cudaError_t launch_tree_mask(const int* parent, int n, int pos0, unsigned* mask,
 
 size_t attn_tree_ws_bytes(int H, int KVH, int D, int type, int past, int n) {
     const TreePlan p = tree_plan(H, KVH, D, type, past, n);
-    if (p.parts() == 1) return 0;
-    return ((size_t)p.parts() * n * H * (D + 2) * sizeof(float) + 255) & ~(size_t)255;
+    if (p.splits == 1) return 0;
+    return ((size_t)p.splits * n * H * (D + 2) * sizeof(float) + 255) & ~(size_t)255;
 }
 
 cudaError_t launch_attn_tree(const TreeArgs& a, cudaStream_t s) {

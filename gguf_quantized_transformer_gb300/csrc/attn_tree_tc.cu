@@ -1,6 +1,5 @@
-// Tree attention over the whole 64-slot tiles of the past on the 5th-generation tensor cores, for calls with many
-// rows: nothing is masked there, every node sees every slot.  The slots after the last whole tile and the nodes' own
-// go to the mma.sync kernel (attn_tree.cu), and the partial results are joined by its merge kernel.
+// Tree attention (attn_tree.cu has the definition) on the 5th-generation tensor cores, for calls with more rows than
+// one mma.sync tile pair.
 //
 // CTA (split, kv head g, row tile): 128 rows (row = node G + head of the group) are the 128 TMEM lanes.  With
 // everything that belongs to a row in tensor memory (q, scores, p and the output: 512 columns), shared memory holds
@@ -13,14 +12,16 @@
 //   fp16 cache    TMA copies 64 slots x 64 dims boxes into the SWIZZLE_128B layout; two products (hi, lo of q or p)
 //   fp32, Q8_0, Q4_0  bulk copies bring the raw rows into a staging ring, four warps for K and four for V write them
 //                 as fp16 hi and lo parts in the same layout; three products (the dropped lo lo is 2^-22 relative).
-//                 A tile is scaled by a power of two that brings its largest value (or scale) near 1, so fp16's
-//                 range never binds: K's goes into the score's factor, V's follows the tiles through a running
-//                 exponent whose moves rescale the output like the softmax's maximum.
-//                 (Rows read through registers instead, three tiles ahead: 192 us where this takes 108 at 64 nodes
+//                 Sixteen slots are scaled by a power of two that brings their largest value (or scale) near 1, so
+//                 fp16's range never binds: K's goes into the scores' factor; V's into p's, relative to a reference
+//                 exponent of the output, which is rescaled when the slots outgrow it.
+//                 (Rows read through registers instead, three tiles ahead: 192 us where this took 108 at 64 nodes
 //                 over 30720 fp32 slots; the warp's loads of several tiles share its few scoreboards.)
 // Warps 0-3 are the softmax (a thread owns a row: the whole tile of its scores in registers, maximum, p, sum), one
 // warp issues the MMAs, scores of up to three tiles ahead of the outputs, so the tensor pipe always has a queue.
 // The reference maximum moves lazily, as in attn_tree.cu, with the same factor 2^8 in p.
+// Tiles that hold nodes (the last ones): a hidden slot's score is -inf by a select; non-finite keys and values and the
+// slots behind the last node become zero operands, and a row that sees a slot so treated becomes NaN.
 // Every wait is bounded: a CTA that gives up lets what it issued finish, frees its TMEM and marks its rows NaN.
 #include <math_constants.h>
 
@@ -38,7 +39,8 @@ constexpr int kAhead = 3;      // tiles whose scores are issued ahead of the out
 constexpr int kQCol = 128, kSCol = 256, kTmem = 512;
 constexpr int kRows = 128;
 constexpr float kLazy2 = 4.f, kBias2 = 8.f;  // as attn_tree.cu's
-constexpr int kConvWarps = 4;  // for K, and as many for V
+constexpr int kConvWarps = 4;  // for K, and as many for V: 16 slots of a tile each
+constexpr int kNoExp = -1000;
 
 template <int TYPE, int D>
 struct TcCfgT {
@@ -49,7 +51,7 @@ struct TcCfgT {
     // staging of raw rows: RR rows a slot, NR slots for K and for V
     static constexpr int RB = TYPE == AF_F32 ? 4 * D : TYPE == AF_KV_Q8_0 ? D : D / 2;
     static constexpr int SB = TYPE == AF_F32 ? 0 : D / 16;   // scale bytes of a row
-    static constexpr int RR = TYPE == AF_F32 ? BK / 2 : BK;
+    static constexpr int RR = TYPE == AF_F32 ? BK / 2 : BK, RU = RR / 16;  // (the rows of RU warps)
     static constexpr int RAW = RR * (RB + SB);
     static constexpr int NR = !SPLIT ? 0 : TYPE == AF_F32 ? (D == 128 ? 3 : 6) : 5;
     static constexpr int OFF_V = NS * SLOT, OFF_RAW = 2 * NS * SLOT;
@@ -68,13 +70,13 @@ struct TcState {
     uint64_t raw_full[2][6], raw_empty[2][6];  // staging slots
     uint64_t s_full[4], p_full[4], pv_done[4];
     uint64_t q_ready, done;
-    uint64_t max_bar[2];
+    uint64_t v_clean;                          // fp16: a tile of nodes has its V checked
     uint32_t tmem_base;
     int copies[2];    // bulk copies issued, for the drain
     volatile int abort;
-    float ek[8];      // 2^exponent of K tiles
-    int ev[8];        // exponent of V tiles
-    float wmax[2][2][kConvWarps];
+    float ek[8][4];   // 2^exponent of K by tile and 16 slots
+    int ev[8][4];     // exponent of V (kNoExp: all zeros)
+    unsigned long long bad[kTreeMax / BK + 2];  // by tile of nodes: slots with a non-finite key or value
 };
 
 // A position in a ring of N slots: its index and the parity of its round.
@@ -155,12 +157,38 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
     for (int i = 0; i < 64; i++) v[i] = __uint_as_float(r[i]);
 }
 
-__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-    const __half2 h = __floats2half2_rn(a, b);
-    const float2 back = __half22float2(h);
-    const __half2 l = __floats2half2_rn(a - back.x, b - back.y);
-    hi = *reinterpret_cast<const uint32_t*>(&h);
-    lo = *reinterpret_cast<const uint32_t*>(&l);
+// two fp32 operations an instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)),
+          "l"(*reinterpret_cast<unsigned long long*>(&c)));
+    return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
+    return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
+    return *reinterpret_cast<float2*>(&r);
+}
+// x = hi + lo in fp16: hi by cutting the fp32 significand to 11 bits (exact in fp16 down to 2^-14; below, off by at most
+// 2^-25), lo the rest rounded: off by at most 2^-22 of x
+__device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {
+    const float2 h = make_float2(__uint_as_float(__float_as_uint(x.x) & 0xFFFFE000u),
+                                 __uint_as_float(__float_as_uint(x.y) & 0xFFFFE000u));
+    const float2 r = fma2(h, make_float2(-1.f, -1.f), x);
+    const __half2 a = __floats2half2_rn(h.x, h.y), b = __floats2half2_rn(r.x, r.y);
+    hi = *reinterpret_cast<const uint32_t*>(&a);
+    lo = *reinterpret_cast<const uint32_t*>(&b);
 }
 
 // ---------------------------------------------------------------- tiles of the converted cache types
@@ -183,26 +211,24 @@ struct Raw8<AF_KV_Q4_0> {
     __half d;
 };
 
-// A thread's chunks of 8 values of a tile: chunk i of thread ct is chunk i * 128 + ct of the rows in order.
+// A thread's chunks of 8 values of its warp's 16 rows: chunk i of a lane is chunk i * 32 + lane of the rows in order.
 template <int TYPE, int D>
 struct RawTile {
-    static constexpr int N = BK * D / 8 / (kConvWarps * 32);
+    static constexpr int N = 16 * D / 8 / 32;
     Raw8<TYPE> c[N];
 };
 
-// Chunks [I0, I0 + N / PARTS) from the staged rows.
-template <int TYPE, int D, int PARTS>
-__device__ __forceinline__ void load_raw(const uint8_t* st, int part, int ct, RawTile<TYPE, D>& r) {
-    using C = TcCfgT<TYPE, D>;
-    constexpr int N = RawTile<TYPE, D>::N / PARTS;
+// st: the warp's 16 rows in a staging slot, sc: their scales.
+template <int TYPE, int D>
+__device__ __forceinline__ void load_raw(const uint8_t* st, const uint8_t* sc, int lane, RawTile<TYPE, D>& r) {
 #pragma unroll
-    for (int i = 0; i < N; i++) {
-        const int idx = i * kConvWarps * 32 + ct;
-        Raw8<TYPE>& c = r.c[part * N + i];
+    for (int i = 0; i < RawTile<TYPE, D>::N; i++) {
+        const int idx = i * 32 + lane;
+        Raw8<TYPE>& c = r.c[i];
         if constexpr (TYPE == AF_F32) {
             // the two halves in an order that differs between groups of four lanes: every bank once per access
             const uint4* p = reinterpret_cast<const uint4*>(st) + idx * 2;
-            const int sw = (ct >> 2) & 1;
+            const int sw = (lane >> 2) & 1;
             const uint4 x = p[sw], y = p[sw ^ 1];
             c.a = sw ? y : x;
             c.b = sw ? x : y;
@@ -211,29 +237,50 @@ __device__ __forceinline__ void load_raw(const uint8_t* st, int part, int ct, Ra
                 c.a = reinterpret_cast<const uint2*>(st)[idx];
             else
                 c.a = reinterpret_cast<const uint32_t*>(st)[idx];
-            c.d = reinterpret_cast<const __half*>(st + C::RR * C::RB)[idx / 4];
+            c.d = reinterpret_cast<const __half*>(sc)[idx / 4];
         }
     }
 }
 
-// Largest magnitude among this thread's values (fp32), or this lane's share of the tile's scales.
+// Rows from `valid` on become zeros, and so does what is not finite; returns the rows (bits) that held such.
 template <int TYPE, int D>
-__device__ __forceinline__ float raw_max(const RawTile<TYPE, D>& r, const uint8_t* st, int lane) {
-    using C = TcCfgT<TYPE, D>;
-    float m = 0.f;
-    if constexpr (TYPE == AF_F32) {
+__device__ __forceinline__ unsigned clean_raw(RawTile<TYPE, D>& r, int valid, int lane) {
+    unsigned rows = 0;
 #pragma unroll
-        for (int i = 0; i < RawTile<TYPE, D>::N; i++) {
+    for (int i = 0; i < RawTile<TYPE, D>::N; i++) {
+        const int row = (i * 32 + lane) / (D / 8);
+        Raw8<TYPE>& c = r.c[i];
+        if constexpr (TYPE == AF_F32) {
+            uint32_t* w[8] = {&c.a.x, &c.a.y, &c.a.z, &c.a.w, &c.b.x, &c.b.y, &c.b.z, &c.b.w};
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+                if (row >= valid || (*w[e] & 0x7F800000u) == 0x7F800000u) {
+                    if (row < valid) rows |= 1u << row;
+                    *w[e] = 0u;
+                }
+        } else {
+            if (row >= valid || (__half_as_ushort(c.d) & 0x7C00u) == 0x7C00u) {
+                if (row < valid) rows |= 1u << row;
+                c.d = __ushort_as_half(0);
+            }
+        }
+    }
+    return rows;
+}
+
+// Largest magnitude among this thread's values (fp32) or scales.
+template <int TYPE, int D>
+__device__ __forceinline__ float raw_max(const RawTile<TYPE, D>& r) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < RawTile<TYPE, D>::N; i++) {
+        if constexpr (TYPE == AF_F32) {
             const uint32_t w[8] = {r.c[i].a.x, r.c[i].a.y, r.c[i].a.z, r.c[i].a.w, r.c[i].b.x, r.c[i].b.y, r.c[i].b.z, r.c[i].b.w};
 #pragma unroll
-            for (int e = 0; e < 8; e++) m = fmaxf(m, fabsf(__uint_as_float(w[e])));
-        }
-    } else {
-        const __half2* w = reinterpret_cast<const __half2*>(st + C::RR * C::RB);
-#pragma unroll
-        for (int i = 0; i < BK * (D / 32) / 2 / 32; i++) {
-            const float2 f = __half22float2(w[i * 32 + lane]);
-            m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
+            for (int e = 0; e < 8; e += 2)
+                m = fmaxf(fmaxf(m, fabsf(__uint_as_float(w[e]))), fabsf(__uint_as_float(w[e + 1])));
+        } else {
+            m = fmaxf(m, fabsf(__half2float(r.c[i].d)));
         }
     }
     return m;
@@ -242,19 +289,21 @@ __device__ __forceinline__ float raw_max(const RawTile<TYPE, D>& r, const uint8_
 __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 __device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
 
-// The tile's fp16 hi and lo parts, times 2^-e, into a slot (SWIZZLE_128B atoms of 64 dims, [64 slots][128 B] each).
+// The fp16 hi and lo parts of the warp's rows row0.., times 2^-e, into a slot (SWIZZLE_128B atoms of 64 dims,
+// [64 slots][128 B] each).
 template <int TYPE, int D>
-__device__ __forceinline__ void store_tile(uint8_t* dst, const RawTile<TYPE, D>& r, int e, int ct) {
+__device__ __forceinline__ void store_tile(uint8_t* dst, const RawTile<TYPE, D>& r, int e, int row0, int lane) {
     constexpr int CPR = D / 8, PART = BK * D * 2;
     const float down = pow2i(-e);
 #pragma unroll
     for (int i = 0; i < RawTile<TYPE, D>::N; i++) {
-        const int idx = i * kConvWarps * 32 + ct, key = idx / CPR, ch = idx % CPR;
+        const int idx = i * 32 + lane, key = row0 + idx / CPR, ch = idx % CPR;
         uint32_t hi[4], lo[4];
         if constexpr (TYPE == AF_F32) {
             const uint32_t w[8] = {r.c[i].a.x, r.c[i].a.y, r.c[i].a.z, r.c[i].a.w, r.c[i].b.x, r.c[i].b.y, r.c[i].b.z, r.c[i].b.w};
 #pragma unroll
-            for (int p = 0; p < 4; p++) split2(__uint_as_float(w[2 * p]) * down, __uint_as_float(w[2 * p + 1]) * down, hi[p], lo[p]);
+            for (int p = 0; p < 4; p++)
+                split2(mul2(make_float2(__uint_as_float(w[2 * p]), __uint_as_float(w[2 * p + 1])), make_float2(down, down)), hi[p], lo[p]);
         } else {
             // codes q are exact in fp16, and so is d 2^-e (11 bits); hi = fp16(q d), lo = q d - hi by a fused
             // multiply-add, exact as long as it is not below fp16's smallest step 2^-24
@@ -296,7 +345,7 @@ __device__ __forceinline__ void store_tile(uint8_t* dst, const RawTile<TYPE, D>&
 template <int TYPE, int D>
 __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
     attn_tree_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, TreeArgs a,
-                        int tiles, int splits, int parts) {
+                        int tiles, int splits) {
     using C = TcCfgT<TYPE, D>;
     constexpr uint32_t kIdS = idesc_f16(kRows, BK);                  // scores: N = slots, B K-major
     constexpr uint32_t kIdO = idesc_f16(kRows, D) | (1u << 16);      // output: N = dims, B MN-major
@@ -308,6 +357,8 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
     const int split = blockIdx.x, g = blockIdx.y, r0 = blockIdx.z * kRows;
     const int t0 = (int)((int64_t)tiles * split / splits), T = (int)((int64_t)tiles * (split + 1) / splits) - t0;
     const int64_t row0 = (int64_t)g * a.c.ctx + (int64_t)t0 * BK;  // first slot row of the split
+    // tiles from tn on hold nodes (or nothing behind them); slots from `valid` on, both counted from t0
+    const int tn = a.past / BK - t0, valid = a.past + a.n - t0 * BK;
 
     pdl_launch_dependents();
     if (tid == 0) {
@@ -320,7 +371,6 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                 mbar_init(&sm.raw_full[x][i], C::SB ? 33 : 1);  // the copy's bytes, and each lane's scales
                 mbar_init(&sm.raw_empty[x][i], kConvWarps);
             }
-            mbar_init(&sm.max_bar[x], kConvWarps);
             sm.copies[x] = 0;
         }
         for (int i = 0; i < 4; i++) {
@@ -328,16 +378,19 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
             mbar_init(&sm.p_full[i], 4);
             mbar_init(&sm.pv_done[i], 1);
         }
+        mbar_init(&sm.v_clean, 4);
         mbar_init(&sm.q_ready, 4);
         mbar_init(&sm.done, 1);
         sm.abort = 0;
         fence_mbar_init();
     }
+    for (int i = tid; i < (int)(sizeof(sm.bad) / 8); i += C::WARPS * 32) sm.bad[i] = 0;
     if (warp == C::MMA_WARP) tmem_alloc(&sm.tmem_base, kTmem);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
+    pdl_wait();  // q, the mask and the cache are written by earlier kernels
 
     if (warp == C::MMA_WARP) {
         // ---------------- MMA issuer: the whole warp walks the tiles (so that descriptors stay in uniform
@@ -417,18 +470,21 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
             for (int i = 0; i < T * (BK / C::RR); i++, r.next()) {
                 if (i >= C::NR && !twait(&sm.raw_empty[x][r.i], r.ph ^ 1, sm)) break;
                 uint8_t* dst = smem + C::OFF_RAW + (x * C::NR + r.i) * C::RAW;
+                const int rows = min(C::RR, max(0, valid - i * C::RR));
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&sm.raw_full[x][r.i], C::RR * C::RB);
-                    bulk_g2s(dst, src + (int64_t)i * C::RR * C::RB, C::RR * C::RB, &sm.raw_full[x][r.i]);
+                    mbar_arrive_expect_tx(&sm.raw_full[x][r.i], rows * C::RB);
+                    if (rows) bulk_g2s(dst, src + (int64_t)i * C::RR * C::RB, rows * C::RB, &sm.raw_full[x][r.i]);
                     sm.copies[x] = i + 1;
                 }
                 if (C::SB) {  // rows may start off 16 bytes: 8- or 4-byte copies
                     constexpr int B = C::SB ? C::SB : 4;
 #pragma unroll
-                    for (int k = 0; k < C::RR; k += 32)
-                        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst) + C::RR * C::RB + (k + lane) * B),
-                                     "l"(sc + ((int64_t)i * C::RR + k + lane) * B), "n"(B)
+                    for (int k = 0; k < C::RR; k += 32) {
+                        const bool in = k + lane < rows;
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst) + C::RR * C::RB + (k + lane) * B),
+                                     "l"(in ? sc + ((int64_t)i * C::RR + k + lane) * B : sc), "n"(B), "r"(in ? B : 0)
                                      : "memory");
+                    }
                     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sm.raw_full[x][r.i]))
                                  : "memory");
                 }
@@ -438,58 +494,48 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
     } else if (warp >= 4) {
         if constexpr (C::SPLIT) {
             // ---------------- fp32, Q8_0, Q4_0: staged rows -> fp16 parts
-            const int x = (warp - 4) / kConvWarps, w = (warp - 4) % kConvWarps, ct = w * 32 + lane;
-            constexpr int PARTS = BK / C::RR;
+            const int x = (warp - 4) / kConvWarps, w = (warp - 4) % kConvWarps;
             Ring<C::NR> rr;
             Ring<C::NS> ro;
-            int ev_max = -126;
             bool ok = true;
             for (int t = 0; t < T; t++, ro.next()) {
                 RawTile<TYPE, D> raw;
-                float m = 0.f;
+                // Every warp waits for every staging slot of the tile and frees it, the ones without its rows too: a
+                // warp that skipped a round of a slot could not tell that round's completion from the next one's.
 #pragma unroll
-                for (int p = 0; p < PARTS; p++) {
+                for (int p = 0; p < kConvWarps / C::RU; p++, rr.next()) {
                     ok = ok && twait(&sm.raw_full[x][rr.i], rr.ph, sm);
                     if (!ok) break;
-                    const uint8_t* st = smem + C::OFF_RAW + (x * C::NR + rr.i) * C::RAW;
-                    load_raw<TYPE, D, PARTS>(st, p, ct, raw);
-                    if (TYPE != AF_F32) m = raw_max<TYPE, D>(raw, st, lane);
+                    if (w / C::RU == p) {
+                        const uint8_t* st = smem + C::OFF_RAW + (x * C::NR + rr.i) * C::RAW;
+                        const int wr = (w % C::RU) * 16;  // the warp's rows in the slot
+                        load_raw<TYPE, D>(st + wr * C::RB, st + C::RR * C::RB + wr * C::SB, lane, raw);
+                    }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm.raw_empty[x][rr.i]);
-                    rr.next();
                 }
                 if (!ok) break;
-                if (TYPE == AF_F32) m = raw_max<TYPE, D>(raw, nullptr, lane);
+                if (t >= tn) {
+                    const unsigned bad = clean_raw<TYPE, D>(raw, valid - t * BK - w * 16, lane);
+                    if (bad) atomicOr(&sm.bad[t - tn], (unsigned long long)bad << (w * 16));
+                }
+                float m = raw_max<TYPE, D>(raw);
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                if (TYPE == AF_F32) {  // the warps hold different rows: exchange their maxima
-                    if (lane == 0) {
-                        sm.wmax[x][t & 1][w] = m;
-                        mbar_arrive(&sm.max_bar[x]);
-                    }
-                    ok = twait(&sm.max_bar[x], t & 1, sm);
-                    if (!ok) break;
-#pragma unroll
-                    for (int i = 0; i < kConvWarps; i++) m = fmaxf(m, sm.wmax[x][t & 1][i]);
-                }
                 // largest value in [1, 2), or largest scale times its largest code in [1, 4)
                 int e = max(exponent_of(m), -126);
                 if (TYPE == AF_KV_Q8_0) e += 6;
                 if (TYPE == AF_KV_Q4_0) e += 2;
                 e = min(e, 126);
-                if (x == 1) {  // follows the largest tile seen; smaller ones come at most 2^-8 below it
-                    ev_max = max(ev_max, e);
-                    e = max(e, ev_max - 8);
-                }
                 if (t >= C::NS) ok = twait(&sm.empty[x][ro.i], ro.ph ^ 1, sm);
                 if (x == 1 && t == C::NS - C::QS) ok = ok && twait(&sm.q_ready, 0, sm);
                 if (!ok) break;
-                store_tile<TYPE, D>(smem + (x ? C::OFF_V : 0) + ro.i * C::SLOT, raw, e, ct);
-                if (ct == 0) {
+                store_tile<TYPE, D>(smem + (x ? C::OFF_V : 0) + ro.i * C::SLOT, raw, e, w * 16, lane);
+                if (lane == 0) {
                     if (x == 1)
-                        sm.ev[t & 7] = e;
+                        sm.ev[t & 7][w] = m == 0.f ? kNoExp : e;
                     else
-                        sm.ek[t & 7] = pow2i(e);
+                        sm.ek[t & 7][w] = pow2i(e);
                 }
                 fence_proxy_async_shared();
                 __syncwarp();
@@ -538,9 +584,11 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
 #pragma unroll
                 for (int i = 0; i < 16; i++) {
                     const float4 x = *stage(st, lane, h * 16 + i);
-                    split2(live ? x.x * sc * k : 0.f, live ? x.y * sc * k : 0.f, hi[2 * i], lo[2 * i]);  // (what a dead
-                    split2(live ? x.z * sc * k : 0.f, live ? x.w * sc * k : 0.f, hi[2 * i + 1], lo[2 * i + 1]);  // row reads
-                }                                                                                          // may be anything)
+                    const float2 lo2 = live ? make_float2(x.x * sc * k, x.y * sc * k) : make_float2(0.f, 0.f);  // (what a
+                    const float2 hi2 = live ? make_float2(x.z * sc * k, x.w * sc * k) : make_float2(0.f, 0.f);  // dead row
+                    split2(lo2, hi[2 * i], lo[2 * i]);                                                          // reads may
+                    split2(hi2, hi[2 * i + 1], lo[2 * i + 1]);                                                  // be anything)
+                }
                 tmem_st32(lane_addr + kQCol + h * 32, hi);
                 tmem_st32(lane_addr + kQCol + D / 2 + h * 32, lo);
             }
@@ -550,45 +598,108 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.q_ready);
         }
+        const int words = (a.n + 31) / 32;
+        const unsigned* mrow = live ? a.mask + (int64_t)(r / G) * words : nullptr;
+        auto window = [&](int t) {  // bit i: the row sees node t + i (t < 0: slots of the past, which every row sees)
+            const int w = t >> 5;
+            const unsigned lo = w < 0 ? ~0u : (mrow && w < words ? __ldcg(mrow + w) : 0u);
+            const unsigned hi = w + 1 < 0 ? ~0u : (mrow && w + 1 < words ? __ldcg(mrow + w + 1) : 0u);
+            const unsigned x = __funnelshift_r(lo, hi, t & 31);
+            return t + 32 <= a.n ? x : (t >= a.n ? 0u : x & ((1u << (a.n - t)) - 1u));  // nothing behind the last node
+        };
+        constexpr int NG = C::SPLIT ? 4 : 1;  // exponents of a tile
         float m_ref = -CUDART_INF_F, l = 0.f;
-        int ev_ref = 0;
+        int ev_ref = kNoExp;
         bool ok = true;
         Ring<C::NS> rv;
-        for (int t = 0; t < T; t++) {
+        for (int t = 0; t < T; t++, rv.next()) {
             const int b = t & 3;
+            const bool nodes = t >= tn;
+            unsigned see[2] = {};
+            if (nodes) {
+                const int j = (t0 + t) * BK - a.past;
+                see[0] = window(j);
+                see[1] = window(j + 32);
+            }
             ok = twait(&sm.s_full[b], (t >> 2) & 1, sm);
             if (!ok) break;
-            float f = rowf;
-            int ev = 0;
-            if (C::SPLIT) {
-                ok = twait(&sm.full[1][rv.i], rv.ph, sm);  // V's exponent is there (K's since its scores were issued)
+            float f[NG];
+            int ev[NG] = {}, ev_max = kNoExp;
+            if (C::SPLIT || nodes) {
+                ok = twait(&sm.full[1][rv.i], rv.ph, sm);  // V's exponents are there (K's since its scores were issued)
                 if (!ok) break;
-                rv.next();
-                f *= sm.ek[t & 7];
-                ev = sm.ev[t & 7];
-                if (t == 0) ev_ref = ev;
+            }
+#pragma unroll
+            for (int q = 0; q < NG; q++) {
+                f[q] = rowf;
+                if (C::SPLIT) {
+                    f[q] = fminf(fmaxf(f[q] * sm.ek[t & 7][q], 0x1p-126f), 0x1p126f);  // (0 or inf times -inf or 0: NaN)
+                    ev[q] = sm.ev[t & 7][q];
+                    ev_max = max(ev_max, ev[q]);
+                }
+            }
+            if (!C::SPLIT && nodes) {  // V of this tile: zeros where it is not finite, and behind the last node
+                uint8_t* v = smem + C::OFF_V + rv.i * C::SLOT;
+#pragma unroll
+                for (int i = 0; i < D / 16; i++) {
+                    const int idx = i * 128 + tid, key = (idx >> 3) % BK;  // 16-byte chunk idx of [D / 64][64 slots][8]
+                    uint4* p = reinterpret_cast<uint4*>(v) + idx;
+                    uint4 x = *p;
+                    uint32_t* w[4] = {&x.x, &x.y, &x.z, &x.w};
+                    bool bad = false;
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const bool lo = (*w[e] & 0x7C00u) == 0x7C00u, hi = (*w[e] & 0x7C000000u) == 0x7C000000u;
+                        bad |= lo | hi;
+                        *w[e] &= (lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u);
+                    }
+                    const bool out = t * BK + key >= valid;
+                    if (out) x = make_uint4(0u, 0u, 0u, 0u);
+                    if (bad || out) *p = x;
+                    if (bad && !out) atomicOr(&sm.bad[t - tn], 1ull << key);
+                }
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.v_clean);
+                ok = twait(&sm.v_clean, (t - max(tn, 0)) & 1, sm);
+                if (!ok) break;
             }
             tc_fence_after();
             const uint32_t s_addr = lane_addr + kSCol + b * BK;
             float s[BK];
             tmem_ld64(s_addr, s);
-            float mx[4];
+            if (nodes) {
+                const unsigned long long bad = *(volatile unsigned long long*)&sm.bad[t - tn];
 #pragma unroll
-            for (int i = 0; i < 4; i++) mx[i] = fmaxf(s[i], s[i + 4]);
+                for (int i = 0; i < BK; i++) {
+                    if (bad >> i & 1) s[i] = CUDART_NAN_F;
+                    if (!(see[i >> 5] >> (i & 31) & 1)) s[i] = -CUDART_INF_F;
+                }
+            }
+            float mt = -CUDART_INF_F;
 #pragma unroll
-            for (int i = 8; i < BK; i++) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
-            const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
+            for (int q = 0; q < NG; q++) {
+                constexpr int W = BK / NG;
+                float x0 = s[q * W], x1 = s[q * W + 1];
+#pragma unroll
+                for (int i = 2; i < W; i += 4) {
+                    x0 = fmaxf(fmaxf(x0, s[q * W + i]), s[q * W + i + 1]);
+                    if (i + 2 < W) x1 = fmaxf(fmaxf(x1, s[q * W + i + 2]), s[q * W + i + 3]);
+                }
+                mt = fmaxf(mt, fmaxf(x0, x1) * f[q]);
+            }
             const bool move = mt > m_ref + kLazy2;
-            if (__any_sync(0xffffffffu, move || ev - ev_ref > 2)) {
+            const bool grow = C::SPLIT && ev_max > ev_ref + 2;
+            if (__any_sync(0xffffffffu, move || grow)) {
                 float up = 1.f;
                 if (mt > m_ref) {
                     up = ex2u(m_ref - mt);
                     m_ref = mt;
                     l *= up;
                 }
-                if (ev > ev_ref) {
-                    up *= ex2u((float)(ev_ref - ev));
-                    ev_ref = ev;
+                if (grow) {
+                    up *= ex2u((float)(ev_ref - ev_max));
+                    ev_ref = ev_max;
                 }
                 if (t > 0) {  // the output holds the tiles before t: wait for them, rescale this warp's rows
                     ok = twait(&sm.pv_done[(t - 1) & 3], ((t - 1) >> 2) & 1, sm);
@@ -606,19 +717,32 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                     tmem_st_wait();
                 }
             }
-            const float shift = C::SPLIT ? (float)(ev - ev_ref) : 0.f;
-            const float mb = (m_ref == -CUDART_INF_F ? 0.f : m_ref) - kBias2 - shift;
-            float sum[4] = {};
+            const float mb = (m_ref == -CUDART_INF_F ? 0.f : m_ref) - kBias2;
             uint32_t hi[32], lo[32];
 #pragma unroll
-            for (int i = 0; i < BK; i += 2) {
-                const float p0 = ex2u(s[i] * f - mb), p1 = ex2u(s[i + 1] * f - mb);
-                sum[(i >> 1) & 1] += p0;
-                sum[2 + ((i >> 1) & 1)] += p1;
-                split2(p0, p1, hi[i / 2], lo[i / 2]);
+            for (int q = 0; q < NG; q++) {
+                constexpr int W = BK / NG;
+                // V's slots are 2^-ev of themselves and the output 2^-ev_ref: p takes the difference
+                const float shift = C::SPLIT && ev[q] != kNoExp ? (float)(ev[q] - ev_ref) : 0.f;
+                const float2 ff = make_float2(f[q], f[q]), mm = make_float2(shift - mb, shift - mb);
+                float2 sum[2] = {};
+#pragma unroll
+                for (int i = 0; i < W; i += 2) {
+                    const float2 y = fma2(make_float2(s[q * W + i], s[q * W + i + 1]), ff, mm);
+                    const float2 p = make_float2(ex2u(y.x), ex2u(y.y));
+                    sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], p);
+                    split2(p, hi[(q * W + i) / 2], lo[(q * W + i) / 2]);
+                }
+                const float2 add = add2(sum[0], sum[1]);
+                if (C::SPLIT && shift < -8.f) {  // small values: p's sum apart from their factor
+                    float z = 0.f;
+#pragma unroll
+                    for (int i = 0; i < W; i++) z += ex2u(s[q * W + i] * f[q] - mb);
+                    l += z;
+                } else {
+                    l += C::SPLIT ? (add.x + add.y) * ex2u(-shift) : add.x + add.y;
+                }
             }
-            const float add = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            l += C::SPLIT ? add * ex2u(-shift) : add;
             tmem_st32(s_addr, hi);
             tmem_st32(s_addr + BK / 2, lo);
             tmem_st_wait();
@@ -630,11 +754,15 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
         ok = ok && twait(&sm.done, 0, sm);
         const int64_t rows = (int64_t)a.c.KVH * R;
         const int64_t row = (int64_t)split * rows + (int64_t)g * R + r;
-        float2* ml = reinterpret_cast<float2*>(a.ws + parts * rows * D);
+        // one split: the result itself (zeros for a row that saw nothing)
+        const bool last = splits == 1;
+        float* base = last ? a.out : a.ws;
+        const int64_t off = !live ? 0 : last ? (int64_t)(r / G) * a.ldo + (int64_t)(g * G + r % G) * D : row * D;
+        uint8_t* st = smem + C::OFF_V + (C::NS - C::QS) * C::SLOT + warp * 32 * D * 4;
         if (ok) {  // every operand has been read: the ring is free
             tc_fence_after();
-            const float up = C::SPLIT ? pow2i(ev_ref) : 1.f;
-            uint8_t* st = smem + C::OFF_V + (C::NS - C::QS) * C::SLOT + warp * 32 * D * 4;
+            float up = C::SPLIT ? pow2i(ev_ref) : 1.f;
+            if (last) up = l == 0.f ? 0.f : up / l;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 float o[32];
@@ -643,14 +771,19 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                 for (int i = 0; i < 32; i += 4)
                     *stage(st, lane, (c + i) / 4) = make_float4(o[i] * up, o[i + 1] * up, o[i + 2] * up, o[i + 3] * up);
             }
-            __syncwarp();
-            const int rw = r0 + warp * 32;  // the warp's first row
-            float4* dst = reinterpret_cast<float4*>(a.ws + ((int64_t)split * rows + (int64_t)g * R + rw) * D);
-#pragma unroll 8
-            for (int i = lane / CPR; i < 32; i += RPI)
-                if (rw + i < R) dst[i * CPR + lane % CPR] = *stage(st, i, lane % CPR);
+        } else {
+            for (int c = 0; c < CPR; c++) *stage(st, lane, c) = make_float4(CUDART_NAN_F, CUDART_NAN_F, CUDART_NAN_F, CUDART_NAN_F);
         }
-        if (live) ml[row] = ok ? make_float2(m_ref, l) : make_float2(CUDART_NAN_F, CUDART_NAN_F);
+        __syncwarp();
+#pragma unroll 8
+        for (int i = 0; i < 32; i += RPI) {
+            const int rr = i + lane / CPR;
+            const int64_t o = __shfl_sync(0xffffffffu, off, rr);
+            if (r0 + warp * 32 + rr < R) reinterpret_cast<float4*>(base + o)[lane % CPR] = *stage(st, rr, lane % CPR);
+        }
+        if (live && !last)
+            reinterpret_cast<float2*>(a.ws + splits * rows * D)[row] =
+                ok ? make_float2(m_ref, l) : make_float2(CUDART_NAN_F, CUDART_NAN_F);
     }
     tc_fence_before();
     __syncthreads();
@@ -667,14 +800,14 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
         tc_fence_after();
         tmem_free(tmem, kTmem);
     }
-    pdl_wait();  // the kernel that does the other slots: the merge waits for this one alone
 }
 
 template <int TYPE, int D>
-cudaError_t go(const TreeArgs& a, const TreeTcPlan& p, int parts, cudaStream_t s) {
+cudaError_t go(const TreeArgs& a, const TreeTcPlan& p, cudaStream_t s) {
     using C = TcCfgT<TYPE, D>;
     auto k = attn_tree_tc_kernel<TYPE, D>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    static SmemOptIn opt;
+    cudaError_t e = opt((const void*)k, C::SMEM);
     if (e) return e;
     CUtensorMap mk = {}, mv = {};
     if (TYPE == AF_F16) {
@@ -682,23 +815,14 @@ cudaError_t go(const TreeArgs& a, const TreeTcPlan& p, int parts, cudaStream_t s
         if (!make_tmap_f16(&mk, a.c.k, rows, D, D, 64, BK) || !make_tmap_f16(&mv, a.c.v, rows, D, D, 64, BK))
             return cudaErrorInvalidValue;
     }
-    cudaLaunchConfig_t cfg = {};
     const int R = a.n * (a.H / a.c.KVH);
-    cfg.gridDim = dim3(p.splits, a.c.KVH, (R + kRows - 1) / kRows);
-    cfg.blockDim = dim3(C::WARPS * 32);
-    cfg.dynamicSmemBytes = C::SMEM;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k, mk, mv, a, p.tiles, p.splits, parts);
+    return launch_chained(k, dim3(p.splits, a.c.KVH, (R + kRows - 1) / kRows), C::WARPS * 32, C::SMEM, s, mk, mv, a, p.tiles,
+                          p.splits);
 }
 
 template <int TYPE>
-cudaError_t go_type(const TreeArgs& a, const TreeTcPlan& p, int parts, cudaStream_t s) {
-    return a.c.D == 64 ? go<TYPE, 64>(a, p, parts, s) : go<TYPE, 128>(a, p, parts, s);
+cudaError_t go_type(const TreeArgs& a, const TreeTcPlan& p, cudaStream_t s) {
+    return a.c.D == 64 ? go<TYPE, 64>(a, p, s) : go<TYPE, 128>(a, p, s);
 }
 
 }  // namespace
@@ -706,21 +830,20 @@ cudaError_t go_type(const TreeArgs& a, const TreeTcPlan& p, int parts, cudaStrea
 TreeTcPlan tree_tc_plan(int H, int KVH, int past, int n) {
     TreeTcPlan p;
     const int R = n * (H / KVH);
-    const int tiles = past / BK;
-    if (R <= 32 || tiles < 4) return p;
-    p.tiles = tiles;
+    if (R <= 32) return p;
+    p.tiles = (past + n + BK - 1) / BK;
     const int64_t ctas = (int64_t)KVH * ((R + kRows - 1) / kRows);
     // one CTA per SM; at least four tiles each
-    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(num_sms() / ctas, tiles / 4));
+    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(num_sms() / ctas, p.tiles / 4));
     return p;
 }
 
-cudaError_t launch_attn_tree_tc(const TreeArgs& a, const TreeTcPlan& p, int parts, cudaStream_t s) {
+cudaError_t launch_attn_tree_tc(const TreeArgs& a, const TreeTcPlan& p, cudaStream_t s) {
     switch (a.c.type) {
-        case AF_F32: return go_type<AF_F32>(a, p, parts, s);
-        case AF_F16: return go_type<AF_F16>(a, p, parts, s);
-        case AF_KV_Q8_0: return go_type<AF_KV_Q8_0>(a, p, parts, s);
-        default: return go_type<AF_KV_Q4_0>(a, p, parts, s);
+        case AF_F32: return go_type<AF_F32>(a, p, s);
+        case AF_F16: return go_type<AF_F16>(a, p, s);
+        case AF_KV_Q8_0: return go_type<AF_KV_Q8_0>(a, p, s);
+        default: return go_type<AF_KV_Q4_0>(a, p, s);
     }
 }
 

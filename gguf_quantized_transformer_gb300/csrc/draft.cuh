@@ -1,8 +1,45 @@
 // Launchers of the drafted-tree operators (rotary positions, cache write and read, tree attention).
 #pragma once
+#include <mutex>
+#include <utility>
+
 #include "common.cuh"
 
 namespace af {
+
+// Launch with programmatic stream serialization: the kernel may start before its predecessor in the stream is done and
+// waits for it (griddepcontrol.wait) before it touches memory.
+template <typename K, typename... A>
+cudaError_t launch_chained(K kernel, dim3 grid, int threads, int smem, cudaStream_t s, A&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+
+// A kernel's opt-in to more than 48 KB of dynamic shared memory, once per device.
+struct SmemOptIn {
+    std::mutex mu;
+    bool done[kMaxDevices] = {};
+    cudaError_t operator()(const void* kernel, int bytes) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e) return e;
+        if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+        std::lock_guard<std::mutex> lk(mu);
+        if (done[dev]) return cudaSuccess;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (!e) done[dev] = true;
+        return e;
+    }
+};
 
 // ---- rotary positions (rope.cu)
 constexpr int kRopeMaxPairs = 128;  // head_dim <= 256
@@ -51,13 +88,13 @@ struct TreeArgs {
     int64_t ldo = 0;
     float* ws = nullptr;
 };
-// The part of a call that the tcgen05 kernel takes (attn_tree_tc.cu): whole 64-slot tiles of the past; splits = 0: none.
+// A call with many rows goes to the tcgen05 kernel (attn_tree_tc.cu): its 64-slot tiles and splits; splits = 0: not.
 struct TreeTcPlan {
     int tiles = 0, splits = 0;
 };
 TreeTcPlan tree_tc_plan(int H, int KVH, int past, int n);
-// Writes parts [0, splits) of the workspace's `parts`, and completes after the kernel launched before it has.
-cudaError_t launch_attn_tree_tc(const TreeArgs& a, const TreeTcPlan& p, int parts, cudaStream_t s);
+// Writes the workspace's parts [0, splits), or the output where there is one.
+cudaError_t launch_attn_tree_tc(const TreeArgs& a, const TreeTcPlan& p, cudaStream_t s);
 
 size_t attn_tree_ws_bytes(int H, int KVH, int D, int type, int past, int n);
 cudaError_t launch_attn_tree(const TreeArgs& a, cudaStream_t s);
