@@ -180,42 +180,42 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
         : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
     return *reinterpret_cast<float2*>(&r);
 }
-// x = hi + lo in fp16: hi by cutting the fp32 significand to 11 bits (exact in fp16 down to 2^-14; below, off by at most
-// 2^-25), lo the rest rounded: off by at most 2^-22 of x
+// x = hi + lo in fp16 (lo off by at most 2^-23 of x, or half of fp16's smallest step 2^-24)
 __device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {
-    const float2 h = make_float2(__uint_as_float(__float_as_uint(x.x) & 0xFFFFE000u),
-                                 __uint_as_float(__float_as_uint(x.y) & 0xFFFFE000u));
-    const float2 r = fma2(h, make_float2(-1.f, -1.f), x);
-    const __half2 a = __floats2half2_rn(h.x, h.y), b = __floats2half2_rn(r.x, r.y);
+    const __half2 a = __floats2half2_rn(x.x, x.y);
+    const float2 r = fma2(__half22float2(a), make_float2(-1.f, -1.f), x);
+    const __half2 b = __floats2half2_rn(r.x, r.y);
     hi = *reinterpret_cast<const uint32_t*>(&a);
     lo = *reinterpret_cast<const uint32_t*>(&b);
 }
 
 // ---------------------------------------------------------------- tiles of the converted cache types
 
-// 8 values of a row as they lie in the cache
+// A lane's piece of its warp's 16 rows as they lie in the cache: piece i of a lane is piece i * 32 + lane of the rows in
+// order, 16 bytes of fp32 values or 8 codes.
 template <int TYPE>
-struct Raw8;
+struct Raw;
 template <>
-struct Raw8<AF_F32> {
-    uint4 a, b;
+struct Raw<AF_F32> {
+    static constexpr int VALUES = 4;
+    uint4 a;
 };
 template <>
-struct Raw8<AF_KV_Q8_0> {
+struct Raw<AF_KV_Q8_0> {
+    static constexpr int VALUES = 8;
     uint2 a;
     __half d;
 };
 template <>
-struct Raw8<AF_KV_Q4_0> {
+struct Raw<AF_KV_Q4_0> {
+    static constexpr int VALUES = 8;
     uint32_t a;
     __half d;
 };
-
-// A thread's chunks of 8 values of its warp's 16 rows: chunk i of a lane is chunk i * 32 + lane of the rows in order.
 template <int TYPE, int D>
 struct RawTile {
-    static constexpr int N = 16 * D / 8 / 32;
-    Raw8<TYPE> c[N];
+    static constexpr int N = 16 * D / Raw<TYPE>::VALUES / 32;
+    Raw<TYPE> c[N];
 };
 
 // st: the warp's 16 rows in a staging slot, sc: their scales.
@@ -224,21 +224,8 @@ __device__ __forceinline__ void load_raw(const uint8_t* st, const uint8_t* sc, i
 #pragma unroll
     for (int i = 0; i < RawTile<TYPE, D>::N; i++) {
         const int idx = i * 32 + lane;
-        Raw8<TYPE>& c = r.c[i];
-        if constexpr (TYPE == AF_F32) {
-            // the two halves in an order that differs between groups of four lanes: every bank once per access
-            const uint4* p = reinterpret_cast<const uint4*>(st) + idx * 2;
-            const int sw = (lane >> 2) & 1;
-            const uint4 x = p[sw], y = p[sw ^ 1];
-            c.a = sw ? y : x;
-            c.b = sw ? x : y;
-        } else {
-            if constexpr (TYPE == AF_KV_Q8_0)
-                c.a = reinterpret_cast<const uint2*>(st)[idx];
-            else
-                c.a = reinterpret_cast<const uint32_t*>(st)[idx];
-            c.d = reinterpret_cast<const __half*>(sc)[idx / 4];
-        }
+        r.c[i].a = reinterpret_cast<const decltype(r.c[i].a)*>(st)[idx];
+        if constexpr (TYPE != AF_F32) r.c[i].d = reinterpret_cast<const __half*>(sc)[idx / 4];
     }
 }
 
@@ -248,12 +235,12 @@ __device__ __forceinline__ unsigned clean_raw(RawTile<TYPE, D>& r, int valid, in
     unsigned rows = 0;
 #pragma unroll
     for (int i = 0; i < RawTile<TYPE, D>::N; i++) {
-        const int row = (i * 32 + lane) / (D / 8);
-        Raw8<TYPE>& c = r.c[i];
+        Raw<TYPE>& c = r.c[i];
+        const int row = (i * 32 + lane) / (D / c.VALUES);
         if constexpr (TYPE == AF_F32) {
-            uint32_t* w[8] = {&c.a.x, &c.a.y, &c.a.z, &c.a.w, &c.b.x, &c.b.y, &c.b.z, &c.b.w};
+            uint32_t* w[4] = {&c.a.x, &c.a.y, &c.a.z, &c.a.w};
 #pragma unroll
-            for (int e = 0; e < 8; e++)
+            for (int e = 0; e < 4; e++)
                 if (row >= valid || (*w[e] & 0x7F800000u) == 0x7F800000u) {
                     if (row < valid) rows |= 1u << row;
                     *w[e] = 0u;
@@ -275,15 +262,29 @@ __device__ __forceinline__ float raw_max(const RawTile<TYPE, D>& r) {
 #pragma unroll
     for (int i = 0; i < RawTile<TYPE, D>::N; i++) {
         if constexpr (TYPE == AF_F32) {
-            const uint32_t w[8] = {r.c[i].a.x, r.c[i].a.y, r.c[i].a.z, r.c[i].a.w, r.c[i].b.x, r.c[i].b.y, r.c[i].b.z, r.c[i].b.w};
-#pragma unroll
-            for (int e = 0; e < 8; e += 2)
-                m = fmaxf(fmaxf(m, fabsf(__uint_as_float(w[e]))), fabsf(__uint_as_float(w[e + 1])));
+            const uint4 a = r.c[i].a;
+            m = fmaxf(fmaxf(m, fabsf(__uint_as_float(a.x))), fabsf(__uint_as_float(a.y)));
+            m = fmaxf(fmaxf(m, fabsf(__uint_as_float(a.z))), fabsf(__uint_as_float(a.w)));
         } else {
             m = fmaxf(m, fabsf(__half2float(r.c[i].d)));
         }
     }
     return m;
+}
+
+__device__ __forceinline__ float warp_max(float m) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return m;
+}
+
+// Arrive, not before x (>= 0) has been computed.
+__device__ __forceinline__ void mbar_arrive_after(uint64_t* bar, float x) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ge.f32 p, %1, 0f00000000;\n\t"
+        "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "f"(x)
+        : "memory");
 }
 
 __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
@@ -293,18 +294,22 @@ __device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<co
 // [64 slots][128 B] each).
 template <int TYPE, int D>
 __device__ __forceinline__ void store_tile(uint8_t* dst, const RawTile<TYPE, D>& r, int e, int row0, int lane) {
-    constexpr int CPR = D / 8, PART = BK * D * 2;
+    constexpr int PPR = D / Raw<TYPE>::VALUES, PART = BK * D * 2;  // pieces per row
     const float down = pow2i(-e);
 #pragma unroll
     for (int i = 0; i < RawTile<TYPE, D>::N; i++) {
-        const int idx = i * 32 + lane, key = row0 + idx / CPR, ch = idx % CPR;
-        uint32_t hi[4], lo[4];
+        const int idx = i * 32 + lane, key = row0 + idx / PPR, d0 = idx % PPR * Raw<TYPE>::VALUES;
+        const uint32_t off = (uint32_t)((d0 >> 6) * BK * 128) + sw128(key, (d0 >> 3) & 7) + (d0 & 7) * 2;
         if constexpr (TYPE == AF_F32) {
-            const uint32_t w[8] = {r.c[i].a.x, r.c[i].a.y, r.c[i].a.z, r.c[i].a.w, r.c[i].b.x, r.c[i].b.y, r.c[i].b.z, r.c[i].b.w};
-#pragma unroll
-            for (int p = 0; p < 4; p++)
-                split2(mul2(make_float2(__uint_as_float(w[2 * p]), __uint_as_float(w[2 * p + 1])), make_float2(down, down)), hi[p], lo[p]);
+            const uint4 a = r.c[i].a;
+            const float2 dd = make_float2(down, down);
+            uint2 hi, lo;
+            split2(mul2(make_float2(__uint_as_float(a.x), __uint_as_float(a.y)), dd), hi.x, lo.x);
+            split2(mul2(make_float2(__uint_as_float(a.z), __uint_as_float(a.w)), dd), hi.y, lo.y);
+            *reinterpret_cast<uint2*>(dst + off) = hi;
+            *reinterpret_cast<uint2*>(dst + PART + off) = lo;
         } else {
+            uint32_t hi[4], lo[4];
             // codes q are exact in fp16, and so is d 2^-e (11 bits); hi = fp16(q d), lo = q d - hi by a fused
             // multiply-add, exact as long as it is not below fp16's smallest step 2^-24
             const __half2 d2 = __float2half2_rn(__half2float(r.c[i].d) * down);
@@ -333,10 +338,9 @@ __device__ __forceinline__ void store_tile(uint8_t* dst, const RawTile<TYPE, D>&
                 hi[p] = h2u(h);
                 lo[p] = h2u(__hfma2(q[p], d2, __hneg2(h)));
             }
+            *reinterpret_cast<uint4*>(dst + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(dst + PART + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
-        const uint32_t off = (uint32_t)((ch >> 3) * BK * 128) + sw128(key, ch & 7);
-        *reinterpret_cast<uint4*>(dst + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(dst + PART + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
 }
 
@@ -401,49 +405,85 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         Ring<C::NS> rk, rv;
         bool ok = twait(&sm.q_ready, 0, sm);
-        auto scores = [&](int t) {
-            if (t >= 4 && !twait(&sm.pv_done[t & 3], ((t - 4) >> 2) & 1, sm)) return false;
-            if (!twait(&sm.full[0][rk.i], rk.ph, sm)) return false;
-            tc_fence_after();
-            if (lead) {
-                const uint64_t kd = kd0 + (uint32_t)(rk.i * (C::SLOT >> 4));
-                const uint32_t d = tm + kSCol + (t & 3) * BK;
+        tc_fence_after();
+        // A step's barriers are looked at while the previous step is being issued (the pipe is busy with it); only if
+        // they were not all complete is there a wait.
+        auto scores_ready = [&](int t) {
+            return (t < 4 || mbar_try_wait(&sm.pv_done[t & 3], ((t - 4) >> 2) & 1)) && mbar_try_wait(&sm.full[0][rk.i], rk.ph);
+        };
+        auto scores_wait = [&](int t) {
+            return (t < 4 || twait(&sm.pv_done[t & 3], ((t - 4) >> 2) & 1, sm)) && twait(&sm.full[0][rk.i], rk.ph, sm);
+        };
+        auto out_ready = [&](int t) {
+            return mbar_try_wait(&sm.full[1][rv.i], rv.ph) && mbar_try_wait(&sm.p_full[t & 3], (t >> 2) & 1);
+        };
+        auto out_wait = [&](int t) { return twait(&sm.full[1][rv.i], rv.ph, sm) && twait(&sm.p_full[t & 3], (t >> 2) & 1, sm); };
+        auto scores = [&](int t, int from, int to) {
+            if (!lead) return;
+            const uint64_t kd = kd0 + (uint32_t)(rk.i * (C::SLOT >> 4));
+            const uint32_t d = tm + kSCol + (t & 3) * BK;
 #pragma unroll
-                for (int kk = 0; kk < D / 16; kk++) {
-                    const uint64_t b = kd + (((kk >> 2) * BK * 128 + (kk & 3) * 32) >> 4);
-                    mma_f16_ts(d, tm + kQCol + kk * 8, b, kIdS, kk > 0);
-                    mma_f16_ts(d, tm + kQCol + D / 2 + kk * 8, b, kIdS, 1);
-                    if (C::SPLIT) mma_f16_ts(d, tm + kQCol + kk * 8, b + (C::PART >> 4), kIdS, 1);
-                }
+            for (int kk = from; kk < to; kk++) {
+                const uint64_t b = kd + (((kk >> 2) * BK * 128 + (kk & 3) * 32) >> 4);
+                mma_f16_ts(d, tm + kQCol + kk * 8, b, kIdS, kk > 0);
+                mma_f16_ts(d, tm + kQCol + D / 2 + kk * 8, b, kIdS, 1);
+                if (C::SPLIT) mma_f16_ts(d, tm + kQCol + kk * 8, b + (C::PART >> 4), kIdS, 1);
+            }
+            if (to == D / 16) {
                 mma_commit(&sm.s_full[t & 3]);
                 mma_commit(&sm.empty[0][rk.i]);
                 if (C::SPLIT) mbar_arrive(&sm.s_full[t & 3]);
             }
-            __syncwarp();
-            rk.next();
-            return true;
         };
-        for (int t = 0; ok && t < min(kAhead, T); t++) ok = scores(t);
-        for (int t = 0; ok && t < T; t++) {
-            ok = twait(&sm.full[1][rv.i], rv.ph, sm) && twait(&sm.p_full[t & 3], (t >> 2) & 1, sm);
-            if (!ok) break;
-            tc_fence_after();
-            if (lead) {
-                const uint64_t vd = vd0 + (uint32_t)(rv.i * (C::SLOT >> 4));
-                const uint32_t p = tm + kSCol + (t & 3) * BK;
+        auto out = [&](int t, int from, int to) {
+            if (!lead) return;
+            const uint64_t vd = vd0 + (uint32_t)(rv.i * (C::SLOT >> 4));
+            const uint32_t p = tm + kSCol + (t & 3) * BK;
 #pragma unroll
-                for (int kk = 0; kk < BK / 16; kk++) {
-                    const uint64_t b = vd + ((kk * 2048) >> 4);
-                    mma_f16_ts(tm, p + kk * 8, b, kIdO, t > 0 || kk > 0);
-                    mma_f16_ts(tm, p + BK / 2 + kk * 8, b, kIdO, 1);
-                    if (C::SPLIT) mma_f16_ts(tm, p + kk * 8, b + (C::PART >> 4), kIdO, 1);
-                }
+            for (int kk = from; kk < to; kk++) {
+                const uint64_t b = vd + ((kk * 2048) >> 4);
+                mma_f16_ts(tm, p + kk * 8, b, kIdO, t > 0 || kk > 0);
+                mma_f16_ts(tm, p + BK / 2 + kk * 8, b, kIdO, 1);
+                if (C::SPLIT) mma_f16_ts(tm, p + kk * 8, b + (C::PART >> 4), kIdO, 1);
+            }
+            if (to == BK / 16) {
                 mma_commit(&sm.pv_done[t & 3]);
                 mma_commit(&sm.empty[1][rv.i]);
             }
+        };
+        for (int t = 0; ok && t < min(kAhead, T); t++) {
+            ok = scores_wait(t);
+            if (!ok) break;
+            tc_fence_after();
+            scores(t, 0, D / 16);
+            __syncwarp();
+            rk.next();
+        }
+        bool next = false;  // the next step's barriers have been seen complete
+        for (int t = 0; ok && t < T; t++) {
+            const bool more = t + kAhead < T;
+            ok = next || out_wait(t);
+            if (!ok) break;
+            tc_fence_after();
+            out(t, 0, BK / 16 - 1);
+            __syncwarp();
+            next = more && __all_sync(0xffffffffu, scores_ready(t + kAhead));
+            out(t, BK / 16 - 1, BK / 16);
             __syncwarp();
             rv.next();
-            if (t + kAhead < T) ok = scores(t + kAhead);
+            if (more) {
+                ok = next || scores_wait(t + kAhead);
+                if (!ok) break;
+                tc_fence_after();
+                scores(t + kAhead, 0, D / 16 - 2);
+                __syncwarp();
+                next = __all_sync(0xffffffffu, out_ready(t + 1));
+                scores(t + kAhead, D / 16 - 2, D / 16);
+                __syncwarp();
+                rk.next();
+            } else {
+                next = false;
+            }
         }
         if (lead) mma_commit(&sm.done);  // always: the drain waits on it
     } else if (warp >= C::COPY_WARP) {
@@ -502,6 +542,12 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                 RawTile<TYPE, D> raw;
                 // Every warp waits for every staging slot of the tile and frees it, the ones without its rows too: a
                 // warp that skipped a round of a slot could not tell that round's completion from the next one's.
+                // A slot is freed when its values are in registers for certain, that is used: an arrival may overtake
+                // loads that are still queued, and the next copy then overwrites what they read (seen as wrong
+                // results of single CTAs).  fp32: the largest value depends on all of them; codes: after they are
+                // stored (below).
+                float m = 0.f;
+                const int slot0 = rr.i;
 #pragma unroll
                 for (int p = 0; p < kConvWarps / C::RU; p++, rr.next()) {
                     ok = ok && twait(&sm.raw_full[x][rr.i], rr.ph, sm);
@@ -510,18 +556,16 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                         const uint8_t* st = smem + C::OFF_RAW + (x * C::NR + rr.i) * C::RAW;
                         const int wr = (w % C::RU) * 16;  // the warp's rows in the slot
                         load_raw<TYPE, D>(st + wr * C::RB, st + C::RR * C::RB + wr * C::SB, lane, raw);
+                        m = warp_max(raw_max<TYPE, D>(raw));
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.raw_empty[x][rr.i]);
+                    if (TYPE == AF_F32 && lane == 0) mbar_arrive_after(&sm.raw_empty[x][rr.i], m);
                 }
                 if (!ok) break;
                 if (t >= tn) {
                     const unsigned bad = clean_raw<TYPE, D>(raw, valid - t * BK - w * 16, lane);
                     if (bad) atomicOr(&sm.bad[t - tn], (unsigned long long)bad << (w * 16));
+                    m = warp_max(raw_max<TYPE, D>(raw));
                 }
-                float m = raw_max<TYPE, D>(raw);
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
                 // largest value in [1, 2), or largest scale times its largest code in [1, 4)
                 int e = max(exponent_of(m), -126);
                 if (TYPE == AF_KV_Q8_0) e += 6;
@@ -531,6 +575,8 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                 if (x == 1 && t == C::NS - C::QS) ok = ok && twait(&sm.q_ready, 0, sm);
                 if (!ok) break;
                 store_tile<TYPE, D>(smem + (x ? C::OFF_V : 0) + ro.i * C::SLOT, raw, e, w * 16, lane);
+                __syncwarp();
+                if (TYPE != AF_F32 && lane == 0) mbar_arrive(&sm.raw_empty[x][slot0]);
                 if (lane == 0) {
                     if (x == 1)
                         sm.ev[t & 7][w] = m == 0.f ? kNoExp : e;
