@@ -7,6 +7,7 @@ is no CPU path: importing this package raises if the library is missing.
 """
 import ctypes
 import os
+import struct
 
 from ._build import LIB_PATH, build  # noqa: F401
 
@@ -104,6 +105,7 @@ def lib():
         L.af_attention_tree_workspace.argtypes = [i32] * 6
         L.af_attention_tree_workspace.restype = u64
         L.af_attention_tree.argtypes = [vp, i64, vp, vp, vp, vp] + [i32] * 7 + [vp, vp, u64, vp, i64, vp]
+        L.af_packed_call.argtypes = [ctypes.c_int, ctypes.c_char_p]
         _lib = L
     return _lib
 
@@ -122,11 +124,24 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_raw_stream = None
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream() if _raw_stream else _find_stream()
     return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _find_stream():
+    """torch's current stream on the current device; the lookup without a Stream object where torch has it."""
+    import torch
+    global _raw_stream
+    s = torch.cuda.current_stream().cuda_stream
+    raw, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    if raw and dev:
+        _raw_stream = lambda: raw(dev())  # noqa: E731
+    return s
 
 
 def make_config(cfg, max_chunk: int = 512) -> af_config:
@@ -300,28 +315,46 @@ def rope_config(head_dim: int, rot_dim: int, layout: str = "interleaved", base: 
                           turns_low, turns_high, magnitude)
 
 
+# The calls below are made many times a step: their arguments go over as one packed record, which costs a third of
+# ctypes' conversion of each (the records' layouts: af_packed_call in api.cu).
+_ROPE = struct.Struct("@PPqPqiiiPiP").pack
+_KV_WRITE = struct.Struct("@PPqiPiPPPPiiiiP").pack
+_KV_READ = struct.Struct("@PPPPiiiiiPiPPqP").pack
+_TREE_MASK = struct.Struct("@PiiPPP").pack
+_TREE = struct.Struct("@PqPPPPiiiiiiiPPQPqP").pack
+
+
+def _addr(t):
+    return 0 if t is None else t if type(t) is int else t.data_ptr()
+
+
+def _packed(op, record):
+    rc = (_lib or lib()).af_packed_call(op, record)
+    return check(rc) if rc else rc
+
+
 def af_rope(cfg: af_rope_config, x_dev, ldx: int, y_dev, ldy: int, dtype: int, n: int, n_heads: int, pos_dev,
             pos0: int = 0, stream=None):
-    return check(lib().af_rope(ctypes.byref(cfg), _ptr(x_dev), ldx, _ptr(y_dev), ldy, dtype, n, n_heads, _ptr(pos_dev),
-                               pos0, _stream(stream)))
+    return _packed(0, _ROPE(ctypes.addressof(cfg), _addr(x_dev), ldx, _addr(y_dev), ldy, dtype, n, n_heads,
+                            _addr(pos_dev), pos0, _stream(stream)))
 
 
 def af_kv_write(k_dev, v_dev, ld: int, n: int, slots_dev, slot0: int, k_cache, k_scales, v_cache, v_scales,
                 kv_dtype: int, n_kv_heads: int, head_dim: int, ctx: int, stream=None):
-    return check(lib().af_kv_write(_ptr(k_dev), _ptr(v_dev), ld, n, _ptr(slots_dev), slot0, _ptr(k_cache),
-                                   _ptr(k_scales), _ptr(v_cache), _ptr(v_scales), kv_dtype, n_kv_heads, head_dim, ctx,
-                                   _stream(stream)))
+    return _packed(1, _KV_WRITE(_addr(k_dev), _addr(v_dev), ld, n, _addr(slots_dev), slot0, _addr(k_cache),
+                                _addr(k_scales), _addr(v_cache), _addr(v_scales), kv_dtype, n_kv_heads, head_dim, ctx,
+                                _stream(stream)))
 
 
 def af_kv_read(k_cache, k_scales, v_cache, v_scales, kv_dtype: int, n_kv_heads: int, head_dim: int, ctx: int, n: int,
                slots_dev, slot0: int, k_dev, v_dev, ld: int, stream=None):
-    return check(lib().af_kv_read(_ptr(k_cache), _ptr(k_scales), _ptr(v_cache), _ptr(v_scales), kv_dtype, n_kv_heads,
-                                  head_dim, ctx, n, _ptr(slots_dev), slot0, _ptr(k_dev), _ptr(v_dev), ld,
-                                  _stream(stream)))
+    return _packed(2, _KV_READ(_addr(k_cache), _addr(k_scales), _addr(v_cache), _addr(v_scales), kv_dtype, n_kv_heads,
+                               head_dim, ctx, n, _addr(slots_dev), slot0, _addr(k_dev), _addr(v_dev), ld,
+                               _stream(stream)))
 
 
 def af_tree_mask(parent_dev, n: int, pos0: int, mask_dev, pos_dev=None, stream=None):
-    return check(lib().af_tree_mask(_ptr(parent_dev), n, pos0, _ptr(mask_dev), _ptr(pos_dev), _stream(stream)))
+    return _packed(3, _TREE_MASK(_addr(parent_dev), n, pos0, _addr(mask_dev), _addr(pos_dev), _stream(stream)))
 
 
 def af_attention_tree_workspace(kv_dtype: int, n_heads: int, n_kv_heads: int, head_dim: int, n_past: int,
@@ -332,9 +365,9 @@ def af_attention_tree_workspace(kv_dtype: int, n_heads: int, n_kv_heads: int, he
 def af_attention_tree(q_dev, ldq: int, k_cache, k_scales, v_cache, v_scales, kv_dtype: int, n_heads: int,
                       n_kv_heads: int, head_dim: int, ctx: int, n_past: int, n: int, mask_dev, ws_dev, ws_bytes: int,
                       out_dev, ldo: int, stream=None):
-    return check(lib().af_attention_tree(_ptr(q_dev), ldq, _ptr(k_cache), _ptr(k_scales), _ptr(v_cache),
-                                         _ptr(v_scales), kv_dtype, n_heads, n_kv_heads, head_dim, ctx, n_past, n,
-                                         _ptr(mask_dev), _ptr(ws_dev), ws_bytes, _ptr(out_dev), ldo, _stream(stream)))
+    return _packed(4, _TREE(_addr(q_dev), ldq, _addr(k_cache), _addr(k_scales), _addr(v_cache), _addr(v_scales),
+                            kv_dtype, n_heads, n_kv_heads, head_dim, ctx, n_past, n, _addr(mask_dev), _addr(ws_dev),
+                            ws_bytes, _addr(out_dev), ldo, _stream(stream)))
 
 
 def af_last_error() -> str:

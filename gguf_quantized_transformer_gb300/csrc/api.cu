@@ -1237,4 +1237,85 @@ int af_attention_tree(const float* q_dev, int64_t ldq, const void* k_cache, cons
     return AF_OK;
 }
 
+// The calls above with their arguments as one record in C layout (members in the order of the arguments): what the
+// Python binding makes, since converting nineteen arguments one by one takes longer than the launch.
+__attribute__((visibility("default"))) int af_packed_call(int op, const void* record) {
+    if (!record) return fail(AF_EINVAL, "null record");
+    switch (op) {
+        case 0: {
+            struct R {
+                const af_rope_config* cfg;
+                const void* x;
+                int64_t ldx;
+                void* y;
+                int64_t ldy;
+                int32_t dtype, n, n_heads;
+                const int32_t* pos;
+                int32_t pos0;
+                void* stream;
+            } r;
+            memcpy(&r, record, sizeof r);
+            return af_rope(r.cfg, r.x, r.ldx, r.y, r.ldy, r.dtype, r.n, r.n_heads, r.pos, r.pos0, r.stream);
+        }
+        case 1: {
+            struct R {
+                const float *k, *v;
+                int64_t ld;
+                int32_t n;
+                const int32_t* slots;
+                int32_t slot0;
+                void *kc, *ks, *vc, *vs;
+                int32_t type, kvh, d, ctx;
+                void* stream;
+            } r;
+            memcpy(&r, record, sizeof r);
+            return af_kv_write(r.k, r.v, r.ld, r.n, r.slots, r.slot0, r.kc, r.ks, r.vc, r.vs, r.type, r.kvh, r.d, r.ctx,
+                               r.stream);
+        }
+        case 2: {
+            struct R {
+                const void *kc, *ks, *vc, *vs;
+                int32_t type, kvh, d, ctx, n;
+                const int32_t* slots;
+                int32_t slot0;
+                float *k, *v;
+                int64_t ld;
+                void* stream;
+            } r;
+            memcpy(&r, record, sizeof r);
+            return af_kv_read(r.kc, r.ks, r.vc, r.vs, r.type, r.kvh, r.d, r.ctx, r.n, r.slots, r.slot0, r.k, r.v, r.ld,
+                              r.stream);
+        }
+        case 3: {
+            struct R {
+                const int32_t* parent;
+                int32_t n, pos0;
+                uint32_t* mask;
+                int32_t* pos;
+                void* stream;
+            } r;
+            memcpy(&r, record, sizeof r);
+            return af_tree_mask(r.parent, r.n, r.pos0, r.mask, r.pos, r.stream);
+        }
+        case 4: {
+            struct R {
+                const float* q;
+                int64_t ldq;
+                const void *kc, *ks, *vc, *vs;
+                int32_t type, h, kvh, d, ctx, past, n;
+                const uint32_t* mask;
+                void* ws;
+                uint64_t ws_bytes;
+                float* out;
+                int64_t ldo;
+                void* stream;
+            } r;
+            memcpy(&r, record, sizeof r);
+            return af_attention_tree(r.q, r.ldq, r.kc, r.ks, r.vc, r.vs, r.type, r.h, r.kvh, r.d, r.ctx, r.past, r.n, r.mask,
+                                     r.ws, r.ws_bytes, r.out, r.ldo, r.stream);
+        }
+        default: return fail(AF_EINVAL, "unknown record");
+    }
+}
+
 }  // extern "C"

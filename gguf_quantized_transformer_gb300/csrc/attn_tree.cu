@@ -38,8 +38,10 @@ namespace {
 __global__ void __launch_bounds__(256)
     tree_mask_kernel(const int* __restrict__ parent, int n, int pos0, unsigned* __restrict__ mask, int* __restrict__ pos) {
     __shared__ int up[kTreeMax];
+    pdl_launch_dependents();
+    pdl_wait();
     for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        const int p = parent[i];
+        const int p = __ldcg(parent + i);
         up[i] = p >= 0 && p < i ? p : -1;
     }
     __syncthreads();
@@ -876,8 +878,7 @@ cudaError_t go_type(const TreeArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_tree_mask(const int* parent, int n, int pos0, unsigned* mask, int* pos, cudaStream_t s) {
-    tree_mask_kernel<<<(n + 7) / 8, 256, 0, s>>>(parent, n, pos0, mask, pos);
-    return cudaGetLastError();
+    return launch_chained(tree_mask_kernel, dim3((n + 7) / 8), 256, 0, s, parent, n, pos0, mask, pos);
 }
 
 size_t attn_tree_ws_bytes(int H, int KVH, int D, int type, int past, int n) {

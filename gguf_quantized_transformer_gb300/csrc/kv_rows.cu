@@ -9,19 +9,37 @@
 // distance of two fp32 numbers near v is at least 2^-24 of v, more than the half step 2^-25 .. 2^-24 that a
 // quotient of that size is rounded by).  A zero d gives zero codes.  A block that holds a NaN, or whose scale
 // overflows fp16, gets a scale that makes all its values NaN: nothing non-finite is turned into a number.
+//
+// Both are bound by HBM.  A CTA takes kRows rows at a time and a thread four values of K and of V of each, all loads
+// before the first use; the grid is a few CTAs per SM.  Data of earlier kernels is read through L2 (the kernels are
+// launched with programmatic serialization).
+#include <algorithm>
+
 #include "draft.cuh"
+#include "tma.cuh"
 
 namespace af {
 
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kRows = 4;
+constexpr int kCtasPerSm = 6;
+
+// OR over the CTA, in every thread
+__device__ __forceinline__ unsigned cta_or(unsigned x) {
+    __shared__ unsigned part[kThreads / 32];
+    x = __reduce_or_sync(0xffffffffu, x);
+    __syncthreads();  // (the previous result has been read)
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = x;
+    __syncthreads();
+    x = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; w++) x |= part[w];
+    return x;
+}
 
 // Eight lanes (an aligned group of the warp) hold the 32 values of a block, four each.
-struct Block4 {
-    float x[4];
-};
-
 template <int TYPE>
 __device__ __forceinline__ void quantize_group(const float (&x)[4], unsigned group, int lane, int (&q)[4], __half& dh) {
     float amax = 0.f;
@@ -96,7 +114,6 @@ __device__ __forceinline__ void store_group(void* base, __half* scales, int64_t 
     }
 }
 
-// One CTA per row of a grid-stride walk; a thread handles four values of K or V at a time.
 template <int TYPE>
 __global__ void __launch_bounds__(kThreads)
     kv_write_kernel(KvRows c, const float* __restrict__ k, const float* __restrict__ v, int64_t ld, int n,
@@ -104,42 +121,79 @@ __global__ void __launch_bounds__(kThreads)
     const int lane = threadIdx.x & 31;
     const unsigned group = 0xffu << (lane & 24);
     const int quads = c.KVH * c.D / 4;  // a multiple of 8
-    for (int r = blockIdx.x; r < n; r += gridDim.x) {
-        int slot = slot0 + r;
+    pdl_launch_dependents();
+    pdl_wait();
+    for (int r0 = blockIdx.x * kRows; r0 < n; r0 += gridDim.x * kRows) {
+        int slot[kRows];  // -1: not written; the same in every thread of the CTA
+#pragma unroll
+        for (int j = 0; j < kRows; j++) slot[j] = r0 + j >= n ? -1 : slots ? __ldcg(slots + r0 + j) : slot0 + r0 + j;
         if (slots) {
-            slot = slots[r];
-            if (slot < 0 || slot >= c.ctx) continue;  // uniform over the CTA
-            // a slot that a later row names too belongs to that row
-            bool again = false;
-            for (int j = r + 1 + threadIdx.x; j < n; j += kThreads) again |= slots[j] == slot;
-            if (__syncthreads_or(again)) continue;
+            unsigned again = 0;  // rows whose slot a later row names too: it belongs to that one
+            for (int i = r0 + 1 + threadIdx.x; i < n; i += kThreads) {
+                const int x = __ldcg(slots + i);
+#pragma unroll
+                for (int j = 0; j < kRows; j++) again |= (i > r0 + j && x == slot[j]) ? 1u << j : 0u;
+            }
+            again = cta_or(again);
+#pragma unroll
+            for (int j = 0; j < kRows; j++)
+                if (slot[j] < 0 || slot[j] >= c.ctx || (again >> j & 1)) slot[j] = -1;
         }
-        for (int i = threadIdx.x; i < 2 * quads; i += kThreads) {
-            const bool isv = i >= quads;
-            const int e0 = (isv ? i - quads : i) * 4;
-            const int g = e0 / c.D, d0 = e0 % c.D;
-            const float4 f = *reinterpret_cast<const float4*>((isv ? v : k) + r * ld + e0);
-            const float x[4] = {f.x, f.y, f.z, f.w};
-            store_group<TYPE>(isv ? c.v : c.k, isv ? c.vs : c.ks, (int64_t)g * c.ctx + slot, c.D, d0, x, group, lane);
+        for (int i = threadIdx.x; i < quads; i += kThreads) {
+            const int e0 = i * 4, g = e0 / c.D, d0 = e0 % c.D;
+            float4 x[2][kRows];
+#pragma unroll
+            for (int j = 0; j < kRows; j++)
+                if (slot[j] >= 0) {
+                    x[0][j] = __ldcg(reinterpret_cast<const float4*>(k + (r0 + j) * ld + e0));
+                    x[1][j] = __ldcg(reinterpret_cast<const float4*>(v + (r0 + j) * ld + e0));
+                }
+#pragma unroll
+            for (int j = 0; j < kRows; j++)
+                if (slot[j] >= 0) {
+                    const int64_t cell = (int64_t)g * c.ctx + slot[j];
+                    const float a[4] = {x[0][j].x, x[0][j].y, x[0][j].z, x[0][j].w};
+                    const float b[4] = {x[1][j].x, x[1][j].y, x[1][j].z, x[1][j].w};
+                    store_group<TYPE>(c.k, c.ks, cell, c.D, d0, a, group, lane);
+                    store_group<TYPE>(c.v, c.vs, cell, c.D, d0, b, group, lane);
+                }
         }
     }
 }
 
+// Four values as they lie in the cache, and as fp32.
 template <int TYPE>
-__device__ __forceinline__ float4 load4(const void* base, const __half* scales, int64_t cell, int D, int d0) {
-    if (TYPE == AF_F32) return *reinterpret_cast<const float4*>((const float*)base + cell * D + d0);
+struct Cell4 {
+    uint4 w;
+    __half d;
+};
+template <int TYPE>
+__device__ __forceinline__ void fetch4(const void* base, const __half* scales, int64_t cell, int D, int d0, Cell4<TYPE>& x) {
+    if (TYPE == AF_F32) {
+        x.w = __ldcg(reinterpret_cast<const uint4*>((const float*)base + cell * D + d0));
+    } else if (TYPE == AF_F16) {
+        const uint2 r = __ldcg(reinterpret_cast<const uint2*>((const __half*)base + cell * D + d0));
+        x.w.x = r.x, x.w.y = r.y;
+    } else {
+        x.d = __ushort_as_half(__ldcg(reinterpret_cast<const unsigned short*>(scales) + cell * (D / 32) + d0 / 32));
+        if (TYPE == AF_KV_Q8_0)
+            x.w.x = __ldcg(reinterpret_cast<const unsigned*>((const uint8_t*)base + cell * D + d0));
+        else
+            x.w.x = __ldcg(reinterpret_cast<const unsigned short*>((const uint8_t*)base + cell * (D / 2) + d0 / 2));
+    }
+}
+template <int TYPE>
+__device__ __forceinline__ float4 value4(const Cell4<TYPE>& x) {
+    if (TYPE == AF_F32) return *reinterpret_cast<const float4*>(&x.w);
     if (TYPE == AF_F16) {
-        const uint2 raw = *reinterpret_cast<const uint2*>((const __half*)base + cell * D + d0);
-        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&raw.x));
-        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&raw.y));
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&x.w.x));
+        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&x.w.y));
         return make_float4(a.x, a.y, b.x, b.y);
     }
-    const float d = __half2float(scales[cell * (D / 32) + d0 / 32]);
-    if (TYPE == AF_KV_Q8_0) {
-        const char4 q = *reinterpret_cast<const char4*>((const uint8_t*)base + cell * D + d0);
-        return make_float4(d * (signed char)q.x, d * (signed char)q.y, d * (signed char)q.z, d * (signed char)q.w);
-    }
-    const unsigned w = *reinterpret_cast<const unsigned short*>((const uint8_t*)base + cell * (D / 2) + d0 / 2);
+    const float d = __half2float(x.d);
+    const unsigned w = x.w.x;
+    if (TYPE == AF_KV_Q8_0)
+        return make_float4(d * (int8_t)(w & 255), d * (int8_t)(w >> 8 & 255), d * (int8_t)(w >> 16 & 255), d * (int8_t)(w >> 24));
     return make_float4(d * ((int)(w & 15) - 8), d * ((int)(w >> 4 & 15) - 8), d * ((int)(w >> 8 & 15) - 8),
                        d * ((int)(w >> 12) - 8));
 }
@@ -149,43 +203,58 @@ __global__ void __launch_bounds__(kThreads)
     kv_read_kernel(KvRows c, int n, const int* __restrict__ slots, int slot0, float* __restrict__ k,
                    float* __restrict__ v, int64_t ld) {
     const int quads = c.KVH * c.D / 4;
-    for (int r = blockIdx.x; r < n; r += gridDim.x) {
-        const int slot = slots ? slots[r] : slot0 + r;
-        if (slot < 0 || slot >= c.ctx) continue;
-        for (int i = threadIdx.x; i < 2 * quads; i += kThreads) {
-            const bool isv = i >= quads;
-            const int e0 = (isv ? i - quads : i) * 4;
-            const int g = e0 / c.D, d0 = e0 % c.D;
-            *reinterpret_cast<float4*>((isv ? v : k) + r * ld + e0) =
-                load4<TYPE>(isv ? c.v : c.k, isv ? c.vs : c.ks, (int64_t)g * c.ctx + slot, c.D, d0);
+    pdl_launch_dependents();
+    pdl_wait();
+    for (int r0 = blockIdx.x * kRows; r0 < n; r0 += gridDim.x * kRows) {
+        int slot[kRows];
+#pragma unroll
+        for (int j = 0; j < kRows; j++) {
+            slot[j] = r0 + j >= n ? -1 : slots ? __ldcg(slots + r0 + j) : slot0 + r0 + j;
+            if (slot[j] >= c.ctx) slot[j] = -1;
+        }
+        for (int i = threadIdx.x; i < quads; i += kThreads) {
+            const int e0 = i * 4, g = e0 / c.D, d0 = e0 % c.D;
+            Cell4<TYPE> x[2][kRows];
+#pragma unroll
+            for (int j = 0; j < kRows; j++)
+                if (slot[j] >= 0) {
+                    fetch4<TYPE>(c.k, c.ks, (int64_t)g * c.ctx + slot[j], c.D, d0, x[0][j]);
+                    fetch4<TYPE>(c.v, c.vs, (int64_t)g * c.ctx + slot[j], c.D, d0, x[1][j]);
+                }
+#pragma unroll
+            for (int j = 0; j < kRows; j++)
+                if (slot[j] >= 0) {
+                    *reinterpret_cast<float4*>(k + (r0 + j) * ld + e0) = value4<TYPE>(x[0][j]);
+                    *reinterpret_cast<float4*>(v + (r0 + j) * ld + e0) = value4<TYPE>(x[1][j]);
+                }
         }
     }
 }
+
+unsigned ctas(int n) { return (unsigned)std::min((n + kRows - 1) / kRows, num_sms() * kCtasPerSm); }
 
 }  // namespace
 
 cudaError_t launch_kv_write(const KvRows& c, const float* k, const float* v, int64_t ld, int n, const int* slots,
                             int slot0, cudaStream_t s) {
-    const unsigned blocks = (unsigned)(n < 65536 ? n : 65536);
+    auto go = [&](auto kernel) { return launch_chained(kernel, dim3(ctas(n)), kThreads, 0, s, c, k, v, ld, n, slots, slot0); };
     switch (c.type) {
-        case AF_F32: kv_write_kernel<AF_F32><<<blocks, kThreads, 0, s>>>(c, k, v, ld, n, slots, slot0); break;
-        case AF_F16: kv_write_kernel<AF_F16><<<blocks, kThreads, 0, s>>>(c, k, v, ld, n, slots, slot0); break;
-        case AF_KV_Q8_0: kv_write_kernel<AF_KV_Q8_0><<<blocks, kThreads, 0, s>>>(c, k, v, ld, n, slots, slot0); break;
-        default: kv_write_kernel<AF_KV_Q4_0><<<blocks, kThreads, 0, s>>>(c, k, v, ld, n, slots, slot0); break;
+        case AF_F32: return go(kv_write_kernel<AF_F32>);
+        case AF_F16: return go(kv_write_kernel<AF_F16>);
+        case AF_KV_Q8_0: return go(kv_write_kernel<AF_KV_Q8_0>);
+        default: return go(kv_write_kernel<AF_KV_Q4_0>);
     }
-    return cudaGetLastError();
 }
 
 cudaError_t launch_kv_read(const KvRows& c, int n, const int* slots, int slot0, float* k, float* v, int64_t ld,
                            cudaStream_t s) {
-    const unsigned blocks = (unsigned)(n < 65536 ? n : 65536);
+    auto go = [&](auto kernel) { return launch_chained(kernel, dim3(ctas(n)), kThreads, 0, s, c, n, slots, slot0, k, v, ld); };
     switch (c.type) {
-        case AF_F32: kv_read_kernel<AF_F32><<<blocks, kThreads, 0, s>>>(c, n, slots, slot0, k, v, ld); break;
-        case AF_F16: kv_read_kernel<AF_F16><<<blocks, kThreads, 0, s>>>(c, n, slots, slot0, k, v, ld); break;
-        case AF_KV_Q8_0: kv_read_kernel<AF_KV_Q8_0><<<blocks, kThreads, 0, s>>>(c, n, slots, slot0, k, v, ld); break;
-        default: kv_read_kernel<AF_KV_Q4_0><<<blocks, kThreads, 0, s>>>(c, n, slots, slot0, k, v, ld); break;
+        case AF_F32: return go(kv_read_kernel<AF_F32>);
+        case AF_F16: return go(kv_read_kernel<AF_F16>);
+        case AF_KV_Q8_0: return go(kv_read_kernel<AF_KV_Q8_0>);
+        default: return go(kv_read_kernel<AF_KV_Q4_0>);
     }
-    return cudaGetLastError();
 }
 
 }  // namespace af

@@ -9,9 +9,13 @@
 // positions, 2^-22 at 2^31.  The integer is reduced to the nearest quarter turn before it becomes a float, so the
 // argument of sin and cos is off by at most 2^-24 of its own value, itself at most pi / 4.
 //
-// Bound by HBM: every value is read and written once.  A thread owns a vector of pairs of one row and computes its
-// sines once for the heads it walks.
+// Sine and cosine on [-pi / 4, pi / 4] are their Taylor series (remainders below 2^-28 and 2^-33), two pairs at a time
+// in packed fp32.
+//
+// Bound by HBM: every value is read and written once.  A thread keeps one unit of the head (its frequencies in registers)
+// and walks rows with it, and the heads of a row with the sines of that row.
 #include "draft.cuh"
+#include "tma.cuh"
 
 namespace af {
 
@@ -19,59 +23,120 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ void turn_sincos(uint64_t turn, int pos, float mag, float& c, float& s) {
-    const uint64_t t = (uint64_t)((int64_t)pos) * turn;            // modulo one turn
-    const unsigned quad = (unsigned)((t + (1ull << 61)) >> 62);     // nearest quarter turn
-    const int rem = (int)((int64_t)(t << 2) >> 32);                 // the rest: [-1/8, 1/8) turn in 2^-34 turns
-    float sn, cs;
-    sincospif((float)rem * 0x1p-33f, &sn, &cs);
-    const float c0 = (quad & 1) ? -sn : cs, s0 = (quad & 1) ? cs : sn;
-    c = mag * ((quad & 2) ? -c0 : c0);
-    s = mag * ((quad & 2) ? -s0 : s0);
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)),
+          "l"(*reinterpret_cast<unsigned long long*>(&c)));
+    return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
+    return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// mag cos and mag sin of pos * turn, for two frequencies
+__device__ __forceinline__ void turn_sincos2(const uint64_t (&turn)[2], int pos, float mag, float (&c)[2], float (&s)[2]) {
+    unsigned quad[2];
+    float x[2];
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        const uint64_t t = (uint64_t)((int64_t)pos) * turn[i];     // modulo one turn
+        const unsigned h = (unsigned)(t >> 32);                     // (what lies below is 2^-32 of a turn)
+        quad[i] = (h + (1u << 29)) >> 30;                           // nearest quarter turn
+        x[i] = (float)(int)((unsigned)(t >> 30));                   // the rest in 2^-34 turns, [-1/8, 1/8) turn
+    }
+    const float2 a = mul2(make_float2(x[0], x[1]), both(3.14159265358979f * 0x1p-33f)), z = mul2(a, a);
+    float2 sn = fma2(z, both(1.f / 362880), both(-1.f / 5040));
+    sn = fma2(z, sn, both(1.f / 120));
+    sn = fma2(z, sn, both(-1.f / 6));
+    sn = fma2(mul2(z, a), sn, a);
+    float2 cs = fma2(z, both(-1.f / 3628800), both(1.f / 40320));
+    cs = fma2(z, cs, both(-1.f / 720));
+    cs = fma2(z, cs, both(1.f / 24));
+    cs = fma2(z, cs, both(-0.5f));
+    cs = fma2(z, cs, both(1.f));
+    const float2 m = both(mag);
+    sn = mul2(sn, m);
+    cs = mul2(cs, m);
+    const float sv[2] = {sn.x, sn.y}, cv[2] = {cs.x, cs.y};
+#pragma unroll
+    for (int i = 0; i < 2; i++) {  // quarter turns: (c, s) -> (-s, c)
+        const float c0 = (quad[i] & 1) ? -sv[i] : cv[i], s0 = (quad[i] & 1) ? cv[i] : sv[i];
+        const unsigned flip = (quad[i] & 2) << 30;
+        c[i] = __uint_as_float(__float_as_uint(c0) ^ flip);
+        s[i] = __uint_as_float(__float_as_uint(s0) ^ flip);
+    }
 }
 
 template <typename T, int N>
 struct alignas(sizeof(T) * N) Vec {
     T e[N];
 };
+// N values through L2 (an earlier kernel of the chain may have written them)
+template <typename T, int N>
+__device__ __forceinline__ Vec<T, N> load(const T* p) {
+    Vec<T, N> v;
+    if constexpr (sizeof(T) * N == 16)
+        *reinterpret_cast<uint4*>(&v) = __ldcg(reinterpret_cast<const uint4*>(p));
+    else if constexpr (sizeof(T) * N == 4)
+        *reinterpret_cast<unsigned*>(&v) = __ldcg(reinterpret_cast<const unsigned*>(p));
+    else
+        *reinterpret_cast<unsigned short*>(&v) = __ldcg(reinterpret_cast<const unsigned short*>(p));
+    return v;
+}
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
 __device__ __forceinline__ void from_f(float v, float& o) { o = v; }
 __device__ __forceinline__ void from_f(float v, __half& o) { o = __float2half_rn(v); }
 
-// V consecutive elements per access.  A unit of a head is: half layout, V pairs (elements i..i+V-1 and the same
-// + R/2); interleaved, V / 2 pairs (V consecutive elements; V = 1: one pair, two accesses of one element); past R,
-// V copied elements.
+// A unit of a head is, in accesses of V values: half layout, V pairs (elements i..i+V-1 and the same + R/2);
+// interleaved, V / 2 pairs (V consecutive elements; V = 1: one pair, two accesses); past R, V copied elements.
+// Rows are n * hgroups: (row, heads hg, hg + hgroups, ..).
 template <typename T, int V, bool HALF>
 __global__ void __launch_bounds__(kThreads)
     rope_kernel(const T* x, T* y, int64_t ldx, int64_t ldy, int n, int heads, int D, int R, const int* __restrict__ pos,
-                int pos0, float mag, int hgroups, const __grid_constant__ RopeTurns turns) {
-    constexpr int P = HALF ? V : (V > 1 ? V / 2 : 1);  // pairs per unit
-    const int rot_units = R / 2 / P, copy_units = (D - R) / V, units = rot_units + copy_units;
-    const int64_t total = (int64_t)n * hgroups * units;
-    for (int64_t w = (int64_t)blockIdx.x * kThreads + threadIdx.x; w < total; w += (int64_t)gridDim.x * kThreads) {
-        const int u = (int)(w % units);
-        const int64_t rg = w / units;
-        const int hg = (int)(rg % hgroups);
-        const int64_t row = rg / hgroups;
+                int pos0, float mag, int hgroups, int units, int rows_per_cta, const __grid_constant__ RopeTurns turns) {
+    constexpr int P = HALF ? V : (V > 1 ? V / 2 : 1), P2 = P > 1 ? P : 2;  // pairs per unit
+    const int rot_units = R / 2 / P;
+    const int u = threadIdx.x % units, rl = threadIdx.x / units;
+    const bool copy = u >= rot_units;
+    pdl_launch_dependents();
+    uint64_t tn[P2];
+#pragma unroll
+    for (int e = 0; e < P2; e++) tn[e] = !copy && e < P ? turns.turn[u * P + e] : 0;
+    pdl_wait();
+    const int64_t total = (int64_t)n * hgroups;
+    for (int64_t w = (int64_t)blockIdx.x * rows_per_cta + rl; w < total; w += (int64_t)gridDim.x * rows_per_cta) {
+        if (rl >= rows_per_cta) break;
+        const int hg = hgroups == 1 ? 0 : (int)(w % hgroups);
+        const int64_t row = hgroups == 1 ? w : w / hgroups;
         const T* xr = x + row * ldx;
         T* yr = y + row * ldy;
-        if (u >= rot_units) {
+        if (copy) {
             const int d = R + (u - rot_units) * V;
-            for (int h = hg; h < heads; h += hgroups)
-                *reinterpret_cast<Vec<T, V>*>(yr + h * D + d) = *reinterpret_cast<const Vec<T, V>*>(xr + h * D + d);
+            for (int h = hg; h < heads; h += hgroups) *reinterpret_cast<Vec<T, V>*>(yr + h * D + d) = load<T, V>(xr + h * D + d);
             continue;
         }
-        const int p = pos ? pos[row] : pos0 + (int)row;
-        float c[P], s[P];
+        const int p = pos ? __ldcg(pos + row) : pos0 + (int)row;
+        float c[P2], s[P2];
 #pragma unroll
-        for (int e = 0; e < P; e++) turn_sincos(turns.turn[u * P + e], p, mag, c[e], s[e]);
+        for (int e = 0; e < P2; e += 2) {
+            const uint64_t t2[2] = {tn[e], tn[e + 1]};
+            float c2[2], s2[2];
+            turn_sincos2(t2, p, mag, c2, s2);
+            c[e] = c2[0], c[e + 1] = c2[1], s[e] = s2[0], s[e + 1] = s2[1];
+        }
         for (int h = hg; h < heads; h += hgroups) {
             if (HALF) {
                 const int64_t ia = (int64_t)h * D + u * V, ib = ia + R / 2;
-                const Vec<T, V> a = *reinterpret_cast<const Vec<T, V>*>(xr + ia);
-                const Vec<T, V> b = *reinterpret_cast<const Vec<T, V>*>(xr + ib);
+                const Vec<T, V> a = load<T, V>(xr + ia), b = load<T, V>(xr + ib);
                 Vec<T, V> oa, ob;
 #pragma unroll
                 for (int e = 0; e < V; e++) {
@@ -82,20 +147,21 @@ __global__ void __launch_bounds__(kThreads)
                 *reinterpret_cast<Vec<T, V>*>(yr + ia) = oa;
                 *reinterpret_cast<Vec<T, V>*>(yr + ib) = ob;
             } else {
-                constexpr int W = V > 1 ? V : 2;
-                constexpr int A = V > 1 ? V : 1;  // elements per access
+                constexpr int W = V > 1 ? V : 2, A = V > 1 ? V : 1;  // elements of the unit, of an access
                 const int64_t i0 = (int64_t)h * D + u * W;
-                alignas(16) T in[W], out[W];
+                Vec<T, A> v[W / A];
 #pragma unroll
-                for (int e = 0; e < W; e += A) *reinterpret_cast<Vec<T, A>*>(in + e) = *reinterpret_cast<const Vec<T, A>*>(xr + i0 + e);
+                for (int e = 0; e < W / A; e++) v[e] = load<T, A>(xr + i0 + e * A);
 #pragma unroll
                 for (int e = 0; e < W; e += 2) {
-                    const float fa = to_f(in[e]), fb = to_f(in[e + 1]);
-                    from_f(fa * c[e / 2] - fb * s[e / 2], out[e]);
-                    from_f(fa * s[e / 2] + fb * c[e / 2], out[e + 1]);
+                    T& a = v[e / A].e[e % A];
+                    T& b = v[(e + 1) / A].e[(e + 1) % A];
+                    const float fa = to_f(a), fb = to_f(b);
+                    from_f(fa * c[e / 2] - fb * s[e / 2], a);
+                    from_f(fa * s[e / 2] + fb * c[e / 2], b);
                 }
 #pragma unroll
-                for (int e = 0; e < W; e += A) *reinterpret_cast<Vec<T, A>*>(yr + i0 + e) = *reinterpret_cast<const Vec<T, A>*>(out + e);
+                for (int e = 0; e < W / A; e++) *reinterpret_cast<Vec<T, A>*>(yr + i0 + e * A) = v[e];
             }
         }
     }
@@ -104,16 +170,14 @@ __global__ void __launch_bounds__(kThreads)
 template <typename T, int V, bool HALF>
 cudaError_t go(const RopeArgs& a, const RopeTurns& t, cudaStream_t s) {
     constexpr int P = HALF ? V : (V > 1 ? V / 2 : 1);
-    const int64_t units = a.R / 2 / P + (a.D - a.R) / V;
+    const int units = a.R / 2 / P + (a.D - a.R) / V, rows = kThreads / units;  // (units <= 255: R >= 2, D <= 256)
     const int64_t room = (int64_t)num_sms() * 2048;
-    int64_t hg = (room + a.n * units - 1) / (a.n * units);  // head groups: enough threads to fill the card
-    if (hg > a.heads) hg = a.heads;
-    if (hg < 1) hg = 1;
-    int64_t blocks = (a.n * hg * units + kThreads - 1) / kThreads;
-    if (blocks > (int64_t)num_sms() * 64) blocks = (int64_t)num_sms() * 64;
-    rope_kernel<T, V, HALF><<<(unsigned)blocks, kThreads, 0, s>>>((const T*)a.x, (T*)a.y, a.ldx, a.ldy, a.n, a.heads, a.D,
-                                                                   a.R, a.pos, a.pos0, a.mag, (int)hg, t);
-    return cudaGetLastError();
+    int64_t hg = (room + a.n * (int64_t)units - 1) / (a.n * (int64_t)units);  // head groups: enough threads to fill the card
+    hg = hg > a.heads ? a.heads : (hg < 1 ? 1 : hg);
+    int64_t blocks = (a.n * hg + rows - 1) / rows;
+    if (blocks > (int64_t)num_sms() * 8) blocks = (int64_t)num_sms() * 8;
+    return launch_chained(rope_kernel<T, V, HALF>, dim3((unsigned)blocks), kThreads, 0, s, (const T*)a.x, (T*)a.y, a.ldx, a.ldy,
+                          a.n, a.heads, a.D, a.R, a.pos, a.pos0, a.mag, (int)hg, units, rows, t);
 }
 
 template <typename T>
