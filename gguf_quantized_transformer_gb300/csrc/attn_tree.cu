@@ -130,8 +130,8 @@ __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) 
 // (a, b) = hi + lo in two fp16 parts each
 __device__ __forceinline__ void split_h2(float a, float b, uint32_t& hi, uint32_t& lo) {
     const __half2 h = __floats2half2_rn(a, b);
-    const float2 back = __half22float2(h);
-    const __half2 l = __floats2half2_rn(a - back.x, b - back.y);
+    const float2 r = fma2(__half22float2(h), both(-1.f), make_float2(a, b));
+    const __half2 l = __floats2half2_rn(r.x, r.y);
     hi = *reinterpret_cast<const uint32_t*>(&h);
     lo = *reinterpret_cast<const uint32_t*>(&l);
 }
@@ -147,17 +147,28 @@ __device__ __forceinline__ uint32_t finite_h2(uint32_t x, bool& bad) {
     return x & ((lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u));
 }
 
-template <int TYPE, int D>
+// Slots a warp takes at a time and warps of a CTA.  The codes' kernels are bound by their instructions: with 16 rows (64
+// registers of output) twelve warps of 168 registers fit.
+__host__ __device__ constexpr int tree_stage(int type, int mt) {
+    return (type == AF_KV_Q8_0 || type == AF_KV_Q4_0) && mt == 1 ? 32 : 16;
+}
+__host__ __device__ constexpr int tree_warps(int type, int D, int mt) {
+    return type == AF_F32 && D == 128 ? 6 : (type == AF_KV_Q8_0 || type == AF_KV_Q4_0) && mt == 1 ? 12 : 8;
+}
+
+template <int TYPE, int D, int MT>
 struct TreeCfg {
     static constexpr bool QUANT = TYPE == AF_KV_Q8_0 || TYPE == AF_KV_Q4_0;
     static constexpr int NB = D / 32;                                             // 32-value blocks of a head
     static constexpr int RB = TYPE == AF_F32 ? 4 * D : TYPE == AF_F16 ? 2 * D : TYPE == AF_KV_Q8_0 ? D : D / 2;  // row bytes
     static constexpr int SB = QUANT ? 2 * NB : 0;                                 // scale bytes of a row
-    static constexpr int KS = QUANT ? 32 : 16;                                    // slots per stage
-    static constexpr int NW = TYPE == AF_F32 && D == 128 ? 6 : 8;                 // warps
+    static constexpr int KS = tree_stage(TYPE, MT);                               // slots per stage
+    static constexpr int NW = tree_warps(TYPE, D, MT);                            // warps
     static constexpr int OV = KS * RB, OKS = 2 * KS * RB, OVS = OKS + KS * SB;    // V, K scales, V scales in a stage
     static constexpr int STAGE = 2 * KS * (RB + SB);
-    static constexpr int NST = 192 * 1024 / (NW * STAGE) < 4 ? 192 * 1024 / (NW * STAGE) : 4;  // stages of a warp
+    static constexpr int RING = (QUANT ? 216 : 192) * 1024;
+    static constexpr int NST = RING / (NW * STAGE) < 4 ? RING / (NW * STAGE) : 4;  // stages of a warp
+    static_assert(NST >= 2, "a stage in flight while one is read");
     static constexpr int DP = D + (TYPE == AF_F16 ? 8 : 4);                       // padded output row of the join
     static constexpr int KQ = TYPE == AF_F32 ? D / 8 : D / 16;                    // mma steps along a head
     // 16-byte chunk permutation of row `key`, so that the fragment loads of a warp meet all banks
@@ -180,19 +191,19 @@ struct TreeCfg {
 };
 template <int TYPE, int D, int MT>
 constexpr int tree_q_bytes() {
-    return TreeCfg<TYPE, D>::KQ * MT * 32 * 16 * 2;
+    return TreeCfg<TYPE, D, MT>::KQ * MT * 32 * 16 * 2;
 }
 template <int TYPE, int D, int MT>
 constexpr int tree_smem() {
-    using C = TreeCfg<TYPE, D>;
+    using C = TreeCfg<TYPE, D, MT>;
     constexpr int ring = C::NW * C::NST * C::STAGE, join = C::NW * 16 * MT * (C::DP + 2) * 4;
     return tree_q_bytes<TYPE, D, MT>() + (ring > join ? ring : join);
 }
 
 // One stage of a warp: slots [key0, key0 + KS), of which those below `end` are read.
-template <int TYPE, int D>
+template <int TYPE, int D, int MT>
 __device__ __forceinline__ void tree_issue(const KvRows& c, int64_t row0, int key0, int end, uint32_t dst, int lane) {
-    using C = TreeCfg<TYPE, D>;
+    using C = TreeCfg<TYPE, D, MT>;
     constexpr int CPR = C::RB / 16;
     const uint8_t* k = (const uint8_t*)c.k + row0 * C::RB;
     const uint8_t* v = (const uint8_t*)c.v + row0 * C::RB;
@@ -205,17 +216,18 @@ __device__ __forceinline__ void tree_issue(const KvRows& c, int64_t row0, int ke
         cp16(dst + C::OV + key * C::RB + ((ch ^ C::swv(key)) << 4), v + off, in);
     }
     if (C::QUANT) {
-        static_assert(!C::QUANT || C::KS == 32, "a lane per slot");
-        const bool in = key0 + lane < end;
-        const int64_t off = row0 + (in ? key0 + lane : 0);
-        cp_small<C::QUANT ? C::SB : 4>(dst + C::OKS + lane * C::SB, (const uint8_t*)c.ks + off * C::SB, in);
-        cp_small<C::QUANT ? C::SB : 4>(dst + C::OVS + lane * C::SB, (const uint8_t*)c.vs + off * C::SB, in);
+        if (C::KS == 32 || lane < C::KS) {
+            const bool in = key0 + lane < end;
+            const int64_t off = row0 + (in ? key0 + lane : 0);
+            cp_small<C::QUANT ? C::SB : 4>(dst + C::OKS + lane * C::SB, (const uint8_t*)c.ks + off * C::SB, in);
+            cp_small<C::QUANT ? C::SB : 4>(dst + C::OVS + lane * C::SB, (const uint8_t*)c.vs + off * C::SB, in);
+        }
     }
 }
 
-// fp32 scales of slots key and key + 1 (key even) of a stage, [slot][block]
+// Scales of slots key (low half) and key + 1 (key even) by block; a: address of slot key's scales, [slot][block]
 template <int NB>
-__device__ __forceinline__ void load_scales(uint32_t a, float (&d)[2][NB]) {
+__device__ __forceinline__ void load_scales(uint32_t a, uint32_t (&d)[NB]) {
     uint32_t w[NB];
     if (NB == 4) {
         const uint4 r = lds128(a);
@@ -225,19 +237,15 @@ __device__ __forceinline__ void load_scales(uint32_t a, float (&d)[2][NB]) {
         w[0] = r.x, w[NB - 1] = r.y;
     }
 #pragma unroll
-    for (int s = 0; s < 2; s++)
-#pragma unroll
-        for (int b = 0; b < NB; b += 2) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[(s * NB + b) / 2]));
-            d[s][b] = f.x;
-            d[s][b + 1] = f.y;
-        }
+    for (int b = 0; b < NB; b++) d[b] = __byte_perm(w[b / 2], w[NB / 2 + b / 2], b & 1 ? 0x7632 : 0x5410);
 }
+__device__ __forceinline__ __half2 as_h2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
+__device__ __forceinline__ uint32_t as_u(__half2 x) { return *reinterpret_cast<const uint32_t*>(&x); }
 
 // The value of (key, dim) of a stage's V, for the element-by-element path.
-template <int TYPE, int D>
+template <int TYPE, int D, int MT>
 __device__ __forceinline__ float stage_value(uint32_t st, int key, int d) {
-    using C = TreeCfg<TYPE, D>;
+    using C = TreeCfg<TYPE, D, MT>;
     const uint32_t row = st + C::OV + key * C::RB;
     auto at = [&](int byte) { return row + ((((byte >> 4) ^ C::swv(key)) << 4) | (byte & 15)); };
     if (TYPE == AF_F32) return __uint_as_float(lds32(at(4 * d)));
@@ -252,9 +260,9 @@ __device__ __forceinline__ float stage_value(uint32_t st, int key, int d) {
 }
 
 template <int TYPE, int D, int MT>
-__global__ void __launch_bounds__(TreeCfg<TYPE, D>::NW * 32, 1) attn_tree_kernel(TreeArgs a, int splits) {
-    using C = TreeCfg<TYPE, D>;
-    constexpr int NW = C::NW, NT = D / 8, KS = C::KS, NB = C::NB, ROWS = 16 * MT;
+__global__ void __launch_bounds__(TreeCfg<TYPE, D, MT>::NW * 32, 1) attn_tree_kernel(TreeArgs a, int splits) {
+    using C = TreeCfg<TYPE, D, MT>;
+    constexpr int NW = C::NW, NT = D / 8, KS = C::KS, GT = KS / 8, NB = C::NB, ROWS = 16 * MT;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float sm_rowf[ROWS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 3, j = lane >> 2;
@@ -271,7 +279,7 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D>::NW * 32, 1) attn_tree_kernel
 #pragma unroll
     for (int i = 0; i < C::NST - 1; i++) {
         const int st = st0 + warp + i * NW;
-        if (st < st1) tree_issue<TYPE, D>(a.c, row0, st * KS, keys, ring + i * C::STAGE, lane);
+        if (st < st1) tree_issue<TYPE, D, MT>(a.c, row0, st * KS, keys, ring + i * C::STAGE, lane);
         cp_commit();
     }
 
@@ -349,14 +357,14 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D>::NW * 32, 1) attn_tree_kernel
             rowf[mt][h] = TYPE == AF_F32 ? 1.f : sm_rowf[r];
             mrow[mt][h] = r0 + r < R ? a.mask + (int64_t)((r0 + r) / G) * words : nullptr;
         }
-    // bit i: the row sees slot key0 + i of the cache (i < 16)
+    // bit i: the row sees slot key0 + i of the cache
     auto window = [&](int mt, int h, int key0) {
         const int t = key0 - a.past, w = t >> 5;  // t < 0: slots of the past, which every row sees
         const unsigned* m = mrow[mt][h];
         const unsigned lo = w < 0 ? ~0u : (m && w < words ? __ldcg(m + w) : 0u);
         const unsigned hi = w + 1 < 0 ? ~0u : (m && w + 1 < words ? __ldcg(m + w + 1) : 0u);
         const unsigned x = __funnelshift_r(lo, hi, t & 31);
-        return t + 16 <= a.n ? x : x & ((1u << max(a.n - t, 0)) - 1u);  // nothing behind the last node
+        return t + 32 <= a.n ? x : (t >= a.n ? 0u : x & ((1u << (a.n - t)) - 1u));  // nothing behind the last node
     };
 
     float o[MT][NT][4] = {}, m_ref[MT][2], l[MT][2] = {};
@@ -371,284 +379,209 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D>::NW * 32, 1) attn_tree_kernel
         asm volatile("" ::: "memory");
         {  // the previous stage's slot takes the stage NST - 1 ahead
             const int nx = st + (C::NST - 1) * NW, ns = slot == 0 ? C::NST - 1 : slot - 1;
-            if (nx < st1) tree_issue<TYPE, D>(a.c, row0, nx * KS, keys, ring + ns * C::STAGE, lane);
+            if (nx < st1) tree_issue<TYPE, D, MT>(a.c, row0, nx * KS, keys, ring + ns * C::STAGE, lane);
             cp_commit();
         }
         const uint32_t base = ring + slot * C::STAGE;
-#pragma unroll 1
-        for (int grp = 0; grp < KS / 16; grp++) {
-            const int key0 = st * KS + grp * 16;
-            if (key0 >= keys) break;
-            const uint32_t kb = base + grp * 16 * C::RB, vb = kb + C::OV;
-            const bool nodes = key0 + 16 > a.past;  // slots of nodes, or behind the last one
-            unsigned see[MT][2] = {};
-            if (nodes)
-#pragma unroll
-                for (int mt = 0; mt < MT; mt++)
-#pragma unroll
-                    for (int h = 0; h < 2; h++) see[mt][h] = window(mt, h, key0);
-            // ---- scores of 16 slots
-            float s[MT][2][4] = {};
-            if constexpr (C::QUANT) {
-                float dk[2][2][NB];
-#pragma unroll
-                for (int t = 0; t < 2; t++) load_scales<NB>(base + C::OKS + (grp * 16 + t * 8 + 2 * c) * C::SB, dk[t]);
-#pragma unroll
-                for (int b = 0; b < NB; b++) {
-                    uint32_t kw[2][4];
-#pragma unroll
-                    for (int t = 0; t < 2; t++) {
-                        const int key = t * 8 + j;
-                        if (TYPE == AF_KV_Q8_0) {
-                            const int byte = 32 * b + 8 * c;
-                            uint2 w = lds64(kb + key * C::RB + ((((byte >> 4) ^ C::swk(key)) << 4) | (byte & 15)));
-                            w.x ^= 0x80808080u, w.y ^= 0x80808080u;
-                            kw[t][0] = hsub2u(__byte_perm(w.x, 0x64646464u, 0x4140), 0x64806480u);
-                            kw[t][1] = hsub2u(__byte_perm(w.x, 0x64646464u, 0x4342), 0x64806480u);
-                            kw[t][2] = hsub2u(__byte_perm(w.y, 0x64646464u, 0x4140), 0x64806480u);
-                            kw[t][3] = hsub2u(__byte_perm(w.y, 0x64646464u, 0x4342), 0x64806480u);
-                        } else {
-                            const uint32_t w = lds32(kb + key * C::RB + ((b ^ C::swk(key)) << 4) + 4 * c);
-#pragma unroll
-                            for (int i = 0; i < 4; i++) kw[t][i] = hsub2u(((w >> (4 * i)) & 0x000F000Fu) | 0x64006400u, 0x64086408u);
-                        }
-                    }
-#pragma unroll
-                    for (int mt = 0; mt < MT; mt++) {
-                        float p[2][4] = {};
-#pragma unroll
-                        for (int e = 0; e < 2; e++) {
-                            const uint4 qh = lds128(sq + ((2 * b + e) * MT + mt) * 1024 + lane * 16);
-                            const uint4 ql = lds128(sq + ((2 * b + e) * MT + mt) * 1024 + 512 + lane * 16);
-#pragma unroll
-                            for (int t = 0; t < 2; t++) {
-                                mma16(p[t], qh, kw[t][2 * e], kw[t][2 * e + 1]);
-                                mma16(p[t], ql, kw[t][2 * e], kw[t][2 * e + 1]);
-                            }
-                        }
-#pragma unroll
-                        for (int t = 0; t < 2; t++)
-#pragma unroll
-                            for (int i = 0; i < 4; i++) s[mt][t][i] += dk[t][i & 1][b] * p[t][i];
-                    }
-                }
-            } else if constexpr (TYPE == AF_F16) {
-#pragma unroll
-                for (int b = 0; b < NB; b++) {
-                    uint4 kw[2];
-#pragma unroll
-                    for (int t = 0; t < 2; t++) {
-                        const int key = t * 8 + j;
-                        kw[t] = lds128(kb + key * C::RB + (((4 * b + c) ^ C::swk(key)) << 4));
-                    }
-#pragma unroll
-                    for (int e = 0; e < 2; e++)
-#pragma unroll
-                        for (int mt = 0; mt < MT; mt++) {
-                            const uint4 qh = lds128(sq + ((2 * b + e) * MT + mt) * 1024 + lane * 16);
-                            const uint4 ql = lds128(sq + ((2 * b + e) * MT + mt) * 1024 + 512 + lane * 16);
-#pragma unroll
-                            for (int t = 0; t < 2; t++) {
-                                mma16(s[mt][t], qh, e ? kw[t].z : kw[t].x, e ? kw[t].w : kw[t].y);
-                                mma16(s[mt][t], ql, e ? kw[t].z : kw[t].x, e ? kw[t].w : kw[t].y);
-                            }
-                        }
-                }
-            } else {
-#pragma unroll
-                for (int b = 0; b < NB; b++) {
-                    uint32_t kh[2][8], kl[2][8];
-#pragma unroll
-                    for (int t = 0; t < 2; t++) {
-                        const int key = t * 8 + j;
-#pragma unroll
-                        for (int u = 0; u < 2; u++) {
-                            const uint4 w = lds128(kb + key * C::RB + (((8 * b + 2 * c + u) ^ C::swk(key)) << 4));
-                            split_tf32(__uint_as_float(w.x), kh[t][4 * u], kl[t][4 * u]);
-                            split_tf32(__uint_as_float(w.y), kh[t][4 * u + 1], kl[t][4 * u + 1]);
-                            split_tf32(__uint_as_float(w.z), kh[t][4 * u + 2], kl[t][4 * u + 2]);
-                            split_tf32(__uint_as_float(w.w), kh[t][4 * u + 3], kl[t][4 * u + 3]);
-                        }
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; e++)
-#pragma unroll
-                        for (int mt = 0; mt < MT; mt++) {
-                            const uint4 qh = lds128(sq + ((4 * b + e) * MT + mt) * 1024 + lane * 16);
-                            const uint4 ql = lds128(sq + ((4 * b + e) * MT + mt) * 1024 + 512 + lane * 16);
-#pragma unroll
-                            for (int t = 0; t < 2; t++) {
-                                mma8(s[mt][t], qh, kh[t][2 * e], kh[t][2 * e + 1]);
-                                mma8(s[mt][t], ql, kh[t][2 * e], kh[t][2 * e + 1]);
-                                mma8(s[mt][t], qh, kl[t][2 * e], kl[t][2 * e + 1]);
-                            }
-                        }
-                }
-            }
-            // ---- mask and softmax
+        const int key0 = st * KS;
+        const uint32_t vb0 = base + C::OV;
+        const bool nodes = key0 + KS > a.past;  // slots of nodes, or behind the last one
+        unsigned see[MT][2] = {};
+        if (nodes)
 #pragma unroll
             for (int mt = 0; mt < MT; mt++)
 #pragma unroll
-                for (int t = 0; t < 2; t++)
+                for (int h = 0; h < 2; h++) see[mt][h] = window(mt, h, key0);
+        // ---- scores of the stage's slots: tile t, columns 2c and 2c + 1, are slots 8 t + 2 c, + 1
+        float s[MT][GT][4] = {};
+        if constexpr (C::QUANT) {
+            uint32_t dk[GT][NB];
 #pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        if (TYPE != AF_F32) s[mt][t][i] *= rowf[mt][i >> 1];
-                        if (nodes && !(see[mt][i >> 1] >> (t * 8 + 2 * c + (i & 1)) & 1)) s[mt][t][i] = -CUDART_INF_F;
-                    }
-            float mx[MT][2];
-            bool move = false;
+            for (int t = 0; t < GT; t++) load_scales<NB>(base + C::OKS + (t * 8 + 2 * c) * C::SB, dk[t]);
 #pragma unroll
-            for (int mt = 0; mt < MT; mt++)
+            for (int b = 0; b < NB; b++) {
+                uint32_t kw[GT][4];
 #pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    float x = fmaxf(fmaxf(s[mt][0][2 * h], s[mt][0][2 * h + 1]), fmaxf(s[mt][1][2 * h], s[mt][1][2 * h + 1]));
-                    mx[mt][h] = x;
-                    move |= x > m_ref[mt][h] + kLazyT;
-                }
-            if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-                for (int mt = 0; mt < MT; mt++)
-#pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        float x = mx[mt][h];
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                        if (x > m_ref[mt][h]) {
-                            const float f = ex2t(m_ref[mt][h] - x);
-                            m_ref[mt][h] = x;
-                            l[mt][h] *= f;
-#pragma unroll
-                            for (int t = 0; t < NT; t++) {
-                                o[mt][t][2 * h] *= f;
-                                o[mt][t][2 * h + 1] *= f;
-                            }
-                        }
-                    }
-            }
-#pragma unroll
-            for (int mt = 0; mt < MT; mt++)
-#pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    const float mb = m_ref[mt][h] == -CUDART_INF_F ? 0.f : m_ref[mt][h] - kBiasT;
-#pragma unroll
-                    for (int t = 0; t < 2; t++)
-#pragma unroll
-                        for (int i = 0; i < 2; i++) {
-                            const float p = ex2t(s[mt][t][2 * h + i] - mb);
-                            s[mt][t][2 * h + i] = p;
-                            l[mt][h] += p;
-                        }
-                }
-            // ---- output
-            bool bad = false;  // non-finite values among the nodes' slots, taken out of the product
-            if constexpr (C::QUANT) {
-                float dv[2][2][NB];
-                float big = 0.f;
-#pragma unroll
-                for (int t = 0; t < 2; t++) {
-                    load_scales<NB>(base + C::OVS + (grp * 16 + t * 8 + 2 * c) * C::SB, dv[t]);
-#pragma unroll
-                    for (int i = 0; i < 2; i++)
-#pragma unroll
-                        for (int b = 0; b < NB; b++) {
-                            if (nodes && !(fabsf(dv[t][i][b]) <= 65504.f)) {
-                                dv[t][i][b] = 0.f;
-                                bad = true;
-                            }
-                            big = fmaxf(big, fabsf(dv[t][i][b]));
-                        }
-                }
-                if (__any_sync(0xffffffffu, big > vlim)) {
-                    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-                    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-                    if (big <= 65504.f) {  // (an infinite scale of the past makes its rows infinite or NaN as it is)
-                        const unsigned e = __float_as_uint(big) >> 23;
-                        const float up = __uint_as_float((254u - e) << 23);  // 2^-exponent(big)
-                        const float f = up / vinv;
-                        vinv = up;
-                        vlim = 4.f * __uint_as_float(e << 23);
-#pragma unroll
-                        for (int mt = 0; mt < MT; mt++)
-#pragma unroll
-                            for (int t = 0; t < NT; t++)
-#pragma unroll
-                                for (int i = 0; i < 4; i++) o[mt][t][i] *= f;
-                    }
-                }
-#pragma unroll
-                for (int b = 0; b < NB; b++) {
-                    uint32_t vw[4][2];
+                for (int t = 0; t < GT; t++) {
+                    const int key = t * 8 + j;
                     if (TYPE == AF_KV_Q8_0) {
-#pragma unroll
-                        for (int h = 0; h < 2; h++) {
-                            uint32_t w[2];
-#pragma unroll
-                            for (int i = 0; i < 2; i++) {
-                                const int key = h * 8 + 2 * c + i, byte = 32 * b + 4 * j;
-                                w[i] = lds32(vb + key * C::RB + ((((byte >> 4) ^ C::swv(key)) << 4) | (byte & 15))) ^ 0x80808080u;
-                            }
-                            const uint32_t x = __byte_perm(w[0], w[1], 0x5140), y = __byte_perm(w[0], w[1], 0x7362);
-                            vw[0][h] = hsub2u(__byte_perm(x, 0x64646464u, 0x4140), 0x64806480u);
-                            vw[1][h] = hsub2u(__byte_perm(x, 0x64646464u, 0x4342), 0x64806480u);
-                            vw[2][h] = hsub2u(__byte_perm(y, 0x64646464u, 0x4140), 0x64806480u);
-                            vw[3][h] = hsub2u(__byte_perm(y, 0x64646464u, 0x4342), 0x64806480u);
-                        }
+                        const int byte = 32 * b + 8 * c;
+                        uint2 w = lds64(base + key * C::RB + ((((byte >> 4) ^ C::swk(j)) << 4) | (byte & 15)));
+                        w.x ^= 0x80808080u, w.y ^= 0x80808080u;
+                        kw[t][0] = hsub2u(__byte_perm(w.x, 0x64646464u, 0x4140), 0x64806480u);
+                        kw[t][1] = hsub2u(__byte_perm(w.x, 0x64646464u, 0x4342), 0x64806480u);
+                        kw[t][2] = hsub2u(__byte_perm(w.y, 0x64646464u, 0x4140), 0x64806480u);
+                        kw[t][3] = hsub2u(__byte_perm(w.y, 0x64646464u, 0x4342), 0x64806480u);
                     } else {
+                        const uint32_t w = lds32(base + key * C::RB + ((b ^ C::swk(j)) << 4) + 4 * c);
 #pragma unroll
-                        for (int h = 0; h < 2; h++) {
-                            const int k0 = h * 8 + 2 * c, k1 = k0 + 1;
-                            const uint32_t w = lds16(vb + k0 * C::RB + ((b ^ C::swv(k0)) << 4) + 2 * j) |
-                                               lds16(vb + k1 * C::RB + ((b ^ C::swv(k1)) << 4) + 2 * j) << 16;
-#pragma unroll
-                            for (int i = 0; i < 4; i++) vw[i][h] = hsub2u(((w >> (4 * i)) & 0x000F000Fu) | 0x64006400u, 0x64086408u);
-                        }
-                    }
-#pragma unroll
-                    for (int mt = 0; mt < MT; mt++) {
-                        uint4 ph, pl;
-                        float x[2][2];
-#pragma unroll
-                        for (int t = 0; t < 2; t++)
-#pragma unroll
-                            for (int i = 0; i < 2; i++) x[t][i] = dv[t][i][b] * vinv;
-                        split_h2(s[mt][0][0] * x[0][0], s[mt][0][1] * x[0][1], ph.x, pl.x);
-                        split_h2(s[mt][0][2] * x[0][0], s[mt][0][3] * x[0][1], ph.y, pl.y);
-                        split_h2(s[mt][1][0] * x[1][0], s[mt][1][1] * x[1][1], ph.z, pl.z);
-                        split_h2(s[mt][1][2] * x[1][0], s[mt][1][3] * x[1][1], ph.w, pl.w);
-#pragma unroll
-                        for (int t = 0; t < 4; t++) {
-                            mma16(o[mt][4 * b + t], ph, vw[t][0], vw[t][1]);
-                            mma16(o[mt][4 * b + t], pl, vw[t][0], vw[t][1]);
-                        }
+                        for (int i = 0; i < 4; i++) kw[t][i] = hsub2u(((w >> (4 * i)) & 0x000F000Fu) | 0x64006400u, 0x64086408u);
                     }
                 }
-            } else if constexpr (TYPE == AF_F16) {
-                uint4 ph[MT], pl[MT];
 #pragma unroll
                 for (int mt = 0; mt < MT; mt++) {
-                    split_h2(s[mt][0][0], s[mt][0][1], ph[mt].x, pl[mt].x);
-                    split_h2(s[mt][0][2], s[mt][0][3], ph[mt].y, pl[mt].y);
-                    split_h2(s[mt][1][0], s[mt][1][1], ph[mt].z, pl[mt].z);
-                    split_h2(s[mt][1][2], s[mt][1][3], ph[mt].w, pl[mt].w);
-                }
-                // lane: row lane & 15 of the 16 slots, chunk (lane >> 4) of the pair
-                const int key = lane & 15;
+                    float p[GT][4] = {};
 #pragma unroll
-                for (int t = 0; t < NT; t += 2) {
-                    uint4 v = ldsm4t(vb + key * C::RB + (((t + (lane >> 4)) ^ C::swv(key)) << 4));
-                    if (nodes) {
-                        v.x = finite_h2(v.x, bad), v.y = finite_h2(v.y, bad);
-                        v.z = finite_h2(v.z, bad), v.w = finite_h2(v.w, bad);
+                    for (int e = 0; e < 2; e++) {
+                        const uint4 qh = lds128(sq + ((2 * b + e) * MT + mt) * 1024 + lane * 16);
+                        const uint4 ql = lds128(sq + ((2 * b + e) * MT + mt) * 1024 + 512 + lane * 16);
+#pragma unroll
+                        for (int t = 0; t < GT; t++) {
+                            mma16(p[t], qh, kw[t][2 * e], kw[t][2 * e + 1]);
+                            mma16(p[t], ql, kw[t][2 * e], kw[t][2 * e + 1]);
+                        }
                     }
+#pragma unroll
+                    for (int t = 0; t < GT; t++) {
+                        const float2 dd = __half22float2(as_h2(dk[t][b]));
+#pragma unroll
+                        for (int h = 0; h < 2; h++) {
+                            const float2 x = fma2(dd, make_float2(p[t][2 * h], p[t][2 * h + 1]),
+                                                  make_float2(s[mt][t][2 * h], s[mt][t][2 * h + 1]));
+                            s[mt][t][2 * h] = x.x, s[mt][t][2 * h + 1] = x.y;
+                        }
+                    }
+                }
+            }
+        } else if constexpr (TYPE == AF_F16) {
+#pragma unroll
+            for (int b = 0; b < NB; b++) {
+                uint4 kw[GT];
+#pragma unroll
+                for (int t = 0; t < GT; t++) kw[t] = lds128(base + (t * 8 + j) * C::RB + (((4 * b + c) ^ C::swk(j)) << 4));
+#pragma unroll
+                for (int e = 0; e < 2; e++)
 #pragma unroll
                     for (int mt = 0; mt < MT; mt++) {
-                        mma16(o[mt][t], ph[mt], v.x, v.y);
-                        mma16(o[mt][t], pl[mt], v.x, v.y);
-                        mma16(o[mt][t + 1], ph[mt], v.z, v.w);
-                        mma16(o[mt][t + 1], pl[mt], v.z, v.w);
+                        const uint4 qh = lds128(sq + ((2 * b + e) * MT + mt) * 1024 + lane * 16);
+                        const uint4 ql = lds128(sq + ((2 * b + e) * MT + mt) * 1024 + 512 + lane * 16);
+#pragma unroll
+                        for (int t = 0; t < GT; t++) {
+                            mma16(s[mt][t], qh, e ? kw[t].z : kw[t].x, e ? kw[t].w : kw[t].y);
+                            mma16(s[mt][t], ql, e ? kw[t].z : kw[t].x, e ? kw[t].w : kw[t].y);
+                        }
+                    }
+            }
+        } else {
+#pragma unroll
+            for (int b = 0; b < NB; b++) {
+                uint32_t kh[GT][8], kl[GT][8];
+#pragma unroll
+                for (int t = 0; t < GT; t++)
+#pragma unroll
+                    for (int u = 0; u < 2; u++) {
+                        const uint4 w = lds128(base + (t * 8 + j) * C::RB + (((8 * b + 2 * c + u) ^ C::swk(j)) << 4));
+                        split_tf32(__uint_as_float(w.x), kh[t][4 * u], kl[t][4 * u]);
+                        split_tf32(__uint_as_float(w.y), kh[t][4 * u + 1], kl[t][4 * u + 1]);
+                        split_tf32(__uint_as_float(w.z), kh[t][4 * u + 2], kl[t][4 * u + 2]);
+                        split_tf32(__uint_as_float(w.w), kh[t][4 * u + 3], kl[t][4 * u + 3]);
+                    }
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+#pragma unroll
+                    for (int mt = 0; mt < MT; mt++) {
+                        const uint4 qh = lds128(sq + ((4 * b + e) * MT + mt) * 1024 + lane * 16);
+                        const uint4 ql = lds128(sq + ((4 * b + e) * MT + mt) * 1024 + 512 + lane * 16);
+#pragma unroll
+                        for (int t = 0; t < GT; t++) {
+                            mma8(s[mt][t], qh, kh[t][2 * e], kh[t][2 * e + 1]);
+                            mma8(s[mt][t], ql, kh[t][2 * e], kh[t][2 * e + 1]);
+                            mma8(s[mt][t], qh, kl[t][2 * e], kl[t][2 * e + 1]);
+                        }
+                    }
+            }
+        }
+        // ---- mask and softmax
+        float mx[MT][2];
+        bool move = false;
+#pragma unroll
+        for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                float x = -CUDART_INF_F;
+#pragma unroll
+                for (int t = 0; t < GT; t++)
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {
+                        float& v = s[mt][t][2 * h + i];
+                        if (TYPE != AF_F32) v *= rowf[mt][h];
+                        if (nodes && !(see[mt][h] >> (t * 8 + 2 * c + i) & 1)) v = -CUDART_INF_F;
+                        x = fmaxf(x, v);
+                    }
+                mx[mt][h] = x;
+                move |= x > m_ref[mt][h] + kLazyT;
+            }
+        if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+            for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    float x = mx[mt][h];
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                    if (x > m_ref[mt][h]) {
+                        const float f = ex2t(m_ref[mt][h] - x);
+                        m_ref[mt][h] = x;
+                        l[mt][h] *= f;
+#pragma unroll
+                        for (int t = 0; t < NT; t++) {
+                            o[mt][t][2 * h] *= f;
+                            o[mt][t][2 * h + 1] *= f;
+                        }
                     }
                 }
-            } else {
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const float mb = m_ref[mt][h] == -CUDART_INF_F ? 0.f : m_ref[mt][h] - kBiasT;
+#pragma unroll
+                for (int t = 0; t < GT; t++)
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {
+                        const float p = ex2t(s[mt][t][2 * h + i] - mb);
+                        s[mt][t][2 * h + i] = p;
+                        l[mt][h] += p;
+                    }
+            }
+        // ---- output, sixteen slots at a time
+        bool bad = false;  // non-finite values among the nodes' slots, taken out of the product
+        uint32_t dv[C::QUANT ? GT : 1][NB];
+        if constexpr (C::QUANT) {
+            __half2 big2 = as_h2(0u);
+#pragma unroll
+            for (int t = 0; t < GT; t++) {
+                load_scales<NB>(base + C::OVS + (t * 8 + 2 * c) * C::SB, dv[t]);
+#pragma unroll
+                for (int b = 0; b < NB; b++) {
+                    if (nodes) dv[t][b] = finite_h2(dv[t][b], bad);
+                    big2 = __hmax2(big2, __habs2(as_h2(dv[t][b])));
+                }
+            }
+            float big = fmaxf(__low2float(big2), __high2float(big2));
+            if (__any_sync(0xffffffffu, big > vlim)) {
+                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+                if (big <= 65504.f) {  // (an infinite scale of the past makes its rows infinite or NaN as it is)
+                    const unsigned e = max(__float_as_uint(big) >> 23, 127u - 15u);  // 2^-exponent(big) is an fp16 number
+                    const float up = __uint_as_float((254u - e) << 23);
+                    const float f = up / vinv;
+                    vinv = up;
+                    vlim = 4.f * __uint_as_float(e << 23);
+#pragma unroll
+                    for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+                        for (int t = 0; t < NT; t++)
+#pragma unroll
+                            for (int i = 0; i < 4; i++) o[mt][t][i] *= f;
+                }
+            }
+        }
+#pragma unroll
+        for (int g16 = 0; g16 < GT / 2; g16++) {
+            const uint32_t vb = vb0 + g16 * 16 * C::RB;
+            if constexpr (TYPE == AF_F32) {
 #pragma unroll
                 for (int t = 0; t < 2; t++) {
                     uint4 ph[MT], pl[MT];
@@ -684,31 +617,106 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D>::NW * 32, 1) attn_tree_kernel
                         }
                     }
                 }
+            } else {
+                uint4 ph[MT], pl[MT];
+#pragma unroll
+                for (int mt = 0; mt < MT; mt++) {
+                    const float(&p0)[4] = s[mt][2 * g16], (&p1)[4] = s[mt][2 * g16 + 1];
+                    split_h2(p0[0], p0[1], ph[mt].x, pl[mt].x);
+                    split_h2(p0[2], p0[3], ph[mt].y, pl[mt].y);
+                    split_h2(p1[0], p1[1], ph[mt].z, pl[mt].z);
+                    split_h2(p1[2], p1[3], ph[mt].w, pl[mt].w);
+                }
+                if constexpr (TYPE == AF_F16) {
+                    // lane: row lane & 15 of the 16 slots, chunk (lane >> 4) of the pair
+                    const int key = lane & 15;
+#pragma unroll
+                    for (int t = 0; t < NT; t += 2) {
+                        uint4 v = ldsm4t(vb + key * C::RB + (((t + (lane >> 4)) ^ C::swv(key)) << 4));
+                        if (nodes) {
+                            v.x = finite_h2(v.x, bad), v.y = finite_h2(v.y, bad);
+                            v.z = finite_h2(v.z, bad), v.w = finite_h2(v.w, bad);
+                        }
+#pragma unroll
+                        for (int mt = 0; mt < MT; mt++) {
+                            mma16(o[mt][t], ph[mt], v.x, v.y);
+                            mma16(o[mt][t], pl[mt], v.x, v.y);
+                            mma16(o[mt][t + 1], ph[mt], v.z, v.w);
+                            mma16(o[mt][t + 1], pl[mt], v.z, v.w);
+                        }
+                    }
+                } else {
+                    const __half2 v2 = __float2half2_rn(vinv);
+#pragma unroll
+                    for (int b = 0; b < NB; b++) {
+                        uint32_t vw[4][2];
+#pragma unroll
+                        for (int h = 0; h < 2; h++) {
+                            const int k0 = h * 8 + 2 * c, k1 = k0 + 1;
+                            if (TYPE == AF_KV_Q8_0) {
+                                const int byte = 32 * b + 4 * j;
+                                const uint32_t w0 = lds32(vb + k0 * C::RB + ((((byte >> 4) ^ C::swv(k0)) << 4) | (byte & 15))) ^ 0x80808080u;
+                                const uint32_t w1 = lds32(vb + k1 * C::RB + ((((byte >> 4) ^ C::swv(k1)) << 4) | (byte & 15))) ^ 0x80808080u;
+                                const uint32_t x = __byte_perm(w0, w1, 0x5140), y = __byte_perm(w0, w1, 0x7362);
+                                vw[0][h] = hsub2u(__byte_perm(x, 0x64646464u, 0x4140), 0x64806480u);
+                                vw[1][h] = hsub2u(__byte_perm(x, 0x64646464u, 0x4342), 0x64806480u);
+                                vw[2][h] = hsub2u(__byte_perm(y, 0x64646464u, 0x4140), 0x64806480u);
+                                vw[3][h] = hsub2u(__byte_perm(y, 0x64646464u, 0x4342), 0x64806480u);
+                            } else {
+                                const uint32_t w = lds16(vb + k0 * C::RB + ((b ^ C::swv(k0)) << 4) + 2 * j) |
+                                                   lds16(vb + k1 * C::RB + ((b ^ C::swv(k1)) << 4) + 2 * j) << 16;
+#pragma unroll
+                                for (int i = 0; i < 4; i++)
+                                    vw[i][h] = hsub2u(((w >> (4 * i)) & 0x000F000Fu) | 0x64006400u, 0x64086408u);
+                            }
+                        }
+                        // p d in two parts: the fp16 product of p's high part, and what it lost plus p's low part's
+                        const __half2 d0 = __hmul2(as_h2(dv[2 * g16][b]), v2), d1 = __hmul2(as_h2(dv[2 * g16 + 1][b]), v2);
+#pragma unroll
+                        for (int mt = 0; mt < MT; mt++) {
+                            uint4 hi, lo;
+                            auto times = [](uint32_t h, uint32_t l, __half2 d, uint32_t& hi, uint32_t& lo) {
+                                const __half2 x = __hmul2_rn(as_h2(h), d);
+                                hi = as_u(x);
+                                lo = as_u(__hfma2(as_h2(l), d, __hfma2(as_h2(h), d, __hneg2(x))));
+                            };
+                            times(ph[mt].x, pl[mt].x, d0, hi.x, lo.x);
+                            times(ph[mt].y, pl[mt].y, d0, hi.y, lo.y);
+                            times(ph[mt].z, pl[mt].z, d1, hi.z, lo.z);
+                            times(ph[mt].w, pl[mt].w, d1, hi.w, lo.w);
+#pragma unroll
+                            for (int t = 0; t < 4; t++) {
+                                mma16(o[mt][4 * b + t], hi, vw[t][0], vw[t][1]);
+                                mma16(o[mt][4 * b + t], lo, vw[t][0], vw[t][1]);
+                            }
+                        }
+                    }
+                }
             }
-            if (nodes && __any_sync(0xffffffffu, bad)) {
-                // rare: add p v of the non-finite values to the rows that see the slot
+        }
+        if (nodes && __any_sync(0xffffffffu, bad)) {
+            // rare: add p v of the non-finite values to the rows that see the slot
+            const float scale = C::QUANT ? vinv : 1.f;
+#pragma unroll
+            for (int t8 = 0; t8 < GT; t8++)
 #pragma unroll 1
-                for (int key = 0; key < 16; key++) {
-                    const int src = (lane & ~3) | ((key & 7) >> 1);
-                    const float scale = C::QUANT ? vinv : 1.f;
+                for (int k = 0; k < 8; k++) {
+                    const int src = (lane & ~3) | (k >> 1), key = t8 * 8 + k;
 #pragma unroll
                     for (int mt = 0; mt < MT; mt++)
 #pragma unroll
                         for (int h = 0; h < 2; h++) {
-                            const float p0 = key < 8 ? s[mt][0][2 * h] : s[mt][1][2 * h];
-                            const float p1 = key < 8 ? s[mt][0][2 * h + 1] : s[mt][1][2 * h + 1];
-                            const float p = __shfl_sync(0xffffffffu, (key & 1) ? p1 : p0, src);
+                            const float p = __shfl_sync(0xffffffffu, (k & 1) ? s[mt][t8][2 * h + 1] : s[mt][t8][2 * h], src);
                             if (!(see[mt][h] >> key & 1)) continue;
 #pragma unroll
                             for (int t = 0; t < NT; t++)
 #pragma unroll
                                 for (int i = 0; i < 2; i++) {
-                                    const float v = stage_value<TYPE, D>(base, grp * 16 + key, C::odim(t, 2 * c + i));
+                                    const float v = stage_value<TYPE, D, MT>(base, key, C::odim(t, 2 * c + i));
                                     if (!(fabsf(v) < CUDART_INF_F)) o[mt][t][2 * h + i] += p * (v * scale);
                                 }
                         }
                 }
-            }
         }
         slot = slot + 1 == C::NST ? 0 : slot + 1;
     }
@@ -837,8 +845,7 @@ TreePlan tree_plan(int H, int KVH, int D, int type, int past, int n) {
     if (p.splits) return p;
     const int R = n * (H / KVH);
     p.mt = R > 16 ? 2 : 1;
-    const bool quant = type == AF_KV_Q8_0 || type == AF_KV_Q4_0;
-    const int ks = quant ? 32 : 16, nw = type == AF_F32 && D == 128 ? 6 : 8;
+    const int ks = tree_stage(type, p.mt), nw = tree_warps(type, D, p.mt);
     const int64_t tiles = (int64_t)KVH * ((R + 16 * p.mt - 1) / (16 * p.mt));
     const int stages = (past + n + ks - 1) / ks;
     int64_t s = num_sms() / tiles;
@@ -855,7 +862,7 @@ cudaError_t go(const TreeArgs& a, const TreePlan& p, cudaStream_t s) {
     cudaError_t e = opt((const void*)k, smem);
     if (e) return e;
     const int R = a.n * (a.H / a.c.KVH);
-    return launch_chained(k, dim3(p.splits, a.c.KVH, (R + 16 * MT - 1) / (16 * MT)), TreeCfg<TYPE, D>::NW * 32, smem, s, a,
+    return launch_chained(k, dim3(p.splits, a.c.KVH, (R + 16 * MT - 1) / (16 * MT)), TreeCfg<TYPE, D, MT>::NW * 32, smem, s, a,
                           p.splits);
 }
 

@@ -157,33 +157,10 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
     for (int i = 0; i < 64; i++) v[i] = __uint_as_float(r[i]);
 }
 
-// two fp32 operations an instruction
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    unsigned long long r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;"
-        : "=l"(r)
-        : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)),
-          "l"(*reinterpret_cast<unsigned long long*>(&c)));
-    return *reinterpret_cast<float2*>(&r);
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    unsigned long long r;
-    asm("add.rn.f32x2 %0, %1, %2;"
-        : "=l"(r)
-        : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
-    return *reinterpret_cast<float2*>(&r);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    unsigned long long r;
-    asm("mul.rn.f32x2 %0, %1, %2;"
-        : "=l"(r)
-        : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
-    return *reinterpret_cast<float2*>(&r);
-}
 // x = hi + lo in fp16 (lo off by at most 2^-23 of x, or half of fp16's smallest step 2^-24)
 __device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {
     const __half2 a = __floats2half2_rn(x.x, x.y);
-    const float2 r = fma2(__half22float2(a), make_float2(-1.f, -1.f), x);
+    const float2 r = fma2(__half22float2(a), both(-1.f), x);
     const __half2 b = __floats2half2_rn(r.x, r.y);
     hi = *reinterpret_cast<const uint32_t*>(&a);
     lo = *reinterpret_cast<const uint32_t*>(&b);
@@ -302,7 +279,7 @@ __device__ __forceinline__ void store_tile(uint8_t* dst, const RawTile<TYPE, D>&
         const uint32_t off = (uint32_t)((d0 >> 6) * BK * 128) + sw128(key, (d0 >> 3) & 7) + (d0 & 7) * 2;
         if constexpr (TYPE == AF_F32) {
             const uint4 a = r.c[i].a;
-            const float2 dd = make_float2(down, down);
+            const float2 dd = both(down);
             uint2 hi, lo;
             split2(mul2(make_float2(__uint_as_float(a.x), __uint_as_float(a.y)), dd), hi.x, lo.x);
             split2(mul2(make_float2(__uint_as_float(a.z), __uint_as_float(a.w)), dd), hi.y, lo.y);
@@ -770,7 +747,7 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                 constexpr int W = BK / NG;
                 // V's slots are 2^-ev of themselves and the output 2^-ev_ref: p takes the difference
                 const float shift = C::SPLIT && ev[q] != kNoExp ? (float)(ev[q] - ev_ref) : 0.f;
-                const float2 ff = make_float2(f[q], f[q]), mm = make_float2(shift - mb, shift - mb);
+                const float2 ff = both(f[q]), mm = both(shift - mb);
                 float2 sum[2] = {};
 #pragma unroll
                 for (int i = 0; i < W; i += 2) {

@@ -4,11 +4,11 @@
 //   Q8_0: d = fp16(max|v| / 127), q = clamp(round-half-away(v / d), -127, 127)
 //   Q4_0: d = fp16(m / -8) with m the value of largest magnitude (the first on ties),
 //         q = clamp(floor(v / d + 1/2), -8, 7)
-// with the decisions those of exact arithmetic: the borders (k + 1/2) d have at most 19 significant bits, so they
-// are fp32 numbers, and the correctly rounded fp32 quotient v / d of a v beside a border stays on its side (the
-// distance of two fp32 numbers near v is at least 2^-24 of v, more than the half step 2^-25 .. 2^-24 that a
-// quotient of that size is rounded by).  A zero d gives zero codes.  A block that holds a NaN, or whose scale
-// overflows fp16, gets a scale that makes all its values NaN: nothing non-finite is turned into a number.
+// with the decisions those of exact arithmetic: with q a guess (v times 1 / d, rounded), q d has at most 8 + 11 bits and
+// is an fp32 number, so r = v - q d comes out of one fused multiply-add exactly (v and q d are within a factor of two
+// of each other, or q = 0), and comparing r with d / 2 corrects the guess.  A zero d gives zero codes.  A block that
+// holds a NaN, or whose scale overflows fp16, gets a scale that makes all its values NaN: nothing non-finite is turned
+// into a number.
 //
 // Both are bound by HBM.  A CTA takes kRows rows at a time and a thread four values of K and of V of each, all loads
 // before the first use; the grid is a few CTAs per SM.  Data of earlier kernels is read through L2 (the kernels are
@@ -67,25 +67,20 @@ __device__ __forceinline__ void quantize_group(const float (&x)[4], unsigned gro
         m = __shfl_sync(group, m, who ? __ffs(who) - 1 : lane);
         dh = __float2half_rn(m / -8.f);
     }
-    if (nan) dh = __ushort_as_half((unsigned short)0x7FFF);
-    const float d = __half2float(dh);
+    if (nan || (__half_as_ushort(dh) & 0x7C00) == 0x7C00) dh = __ushort_as_half((unsigned short)0x7FFF);
+    const float d = fabsf(__half2float(dh)), rd = d == 0.f ? 0.f : __frcp_rn(d), h = 0.5f * d;
+    constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer, in the low bits
 #pragma unroll
     for (int e = 0; e < 4; e++) {
-        int v = 0;
-        if (d != 0.f) {
-            const float t = x[e] / d;
-            if (TYPE == AF_KV_Q8_0) {
-                const float f = floorf(fabsf(t));
-                v = (int)f + (fabsf(t) - f >= 0.5f ? 1 : 0);
-                v = v > 127 ? 127 : v;
-                v = t < 0.f ? -v : v;
-            } else {
-                const float f = floorf(t);
-                v = (int)f + (t - f >= 0.5f ? 1 : 0);
-                v = v < -8 ? -8 : (v > 7 ? 7 : v);
-            }
-        }
-        q[e] = v;
+        // the rounding is half away from zero on |v| for Q8_0, half up on v / d for Q4_0: half up on y / |d| either way
+        const float y = TYPE == AF_KV_Q8_0 ? fabsf(x[e]) : (__half_as_ushort(dh) & 0x8000 ? -x[e] : x[e]);
+        const float g = y * rd + kMagic;
+        const float r = fmaf(-(g - kMagic), d, y);
+        int v = __float_as_int(g) - 0x4B400000;
+        v += (r >= h ? 1 : 0) - (r < -h ? 1 : 0);
+        v = TYPE == AF_KV_Q8_0 ? min(v, 127) : min(max(v, -8), 7);
+        if (TYPE == AF_KV_Q8_0 && x[e] < 0.f) v = -v;
+        q[e] = d > 0.f ? v : 0;
     }
 }
 

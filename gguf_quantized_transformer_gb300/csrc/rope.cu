@@ -23,25 +23,8 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    unsigned long long r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;"
-        : "=l"(r)
-        : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)),
-          "l"(*reinterpret_cast<unsigned long long*>(&c)));
-    return *reinterpret_cast<float2*>(&r);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    unsigned long long r;
-    asm("mul.rn.f32x2 %0, %1, %2;"
-        : "=l"(r)
-        : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
-    return *reinterpret_cast<float2*>(&r);
-}
-__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
-
 // mag cos and mag sin of pos * turn, for two frequencies
-__device__ __forceinline__ void turn_sincos2(const uint64_t (&turn)[2], int pos, float mag, float (&c)[2], float (&s)[2]) {
+__device__ __forceinline__ void turn_sincos2(const uint64_t (&turn)[2], int pos, float mag, float2& co, float2& so) {
     unsigned quad[2];
     float x[2];
 #pragma unroll
@@ -65,6 +48,7 @@ __device__ __forceinline__ void turn_sincos2(const uint64_t (&turn)[2], int pos,
     sn = mul2(sn, m);
     cs = mul2(cs, m);
     const float sv[2] = {sn.x, sn.y}, cv[2] = {cs.x, cs.y};
+    float c[2], s[2];
 #pragma unroll
     for (int i = 0; i < 2; i++) {  // quarter turns: (c, s) -> (-s, c)
         const float c0 = (quad[i] & 1) ? -sv[i] : cv[i], s0 = (quad[i] & 1) ? cv[i] : sv[i];
@@ -72,6 +56,8 @@ __device__ __forceinline__ void turn_sincos2(const uint64_t (&turn)[2], int pos,
         c[i] = __uint_as_float(__float_as_uint(c0) ^ flip);
         s[i] = __uint_as_float(__float_as_uint(s0) ^ flip);
     }
+    co = make_float2(c[0], c[1]);
+    so = make_float2(s[0], s[1]);
 }
 
 template <typename T, int N>
@@ -91,6 +77,19 @@ __device__ __forceinline__ Vec<T, N> load(const T* p) {
     return v;
 }
 
+// values e and e + 1 of a vector, as fp32 and back
+template <int N>
+__device__ __forceinline__ float2 pair_of(const Vec<float, N>& v, int e) { return make_float2(v.e[e], v.e[e + 1]); }
+template <int N>
+__device__ __forceinline__ float2 pair_of(const Vec<__half, N>& v, int e) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&v.e[e]));
+}
+template <int N>
+__device__ __forceinline__ void set_pair(Vec<float, N>& v, int e, float2 x) { v.e[e] = x.x, v.e[e + 1] = x.y; }
+template <int N>
+__device__ __forceinline__ void set_pair(Vec<__half, N>& v, int e, float2 x) {
+    *reinterpret_cast<__half2*>(&v.e[e]) = __floats2half2_rn(x.x, x.y);
+}
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
 __device__ __forceinline__ void from_f(float v, float& o) { o = v; }
@@ -124,45 +123,44 @@ __global__ void __launch_bounds__(kThreads)
             for (int h = hg; h < heads; h += hgroups) *reinterpret_cast<Vec<T, V>*>(yr + h * D + d) = load<T, V>(xr + h * D + d);
             continue;
         }
+        // the first head's values are on their way while the sines are computed
+        constexpr int W = HALF ? V : (V > 1 ? V : 2), A = HALF ? V : (V > 1 ? V : 1), NA = HALF ? 2 : W / A;  // accesses
+        auto at = [&](int h, int e) { return (int64_t)h * D + u * W + e * (HALF ? R / 2 : A); };
+        Vec<T, A> v[NA];
+#pragma unroll
+        for (int e = 0; e < NA; e++) v[e] = load<T, A>(xr + at(hg, e));
         const int p = pos ? __ldcg(pos + row) : pos0 + (int)row;
-        float c[P2], s[P2];
+        float2 c[P2 / 2], s[P2 / 2];
 #pragma unroll
         for (int e = 0; e < P2; e += 2) {
             const uint64_t t2[2] = {tn[e], tn[e + 1]};
-            float c2[2], s2[2];
-            turn_sincos2(t2, p, mag, c2, s2);
-            c[e] = c2[0], c[e + 1] = c2[1], s[e] = s2[0], s[e + 1] = s2[1];
+            turn_sincos2(t2, p, mag, c[e / 2], s[e / 2]);
         }
         for (int h = hg; h < heads; h += hgroups) {
-            if (HALF) {
-                const int64_t ia = (int64_t)h * D + u * V, ib = ia + R / 2;
-                const Vec<T, V> a = load<T, V>(xr + ia), b = load<T, V>(xr + ib);
-                Vec<T, V> oa, ob;
+            if (h != hg)
 #pragma unroll
-                for (int e = 0; e < V; e++) {
-                    const float fa = to_f(a.e[e]), fb = to_f(b.e[e]);
-                    from_f(fa * c[e] - fb * s[e], oa.e[e]);
-                    from_f(fa * s[e] + fb * c[e], ob.e[e]);
+                for (int e = 0; e < NA; e++) v[e] = load<T, A>(xr + at(h, e));
+            if constexpr (V == 1) {  // one pair in two accesses
+                const float a = to_f(v[0].e[0]), b = to_f(v[1].e[0]);
+                from_f(a * c[0].x - b * s[0].x, v[0].e[0]);
+                from_f(a * s[0].x + b * c[0].x, v[1].e[0]);
+            } else if constexpr (HALF) {
+#pragma unroll
+                for (int e = 0; e < V; e += 2) {
+                    const float2 a = pair_of(v[0], e), b = pair_of(v[1], e), cc = c[e / 2], ss = s[e / 2];
+                    set_pair(v[0], e, fma2(mul2(b, ss), both(-1.f), mul2(a, cc)));
+                    set_pair(v[1], e, fma2(a, ss, mul2(b, cc)));
                 }
-                *reinterpret_cast<Vec<T, V>*>(yr + ia) = oa;
-                *reinterpret_cast<Vec<T, V>*>(yr + ib) = ob;
             } else {
-                constexpr int W = V > 1 ? V : 2, A = V > 1 ? V : 1;  // elements of the unit, of an access
-                const int64_t i0 = (int64_t)h * D + u * W;
-                Vec<T, A> v[W / A];
 #pragma unroll
-                for (int e = 0; e < W / A; e++) v[e] = load<T, A>(xr + i0 + e * A);
-#pragma unroll
-                for (int e = 0; e < W; e += 2) {
-                    T& a = v[e / A].e[e % A];
-                    T& b = v[(e + 1) / A].e[(e + 1) % A];
-                    const float fa = to_f(a), fb = to_f(b);
-                    from_f(fa * c[e / 2] - fb * s[e / 2], a);
-                    from_f(fa * s[e / 2] + fb * c[e / 2], b);
+                for (int e = 0; e < V; e += 2) {  // pair e / 2
+                    const float2 ab = pair_of(v[0], e);
+                    const float ce = e & 2 ? c[e / 4].y : c[e / 4].x, se = e & 2 ? s[e / 4].y : s[e / 4].x;
+                    set_pair(v[0], e, fma2(make_float2(-ab.y, ab.x), both(se), mul2(ab, both(ce))));
                 }
-#pragma unroll
-                for (int e = 0; e < W / A; e++) *reinterpret_cast<Vec<T, A>*>(yr + i0 + e * A) = v[e];
             }
+#pragma unroll
+            for (int e = 0; e < NA; e++) *reinterpret_cast<Vec<T, A>*>(yr + at(h, e)) = v[e];
         }
     }
 }
