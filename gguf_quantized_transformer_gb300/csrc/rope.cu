@@ -99,69 +99,116 @@ __device__ __forceinline__ void from_f(float v, __half& o) { o = __float2half_rn
 // interleaved, V / 2 pairs (V consecutive elements; V = 1: one pair, two accesses); past R, V copied elements.
 // Rows are n * hgroups: (row, heads hg, hg + hgroups, ..).
 template <typename T, int V, bool HALF>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, HALF && V > 4 ? 2 : 3)
     rope_kernel(const T* x, T* y, int64_t ldx, int64_t ldy, int n, int heads, int D, int R, const int* __restrict__ pos,
                 int pos0, float mag, int hgroups, int units, int rows_per_cta, const __grid_constant__ RopeTurns turns) {
     constexpr int P = HALF ? V : (V > 1 ? V / 2 : 1), P2 = P > 1 ? P : 2;  // pairs per unit
     const int rot_units = R / 2 / P;
-    const int u = threadIdx.x % units, rl = threadIdx.x / units;
-    const bool copy = u >= rot_units;
+    // the rotating threads of all the CTA's rows come first: few warps hold both kinds
+    const int tid = threadIdx.x, nrot = rot_units * rows_per_cta;
+    const bool copy = tid >= nrot;
+    const int rl = copy ? (tid - nrot) / max(units - rot_units, 1) : tid / rot_units;
+    const int u = copy ? rot_units + (tid - nrot) % max(units - rot_units, 1) : tid % rot_units;
     pdl_launch_dependents();
+    // (through shared memory: lanes that read parameters at different offsets take turns)
+    __shared__ uint64_t turn[kRopeMaxPairs];
+    if (tid < R / 2) turn[tid] = turns.turn[tid];
+    __syncthreads();
     uint64_t tn[P2];
 #pragma unroll
-    for (int e = 0; e < P2; e++) tn[e] = !copy && e < P ? turns.turn[u * P + e] : 0;
+    for (int e = 0; e < P2; e++) tn[e] = !copy && e < P ? turn[u * P + e] : 0;
     pdl_wait();
-    const int64_t total = (int64_t)n * hgroups;
-    for (int64_t w = (int64_t)blockIdx.x * rows_per_cta + rl; w < total; w += (int64_t)gridDim.x * rows_per_cta) {
-        if (rl >= rows_per_cta) break;
-        const int hg = hgroups == 1 ? 0 : (int)(w % hgroups);
-        const int64_t row = hgroups == 1 ? w : w / hgroups;
-        const T* xr = x + row * ldx;
-        T* yr = y + row * ldy;
-        if (copy) {
-            const int d = R + (u - rot_units) * V;
-            for (int h = hg; h < heads; h += hgroups) *reinterpret_cast<Vec<T, V>*>(yr + h * D + d) = load<T, V>(xr + h * D + d);
-            continue;
-        }
-        // the first head's values are on their way while the sines are computed
-        constexpr int W = HALF ? V : (V > 1 ? V : 2), A = HALF ? V : (V > 1 ? V : 1), NA = HALF ? 2 : W / A;  // accesses
-        auto at = [&](int h, int e) { return (int64_t)h * D + u * W + e * (HALF ? R / 2 : A); };
+    // The accesses of this thread's unit in a head: NA of A values.
+    constexpr int W = HALF ? V : (V > 1 ? V : 2), A = HALF ? V : (V > 1 ? V : 1), NA = HALF ? 2 : W / A;
+    const int first = copy ? R + (u - rot_units) * V : u * W, step = HALF ? R / 2 : A;
+    struct Unit {
         Vec<T, A> v[NA];
+    };
+    auto get = [&](const T* p) {
+        Unit x;
+        x.v[0] = load<T, A>(p + first);
 #pragma unroll
-        for (int e = 0; e < NA; e++) v[e] = load<T, A>(xr + at(hg, e));
-        const int p = pos ? __ldcg(pos + row) : pos0 + (int)row;
-        float2 c[P2 / 2], s[P2 / 2];
-#pragma unroll
-        for (int e = 0; e < P2; e += 2) {
-            const uint64_t t2[2] = {tn[e], tn[e + 1]};
-            turn_sincos2(t2, p, mag, c[e / 2], s[e / 2]);
-        }
-        for (int h = hg; h < heads; h += hgroups) {
-            if (h != hg)
-#pragma unroll
-                for (int e = 0; e < NA; e++) v[e] = load<T, A>(xr + at(h, e));
+        for (int e = 1; e < NA; e++)
+            if (!copy) x.v[e] = load<T, A>(p + first + e * step);
+        return x;
+    };
+    auto put = [&](T* p, Unit x, const float2 (&c)[P2 / 2], const float2 (&s)[P2 / 2]) {
+        if (!copy) {
             if constexpr (V == 1) {  // one pair in two accesses
-                const float a = to_f(v[0].e[0]), b = to_f(v[1].e[0]);
-                from_f(a * c[0].x - b * s[0].x, v[0].e[0]);
-                from_f(a * s[0].x + b * c[0].x, v[1].e[0]);
+                const float a = to_f(x.v[0].e[0]), b = to_f(x.v[1].e[0]);
+                from_f(a * c[0].x - b * s[0].x, x.v[0].e[0]);
+                from_f(a * s[0].x + b * c[0].x, x.v[1].e[0]);
             } else if constexpr (HALF) {
 #pragma unroll
                 for (int e = 0; e < V; e += 2) {
-                    const float2 a = pair_of(v[0], e), b = pair_of(v[1], e), cc = c[e / 2], ss = s[e / 2];
-                    set_pair(v[0], e, fma2(mul2(b, ss), both(-1.f), mul2(a, cc)));
-                    set_pair(v[1], e, fma2(a, ss, mul2(b, cc)));
+                    const float2 a = pair_of(x.v[0], e), b = pair_of(x.v[1], e), cc = c[e / 2], ss = s[e / 2];
+                    set_pair(x.v[0], e, fma2(mul2(b, ss), both(-1.f), mul2(a, cc)));
+                    set_pair(x.v[1], e, fma2(a, ss, mul2(b, cc)));
                 }
             } else {
 #pragma unroll
                 for (int e = 0; e < V; e += 2) {  // pair e / 2
-                    const float2 ab = pair_of(v[0], e);
+                    const float2 ab = pair_of(x.v[0], e);
                     const float ce = e & 2 ? c[e / 4].y : c[e / 4].x, se = e & 2 ? s[e / 4].y : s[e / 4].x;
-                    set_pair(v[0], e, fma2(make_float2(-ab.y, ab.x), both(se), mul2(ab, both(ce))));
+                    set_pair(x.v[0], e, fma2(make_float2(-ab.y, ab.x), both(se), mul2(ab, both(ce))));
                 }
             }
-#pragma unroll
-            for (int e = 0; e < NA; e++) *reinterpret_cast<Vec<T, A>*>(yr + at(h, e)) = v[e];
         }
+        *reinterpret_cast<Vec<T, A>*>(p + first) = x.v[0];
+#pragma unroll
+        for (int e = 1; e < NA; e++)
+            if (!copy) *reinterpret_cast<Vec<T, A>*>(p + first + e * step) = x.v[e];
+    };
+    if (tid >= units * rows_per_cta) return;
+    const int64_t total = (int64_t)n * hgroups, stride = (int64_t)gridDim.x * rows_per_cta;
+    // item w: row w / hgroups, first head w % hgroups (several head groups: total is a small number)
+    auto row_of = [&](int64_t w) { return hgroups == 1 ? w : (int64_t)((unsigned)w / (unsigned)hgroups); };
+    auto head_of = [&](int64_t w) { return hgroups == 1 ? 0 : (int)((unsigned)w % (unsigned)hgroups); };
+    int64_t w = (int64_t)blockIdx.x * rows_per_cta + rl;
+    if (w >= total) return;
+    int64_t row = row_of(w);
+    int hg = head_of(w);
+    const T* xr = x + row * ldx;
+    Unit cur = get(xr + hg * D);
+    int p = pos ? __ldcg(pos + row) : pos0 + (int)row;
+    float2 c[P2 / 2], s[P2 / 2];
+    int p_of = 0;
+    bool fresh = true;
+    while (true) {
+        // the next item's first head and position are on their way while this one is worked on
+        const int64_t wn = w + stride;
+        int64_t rn = row;
+        int hn = hg, pn = 0;
+        const T* xn = xr;
+        Unit next = cur;
+        if (wn < total) {
+            rn = row_of(wn);
+            hn = head_of(wn);
+            xn = x + rn * ldx;
+            next = get(xn + hn * D);
+            pn = pos ? __ldcg(pos + rn) : pos0 + (int)rn;
+        }
+        T* yr = y + row * ldy;
+        if (fresh || p != p_of) {  // rows that share a position (a cache that moves) share its sines
+#pragma unroll
+            for (int e = 0; e < P2; e += 2) {
+                const uint64_t t2[2] = {tn[e], tn[e + 1]};
+                turn_sincos2(t2, p, mag, c[e / 2], s[e / 2]);
+            }
+            p_of = p;
+            fresh = false;
+        }
+        put(yr + hg * D, cur, c, s);
+        for (int h = hg + hgroups; h < heads; h += 2 * hgroups) {
+            const bool two = h + hgroups < heads;
+            const Unit a = get(xr + h * D);
+            Unit b = a;
+            if (two) b = get(xr + (h + hgroups) * D);
+            put(yr + h * D, a, c, s);
+            if (two) put(yr + (h + hgroups) * D, b, c, s);
+        }
+        if (wn >= total) break;
+        w = wn, row = rn, hg = hn, xr = xn, cur = next, p = pn;
     }
 }
 
