@@ -4,14 +4,15 @@
 //   Q8_0: d = fp16(max|v| / 127), q = clamp(round-half-away(v / d), -127, 127)
 //   Q4_0: d = fp16(m / -8) with m the value of largest magnitude (the first on ties),
 //         q = clamp(floor(v / d + 1/2), -8, 7)
-// with the decisions those of exact arithmetic: with q a guess (v times 1 / d, rounded), q d has at most 8 + 11 bits and
-// is an fp32 number, so r = v - q d comes out of one fused multiply-add exactly (v and q d are within a factor of two
-// of each other, or q = 0), and comparing r with d / 2 corrects the guess.  A zero d gives zero codes.  A block that
-// holds a NaN, or whose scale overflows fp16, gets a scale that makes all its values NaN: nothing non-finite is turned
-// into a number.
+// with the decisions those of exact arithmetic: q is guessed as v times a 1 / d that is a little small, rounded, so it is
+// right or one too near zero.  q d has at most 8 + 11 bits and is an fp32 number, and |q| d <= |v| < 2 |q| d (or q = 0),
+// so r = v - q d comes out of one fused multiply-add exactly, and comparing r with d / 2 corrects the guess.  A zero d
+// gives zero codes.  A block that holds a NaN, or whose scale overflows fp16, gets a NaN as its scale: nothing
+// non-finite is turned into a number.
 //
-// Both are bound by HBM.  A CTA takes kRows rows at a time and a thread four values of K and of V of each, all loads
-// before the first use; the grid is a few CTAs per SM.  Data of earlier kernels is read through L2 (the kernels are
+// Both are bound by HBM.  A CTA takes a few rows at a time, all loads before the first use (writing: a thread holds eight
+// values of a block, two float4 64 bytes apart, so that four lanes share a block's scale); the grid is a few CTAs per
+// SM.  Data of earlier kernels is read through L2 (the kernels are
 // launched with programmatic serialization).
 #include <algorithm>
 
@@ -23,7 +24,7 @@ namespace af {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRows = 4;
+constexpr int kRows = 4, kWriteRows = 4;
 constexpr int kCtasPerSm = 6;
 
 // OR over the CTA, in every thread
@@ -39,42 +40,44 @@ __device__ __forceinline__ unsigned cta_or(unsigned x) {
     return x;
 }
 
-// Eight lanes (an aligned group of the warp) hold the 32 values of a block, four each.
+// Four lanes (an aligned group of the warp) hold the 32 values of a block: lane i of them quads i and 4 + i.
 template <int TYPE>
-__device__ __forceinline__ void quantize_group(const float (&x)[4], unsigned group, int lane, int (&q)[4], __half& dh) {
-    float amax = 0.f;
-    bool nan = false;
+__device__ __forceinline__ void quantize_group(const float (&x)[8], unsigned group, int lane, int (&q)[8], __half& dh) {
+    unsigned amax = 0;  // magnitudes order like their bits, NaNs above infinity
 #pragma unroll
-    for (int e = 0; e < 4; e++) {
-        amax = fmaxf(amax, fabsf(x[e]));
-        nan |= x[e] != x[e];
-    }
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(group, amax, o));
-    nan = (__ballot_sync(group, nan) & group) != 0;
+    for (int e = 0; e < 8; e++) amax = max(amax, __float_as_uint(x[e]) & 0x7FFFFFFFu);
+    amax = max(amax, __shfl_xor_sync(group, amax, 1));
+    amax = max(amax, __shfl_xor_sync(group, amax, 2));
+    float m = __uint_as_float(amax);
     if (TYPE == AF_KV_Q8_0) {
-        dh = __float2half_rn(amax / 127.f);
+        m = m / 127.f;
     } else {
-        float m = 0.f;
-        bool has = false;
+        // the sign of the first value of that magnitude: of the first quads (by lane), then of the second
+        unsigned mine = 0;  // 1: in the first quad, 2: in the second; << 2: negative there
 #pragma unroll
-        for (int e = 3; e >= 0; e--)
-            if (fabsf(x[e]) == amax) {
-                m = x[e];
-                has = true;
+        for (int e = 7; e >= 0; e--)
+            if ((__float_as_uint(x[e]) & 0x7FFFFFFFu) == amax) {
+                const unsigned w = e < 4 ? 1u : 2u;
+                mine = (mine & ~(w << 2)) | w | (__float_as_uint(x[e]) >> 31 ? w << 2 : 0u);
             }
-        const unsigned who = __ballot_sync(group, has) & group;  // empty only when the block holds NaN alone
-        m = __shfl_sync(group, m, who ? __ffs(who) - 1 : lane);
-        dh = __float2half_rn(m / -8.f);
+        const unsigned first = __ballot_sync(group, mine & 1) & group, second = __ballot_sync(group, mine & 2) & group;
+        const int src = first ? __ffs(first) - 1 : second ? __ffs(second) - 1 : lane;
+        const unsigned theirs = __shfl_sync(group, mine, src);
+        const bool negative = theirs & (first ? 4u : 8u);
+        m = negative ? m * 0.125f : m * -0.125f;
     }
-    if (nan || (__half_as_ushort(dh) & 0x7C00) == 0x7C00) dh = __ushort_as_half((unsigned short)0x7FFF);
-    const float d = fabsf(__half2float(dh)), rd = d == 0.f ? 0.f : __frcp_rn(d), h = 0.5f * d;
+    dh = __float2half_rn(m);
+    if ((__half_as_ushort(dh) & 0x7C00) == 0x7C00) dh = __ushort_as_half((unsigned short)0x7FFF);
+    const float d = fabsf(__half2float(dh)), h = 0.5f * d;
+    float rd;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(rd) : "f"(d));
+    rd *= 1.f - 0x1p-20f;  // (the approximation is off by 2^-23)
     constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer, in the low bits
 #pragma unroll
-    for (int e = 0; e < 4; e++) {
+    for (int e = 0; e < 8; e++) {
         // the rounding is half away from zero on |v| for Q8_0, half up on v / d for Q4_0: half up on y / |d| either way
         const float y = TYPE == AF_KV_Q8_0 ? fabsf(x[e]) : (__half_as_ushort(dh) & 0x8000 ? -x[e] : x[e]);
-        const float g = y * rd + kMagic;
+        const float g = fmaf(y, rd, kMagic);
         const float r = fmaf(-(g - kMagic), d, y);
         int v = __float_as_int(g) - 0x4B400000;
         v += (r >= h ? 1 : 0) - (r < -h ? 1 : 0);
@@ -84,29 +87,30 @@ __device__ __forceinline__ void quantize_group(const float (&x)[4], unsigned gro
     }
 }
 
+// The thread's eight values (at dims d0.. and d0 + 16.. of cell `cell`) into the cache.
 template <int TYPE>
-__device__ __forceinline__ void store_group(void* base, __half* scales, int64_t cell, int D, int d0, const float (&x)[4],
+__device__ __forceinline__ void store_group(void* base, __half* scales, int64_t cell, int D, int d0, const float (&x)[8],
                                             unsigned group, int lane) {
-    if (TYPE == AF_F32) {
-        *reinterpret_cast<float4*>((float*)base + cell * D + d0) = make_float4(x[0], x[1], x[2], x[3]);
-    } else if (TYPE == AF_F16) {
-        __half2 h[2] = {__floats2half2_rn(x[0], x[1]), __floats2half2_rn(x[2], x[3])};
-        *reinterpret_cast<uint2*>((__half*)base + cell * D + d0) = *reinterpret_cast<const uint2*>(h);
-    } else {
-        int q[4];
-        __half dh;
-        quantize_group<TYPE>(x, group, lane, q, dh);
-        if (TYPE == AF_KV_Q8_0) {
-            const unsigned w = (unsigned)(q[0] & 255) | (unsigned)(q[1] & 255) << 8 | (unsigned)(q[2] & 255) << 16 |
-                               (unsigned)(q[3] & 255) << 24;
-            *reinterpret_cast<unsigned*>((uint8_t*)base + cell * D + d0) = w;
+    int q[8];
+    __half dh;
+    if (TYPE == AF_KV_Q8_0 || TYPE == AF_KV_Q4_0) quantize_group<TYPE>(x, group, lane, q, dh);
+#pragma unroll
+    for (int e = 0; e < 8; e += 4) {
+        const int d = d0 + 4 * e;
+        if (TYPE == AF_F32) {
+            *reinterpret_cast<float4*>((float*)base + cell * D + d) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+        } else if (TYPE == AF_F16) {
+            __half2 h[2] = {__floats2half2_rn(x[e], x[e + 1]), __floats2half2_rn(x[e + 2], x[e + 3])};
+            *reinterpret_cast<uint2*>((__half*)base + cell * D + d) = *reinterpret_cast<const uint2*>(h);
+        } else if (TYPE == AF_KV_Q8_0) {
+            *reinterpret_cast<unsigned*>((uint8_t*)base + cell * D + d) =
+                __byte_perm(__byte_perm(q[e], q[e + 1], 0x0040), __byte_perm(q[e + 2], q[e + 3], 0x0040), 0x5410);
         } else {
-            const unsigned w = (unsigned)(q[0] + 8) | (unsigned)(q[1] + 8) << 4 | (unsigned)(q[2] + 8) << 8 |
-                               (unsigned)(q[3] + 8) << 12;
-            *reinterpret_cast<unsigned short*>((uint8_t*)base + cell * (D / 2) + d0 / 2) = (unsigned short)w;
+            *reinterpret_cast<unsigned short*>((uint8_t*)base + cell * (D / 2) + d / 2) =
+                (unsigned short)((q[e] + 8) | (q[e + 1] + 8) << 4 | (q[e + 2] + 8) << 8 | (q[e + 3] + 8) << 12);
         }
-        if ((lane & 7) == 0) scales[cell * (D / 32) + d0 / 32] = dh;
     }
+    if ((TYPE == AF_KV_Q8_0 || TYPE == AF_KV_Q4_0) && (lane & 3) == 0) scales[cell * (D / 32) + d0 / 32] = dh;
 }
 
 template <int TYPE>
@@ -114,43 +118,42 @@ __global__ void __launch_bounds__(kThreads)
     kv_write_kernel(KvRows c, const float* __restrict__ k, const float* __restrict__ v, int64_t ld, int n,
                     const int* __restrict__ slots, int slot0) {
     const int lane = threadIdx.x & 31;
-    const unsigned group = 0xffu << (lane & 24);
-    const int quads = c.KVH * c.D / 4;  // a multiple of 8
+    const unsigned group = 0xfu << (lane & 28);
+    const int octs = c.KVH * c.D / 8;  // a multiple of 4
     pdl_launch_dependents();
     pdl_wait();
-    for (int r0 = blockIdx.x * kRows; r0 < n; r0 += gridDim.x * kRows) {
-        int slot[kRows];  // -1: not written; the same in every thread of the CTA
+    for (int r0 = blockIdx.x * kWriteRows; r0 < n; r0 += gridDim.x * kWriteRows) {
+        int slot[kWriteRows];  // -1: not written; the same in every thread of the CTA
 #pragma unroll
-        for (int j = 0; j < kRows; j++) slot[j] = r0 + j >= n ? -1 : slots ? __ldcg(slots + r0 + j) : slot0 + r0 + j;
+        for (int j = 0; j < kWriteRows; j++) slot[j] = r0 + j >= n ? -1 : slots ? __ldcg(slots + r0 + j) : slot0 + r0 + j;
         if (slots) {
             unsigned again = 0;  // rows whose slot a later row names too: it belongs to that one
             for (int i = r0 + 1 + threadIdx.x; i < n; i += kThreads) {
                 const int x = __ldcg(slots + i);
 #pragma unroll
-                for (int j = 0; j < kRows; j++) again |= (i > r0 + j && x == slot[j]) ? 1u << j : 0u;
+                for (int j = 0; j < kWriteRows; j++) again |= (i > r0 + j && x == slot[j]) ? 1u << j : 0u;
             }
             again = cta_or(again);
 #pragma unroll
-            for (int j = 0; j < kRows; j++)
+            for (int j = 0; j < kWriteRows; j++)
                 if (slot[j] < 0 || slot[j] >= c.ctx || (again >> j & 1)) slot[j] = -1;
         }
-        for (int i = threadIdx.x; i < quads; i += kThreads) {
-            const int e0 = i * 4, g = e0 / c.D, d0 = e0 % c.D;
-            float4 x[2][kRows];
+        for (int i = threadIdx.x; i < 2 * octs; i += kThreads) {  // K, then V
+            const bool isv = i >= octs;
+            const int b = (isv ? i - octs : i) >> 2, e0 = b * 32 + (i & 3) * 4, g = e0 / c.D, d0 = e0 - g * c.D;
+            const float* src = (isv ? v : k) + r0 * ld + e0;
+            float4 x[kWriteRows][2];
 #pragma unroll
-            for (int j = 0; j < kRows; j++)
+            for (int j = 0; j < kWriteRows; j++)
                 if (slot[j] >= 0) {
-                    x[0][j] = __ldcg(reinterpret_cast<const float4*>(k + (r0 + j) * ld + e0));
-                    x[1][j] = __ldcg(reinterpret_cast<const float4*>(v + (r0 + j) * ld + e0));
+                    x[j][0] = __ldcg(reinterpret_cast<const float4*>(src + j * ld));
+                    x[j][1] = __ldcg(reinterpret_cast<const float4*>(src + j * ld + 16));
                 }
 #pragma unroll
-            for (int j = 0; j < kRows; j++)
+            for (int j = 0; j < kWriteRows; j++)
                 if (slot[j] >= 0) {
-                    const int64_t cell = (int64_t)g * c.ctx + slot[j];
-                    const float a[4] = {x[0][j].x, x[0][j].y, x[0][j].z, x[0][j].w};
-                    const float b[4] = {x[1][j].x, x[1][j].y, x[1][j].z, x[1][j].w};
-                    store_group<TYPE>(c.k, c.ks, cell, c.D, d0, a, group, lane);
-                    store_group<TYPE>(c.v, c.vs, cell, c.D, d0, b, group, lane);
+                    const float a[8] = {x[j][0].x, x[j][0].y, x[j][0].z, x[j][0].w, x[j][1].x, x[j][1].y, x[j][1].z, x[j][1].w};
+                    store_group<TYPE>(isv ? c.v : c.k, isv ? c.vs : c.ks, (int64_t)g * c.ctx + slot[j], c.D, d0, a, group, lane);
                 }
         }
     }
