@@ -6,7 +6,8 @@
 // only K and V operands, and an MMA reads nothing else from it:
 //   columns [0, D)            output accumulator, fp32
 //   columns [128, 128 + D)    q, scaled by log2 e / sqrt(D) and a power of two per row, as fp16 hi and lo parts
-//   columns [256 + 64 b, ..)  b < 4: scores of a tile (64 fp32 columns), overwritten by p as fp16 hi and lo parts
+//   columns [256 + 64 b, ..)  b < 4: scores of a tile (64 fp32 columns), overwritten, 32 slots by 32, by p's fp16 hi
+//                             and lo parts (16 columns each)
 // Both products take their A operand (q, p) from tensor memory and B from shared memory: K rows [slot][dim] are
 // K-major, V rows [slot][dim] MN-major, so neither is transposed and both have the cache's own order:
 //   fp16 cache    TMA copies 64 slots x 64 dims boxes into the SWIZZLE_128B layout; two products (hi, lo of q or p)
@@ -17,8 +18,10 @@
 //                 exponent of the output, which is rescaled when the slots outgrow it.
 //                 (Rows read through registers instead, three tiles ahead: 192 us where this took 108 at 64 nodes
 //                 over 30720 fp32 slots; the warp's loads of several tiles share its few scoreboards.)
-// Warps 0-3 are the softmax (a thread owns a row: the whole tile of its scores in registers, maximum, p, sum), one
-// warp issues the MMAs, scores of up to three tiles ahead of the outputs, so the tensor pipe always has a queue.
+// Warps 0-7 are the softmax: a thread owns a row and 32 of a tile's slots (its scores in registers: maximum, p, sum), the
+// two of a row exchange their maxima tile by tile.  (One thread for all 64 slots was the longest chain of the pipeline:
+// some 500 instructions a tile and a warp beside eight converting warps, TBD.)  One warp issues the MMAs, scores of up to
+// three tiles ahead of the outputs, so the tensor pipe always has a queue.
 // The reference maximum moves lazily, as in attn_tree.cu, with the same factor 2^8 in p.
 // Tiles that hold nodes (the last ones): a hidden slot's score is -inf by a select; non-finite keys and values and the
 // slots behind the last node become zero operands, and a row that sees a slot so treated becomes NaN.
@@ -41,6 +44,7 @@ constexpr int kRows = 128;
 constexpr float kLazy2 = 4.f, kBias2 = 8.f;  // as attn_tree.cu's
 constexpr int kConvWarps = 4;  // for K, and as many for V: 16 slots of a tile each
 constexpr int kNoExp = -1000;
+constexpr int kSoftWarps = 8;  // two per 32 rows
 
 template <int TYPE, int D>
 struct TcCfgT {
@@ -57,20 +61,22 @@ struct TcCfgT {
     static constexpr int OFF_V = NS * SLOT, OFF_RAW = 2 * NS * SLOT;
     static constexpr int QS = kRows * D * 4 / SLOT;          // the last V slots, through which q and the output pass
     static_assert(QS <= NS, "q fits the V slots");
-    static constexpr int MMA_WARP = 4 + (SPLIT ? 2 * kConvWarps : 0), COPY_WARP = MMA_WARP + 1;  // + 1: V's copies
+    static constexpr int MMA_WARP = kSoftWarps + (SPLIT ? 2 * kConvWarps : 0), COPY_WARP = MMA_WARP + 1;  // + 1: V's copies
     static constexpr int WARPS = COPY_WARP + 2;
     // at least more than half of an SM's shared memory: a CTA takes all of its tensor memory
     static constexpr int USED = OFF_RAW + 2 * NR * RAW;
-    static constexpr int SMEM = (USED > 120 * 1024 ? USED : 120 * 1024) + 1024;
+    static constexpr int SMEM = USED > 120 * 1024 ? USED : 120 * 1024;
 };
 
 // Of pairs, [0] is K's and [1] V's.
-struct TcState {
+struct alignas(1024) TcState {  // (the operand slots behind it need 1024 bytes)
     uint64_t full[2][6], empty[2][6];          // operand slots
     uint64_t raw_full[2][6], raw_empty[2][6];  // staging slots
     uint64_t s_full[4], p_full[4], pv_done[4];
     uint64_t q_ready, done;
     uint64_t v_clean;                          // fp16: a tile of nodes has its V checked
+    uint64_t pair[4];                          // the two softmax warps of 32 rows
+    float pair_x[2][4][2][32];                 // what they exchange
     uint32_t tmem_base;
     int copies[2];    // bulk copies issued, for the drain
     volatile int abort;
@@ -133,28 +139,14 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t chunk) {
     return d;
 }
 
-// 32 lanes x 64 columns, waited for
-__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
-    uint32_t r[64];
+// Whole warp: 16 columns of 32 lanes (waited for with tmem_st_wait)
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
-        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
-        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]),
-          "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]),
-          "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
-          "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]),
-          "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
-        : "r"(taddr)
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
-#pragma unroll
-    for (int i = 0; i < 64; i++) v[i] = __uint_as_float(r[i]);
 }
 
 // x = hi + lo in fp16 (lo off by at most 2^-23 of x, or half of fp16's smallest step 2^-24)
@@ -190,60 +182,50 @@ struct Raw<AF_KV_Q4_0> {
     __half d;
 };
 template <int TYPE, int D>
-struct RawTile {
-    static constexpr int N = 16 * D / Raw<TYPE>::VALUES / 32;
-    Raw<TYPE> c[N];
-};
-
-// st: the warp's 16 rows in a staging slot, sc: their scales.
-template <int TYPE, int D>
-__device__ __forceinline__ void load_raw(const uint8_t* st, const uint8_t* sc, int lane, RawTile<TYPE, D>& r) {
-#pragma unroll
-    for (int i = 0; i < RawTile<TYPE, D>::N; i++) {
-        const int idx = i * 32 + lane;
-        r.c[i].a = reinterpret_cast<const decltype(r.c[i].a)*>(st)[idx];
-        if constexpr (TYPE != AF_F32) r.c[i].d = reinterpret_cast<const __half*>(sc)[idx / 4];
-    }
+constexpr int raw_pieces() {
+    return 16 * D / Raw<TYPE>::VALUES / 32;
 }
 
-// Rows from `valid` on become zeros, and so does what is not finite; returns the rows (bits) that held such.
-template <int TYPE, int D>
-__device__ __forceinline__ unsigned clean_raw(RawTile<TYPE, D>& r, int valid, int lane) {
-    unsigned rows = 0;
-#pragma unroll
-    for (int i = 0; i < RawTile<TYPE, D>::N; i++) {
-        Raw<TYPE>& c = r.c[i];
-        const int row = (i * 32 + lane) / (D / c.VALUES);
+// Piece i from the staged rows st and their scales.  NODES: rows from `valid` on read as zeros, and so does what is not
+// finite, whose rows are marked in `bad`.
+template <int TYPE, int D, bool NODES>
+__device__ __forceinline__ Raw<TYPE> load_raw(const uint8_t* st, const uint8_t* sc, int i, int valid, int lane, unsigned& bad) {
+    const int idx = i * 32 + lane;
+    Raw<TYPE> c;
+    c.a = reinterpret_cast<const decltype(c.a)*>(st)[idx];
+    if constexpr (TYPE != AF_F32) c.d = reinterpret_cast<const __half*>(sc)[idx / 4];
+    if (NODES) {
+        const int row = idx / (D / c.VALUES);
         if constexpr (TYPE == AF_F32) {
             uint32_t* w[4] = {&c.a.x, &c.a.y, &c.a.z, &c.a.w};
 #pragma unroll
             for (int e = 0; e < 4; e++)
                 if (row >= valid || (*w[e] & 0x7F800000u) == 0x7F800000u) {
-                    if (row < valid) rows |= 1u << row;
+                    if (row < valid) bad |= 1u << row;
                     *w[e] = 0u;
                 }
         } else {
             if (row >= valid || (__half_as_ushort(c.d) & 0x7C00u) == 0x7C00u) {
-                if (row < valid) rows |= 1u << row;
+                if (row < valid) bad |= 1u << row;
                 c.d = __ushort_as_half(0);
             }
         }
     }
-    return rows;
+    return c;
 }
 
-// Largest magnitude among this thread's values (fp32) or scales.
-template <int TYPE, int D>
-__device__ __forceinline__ float raw_max(const RawTile<TYPE, D>& r) {
+// Largest magnitude among this lane's values (fp32) or scales.
+template <int TYPE, int D, bool NODES>
+__device__ __forceinline__ float raw_max(const uint8_t* st, const uint8_t* sc, int valid, int lane, unsigned& bad) {
     float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < RawTile<TYPE, D>::N; i++) {
+    for (int i = 0; i < raw_pieces<TYPE, D>(); i++) {
+        const Raw<TYPE> c = load_raw<TYPE, D, NODES>(st, sc, i, valid, lane, bad);
         if constexpr (TYPE == AF_F32) {
-            const uint4 a = r.c[i].a;
-            m = fmaxf(fmaxf(m, fabsf(__uint_as_float(a.x))), fabsf(__uint_as_float(a.y)));
-            m = fmaxf(fmaxf(m, fabsf(__uint_as_float(a.z))), fabsf(__uint_as_float(a.w)));
+            m = fmaxf(fmaxf(m, fabsf(__uint_as_float(c.a.x))), fabsf(__uint_as_float(c.a.y)));
+            m = fmaxf(fmaxf(m, fabsf(__uint_as_float(c.a.z))), fabsf(__uint_as_float(c.a.w)));
         } else {
-            m = fmaxf(m, fabsf(__half2float(r.c[i].d)));
+            m = fmaxf(m, fabsf(__half2float(c.d)));
         }
     }
     return m;
@@ -255,30 +237,23 @@ __device__ __forceinline__ float warp_max(float m) {
     return m;
 }
 
-// Arrive, not before x (>= 0) has been computed.
-__device__ __forceinline__ void mbar_arrive_after(uint64_t* bar, float x) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ge.f32 p, %1, 0f00000000;\n\t"
-        "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar)),
-        "f"(x)
-        : "memory");
-}
-
 __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 __device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
 
 // The fp16 hi and lo parts of the warp's rows row0.., times 2^-e, into a slot (SWIZZLE_128B atoms of 64 dims,
 // [64 slots][128 B] each).
-template <int TYPE, int D>
-__device__ __forceinline__ void store_tile(uint8_t* dst, const RawTile<TYPE, D>& r, int e, int row0, int lane) {
+template <int TYPE, int D, bool NODES>
+__device__ __forceinline__ void store_tile(uint8_t* dst, const uint8_t* st, const uint8_t* sc, int e, int row0, int valid, int lane) {
     constexpr int PPR = D / Raw<TYPE>::VALUES, PART = BK * D * 2;  // pieces per row
     const float down = pow2i(-e);
 #pragma unroll
-    for (int i = 0; i < RawTile<TYPE, D>::N; i++) {
+    for (int i = 0; i < raw_pieces<TYPE, D>(); i++) {
+        unsigned bad = 0;
+        const Raw<TYPE> r = load_raw<TYPE, D, NODES>(st, sc, i, valid, lane, bad);
         const int idx = i * 32 + lane, key = row0 + idx / PPR, d0 = idx % PPR * Raw<TYPE>::VALUES;
         const uint32_t off = (uint32_t)((d0 >> 6) * BK * 128) + sw128(key, (d0 >> 3) & 7) + (d0 & 7) * 2;
         if constexpr (TYPE == AF_F32) {
-            const uint4 a = r.c[i].a;
+            const uint4 a = r.a;
             const float2 dd = both(down);
             uint2 hi, lo;
             split2(mul2(make_float2(__uint_as_float(a.x), __uint_as_float(a.y)), dd), hi.x, lo.x);
@@ -289,10 +264,10 @@ __device__ __forceinline__ void store_tile(uint8_t* dst, const RawTile<TYPE, D>&
             uint32_t hi[4], lo[4];
             // codes q are exact in fp16, and so is d 2^-e (11 bits); hi = fp16(q d), lo = q d - hi by a fused
             // multiply-add, exact as long as it is not below fp16's smallest step 2^-24
-            const __half2 d2 = __float2half2_rn(__half2float(r.c[i].d) * down);
+            const __half2 d2 = __float2half2_rn(__half2float(r.d) * down);
             __half2 q[4];
             if constexpr (TYPE == AF_KV_Q8_0) {
-                const uint32_t x = r.c[i].a.x ^ 0x80808080u, y = r.c[i].a.y ^ 0x80808080u;
+                const uint32_t x = r.a.x ^ 0x80808080u, y = r.a.y ^ 0x80808080u;
                 const __half2 off = u2h(0x64806480u);
                 q[0] = __hsub2(u2h(__byte_perm(x, 0x64646464u, 0x4140)), off);
                 q[1] = __hsub2(u2h(__byte_perm(x, 0x64646464u, 0x4342)), off);
@@ -300,7 +275,7 @@ __device__ __forceinline__ void store_tile(uint8_t* dst, const RawTile<TYPE, D>&
                 q[3] = __hsub2(u2h(__byte_perm(y, 0x64646464u, 0x4342)), off);
             } else {
                 const __half2 off = u2h(0x64086408u);
-                const uint32_t x = r.c[i].a;
+                const uint32_t x = r.a;
                 __half2 n[4];  // dims (p, p + 4)
 #pragma unroll
                 for (int p = 0; p < 4; p++) n[p] = __hsub2(u2h(((x >> (4 * p)) & 0x000F000Fu) | 0x64006400u), off);
@@ -330,9 +305,9 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
     using C = TcCfgT<TYPE, D>;
     constexpr uint32_t kIdS = idesc_f16(kRows, BK);                  // scores: N = slots, B K-major
     constexpr uint32_t kIdO = idesc_f16(kRows, D) | (1u << 16);      // output: N = dims, B MN-major
-    extern __shared__ uint8_t smem_raw[];
+    extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ TcState sm;
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    static_assert(sizeof(TcState) + C::SMEM <= 227 * 1024, "an SM's shared memory");
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int G = a.H / a.c.KVH, R = a.n * G;
     const int split = blockIdx.x, g = blockIdx.y, r0 = blockIdx.z * kRows;
@@ -356,11 +331,12 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
         }
         for (int i = 0; i < 4; i++) {
             mbar_init(&sm.s_full[i], C::SPLIT ? 2 : 1);  // the commit, and the issuer for K's exponent
-            mbar_init(&sm.p_full[i], 4);
+            mbar_init(&sm.p_full[i], kSoftWarps);
             mbar_init(&sm.pv_done[i], 1);
+            mbar_init(&sm.pair[i], 2);
         }
-        mbar_init(&sm.v_clean, 4);
-        mbar_init(&sm.q_ready, 4);
+        mbar_init(&sm.v_clean, kSoftWarps);
+        mbar_init(&sm.q_ready, kSoftWarps);
         mbar_init(&sm.done, 1);
         sm.abort = 0;
         fence_mbar_init();
@@ -419,9 +395,10 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
 #pragma unroll
             for (int kk = from; kk < to; kk++) {
                 const uint64_t b = vd + ((kk * 2048) >> 4);
-                mma_f16_ts(tm, p + kk * 8, b, kIdO, t > 0 || kk > 0);
-                mma_f16_ts(tm, p + BK / 2 + kk * 8, b, kIdO, 1);
-                if (C::SPLIT) mma_f16_ts(tm, p + kk * 8, b + (C::PART >> 4), kIdO, 1);
+                const uint32_t hi = p + (kk >> 1) * 32 + (kk & 1) * 8, lo = hi + 16;
+                mma_f16_ts(tm, hi, b, kIdO, t > 0 || kk > 0);
+                mma_f16_ts(tm, lo, b, kIdO, 1);
+                if (C::SPLIT) mma_f16_ts(tm, hi, b + (C::PART >> 4), kIdO, 1);
             }
             if (to == BK / 16) {
                 mma_commit(&sm.pv_done[t & 3]);
@@ -508,41 +485,42 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
         }
-    } else if (warp >= 4) {
+    } else if (warp >= kSoftWarps) {
         if constexpr (C::SPLIT) {
             // ---------------- fp32, Q8_0, Q4_0: staged rows -> fp16 parts
-            const int x = (warp - 4) / kConvWarps, w = (warp - 4) % kConvWarps;
+            const int x = (warp - kSoftWarps) / kConvWarps, w = (warp - kSoftWarps) % kConvWarps;
             Ring<C::NR> rr;
             Ring<C::NS> ro;
             bool ok = true;
             for (int t = 0; t < T; t++, ro.next()) {
-                RawTile<TYPE, D> raw;
                 // Every warp waits for every staging slot of the tile and frees it, the ones without its rows too: a
                 // warp that skipped a round of a slot could not tell that round's completion from the next one's.
-                // A slot is freed when its values are in registers for certain, that is used: an arrival may overtake
-                // loads that are still queued, and the next copy then overwrites what they read (seen as wrong
-                // results of single CTAs).  fp32: the largest value depends on all of them; codes: after they are
-                // stored (below).
-                float m = 0.f;
-                const int slot0 = rr.i;
+                // A slot is freed once its values have been used (below, after they are stored): an arrival may
+                // overtake loads that are still queued, and the next copy then overwrites what they read (seen as wrong
+                // results of single CTAs).
+                int mine = 0;
 #pragma unroll
                 for (int p = 0; p < kConvWarps / C::RU; p++, rr.next()) {
                     ok = ok && twait(&sm.raw_full[x][rr.i], rr.ph, sm);
                     if (!ok) break;
-                    if (w / C::RU == p) {
-                        const uint8_t* st = smem + C::OFF_RAW + (x * C::NR + rr.i) * C::RAW;
-                        const int wr = (w % C::RU) * 16;  // the warp's rows in the slot
-                        load_raw<TYPE, D>(st + wr * C::RB, st + C::RR * C::RB + wr * C::SB, lane, raw);
-                        m = warp_max(raw_max<TYPE, D>(raw));
-                    }
-                    if (TYPE == AF_F32 && lane == 0) mbar_arrive_after(&sm.raw_empty[x][rr.i], m);
+                    if (w / C::RU == p)
+                        mine = rr.i;
+                    else if (lane == 0)
+                        mbar_arrive(&sm.raw_empty[x][rr.i]);
                 }
                 if (!ok) break;
-                if (t >= tn) {
-                    const unsigned bad = clean_raw<TYPE, D>(raw, valid - t * BK - w * 16, lane);
-                    if (bad) atomicOr(&sm.bad[t - tn], (unsigned long long)bad << (w * 16));
-                    m = warp_max(raw_max<TYPE, D>(raw));
-                }
+                const uint8_t* st = smem + C::OFF_RAW + (x * C::NR + mine) * C::RAW;
+                const int wr = (w % C::RU) * 16;  // the warp's rows in the slot
+                const uint8_t *rows = st + wr * C::RB, *scales = st + C::RR * C::RB + wr * C::SB;
+                const int left = t >= tn ? valid - t * BK - w * 16 : 16;  // the warp's rows that hold slots
+                unsigned bad = 0;
+                float m = 0.f;
+                if (t >= tn)
+                    m = raw_max<TYPE, D, true>(rows, scales, left, lane, bad);
+                else
+                    m = raw_max<TYPE, D, false>(rows, scales, left, lane, bad);
+                m = warp_max(m);
+                if (bad) atomicOr(&sm.bad[t - tn], (unsigned long long)bad << (w * 16));
                 // largest value in [1, 2), or largest scale times its largest code in [1, 4)
                 int e = max(exponent_of(m), -126);
                 if (TYPE == AF_KV_Q8_0) e += 6;
@@ -551,9 +529,13 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                 if (t >= C::NS) ok = twait(&sm.empty[x][ro.i], ro.ph ^ 1, sm);
                 if (x == 1 && t == C::NS - C::QS) ok = ok && twait(&sm.q_ready, 0, sm);
                 if (!ok) break;
-                store_tile<TYPE, D>(smem + (x ? C::OFF_V : 0) + ro.i * C::SLOT, raw, e, w * 16, lane);
+                uint8_t* dst = smem + (x ? C::OFF_V : 0) + ro.i * C::SLOT;
+                if (t >= tn)
+                    store_tile<TYPE, D, true>(dst, rows, scales, e, w * 16, left, lane);
+                else
+                    store_tile<TYPE, D, false>(dst, rows, scales, e, w * 16, left, lane);
                 __syncwarp();
-                if (TYPE != AF_F32 && lane == 0) mbar_arrive(&sm.raw_empty[x][slot0]);
+                if (lane == 0) mbar_arrive(&sm.raw_empty[x][mine]);
                 if (lane == 0) {
                     if (x == 1)
                         sm.ev[t & 7][w] = m == 0.f ? kNoExp : e;
@@ -566,54 +548,59 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
             }
         }
     } else {
-        // ---------------- softmax: thread = row
-        const int r = r0 + tid;
+        // ---------------- softmax: thread = row and half of a tile's slots
+        const int quad = warp & 3, half = warp >> 2;
+        const int r = r0 + quad * 32 + lane;
         const bool live = r < R;
-        const uint32_t lane_addr = tmem + ((uint32_t)(warp * 32) << 16);
+        const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
+        unsigned pair_ph = 0;
+        auto meet = [&]() {  // both warps of the rows
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.pair[quad]);
+            const bool met = twait(&sm.pair[quad], pair_ph, sm);
+            pair_ph ^= 1;
+            return met;
+        };
         float rowf = 1.f;
         // Rows pass through shared memory, so that global accesses are whole rows: chunk c (16 bytes) of row r sits at
         // c ^ (r & 7).
         constexpr int CPR = D / 4, RPI = 32 / CPR;  // chunks per row, rows per warp access
         auto stage = [&](uint8_t* base, int rr, int c) { return reinterpret_cast<float4*>(base + rr * D * 4 + ((c ^ (rr & 7)) << 4)); };
-        {  // q: scaled to [1, 2), split, into tensor memory
-            uint8_t* st = smem + C::OFF_V + (C::NS - C::QS) * C::SLOT + warp * 32 * D * 4;
+        uint8_t* const st = smem + C::OFF_V + (C::NS - C::QS) * C::SLOT + quad * 32 * D * 4;
+        bool ok;
+        {  // q: scaled to [1, 2), split, into tensor memory; each warp brings 16 rows and converts half of the dims
             const int64_t off = live ? (int64_t)(r / G) * a.ldq + (int64_t)(g * G + r % G) * D : 0;
-            const int c = lane % CPR;
+            const int c = lane % CPR, i0 = half * 16;
+            float4 x[16 / RPI];
 #pragma unroll
-            for (int i0 = 0; i0 < 32; i0 += 16) {
-                float4 x[16 / RPI];
-#pragma unroll
-                for (int i = 0; i < 16 / RPI; i++) {
-                    const int64_t o = __shfl_sync(0xffffffffu, off, i0 + i * RPI + lane / CPR);
-                    x[i] = __ldcg(reinterpret_cast<const float4*>(a.q + o) + c);
-                }
-#pragma unroll
-                for (int i = 0; i < 16 / RPI; i++) *stage(st, i0 + i * RPI + lane / CPR, c) = x[i];
+            for (int i = 0; i < 16 / RPI; i++) {
+                const int64_t o = __shfl_sync(0xffffffffu, off, i0 + i * RPI + lane / CPR);
+                x[i] = __ldcg(reinterpret_cast<const float4*>(a.q + o) + c);
             }
-            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 16 / RPI; i++) *stage(st, i0 + i * RPI + lane / CPR, c) = x[i];
+            ok = meet();
             const float sc = live ? rsqrtf((float)D) * 1.4426950408889634f : 0.f;
             float mx = 0.f;
 #pragma unroll 8
             for (int i = 0; i < CPR; i++) {
-                const float4 x = *stage(st, lane, i);
-                mx = fmaxf(mx, fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))));
+                const float4 y = *stage(st, lane, i);
+                mx = fmaxf(mx, fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w))));
             }
             const int e = min(max(exponent_of(mx * sc), -100), 126);
             rowf = pow2i(e);
             const float k = pow2i(-e);
 #pragma unroll 1
-            for (int h = 0; h < D / 64; h++) {
-                uint32_t hi[32], lo[32];
+            for (int h = half; h < D / 32; h += 2) {  // 32 dims: 16 columns of hi parts, 16 of lo parts
+                uint32_t hi[16], lo[16];
 #pragma unroll
-                for (int i = 0; i < 16; i++) {
-                    const float4 x = *stage(st, lane, h * 16 + i);
-                    const float2 lo2 = live ? make_float2(x.x * sc * k, x.y * sc * k) : make_float2(0.f, 0.f);  // (what a
-                    const float2 hi2 = live ? make_float2(x.z * sc * k, x.w * sc * k) : make_float2(0.f, 0.f);  // dead row
-                    split2(lo2, hi[2 * i], lo[2 * i]);                                                          // reads may
-                    split2(hi2, hi[2 * i + 1], lo[2 * i + 1]);                                                  // be anything)
+                for (int i = 0; i < 8; i++) {
+                    const float4 y = *stage(st, lane, h * 8 + i);  // (what a dead row reads may be anything)
+                    split2(live ? make_float2(y.x * sc * k, y.y * sc * k) : both(0.f), hi[2 * i], lo[2 * i]);
+                    split2(live ? make_float2(y.z * sc * k, y.w * sc * k) : both(0.f), hi[2 * i + 1], lo[2 * i + 1]);
                 }
-                tmem_st32(lane_addr + kQCol + h * 32, hi);
-                tmem_st32(lane_addr + kQCol + D / 2 + h * 32, lo);
+                tmem_st16(lane_addr + kQCol + h * 16, hi);
+                tmem_st16(lane_addr + kQCol + D / 2 + h * 16, lo);
             }
             tmem_st_wait();
             tc_fence_before();
@@ -630,20 +617,14 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
             const unsigned x = __funnelshift_r(lo, hi, t & 31);
             return t + 32 <= a.n ? x : (t >= a.n ? 0u : x & ((1u << (a.n - t)) - 1u));  // nothing behind the last node
         };
-        constexpr int NG = C::SPLIT ? 4 : 1;  // exponents of a tile
+        constexpr int NG = C::SPLIT ? 2 : 1, W = 32 / NG;  // exponents of this half, slots of each
         float m_ref = -CUDART_INF_F, l = 0.f;
         int ev_ref = kNoExp;
-        bool ok = true;
         Ring<C::NS> rv;
-        for (int t = 0; t < T; t++, rv.next()) {
+        for (int t = 0; ok && t < T; t++, rv.next()) {
             const int b = t & 3;
             const bool nodes = t >= tn;
-            unsigned see[2] = {};
-            if (nodes) {
-                const int j = (t0 + t) * BK - a.past;
-                see[0] = window(j);
-                see[1] = window(j + 32);
-            }
+            const unsigned see = nodes ? window((t0 + t) * BK - a.past + half * 32) : ~0u;
             ok = twait(&sm.s_full[b], (t >> 2) & 1, sm);
             if (!ok) break;
             float f[NG];
@@ -653,19 +634,21 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                 if (!ok) break;
             }
 #pragma unroll
-            for (int q = 0; q < NG; q++) {
-                f[q] = rowf;
-                if (C::SPLIT) {
-                    f[q] = fminf(fmaxf(f[q] * sm.ek[t & 7][q], 0x1p-126f), 0x1p126f);  // (0 or inf times -inf or 0: NaN)
-                    ev[q] = sm.ev[t & 7][q];
-                    ev_max = max(ev_max, ev[q]);
+            for (int q = 0; q < NG; q++) f[q] = rowf;
+            if (C::SPLIT) {
+#pragma unroll
+                for (int q = 0; q < 4; q++) ev_max = max(ev_max, sm.ev[t & 7][q]);
+#pragma unroll
+                for (int q = 0; q < NG; q++) {
+                    f[q] = fminf(fmaxf(f[q] * sm.ek[t & 7][half * NG + q], 0x1p-126f), 0x1p126f);  // (0 or inf times -inf or 0: NaN)
+                    ev[q] = sm.ev[t & 7][half * NG + q];
                 }
             }
             if (!C::SPLIT && nodes) {  // V of this tile: zeros where it is not finite, and behind the last node
                 uint8_t* v = smem + C::OFF_V + rv.i * C::SLOT;
 #pragma unroll
-                for (int i = 0; i < D / 16; i++) {
-                    const int idx = i * 128 + tid, key = (idx >> 3) % BK;  // 16-byte chunk idx of [D / 64][64 slots][8]
+                for (int i = 0; i < D / 32; i++) {
+                    const int idx = i * kSoftWarps * 32 + tid, key = (idx >> 3) % BK;  // 16-byte chunk idx of [D / 64][64 slots][8]
                     uint4* p = reinterpret_cast<uint4*>(v) + idx;
                     uint4 x = *p;
                     uint32_t* w[4] = {&x.x, &x.y, &x.z, &x.w};
@@ -688,21 +671,20 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                 if (!ok) break;
             }
             tc_fence_after();
-            const uint32_t s_addr = lane_addr + kSCol + b * BK;
-            float s[BK];
-            tmem_ld64(s_addr, s);
+            const uint32_t s_addr = lane_addr + kSCol + b * BK + half * 32;
+            float s[32];
+            tmem_ld32(s_addr, s);
             if (nodes) {
-                const unsigned long long bad = *(volatile unsigned long long*)&sm.bad[t - tn];
+                const unsigned bad = (unsigned)(*(volatile unsigned long long*)&sm.bad[t - tn] >> (half * 32));
 #pragma unroll
-                for (int i = 0; i < BK; i++) {
+                for (int i = 0; i < 32; i++) {
                     if (bad >> i & 1) s[i] = CUDART_NAN_F;
-                    if (!(see[i >> 5] >> (i & 31) & 1)) s[i] = -CUDART_INF_F;
+                    if (!(see >> i & 1)) s[i] = -CUDART_INF_F;
                 }
             }
             float mt = -CUDART_INF_F;
 #pragma unroll
             for (int q = 0; q < NG; q++) {
-                constexpr int W = BK / NG;
                 float x0 = s[q * W], x1 = s[q * W + 1];
 #pragma unroll
                 for (int i = 2; i < W; i += 4) {
@@ -711,9 +693,13 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                 }
                 mt = fmaxf(mt, fmaxf(x0, x1) * f[q]);
             }
+            sm.pair_x[t & 1][quad][half][lane] = mt;
+            ok = meet();
+            if (!ok) break;
+            mt = fmaxf(mt, sm.pair_x[t & 1][quad][half ^ 1][lane]);
             const bool move = mt > m_ref + kLazy2;
             const bool grow = C::SPLIT && ev_max > ev_ref + 2;
-            if (__any_sync(0xffffffffu, move || grow)) {
+            if (__any_sync(0xffffffffu, move || grow)) {  // the same in both warps
                 float up = 1.f;
                 if (mt > m_ref) {
                     up = ex2u(m_ref - mt);
@@ -724,12 +710,12 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                     up *= ex2u((float)(ev_ref - ev_max));
                     ev_ref = ev_max;
                 }
-                if (t > 0) {  // the output holds the tiles before t: wait for them, rescale this warp's rows
+                if (t > 0) {  // the output holds the tiles before t: wait for them, rescale these rows, half of the dims each
                     ok = twait(&sm.pv_done[(t - 1) & 3], ((t - 1) >> 2) & 1, sm);
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
+                    for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
                         float o[32];
                         uint32_t u[32];
                         tmem_ld32(lane_addr + c, o);
@@ -741,10 +727,9 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                 }
             }
             const float mb = (m_ref == -CUDART_INF_F ? 0.f : m_ref) - kBias2;
-            uint32_t hi[32], lo[32];
+            uint32_t p32[32];  // hi parts, then lo parts
 #pragma unroll
             for (int q = 0; q < NG; q++) {
-                constexpr int W = BK / NG;
                 // V's slots are 2^-ev of themselves and the output 2^-ev_ref: p takes the difference
                 const float shift = C::SPLIT && ev[q] != kNoExp ? (float)(ev[q] - ev_ref) : 0.f;
                 const float2 ff = both(f[q]), mm = both(shift - mb);
@@ -754,7 +739,7 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                     const float2 y = fma2(make_float2(s[q * W + i], s[q * W + i + 1]), ff, mm);
                     const float2 p = make_float2(ex2u(y.x), ex2u(y.y));
                     sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], p);
-                    split2(p, hi[(q * W + i) / 2], lo[(q * W + i) / 2]);
+                    split2(p, p32[(q * W + i) / 2], p32[16 + (q * W + i) / 2]);
                 }
                 const float2 add = add2(sum[0], sum[1]);
                 if (C::SPLIT && shift < -8.f) {  // small values: p's sum apart from their factor
@@ -766,28 +751,31 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                     l += C::SPLIT ? (add.x + add.y) * ex2u(-shift) : add.x + add.y;
                 }
             }
-            tmem_st32(s_addr, hi);
-            tmem_st32(s_addr + BK / 2, lo);
+            tmem_st32(s_addr, p32);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.p_full[b]);
         }
-        // ---- this split's part of the row
-        ok = ok && twait(&sm.done, 0, sm);
+        // ---- this split's part of the row: the sum of both halves, and half of the dims each
+        if (ok) {
+            sm.pair_x[T & 1][quad][half][lane] = l;
+            ok = meet() && twait(&sm.done, 0, sm);
+            l += sm.pair_x[T & 1][quad][half ^ 1][lane];
+        }
         const int64_t rows = (int64_t)a.c.KVH * R;
         const int64_t row = (int64_t)split * rows + (int64_t)g * R + r;
         // one split: the result itself (zeros for a row that saw nothing)
         const bool last = splits == 1;
         float* base = last ? a.out : a.ws;
         const int64_t off = !live ? 0 : last ? (int64_t)(r / G) * a.ldo + (int64_t)(g * G + r % G) * D : row * D;
-        uint8_t* st = smem + C::OFF_V + (C::NS - C::QS) * C::SLOT + warp * 32 * D * 4;
+        constexpr int HC = CPR / 2;  // chunks of half a row
         if (ok) {  // every operand has been read: the ring is free
             tc_fence_after();
             float up = C::SPLIT ? pow2i(ev_ref) : 1.f;
             if (last) up = l == 0.f ? 0.f : up / l;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
+            for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
                 float o[32];
                 tmem_ld32(lane_addr + c, o);
 #pragma unroll
@@ -795,16 +783,17 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                     *stage(st, lane, (c + i) / 4) = make_float4(o[i] * up, o[i + 1] * up, o[i + 2] * up, o[i + 3] * up);
             }
         } else {
-            for (int c = 0; c < CPR; c++) *stage(st, lane, c) = make_float4(CUDART_NAN_F, CUDART_NAN_F, CUDART_NAN_F, CUDART_NAN_F);
+            for (int c = 0; c < HC; c++)
+                *stage(st, lane, half * HC + c) = make_float4(CUDART_NAN_F, CUDART_NAN_F, CUDART_NAN_F, CUDART_NAN_F);
         }
         __syncwarp();
 #pragma unroll 8
-        for (int i = 0; i < 32; i += RPI) {
-            const int rr = i + lane / CPR;
+        for (int i = 0; i < 32; i += 32 / HC) {
+            const int rr = i + lane / HC, c = half * HC + lane % HC;
             const int64_t o = __shfl_sync(0xffffffffu, off, rr);
-            if (r0 + warp * 32 + rr < R) reinterpret_cast<float4*>(base + o)[lane % CPR] = *stage(st, rr, lane % CPR);
+            if (r0 + quad * 32 + rr < R) reinterpret_cast<float4*>(base + o)[c] = *stage(st, rr, c);
         }
-        if (live && !last)
+        if (live && !last && half == 0)
             reinterpret_cast<float2*>(a.ws + splits * rows * D)[row] =
                 ok ? make_float2(m_ref, l) : make_float2(CUDART_NAN_F, CUDART_NAN_F);
     }
