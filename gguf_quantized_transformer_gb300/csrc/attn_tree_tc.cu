@@ -185,6 +185,12 @@ template <int TYPE, int D>
 constexpr int raw_pieces() {
     return 16 * D / Raw<TYPE>::VALUES / 32;
 }
+// A warp's rows in registers.  fp32 rows are kept from the look for their largest value to their conversion, so that the
+// staging slot is free after the first (the slots hold less than two tiles of K and of V); codes are read again.
+template <int TYPE, int D>
+struct Kept {
+    Raw<TYPE> c[TYPE == AF_F32 ? raw_pieces<TYPE, D>() : 1];
+};
 
 // Piece i from the staged rows st and their scales.  NODES: rows from `valid` on read as zeros, and so does what is not
 // finite, whose rows are marked in `bad`.
@@ -216,12 +222,14 @@ __device__ __forceinline__ Raw<TYPE> load_raw(const uint8_t* st, const uint8_t* 
 
 // Largest magnitude among this lane's values (fp32) or scales.
 template <int TYPE, int D, bool NODES>
-__device__ __forceinline__ float raw_max(const uint8_t* st, const uint8_t* sc, int valid, int lane, unsigned& bad) {
+__device__ __forceinline__ float raw_max(const uint8_t* st, const uint8_t* sc, int valid, int lane, unsigned& bad,
+                                         Kept<TYPE, D>& kept) {
     float m = 0.f;
 #pragma unroll
     for (int i = 0; i < raw_pieces<TYPE, D>(); i++) {
         const Raw<TYPE> c = load_raw<TYPE, D, NODES>(st, sc, i, valid, lane, bad);
         if constexpr (TYPE == AF_F32) {
+            kept.c[i] = c;
             m = fmaxf(fmaxf(m, fabsf(__uint_as_float(c.a.x))), fabsf(__uint_as_float(c.a.y)));
             m = fmaxf(fmaxf(m, fabsf(__uint_as_float(c.a.z))), fabsf(__uint_as_float(c.a.w)));
         } else {
@@ -237,19 +245,29 @@ __device__ __forceinline__ float warp_max(float m) {
     return m;
 }
 
+// Arrive, not before x (>= 0) has been computed.
+__device__ __forceinline__ void mbar_arrive_after(uint64_t* bar, float x) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ge.f32 p, %1, 0f00000000;\n\t"
+        "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "f"(x)
+        : "memory");
+}
+
 __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 __device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
 
 // The fp16 hi and lo parts of the warp's rows row0.., times 2^-e, into a slot (SWIZZLE_128B atoms of 64 dims,
 // [64 slots][128 B] each).
 template <int TYPE, int D, bool NODES>
-__device__ __forceinline__ void store_tile(uint8_t* dst, const uint8_t* st, const uint8_t* sc, int e, int row0, int valid, int lane) {
+__device__ __forceinline__ void store_tile(uint8_t* dst, const uint8_t* st, const uint8_t* sc, int e, int row0, int valid, int lane,
+                                           const Kept<TYPE, D>& kept) {
     constexpr int PPR = D / Raw<TYPE>::VALUES, PART = BK * D * 2;  // pieces per row
     const float down = pow2i(-e);
 #pragma unroll
     for (int i = 0; i < raw_pieces<TYPE, D>(); i++) {
         unsigned bad = 0;
-        const Raw<TYPE> r = load_raw<TYPE, D, NODES>(st, sc, i, valid, lane, bad);
+        const Raw<TYPE> r = TYPE == AF_F32 ? kept.c[TYPE == AF_F32 ? i : 0] : load_raw<TYPE, D, NODES>(st, sc, i, valid, lane, bad);
         const int idx = i * 32 + lane, key = row0 + idx / PPR, d0 = idx % PPR * Raw<TYPE>::VALUES;
         const uint32_t off = (uint32_t)((d0 >> 6) * BK * 128) + sw128(key, (d0 >> 3) & 7) + (d0 & 7) * 2;
         if constexpr (TYPE == AF_F32) {
@@ -495,9 +513,9 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
             for (int t = 0; t < T; t++, ro.next()) {
                 // Every warp waits for every staging slot of the tile and frees it, the ones without its rows too: a
                 // warp that skipped a round of a slot could not tell that round's completion from the next one's.
-                // A slot is freed once its values have been used (below, after they are stored): an arrival may
-                // overtake loads that are still queued, and the next copy then overwrites what they read (seen as wrong
-                // results of single CTAs).
+                // A slot is freed once its values have been used (fp32: their maximum depends on all of them; codes: after
+                // they are stored): an arrival may overtake loads that are still queued, and the next copy then overwrites
+                // what they read (seen as wrong results of single CTAs).
                 int mine = 0;
 #pragma unroll
                 for (int p = 0; p < kConvWarps / C::RU; p++, rr.next()) {
@@ -515,11 +533,13 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                 const int left = t >= tn ? valid - t * BK - w * 16 : 16;  // the warp's rows that hold slots
                 unsigned bad = 0;
                 float m = 0.f;
+                Kept<TYPE, D> kept;
                 if (t >= tn)
-                    m = raw_max<TYPE, D, true>(rows, scales, left, lane, bad);
+                    m = raw_max<TYPE, D, true>(rows, scales, left, lane, bad, kept);
                 else
-                    m = raw_max<TYPE, D, false>(rows, scales, left, lane, bad);
+                    m = raw_max<TYPE, D, false>(rows, scales, left, lane, bad, kept);
                 m = warp_max(m);
+                if (TYPE == AF_F32 && lane == 0) mbar_arrive_after(&sm.raw_empty[x][mine], m);
                 if (bad) atomicOr(&sm.bad[t - tn], (unsigned long long)bad << (w * 16));
                 // largest value in [1, 2), or largest scale times its largest code in [1, 4)
                 int e = max(exponent_of(m), -126);
@@ -531,11 +551,11 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                 if (!ok) break;
                 uint8_t* dst = smem + (x ? C::OFF_V : 0) + ro.i * C::SLOT;
                 if (t >= tn)
-                    store_tile<TYPE, D, true>(dst, rows, scales, e, w * 16, left, lane);
+                    store_tile<TYPE, D, true>(dst, rows, scales, e, w * 16, left, lane, kept);
                 else
-                    store_tile<TYPE, D, false>(dst, rows, scales, e, w * 16, left, lane);
+                    store_tile<TYPE, D, false>(dst, rows, scales, e, w * 16, left, lane, kept);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.raw_empty[x][mine]);
+                if (TYPE != AF_F32 && lane == 0) mbar_arrive(&sm.raw_empty[x][mine]);
                 if (lane == 0) {
                     if (x == 1)
                         sm.ev[t & 7][w] = m == 0.f ? kNoExp : e;
