@@ -20,6 +20,10 @@
 // The reference maximum of the softmax moves only when a score exceeds it by more than 4 (in powers of two); p
 // carries a factor 2^8 so that small p keep their low part above fp16's subnormal step.  Sums are fp32.
 //
+// A call of up to 8 rows (MT = 0) puts the hi parts of q and p into rows 0-7 of the 16-row tile and the lo parts into rows
+// 8-15: one product instead of two, whose halves are added (one token over 30000 Q8_0 slots: 28.2 us with two products,
+// 22.6 with one; fp32 63.4 and 55.4).
+//
 // Hidden slots: a masked score is -inf (a select, so NaN does not survive); in the groups of slots that hold nodes,
 // non-finite values are taken out of the product and added element by element to the rows that see them.
 #include <math_constants.h>
@@ -150,15 +154,17 @@ __device__ __forceinline__ uint32_t finite_h2(uint32_t x, bool& bad) {
 // Slots a warp takes at a time and warps of a CTA.  The codes' kernels are bound by their instructions: with 16 rows (64
 // registers of output) twelve warps of 168 registers fit.
 __host__ __device__ constexpr int tree_stage(int type, int mt) {
-    return (type == AF_KV_Q8_0 || type == AF_KV_Q4_0) && mt == 1 ? 32 : 16;
+    return (type == AF_KV_Q8_0 || type == AF_KV_Q4_0) && mt <= 1 ? 32 : 16;
 }
 __host__ __device__ constexpr int tree_warps(int type, int D, int mt) {
-    return type == AF_F32 && D == 128 ? 6 : (type == AF_KV_Q8_0 || type == AF_KV_Q4_0) && mt == 1 ? 12 : 8;
+    return type == AF_F32 && D == 128 ? 6 : (type == AF_KV_Q8_0 || type == AF_KV_Q4_0) && mt <= 1 ? 12 : 8;
 }
 
 template <int TYPE, int D, int MT>
 struct TreeCfg {
     static constexpr bool QUANT = TYPE == AF_KV_Q8_0 || TYPE == AF_KV_Q4_0;
+    static constexpr bool PACK = MT == 0;
+    static constexpr int ROWS = PACK ? 8 : 16 * MT;
     static constexpr int NB = D / 32;                                             // 32-value blocks of a head
     static constexpr int RB = TYPE == AF_F32 ? 4 * D : TYPE == AF_F16 ? 2 * D : TYPE == AF_KV_Q8_0 ? D : D / 2;  // row bytes
     static constexpr int SB = QUANT ? 2 * NB : 0;                                 // scale bytes of a row
@@ -191,12 +197,12 @@ struct TreeCfg {
 };
 template <int TYPE, int D, int MT>
 constexpr int tree_q_bytes() {
-    return TreeCfg<TYPE, D, MT>::KQ * MT * 32 * 16 * 2;
+    return TreeCfg<TYPE, D, MT>::KQ * 32 * 16 * (MT ? 2 * MT : 1);
 }
 template <int TYPE, int D, int MT>
 constexpr int tree_smem() {
     using C = TreeCfg<TYPE, D, MT>;
-    constexpr int ring = C::NW * C::NST * C::STAGE, join = C::NW * 16 * MT * (C::DP + 2) * 4;
+    constexpr int ring = C::NW * C::NST * C::STAGE, join = C::NW * C::ROWS * (C::DP + 2) * 4;
     return tree_q_bytes<TYPE, D, MT>() + (ring > join ? ring : join);
 }
 
@@ -259,10 +265,13 @@ __device__ __forceinline__ float stage_value(uint32_t st, int key, int d) {
     return s * (float)((int)(w >> (4 * (d & 3)) & 15) - 8);
 }
 
-template <int TYPE, int D, int MT>
-__global__ void __launch_bounds__(TreeCfg<TYPE, D, MT>::NW * 32, 1) attn_tree_kernel(TreeArgs a, int splits) {
-    using C = TreeCfg<TYPE, D, MT>;
-    constexpr int NW = C::NW, NT = D / 8, KS = C::KS, GT = KS / 8, NB = C::NB, ROWS = 16 * MT;
+template <int TYPE, int D, int MT_>
+__global__ void __launch_bounds__(TreeCfg<TYPE, D, MT_>::NW * 32, 1) attn_tree_kernel(TreeArgs a, int splits) {
+    using C = TreeCfg<TYPE, D, MT_>;
+    constexpr bool PACK = C::PACK;
+    constexpr int MT = PACK ? 1 : MT_, NH = PACK ? 1 : 2;  // row tiles, rows of a tile per thread
+    constexpr int QP = PACK ? 1 : 2;                       // fragments of q per step and row tile
+    constexpr int NW = C::NW, NT = D / 8, KS = C::KS, GT = KS / 8, NB = C::NB, ROWS = C::ROWS;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float sm_rowf[ROWS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 3, j = lane >> 2;
@@ -271,7 +280,7 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT>::NW * 32, 1) attn_tree_ke
     const int stages = (keys + KS - 1) / KS;
     const int st0 = (int)((int64_t)stages * split / splits), st1 = (int)((int64_t)stages * (split + 1) / splits);
     const int64_t row0 = (int64_t)g * a.c.ctx;
-    const uint32_t sq = smem_u32(smem), ring = sq + tree_q_bytes<TYPE, D, MT>() + warp * C::NST * C::STAGE;
+    const uint32_t sq = smem_u32(smem), ring = sq + tree_q_bytes<TYPE, D, MT_>() + warp * C::NST * C::STAGE;
 
     pdl_launch_dependents();
     pdl_wait();  // q, the mask and the cache are written by earlier kernels
@@ -279,7 +288,7 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT>::NW * 32, 1) attn_tree_ke
 #pragma unroll
     for (int i = 0; i < C::NST - 1; i++) {
         const int st = st0 + warp + i * NW;
-        if (st < st1) tree_issue<TYPE, D, MT>(a.c, row0, st * KS, keys, ring + i * C::STAGE, lane);
+        if (st < st1) tree_issue<TYPE, D, MT_>(a.c, row0, st * KS, keys, ring + i * C::STAGE, lane);
         cp_commit();
     }
 
@@ -315,16 +324,18 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT>::NW * 32, 1) attn_tree_ke
         if (lane < D / 4) {
             const int mt = r >> 4, rr = r & 15, b = lane >> 3, cc = (lane & 7) >> 1, par = lane & 1;
             const uint32_t lane_off = (uint32_t)((rr & 7) * 4 + cc) * 16, hi8 = (uint32_t)(rr >> 3);
-            auto frag = [&](int step, int part) { return sq + (uint32_t)((step * MT + mt) * 2 + part) * 512 + lane_off; };
+            // register of half h: rows 8-15 are the second of a pair, of the same part or (PACK) the lo part
+            auto frag = [&](int step, int h, int part) {
+                return sq + (uint32_t)((step * MT + mt) * QP + (PACK ? 0 : part)) * 512 + lane_off + (2 * h + (PACK ? part : hi8)) * 4;
+            };
             if (TYPE == AF_F32) {
 #pragma unroll
                 for (int i = 0; i < 4; i++) {  // dim 8 cc + 2 s + h: register 2 h + (row >= 8) of step 4 b + s
                     uint32_t hi, lo;
                     split_tf32(x[i], hi, lo);
                     const int step = 4 * b + 2 * par + (i >> 1);
-                    const uint32_t reg = (2 * (i & 1) + hi8) * 4;
-                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(frag(step, 0) + reg), "r"(hi) : "memory");
-                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(frag(step, 1) + reg), "r"(lo) : "memory");
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(frag(step, i & 1, 0)), "r"(hi) : "memory");
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(frag(step, i & 1, 1)), "r"(lo) : "memory");
                 }
             } else {
                 uint32_t hi[2], lo[2];
@@ -336,23 +347,22 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT>::NW * 32, 1) attn_tree_ke
                     const int dd = 4 * par + i;
                     const int s = TYPE == AF_KV_Q4_0 ? (dd & 3) >> 1 : dd >> 2, h = TYPE == AF_KV_Q4_0 ? dd & 1 : (dd >> 1) & 1;
                     const int e = TYPE == AF_KV_Q4_0 ? dd >> 2 : dd & 1;
-                    const uint32_t reg = (2 * h + hi8) * 4 + 2 * e;
                     const unsigned short vh = (unsigned short)(hi[i >> 1] >> (16 * (i & 1)));
                     const unsigned short vl = (unsigned short)(lo[i >> 1] >> (16 * (i & 1)));
-                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(frag(2 * b + s, 0) + reg), "h"(vh) : "memory");
-                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(frag(2 * b + s, 1) + reg), "h"(vl) : "memory");
+                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(frag(2 * b + s, h, 0) + 2 * e), "h"(vh) : "memory");
+                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(frag(2 * b + s, h, 1) + 2 * e), "h"(vl) : "memory");
                 }
             }
         }
     }
     __syncthreads();
-    float rowf[MT][2];
-    const unsigned* mrow[MT][2];  // mask words of this thread's rows
+    float rowf[MT][NH];
+    const unsigned* mrow[MT][NH];  // mask words of this thread's rows
     const int words = (a.n + 31) / 32;
 #pragma unroll
     for (int mt = 0; mt < MT; mt++)
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
+        for (int h = 0; h < NH; h++) {
             const int r = mt * 16 + h * 8 + j;
             rowf[mt][h] = TYPE == AF_F32 ? 1.f : sm_rowf[r];
             mrow[mt][h] = r0 + r < R ? a.mask + (int64_t)((r0 + r) / G) * words : nullptr;
@@ -367,9 +377,11 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT>::NW * 32, 1) attn_tree_ke
         return t + 32 <= a.n ? x : (t >= a.n ? 0u : x & ((1u << (a.n - t)) - 1u));  // nothing behind the last node
     };
 
-    float o[MT][NT][4] = {}, m_ref[MT][2], l[MT][2] = {};
+    float o[MT][NT][4] = {}, m_ref[MT][NH], l[MT][NH] = {};
 #pragma unroll
-    for (int mt = 0; mt < MT; mt++) m_ref[mt][0] = m_ref[mt][1] = -CUDART_INF_F;
+    for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+        for (int h = 0; h < NH; h++) m_ref[mt][h] = -CUDART_INF_F;
     float vinv = 1.f, vlim = 0.f;  // quantized: V's scales are taken times vinv, a power of two
 
     int slot = 0;
@@ -379,19 +391,19 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT>::NW * 32, 1) attn_tree_ke
         asm volatile("" ::: "memory");
         {  // the previous stage's slot takes the stage NST - 1 ahead
             const int nx = st + (C::NST - 1) * NW, ns = slot == 0 ? C::NST - 1 : slot - 1;
-            if (nx < st1) tree_issue<TYPE, D, MT>(a.c, row0, nx * KS, keys, ring + ns * C::STAGE, lane);
+            if (nx < st1) tree_issue<TYPE, D, MT_>(a.c, row0, nx * KS, keys, ring + ns * C::STAGE, lane);
             cp_commit();
         }
         const uint32_t base = ring + slot * C::STAGE;
         const int key0 = st * KS;
         const uint32_t vb0 = base + C::OV;
         const bool nodes = key0 + KS > a.past;  // slots of nodes, or behind the last one
-        unsigned see[MT][2] = {};
+        unsigned see[MT][NH] = {};
         if (nodes)
 #pragma unroll
             for (int mt = 0; mt < MT; mt++)
 #pragma unroll
-                for (int h = 0; h < 2; h++) see[mt][h] = window(mt, h, key0);
+                for (int h = 0; h < NH; h++) see[mt][h] = window(mt, h, key0);
         // ---- scores of the stage's slots: tile t, columns 2c and 2c + 1, are slots 8 t + 2 c, + 1
         float s[MT][GT][4] = {};
         if constexpr (C::QUANT) {
@@ -423,19 +435,19 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT>::NW * 32, 1) attn_tree_ke
                     float p[GT][4] = {};
 #pragma unroll
                     for (int e = 0; e < 2; e++) {
-                        const uint4 qh = lds128(sq + ((2 * b + e) * MT + mt) * 1024 + lane * 16);
-                        const uint4 ql = lds128(sq + ((2 * b + e) * MT + mt) * 1024 + 512 + lane * 16);
+                        const uint4 qh = lds128(sq + ((2 * b + e) * MT + mt) * QP * 512 + lane * 16);
+                        const uint4 ql = PACK ? qh : lds128(sq + ((2 * b + e) * MT + mt) * 1024 + 512 + lane * 16);
 #pragma unroll
                         for (int t = 0; t < GT; t++) {
                             mma16(p[t], qh, kw[t][2 * e], kw[t][2 * e + 1]);
-                            mma16(p[t], ql, kw[t][2 * e], kw[t][2 * e + 1]);
+                            if (!PACK) mma16(p[t], ql, kw[t][2 * e], kw[t][2 * e + 1]);
                         }
                     }
 #pragma unroll
                     for (int t = 0; t < GT; t++) {
                         const float2 dd = __half22float2(as_h2(dk[t][b]));
 #pragma unroll
-                        for (int h = 0; h < 2; h++) {
+                        for (int h = 0; h < 2; h++) {  // (PACK: the lo parts' scores too, added below)
                             const float2 x = fma2(dd, make_float2(p[t][2 * h], p[t][2 * h + 1]),
                                                   make_float2(s[mt][t][2 * h], s[mt][t][2 * h + 1]));
                             s[mt][t][2 * h] = x.x, s[mt][t][2 * h + 1] = x.y;
@@ -453,12 +465,12 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT>::NW * 32, 1) attn_tree_ke
                 for (int e = 0; e < 2; e++)
 #pragma unroll
                     for (int mt = 0; mt < MT; mt++) {
-                        const uint4 qh = lds128(sq + ((2 * b + e) * MT + mt) * 1024 + lane * 16);
-                        const uint4 ql = lds128(sq + ((2 * b + e) * MT + mt) * 1024 + 512 + lane * 16);
+                        const uint4 qh = lds128(sq + ((2 * b + e) * MT + mt) * QP * 512 + lane * 16);
+                        const uint4 ql = PACK ? qh : lds128(sq + ((2 * b + e) * MT + mt) * 1024 + 512 + lane * 16);
 #pragma unroll
                         for (int t = 0; t < GT; t++) {
                             mma16(s[mt][t], qh, e ? kw[t].z : kw[t].x, e ? kw[t].w : kw[t].y);
-                            mma16(s[mt][t], ql, e ? kw[t].z : kw[t].x, e ? kw[t].w : kw[t].y);
+                            if (!PACK) mma16(s[mt][t], ql, e ? kw[t].z : kw[t].x, e ? kw[t].w : kw[t].y);
                         }
                     }
             }
@@ -480,24 +492,27 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT>::NW * 32, 1) attn_tree_ke
                 for (int e = 0; e < 4; e++)
 #pragma unroll
                     for (int mt = 0; mt < MT; mt++) {
-                        const uint4 qh = lds128(sq + ((4 * b + e) * MT + mt) * 1024 + lane * 16);
-                        const uint4 ql = lds128(sq + ((4 * b + e) * MT + mt) * 1024 + 512 + lane * 16);
+                        const uint4 qh = lds128(sq + ((4 * b + e) * MT + mt) * QP * 512 + lane * 16);
+                        const uint4 ql = PACK ? qh : lds128(sq + ((4 * b + e) * MT + mt) * 1024 + 512 + lane * 16);
 #pragma unroll
                         for (int t = 0; t < GT; t++) {
                             mma8(s[mt][t], qh, kh[t][2 * e], kh[t][2 * e + 1]);
-                            mma8(s[mt][t], ql, kh[t][2 * e], kh[t][2 * e + 1]);
+                            if (!PACK) mma8(s[mt][t], ql, kh[t][2 * e], kh[t][2 * e + 1]);
                             mma8(s[mt][t], qh, kl[t][2 * e], kl[t][2 * e + 1]);
                         }
                     }
             }
         }
+        if (PACK)
+#pragma unroll
+            for (int t = 0; t < GT; t++) s[0][t][0] += s[0][t][2], s[0][t][1] += s[0][t][3];
         // ---- mask and softmax
-        float mx[MT][2];
+        float mx[MT][NH];
         bool move = false;
 #pragma unroll
         for (int mt = 0; mt < MT; mt++)
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
+            for (int h = 0; h < NH; h++) {
                 float x = -CUDART_INF_F;
 #pragma unroll
                 for (int t = 0; t < GT; t++)
@@ -515,7 +530,7 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT>::NW * 32, 1) attn_tree_ke
 #pragma unroll
             for (int mt = 0; mt < MT; mt++)
 #pragma unroll
-                for (int h = 0; h < 2; h++) {
+                for (int h = 0; h < NH; h++) {
                     float x = mx[mt][h];
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
@@ -527,6 +542,7 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT>::NW * 32, 1) attn_tree_ke
                         for (int t = 0; t < NT; t++) {
                             o[mt][t][2 * h] *= f;
                             o[mt][t][2 * h + 1] *= f;
+                            if (PACK) o[mt][t][2] *= f, o[mt][t][3] *= f;
                         }
                     }
                 }
@@ -534,7 +550,7 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT>::NW * 32, 1) attn_tree_ke
 #pragma unroll
         for (int mt = 0; mt < MT; mt++)
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
+            for (int h = 0; h < NH; h++) {
                 const float mb = m_ref[mt][h] == -CUDART_INF_F ? 0.f : m_ref[mt][h] - kBiasT;
 #pragma unroll
                 for (int t = 0; t < GT; t++)
@@ -587,10 +603,12 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT>::NW * 32, 1) attn_tree_ke
                     uint4 ph[MT], pl[MT];
 #pragma unroll
                     for (int mt = 0; mt < MT; mt++) {  // slot 2c is k = c, slot 2c + 1 is k = c + 4
-                        split_tf32(s[mt][t][0], ph[mt].x, pl[mt].x);
-                        split_tf32(s[mt][t][2], ph[mt].y, pl[mt].y);
-                        split_tf32(s[mt][t][1], ph[mt].z, pl[mt].z);
-                        split_tf32(s[mt][t][3], ph[mt].w, pl[mt].w);
+                        split_tf32(s[mt][t][0], ph[mt].x, PACK ? ph[mt].y : pl[mt].x);
+                        split_tf32(s[mt][t][1], ph[mt].z, PACK ? ph[mt].w : pl[mt].z);
+                        if (!PACK) {
+                            split_tf32(s[mt][t][2], ph[mt].y, pl[mt].y);
+                            split_tf32(s[mt][t][3], ph[mt].w, pl[mt].w);
+                        }
                     }
                     const int k0 = t * 8 + 2 * c, k1 = k0 + 1;
 #pragma unroll
@@ -611,7 +629,7 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT>::NW * 32, 1) attn_tree_ke
 #pragma unroll
                             for (int mt = 0; mt < MT; mt++) {
                                 mma8(o[mt][4 * b + i], ph[mt], xh, yh);
-                                mma8(o[mt][4 * b + i], pl[mt], xh, yh);
+                                if (!PACK) mma8(o[mt][4 * b + i], pl[mt], xh, yh);
                                 mma8(o[mt][4 * b + i], ph[mt], xl, yl);
                             }
                         }
@@ -622,10 +640,12 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT>::NW * 32, 1) attn_tree_ke
 #pragma unroll
                 for (int mt = 0; mt < MT; mt++) {
                     const float(&p0)[4] = s[mt][2 * g16], (&p1)[4] = s[mt][2 * g16 + 1];
-                    split_h2(p0[0], p0[1], ph[mt].x, pl[mt].x);
-                    split_h2(p0[2], p0[3], ph[mt].y, pl[mt].y);
-                    split_h2(p1[0], p1[1], ph[mt].z, pl[mt].z);
-                    split_h2(p1[2], p1[3], ph[mt].w, pl[mt].w);
+                    split_h2(p0[0], p0[1], ph[mt].x, PACK ? ph[mt].y : pl[mt].x);
+                    split_h2(p1[0], p1[1], ph[mt].z, PACK ? ph[mt].w : pl[mt].z);
+                    if (!PACK) {
+                        split_h2(p0[2], p0[3], ph[mt].y, pl[mt].y);
+                        split_h2(p1[2], p1[3], ph[mt].w, pl[mt].w);
+                    }
                 }
                 if constexpr (TYPE == AF_F16) {
                     // lane: row lane & 15 of the 16 slots, chunk (lane >> 4) of the pair
@@ -640,9 +660,11 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT>::NW * 32, 1) attn_tree_ke
 #pragma unroll
                         for (int mt = 0; mt < MT; mt++) {
                             mma16(o[mt][t], ph[mt], v.x, v.y);
-                            mma16(o[mt][t], pl[mt], v.x, v.y);
                             mma16(o[mt][t + 1], ph[mt], v.z, v.w);
-                            mma16(o[mt][t + 1], pl[mt], v.z, v.w);
+                            if (!PACK) {
+                                mma16(o[mt][t], pl[mt], v.x, v.y);
+                                mma16(o[mt][t + 1], pl[mt], v.z, v.w);
+                            }
                         }
                     }
                 } else {
@@ -680,14 +702,19 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT>::NW * 32, 1) attn_tree_ke
                                 hi = as_u(x);
                                 lo = as_u(__hfma2(as_h2(l), d, __hfma2(as_h2(h), d, __hneg2(x))));
                             };
-                            times(ph[mt].x, pl[mt].x, d0, hi.x, lo.x);
-                            times(ph[mt].y, pl[mt].y, d0, hi.y, lo.y);
-                            times(ph[mt].z, pl[mt].z, d1, hi.z, lo.z);
-                            times(ph[mt].w, pl[mt].w, d1, hi.w, lo.w);
+                            if (PACK) {
+                                times(ph[mt].x, ph[mt].y, d0, hi.x, hi.y);
+                                times(ph[mt].z, ph[mt].w, d1, hi.z, hi.w);
+                            } else {
+                                times(ph[mt].x, pl[mt].x, d0, hi.x, lo.x);
+                                times(ph[mt].y, pl[mt].y, d0, hi.y, lo.y);
+                                times(ph[mt].z, pl[mt].z, d1, hi.z, lo.z);
+                                times(ph[mt].w, pl[mt].w, d1, hi.w, lo.w);
+                            }
 #pragma unroll
                             for (int t = 0; t < 4; t++) {
                                 mma16(o[mt][4 * b + t], hi, vw[t][0], vw[t][1]);
-                                mma16(o[mt][4 * b + t], lo, vw[t][0], vw[t][1]);
+                                if (!PACK) mma16(o[mt][4 * b + t], lo, vw[t][0], vw[t][1]);
                             }
                         }
                     }
@@ -705,14 +732,14 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT>::NW * 32, 1) attn_tree_ke
 #pragma unroll
                     for (int mt = 0; mt < MT; mt++)
 #pragma unroll
-                        for (int h = 0; h < 2; h++) {
+                        for (int h = 0; h < NH; h++) {
                             const float p = __shfl_sync(0xffffffffu, (k & 1) ? s[mt][t8][2 * h + 1] : s[mt][t8][2 * h], src);
                             if (!(see[mt][h] >> key & 1)) continue;
 #pragma unroll
                             for (int t = 0; t < NT; t++)
 #pragma unroll
                                 for (int i = 0; i < 2; i++) {
-                                    const float v = stage_value<TYPE, D, MT>(base, key, C::odim(t, 2 * c + i));
+                                    const float v = stage_value<TYPE, D, MT_>(base, key, C::odim(t, 2 * c + i));
                                     if (!(fabsf(v) < CUDART_INF_F)) o[mt][t][2 * h + i] += p * (v * scale);
                                 }
                         }
@@ -723,14 +750,17 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT>::NW * 32, 1) attn_tree_ke
     cp_wait<0>();
     __syncthreads();
 
+    if (PACK)
+#pragma unroll
+        for (int t = 0; t < NT; t++) o[0][t][0] += o[0][t][2], o[0][t][1] += o[0][t][3];
     // ---- join the warps: [warp][row][D] outputs, then [warp][row] (m, l)
-    float* so = reinterpret_cast<float*>(smem + tree_q_bytes<TYPE, D, MT>());
+    float* so = reinterpret_cast<float*>(smem + tree_q_bytes<TYPE, D, MT_>());
     float2* sml = reinterpret_cast<float2*>(so + NW * ROWS * C::DP);
     const float back = C::QUANT ? 1.f / vinv : 1.f;
 #pragma unroll
     for (int mt = 0; mt < MT; mt++)
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
+        for (int h = 0; h < NH; h++) {
             const int r = mt * 16 + h * 8 + j;
             float x = l[mt][h];
             x += __shfl_xor_sync(0xffffffffu, x, 1);
@@ -831,8 +861,8 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(TreeArgs a, int splits)
         make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
 }
 
-// The tcgen05 kernel, or this file's over row tiles of 32 (16 where there are no more) and so many splits that they fill
-// the SMs, as long as every warp has a stage.
+// The tcgen05 kernel, or this file's with one row tile of 8, 16 or 32 and so many splits that they fill the SMs, as long as
+// every warp has a stage.
 struct TreePlan {
     TreeTcPlan tc;
     int mt = 1, splits = 1;
@@ -840,13 +870,13 @@ struct TreePlan {
 
 TreePlan tree_plan(int H, int KVH, int D, int type, int past, int n) {
     TreePlan p;
-    p.tc = tree_tc_plan(H, KVH, past, n);
+    p.tc = tree_tc_plan(H, KVH, type, past, n);
     p.splits = p.tc.splits;
     if (p.splits) return p;
     const int R = n * (H / KVH);
-    p.mt = R > 16 ? 2 : 1;
+    p.mt = R > 16 ? 2 : R > 8 ? 1 : 0;
     const int ks = tree_stage(type, p.mt), nw = tree_warps(type, D, p.mt);
-    const int64_t tiles = (int64_t)KVH * ((R + 16 * p.mt - 1) / (16 * p.mt));
+    const int64_t tiles = KVH;  // (one row tile)
     const int stages = (past + n + ks - 1) / ks;
     int64_t s = num_sms() / tiles;
     s = std::min<int64_t>(s, (stages + nw - 1) / nw);
@@ -862,8 +892,8 @@ cudaError_t go(const TreeArgs& a, const TreePlan& p, cudaStream_t s) {
     cudaError_t e = opt((const void*)k, smem);
     if (e) return e;
     const int R = a.n * (a.H / a.c.KVH);
-    return launch_chained(k, dim3(p.splits, a.c.KVH, (R + 16 * MT - 1) / (16 * MT)), TreeCfg<TYPE, D, MT>::NW * 32, smem, s, a,
-                          p.splits);
+    constexpr int rows = TreeCfg<TYPE, D, MT>::ROWS;
+    return launch_chained(k, dim3(p.splits, a.c.KVH, (R + rows - 1) / rows), TreeCfg<TYPE, D, MT>::NW * 32, smem, s, a, p.splits);
 }
 
 template <int TYPE>
@@ -873,9 +903,9 @@ cudaError_t go_type(const TreeArgs& a, cudaStream_t s) {
     if (p.tc.splits)
         e = launch_attn_tree_tc(a, p.tc, s);
     else if (a.c.D == 64)
-        e = p.mt == 1 ? go<TYPE, 64, 1>(a, p, s) : go<TYPE, 64, 2>(a, p, s);
+        e = p.mt == 0 ? go<TYPE, 64, 0>(a, p, s) : p.mt == 1 ? go<TYPE, 64, 1>(a, p, s) : go<TYPE, 64, 2>(a, p, s);
     else
-        e = p.mt == 1 ? go<TYPE, 128, 1>(a, p, s) : go<TYPE, 128, 2>(a, p, s);
+        e = p.mt == 0 ? go<TYPE, 128, 0>(a, p, s) : p.mt == 1 ? go<TYPE, 128, 1>(a, p, s) : go<TYPE, 128, 2>(a, p, s);
     if (e || p.splits == 1) return e;
     const dim3 grid((a.H * a.n + 7) / 8);
     return a.c.D == 64 ? launch_chained(tree_merge_kernel<64>, grid, 256, 0, s, a, p.splits)

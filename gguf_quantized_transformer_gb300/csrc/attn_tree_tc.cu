@@ -20,7 +20,7 @@
 //                 over 30720 fp32 slots; the warp's loads of several tiles share its few scoreboards.)
 // Warps 0-7 are the softmax: a thread owns a row and 32 of a tile's slots (its scores in registers: maximum, p, sum), the
 // two of a row exchange their maxima tile by tile.  (One thread for all 64 slots was the longest chain of the pipeline:
-// some 500 instructions a tile and a warp beside eight converting warps, TBD.)  One warp issues the MMAs, scores of up to
+// some 500 instructions a tile and a warp beside eight converting warps: 25 nodes over 30011 Q8_0 slots 50.3 us, 47.5 so.)  One warp issues the MMAs, scores of up to
 // three tiles ahead of the outputs, so the tensor pipe always has a queue.
 // The reference maximum moves lazily, as in attn_tree.cu, with the same factor 2^8 in p.
 // Tiles that hold nodes (the last ones): a hidden slot's score is -inf by a select; non-finite keys and values and the
@@ -859,14 +859,17 @@ cudaError_t go_type(const TreeArgs& a, const TreeTcPlan& p, cudaStream_t s) {
 
 }  // namespace
 
-TreeTcPlan tree_tc_plan(int H, int KVH, int past, int n) {
+TreeTcPlan tree_tc_plan(int H, int KVH, int type, int past, int n) {
     TreeTcPlan p;
     const int R = n * (H / KVH);
-    if (R <= 32) return p;
+    // More than 32 rows; of fp32 caches, whose mma.sync kernel needs three tf32 products, more than 16 over a long past
+    // (32 rows over 4000 slots: 29 us there, 21 here; over 1000: 15.2 there, 16.5 here).
+    if (R <= (type == AF_F32 && past + n >= 2048 ? 16 : 32)) return p;
     p.tiles = (past + n + BK - 1) / BK;
     const int64_t ctas = (int64_t)KVH * ((R + kRows - 1) / kRows);
-    // one CTA per SM; at least four tiles each
-    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(num_sms() / ctas, p.tiles / 4));
+    // one CTA per SM, two tiles each or more (64 nodes over 448 fp16 slots: 12.1 us, 13.6 with four), but a few tiles are
+    // quicker than a merge (over 192: 10.4 us in one split, 12.0 in two)
+    p.splits = p.tiles <= 4 ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(num_sms() / ctas, p.tiles / 2));
     return p;
 }
 
