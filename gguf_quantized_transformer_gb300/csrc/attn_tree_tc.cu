@@ -4,10 +4,15 @@
 // CTA (split, kv head g, row tile): 128 rows (row = node G + head of the group) are the 128 TMEM lanes.  With
 // everything that belongs to a row in tensor memory (q, scores, p and the output: 512 columns), shared memory holds
 // only K and V operands, and an MMA reads nothing else from it:
-//   columns [0, D)            output accumulator, fp32
-//   columns [128, 128 + D)    q, scaled by log2 e / sqrt(D) and a power of two per row, as fp16 hi and lo parts
-//   columns [256 + 64 b, ..)  b < 4: scores of a tile (64 fp32 columns), overwritten, 32 slots by 32, by p's fp16 hi
-//                             and lo parts (16 columns each)
+//   columns [0, D)          output accumulator of up to kFlush tiles, fp32
+//   columns [D, 2 D)        the output of the tiles before them
+//   columns [2 D, 3 D)      q, scaled by log2 e / sqrt(D) and a power of two per row, as fp16 hi and lo parts
+//   columns [3 D + 64 b..)  scores of a tile (64 fp32 columns, b < 2 or, with D = 64, 4), overwritten, 32 slots by 32, by
+//                           p's fp16 hi and lo parts (16 columns each)
+// The tensor cores' fp32 sums are cut, not rounded: every product added to a sum takes up to 2^-23 of it, always towards
+// zero.  So the small lo products come first, before the sum has its size, and the output is added to the older tiles'
+// by the softmax warps, rounded, every kFlush tiles (64 nodes over 30720 fp32 slots were off by 1.3e-5 of the result's
+// norm with one sum of 53 tiles, 1.2e-6 so, in the same time).
 // Both products take their A operand (q, p) from tensor memory and B from shared memory: K rows [slot][dim] are
 // K-major, V rows [slot][dim] MN-major, so neither is transposed and both have the cache's own order:
 //   fp16 cache    TMA copies 64 slots x 64 dims boxes into the SWIZZLE_128B layout; two products (hi, lo of q or p)
@@ -38,8 +43,8 @@ namespace af {
 namespace {
 
 constexpr int BK = 64;         // slots per tile
-constexpr int kAhead = 3;      // tiles whose scores are issued ahead of the outputs
-constexpr int kQCol = 128, kSCol = 256, kTmem = 512;
+constexpr int kFlush = 4;      // tiles of one output sum
+constexpr int kTmem = 512;
 constexpr int kRows = 128;
 constexpr float kLazy2 = 4.f, kBias2 = 8.f;  // as attn_tree.cu's
 constexpr int kConvWarps = 4;  // for K, and as many for V: 16 slots of a tile each
@@ -49,14 +54,18 @@ constexpr int kSoftWarps = 8;  // two per 32 rows
 template <int TYPE, int D>
 struct TcCfgT {
     static constexpr bool SPLIT = TYPE != AF_F16;
+    static constexpr int ACC = D, QCOL = 2 * D, SCOL = 3 * D;    // tensor memory columns
+    static constexpr int SB = D == 128 ? 2 : 4;               // score buffers (what is left of tensor memory)
+    static constexpr int AHEAD = D == 128 ? 2 : 3;            // tiles whose scores are issued ahead of the outputs
+    static_assert(SCOL + SB * BK <= kTmem, "tensor memory");
     static constexpr int PART = BK * D * 2;                  // one fp16 operand of a tile
     static constexpr int SLOT = PART * (SPLIT ? 2 : 1);      // hi (and lo)
     static constexpr int NS = SPLIT ? (D == 128 ? 2 : 4) : 6;  // operand slots of K, and of V
     // staging of raw rows: RR rows a slot, NR slots for K and for V
     static constexpr int RB = TYPE == AF_F32 ? 4 * D : TYPE == AF_KV_Q8_0 ? D : D / 2;
-    static constexpr int SB = TYPE == AF_F32 ? 0 : D / 16;   // scale bytes of a row
+    static constexpr int SCB = TYPE == AF_F32 ? 0 : D / 16;  // scale bytes of a row
     static constexpr int RR = TYPE == AF_F32 ? BK / 2 : BK, RU = RR / 16;  // (the rows of RU warps)
-    static constexpr int RAW = RR * (RB + SB);
+    static constexpr int RAW = RR * (RB + SCB);
     static constexpr int NR = !SPLIT ? 0 : TYPE == AF_F32 ? (D == 128 ? 3 : 6) : 5;
     static constexpr int OFF_V = NS * SLOT, OFF_RAW = 2 * NS * SLOT;
     static constexpr int QS = kRows * D * 4 / SLOT;          // the last V slots, through which q and the output pass
@@ -114,6 +123,16 @@ __device__ __forceinline__ bool twait1(uint64_t* bar, unsigned parity, TcState& 
     return false;
 }
 
+// Whether the phase is complete, without waiting at all (a try_wait may suspend the warp for thousands of cycles).
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, unsigned parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(smem_u32(bar)), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
+
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
@@ -139,6 +158,20 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t chunk) {
     return d;
 }
 
+// Whole warp: 16 columns of 32 lanes, waited for
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; i++) v[i] = __uint_as_float(r[i]);
+}
 // Whole warp: 16 columns of 32 lanes (waited for with tmem_st_wait)
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
     asm volatile(
@@ -342,7 +375,7 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                 mbar_init(&sm.empty[x][i], 1);
             }
             for (int i = 0; i < C::NR; i++) {
-                mbar_init(&sm.raw_full[x][i], C::SB ? 33 : 1);  // the copy's bytes, and each lane's scales
+                mbar_init(&sm.raw_full[x][i], C::SCB ? 33 : 1);  // the copy's bytes, and each lane's scales
                 mbar_init(&sm.raw_empty[x][i], kConvWarps);
             }
             sm.copies[x] = 0;
@@ -374,83 +407,92 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
         const uint32_t sbase = smem_u32(smem);
         const uint64_t kd0 = umma_desc_sw128(sbase), vd0 = desc_mn(sbase + C::OFF_V, BK * 128);
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        constexpr int SB = C::SB;
         Ring<C::NS> rk, rv;
         bool ok = twait(&sm.q_ready, 0, sm);
         tc_fence_after();
         // A step's barriers are looked at while the previous step is being issued (the pipe is busy with it); only if
         // they were not all complete is there a wait.
         auto scores_ready = [&](int t) {
-            return (t < 4 || mbar_try_wait(&sm.pv_done[t & 3], ((t - 4) >> 2) & 1)) && mbar_try_wait(&sm.full[0][rk.i], rk.ph);
+            return (t < SB || mbar_test(&sm.pv_done[t % SB], (t / SB - 1) & 1)) && mbar_test(&sm.full[0][rk.i], rk.ph);
         };
         auto scores_wait = [&](int t) {
-            return (t < 4 || twait(&sm.pv_done[t & 3], ((t - 4) >> 2) & 1, sm)) && twait(&sm.full[0][rk.i], rk.ph, sm);
+            return (t < SB || twait(&sm.pv_done[t % SB], (t / SB - 1) & 1, sm)) && twait(&sm.full[0][rk.i], rk.ph, sm);
         };
         auto out_ready = [&](int t) {
-            return mbar_try_wait(&sm.full[1][rv.i], rv.ph) && mbar_try_wait(&sm.p_full[t & 3], (t >> 2) & 1);
+            return mbar_test(&sm.full[1][rv.i], rv.ph) && mbar_test(&sm.p_full[t % SB], (t / SB) & 1);
         };
-        auto out_wait = [&](int t) { return twait(&sm.full[1][rv.i], rv.ph, sm) && twait(&sm.p_full[t & 3], (t >> 2) & 1, sm); };
+        auto out_wait = [&](int t) { return twait(&sm.full[1][rv.i], rv.ph, sm) && twait(&sm.p_full[t % SB], (t / SB) & 1, sm); };
         auto scores = [&](int t, int from, int to) {
             if (!lead) return;
             const uint64_t kd = kd0 + (uint32_t)(rk.i * (C::SLOT >> 4));
-            const uint32_t d = tm + kSCol + (t & 3) * BK;
+            const uint32_t d = tm + C::SCOL + t % SB * BK;
 #pragma unroll
-            for (int kk = from; kk < to; kk++) {
+            for (int i = from; i < to; i++) {  // steps of lo products, then of hi products
+                const int kk = i % (D / 16);
                 const uint64_t b = kd + (((kk >> 2) * BK * 128 + (kk & 3) * 32) >> 4);
-                mma_f16_ts(d, tm + kQCol + kk * 8, b, kIdS, kk > 0);
-                mma_f16_ts(d, tm + kQCol + D / 2 + kk * 8, b, kIdS, 1);
-                if (C::SPLIT) mma_f16_ts(d, tm + kQCol + kk * 8, b + (C::PART >> 4), kIdS, 1);
+                if (i < D / 16) {
+                    mma_f16_ts(d, tm + C::QCOL + D / 2 + kk * 8, b, kIdS, kk > 0);
+                    if (C::SPLIT) mma_f16_ts(d, tm + C::QCOL + kk * 8, b + (C::PART >> 4), kIdS, 1);
+                } else {
+                    mma_f16_ts(d, tm + C::QCOL + kk * 8, b, kIdS, 1);
+                }
             }
-            if (to == D / 16) {
-                mma_commit(&sm.s_full[t & 3]);
+            if (to == D / 8) {
+                mma_commit(&sm.s_full[t % SB]);
                 mma_commit(&sm.empty[0][rk.i]);
-                if (C::SPLIT) mbar_arrive(&sm.s_full[t & 3]);
+                if (C::SPLIT) mbar_arrive(&sm.s_full[t % SB]);
             }
         };
         auto out = [&](int t, int from, int to) {
             if (!lead) return;
             const uint64_t vd = vd0 + (uint32_t)(rv.i * (C::SLOT >> 4));
-            const uint32_t p = tm + kSCol + (t & 3) * BK;
+            const uint32_t p = tm + C::SCOL + t % SB * BK;
 #pragma unroll
-            for (int kk = from; kk < to; kk++) {
+            for (int i = from; i < to; i++) {
+                const int kk = i % (BK / 16);
                 const uint64_t b = vd + ((kk * 2048) >> 4);
                 const uint32_t hi = p + (kk >> 1) * 32 + (kk & 1) * 8, lo = hi + 16;
-                mma_f16_ts(tm, hi, b, kIdO, t > 0 || kk > 0);
-                mma_f16_ts(tm, lo, b, kIdO, 1);
-                if (C::SPLIT) mma_f16_ts(tm, hi, b + (C::PART >> 4), kIdO, 1);
+                if (i < BK / 16) {
+                    mma_f16_ts(tm, lo, b, kIdO, t % kFlush > 0 || kk > 0);
+                    if (C::SPLIT) mma_f16_ts(tm, hi, b + (C::PART >> 4), kIdO, 1);
+                } else {
+                    mma_f16_ts(tm, hi, b, kIdO, 1);
+                }
             }
-            if (to == BK / 16) {
-                mma_commit(&sm.pv_done[t & 3]);
+            if (to == BK / 8) {
+                mma_commit(&sm.pv_done[t % SB]);
                 mma_commit(&sm.empty[1][rv.i]);
             }
         };
-        for (int t = 0; ok && t < min(kAhead, T); t++) {
+        for (int t = 0; ok && t < min(C::AHEAD, T); t++) {
             ok = scores_wait(t);
             if (!ok) break;
             tc_fence_after();
-            scores(t, 0, D / 16);
+            scores(t, 0, D / 8);
             __syncwarp();
             rk.next();
         }
         bool next = false;  // the next step's barriers have been seen complete
         for (int t = 0; ok && t < T; t++) {
-            const bool more = t + kAhead < T;
+            const bool more = t + C::AHEAD < T;
             ok = next || out_wait(t);
             if (!ok) break;
             tc_fence_after();
-            out(t, 0, BK / 16 - 1);
+            out(t, 0, BK / 8 - 2);
             __syncwarp();
-            next = more && __all_sync(0xffffffffu, scores_ready(t + kAhead));
-            out(t, BK / 16 - 1, BK / 16);
+            next = more && __all_sync(0xffffffffu, scores_ready(t + C::AHEAD));
+            out(t, BK / 8 - 2, BK / 8);
             __syncwarp();
             rv.next();
             if (more) {
-                ok = next || scores_wait(t + kAhead);
+                ok = next || scores_wait(t + C::AHEAD);
                 if (!ok) break;
                 tc_fence_after();
-                scores(t + kAhead, 0, D / 16 - 2);
+                scores(t + C::AHEAD, 0, D / 8 - 4);
                 __syncwarp();
                 next = __all_sync(0xffffffffu, out_ready(t + 1));
-                scores(t + kAhead, D / 16 - 2, D / 16);
+                scores(t + C::AHEAD, D / 8 - 4, D / 8);
                 __syncwarp();
                 rk.next();
             } else {
@@ -477,7 +519,7 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
         } else {
             // ---------------- raw rows into the staging ring: one bulk copy, and the scales by the lanes
             const uint8_t* src = (const uint8_t*)(x ? a.c.v : a.c.k) + row0 * C::RB;
-            const uint8_t* sc = (const uint8_t*)(x ? a.c.vs : a.c.ks) + row0 * C::SB;
+            const uint8_t* sc = (const uint8_t*)(x ? a.c.vs : a.c.ks) + row0 * C::SCB;
             Ring<C::NR> r;
             for (int i = 0; i < T * (BK / C::RR); i++, r.next()) {
                 if (i >= C::NR && !twait(&sm.raw_empty[x][r.i], r.ph ^ 1, sm)) break;
@@ -488,8 +530,8 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                     if (rows) bulk_g2s(dst, src + (int64_t)i * C::RR * C::RB, rows * C::RB, &sm.raw_full[x][r.i]);
                     sm.copies[x] = i + 1;
                 }
-                if (C::SB) {  // rows may start off 16 bytes: 8- or 4-byte copies
-                    constexpr int B = C::SB ? C::SB : 4;
+                if (C::SCB) {  // rows may start off 16 bytes: 8- or 4-byte copies
+                    constexpr int B = C::SCB ? C::SCB : 4;
 #pragma unroll
                     for (int k = 0; k < C::RR; k += 32) {
                         const bool in = k + lane < rows;
@@ -529,7 +571,7 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                 if (!ok) break;
                 const uint8_t* st = smem + C::OFF_RAW + (x * C::NR + mine) * C::RAW;
                 const int wr = (w % C::RU) * 16;  // the warp's rows in the slot
-                const uint8_t *rows = st + wr * C::RB, *scales = st + C::RR * C::RB + wr * C::SB;
+                const uint8_t *rows = st + wr * C::RB, *scales = st + C::RR * C::RB + wr * C::SCB;
                 const int left = t >= tn ? valid - t * BK - w * 16 : 16;  // the warp's rows that hold slots
                 unsigned bad = 0;
                 float m = 0.f;
@@ -619,8 +661,8 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                     split2(live ? make_float2(y.x * sc * k, y.y * sc * k) : both(0.f), hi[2 * i], lo[2 * i]);
                     split2(live ? make_float2(y.z * sc * k, y.w * sc * k) : both(0.f), hi[2 * i + 1], lo[2 * i + 1]);
                 }
-                tmem_st16(lane_addr + kQCol + h * 16, hi);
-                tmem_st16(lane_addr + kQCol + D / 2 + h * 16, lo);
+                tmem_st16(lane_addr + C::QCOL + h * 16, hi);
+                tmem_st16(lane_addr + C::QCOL + D / 2 + h * 16, lo);
             }
             tmem_st_wait();
             tc_fence_before();
@@ -642,10 +684,11 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
         int ev_ref = kNoExp;
         Ring<C::NS> rv;
         for (int t = 0; ok && t < T; t++, rv.next()) {
-            const int b = t & 3;
+            const int b = t % C::SB;
+            const unsigned ph = (t / C::SB) & 1;
             const bool nodes = t >= tn;
             const unsigned see = nodes ? window((t0 + t) * BK - a.past + half * 32) : ~0u;
-            ok = twait(&sm.s_full[b], (t >> 2) & 1, sm);
+            ok = twait(&sm.s_full[b], ph, sm);
             if (!ok) break;
             float f[NG];
             int ev[NG] = {}, ev_max = kNoExp;
@@ -691,7 +734,7 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                 if (!ok) break;
             }
             tc_fence_after();
-            const uint32_t s_addr = lane_addr + kSCol + b * BK + half * 32;
+            const uint32_t s_addr = lane_addr + C::SCOL + b * BK + half * 32;
             float s[32];
             tmem_ld32(s_addr, s);
             if (nodes) {
@@ -719,29 +762,45 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
             mt = fmaxf(mt, sm.pair_x[t & 1][quad][half ^ 1][lane]);
             const bool move = mt > m_ref + kLazy2;
             const bool grow = C::SPLIT && ev_max > ev_ref + 2;
-            if (__any_sync(0xffffffffu, move || grow)) {  // the same in both warps
+            const bool flush = t > 0 && t % kFlush == 0;  // the output sum starts again with this tile
+            const bool change = __any_sync(0xffffffffu, move || grow);  // (the same in both warps)
+            if (change || flush) {
                 float up = 1.f;
-                if (mt > m_ref) {
-                    up = ex2u(m_ref - mt);
-                    m_ref = mt;
-                    l *= up;
+                if (change) {
+                    if (mt > m_ref) {
+                        up = ex2u(m_ref - mt);
+                        m_ref = mt;
+                        l *= up;
+                    }
+                    if (grow) {
+                        up *= ex2u((float)(ev_ref - ev_max));
+                        ev_ref = ev_max;
+                    }
                 }
-                if (grow) {
-                    up *= ex2u((float)(ev_ref - ev_max));
-                    ev_ref = ev_max;
-                }
-                if (t > 0) {  // the output holds the tiles before t: wait for them, rescale these rows, half of the dims each
-                    ok = twait(&sm.pv_done[(t - 1) & 3], ((t - 1) >> 2) & 1, sm);
+                if (t > 0) {  // the output holds the tiles before t: wait for them; half of the dims each
+                    ok = twait(&sm.pv_done[(t - 1) % C::SB], ((t - 1) / C::SB) & 1, sm);
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
-                        float o[32];
-                        uint32_t u[32];
-                        tmem_ld32(lane_addr + c, o);
+                    for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
+                        float o[16], acc[16];
+                        uint32_t u[16];
+                        if (t > kFlush) tmem_ld16(lane_addr + C::ACC + c, acc);
+                        tmem_ld16(lane_addr + c, o);
+                        if (flush) {
 #pragma unroll
-                        for (int i = 0; i < 32; i++) u[i] = __float_as_uint(o[i] * up);
-                        tmem_st32(lane_addr + c, u);
+                            for (int i = 0; i < 16; i++) u[i] = __float_as_uint((t > kFlush ? acc[i] + o[i] : o[i]) * up);
+                            tmem_st16(lane_addr + C::ACC + c, u);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; i++) u[i] = __float_as_uint(o[i] * up);
+                            tmem_st16(lane_addr + c, u);
+                            if (t > kFlush) {
+#pragma unroll
+                                for (int i = 0; i < 16; i++) u[i] = __float_as_uint(acc[i] * up);
+                                tmem_st16(lane_addr + C::ACC + c, u);
+                            }
+                        }
                     }
                     tmem_st_wait();
                 }
@@ -798,6 +857,12 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
             for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
                 float o[32];
                 tmem_ld32(lane_addr + c, o);
+                if (T > kFlush) {
+                    float acc[32];
+                    tmem_ld32(lane_addr + C::ACC + c, acc);
+#pragma unroll
+                    for (int i = 0; i < 32; i++) o[i] += acc[i];
+                }
 #pragma unroll
                 for (int i = 0; i < 32; i += 4)
                     *stage(st, lane, (c + i) / 4) = make_float4(o[i] * up, o[i + 1] * up, o[i + 2] * up, o[i + 3] * up);

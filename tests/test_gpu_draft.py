@@ -541,6 +541,54 @@ def test_attention_tree_repeats_captures_and_streams(af, t, past, n):
     assert torch.equal(bufs[0][2], want[0]) and torch.equal(bufs[1][2], want[1])
 
 
+@pytest.mark.parametrize("t", KV)
+@pytest.mark.parametrize("past,n", [(2000, 8), (900, 96)])
+@pytest.mark.parametrize("nstreams", [1, 2])
+def test_attention_tree_calls_in_a_row(af, t, past, n, nstreams):
+    """Calls that follow one another without a pause (a call's blocks start while the one before it ends) give the bits of
+    a call by itself."""
+    H, KVH, D = 32, 8, 128
+    rng = np.random.default_rng(17)
+    ctx = past + n
+    cache, k, v = filled(af, t, rng, KVH, D, ctx, ctx)
+    q = rng.standard_normal((n, H * D)).astype(np.float32)
+    see, _ = closure(random_parents(rng, n))
+    want = attend(af, t, cache, q, H, KVH, D, ctx, past, see)
+    need = max(256, af.af_attention_tree_workspace(af.KVTYPE[t], H, KVH, D, past, n))
+    qd, mask = _dev(q), _dev(pack(see))
+    streams = [torch.cuda.Stream() for _ in range(nstreams)]
+    ws = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in streams]
+    outs = [[torch.zeros(n, H * D, device="cuda") for _ in range(20)] for _ in streams]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for s, w, o in zip(streams, ws, outs):
+            af.af_attention_tree(qd, H * D, *cache, af.KVTYPE[t], H, KVH, D, ctx, past, n, mask, w, need, o[i], H * D, s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want) for o in outs for x in o)
+
+
+@pytest.mark.parametrize("t", KV)
+def test_attention_tree_long_sums(af, t):
+    """Over 125 tiles in one block the error does not grow with their number: the tensor cores cut their sums by up to
+    2^-23 at each of the 12 products of a tile, over 4 tiles at most; with the two-part operands, the exponential and the
+    row sum (2^-21 together, and as much for the joining of the sums) 48 * 2^-23 + 2^-20 of the result's norm."""
+    H, KVH, D, past, n = 8, 8, 128, 15500, 1000
+    rng = np.random.default_rng(18)
+    cache, k, v = filled(af, t, rng, KVH, D, past + n, past + n)
+    q = rng.standard_normal((n, H, D)).astype(np.float32)
+    see, _ = closure(random_parents(rng, n))
+    got = attend(af, t, cache, q, H, KVH, D, past + n, past, see).double().cpu().view(n, H, D)
+    seen = torch.cat((torch.ones(n, past, dtype=torch.bool), torch.from_numpy(see)), 1).cuda()
+    err = norm = 0.0
+    for h in range(H):
+        z = torch.from_numpy(q[:, h].astype(np.float64)).cuda() @ torch.from_numpy(k[h].astype(np.float64)).cuda().T * D ** -0.5
+        z = torch.softmax(torch.where(seen, z, -torch.inf), -1) @ torch.from_numpy(v[h].astype(np.float64)).cuda()
+        err += float((got[:, h].cuda() - z).square().sum())
+        norm += float(z.square().sum())
+    print(f"err {(err / norm) ** 0.5:.2e}")
+    assert (err / norm) ** 0.5 <= 48 * 2.0 ** -23 + 2.0 ** -20
+
+
 # ---------------------------------------------------------------- together
 
 @pytest.mark.parametrize("t", KV)
