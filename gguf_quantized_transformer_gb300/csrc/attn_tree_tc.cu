@@ -45,6 +45,7 @@ namespace {
 constexpr int BK = 64;         // slots per tile
 constexpr int kFlush = 4;      // tiles of one output sum
 constexpr int kTmem = 512;
+constexpr int kQueueBar = 1;   // named barrier: q has been read
 constexpr int kRows = 128;
 constexpr float kLazy2 = 4.f, kBias2 = 8.f;  // as attn_tree.cu's
 constexpr int kConvWarps = 4;  // for K, and as many for V: 16 slots of a tile each
@@ -123,6 +124,9 @@ __device__ __forceinline__ bool twait1(uint64_t* bar, unsigned parity, TcState& 
     return false;
 }
 
+// Named barrier (whole warps), `threads` in all: some arrive, the others wait for them.
+__device__ __forceinline__ void bar_arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+__device__ __forceinline__ void bar_wait(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 // Whether the phase is complete, without waiting at all (a try_wait may suspend the warp for thousands of cycles).
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, unsigned parity) {
     uint32_t ok;
@@ -367,7 +371,6 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
     // tiles from tn on hold nodes (or nothing behind them); slots from `valid` on, both counted from t0
     const int tn = a.past / BK - t0, valid = a.past + a.n - t0 * BK;
 
-    pdl_launch_dependents();
     if (tid == 0) {
         for (int x = 0; x < 2; x++) {
             for (int i = 0; i < C::NS; i++) {
@@ -398,6 +401,9 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
+    // (softmax threads) where the thread's row of q starts
+    const int qr = r0 + (warp & 3) * 32 + lane;
+    const int64_t qoff = qr < R ? (int64_t)(qr / G) * a.ldq + (int64_t)(g * G + qr % G) * D : 0;
     pdl_wait();  // q, the mask and the cache are written by earlier kernels
 
     if (warp == C::MMA_WARP) {
@@ -411,6 +417,9 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
         Ring<C::NS> rk, rv;
         bool ok = twait(&sm.q_ready, 0, sm);
         tc_fence_after();
+        // here and not at the top: the next kernel's blocks start beside the first tiles, not beside q's loads (64 nodes
+        // over 448 fp16 slots: 10.5 us, 11.0 from the top)
+        pdl_launch_dependents();
         // A step's barriers are looked at while the previous step is being issued (the pipe is busy with it); only if
         // they were not all complete is there a wait.
         auto scores_ready = [&](int t) {
@@ -502,6 +511,7 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
         if (lead) mma_commit(&sm.done);  // always: the drain waits on it
     } else if (warp >= C::COPY_WARP) {
         const int x = warp - C::COPY_WARP;  // 0: K, 1: V
+        bar_wait(kQueueBar, (kSoftWarps + 2) * 32);
         if constexpr (!C::SPLIT) {
             // ---------------- fp16: TMA straight into the operand layout
             if (lane == 0) {
@@ -631,38 +641,43 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
         uint8_t* const st = smem + C::OFF_V + (C::NS - C::QS) * C::SLOT + quad * 32 * D * 4;
         bool ok;
         {  // q: scaled to [1, 2), split, into tensor memory; each warp brings 16 rows and converts half of the dims
-            const int64_t off = live ? (int64_t)(r / G) * a.ldq + (int64_t)(g * G + r % G) * D : 0;
             const int c = lane % CPR, i0 = half * 16;
-            float4 x[16 / RPI];
 #pragma unroll
             for (int i = 0; i < 16 / RPI; i++) {
-                const int64_t o = __shfl_sync(0xffffffffu, off, i0 + i * RPI + lane / CPR);
-                x[i] = __ldcg(reinterpret_cast<const float4*>(a.q + o) + c);
+                const int rr = i0 + i * RPI + lane / CPR;
+                const int64_t o = __shfl_sync(0xffffffffu, qoff, rr);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(stage(st, rr, c))), "l"(a.q + o + c * 4) : "memory");
             }
-#pragma unroll
-            for (int i = 0; i < 16 / RPI; i++) *stage(st, i0 + i * RPI + lane / CPR, c) = x[i];
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            bar_arrive(kQueueBar, (kSoftWarps + 2) * 32);  // K's and V's copies come after q, which is waited for first
             ok = meet();
-            const float sc = live ? rsqrtf((float)D) * 1.4426950408889634f : 0.f;
+            // half of the row's dims each; what a dead row reads may be anything
+            float4 y[CPR / 2];
             float mx = 0.f;
-#pragma unroll 8
-            for (int i = 0; i < CPR; i++) {
-                const float4 y = *stage(st, lane, i);
-                mx = fmaxf(mx, fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w))));
+#pragma unroll
+            for (int i = 0; i < CPR / 2; i++) {
+                y[i] = *stage(st, lane, half * (CPR / 2) + i);
+                mx = fmaxf(mx, fmaxf(fmaxf(fabsf(y[i].x), fabsf(y[i].y)), fmaxf(fabsf(y[i].z), fabsf(y[i].w))));
             }
+            sm.pair_x[1][quad][half][lane] = mx;
+            ok = ok && meet();
+            mx = fmaxf(mx, sm.pair_x[1][quad][half ^ 1][lane]);
+            const float sc = live ? rsqrtf((float)D) * 1.4426950408889634f : 0.f;
             const int e = min(max(exponent_of(mx * sc), -100), 126);
             rowf = pow2i(e);
-            const float k = pow2i(-e);
-#pragma unroll 1
-            for (int h = half; h < D / 32; h += 2) {  // 32 dims: 16 columns of hi parts, 16 of lo parts
+            const float2 k = both(pow2i(-e)), scale = both(sc);
+#pragma unroll
+            for (int h = 0; h < D / 64; h++) {  // 32 dims: 16 columns of hi parts, 16 of lo parts
                 uint32_t hi[16], lo[16];
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
-                    const float4 y = *stage(st, lane, h * 8 + i);  // (what a dead row reads may be anything)
-                    split2(live ? make_float2(y.x * sc * k, y.y * sc * k) : both(0.f), hi[2 * i], lo[2 * i]);
-                    split2(live ? make_float2(y.z * sc * k, y.w * sc * k) : both(0.f), hi[2 * i + 1], lo[2 * i + 1]);
+                    const float4 z = y[h * 8 + i];
+                    split2(live ? mul2(mul2(make_float2(z.x, z.y), scale), k) : both(0.f), hi[2 * i], lo[2 * i]);
+                    split2(live ? mul2(mul2(make_float2(z.z, z.w), scale), k) : both(0.f), hi[2 * i + 1], lo[2 * i + 1]);
                 }
-                tmem_st16(lane_addr + C::QCOL + h * 16, hi);
-                tmem_st16(lane_addr + C::QCOL + D / 2 + h * 16, lo);
+                const int col = (half * (D / 64) + h) * 16;
+                tmem_st16(lane_addr + C::QCOL + col, hi);
+                tmem_st16(lane_addr + C::QCOL + D / 2 + col, lo);
             }
             tmem_st_wait();
             tc_fence_before();
@@ -872,11 +887,14 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                 *stage(st, lane, half * HC + c) = make_float4(CUDART_NAN_F, CUDART_NAN_F, CUDART_NAN_F, CUDART_NAN_F);
         }
         __syncwarp();
-#pragma unroll 8
-        for (int i = 0; i < 32; i += 32 / HC) {
-            const int rr = i + lane / HC, c = half * HC + lane % HC;
-            const int64_t o = __shfl_sync(0xffffffffu, off, rr);
-            if (r0 + quad * 32 + rr < R) reinterpret_cast<float4*>(base + o)[c] = *stage(st, rr, c);
+        const int c = half * HC + lane % HC;
+        int64_t o[HC];
+#pragma unroll
+        for (int i = 0; i < HC; i++) o[i] = __shfl_sync(0xffffffffu, off, i * (32 / HC) + lane / HC);
+#pragma unroll
+        for (int i = 0; i < HC; i++) {
+            const int rr = i * (32 / HC) + lane / HC;
+            if (r0 + quad * 32 + rr < R) reinterpret_cast<float4*>(base + o[i])[c] = *stage(st, rr, c);
         }
         if (live && !last && half == 0)
             reinterpret_cast<float2*>(a.ws + splits * rows * D)[row] =
