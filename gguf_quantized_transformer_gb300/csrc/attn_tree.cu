@@ -73,10 +73,6 @@ __device__ __forceinline__ float ex2t(float x) {
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool in) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
-template <int B>
-__device__ __forceinline__ void cp_small(uint32_t dst, const void* src, bool in) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(B), "r"(in ? B : 0) : "memory");
-}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() {
@@ -206,9 +202,31 @@ constexpr int tree_smem() {
     return tree_q_bytes<TYPE, D, MT>() + (ring > join ? ring : join);
 }
 
-// One stage of a warp: slots [key0, key0 + KS), of which those below `end` are read.
+// A lane's scales of a stage (slot `lane`, K and V) on their way through registers: copies of 4 or 8 bytes would go through
+// L1, which may hold what an earlier kernel of the chain has overwritten since.
+struct TreeScales {
+    uint2 k, v;
+    uint32_t dst = 0;  // 0: none
+};
 template <int TYPE, int D, int MT>
-__device__ __forceinline__ void tree_issue(const KvRows& c, int64_t row0, int key0, int end, uint32_t dst, int lane) {
+__device__ __forceinline__ void tree_put(const TreeScales& s, int lane) {
+    using C = TreeCfg<TYPE, D, MT>;
+    if (!C::QUANT || !s.dst || (C::KS < 32 && lane >= C::KS)) return;
+    const uint32_t k = s.dst + C::OKS + lane * C::SB, v = s.dst + C::OVS + lane * C::SB;
+    if (C::SB == 8) {
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(k), "r"(s.k.x), "r"(s.k.y) : "memory");
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(v), "r"(s.v.x), "r"(s.v.y) : "memory");
+    } else {
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(k), "r"(s.k.x) : "memory");
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(v), "r"(s.v.x) : "memory");
+    }
+}
+
+// One stage of a warp: slots [key0, key0 + KS), of which those below `end` are read.  The scales come back in `s`, for
+// tree_put once they are there.
+template <int TYPE, int D, int MT>
+__device__ __forceinline__ void tree_issue(const KvRows& c, int64_t row0, int key0, int end, uint32_t dst, int lane,
+                                           TreeScales& s) {
     using C = TreeCfg<TYPE, D, MT>;
     constexpr int CPR = C::RB / 16;
     const uint8_t* k = (const uint8_t*)c.k + row0 * C::RB;
@@ -222,11 +240,17 @@ __device__ __forceinline__ void tree_issue(const KvRows& c, int64_t row0, int ke
         cp16(dst + C::OV + key * C::RB + ((ch ^ C::swv(key)) << 4), v + off, in);
     }
     if (C::QUANT) {
-        if (C::KS == 32 || lane < C::KS) {
-            const bool in = key0 + lane < end;
-            const int64_t off = row0 + (in ? key0 + lane : 0);
-            cp_small<C::QUANT ? C::SB : 4>(dst + C::OKS + lane * C::SB, (const uint8_t*)c.ks + off * C::SB, in);
-            cp_small<C::QUANT ? C::SB : 4>(dst + C::OVS + lane * C::SB, (const uint8_t*)c.vs + off * C::SB, in);
+        s.dst = dst;
+        s.k = s.v = make_uint2(0u, 0u);
+        if ((C::KS == 32 || lane < C::KS) && key0 + lane < end) {
+            const int64_t off = (row0 + key0 + lane) * C::SB;
+            if (C::SB == 8) {
+                s.k = __ldcg(reinterpret_cast<const uint2*>((const uint8_t*)c.ks + off));
+                s.v = __ldcg(reinterpret_cast<const uint2*>((const uint8_t*)c.vs + off));
+            } else {
+                s.k.x = __ldcg(reinterpret_cast<const unsigned*>((const uint8_t*)c.ks + off));
+                s.v.x = __ldcg(reinterpret_cast<const unsigned*>((const uint8_t*)c.vs + off));
+            }
         }
     }
 }
@@ -285,10 +309,11 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT_>::NW * 32, 1) attn_tree_k
     pdl_launch_dependents();
     pdl_wait();  // q, the mask and the cache are written by earlier kernels
     // ---- the first stages are on their way while q is prepared
+    TreeScales first[C::NST - 1];
 #pragma unroll
     for (int i = 0; i < C::NST - 1; i++) {
         const int st = st0 + warp + i * NW;
-        if (st < st1) tree_issue<TYPE, D, MT_>(a.c, row0, st * KS, keys, ring + i * C::STAGE, lane);
+        if (st < st1) tree_issue<TYPE, D, MT_>(a.c, row0, st * KS, keys, ring + i * C::STAGE, lane, first[i]);
         cp_commit();
     }
 
@@ -385,13 +410,18 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT_>::NW * 32, 1) attn_tree_k
     float vinv = 1.f, vlim = 0.f;  // quantized: V's scales are taken times vinv, a power of two
 
     int slot = 0;
+    TreeScales scales;
+#pragma unroll
+    for (int i = 0; i < C::NST - 1; i++) tree_put<TYPE, D, MT_>(first[i], lane);
     for (int st = st0 + warp; st < st1; st += NW) {
         cp_wait<C::NST - 2>();
+        tree_put<TYPE, D, MT_>(scales, lane);  // of the stage issued last, with NST = 2 this one
         __syncwarp();  // every lane's copies of this stage have landed, and every lane is done with the previous one
         asm volatile("" ::: "memory");
         {  // the previous stage's slot takes the stage NST - 1 ahead
             const int nx = st + (C::NST - 1) * NW, ns = slot == 0 ? C::NST - 1 : slot - 1;
-            if (nx < st1) tree_issue<TYPE, D, MT_>(a.c, row0, nx * KS, keys, ring + ns * C::STAGE, lane);
+            scales.dst = 0;
+            if (nx < st1) tree_issue<TYPE, D, MT_>(a.c, row0, nx * KS, keys, ring + ns * C::STAGE, lane, scales);
             cp_commit();
         }
         const uint32_t base = ring + slot * C::STAGE;

@@ -21,12 +21,12 @@
 //                 Sixteen slots are scaled by a power of two that brings their largest value (or scale) near 1, so
 //                 fp16's range never binds: K's goes into the scores' factor; V's into p's, relative to a reference
 //                 exponent of the output, which is rescaled when the slots outgrow it.
-//                 (Rows read through registers instead, three tiles ahead: 192 us where this took 108 at 64 nodes
+//                 (Rows read through registers instead, three tiles ahead: 192 us where this took 107 at 64 nodes
 //                 over 30720 fp32 slots; the warp's loads of several tiles share its few scoreboards.)
 // Warps 0-7 are the softmax: a thread owns a row and 32 of a tile's slots (its scores in registers: maximum, p, sum), the
 // two of a row exchange their maxima tile by tile.  (One thread for all 64 slots was the longest chain of the pipeline:
-// some 500 instructions a tile and a warp beside eight converting warps: 25 nodes over 30011 Q8_0 slots 50.3 us, 47.5 so.)  One warp issues the MMAs, scores of up to
-// three tiles ahead of the outputs, so the tensor pipe always has a queue.
+// some 500 instructions a tile and a warp beside eight converting warps: 25 nodes over 30011 Q8_0 slots 50.3 us, 47.5 so.)
+// One warp issues the MMAs, scores two (D = 64: three) tiles ahead of the outputs.
 // The reference maximum moves lazily, as in attn_tree.cu, with the same factor 2^8 in p.
 // Tiles that hold nodes (the last ones): a hidden slot's score is -inf by a select; non-finite keys and values and the
 // slots behind the last node become zero operands, and a row that sees a slot so treated becomes NaN.
@@ -49,7 +49,7 @@ constexpr int kQueueBar = 1;   // named barrier: q has been read
 constexpr int kRows = 128;
 constexpr float kLazy2 = 4.f, kBias2 = 8.f;  // as attn_tree.cu's
 constexpr int kConvWarps = 4;  // for K, and as many for V: 16 slots of a tile each
-constexpr int kNoExp = -1000;
+constexpr int kNoExp = -1000, kMaxExp = 126;  // exponents of 16 slots; above: an infinity among them
 constexpr int kSoftWarps = 8;  // two per 32 rows
 
 template <int TYPE, int D>
@@ -295,12 +295,13 @@ __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<co
 __device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
 
 // The fp16 hi and lo parts of the warp's rows row0.., times 2^-e, into a slot (SWIZZLE_128B atoms of 64 dims,
-// [64 slots][128 B] each).
+// [64 slots][128 B] each).  Rows with an infinity, which every row of q sees (others are taken out), become NaN: at its
+// exponent the finite ones would vanish.
 template <int TYPE, int D, bool NODES>
 __device__ __forceinline__ void store_tile(uint8_t* dst, const uint8_t* st, const uint8_t* sc, int e, int row0, int valid, int lane,
                                            const Kept<TYPE, D>& kept) {
     constexpr int PPR = D / Raw<TYPE>::VALUES, PART = BK * D * 2;  // pieces per row
-    const float down = pow2i(-e);
+    const float down = e > kMaxExp ? CUDART_NAN_F : pow2i(-e);
 #pragma unroll
     for (int i = 0; i < raw_pieces<TYPE, D>(); i++) {
         unsigned bad = 0;
@@ -531,7 +532,27 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
             const uint8_t* src = (const uint8_t*)(x ? a.c.v : a.c.k) + row0 * C::RB;
             const uint8_t* sc = (const uint8_t*)(x ? a.c.vs : a.c.ks) + row0 * C::SCB;
             Ring<C::NR> r;
-            for (int i = 0; i < T * (BK / C::RR); i++, r.next()) {
+            // The scales go through registers, a slot ahead: copies of 4 or 8 bytes (rows may start off 16) would go
+            // through L1, which may hold what an earlier kernel of the chain has overwritten since.
+            constexpr int NS = C::SCB ? C::RR / 32 : 1;
+            uint2 scale[NS] = {};
+            auto fetch = [&](int i) {
+                if (C::SCB == 0) return;
+#pragma unroll
+                for (int k = 0; k < NS; k++) {
+                    const uint8_t* p = sc + ((int64_t)i * C::RR + k * 32 + lane) * C::SCB;
+                    scale[k] = make_uint2(0u, 0u);
+                    if (i * C::RR + k * 32 + lane < valid) {
+                        if (C::SCB == 8)
+                            scale[k] = __ldcg(reinterpret_cast<const uint2*>(p));
+                        else
+                            scale[k].x = __ldcg(reinterpret_cast<const unsigned*>(p));
+                    }
+                }
+            };
+            const int slots = T * (BK / C::RR);
+            fetch(0);
+            for (int i = 0; i < slots; i++, r.next()) {
                 if (i >= C::NR && !twait(&sm.raw_empty[x][r.i], r.ph ^ 1, sm)) break;
                 uint8_t* dst = smem + C::OFF_RAW + (x * C::NR + r.i) * C::RAW;
                 const int rows = min(C::RR, max(0, valid - i * C::RR));
@@ -540,20 +561,19 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                     if (rows) bulk_g2s(dst, src + (int64_t)i * C::RR * C::RB, rows * C::RB, &sm.raw_full[x][r.i]);
                     sm.copies[x] = i + 1;
                 }
-                if (C::SCB) {  // rows may start off 16 bytes: 8- or 4-byte copies
-                    constexpr int B = C::SCB ? C::SCB : 4;
+                if (C::SCB) {
 #pragma unroll
-                    for (int k = 0; k < C::RR; k += 32) {
-                        const bool in = k + lane < rows;
-                        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst) + C::RR * C::RB + (k + lane) * B),
-                                     "l"(in ? sc + ((int64_t)i * C::RR + k + lane) * B : sc), "n"(B), "r"(in ? B : 0)
-                                     : "memory");
+                    for (int k = 0; k < NS; k++) {
+                        uint8_t* p = dst + C::RR * C::RB + (k * 32 + lane) * C::SCB;
+                        if (C::SCB == 8)
+                            *reinterpret_cast<uint2*>(p) = scale[k];
+                        else
+                            *reinterpret_cast<unsigned*>(p) = scale[k].x;
                     }
-                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sm.raw_full[x][r.i]))
-                                 : "memory");
+                    mbar_arrive(&sm.raw_full[x][r.i]);
+                    if (i + 1 < slots) fetch(i + 1);
                 }
             }
-            asm volatile("cp.async.wait_all;" ::: "memory");
         }
     } else if (warp >= kSoftWarps) {
         if constexpr (C::SPLIT) {
@@ -595,9 +615,10 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                 if (bad) atomicOr(&sm.bad[t - tn], (unsigned long long)bad << (w * 16));
                 // largest value in [1, 2), or largest scale times its largest code in [1, 4)
                 int e = max(exponent_of(m), -126);
+                const bool inf = e == 128;
                 if (TYPE == AF_KV_Q8_0) e += 6;
                 if (TYPE == AF_KV_Q4_0) e += 2;
-                e = min(e, 126);
+                e = inf ? kMaxExp + 1 : min(e, kMaxExp);
                 if (t >= C::NS) ok = twait(&sm.empty[x][ro.i], ro.ph ^ 1, sm);
                 if (x == 1 && t == C::NS - C::QS) ok = ok && twait(&sm.q_ready, 0, sm);
                 if (!ok) break;
@@ -610,9 +631,9 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                 if (TYPE != AF_F32 && lane == 0) mbar_arrive(&sm.raw_empty[x][mine]);
                 if (lane == 0) {
                     if (x == 1)
-                        sm.ev[t & 7][w] = m == 0.f ? kNoExp : e;
+                        sm.ev[t & 7][w] = m == 0.f ? kNoExp : min(e, kMaxExp);
                     else
-                        sm.ek[t & 7][w] = pow2i(e);
+                        sm.ek[t & 7][w] = pow2i(min(e, kMaxExp));
                 }
                 fence_proxy_async_shared();
                 __syncwarp();

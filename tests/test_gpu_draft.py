@@ -457,6 +457,36 @@ def test_attention_tree_hidden_slots_reach_no_row(af, t, what, past, n):
     assert not np.array_equal(got[7], clean[7])
 
 
+@pytest.mark.parametrize("t,what", [("f32", "k"), ("f16", "k"), ("f32", "v"), ("f16", "v"), ("q8_0", "v"), ("q4_0", "v")])
+@pytest.mark.parametrize("n", [3, 24, 70])
+def test_attention_tree_infinities_in_the_past(af, t, what, n):
+    """An infinite key, value or value's scale among the slots that every row sees: a result is what the definition gives
+    or not finite, never a finite number that left slots out."""
+    H, KVH, D, past = 8, 2, 128, 300
+    rng = np.random.default_rng(19)
+    cache, k, v = filled(af, t, rng, KVH, D, past + n, past + n)
+    q = rng.standard_normal((n, H, D)).astype(np.float32)
+    see, _ = closure(random_parents(rng, n))
+    tol = attn_tol(q, k, v)
+    ki, ksi, vi, vsi = cache
+    x, scales = (ki, ksi) if what == "k" else (vi, vsi)
+    if t in ("f32", "f16"):
+        x.view(torch.float32 if t == "f32" else torch.float16).view(KVH, past + n, D)[:, 37, 40] = float("inf")
+    else:
+        scales.view(torch.float16).view(KVH, past + n, D // 32)[:, 37, 1] = float("inf")
+    got = attend(af, t, cache, q, H, KVH, D, past + n, past, see).cpu().numpy().astype(np.float64).reshape(n, H, D)
+    if what == "k":
+        k = k.copy()
+        k[:, 37, 40] = np.inf
+    else:
+        assert not np.isfinite(got[:, :, 40]).any()
+    with np.errstate(invalid="ignore"):
+        ref = attn_ref(q.astype(np.float64), k, v, see, past)
+    assert not np.isfinite(got[~np.isfinite(ref)]).any()
+    fine = np.isfinite(got)
+    assert np.abs(got - ref)[fine].max(initial=0) <= tol
+
+
 @pytest.mark.parametrize("t", KV)
 def test_attention_tree_wide_scores_and_small_values(af, t):
     """Scores far apart (one slot takes nearly all the weight), and values whose sizes differ by blocks and slots."""
@@ -565,6 +595,38 @@ def test_attention_tree_calls_in_a_row(af, t, past, n, nstreams):
             af.af_attention_tree(qd, H * D, *cache, af.KVTYPE[t], H, KVH, D, ctx, past, n, mask, w, need, o[i], H * D, s)
     torch.cuda.synchronize()
     assert all(torch.equal(x, want) for o in outs for x in o)
+
+
+@pytest.mark.parametrize("t", KV)
+@pytest.mark.parametrize("past,n", [(500, 8), (60, 64)])
+def test_attention_tree_sees_rows_written_just_before(af, t, past, n):
+    """Writes and attention in turn, without a pause between them: each attention sees the rows written before it, and no
+    older ones that an SM still holds."""
+    H, KVH, D = 32, 8, 128
+    rng = np.random.default_rng(20)
+    ctx = past + n + 3
+    cache, _, _ = filled(af, t, rng, KVH, D, ctx, past + n)
+    rows = [_dev((rng.standard_normal((n, KVH * D)) * 4.0 ** i).astype(np.float32)) for i in range(3)]
+    q = _dev(rng.standard_normal((n, H * D)).astype(np.float32))
+    see, _ = closure(random_parents(rng, n))
+    mask = _dev(pack(see))
+    need = max(256, af.af_attention_tree_workspace(af.KVTYPE[t], H, KVH, D, past, n))
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+
+    def step(i, out):
+        write(af, t, cache, rows[i], rows[i], KVH, D, ctx, slot0=past)
+        af.af_attention_tree(q, H * D, *cache, af.KVTYPE[t], H, KVH, D, ctx, past, n, mask, ws, need, out, H * D)
+
+    want = [torch.zeros(n, H * D, device="cuda") for _ in rows]
+    for i, out in enumerate(want):
+        torch.cuda.synchronize()
+        step(i, out)
+    outs = [torch.zeros(n, H * D, device="cuda") for _ in range(30)]
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        step(i % 3, out)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want[i % 3]) for i, x in enumerate(outs))
 
 
 @pytest.mark.parametrize("t", KV)
