@@ -458,6 +458,9 @@ int af_tree_mask(const int32_t* parent_dev, int32_t n, int32_t pos0, uint32_t* m
  *   ws_dev    scratch of at least af_attention_tree_workspace bytes (NULL where that is 0), 256-byte aligned, of any
  *             contents; calls that may overlap in time need scratch of their own
  *   out_dev   fp32 [n] rows, ldo apart
+ * Results keep fp32's precision (2^-20 of the row's score sums and values), and their bits do not change from call to
+ * call.  A row that sees a NaN or an infinity gets what the formula gives or NaN in its place, in any of its values.  The
+ * kernels' waits are bounded: rows of a call whose wait gave up (copies that never arrive) are NaN.
  * 1 <= n <= 1024, 0 <= n_past, n_past + n <= ctx; head_dim 64 or 128, any whole group up to 64.  Pointers are 16-byte
  * aligned (mask_dev: 4), ldq and ldo multiples of 4.  Asynchronous on `stream`, allocates nothing, can be captured
  * (the first call on a device loads the kernels: make it before a capture).
