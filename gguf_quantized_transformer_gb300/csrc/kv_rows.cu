@@ -124,8 +124,7 @@ __global__ void __launch_bounds__(kThreads)
                     const int* __restrict__ slots, int slot0) {
     const int lane = threadIdx.x & 31;
     const int octs = c.KVH * c.D / 8;  // a multiple of 4
-    pdl_launch_dependents();
-    pdl_wait();
+    pdl_wait();  // (and no early launch of the next kernel: see launch_chained)
     for (int r0 = blockIdx.x * kWriteRows; r0 < n; r0 += gridDim.x * kWriteRows) {
         int slot[kWriteRows];  // -1: not written; the same in every thread of the CTA
 #pragma unroll
@@ -163,6 +162,7 @@ __global__ void __launch_bounds__(kThreads)
                 }
         }
     }
+    __threadfence();
 }
 
 // Four values as they lie in the cache, and as fp32.

@@ -109,7 +109,6 @@ __global__ void __launch_bounds__(kThreads, HALF && V > 4 ? 2 : 3)
     const bool copy = tid >= nrot;
     const int rl = copy ? (tid - nrot) / max(units - rot_units, 1) : tid / rot_units;
     const int u = copy ? rot_units + (tid - nrot) % max(units - rot_units, 1) : tid % rot_units;
-    pdl_launch_dependents();
     // (through shared memory: lanes that read parameters at different offsets take turns)
     __shared__ uint64_t turn[kRopeMaxPairs];
     if (tid < R / 2) turn[tid] = turns.turn[tid];
@@ -210,6 +209,7 @@ __global__ void __launch_bounds__(kThreads, HALF && V > 4 ? 2 : 3)
         if (wn >= total) break;
         w = wn, row = rn, hg = hn, xr = xn, cur = next, p = pn;
     }
+    __threadfence();  // (and no early launch of the next kernel: see launch_chained)
 }
 
 template <typename T, int V, bool HALF>

@@ -629,6 +629,39 @@ def test_attention_tree_sees_rows_written_just_before(af, t, past, n):
     assert all(torch.equal(x, want[i % 3]) for i, x in enumerate(outs))
 
 
+@pytest.mark.parametrize("t", ["f32", "f16"])
+@pytest.mark.parametrize("ctx", [1024, 6000])
+@pytest.mark.parametrize("how", ["write", "rope"])
+def test_decode_attention_sees_a_cache_changed_just_before(af, t, ctx, how):
+    """The decode attention reads ahead in the cache, so the kernel before it must not let it start early."""
+    H, KVH, D, pos = 32, 8, 128, ctx - 1
+    rng = np.random.default_rng(21)
+    cache, _, _ = filled(af, t, rng, KVH, D, ctx, ctx)
+    rows = [_dev((rng.standard_normal((ctx, KVH * D)) * 2.0 ** i).astype(np.float32)) for i in range(2)]
+    q = _dev(rng.standard_normal(H * D).astype(np.float32))
+    cfg = af.rope_config(D, D, "half", 10000.0)
+    keys = [cache[0].clone(), cache[0].flip(1).contiguous()]
+
+    def step(i, out):
+        if how == "write":
+            write(af, t, cache, rows[i], rows[i], KVH, D, ctx)
+        else:
+            af.af_rope(cfg, keys[i], D, cache[0], D, af.AF_F32 if t == "f32" else af.AF_F16, KVH * ctx, 1, None, 0)
+        af.af_attention_decode_static(q, cache[0], cache[2], af.KVTYPE[t], H, KVH, D, ctx, pos, out)
+
+    want = [torch.zeros(H * D, device="cuda") for _ in range(2)]
+    for i in (0, 1):
+        torch.cuda.synchronize()
+        step(i, want[i])
+    outs = [torch.zeros(H * D, device="cuda") for _ in range(20)]
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        step(i % 2, out)
+    torch.cuda.synchronize()
+    assert not torch.equal(want[0], want[1])
+    assert all(torch.equal(x, want[i % 2]) for i, x in enumerate(outs))
+
+
 @pytest.mark.parametrize("t", KV)
 def test_attention_tree_long_sums(af, t):
     """Over 125 tiles in one block the error does not grow with their number: the tensor cores cut their sums by up to
