@@ -15,6 +15,7 @@
 // SM.  Data of earlier kernels is read through L2 (the kernels are
 // launched with programmatic serialization).
 #include <algorithm>
+#include <type_traits>
 
 #include "draft.cuh"
 #include "tma.cuh"
@@ -24,7 +25,7 @@ namespace af {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRows = 4, kWriteRows = 2;
+constexpr int kRows = 4, kWriteRows = 2, kGroup = 16;
 constexpr int kCtasPerSm = 8;
 
 // OR over the CTA, in every thread
@@ -121,45 +122,57 @@ __device__ __forceinline__ void store_group(void* base, __half* scales, int64_t 
 template <int TYPE>
 __global__ void __launch_bounds__(kThreads)
     kv_write_kernel(KvRows c, const float* __restrict__ k, const float* __restrict__ v, int64_t ld, int n,
-                    const int* __restrict__ slots, int slot0) {
+                    const int* __restrict__ slots, int slot0, int group) {
     const int lane = threadIdx.x & 31;
     const int octs = c.KVH * c.D / 8;  // a multiple of 4
     pdl_wait();  // (and no early launch of the next kernel: see launch_chained)
-    for (int r0 = blockIdx.x * kWriteRows; r0 < n; r0 += gridDim.x * kWriteRows) {
-        int slot[kWriteRows];  // -1: not written; the same in every thread of the CTA
-#pragma unroll
-        for (int j = 0; j < kWriteRows; j++) slot[j] = r0 + j >= n ? -1 : slots ? __ldcg(slots + r0 + j) : slot0 + r0 + j;
+    for (int g0 = blockIdx.x * group; g0 < n; g0 += gridDim.x * group) {
+        unsigned again = 0;  // rows of the group whose slot a later row names too: it belongs to that one
         if (slots) {
-            unsigned again = 0;  // rows whose slot a later row names too: it belongs to that one
-            for (int i = r0 + 1 + threadIdx.x; i < n; i += kThreads) {
-                const int x = __ldcg(slots + i);
+            auto search = [&](auto rows) {
+                constexpr int N = decltype(rows)::value;
+                int named[N];
 #pragma unroll
-                for (int j = 0; j < kWriteRows; j++) again |= (i > r0 + j && x == slot[j]) ? 1u << j : 0u;
-            }
+                for (int j = 0; j < N; j++) named[j] = j < group && g0 + j < n ? __ldcg(slots + g0 + j) : -1;
+                for (int i = g0 + 1 + threadIdx.x; i < n; i += kThreads) {
+                    const int x = __ldcg(slots + i);
+#pragma unroll
+                    for (int j = 0; j < N; j++) again |= (i > g0 + j && x == named[j]) ? 1u << j : 0u;
+                }
+            };
+            if (group == kWriteRows)
+                search(std::integral_constant<int, kWriteRows>());
+            else
+                search(std::integral_constant<int, kGroup>());
             again = cta_or(again);
-#pragma unroll
-            for (int j = 0; j < kWriteRows; j++)
-                if (slot[j] < 0 || slot[j] >= c.ctx || (again >> j & 1)) slot[j] = -1;
         }
-        for (int i0 = threadIdx.x - lane; i0 < 2 * octs; i0 += kThreads) {  // K, then V; whole warps
-            const bool in = i0 + lane < 2 * octs;
-            const int i = in ? i0 + lane : 0;
-            const bool isv = i >= octs;
-            const int b = (isv ? i - octs : i) >> 2, e0 = b * 32 + (i & 3) * 4, g = e0 / c.D, d0 = e0 - g * c.D;
-            const float* src = (isv ? v : k) + r0 * ld + e0;
-            float4 x[kWriteRows][2];
+        for (int r0 = g0; r0 < min(n, g0 + group); r0 += kWriteRows, again >>= kWriteRows) {
+            int slot[kWriteRows];  // -1: not written; the same in every thread of the CTA
 #pragma unroll
-            for (int j = 0; j < kWriteRows; j++)
-                if (slot[j] >= 0) {
-                    x[j][0] = __ldcg(reinterpret_cast<const float4*>(src + j * ld));
-                    x[j][1] = __ldcg(reinterpret_cast<const float4*>(src + j * ld + 16));
-                }
+            for (int j = 0; j < kWriteRows; j++) {
+                slot[j] = r0 + j >= n ? -1 : slots ? __ldcg(slots + r0 + j) : slot0 + r0 + j;
+                if (slot[j] >= c.ctx || (again >> j & 1)) slot[j] = -1;
+            }
+            for (int i0 = threadIdx.x - lane; i0 < 2 * octs; i0 += kThreads) {  // K, then V; whole warps
+                const bool in = i0 + lane < 2 * octs;
+                const int i = in ? i0 + lane : 0;
+                const bool isv = i >= octs;
+                const int b = (isv ? i - octs : i) >> 2, e0 = b * 32 + (i & 3) * 4, g = e0 / c.D, d0 = e0 - g * c.D;
+                const float* src = (isv ? v : k) + r0 * ld + e0;
+                float4 x[kWriteRows][2];
 #pragma unroll
-            for (int j = 0; j < kWriteRows; j++)
-                if (slot[j] >= 0) {
-                    const float a[8] = {x[j][0].x, x[j][0].y, x[j][0].z, x[j][0].w, x[j][1].x, x[j][1].y, x[j][1].z, x[j][1].w};
-                    store_group<TYPE>(isv ? c.v : c.k, isv ? c.vs : c.ks, (int64_t)g * c.ctx + slot[j], c.D, d0, a, lane, in);
-                }
+                for (int j = 0; j < kWriteRows; j++)
+                    if (slot[j] >= 0) {
+                        x[j][0] = __ldcg(reinterpret_cast<const float4*>(src + j * ld));
+                        x[j][1] = __ldcg(reinterpret_cast<const float4*>(src + j * ld + 16));
+                    }
+#pragma unroll
+                for (int j = 0; j < kWriteRows; j++)
+                    if (slot[j] >= 0) {
+                        const float a[8] = {x[j][0].x, x[j][0].y, x[j][0].z, x[j][0].w, x[j][1].x, x[j][1].y, x[j][1].z, x[j][1].w};
+                        store_group<TYPE>(isv ? c.v : c.k, isv ? c.vs : c.ks, (int64_t)g * c.ctx + slot[j], c.D, d0, a, lane, in);
+                    }
+            }
         }
     }
     __threadfence();
@@ -241,7 +254,13 @@ unsigned ctas(int n, int rows) { return (unsigned)std::min((n + rows - 1) / rows
 
 cudaError_t launch_kv_write(const KvRows& c, const float* k, const float* v, int64_t ld, int n, const int* slots,
                             int slot0, cudaStream_t s) {
-    auto go = [&](auto kernel) { return launch_chained(kernel, dim3(ctas(n, kWriteRows)), kThreads, 0, s, c, k, v, ld, n, slots, slot0); };
+    // Rows that share one search for later rows of their slots: more where a CTA has more rows (30000 listed fp16 rows:
+    // 203 us, 392 with searches for two rows; a run of slots 118)
+    int group = kWriteRows;
+    while (slots && group < kGroup && (int64_t)group * num_sms() * kCtasPerSm < n) group *= 2;
+    auto go = [&](auto kernel) {
+        return launch_chained(kernel, dim3(ctas(n, group)), kThreads, 0, s, c, k, v, ld, n, slots, slot0, group);
+    };
     switch (c.type) {
         case AF_F32: return go(kv_write_kernel<AF_F32>);
         case AF_F16: return go(kv_write_kernel<AF_F16>);

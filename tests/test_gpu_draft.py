@@ -273,6 +273,24 @@ def test_kv_same_slot_twice_last_row_wins(af, t):
             assert np.array_equal(gv[s].astype(np.float64), held(-k[rows[-1]].reshape(kvh, d), t).reshape(-1)), s
 
 
+@pytest.mark.parametrize("n", [4000, 9001, 33333])
+def test_kv_many_listed_rows_last_row_wins(af, n):
+    """Lists so long that blocks search for several rows at once."""
+    kvh, d, ctx = 1, 32, 3001
+    rng = np.random.default_rng(n)
+    k = rng.standard_normal((n, kvh * d)).astype(np.float32)
+    slots = rng.integers(-2, ctx + 2, n).astype(np.int32)
+    slots[-1] = slots[0] = 7
+    cache = new_cache("f32", kvh, ctx, d)
+    write(af, "f32", cache, _dev(k), _dev(-k), kvh, d, ctx, _dev(slots))
+    want = np.zeros((ctx, kvh * d), np.float32)
+    for r, s in enumerate(slots):
+        if 0 <= s < ctx:
+            want[s] = k[r]
+    gk, gv = read(af, "f32", cache, ctx, kvh, d, ctx)
+    assert np.array_equal(gk, want) and np.array_equal(gv, -want)
+
+
 @pytest.mark.parametrize("t", ["q8_0", "q4_0"])
 def test_kv_non_finite_blocks_read_back_as_nan(af, t):
     k = np.random.default_rng(7).standard_normal((1, 128)).astype(np.float32)
