@@ -967,12 +967,12 @@ TreeTcPlan tree_tc_plan(int H, int KVH, int type, int past, int n) {
     TreeTcPlan p;
     const int R = n * (H / KVH);
     // More than 32 rows; of fp32 caches, whose mma.sync kernel needs three tf32 products, more than 16 over a long past
-    // (32 rows over 4000 slots: 29 us there, 21 here; over 1000: 15.2 there, 16.5 here).
-    if (R <= (type == AF_F32 && past + n >= 2048 ? 16 : 32)) return p;
+    // (32 rows over 4000 slots: 26.5 us there, 21.1 here; over 1000: 14.4 there, 13.4 here).
+    if (R <= (type == AF_F32 && past + n >= 1024 ? 16 : 32)) return p;
     p.tiles = (past + n + BK - 1) / BK;
     const int64_t ctas = (int64_t)KVH * ((R + kRows - 1) / kRows);
-    // one CTA per SM, two tiles each or more (64 nodes over 448 fp16 slots: 12.1 us, 13.6 with four), but a few tiles are
-    // quicker than a merge (over 192: 10.4 us in one split, 12.0 in two)
+    // one CTA per SM, two tiles each or more (64 nodes over 448 fp16 slots: 11.4 us, 12.9 with four), but a few tiles are
+    // not worth a merge (64 nodes, 256 slots: fp16 9.9 us in one split, 10.1 in two; fp32 13.2 and 12.1)
     p.splits = p.tiles <= 4 ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(num_sms() / ctas, p.tiles / 2));
     return p;
 }
