@@ -33,9 +33,9 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // Launch with programmatic stream serialization: the kernel may start before its predecessor in the stream is done and
-// waits for it (griddepcontrol.wait) before it touches memory.  A kernel that may write a cache (rows, keys that move) does
-// not launch its dependents early, and its stores are visible before it ends: the decode attention reads all but the last
-// slot before its own wait, so it would see the cache as it was.
+// waits for it (griddepcontrol.wait) before it touches memory.  A kernel that may write a cache (rows, keys that move, slots
+// read back as the fp32 cache of a kv head) does not launch its dependents early, and its stores are visible before it ends:
+// the decode attention reads all but the last slot before its own wait, so it would see the cache as it was.
 template <typename K, typename... A>
 cudaError_t launch_chained(K kernel, dim3 grid, int threads, int smem, cudaStream_t s, A&&... args) {
     cudaLaunchConfig_t cfg = {};

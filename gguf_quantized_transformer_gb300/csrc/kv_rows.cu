@@ -220,8 +220,7 @@ __global__ void __launch_bounds__(kThreads)
     kv_read_kernel(KvRows c, int n, const int* __restrict__ slots, int slot0, float* __restrict__ k,
                    float* __restrict__ v, int64_t ld) {
     const int quads = c.KVH * c.D / 4;
-    pdl_launch_dependents();
-    pdl_wait();
+    pdl_wait();  // (and no early launch of the next kernel: rows of one kv head are an fp32 cache, see launch_chained)
     for (int r0 = blockIdx.x * kRows; r0 < n; r0 += gridDim.x * kRows) {
         int slot[kRows];
 #pragma unroll
@@ -246,6 +245,7 @@ __global__ void __launch_bounds__(kThreads)
                 }
         }
     }
+    __threadfence();
 }
 
 unsigned ctas(int n, int rows) { return (unsigned)std::min((n + rows - 1) / rows, num_sms() * kCtasPerSm); }

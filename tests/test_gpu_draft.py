@@ -681,6 +681,36 @@ def test_decode_attention_sees_a_cache_changed_just_before(af, t, ctx, how):
 
 
 @pytest.mark.parametrize("t", KV)
+@pytest.mark.parametrize("ctx", [1024, 6000])
+def test_decode_attention_sees_slots_read_back_just_before(af, t, ctx):
+    """A kv head's slots, read back by one call a head, are an fp32 cache for the decode attention behind them."""
+    H, KVH, D, pos = 32, 8, 128, ctx - 1
+    rng = np.random.default_rng(22)
+    src = [filled(af, t, rng, KVH, D, ctx, ctx)[0] for _ in range(2)]
+    heads = [[[None if x is None else x[h] for x in c] for h in range(KVH)] for c in src]
+    k, v = (torch.zeros(KVH, ctx, D, device="cuda") for _ in range(2))
+    kd, vd = [k[h] for h in range(KVH)], [v[h] for h in range(KVH)]
+    q = _dev(rng.standard_normal(H * D).astype(np.float32))
+
+    def step(i, out):
+        for h in range(KVH):
+            af.af_kv_read(*heads[i][h], af.KVTYPE[t], 1, D, ctx, ctx, None, 0, kd[h], vd[h], D)
+        af.af_attention_decode_static(q, k, v, af.AF_F32, H, KVH, D, ctx, pos, out)
+
+    want = [torch.zeros(H * D, device="cuda") for _ in range(2)]
+    for i in (0, 1):
+        torch.cuda.synchronize()
+        step(i, want[i])
+    outs = [torch.zeros(H * D, device="cuda") for _ in range(20)]
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        step(i % 2, out)
+    torch.cuda.synchronize()
+    assert not torch.equal(want[0], want[1])
+    assert all(torch.equal(x, want[i % 2]) for i, x in enumerate(outs))
+
+
+@pytest.mark.parametrize("t", KV)
 def test_attention_tree_long_sums(af, t):
     """Over 125 tiles in one block the error does not grow with their number: the tensor cores cut their sums by up to
     2^-23 at each of the 12 products of a tile, over 2 tiles at most; with the two-part operands, the exponential and the
