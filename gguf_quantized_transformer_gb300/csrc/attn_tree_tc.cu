@@ -405,6 +405,14 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
     // (softmax threads) where the thread's row of q starts
     const int qr = r0 + (warp & 3) * 32 + lane;
     const int64_t qoff = qr < R ? (int64_t)(qr / G) * a.ldq + (int64_t)(g * G + qr % G) * D : 0;
+    // q and the output pass through the last V slots, so that global accesses are whole rows: chunk c (16 bytes) of row rr
+    // of 32 sits at c ^ (rr & 7).
+    constexpr int CPR = D / 4;  // chunks per row
+    auto stage = [&](int quad, int rr, int c) {
+        return reinterpret_cast<float4*>(smem + C::OFF_V + (C::NS - C::QS) * C::SLOT + (quad * 32 + rr) * D * 4 + ((c ^ (rr & 7)) << 4));
+    };
+    float row_l = 0.f, row_m = 0.f;  // (softmax threads) the row's sum, maximum and exponent
+    int row_ev = 0;
     pdl_wait();  // q, the mask and the cache are written by earlier kernels
 
     if (warp == C::MMA_WARP) {
@@ -655,11 +663,7 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
             return met;
         };
         float rowf = 1.f;
-        // Rows pass through shared memory, so that global accesses are whole rows: chunk c (16 bytes) of row r sits at
-        // c ^ (r & 7).
-        constexpr int CPR = D / 4, RPI = 32 / CPR;  // chunks per row, rows per warp access
-        auto stage = [&](uint8_t* base, int rr, int c) { return reinterpret_cast<float4*>(base + rr * D * 4 + ((c ^ (rr & 7)) << 4)); };
-        uint8_t* const st = smem + C::OFF_V + (C::NS - C::QS) * C::SLOT + quad * 32 * D * 4;
+        constexpr int RPI = 32 / CPR;  // rows per warp access
         bool ok;
         {  // q: scaled to [1, 2), split, into tensor memory; each warp brings 16 rows and converts half of the dims
             const int c = lane % CPR, i0 = half * 16;
@@ -667,7 +671,7 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
             for (int i = 0; i < 16 / RPI; i++) {
                 const int rr = i0 + i * RPI + lane / CPR;
                 const int64_t o = __shfl_sync(0xffffffffu, qoff, rr);
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(stage(st, rr, c))), "l"(a.q + o + c * 4) : "memory");
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(stage(quad, rr, c))), "l"(a.q + o + c * 4) : "memory");
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
             bar_arrive(kQueueBar, (kSoftWarps + 2) * 32);  // K's and V's copies come after q, which is waited for first
@@ -677,7 +681,7 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
             float mx = 0.f;
 #pragma unroll
             for (int i = 0; i < CPR / 2; i++) {
-                y[i] = *stage(st, lane, half * (CPR / 2) + i);
+                y[i] = *stage(quad, lane, half * (CPR / 2) + i);
                 mx = fmaxf(mx, fmaxf(fmaxf(fabsf(y[i].x), fabsf(y[i].y)), fmaxf(fabsf(y[i].z), fabsf(y[i].w))));
             }
             sm.pair_x[1][quad][half][lane] = mx;
@@ -872,23 +876,33 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.p_full[b]);
         }
-        // ---- this split's part of the row: the sum of both halves, and half of the dims each
+        // ---- the row's sum is that of both halves
         if (ok) {
             sm.pair_x[T & 1][quad][half][lane] = l;
             ok = meet() && twait(&sm.done, 0, sm);
             l += sm.pair_x[T & 1][quad][half ^ 1][lane];
         }
+        row_l = l;
+        row_m = m_ref;
+        row_ev = ev_ref;
+    }
+    tc_fence_before();
+    __syncthreads();  // every wait is behind: whether one of them gave up holds for the whole CTA
+    const bool gave_up = sm.abort;
+    if (warp < kSoftWarps) {
+        // ---------------- this split's part of the rows, half of the dims a thread
+        const int quad = warp & 3, half = warp >> 2, r = r0 + quad * 32 + lane;
+        const bool live = r < R, last = splits == 1;  // last: the result itself (zeros for a row that saw nothing)
+        const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
         const int64_t rows = (int64_t)a.c.KVH * R;
         const int64_t row = (int64_t)split * rows + (int64_t)g * R + r;
-        // one split: the result itself (zeros for a row that saw nothing)
-        const bool last = splits == 1;
         float* base = last ? a.out : a.ws;
         const int64_t off = !live ? 0 : last ? (int64_t)(r / G) * a.ldo + (int64_t)(g * G + r % G) * D : row * D;
-        constexpr int HC = CPR / 2;  // chunks of half a row
-        if (ok) {  // every operand has been read: the ring is free
+        if (!gave_up) {  // every operand has been read: the ring is free
+            constexpr int HC = CPR / 2;  // chunks of half a row
             tc_fence_after();
-            float up = C::SPLIT ? pow2i(ev_ref) : 1.f;
-            if (last) up = l == 0.f ? 0.f : up / l;
+            float up = C::SPLIT ? pow2i(row_ev) : 1.f;
+            if (last) up = row_l == 0.f ? 0.f : up / row_l;
 #pragma unroll 1
             for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
                 float o[32];
@@ -901,29 +915,30 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                 }
 #pragma unroll
                 for (int i = 0; i < 32; i += 4)
-                    *stage(st, lane, (c + i) / 4) = make_float4(o[i] * up, o[i + 1] * up, o[i + 2] * up, o[i + 3] * up);
+                    *stage(quad, lane, (c + i) / 4) = make_float4(o[i] * up, o[i + 1] * up, o[i + 2] * up, o[i + 3] * up);
             }
-        } else {
-            for (int c = 0; c < HC; c++)
-                *stage(st, lane, half * HC + c) = make_float4(CUDART_NAN_F, CUDART_NAN_F, CUDART_NAN_F, CUDART_NAN_F);
-        }
-        __syncwarp();
-        const int c = half * HC + lane % HC;
-        int64_t o[HC];
+            __syncwarp();
+            const int c = half * HC + lane % HC;
+            int64_t o[HC];
 #pragma unroll
-        for (int i = 0; i < HC; i++) o[i] = __shfl_sync(0xffffffffu, off, i * (32 / HC) + lane / HC);
+            for (int i = 0; i < HC; i++) o[i] = __shfl_sync(0xffffffffu, off, i * (32 / HC) + lane / HC);
 #pragma unroll
-        for (int i = 0; i < HC; i++) {
-            const int rr = i * (32 / HC) + lane / HC;
-            if (r0 + quad * 32 + rr < R) reinterpret_cast<float4*>(base + o[i])[c] = *stage(st, rr, c);
+            for (int i = 0; i < HC; i++) {
+                const int rr = i * (32 / HC) + lane / HC;
+                if (r0 + quad * 32 + rr < R) reinterpret_cast<float4*>(base + o[i])[c] = *stage(quad, rr, c);
+            }
+        } else if (live) {  // copies and MMAs may still be in flight: nothing goes through shared memory
+            for (int i = 0; i < D / 8; i++)
+                reinterpret_cast<float4*>(base + off)[half * (D / 8) + i] =
+                    make_float4(CUDART_NAN_F, CUDART_NAN_F, CUDART_NAN_F, CUDART_NAN_F);
         }
         if (live && !last && half == 0)
             reinterpret_cast<float2*>(a.ws + splits * rows * D)[row] =
-                ok ? make_float2(m_ref, l) : make_float2(CUDART_NAN_F, CUDART_NAN_F);
+                gave_up ? make_float2(CUDART_NAN_F, CUDART_NAN_F) : make_float2(row_m, row_l);
     }
     tc_fence_before();
     __syncthreads();
-    if (sm.abort && tid == 0) {  // let what was issued finish before leaving
+    if (gave_up && tid == 0) {  // let what was issued finish before leaving
         mbar_wait_bounded(&sm.done, 0);
         for (int x = 0; x < 2; x++) {
             constexpr int N = C::SPLIT ? C::NR : C::NS;
