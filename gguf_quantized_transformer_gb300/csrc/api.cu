@@ -1132,7 +1132,8 @@ int check_tree(int32_t type, int32_t H, int32_t KVH, int32_t D, int32_t past, in
     if ((D != 64 && D != 128) || H / KVH > 64 || H > 65535)
         return fail(AF_ENOTIMPL, "tree attention supports head_dim 64 / 128 and groups up to 64");
     if (n < 1 || n > kTreeMax) return fail(AF_ERANGE, "n=%d outside [1, %d]", n, kTreeMax);
-    if (past < 0 || past > INT32_MAX - kTreeMax) return fail(AF_ERANGE, "n_past=%d", past);
+    // (the last tile's slots are counted past the last node's, in 32 bits)
+    if (past < 0 || past > INT32_MAX - 2 * kTreeMax) return fail(AF_ERANGE, "n_past=%d", past);
     return AF_OK;
 }
 

@@ -461,7 +461,7 @@ int af_tree_mask(const int32_t* parent_dev, int32_t n, int32_t pos0, uint32_t* m
  * Results keep fp32's precision (2^-20 of the row's score sums and values), and their bits do not change from call to
  * call.  A row that sees a NaN or an infinity gets what the formula gives or NaN in its place, in any of its values.  The
  * kernels' waits are bounded: rows of a call whose wait gave up (copies that never arrive) are NaN.
- * 1 <= n <= 1024, 0 <= n_past, n_past + n <= ctx; head_dim 64 or 128, any whole group up to 64.  Pointers are 16-byte
+ * 1 <= n <= 1024, 0 <= n_past <= 2^31 - 2049, n_past + n <= ctx, n_kv_heads * ctx < 2^31; head_dim 64 or 128, any whole group up to 64.  Pointers are 16-byte
  * aligned (mask_dev: 4), ldq and ldo multiples of 4.  Asynchronous on `stream`, allocates nothing, can be captured
  * (the first call on a device loads the kernels: make it before a capture).
  * Errors: AF_EINVAL, AF_ERANGE, AF_ENOTIMPL, AF_ECUDA.

@@ -109,3 +109,17 @@ def test_workspace_covers_the_documented_range():
             for past in (0, 1, 31, 4096, 30720, 1 << 20):
                 for n in (1, 4, 64, 1024):
                     assert 0 <= af.af_attention_tree_workspace(t, h, kvh, d, past, n) <= 256 << 20
+
+
+def test_tree_pasts_at_the_end_of_the_integers():
+    """Slots are counted in 32 bits, tiles past the last one among them: a past that leaves no room for a tile is refused."""
+    af = _af()
+    L = af.lib()
+    big = 2 ** 31 - 1
+    for t in (af.AF_F32, af.AF_F16):
+        for n in (1, 40, 1024):
+            for past in (big - n, big - 1024, big - 2047):
+                assert L.af_attention_tree(P, 64, P, None, P, None, t, 1, 1, 64, big, past, n, P, None, 0, P, 64,
+                                           None) == af.AF_ERANGE
+                assert af.af_attention_tree_workspace(t, 1, 1, 64, past, n) == 0
+    assert af.af_attention_tree_workspace(af.AF_F32, 1, 1, 64, big - 2048, 1024) <= 256 << 20
