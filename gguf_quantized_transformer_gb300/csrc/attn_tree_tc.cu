@@ -19,8 +19,10 @@
 //   fp32, Q8_0, Q4_0  bulk copies bring the raw rows into a staging ring, four warps for K and four for V write them
 //                 as fp16 hi and lo parts in the same layout; three products (the dropped lo lo is 2^-22 relative).
 //                 Sixteen slots are scaled by a power of two that brings their largest value (or scale) near 1, so
-//                 fp16's range never binds: K's goes into the scores' factor; V's into p's, relative to a reference
-//                 exponent of the output, which is rescaled when the slots outgrow it.
+//                 fp16's range never binds; where the slots' own largest values are more than 2^kSpread apart, each slot
+//                 by its own (one large key, hidden or not, would leave its neighbours few bits).  K's power goes into
+//                 the scores; V's into p, relative to a reference exponent of the row's output, which is rescaled when
+//                 p times V, over the slots that the row sees, outgrows it.
 //                 (Rows read through registers instead, three tiles ahead: 192 us where this took 107 at 64 nodes
 //                 over 30720 fp32 slots; the warp's loads of several tiles share its few scoreboards.)
 // Warps 0-7 are the softmax: a thread owns a row and 32 of a tile's slots (its scores in registers: maximum, p, sum), the
@@ -49,7 +51,9 @@ constexpr int kQueueBar = 1;   // named barrier: q has been read
 constexpr int kRows = 128;
 constexpr float kLazy2 = 4.f, kBias2 = 8.f;  // as attn_tree.cu's
 constexpr int kConvWarps = 4;  // for K, and as many for V: 16 slots of a tile each
-constexpr int kNoExp = -1000, kMaxExp = 126;  // exponents of 16 slots; above: an infinity among them
+constexpr int kNoExp = -128, kMaxExp = 126;  // exponents of slots: of zeros, and the largest (an infinity's too)
+constexpr int kNoRef = -1000;  // the output's reference exponent before it has one
+constexpr int kSpread = 3;     // 16 slots whose exponents differ by more than this have their own
 constexpr int kSoftWarps = 8;  // two per 32 rows
 
 template <int TYPE, int D>
@@ -67,7 +71,11 @@ struct TcCfgT {
     static constexpr int SCB = TYPE == AF_F32 ? 0 : D / 16;  // scale bytes of a row
     static constexpr int RR = TYPE == AF_F32 ? BK / 2 : BK, RU = RR / 16;  // (the rows of RU warps)
     static constexpr int RAW = RR * (RB + SCB);
-    static constexpr int NR = !SPLIT ? 0 : TYPE == AF_F32 ? (D == 128 ? 3 : 6) : 5;
+    static constexpr int NR = !SPLIT ? 0 : TYPE == AF_F32 ? (D == 128 ? 3 : 5) : 5;
+    // tiles whose K exponents are kept: while the softmax is at tile t, the scores of t + AHEAD - 1 may be done and the
+    // converters at the tile NS after that
+    static constexpr int EK = !SPLIT ? 1 : D == 128 ? 4 : 8;
+    static_assert(!SPLIT || AHEAD + NS <= EK, "exponents of K are read before they are overwritten");
     static constexpr int OFF_V = NS * SLOT, OFF_RAW = 2 * NS * SLOT;
     static constexpr int QS = kRows * D * 4 / SLOT;          // the last V slots, through which q and the output pass
     static_assert(QS <= NS, "q fits the V slots");
@@ -79,10 +87,14 @@ struct TcCfgT {
 };
 
 // Of pairs, [0] is K's and [1] V's.
+template <typename C>
 struct alignas(1024) TcState {  // (the operand slots behind it need 1024 bytes)
-    uint64_t full[2][6], empty[2][6];          // operand slots
-    uint64_t raw_full[2][6], raw_empty[2][6];  // staging slots
-    uint64_t s_full[4], p_full[4], pv_done[4];
+    static constexpr int NR = C::NR ? C::NR : 1;
+    int8_t ek[C::EK][BK], ev[C::NS][BK];  // exponents of the slots' K by tile, of V by operand slot (kNoExp: zeros)
+    uint32_t ek_own[C::EK], ev_own[C::NS];  // by byte: whether 16 slots have exponents of their own
+    uint64_t full[2][C::NS], empty[2][C::NS];  // operand slots
+    uint64_t raw_full[2][NR], raw_empty[2][NR];  // staging slots
+    uint64_t s_full[C::SB], p_full[C::SB], pv_done[C::SB];
     uint64_t q_ready, done;
     uint64_t v_clean;                          // fp16: a tile of nodes has its V checked
     uint64_t pair[4];                          // the two softmax warps of 32 rows
@@ -90,8 +102,6 @@ struct alignas(1024) TcState {  // (the operand slots behind it need 1024 bytes)
     uint32_t tmem_base;
     int copies[2];    // bulk copies issued, for the drain
     volatile int abort;
-    float ek[8][4];   // 2^exponent of K by tile and 16 slots
-    int ev[8][4];     // exponent of V (kNoExp: all zeros)
     unsigned long long bad[kTreeMax / BK + 2];  // by tile of nodes: slots with a non-finite key or value
 };
 
@@ -105,7 +115,8 @@ struct Ring {
     }
 };
 
-__device__ __forceinline__ bool twait(uint64_t* bar, unsigned parity, TcState& sm) {  // whole warp
+template <typename S>
+__device__ __forceinline__ bool twait(uint64_t* bar, unsigned parity, S& sm) {  // whole warp
     bool ok = false;
     for (unsigned i = 0; i < kWaitLimit && !ok; i++) {
         ok = mbar_try_wait(bar, parity);
@@ -115,7 +126,8 @@ __device__ __forceinline__ bool twait(uint64_t* bar, unsigned parity, TcState& s
     if (!ok) sm.abort = 1;
     return ok;
 }
-__device__ __forceinline__ bool twait1(uint64_t* bar, unsigned parity, TcState& sm) {  // one thread
+template <typename S>
+__device__ __forceinline__ bool twait1(uint64_t* bar, unsigned parity, S& sm) {  // one thread
     for (unsigned i = 0; i < kWaitLimit; i++) {
         if (mbar_try_wait(bar, parity)) return true;
         if (sm.abort) return false;
@@ -257,56 +269,91 @@ __device__ __forceinline__ Raw<TYPE> load_raw(const uint8_t* st, const uint8_t* 
     return c;
 }
 
-// Largest magnitude among this lane's values (fp32) or scales.
+// The bits of the largest magnitude (or scale) of row `lane` of the warp's 16 (0 in the other lanes; NaNs count as above
+// infinity).
 template <int TYPE, int D, bool NODES>
-__device__ __forceinline__ float raw_max(const uint8_t* st, const uint8_t* sc, int valid, int lane, unsigned& bad,
-                                         Kept<TYPE, D>& kept) {
-    float m = 0.f;
+__device__ __forceinline__ unsigned row_max(const uint8_t* st, const uint8_t* sc, int valid, int lane, unsigned& bad,
+                                            Kept<TYPE, D>& kept) {
+    unsigned mine = 0;
+    if constexpr (TYPE == AF_F32) {
 #pragma unroll
-    for (int i = 0; i < raw_pieces<TYPE, D>(); i++) {
-        const Raw<TYPE> c = load_raw<TYPE, D, NODES>(st, sc, i, valid, lane, bad);
-        if constexpr (TYPE == AF_F32) {
+        for (int i = 0; i < raw_pieces<TYPE, D>(); i++) {  // one row a piece, or two (D = 64)
+            const Raw<TYPE> c = load_raw<TYPE, D, NODES>(st, sc, i, valid, lane, bad);
             kept.c[i] = c;
-            m = fmaxf(fmaxf(m, fabsf(__uint_as_float(c.a.x))), fabsf(__uint_as_float(c.a.y)));
-            m = fmaxf(fmaxf(m, fabsf(__uint_as_float(c.a.z))), fabsf(__uint_as_float(c.a.w)));
-        } else {
-            m = fmaxf(m, fabsf(__half2float(c.d)));
+            const unsigned m = max(max(c.a.x & 0x7FFFFFFFu, c.a.y & 0x7FFFFFFFu), max(c.a.z & 0x7FFFFFFFu, c.a.w & 0x7FFFFFFFu));
+            if (D == 128) {
+                const unsigned r = __reduce_max_sync(0xffffffffu, m);
+                if (lane == i) mine = r;
+            } else {
+                const unsigned r0 = __reduce_max_sync(0xffffffffu, lane < 16 ? m : 0u);
+                const unsigned r1 = __reduce_max_sync(0xffffffffu, lane < 16 ? 0u : m);
+                if (lane >> 1 == i) mine = lane & 1 ? r1 : r0;
+            }
         }
-    }
-    return m;
-}
-
-__device__ __forceinline__ float warp_max(float m) {
+    } else if (lane < 16) {
+        unsigned m = 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    return m;
+        for (int i = 0; i < D / 64; i++) {  // two scales
+            unsigned w = reinterpret_cast<const unsigned*>(sc)[lane * (D / 64) + i] & 0x7FFF7FFFu;
+            if (NODES) {
+                const bool lo = (w & 0x7C00u) == 0x7C00u, hi = (w & 0x7C000000u) == 0x7C000000u;
+                if (lane < valid && (lo || hi)) bad |= 1u << lane;
+                w = lane < valid ? w & ((lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u)) : 0u;
+            }
+            m = max(m, max(w & 0xFFFFu, w >> 16));
+        }
+        mine = __float_as_uint(__half2float(__ushort_as_half((unsigned short)m)));
+    }
+    return mine;
 }
 
-// Arrive, not before x (>= 0) has been computed.
-__device__ __forceinline__ void mbar_arrive_after(uint64_t* bar, float x) {
+// The exponents with which a warp's 16 rows are stored: row `lane`'s own one and the factor 2^-that (NaN: the row holds an
+// infinity or a NaN, and every row of q sees it, since others are taken out: at its exponent the finite values would
+// vanish), or one for all.
+struct RowExps {
+    int e;        // of row `lane` (< 16); kNoExp: zeros
+    float down, common;
+    bool own;
+};
+template <int TYPE>
+__device__ __forceinline__ RowExps row_exps(unsigned bits, int lane) {
+    // largest value in [1, 2), or largest scale times its largest code in [1, 4)
+    constexpr int code = TYPE == AF_KV_Q8_0 ? 6 : TYPE == AF_KV_Q4_0 ? 2 : 0;
+    const bool some = lane < 16 && bits != 0, inf = bits >= 0x7F800000u;
+    const int e = min(max((int)(bits >> 23) - 127, -126) + code, kMaxExp);
+    const int hi = __reduce_max_sync(0xffffffffu, some ? e : kNoExp), lo = __reduce_min_sync(0xffffffffu, some ? e : 127);
+    RowExps x;
+    x.own = __any_sync(0xffffffffu, inf) || hi - lo > kSpread;
+    x.e = !x.own ? hi : some ? e : kNoExp;
+    x.down = inf ? CUDART_NAN_F : pow2i(-x.e);
+    x.common = pow2i(-hi);
+    return x;
+}
+
+// Arrive, not before x (never all ones) has been computed.
+__device__ __forceinline__ void mbar_arrive_after(uint64_t* bar, unsigned x) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ge.f32 p, %1, 0f00000000;\n\t"
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0xffffffff;\n\t"
         "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar)),
-        "f"(x)
+        "r"(x)
         : "memory");
 }
 
 __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 __device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
 
-// The fp16 hi and lo parts of the warp's rows row0.., times 2^-e, into a slot (SWIZZLE_128B atoms of 64 dims,
-// [64 slots][128 B] each).  Rows with an infinity, which every row of q sees (others are taken out), become NaN: at its
-// exponent the finite ones would vanish.
+// The fp16 hi and lo parts of the warp's rows row0.., times their 2^-exponent, into a slot (SWIZZLE_128B atoms of 64 dims,
+// [64 slots][128 B] each).
 template <int TYPE, int D, bool NODES>
-__device__ __forceinline__ void store_tile(uint8_t* dst, const uint8_t* st, const uint8_t* sc, int e, int row0, int valid, int lane,
-                                           const Kept<TYPE, D>& kept) {
+__device__ __forceinline__ void store_tile(uint8_t* dst, const uint8_t* st, const uint8_t* sc, const RowExps& x, int row0, int valid,
+                                           int lane, const Kept<TYPE, D>& kept) {
     constexpr int PPR = D / Raw<TYPE>::VALUES, PART = BK * D * 2;  // pieces per row
-    const float down = e > kMaxExp ? CUDART_NAN_F : pow2i(-e);
 #pragma unroll
     for (int i = 0; i < raw_pieces<TYPE, D>(); i++) {
         unsigned bad = 0;
         const Raw<TYPE> r = TYPE == AF_F32 ? kept.c[TYPE == AF_F32 ? i : 0] : load_raw<TYPE, D, NODES>(st, sc, i, valid, lane, bad);
         const int idx = i * 32 + lane, key = row0 + idx / PPR, d0 = idx % PPR * Raw<TYPE>::VALUES;
+        const float down = x.own ? __shfl_sync(0xffffffffu, x.down, idx / PPR) : x.common;
         const uint32_t off = (uint32_t)((d0 >> 6) * BK * 128) + sw128(key, (d0 >> 3) & 7) + (d0 & 7) * 2;
         if constexpr (TYPE == AF_F32) {
             const uint4 a = r.a;
@@ -323,18 +370,18 @@ __device__ __forceinline__ void store_tile(uint8_t* dst, const uint8_t* st, cons
             const __half2 d2 = __float2half2_rn(__half2float(r.d) * down);
             __half2 q[4];
             if constexpr (TYPE == AF_KV_Q8_0) {
-                const uint32_t x = r.a.x ^ 0x80808080u, y = r.a.y ^ 0x80808080u;
+                const uint32_t w = r.a.x ^ 0x80808080u, y = r.a.y ^ 0x80808080u;
                 const __half2 off = u2h(0x64806480u);
-                q[0] = __hsub2(u2h(__byte_perm(x, 0x64646464u, 0x4140)), off);
-                q[1] = __hsub2(u2h(__byte_perm(x, 0x64646464u, 0x4342)), off);
+                q[0] = __hsub2(u2h(__byte_perm(w, 0x64646464u, 0x4140)), off);
+                q[1] = __hsub2(u2h(__byte_perm(w, 0x64646464u, 0x4342)), off);
                 q[2] = __hsub2(u2h(__byte_perm(y, 0x64646464u, 0x4140)), off);
                 q[3] = __hsub2(u2h(__byte_perm(y, 0x64646464u, 0x4342)), off);
             } else {
                 const __half2 off = u2h(0x64086408u);
-                const uint32_t x = r.a;
+                const uint32_t w = r.a;
                 __half2 n[4];  // dims (p, p + 4)
 #pragma unroll
-                for (int p = 0; p < 4; p++) n[p] = __hsub2(u2h(((x >> (4 * p)) & 0x000F000Fu) | 0x64006400u), off);
+                for (int p = 0; p < 4; p++) n[p] = __hsub2(u2h(((w >> (4 * p)) & 0x000F000Fu) | 0x64006400u), off);
                 q[0] = __lows2half2(n[0], n[1]);
                 q[1] = __lows2half2(n[2], n[3]);
                 q[2] = __highs2half2(n[0], n[1]);
@@ -362,8 +409,8 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
     constexpr uint32_t kIdS = idesc_f16(kRows, BK);                  // scores: N = slots, B K-major
     constexpr uint32_t kIdO = idesc_f16(kRows, D) | (1u << 16);      // output: N = dims, B MN-major
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ TcState sm;
-    static_assert(sizeof(TcState) + C::SMEM <= 227 * 1024, "an SM's shared memory");
+    __shared__ TcState<C> sm;
+    static_assert(sizeof(sm) + C::SMEM <= 227 * 1024, "an SM's shared memory");
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int G = a.H / a.c.KVH, R = a.n * G;
     const int split = blockIdx.x, g = blockIdx.y, r0 = blockIdx.z * kRows;
@@ -384,12 +431,12 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
             }
             sm.copies[x] = 0;
         }
-        for (int i = 0; i < 4; i++) {
+        for (int i = 0; i < C::SB; i++) {
             mbar_init(&sm.s_full[i], C::SPLIT ? 2 : 1);  // the commit, and the issuer for K's exponent
             mbar_init(&sm.p_full[i], kSoftWarps);
             mbar_init(&sm.pv_done[i], 1);
-            mbar_init(&sm.pair[i], 2);
         }
+        for (int i = 0; i < 4; i++) mbar_init(&sm.pair[i], 2);
         mbar_init(&sm.v_clean, kSoftWarps);
         mbar_init(&sm.q_ready, kSoftWarps);
         mbar_init(&sm.done, 1);
@@ -611,38 +658,30 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                 const int wr = (w % C::RU) * 16;  // the warp's rows in the slot
                 const uint8_t *rows = st + wr * C::RB, *scales = st + C::RR * C::RB + wr * C::SCB;
                 const int left = t >= tn ? valid - t * BK - w * 16 : 16;  // the warp's rows that hold slots
-                unsigned bad = 0;
-                float m = 0.f;
+                unsigned bad = 0, m;
                 Kept<TYPE, D> kept;
                 if (t >= tn)
-                    m = raw_max<TYPE, D, true>(rows, scales, left, lane, bad, kept);
+                    m = row_max<TYPE, D, true>(rows, scales, left, lane, bad, kept);
                 else
-                    m = raw_max<TYPE, D, false>(rows, scales, left, lane, bad, kept);
-                m = warp_max(m);
-                if (TYPE == AF_F32 && lane == 0) mbar_arrive_after(&sm.raw_empty[x][mine], m);
+                    m = row_max<TYPE, D, false>(rows, scales, left, lane, bad, kept);
+                const RowExps exps = row_exps<TYPE>(m, lane);
+                if (TYPE == AF_F32) {
+                    const unsigned all = __reduce_or_sync(0xffffffffu, m);
+                    if (lane == 0) mbar_arrive_after(&sm.raw_empty[x][mine], all);
+                }
                 if (bad) atomicOr(&sm.bad[t - tn], (unsigned long long)bad << (w * 16));
-                // largest value in [1, 2), or largest scale times its largest code in [1, 4)
-                int e = max(exponent_of(m), -126);
-                const bool inf = e == 128;
-                if (TYPE == AF_KV_Q8_0) e += 6;
-                if (TYPE == AF_KV_Q4_0) e += 2;
-                e = inf ? kMaxExp + 1 : min(e, kMaxExp);
                 if (t >= C::NS) ok = twait(&sm.empty[x][ro.i], ro.ph ^ 1, sm);
                 if (x == 1 && t == C::NS - C::QS) ok = ok && twait(&sm.q_ready, 0, sm);
                 if (!ok) break;
                 uint8_t* dst = smem + (x ? C::OFF_V : 0) + ro.i * C::SLOT;
                 if (t >= tn)
-                    store_tile<TYPE, D, true>(dst, rows, scales, e, w * 16, left, lane, kept);
+                    store_tile<TYPE, D, true>(dst, rows, scales, exps, w * 16, left, lane, kept);
                 else
-                    store_tile<TYPE, D, false>(dst, rows, scales, e, w * 16, left, lane, kept);
+                    store_tile<TYPE, D, false>(dst, rows, scales, exps, w * 16, left, lane, kept);
+                if (lane < 16) (x ? sm.ev[ro.i] : sm.ek[t % C::EK])[w * 16 + lane] = (int8_t)exps.e;
+                if (lane == 0) reinterpret_cast<uint8_t*>(x ? &sm.ev_own[ro.i] : &sm.ek_own[t % C::EK])[w] = exps.own;
                 __syncwarp();
                 if (TYPE != AF_F32 && lane == 0) mbar_arrive(&sm.raw_empty[x][mine]);
-                if (lane == 0) {
-                    if (x == 1)
-                        sm.ev[t & 7][w] = m == 0.f ? kNoExp : min(e, kMaxExp);
-                    else
-                        sm.ek[t & 7][w] = pow2i(min(e, kMaxExp));
-                }
                 fence_proxy_async_shared();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.full[x][ro.i]);
@@ -721,7 +760,14 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
         };
         constexpr int NG = C::SPLIT ? 2 : 1, W = 32 / NG;  // exponents of this half, slots of each
         float m_ref = -CUDART_INF_F, l = 0.f;
-        int ev_ref = kNoExp;
+        // The output holds sums of w V 2^-ev, w = p 2^(ev - ev_ref): ev_ref keeps the largest score plus exponent of V so far
+        // (z_run) near m_ref + ev_ref.
+        int ev_ref = kNoRef;
+        float z_run = -CUDART_INF_F;
+        auto factor = [&](int e) {  // of scores, from q's and K's exponents
+            return fminf(fmaxf(rowf * pow2i(e), 0x1p-126f), 0x1p126f);  // (0 or inf times -inf or 0: NaN)
+        };
+        auto exp_of = [](uint32_t word, int i) { return (int)(word << (24 - 8 * i)) >> 24; };  // byte i, signed
         Ring<C::NS> rv;
         for (int t = 0; ok && t < T; t++, rv.next()) {
             const int b = t % C::SB;
@@ -731,7 +777,8 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
             ok = twait(&sm.s_full[b], ph, sm);
             if (!ok) break;
             float f[NG];
-            int ev[NG] = {}, ev_max = kNoExp;
+            int ev[NG] = {}, ev_hi = kNoExp;
+            bool apart = false;  // V's exponents differ too much for the largest to stand for all
             if (C::SPLIT || nodes) {
                 ok = twait(&sm.full[1][rv.i], rv.ph, sm);  // V's exponents are there (K's since its scores were issued)
                 if (!ok) break;
@@ -739,12 +786,18 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
 #pragma unroll
             for (int q = 0; q < NG; q++) f[q] = rowf;
             if (C::SPLIT) {
+                int ev_lo = 127;
 #pragma unroll
-                for (int q = 0; q < 4; q++) ev_max = max(ev_max, sm.ev[t & 7][q]);
+                for (int q = 0; q < 4; q++) {
+                    const int e = sm.ev[rv.i][16 * q];
+                    ev_hi = max(ev_hi, e);
+                    if (e != kNoExp) ev_lo = min(ev_lo, e);
+                }
+                apart = sm.ev_own[rv.i] || ev_hi - ev_lo > kSpread;
 #pragma unroll
                 for (int q = 0; q < NG; q++) {
-                    f[q] = fminf(fmaxf(f[q] * sm.ek[t & 7][half * NG + q], 0x1p-126f), 0x1p126f);  // (0 or inf times -inf or 0: NaN)
-                    ev[q] = sm.ev[t & 7][half * NG + q];
+                    f[q] = factor(sm.ek[t % C::EK][half * 32 + q * W]);
+                    ev[q] = sm.ev[rv.i][half * 32 + q * W];
                 }
             }
             if (!C::SPLIT && nodes) {  // V of this tile: zeros where it is not finite, and behind the last node
@@ -777,6 +830,13 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
             const uint32_t s_addr = lane_addr + C::SCOL + b * BK + half * 32;
             float s[32];
             tmem_ld32(s_addr, s);
+            if (C::SPLIT && sm.ek_own[t % C::EK]) {  // keys with exponents of their own
+                const uint32_t* e4 = reinterpret_cast<const uint32_t*>(sm.ek[t % C::EK] + half * 32);
+#pragma unroll
+                for (int i = 0; i < 32; i++) s[i] *= factor(exp_of(e4[i / 4], i % 4));
+#pragma unroll
+                for (int q = 0; q < NG; q++) f[q] = 1.f;
+            }
             if (nodes) {
                 const unsigned bad = (unsigned)(*(volatile unsigned long long*)&sm.bad[t - tn] >> (half * 32));
 #pragma unroll
@@ -800,22 +860,41 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
             ok = meet();
             if (!ok) break;
             mt = fmaxf(mt, sm.pair_x[t & 1][quad][half ^ 1][lane]);
+            float z = C::SPLIT && ev_hi != kNoExp ? mt + (float)ev_hi : -CUDART_INF_F;
+            if (C::SPLIT && apart) {  // (the same in both warps)
+                z = -CUDART_INF_F;
+                const uint32_t* e4 = reinterpret_cast<const uint32_t*>(sm.ev[rv.i] + half * 32);
+#pragma unroll
+                for (int i = 0; i < 32; i++) {
+                    const int e = exp_of(e4[i / 4], i % 4);
+                    if (e != kNoExp) z = fmaxf(z, s[i] * f[i / W] + (float)e);
+                }
+                sm.pair_x[(t & 1) ^ 1][quad][half][lane] = z;  // (both have read the previous tile's)
+                ok = meet();
+                z = fmaxf(z, sm.pair_x[(t & 1) ^ 1][quad][half ^ 1][lane]);
+                ok = ok && meet();  // (both have read it: the next tile's may be written)
+                if (!ok) break;
+            }
+            z_run = fmaxf(z_run, z);
             const bool move = mt > m_ref + kLazy2;
-            const bool grow = C::SPLIT && ev_max > ev_ref + 2;
+            const bool grow = C::SPLIT && z > m_ref + (float)ev_ref + kLazy2;
             const bool flush = t > 0 && t % kFlush == 0;  // the output sum starts again with this tile
             const bool change = __any_sync(0xffffffffu, move || grow);  // (the same in both warps)
             if (change || flush) {
                 float up = 1.f;
                 if (change) {
+                    float d = 0.f;
                     if (mt > m_ref) {
-                        up = ex2u(m_ref - mt);
+                        d = m_ref - mt;
                         m_ref = mt;
-                        l *= up;
+                        l *= ex2u(d);
                     }
-                    if (grow) {
-                        up *= ex2u((float)(ev_ref - ev_max));
-                        ev_ref = ev_max;
+                    if (C::SPLIT && z_run > -CUDART_INF_F) {
+                        const int e = (int)ceilf(fminf(fmaxf(z_run - m_ref, -126.f), 127.f));
+                        d += (float)(ev_ref - e);
+                        ev_ref = e;
                     }
+                    up = ex2u(d);
                 }
                 if (t > 0) {  // the output holds the tiles before t: wait for them; half of the dims each
                     ok = twait(&sm.pv_done[(t - 1) % C::SB], ((t - 1) / C::SB) & 1, sm);
@@ -847,27 +926,43 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
             }
             const float mb = (m_ref == -CUDART_INF_F ? 0.f : m_ref) - kBias2;
             uint32_t p32[32];  // hi parts, then lo parts
+            if (C::SPLIT && apart) {
+                const uint32_t* e4 = reinterpret_cast<const uint32_t*>(sm.ev[rv.i] + half * 32);
 #pragma unroll
-            for (int q = 0; q < NG; q++) {
-                // V's slots are 2^-ev of themselves and the output 2^-ev_ref: p takes the difference
-                const float shift = C::SPLIT && ev[q] != kNoExp ? (float)(ev[q] - ev_ref) : 0.f;
-                const float2 ff = both(f[q]), mm = both(shift - mb);
-                float2 sum[2] = {};
+                for (int i = 0; i < 32; i += 2) {
+                    float w[2];
 #pragma unroll
-                for (int i = 0; i < W; i += 2) {
-                    const float2 y = fma2(make_float2(s[q * W + i], s[q * W + i + 1]), ff, mm);
-                    const float2 p = make_float2(ex2u(y.x), ex2u(y.y));
-                    sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], p);
-                    split2(p, p32[(q * W + i) / 2], p32[16 + (q * W + i) / 2]);
+                    for (int k = 0; k < 2; k++) {
+                        const int e = exp_of(e4[i / 4], (i + k) % 4);
+                        const float y = s[i + k] * f[i / W] - mb;
+                        l += ex2u(y);
+                        w[k] = e == kNoExp ? 0.f : ex2u(y + (float)(e - ev_ref));
+                    }
+                    split2(make_float2(w[0], w[1]), p32[i / 2], p32[16 + i / 2]);
                 }
-                const float2 add = add2(sum[0], sum[1]);
-                if (C::SPLIT && shift < -8.f) {  // small values: p's sum apart from their factor
-                    float z = 0.f;
+            } else {
 #pragma unroll
-                    for (int i = 0; i < W; i++) z += ex2u(s[q * W + i] * f[q] - mb);
-                    l += z;
-                } else {
-                    l += C::SPLIT ? (add.x + add.y) * ex2u(-shift) : add.x + add.y;
+                for (int q = 0; q < NG; q++) {
+                    // V's slots are 2^-ev of themselves and the output 2^-ev_ref: p takes the difference
+                    const float shift = C::SPLIT && ev[q] != kNoExp ? (float)(ev[q] - ev_ref) : 0.f;
+                    const float2 ff = both(f[q]), mm = both(shift - mb);
+                    float2 sum[2] = {};
+#pragma unroll
+                    for (int i = 0; i < W; i += 2) {
+                        const float2 y = fma2(make_float2(s[q * W + i], s[q * W + i + 1]), ff, mm);
+                        const float2 p = make_float2(ex2u(y.x), ex2u(y.y));
+                        sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], p);
+                        split2(p, p32[(q * W + i) / 2], p32[16 + (q * W + i) / 2]);
+                    }
+                    const float2 add = add2(sum[0], sum[1]);
+                    if (C::SPLIT && shift < -8.f) {  // small values: p's sum apart from their factor
+                        float z = 0.f;
+#pragma unroll
+                        for (int i = 0; i < W; i++) z += ex2u(s[q * W + i] * f[q] - mb);
+                        l += z;
+                    } else {
+                        l += C::SPLIT ? (add.x + add.y) * ex2u(-shift) : add.x + add.y;
+                    }
                 }
             }
             tmem_st32(s_addr, p32);

@@ -732,6 +732,92 @@ def test_attention_tree_long_sums(af, t):
     assert (err / norm) ** 0.5 <= 24 * 2.0 ** -23 + 2.0 ** -20
 
 
+def on_gpu(af, t, k, v, kvh, d):
+    """A cache of k, v [m, kvh, d] (device, fp32) and what it holds, float64 [kvh, m, d] on the device."""
+    m = k.shape[0]
+    cache = new_cache(t, kvh, m, d)
+    write(af, t, cache, k.reshape(m, kvh * d), v.reshape(m, kvh * d), kvh, d, m)
+    back = [torch.empty(m, kvh * d, device="cuda") for _ in range(2)]
+    af.af_kv_read(*cache, af.KVTYPE[t], kvh, d, m, m, None, 0, *back, kvh * d)
+    return cache, *(x.view(m, kvh, d).transpose(0, 1).double() for x in back)
+
+
+def attn_ref_gpu(q, k, v, see, past):
+    """attn_ref on the device: q [n, H, D] float32 array, k and v [KVH, m, D] float64 on the device -> [n, H, D]."""
+    n, H, D = q.shape
+    G = H // k.shape[0]
+    seen = torch.cat((torch.ones(n, past, dtype=torch.bool), torch.from_numpy(see)), 1).cuda()
+    out = torch.empty(n, H, D, dtype=torch.float64, device="cuda")
+    for h in range(H):
+        z = torch.from_numpy(q[:, h].astype(np.float64)).cuda() @ k[h // G].T * D ** -0.5
+        out[:, h] = torch.softmax(torch.where(seen, z, -torch.inf), -1) @ v[h // G]
+    return out
+
+
+LARGE = [("f32", 1e3), ("f32", 1e4), ("f32", 1e6), ("f32", 1e30), ("f32", float(np.finfo(np.float32).max)),
+         ("f16", 65504.0), ("q8_0", 1e3), ("q8_0", 1e6), ("q8_0", 127 * 65504.0), ("q4_0", 1e3), ("q4_0", 8 * 65504.0)]
+
+
+@pytest.mark.parametrize("t,size", LARGE)
+@pytest.mark.parametrize("what", ["k", "v", "kv"])
+@pytest.mark.parametrize("D,past,n", [(64, 50, 20), (128, 50, 24), (128, 0, 130), (64, 300, 130)])
+def test_attention_tree_large_hidden_slots_reach_no_row(af, t, size, what, D, past, n):
+    """A slot that holds large finite numbers (an unwritten one of a padded tree, a mask's lowest value) costs the rows that
+    do not see it nothing, in slots next to it and in later ones.  In the result's norm: the parts of q, k, p and v move
+    scores and products by 2^-21 each, sums, exponential and join by as much: 2^-18 holds them four times over."""
+    H, KVH, j = 8, 2, 1
+    rng = np.random.default_rng(23)
+    m = past + n
+    k, v = (rng.standard_normal((m, KVH, D)).astype(np.float32) for _ in range(2))
+    q = rng.standard_normal((n, H, D)).astype(np.float32)
+    see, _ = closure(random_parents(rng, n))
+    see[:, j] = False
+    see[j, j] = True
+    tol = attn_tol(q, k.transpose(1, 0, 2), v.transpose(1, 0, 2))
+    big = (rng.choice([-1.0, 1.0], (KVH, D)) * rng.uniform(0.5, 1, (KVH, D)) * size).astype(np.float32)
+    big[:, ::32] = np.float32(size)  # the largest magnitude of each block
+    if t == "q4_0":
+        big[:, ::32] = -np.float32(size)
+    if "k" in what:
+        k[past + j] = big
+    if "v" in what:
+        v[past + j] = big
+    cache, kh, vh = on_gpu(af, t, _dev(k), _dev(v), KVH, D)
+    assert torch.isfinite(kh).all() and torch.isfinite(vh).all()
+    got = attend(af, t, cache, q, H, KVH, D, m, past, see).double().view(n, H, D)
+    ref = attn_ref_gpu(q, kh, vh, see, past)
+    rest = [i for i in range(n) if i != j]
+    err = (got - ref)[rest].abs().max().item()
+    assert err <= tol, (err, tol)
+    norm = ((got - ref)[rest].norm() / ref[rest].norm()).item()
+    print(f"norm {norm:.2e}")
+    assert norm <= 2.0 ** -18
+
+
+@pytest.mark.parametrize("t,size", [("f32", 1e3), ("f32", 1e6), ("f32", 1e30), ("f16", 6e4), ("q8_0", 1e3), ("q8_0", 1e6),
+                                    ("q4_0", 1e3), ("q4_0", 1e5)])
+@pytest.mark.parametrize("at", [5, 290, 611])
+@pytest.mark.parametrize("n", [24, 70])
+def test_attention_tree_large_slot_of_no_weight(af, t, size, at, n):
+    """A slot that every row sees, with a key far from all queries (its weight is below 2^-150) and large values: the other
+    slots' scores and values keep their precision."""
+    H, KVH, D, past = 8, 2, 128, 700
+    rng = np.random.default_rng(24)
+    m = past + n
+    k, v = (rng.standard_normal((m, KVH, D)).astype(np.float32) for _ in range(2))
+    q = (rng.standard_normal((n, H, D)) + 0.5).astype(np.float32)
+    see, _ = closure(random_parents(rng, n))
+    tol = attn_tol(q, k.transpose(1, 0, 2), v.transpose(1, 0, 2))
+    k[at], v[at] = -200.0, size * rng.choice([-1.0, 1.0], (KVH, D))
+    cache, kh, vh = on_gpu(af, t, _dev(k), _dev(v), KVH, D)
+    got = attend(af, t, cache, q, H, KVH, D, m, past, see).double().view(n, H, D)
+    z = torch.einsum("nhd,hd->nh", torch.from_numpy(q).cuda().double(), kh[:, at].repeat_interleave(H // KVH, 0)) * D ** -0.5
+    far = z < -150 - 20  # (the others' scores are above -20)
+    assert far.float().mean() > 0.9
+    err = ((got - attn_ref_gpu(q, kh, vh, see, past)).abs().amax(-1) * far).max().item()
+    assert err <= tol, (err, tol)
+
+
 # ---------------------------------------------------------------- together
 
 @pytest.mark.parametrize("t", KV)
