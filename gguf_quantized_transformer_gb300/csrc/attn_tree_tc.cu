@@ -36,6 +36,7 @@
 #include <math_constants.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "draft.cuh"
 #include "tcgen05.cuh"
@@ -52,7 +53,7 @@ constexpr int kRows = 128;
 constexpr float kLazy2 = 4.f, kBias2 = 8.f;  // as attn_tree.cu's
 constexpr int kConvWarps = 4;  // for K, and as many for V: 16 slots of a tile each
 constexpr int kNoExp = -128, kMaxExp = 126;  // exponents of slots: of zeros, and the largest (an infinity's too)
-constexpr int kNoRef = -1000;  // the output's reference exponent before it has one
+constexpr float kNoRef = -1000.f;  // the output's reference exponent before it has one
 constexpr int kSpread = 3;     // 16 slots whose exponents differ by more than this have their own
 constexpr int kSoftWarps = 8;  // two per 32 rows
 
@@ -89,9 +90,11 @@ struct TcCfgT {
 // Of pairs, [0] is K's and [1] V's.
 template <typename C>
 struct alignas(1024) TcState {  // (the operand slots behind it need 1024 bytes)
-    static constexpr int NR = C::NR ? C::NR : 1;
-    int8_t ek[C::EK][BK], ev[C::NS][BK];  // exponents of the slots' K by tile, of V by operand slot (kNoExp: zeros)
-    uint32_t ek_own[C::EK], ev_own[C::NS];  // by byte: whether 16 slots have exponents of their own
+    static constexpr int NR = C::NR ? C::NR : 1, NE = C::SPLIT ? C::NS : 1;
+    // by tile and 16 slots, K's 2^exponent (infinity: the slots have exponents of their own); by operand slot, V's exponent
+    // (infinity likewise, NaN: zeros)
+    float kf[C::EK][4], vf[NE][4];
+    int8_t ek[C::EK][BK], ev[NE][BK];  // the slots' exponents (kNoExp: zeros)
     uint64_t full[2][C::NS], empty[2][C::NS];  // operand slots
     uint64_t raw_full[2][NR], raw_empty[2][NR];  // staging slots
     uint64_t s_full[C::SB], p_full[C::SB], pv_done[C::SB];
@@ -196,6 +199,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
+}
+
+// The factor of scores, from q's and K's powers of two
+__device__ __forceinline__ float score_factor(float qf, float kf) {
+    return fminf(fmaxf(qf * kf, 0x1p-126f), 0x1p126f);  // (0 or inf times -inf or 0: NaN)
 }
 
 // x = hi + lo in fp16 (lo off by at most 2^-23 of x, or half of fp16's smallest step 2^-24)
@@ -309,24 +317,29 @@ __device__ __forceinline__ unsigned row_max(const uint8_t* st, const uint8_t* sc
 
 // The exponents with which a warp's 16 rows are stored: row `lane`'s own one and the factor 2^-that (NaN: the row holds an
 // infinity or a NaN, and every row of q sees it, since others are taken out: at its exponent the finite values would
-// vanish), or one for all.
+// vanish).  Where they differ little, all rows have the largest.
 struct RowExps {
-    int e;        // of row `lane` (< 16); kNoExp: zeros
-    float down, common;
+    int e;       // of row `lane` (< 16); kNoExp: zeros
+    float down;
+    int hi;
+    unsigned largest;  // bits of the largest value
     bool own;
+    __device__ __forceinline__ float factor() const { return pow2i(hi); }
+    __device__ __forceinline__ float exponent() const { return hi == kNoExp ? CUDART_NAN_F : (float)hi; }
 };
 template <int TYPE>
-__device__ __forceinline__ RowExps row_exps(unsigned bits, int lane) {
+__device__ __forceinline__ RowExps row_exps(unsigned bits) {
     // largest value in [1, 2), or largest scale times its largest code in [1, 4)
     constexpr int code = TYPE == AF_KV_Q8_0 ? 6 : TYPE == AF_KV_Q4_0 ? 2 : 0;
-    const bool some = lane < 16 && bits != 0, inf = bits >= 0x7F800000u;
-    const int e = min(max((int)(bits >> 23) - 127, -126) + code, kMaxExp);
-    const int hi = __reduce_max_sync(0xffffffffu, some ? e : kNoExp), lo = __reduce_min_sync(0xffffffffu, some ? e : 127);
+    auto exponent = [](unsigned b) { return b ? min(max((int)(b >> 23) - 127, -126) + code, kMaxExp) : kNoExp; };
     RowExps x;
-    x.own = __any_sync(0xffffffffu, inf) || hi - lo > kSpread;
-    x.e = !x.own ? hi : some ? e : kNoExp;
+    x.largest = __reduce_max_sync(0xffffffffu, bits);
+    x.hi = exponent(x.largest);
+    const int e = exponent(bits);
+    const bool inf = bits >= 0x7F800000u;
+    x.own = __any_sync(0xffffffffu, inf || (e != kNoExp && e < x.hi - kSpread));
+    x.e = x.own ? e : x.hi;
     x.down = inf ? CUDART_NAN_F : pow2i(-x.e);
-    x.common = pow2i(-hi);
     return x;
 }
 
@@ -343,21 +356,42 @@ __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<co
 __device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
 
 // The fp16 hi and lo parts of the warp's rows row0.., times their 2^-exponent, into a slot (SWIZZLE_128B atoms of 64 dims,
-// [64 slots][128 B] each).
+// [64 slots][128 B] each).  fp32 rows with exponents of their own are read again by store_own (rare: rolled, and apart
+// from the registers that keep the rows).
+template <int D>
+__device__ __forceinline__ uint32_t tile_offset(int key, int d0) {
+    return (uint32_t)((d0 >> 6) * BK * 128) + sw128(key, (d0 >> 3) & 7) + (d0 & 7) * 2;
+}
+template <int D>
+__device__ __noinline__ void store_own(uint8_t* dst, const uint8_t* st, const RowExps& x, int row0, int valid, int lane) {
+#pragma unroll 1
+    for (int i = 0; i < raw_pieces<AF_F32, D>(); i++) {
+        unsigned bad = 0;
+        const Raw<AF_F32> r = load_raw<AF_F32, D, true>(st, nullptr, i, valid, lane, bad);  // (past: non-finite rows become NaN)
+        const int idx = i * 32 + lane;
+        const float2 dd = both(__shfl_sync(0xffffffffu, x.down, idx / (D / 4)));
+        const uint32_t off = tile_offset<D>(row0 + idx / (D / 4), idx % (D / 4) * 4);
+        uint2 hi, lo;
+        split2(mul2(make_float2(__uint_as_float(r.a.x), __uint_as_float(r.a.y)), dd), hi.x, lo.x);
+        split2(mul2(make_float2(__uint_as_float(r.a.z), __uint_as_float(r.a.w)), dd), hi.y, lo.y);
+        *reinterpret_cast<uint2*>(dst + off) = hi;
+        *reinterpret_cast<uint2*>(dst + BK * D * 2 + off) = lo;
+    }
+}
 template <int TYPE, int D, bool NODES>
 __device__ __forceinline__ void store_tile(uint8_t* dst, const uint8_t* st, const uint8_t* sc, const RowExps& x, int row0, int valid,
                                            int lane, const Kept<TYPE, D>& kept) {
     constexpr int PPR = D / Raw<TYPE>::VALUES, PART = BK * D * 2;  // pieces per row
+    const float all = pow2i(-x.hi);
 #pragma unroll
     for (int i = 0; i < raw_pieces<TYPE, D>(); i++) {
         unsigned bad = 0;
         const Raw<TYPE> r = TYPE == AF_F32 ? kept.c[TYPE == AF_F32 ? i : 0] : load_raw<TYPE, D, NODES>(st, sc, i, valid, lane, bad);
         const int idx = i * 32 + lane, key = row0 + idx / PPR, d0 = idx % PPR * Raw<TYPE>::VALUES;
-        const float down = x.own ? __shfl_sync(0xffffffffu, x.down, idx / PPR) : x.common;
-        const uint32_t off = (uint32_t)((d0 >> 6) * BK * 128) + sw128(key, (d0 >> 3) & 7) + (d0 & 7) * 2;
+        const uint32_t off = tile_offset<D>(key, d0);
         if constexpr (TYPE == AF_F32) {
             const uint4 a = r.a;
-            const float2 dd = both(down);
+            const float2 dd = both(all);
             uint2 hi, lo;
             split2(mul2(make_float2(__uint_as_float(a.x), __uint_as_float(a.y)), dd), hi.x, lo.x);
             split2(mul2(make_float2(__uint_as_float(a.z), __uint_as_float(a.w)), dd), hi.y, lo.y);
@@ -367,7 +401,7 @@ __device__ __forceinline__ void store_tile(uint8_t* dst, const uint8_t* st, cons
             uint32_t hi[4], lo[4];
             // codes q are exact in fp16, and so is d 2^-e (11 bits); hi = fp16(q d), lo = q d - hi by a fused
             // multiply-add, exact as long as it is not below fp16's smallest step 2^-24
-            const __half2 d2 = __float2half2_rn(__half2float(r.d) * down);
+            const __half2 d2 = __float2half2_rn(__half2float(r.d) * __shfl_sync(0xffffffffu, x.down, idx / PPR));
             __half2 q[4];
             if constexpr (TYPE == AF_KV_Q8_0) {
                 const uint32_t w = r.a.x ^ 0x80808080u, y = r.a.y ^ 0x80808080u;
@@ -397,6 +431,43 @@ __device__ __forceinline__ void store_tile(uint8_t* dst, const uint8_t* st, cons
             *reinterpret_cast<uint4*>(dst + PART + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
     }
+}
+
+// Half of a tile (32 slots a thread) where keys or values differ too much for one exponent in 16 or 64 slots.  Its scores in
+// tensor memory become scores plus V's exponent (-infinity for zero values), so that the common code weighs them as if all
+// exponents were 0; the largest score and the sum of 2^(score - that) come back.  Rare, and out of line: among the
+// common tiles' code it cost them 3 to 8%.
+__device__ __noinline__ float2 own_scores(uint32_t s_addr, const int8_t* ek, const int8_t* ev, float rowf, unsigned see, unsigned bad) {
+    float m = -CUDART_INF_F, l = 0.f;
+    for (int c = 0; c < 32; c += 16) {
+        float s[16];
+        uint32_t u[16];
+        tmem_ld16(s_addr + c, s);
+#pragma unroll
+        for (int i = 0; i < 16; i++) {
+            s[i] *= score_factor(rowf, pow2i(ek[c + i]));
+            if (bad >> (c + i) & 1) s[i] = CUDART_NAN_F;
+            if (!(see >> (c + i) & 1)) s[i] = -CUDART_INF_F;
+            m = fmaxf(m, s[i]);
+            u[i] = __float_as_uint(s[i]);
+        }
+        tmem_st16(s_addr + c, u);
+        tmem_st_wait();
+    }
+    const float m0 = m == -CUDART_INF_F ? 0.f : m;
+    for (int c = 0; c < 32; c += 16) {
+        float s[16];
+        uint32_t u[16];
+        tmem_ld16(s_addr + c, s);
+#pragma unroll
+        for (int i = 0; i < 16; i++) {
+            l += ex2u(s[i] - m0);
+            u[i] = __float_as_uint(s[i] + (ev[c + i] == kNoExp ? -CUDART_INF_F : (float)ev[c + i]));
+        }
+        tmem_st16(s_addr + c, u);
+        tmem_st_wait();
+    }
+    return make_float2(m, l);
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -459,7 +530,7 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
         return reinterpret_cast<float4*>(smem + C::OFF_V + (C::NS - C::QS) * C::SLOT + (quad * 32 + rr) * D * 4 + ((c ^ (rr & 7)) << 4));
     };
     float row_l = 0.f, row_m = 0.f;  // (softmax threads) the row's sum, maximum and exponent
-    int row_ev = 0;
+    float row_ev = 0.f;
     pdl_wait();  // q, the mask and the cache are written by earlier kernels
 
     if (warp == C::MMA_WARP) {
@@ -664,24 +735,23 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                     m = row_max<TYPE, D, true>(rows, scales, left, lane, bad, kept);
                 else
                     m = row_max<TYPE, D, false>(rows, scales, left, lane, bad, kept);
-                const RowExps exps = row_exps<TYPE>(m, lane);
-                if (TYPE == AF_F32) {
-                    const unsigned all = __reduce_or_sync(0xffffffffu, m);
-                    if (lane == 0) mbar_arrive_after(&sm.raw_empty[x][mine], all);
-                }
+                const RowExps exps = row_exps<TYPE>(m);
+                if (TYPE == AF_F32 && !exps.own && lane == 0) mbar_arrive_after(&sm.raw_empty[x][mine], exps.largest);
                 if (bad) atomicOr(&sm.bad[t - tn], (unsigned long long)bad << (w * 16));
                 if (t >= C::NS) ok = twait(&sm.empty[x][ro.i], ro.ph ^ 1, sm);
                 if (x == 1 && t == C::NS - C::QS) ok = ok && twait(&sm.q_ready, 0, sm);
                 if (!ok) break;
                 uint8_t* dst = smem + (x ? C::OFF_V : 0) + ro.i * C::SLOT;
-                if (t >= tn)
+                if (TYPE == AF_F32 && exps.own)
+                    store_own<D>(dst, rows, exps, w * 16, left, lane);
+                else if (t >= tn)
                     store_tile<TYPE, D, true>(dst, rows, scales, exps, w * 16, left, lane, kept);
                 else
                     store_tile<TYPE, D, false>(dst, rows, scales, exps, w * 16, left, lane, kept);
                 if (lane < 16) (x ? sm.ev[ro.i] : sm.ek[t % C::EK])[w * 16 + lane] = (int8_t)exps.e;
-                if (lane == 0) reinterpret_cast<uint8_t*>(x ? &sm.ev_own[ro.i] : &sm.ek_own[t % C::EK])[w] = exps.own;
+                if (lane == 0) (x ? sm.vf[ro.i] : sm.kf[t % C::EK])[w] = exps.own ? CUDART_INF_F : x ? exps.exponent() : exps.factor();
                 __syncwarp();
-                if (TYPE != AF_F32 && lane == 0) mbar_arrive(&sm.raw_empty[x][mine]);
+                if ((TYPE != AF_F32 || exps.own) && lane == 0) mbar_arrive(&sm.raw_empty[x][mine]);
                 fence_proxy_async_shared();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.full[x][ro.i]);
@@ -762,43 +832,32 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
         float m_ref = -CUDART_INF_F, l = 0.f;
         // The output holds sums of w V 2^-ev, w = p 2^(ev - ev_ref): ev_ref keeps the largest score plus exponent of V so far
         // (z_run) near m_ref + ev_ref.
-        int ev_ref = kNoRef;
-        float z_run = -CUDART_INF_F;
-        auto factor = [&](int e) {  // of scores, from q's and K's exponents
-            return fminf(fmaxf(rowf * pow2i(e), 0x1p-126f), 0x1p126f);  // (0 or inf times -inf or 0: NaN)
-        };
-        auto exp_of = [](uint32_t word, int i) { return (int)(word << (24 - 8 * i)) >> 24; };  // byte i, signed
+        float ev_ref = kNoRef, z_run = -CUDART_INF_F;
         Ring<C::NS> rv;
         for (int t = 0; ok && t < T; t++, rv.next()) {
             const int b = t % C::SB;
-            const unsigned ph = (t / C::SB) & 1;
             const bool nodes = t >= tn;
             const unsigned see = nodes ? window((t0 + t) * BK - a.past + half * 32) : ~0u;
-            ok = twait(&sm.s_full[b], ph, sm);
+            ok = twait(&sm.s_full[b], (t / C::SB) & 1, sm);
             if (!ok) break;
-            float f[NG];
-            int ev[NG] = {}, ev_hi = kNoExp;
-            bool apart = false;  // V's exponents differ too much for the largest to stand for all
             if (C::SPLIT || nodes) {
                 ok = twait(&sm.full[1][rv.i], rv.ph, sm);  // V's exponents are there (K's since its scores were issued)
                 if (!ok) break;
             }
+            float f[NG], ev[NG], ev_hi = 0.f;
+            bool apart = false;  // exponents differ too much for one in 16 (V: in 64) slots
 #pragma unroll
             for (int q = 0; q < NG; q++) f[q] = rowf;
             if (C::SPLIT) {
-                int ev_lo = 127;
-#pragma unroll
-                for (int q = 0; q < 4; q++) {
-                    const int e = sm.ev[rv.i][16 * q];
-                    ev_hi = max(ev_hi, e);
-                    if (e != kNoExp) ev_lo = min(ev_lo, e);
-                }
-                apart = sm.ev_own[rv.i] || ev_hi - ev_lo > kSpread;
-#pragma unroll
-                for (int q = 0; q < NG; q++) {
-                    f[q] = factor(sm.ek[t % C::EK][half * 32 + q * W]);
-                    ev[q] = sm.ev[rv.i][half * 32 + q * W];
-                }
+                const float4 kf = *reinterpret_cast<const float4*>(sm.kf[t % C::EK]);
+                const float4 vf = *reinterpret_cast<const float4*>(sm.vf[rv.i]);
+                f[0] = score_factor(rowf, half ? kf.z : kf.x);
+                f[NG - 1] = score_factor(rowf, half ? kf.w : kf.y);
+                ev_hi = fmaxf(fmaxf(vf.x, vf.y), fmaxf(vf.z, vf.w));  // (not of zeros, NaN)
+                const float ev_lo = fminf(fminf(vf.x, vf.y), fminf(vf.z, vf.w));
+                apart = !(ev_hi - ev_lo <= (float)kSpread) || fmaxf(fmaxf(kf.x, kf.y), fmaxf(kf.z, kf.w)) == CUDART_INF_F;
+                ev[0] = half ? vf.z : vf.x;
+                ev[NG - 1] = half ? vf.w : vf.y;
             }
             if (!C::SPLIT && nodes) {  // V of this tile: zeros where it is not finite, and behind the last node
                 uint8_t* v = smem + C::OFF_V + rv.i * C::SLOT;
@@ -828,15 +887,21 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
             }
             tc_fence_after();
             const uint32_t s_addr = lane_addr + C::SCOL + b * BK + half * 32;
+            float own_m = 0.f, own_l = 0.f;
+            if (C::SPLIT && apart) {  // (the same in every lane and in both warps of a row)
+                const unsigned bad = nodes ? (unsigned)(*(volatile unsigned long long*)&sm.bad[t - tn] >> (half * 32)) : 0u;
+                const float2 own = own_scores(s_addr, sm.ek[t % C::EK] + half * 32, sm.ev[rv.i] + half * 32, rowf, see, bad);
+                sm.pair_x[t & 1][quad][half][lane] = own.x;
+                ok = meet();
+                own_m = fmaxf(own.x, sm.pair_x[t & 1][quad][half ^ 1][lane]);
+                ok = ok && meet();  // (both have read it)
+                if (!ok) break;
+                own_l = own.x == -CUDART_INF_F ? own.y : own.y * ex2u(own.x - own_m);
+#pragma unroll
+                for (int q = 0; q < NG; q++) f[q] = 1.f, ev[q] = 0.f;
+            }
             float s[32];
             tmem_ld32(s_addr, s);
-            if (C::SPLIT && sm.ek_own[t % C::EK]) {  // keys with exponents of their own
-                const uint32_t* e4 = reinterpret_cast<const uint32_t*>(sm.ek[t % C::EK] + half * 32);
-#pragma unroll
-                for (int i = 0; i < 32; i++) s[i] *= factor(exp_of(e4[i / 4], i % 4));
-#pragma unroll
-                for (int q = 0; q < NG; q++) f[q] = 1.f;
-            }
             if (nodes) {
                 const unsigned bad = (unsigned)(*(volatile unsigned long long*)&sm.bad[t - tn] >> (half * 32));
 #pragma unroll
@@ -860,24 +925,11 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
             ok = meet();
             if (!ok) break;
             mt = fmaxf(mt, sm.pair_x[t & 1][quad][half ^ 1][lane]);
-            float z = C::SPLIT && ev_hi != kNoExp ? mt + (float)ev_hi : -CUDART_INF_F;
-            if (C::SPLIT && apart) {  // (the same in both warps)
-                z = -CUDART_INF_F;
-                const uint32_t* e4 = reinterpret_cast<const uint32_t*>(sm.ev[rv.i] + half * 32);
-#pragma unroll
-                for (int i = 0; i < 32; i++) {
-                    const int e = exp_of(e4[i / 4], i % 4);
-                    if (e != kNoExp) z = fmaxf(z, s[i] * f[i / W] + (float)e);
-                }
-                sm.pair_x[(t & 1) ^ 1][quad][half][lane] = z;  // (both have read the previous tile's)
-                ok = meet();
-                z = fmaxf(z, sm.pair_x[(t & 1) ^ 1][quad][half ^ 1][lane]);
-                ok = ok && meet();  // (both have read it: the next tile's may be written)
-                if (!ok) break;
-            }
+            const float z = C::SPLIT && apart ? mt : mt + ev_hi;  // the largest score plus exponent of V
+            if (C::SPLIT && apart) mt = own_m;
             z_run = fmaxf(z_run, z);
             const bool move = mt > m_ref + kLazy2;
-            const bool grow = C::SPLIT && z > m_ref + (float)ev_ref + kLazy2;
+            const bool grow = C::SPLIT && z > m_ref + ev_ref + kLazy2;
             const bool flush = t > 0 && t % kFlush == 0;  // the output sum starts again with this tile
             const bool change = __any_sync(0xffffffffu, move || grow);  // (the same in both warps)
             if (change || flush) {
@@ -890,8 +942,8 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
                         l *= ex2u(d);
                     }
                     if (C::SPLIT && z_run > -CUDART_INF_F) {
-                        const int e = (int)ceilf(fminf(fmaxf(z_run - m_ref, -126.f), 127.f));
-                        d += (float)(ev_ref - e);
+                        const float e = ceilf(fminf(fmaxf(z_run - m_ref, -126.f), 127.f));
+                        d += ev_ref - e;
                         ev_ref = e;
                     }
                     up = ex2u(d);
@@ -926,43 +978,29 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
             }
             const float mb = (m_ref == -CUDART_INF_F ? 0.f : m_ref) - kBias2;
             uint32_t p32[32];  // hi parts, then lo parts
-            if (C::SPLIT && apart) {
-                const uint32_t* e4 = reinterpret_cast<const uint32_t*>(sm.ev[rv.i] + half * 32);
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                    float w[2];
+            for (int q = 0; q < NG; q++) {
+                // V's slots are 2^-ev of themselves and the output 2^-ev_ref: p takes the difference
+                const float shift = C::SPLIT ? fmaxf(ev[q] - ev_ref, kNoRef) : 0.f;  // (zeros: NaN)
+                const float2 ff = both(f[q]), mm = both(shift - mb);
+                float2 sum[2] = {};
 #pragma unroll
-                    for (int k = 0; k < 2; k++) {
-                        const int e = exp_of(e4[i / 4], (i + k) % 4);
-                        const float y = s[i + k] * f[i / W] - mb;
-                        l += ex2u(y);
-                        w[k] = e == kNoExp ? 0.f : ex2u(y + (float)(e - ev_ref));
-                    }
-                    split2(make_float2(w[0], w[1]), p32[i / 2], p32[16 + i / 2]);
+                for (int i = 0; i < W; i += 2) {
+                    const float2 y = fma2(make_float2(s[q * W + i], s[q * W + i + 1]), ff, mm);
+                    const float2 p = make_float2(ex2u(y.x), ex2u(y.y));
+                    sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], p);
+                    split2(p, p32[(q * W + i) / 2], p32[16 + (q * W + i) / 2]);
                 }
-            } else {
+                const float2 add = add2(sum[0], sum[1]);
+                if (C::SPLIT && apart) {
+                    if (q == 0) l += own_l * ex2u(own_m - mb);
+                } else if (C::SPLIT && shift < -8.f) {  // small values: p's sum apart from their factor
+                    float z = 0.f;
 #pragma unroll
-                for (int q = 0; q < NG; q++) {
-                    // V's slots are 2^-ev of themselves and the output 2^-ev_ref: p takes the difference
-                    const float shift = C::SPLIT && ev[q] != kNoExp ? (float)(ev[q] - ev_ref) : 0.f;
-                    const float2 ff = both(f[q]), mm = both(shift - mb);
-                    float2 sum[2] = {};
-#pragma unroll
-                    for (int i = 0; i < W; i += 2) {
-                        const float2 y = fma2(make_float2(s[q * W + i], s[q * W + i + 1]), ff, mm);
-                        const float2 p = make_float2(ex2u(y.x), ex2u(y.y));
-                        sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], p);
-                        split2(p, p32[(q * W + i) / 2], p32[16 + (q * W + i) / 2]);
-                    }
-                    const float2 add = add2(sum[0], sum[1]);
-                    if (C::SPLIT && shift < -8.f) {  // small values: p's sum apart from their factor
-                        float z = 0.f;
-#pragma unroll
-                        for (int i = 0; i < W; i++) z += ex2u(s[q * W + i] * f[q] - mb);
-                        l += z;
-                    } else {
-                        l += C::SPLIT ? (add.x + add.y) * ex2u(-shift) : add.x + add.y;
-                    }
+                    for (int i = 0; i < W; i++) z += ex2u(s[q * W + i] * f[q] - mb);
+                    l += z;
+                } else {
+                    l += C::SPLIT ? (add.x + add.y) * ex2u(-shift) : add.x + add.y;
                 }
             }
             tmem_st32(s_addr, p32);
@@ -996,7 +1034,7 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
         if (!gave_up) {  // every operand has been read: the ring is free
             constexpr int HC = CPR / 2;  // chunks of half a row
             tc_fence_after();
-            float up = C::SPLIT ? pow2i(row_ev) : 1.f;
+            float up = C::SPLIT ? pow2i((int)row_ev) : 1.f;
             if (last) up = row_l == 0.f ? 0.f : up / row_l;
 #pragma unroll 1
             for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
