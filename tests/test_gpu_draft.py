@@ -794,6 +794,13 @@ def test_attention_tree_large_hidden_slots_reach_no_row(af, t, size, what, D, pa
     assert norm <= 2.0 ** -18
 
 
+@pytest.mark.parametrize("t,size", [x for x in LARGE if x[0] in ("f32", "f16")])
+@pytest.mark.parametrize("what", ["k", "v", "kv"])
+@pytest.mark.parametrize("D,past,n", [(64, 50, 2), (128, 50, 3), (64, 40, 7)])
+def test_attention_tree_large_hidden_slots_of_few_rows(af, t, size, what, D, past, n):
+    test_attention_tree_large_hidden_slots_reach_no_row(af, t, size, what, D, past, n)
+
+
 @pytest.mark.parametrize("t,size", [("f32", 1e3), ("f32", 1e6), ("f32", 1e30), ("f16", 6e4), ("q8_0", 1e3), ("q8_0", 1e6),
                                     ("q4_0", 1e3), ("q4_0", 1e5)])
 @pytest.mark.parametrize("at", [5, 290, 611])
