@@ -14,8 +14,11 @@
 //    two per row, so no magnitude overflows) or tf32; so is p.
 //  - fp16 cache: K and V are operands as they are; two products each (hi and lo).
 //  - Q8_0 / Q4_0: the integer codes are exact fp16 operands.  A key's scale multiplies its fp32 partial score of
-//    each 32-value block; a value's scale multiplies p, per block, before p is split (with a power of two that
-//    follows the largest scale seen, so that p d stays in fp16's range).
+//    each 32-value block; a value's scale multiplies p, per block, before p is split.  Both stay in fp16's range: a
+//    thread takes its slots' scales times 2^-ev, which brings them near 1, and p times 2^(ev - ov), where the row's
+//    exponent ov follows the largest p 2^ev of the slots that the row sees.  A stage in which a thread's scales are
+//    more than 2^8 apart (one large scale, hidden or not, would leave the others few bits) is walked again for the
+//    smaller ones.
 //  - fp32 cache: tf32 parts of K and V too, three products (the dropped lo lo product is 2^-21 relative at most).
 // The reference maximum of the softmax moves only when a score exceeds it by more than 4 (in powers of two); p
 // carries a factor 2^8 so that small p keep their low part above fp16's subnormal step.  Sums are fp32.
@@ -29,6 +32,7 @@
 #include <math_constants.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "draft.cuh"
 #include "tma.cuh"
@@ -64,6 +68,7 @@ __global__ void __launch_bounds__(256)
 constexpr float kLog2eT = 1.4426950408889634f;
 constexpr float kLazyT = 4.f;  // powers of two by which a score may exceed the reference maximum
 constexpr float kBiasT = 8.f;  // p = 2^(s - m + kBiasT): at most 2^12
+constexpr float kNoRefT = -1000.f;  // a row's exponent of the output before it has one
 
 __device__ __forceinline__ float ex2t(float x) {
     float y;
@@ -410,22 +415,28 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT_>::NW * 32, 1) attn_tree_k
     };
 
     float o[MT][NT][4] = {}, m_ref[MT][NH], l[MT][NH] = {};
+    // Quantized: this thread's scales are taken times 2^-ev (above vlim / 2^8 and up to vlim = 2^(ev + 2)), p times 2^(ev - ov),
+    // so that the output is held times 2^-ov and the thread's part of the sum times 2^(ev - ov).
+    float ov[MT][NH], ev = C::QUANT ? -15.f : 0.f, vlim = 0x1p-13f;
 #pragma unroll
     for (int mt = 0; mt < MT; mt++)
 #pragma unroll
-        for (int h = 0; h < NH; h++) m_ref[mt][h] = -CUDART_INF_F;
-    float vinv = 1.f, vlim = 0.f;  // quantized: V's scales are taken times vinv, a power of two
+        for (int h = 0; h < NH; h++) m_ref[mt][h] = -CUDART_INF_F, ov[mt][h] = C::QUANT ? kNoRefT : 0.f;
 
     int slot = 0;
     TreeScales scales;
 #pragma unroll
     for (int i = 0; i < C::NST - 1; i++) tree_put<TYPE, D, MT_>(first[i], lane);
-    for (int st = st0 + warp; st < st1; st += NW) {
-        cp_wait<C::NST - 2>();
-        tree_put<TYPE, D, MT_>(scales, lane);  // of the stage issued last, with NST = 2 this one
-        __syncwarp();  // every lane's copies of this stage have landed, and every lane is done with the previous one
-        asm volatile("" ::: "memory");
-        {  // the previous stage's slot takes the stage NST - 1 ahead
+    constexpr unsigned kAll = (1u << (2 * GT)) - 1;
+    unsigned todo = kAll;  // quantized: bit 2 t + i: this thread's slot 8 t + 2 c + i has to be walked yet
+    bool again = false;    // this stage has been walked and is so once more, for slots that are left
+    for (int st = st0 + warp; st < st1;) {
+        if (!again) {
+            cp_wait<C::NST - 2>();
+            tree_put<TYPE, D, MT_>(scales, lane);  // of the stage issued last, with NST = 2 this one
+            __syncwarp();  // every lane's copies of this stage have landed, and every lane is done with the previous one
+            asm volatile("" ::: "memory");
+            // the previous stage's slot takes the stage NST - 1 ahead
             const int nx = st + (C::NST - 1) * NW, ns = slot == 0 ? C::NST - 1 : slot - 1;
             scales.dst = 0;
             if (nx < st1) tree_issue<TYPE, D, MT_>(a.c, row0, nx * KS, keys, ring + ns * C::STAGE, lane, scales);
@@ -543,6 +554,74 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT_>::NW * 32, 1) attn_tree_k
         if (PACK)
 #pragma unroll
             for (int t = 0; t < GT; t++) s[0][t][0] += s[0][t][2], s[0][t][1] += s[0][t][3];
+        // ---- the slots of this walk of the stage, by the largest of their values' scales
+        uint32_t dv[C::QUANT ? GT : 1][NB];
+        again = false;
+        if constexpr (C::QUANT) {
+            __half2 most[GT], least = as_h2(0x7BFF7BFFu);  // by slot; of the slots that are not zeros
+            auto find = [&](auto finite) {
+#pragma unroll
+                for (int t = 0; t < GT; t++) {
+                    if (!decltype(finite)::value) load_scales<NB>(base + C::OVS + (t * 8 + 2 * c) * C::SB, dv[t]);
+                    most[t] = as_h2(0u);
+                    bool any = false;
+#pragma unroll
+                    for (int b = 0; b < NB; b++)
+                        most[t] = __hmax2(most[t], __habs2(as_h2(decltype(finite)::value ? finite_h2(dv[t][b], any) : dv[t][b])));
+                }
+            };
+            auto largest = [&]() {
+                __half2 x = most[0];
+#pragma unroll
+                for (int t = 1; t < GT; t++) x = __hmax2(x, most[t]);
+                return fmaxf(__low2float(x), __high2float(x));
+            };
+            find(std::false_type());
+#pragma unroll
+            for (int t = 0; t < GT; t++) least = __hmin2(least, __hfma2(__heq2(most[t], as_h2(0u)), as_h2(0x7BFF7BFFu), most[t]));
+            const float small = fminf(__low2float(least), __high2float(least));
+            if (__any_sync(0xffffffffu, todo != kAll || largest() > vlim || small < vlim * 0x1p-8f)) {
+                find(std::true_type());  // of the finite scales (an infinite one stays one) that have not been walked
+#pragma unroll
+                for (int t = 0; t < GT; t++)
+                    most[t] = as_h2(as_u(most[t]) & ((todo >> (2 * t) & 1 ? 0xFFFFu : 0u) | (todo >> (2 * t + 1) & 1 ? 0xFFFF0000u : 0u)));
+                const float big = largest(), limit = big * 0x1p-7f;
+                unsigned later = 0;
+#pragma unroll
+                for (int t = 0; t < GT; t++) {
+                    const float x0 = __low2float(most[t]), x1 = __high2float(most[t]);
+                    later |= (x0 != 0.f && x0 < limit ? 1u << (2 * t) : 0u) | (x1 != 0.f && x1 < limit ? 2u << (2 * t) : 0u);
+                }
+                const unsigned now = todo & ~later;
+                todo = later;
+                again = __any_sync(0xffffffffu, later != 0);
+                if (now != kAll) {
+#pragma unroll
+                    for (int t = 0; t < GT; t++) {
+                        const bool in0 = now >> (2 * t) & 1, in1 = now >> (2 * t + 1) & 1;
+#pragma unroll
+                        for (int b = 0; b < NB; b++) dv[t][b] &= (in0 ? 0xFFFFu : 0u) | (in1 ? 0xFFFF0000u : 0u);
+#pragma unroll
+                        for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+                            for (int h = 0; h < NH; h++) {
+                                if (!in0) s[mt][t][2 * h] = -CUDART_INF_F;
+                                if (!in1) s[mt][t][2 * h + 1] = -CUDART_INF_F;
+                            }
+                    }
+                }
+                if (big > 0.f) {  // (2^-ev is an fp16 number)
+                    const int e = min(max((int)(__float_as_uint(big) >> 23) - 127, -15), 14);
+                    const float f = ex2t((float)e - ev);
+                    ev = (float)e;
+                    vlim = __uint_as_float((unsigned)(e + 129) << 23);
+#pragma unroll
+                    for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+                        for (int h = 0; h < NH; h++) l[mt][h] *= f;
+                }
+            }
+        }
         // ---- mask and softmax
         float mx[MT][NH];
         bool move = false;
@@ -561,19 +640,30 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT_>::NW * 32, 1) attn_tree_k
                         x = fmaxf(x, v);
                     }
                 mx[mt][h] = x;
-                move |= x > m_ref[mt][h] + kLazyT;
+                move |= x > m_ref[mt][h] + (C::QUANT ? fminf(ov[mt][h] - ev, 0.f) + kLazyT : kLazyT);
             }
         if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
             for (int mt = 0; mt < MT; mt++)
 #pragma unroll
                 for (int h = 0; h < NH; h++) {
-                    float x = mx[mt][h];
+                    float x = mx[mt][h], z = x + ev;
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                    if (x > m_ref[mt][h]) {
-                        const float f = ex2t(m_ref[mt][h] - x);
-                        m_ref[mt][h] = x;
+                    if (C::QUANT) {
+                        z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 1));
+                        z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 2));
+                    }
+                    const bool grow = C::QUANT && z > m_ref[mt][h] + ov[mt][h];
+                    if (x > m_ref[mt][h] || grow) {
+                        float d = x > m_ref[mt][h] ? m_ref[mt][h] - x : 0.f;
+                        m_ref[mt][h] = fmaxf(m_ref[mt][h], x);
+                        if (C::QUANT) {  // m + ov follows z, and stays (rounded up: p 2^ev grows no larger) when m moves alone
+                            const float e = fmaxf(grow ? ceilf(z - m_ref[mt][h]) : ov[mt][h] + ceilf(d), -60.f);
+                            d += ov[mt][h] - e;
+                            ov[mt][h] = e;
+                        }
+                        const float f = ex2t(d);
                         l[mt][h] *= f;
 #pragma unroll
                         for (int t = 0; t < NT; t++) {
@@ -588,7 +678,7 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT_>::NW * 32, 1) attn_tree_k
         for (int mt = 0; mt < MT; mt++)
 #pragma unroll
             for (int h = 0; h < NH; h++) {
-                const float mb = m_ref[mt][h] == -CUDART_INF_F ? 0.f : m_ref[mt][h] - kBiasT;
+                const float mb = m_ref[mt][h] == -CUDART_INF_F ? 0.f : m_ref[mt][h] + (C::QUANT ? ov[mt][h] - ev - kBiasT : -kBiasT);
 #pragma unroll
                 for (int t = 0; t < GT; t++)
 #pragma unroll
@@ -600,34 +690,14 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT_>::NW * 32, 1) attn_tree_k
             }
         // ---- output, sixteen slots at a time
         bool bad = false;  // non-finite values among the nodes' slots, taken out of the product
-        uint32_t dv[C::QUANT ? GT : 1][NB];
         if constexpr (C::QUANT) {
-            __half2 big2 = as_h2(0u);
+            const __half2 down = __float2half2_rn(__uint_as_float((256u << 23) - __float_as_uint(vlim)));
 #pragma unroll
             for (int t = 0; t < GT; t++) {
-                load_scales<NB>(base + C::OVS + (t * 8 + 2 * c) * C::SB, dv[t]);
 #pragma unroll
                 for (int b = 0; b < NB; b++) {
                     if (nodes) dv[t][b] = finite_h2(dv[t][b], bad);
-                    big2 = __hmax2(big2, __habs2(as_h2(dv[t][b])));
-                }
-            }
-            float big = fmaxf(__low2float(big2), __high2float(big2));
-            if (__any_sync(0xffffffffu, big > vlim)) {
-                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-                if (big <= 65504.f) {  // (an infinite scale of the past makes its rows infinite or NaN as it is)
-                    const unsigned e = max(__float_as_uint(big) >> 23, 127u - 15u);  // 2^-exponent(big) is an fp16 number
-                    const float up = __uint_as_float((254u - e) << 23);
-                    const float f = up / vinv;
-                    vinv = up;
-                    vlim = 4.f * __uint_as_float(e << 23);
-#pragma unroll
-                    for (int mt = 0; mt < MT; mt++)
-#pragma unroll
-                        for (int t = 0; t < NT; t++)
-#pragma unroll
-                            for (int i = 0; i < 4; i++) o[mt][t][i] *= f;
+                    dv[t][b] = as_u(__hmul2(as_h2(dv[t][b]), down));
                 }
             }
         }
@@ -705,7 +775,6 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT_>::NW * 32, 1) attn_tree_k
                         }
                     }
                 } else {
-                    const __half2 v2 = __float2half2_rn(vinv);
 #pragma unroll
                     for (int b = 0; b < NB; b++) {
                         uint32_t vw[4][2];
@@ -730,7 +799,7 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT_>::NW * 32, 1) attn_tree_k
                             }
                         }
                         // p d in two parts: the fp16 product of p's high part, and what it lost plus p's low part's
-                        const __half2 d0 = __hmul2(as_h2(dv[2 * g16][b]), v2), d1 = __hmul2(as_h2(dv[2 * g16 + 1][b]), v2);
+                        const __half2 d0 = as_h2(dv[2 * g16][b]), d1 = as_h2(dv[2 * g16 + 1][b]);
 #pragma unroll
                         for (int mt = 0; mt < MT; mt++) {
                             uint4 hi, lo;
@@ -760,7 +829,6 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT_>::NW * 32, 1) attn_tree_k
         }
         if (nodes && __any_sync(0xffffffffu, bad)) {
             // rare: add p v of the non-finite values to the rows that see the slot
-            const float scale = C::QUANT ? vinv : 1.f;
 #pragma unroll
             for (int t8 = 0; t8 < GT; t8++)
 #pragma unroll 1
@@ -777,12 +845,16 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT_>::NW * 32, 1) attn_tree_k
 #pragma unroll
                                 for (int i = 0; i < 2; i++) {
                                     const float v = stage_value<TYPE, D, MT_>(base, key, C::odim(t, 2 * c + i));
-                                    if (!(fabsf(v) < CUDART_INF_F)) o[mt][t][2 * h + i] += p * (v * scale);
+                                    if (!(fabsf(v) < CUDART_INF_F)) o[mt][t][2 * h + i] += p * v;
                                 }
                         }
                 }
         }
-        slot = slot + 1 == C::NST ? 0 : slot + 1;
+        if (!again) {
+            todo = kAll;
+            st += NW;
+            slot = slot + 1 == C::NST ? 0 : slot + 1;
+        }
     }
     cp_wait<0>();
     __syncthreads();
@@ -793,13 +865,13 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT_>::NW * 32, 1) attn_tree_k
     // ---- join the warps: [warp][row][D] outputs, then [warp][row] (m, l)
     float* so = reinterpret_cast<float*>(smem + tree_q_bytes<TYPE, D, MT_>());
     float2* sml = reinterpret_cast<float2*>(so + NW * ROWS * C::DP);
-    const float back = C::QUANT ? 1.f / vinv : 1.f;
 #pragma unroll
     for (int mt = 0; mt < MT; mt++)
 #pragma unroll
         for (int h = 0; h < NH; h++) {
             const int r = mt * 16 + h * 8 + j;
-            float x = l[mt][h];
+            const float back = C::QUANT ? ex2t(ov[mt][h]) : 1.f;
+            float x = C::QUANT ? l[mt][h] * ex2t(ov[mt][h] - ev) : l[mt][h];
             x += __shfl_xor_sync(0xffffffffu, x, 1);
             x += __shfl_xor_sync(0xffffffffu, x, 2);
             if (c == 0) sml[warp * ROWS + r] = make_float2(m_ref[mt][h], x);

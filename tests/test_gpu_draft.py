@@ -794,7 +794,7 @@ def test_attention_tree_large_hidden_slots_reach_no_row(af, t, size, what, D, pa
     assert norm <= 2.0 ** -18
 
 
-@pytest.mark.parametrize("t,size", [x for x in LARGE if x[0] in ("f32", "f16")])
+@pytest.mark.parametrize("t,size", LARGE)
 @pytest.mark.parametrize("what", ["k", "v", "kv"])
 @pytest.mark.parametrize("D,past,n", [(64, 50, 2), (128, 50, 3), (64, 40, 7)])
 def test_attention_tree_large_hidden_slots_of_few_rows(af, t, size, what, D, past, n):
@@ -804,7 +804,7 @@ def test_attention_tree_large_hidden_slots_of_few_rows(af, t, size, what, D, pas
 @pytest.mark.parametrize("t,size", [("f32", 1e3), ("f32", 1e6), ("f32", 1e30), ("f16", 6e4), ("q8_0", 1e3), ("q8_0", 1e6),
                                     ("q4_0", 1e3), ("q4_0", 1e5)])
 @pytest.mark.parametrize("at", [5, 290, 611])
-@pytest.mark.parametrize("n", [24, 70])
+@pytest.mark.parametrize("n", [1, 3, 8, 24, 70])
 def test_attention_tree_large_slot_of_no_weight(af, t, size, at, n):
     """A slot that every row sees, with a key far from all queries (its weight is below 2^-150) and large values: the other
     slots' scores and values keep their precision."""
@@ -822,6 +822,38 @@ def test_attention_tree_large_slot_of_no_weight(af, t, size, at, n):
     far = z < -150 - 20  # (the others' scores are above -20)
     assert far.float().mean() > 0.9
     err = ((got - attn_ref_gpu(q, kh, vh, see, past)).abs().amax(-1) * far).max().item()
+    assert err <= tol, (err, tol)
+
+
+SMALL = [  # H, KVH, D, past, n: few rows over many slots
+    (32, 32, 128, 8200, 1), (32, 32, 64, 8200, 8), (32, 32, 128, 8200, 12), (32, 32, 64, 8200, 16), (32, 32, 128, 8200, 24),
+    (32, 32, 64, 8200, 32), (32, 8, 128, 40000, 2), (32, 8, 128, 40000, 8), (4, 1, 128, 60000, 1), (16, 1, 64, 60000, 2),
+]
+
+
+@pytest.mark.parametrize("t", KV)
+@pytest.mark.parametrize("H,KVH,D,past,n", SMALL)
+def test_attention_tree_few_rows_over_many_slots(af, t, H, KVH, D, past, n):
+    """Long walks of the small-row kernel: its rings go round, maxima and scales of values move on the way, the result is a
+    join of many parts.  Scores drift and values grow along the cache."""
+    g = torch.Generator(device="cuda").manual_seed(past + n)
+    m = past + n
+    along = torch.linspace(-1, 1, m, device="cuda")[:, None, None]
+    q = torch.randn(n, H, D, generator=g, device="cuda") + 0.3
+    k = torch.randn(m, KVH, D, generator=g, device="cuda") + 3 * along
+    v = torch.randn(m, KVH, D, generator=g, device="cuda") * torch.exp(3 * along)
+    cache, kh, vh = on_gpu(af, t, k, v, KVH, D)
+    see = np.tril(np.ones((n, n), bool))
+    q = q.cpu().numpy()
+    splits = af.af_attention_tree_workspace(af.KVTYPE[t], H, KVH, D, past, n) // (n * H * (D + 2) * 4)
+    if KVH == 1:
+        assert splits > 32
+    else:  # at most 384 slots a round of a block's warps
+        assert 1 < splits and m / splits > 5 * 384
+    got = attend(af, t, cache, q, H, KVH, D, m, past, see).double().view(n, H, D)
+    tol = attn_tol(q, kh.cpu().numpy(), vh.cpu().numpy())
+    err = (got - attn_ref_gpu(q, kh, vh, see, past)).abs().max().item()
+    print(f"err {err:.2e} tol {tol:.2e}")
     assert err <= tol, (err, tol)
 
 
