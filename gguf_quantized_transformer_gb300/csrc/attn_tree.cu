@@ -20,6 +20,9 @@
 //    more than 2^8 apart (one large scale, hidden or not, would leave the others few bits) is walked again for the
 //    smaller ones.
 //  - fp32 cache: tf32 parts of K and V too, three products (the dropped lo lo product is 2^-21 relative at most).
+// The tensor cores cut their fp32 sums (every product takes up to 2^-23 of the sum, towards zero: one sum over a warp's 80
+// stages of fp32 slots was off by 1.1e-5 of the result's norm), so a stage's output starts from zero and is added,
+// rounded, to the walk's: 1.2e-7.  (fp32, 1 and 4 tokens over 30000 slots: 48.3 and 65.9 us, 45.2 and 55.7 with one sum.)
 // The reference maximum of the softmax moves only when a score exceeds it by more than 4 (in powers of two); p
 // carries a factor 2^8 so that small p keep their low part above fp16's subnormal step.  Sums are fp32.
 //
@@ -122,6 +125,27 @@ __device__ __forceinline__ void mma8(float (&c)[4], const uint4& a, uint32_t b0,
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
+// The same onto zero
+__device__ __forceinline__ void mma16z(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma8z(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.f));
+}
+// o += c, rounded: a stage's sum joins the walk's
+__device__ __forceinline__ void add4(float (&o)[4], const float (&c)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+        const float2 x = add2(make_float2(o[i], o[i + 1]), make_float2(c[i], c[i + 1]));
+        o[i] = x.x, o[i + 1] = x.y;
+    }
+}
 __device__ __forceinline__ uint32_t tf32_of(float x) {
     uint32_t r;
     asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
@@ -159,13 +183,13 @@ __device__ __forceinline__ uint32_t finite_h2(uint32_t x, bool& bad) {
     return x & ((lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u));
 }
 
-// Slots a warp takes at a time and warps of a CTA.  The codes' kernels are bound by their instructions: with 16 rows (64
-// registers of output) twelve warps of 168 registers fit.
+// Slots a warp takes at a time and warps of a CTA.  Of up to 8 rows over codes twelve warps of 168 registers fit (one token
+// over 30000 Q8_0 slots 22.5 us, 24.0 with ten); with 16 rows a stage's sums need more (4 tokens 29.4 us, 34.5 with twelve).
 __host__ __device__ constexpr int tree_stage(int type, int mt) {
     return (type == AF_KV_Q8_0 || type == AF_KV_Q4_0) && mt <= 1 ? 32 : 16;
 }
 __host__ __device__ constexpr int tree_warps(int type, int D, int mt) {
-    return type == AF_F32 && D == 128 ? 6 : (type == AF_KV_Q8_0 || type == AF_KV_Q4_0) && mt <= 1 ? 12 : 8;
+    return type == AF_F32 && D == 128 ? 6 : (type == AF_KV_Q8_0 || type == AF_KV_Q4_0) && mt == 0 ? 12 : 8;
 }
 
 template <int TYPE, int D, int MT>
@@ -688,7 +712,7 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT_>::NW * 32, 1) attn_tree_k
                         l[mt][h] += p;
                     }
             }
-        // ---- output, sixteen slots at a time
+        // ---- output
         bool bad = false;  // non-finite values among the nodes' slots, taken out of the product
         if constexpr (C::QUANT) {
             const __half2 down = __float2half2_rn(__uint_as_float((256u << 23) - __float_as_uint(vlim)));
@@ -701,82 +725,104 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT_>::NW * 32, 1) attn_tree_k
                 }
             }
         }
+        if constexpr (TYPE == AF_F32) {
+            uint4 ph[GT][MT], pl[GT][MT];
 #pragma unroll
-        for (int g16 = 0; g16 < GT / 2; g16++) {
-            const uint32_t vb = vb0 + g16 * 16 * C::RB;
-            if constexpr (TYPE == AF_F32) {
+            for (int t = 0; t < GT; t++)
 #pragma unroll
-                for (int t = 0; t < 2; t++) {
-                    uint4 ph[MT], pl[MT];
-#pragma unroll
-                    for (int mt = 0; mt < MT; mt++) {  // slot 2c is k = c, slot 2c + 1 is k = c + 4
-                        split_tf32(s[mt][t][0], ph[mt].x, PACK ? ph[mt].y : pl[mt].x);
-                        split_tf32(s[mt][t][1], ph[mt].z, PACK ? ph[mt].w : pl[mt].z);
-                        if (!PACK) {
-                            split_tf32(s[mt][t][2], ph[mt].y, pl[mt].y);
-                            split_tf32(s[mt][t][3], ph[mt].w, pl[mt].w);
-                        }
-                    }
-                    const int k0 = t * 8 + 2 * c, k1 = k0 + 1;
-#pragma unroll
-                    for (int b = 0; b < NB; b++) {
-                        const uint4 x = lds128(vb + k0 * C::RB + (((8 * b + j) ^ C::swv(k0)) << 4));
-                        const uint4 y = lds128(vb + k1 * C::RB + (((8 * b + j) ^ C::swv(k1)) << 4));
-                        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                        for (int i = 0; i < 4; i++) {
-                            float fx = __uint_as_float(xs[i]), fy = __uint_as_float(ys[i]);
-                            if (nodes) {
-                                if (!(fabsf(fx) < CUDART_INF_F)) fx = 0.f, bad = true;
-                                if (!(fabsf(fy) < CUDART_INF_F)) fy = 0.f, bad = true;
-                            }
-                            uint32_t xh, xl, yh, yl;
-                            cut_tf32(fx, xh, xl);
-                            cut_tf32(fy, yh, yl);
-#pragma unroll
-                            for (int mt = 0; mt < MT; mt++) {
-                                mma8(o[mt][4 * b + i], ph[mt], xh, yh);
-                                if (!PACK) mma8(o[mt][4 * b + i], pl[mt], xh, yh);
-                                mma8(o[mt][4 * b + i], ph[mt], xl, yl);
-                            }
-                        }
+                for (int mt = 0; mt < MT; mt++) {  // slot 2c is k = c, slot 2c + 1 is k = c + 4
+                    split_tf32(s[mt][t][0], ph[t][mt].x, PACK ? ph[t][mt].y : pl[t][mt].x);
+                    split_tf32(s[mt][t][1], ph[t][mt].z, PACK ? ph[t][mt].w : pl[t][mt].z);
+                    if (!PACK) {
+                        split_tf32(s[mt][t][2], ph[t][mt].y, pl[t][mt].y);
+                        split_tf32(s[mt][t][3], ph[t][mt].w, pl[t][mt].w);
                     }
                 }
-            } else {
-                uint4 ph[MT], pl[MT];
+#pragma unroll
+            for (int b = 0; b < NB; b++) {
+                float sum[MT][4][4];  // of the stage
+#pragma unroll
+                for (int t = 0; t < GT; t++) {
+                    const int k0 = t * 8 + 2 * c, k1 = k0 + 1;
+                    const uint4 x = lds128(vb0 + k0 * C::RB + (((8 * b + j) ^ C::swv(k0)) << 4));
+                    const uint4 y = lds128(vb0 + k1 * C::RB + (((8 * b + j) ^ C::swv(k1)) << 4));
+                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+                    uint32_t xh[4], xl[4], yh[4], yl[4];
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        float fx = __uint_as_float(xs[i]), fy = __uint_as_float(ys[i]);
+                        if (nodes) {
+                            if (!(fabsf(fx) < CUDART_INF_F)) fx = 0.f, bad = true;
+                            if (!(fabsf(fy) < CUDART_INF_F)) fy = 0.f, bad = true;
+                        }
+                        cut_tf32(fx, xh[i], xl[i]);
+                        cut_tf32(fy, yh[i], yl[i]);
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < MT; mt++) {
+#pragma unroll
+                        for (int i = 0; i < 4; i++)
+                            if (t == 0)
+                                mma8z(sum[mt][i], ph[t][mt], xl[i], yl[i]);
+                            else
+                                mma8(sum[mt][i], ph[t][mt], xl[i], yl[i]);
+#pragma unroll
+                        for (int i = 0; i < 4; i++)
+                            if (!PACK) mma8(sum[mt][i], pl[t][mt], xh[i], yh[i]);
+#pragma unroll
+                        for (int i = 0; i < 4; i++) mma8(sum[mt][i], ph[t][mt], xh[i], yh[i]);
+                    }
+                }
+#pragma unroll
+                for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+                    for (int i = 0; i < 4; i++) add4(o[mt][4 * b + i], sum[mt][i]);
+            }
+        } else {
+            constexpr int G16 = GT / 2;
+            uint4 ph[G16][MT], pl[G16][MT];
+#pragma unroll
+            for (int g16 = 0; g16 < G16; g16++)
 #pragma unroll
                 for (int mt = 0; mt < MT; mt++) {
                     const float(&p0)[4] = s[mt][2 * g16], (&p1)[4] = s[mt][2 * g16 + 1];
-                    split_h2(p0[0], p0[1], ph[mt].x, PACK ? ph[mt].y : pl[mt].x);
-                    split_h2(p1[0], p1[1], ph[mt].z, PACK ? ph[mt].w : pl[mt].z);
+                    split_h2(p0[0], p0[1], ph[g16][mt].x, PACK ? ph[g16][mt].y : pl[g16][mt].x);
+                    split_h2(p1[0], p1[1], ph[g16][mt].z, PACK ? ph[g16][mt].w : pl[g16][mt].z);
                     if (!PACK) {
-                        split_h2(p0[2], p0[3], ph[mt].y, pl[mt].y);
-                        split_h2(p1[2], p1[3], ph[mt].w, pl[mt].w);
+                        split_h2(p0[2], p0[3], ph[g16][mt].y, pl[g16][mt].y);
+                        split_h2(p1[2], p1[3], ph[g16][mt].w, pl[g16][mt].w);
                     }
                 }
-                if constexpr (TYPE == AF_F16) {
-                    // lane: row lane & 15 of the 16 slots, chunk (lane >> 4) of the pair
-                    const int key = lane & 15;
+            if constexpr (TYPE == AF_F16) {
+                // lane: row lane & 15 of the 16 slots, chunk (lane >> 4) of the pair
+                const int key = lane & 15;
 #pragma unroll
-                    for (int t = 0; t < NT; t += 2) {
-                        uint4 v = ldsm4t(vb + key * C::RB + (((t + (lane >> 4)) ^ C::swv(key)) << 4));
-                        if (nodes) {
-                            v.x = finite_h2(v.x, bad), v.y = finite_h2(v.y, bad);
-                            v.z = finite_h2(v.z, bad), v.w = finite_h2(v.w, bad);
-                        }
-#pragma unroll
-                        for (int mt = 0; mt < MT; mt++) {
-                            mma16(o[mt][t], ph[mt], v.x, v.y);
-                            mma16(o[mt][t + 1], ph[mt], v.z, v.w);
-                            if (!PACK) {
-                                mma16(o[mt][t], pl[mt], v.x, v.y);
-                                mma16(o[mt][t + 1], pl[mt], v.z, v.w);
-                            }
-                        }
+                for (int t = 0; t < NT; t += 2) {
+                    uint4 v = ldsm4t(vb0 + key * C::RB + (((t + (lane >> 4)) ^ C::swv(key)) << 4));
+                    if (nodes) {
+                        v.x = finite_h2(v.x, bad), v.y = finite_h2(v.y, bad);
+                        v.z = finite_h2(v.z, bad), v.w = finite_h2(v.w, bad);
                     }
-                } else {
 #pragma unroll
-                    for (int b = 0; b < NB; b++) {
+                    for (int mt = 0; mt < MT; mt++) {
+                        float x[4], y[4];
+                        mma16z(x, PACK ? ph[0][mt] : pl[0][mt], v.x, v.y);
+                        mma16z(y, PACK ? ph[0][mt] : pl[0][mt], v.z, v.w);
+                        if (!PACK) {
+                            mma16(x, ph[0][mt], v.x, v.y);
+                            mma16(y, ph[0][mt], v.z, v.w);
+                        }
+                        add4(o[mt][t], x);
+                        add4(o[mt][t + 1], y);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int b = 0; b < NB; b++) {
+                    float sum[MT][4][4];  // of the stage
+#pragma unroll
+                    for (int g16 = 0; g16 < G16; g16++) {
+                        const uint32_t vb = vb0 + g16 * 16 * C::RB;
                         uint32_t vw[4][2];
 #pragma unroll
                         for (int h = 0; h < 2; h++) {
@@ -802,6 +848,7 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT_>::NW * 32, 1) attn_tree_k
                         const __half2 d0 = as_h2(dv[2 * g16][b]), d1 = as_h2(dv[2 * g16 + 1][b]);
 #pragma unroll
                         for (int mt = 0; mt < MT; mt++) {
+                            const uint4 qh = ph[g16][mt], ql = pl[g16][mt];
                             uint4 hi, lo;
                             auto times = [](uint32_t h, uint32_t l, __half2 d, uint32_t& hi, uint32_t& lo) {
                                 const __half2 x = __hmul2_rn(as_h2(h), d);
@@ -809,21 +856,29 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT_>::NW * 32, 1) attn_tree_k
                                 lo = as_u(__hfma2(as_h2(l), d, __hfma2(as_h2(h), d, __hneg2(x))));
                             };
                             if (PACK) {
-                                times(ph[mt].x, ph[mt].y, d0, hi.x, hi.y);
-                                times(ph[mt].z, ph[mt].w, d1, hi.z, hi.w);
+                                times(qh.x, qh.y, d0, hi.x, hi.y);
+                                times(qh.z, qh.w, d1, hi.z, hi.w);
                             } else {
-                                times(ph[mt].x, pl[mt].x, d0, hi.x, lo.x);
-                                times(ph[mt].y, pl[mt].y, d0, hi.y, lo.y);
-                                times(ph[mt].z, pl[mt].z, d1, hi.z, lo.z);
-                                times(ph[mt].w, pl[mt].w, d1, hi.w, lo.w);
+                                times(qh.x, ql.x, d0, hi.x, lo.x);
+                                times(qh.y, ql.y, d0, hi.y, lo.y);
+                                times(qh.z, ql.z, d1, hi.z, lo.z);
+                                times(qh.w, ql.w, d1, hi.w, lo.w);
                             }
 #pragma unroll
-                            for (int t = 0; t < 4; t++) {
-                                mma16(o[mt][4 * b + t], hi, vw[t][0], vw[t][1]);
-                                if (!PACK) mma16(o[mt][4 * b + t], lo, vw[t][0], vw[t][1]);
-                            }
+                            for (int t = 0; t < 4; t++)
+                                if (g16 == 0)
+                                    mma16z(sum[mt][t], PACK ? hi : lo, vw[t][0], vw[t][1]);
+                                else
+                                    mma16(sum[mt][t], PACK ? hi : lo, vw[t][0], vw[t][1]);
+#pragma unroll
+                            for (int t = 0; t < 4; t++)
+                                if (!PACK) mma16(sum[mt][t], hi, vw[t][0], vw[t][1]);
                         }
                     }
+#pragma unroll
+                    for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+                        for (int t = 0; t < 4; t++) add4(o[mt][4 * b + t], sum[mt][t]);
                 }
             }
         }

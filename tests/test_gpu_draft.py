@@ -857,6 +857,28 @@ def test_attention_tree_few_rows_over_many_slots(af, t, H, KVH, D, past, n):
     assert err <= tol, (err, tol)
 
 
+@pytest.mark.parametrize("t", KV)
+@pytest.mark.parametrize("D,n", [(128, 1), (128, 8), (128, 16), (64, 8), (64, 16), (128, 32)])
+def test_attention_tree_few_rows_long_sums(af, t, D, n):
+    """Values of one sign over some 80 stages a warp: the tensor cores cut their sums (by up to 2^-23 at each product, always
+    towards zero), so a sum of all of them would be off by 3e-5.  A stage's sum starts from zero: at most 12 products,
+    12 * 2^-23, and 2^-20 for the parts, the exponential, the row sum and the joining of the sums, of the result's norm."""
+    H = KVH = 32
+    past = 30000
+    g = torch.Generator(device="cuda").manual_seed(n)
+    m = past + n
+    k = torch.randn(m, KVH, D, generator=g, device="cuda")
+    v = torch.rand(m, KVH, D, generator=g, device="cuda") + 0.5
+    q = torch.randn(n, H, D, generator=g, device="cuda").cpu().numpy()
+    cache, kh, vh = on_gpu(af, t, k, v, KVH, D)
+    see = np.tril(np.ones((n, n), bool))
+    got = attend(af, t, cache, q, H, KVH, D, m, past, see).double().view(n, H, D)
+    ref = attn_ref_gpu(q, kh, vh, see, past)
+    err = ((got - ref).norm() / ref.norm()).item()
+    print(f"err {err:.2e} mean {((got - ref) / ref).mean().item():.2e}")
+    assert err <= 12 * 2.0 ** -23 + 2.0 ** -20
+
+
 # ---------------------------------------------------------------- together
 
 @pytest.mark.parametrize("t", KV)
