@@ -1060,7 +1060,7 @@ struct TreePlan {
 
 TreePlan tree_plan(int H, int KVH, int D, int type, int past, int n) {
     TreePlan p;
-    p.tc = tree_tc_plan(H, KVH, type, past, n);
+    p.tc = tree_tc_plan(H, KVH, D, type, past, n);
     p.splits = p.tc.splits;
     if (p.splits) return p;
     const int R = n * (H / KVH);

@@ -119,7 +119,7 @@ struct TreeArgs {
 struct TreeTcPlan {
     int tiles = 0, splits = 0;
 };
-TreeTcPlan tree_tc_plan(int H, int KVH, int type, int past, int n);
+TreeTcPlan tree_tc_plan(int H, int KVH, int D, int type, int past, int n);
 // Writes the workspace's parts [0, splits), or the output where there is one.
 cudaError_t launch_attn_tree_tc(const TreeArgs& a, const TreeTcPlan& p, cudaStream_t s);
 
