@@ -1,7 +1,7 @@
 // Attention for a tree of drafted tokens: node i of n sees the cached slots 0..past-1 and, of the slots
 // past..past+n-1 that hold the nodes' own keys and values, those whose bit its mask row has:
 //   out_i = sum_j p_ij v_j / sum_j p_ij,   p_ij = exp(q_i . k_j / sqrt(D)).
-// A row that sees no slot gives zeros.
+// A row that sees no slot gives zeros; one whose scores are all -infinity has no softmax and gives NaN.
 //
 // The rows of a kv head are its n nodes times the G heads of its group (row = node G + head), so that every cached
 // byte is read once for all of them.  Split-KV: CTA (split, kv head, row tile of 16 MT rows) walks its range of
@@ -966,8 +966,8 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT_>::NW * 32, 1) attn_tree_k
             den += f * ml.y;
         }
         if (splits == 1) {
-            const float inv = den == 0.f ? 0.f : 1.f / den;
             const int node = (r0 + r) / G, head = g * G + (r0 + r) % G;
+            const float inv = row_inverse(a, node, den);
             *reinterpret_cast<float4*>(a.out + (int64_t)node * a.ldo + (int64_t)head * D + d) =
                 make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
         } else {
@@ -1037,8 +1037,8 @@ __global__ void __launch_bounds__(128, 9) tree_merge_kernel(TreeArgs a, int spli
         }
     }
     if (d >= D || at >= rows) return;
-    const float inv = den == 0.f ? 0.f : 1.f / den;
     const int g = row / R, node = (row % R) / G, head = g * G + row % R % G;
+    const float inv = row_inverse(a, node, den);
     *reinterpret_cast<float4*>(a.out + (int64_t)node * a.ldo + (int64_t)head * D + d) =
         make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
 }

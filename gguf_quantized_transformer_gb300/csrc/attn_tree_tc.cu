@@ -1035,7 +1035,7 @@ __global__ void __launch_bounds__(TcCfgT<TYPE, D>::WARPS * 32, 1)
             constexpr int HC = CPR / 2;  // chunks of half a row
             tc_fence_after();
             float up = C::SPLIT ? pow2i((int)row_ev) : 1.f;
-            if (last) up = row_l == 0.f ? 0.f : up / row_l;
+            if (last) up *= live ? row_inverse(a, r / G, row_l) : 0.f;
 #pragma unroll 1
             for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
                 float o[32];

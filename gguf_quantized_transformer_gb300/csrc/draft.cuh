@@ -115,6 +115,16 @@ struct TreeArgs {
     int64_t ldo = 0;
     float* ws = nullptr;
 };
+// What a row's sums are multiplied with: one over the sum of its weights; where that is 0, 0 for a row that sees no slot, and
+// NaN for one that sees some, whose scores are all -infinity.
+__device__ __forceinline__ float row_inverse(const TreeArgs& a, int node, float sum) {
+    if (sum != 0.f) return 1.f / sum;
+    bool sees = a.past > 0;
+    const int words = (a.n + 31) / 32;
+    for (int w = 0; w < words && !sees; w++)
+        sees = (__ldcg(a.mask + (int64_t)node * words + w) & (w == words - 1 && a.n % 32 ? (1u << (a.n % 32)) - 1u : ~0u)) != 0;
+    return sees ? __uint_as_float(0x7FC00000u) : 0.f;
+}
 // A call with many rows goes to the tcgen05 kernel (attn_tree_tc.cu): its 64-slot tiles and splits; splits = 0: not.
 struct TreeTcPlan {
     int tiles = 0, splits = 0;

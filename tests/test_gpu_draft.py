@@ -879,6 +879,26 @@ def test_attention_tree_few_rows_long_sums(af, t, D, n):
     assert err <= 12 * 2.0 ** -23 + 2.0 ** -20
 
 
+@pytest.mark.parametrize("t,qv,kv", [("f32", 0.5, -np.inf), ("f16", 0.5, -np.inf), ("f32", 2.0 ** 68, -2.0 ** 68)])
+@pytest.mark.parametrize("past,n", [(0, 2), (40, 3), (600, 3), (0, 70), (600, 70)])
+def test_attention_tree_rows_that_see_only_minus_infinity(af, t, qv, kv, past, n):
+    """Scores that are all -infinity (or below fp32's range) have no softmax: such a row is not the zeros of a row that sees
+    nothing."""
+    H, KVH, D = 8, 2, 64
+    m = past + n
+    q = np.full((n, H, D), qv, np.float32)
+    k = torch.full((m, KVH, D), kv, device="cuda")
+    see = np.eye(n, dtype=bool)
+    if past == 0:
+        see[0] = False
+    cache = new_cache(t, KVH, m, D)
+    write(af, t, cache, k.view(m, -1), torch.ones(m, KVH * D, device="cuda"), KVH, D, m)
+    got = attend(af, t, cache, q, H, KVH, D, m, past, see)
+    blind = 1 if past == 0 else 0
+    assert got[blind:].isnan().all()
+    assert (got[:blind] == 0).all()
+
+
 # ---------------------------------------------------------------- together
 
 @pytest.mark.parametrize("t", KV)
