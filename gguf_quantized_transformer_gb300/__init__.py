@@ -45,7 +45,7 @@ class af_weights(ctypes.Structure):
 
 class af_rope_config(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("head_dim", "rot_dim", "layout", "scaling", "native_ctx")] + \
-               [(n, ctypes.c_float) for n in ("base", "factor", "turns_low", "turns_high", "magnitude")]
+               [(n, ctypes.c_double) for n in ("base", "factor", "turns_low", "turns_high", "magnitude")]
 
 
 _lib = None

@@ -1050,7 +1050,7 @@ int af_model_sample(af_model* m, const float* logits_dev, const int32_t* recent_
 
 namespace {
 
-bool finite_pos(float x) { return x > 0.f && x <= 3.4e38f; }
+bool finite_pos(double x) { return x > 0.0 && x <= 3.4e38; }
 
 int check_rope(const af_rope_config* c) {
     if (c->head_dim <= 0 || c->head_dim % 2) return fail(AF_EINVAL, "head_dim %d must be even", c->head_dim);
@@ -1059,13 +1059,13 @@ int check_rope(const af_rope_config* c) {
         return fail(AF_EINVAL, "rot_dim %d must be even and in [2, head_dim]", c->rot_dim);
     if (c->layout != AF_ROPE_INTERLEAVED && c->layout != AF_ROPE_HALF) return fail(AF_EINVAL, "bad layout");
     if (c->scaling < AF_ROPE_NONE || c->scaling > AF_ROPE_YARN) return fail(AF_EINVAL, "bad scaling");
-    if (!finite_pos(c->base) || c->base <= 1.f) return fail(AF_EINVAL, "base must be a finite number above 1");
+    if (!finite_pos(c->base) || c->base <= 1.0) return fail(AF_EINVAL, "base must be a finite number above 1");
     if (c->scaling != AF_ROPE_NONE && !finite_pos(c->factor)) return fail(AF_EINVAL, "factor must be finite and > 0");
     if (c->scaling == AF_ROPE_NTK && c->rot_dim < 4) return fail(AF_EINVAL, "AF_ROPE_NTK needs rot_dim >= 4");
     if (c->scaling == AF_ROPE_YARN &&
-        (c->native_ctx <= 0 || !(c->turns_low >= 0.f) || !finite_pos(c->turns_high) || c->turns_high <= c->turns_low))
+        (c->native_ctx <= 0 || !(c->turns_low >= 0.0) || !finite_pos(c->turns_high) || c->turns_high <= c->turns_low))
         return fail(AF_EINVAL, "AF_ROPE_YARN needs native_ctx > 0 and 0 <= turns_low < turns_high");
-    if (c->magnitude != 0.f && !finite_pos(c->magnitude)) return fail(AF_EINVAL, "magnitude must be finite and > 0 (0 = 1)");
+    if (c->magnitude != 0.0 && !finite_pos(c->magnitude)) return fail(AF_EINVAL, "magnitude must be finite and > 0 (0 = 1)");
     return AF_OK;
 }
 
@@ -1170,7 +1170,7 @@ int af_rope(const af_rope_config* cfg, const void* x_dev, int64_t ldx, void* y_d
     a.half = cfg->layout == AF_ROPE_HALF;
     a.pos = pos_dev;
     a.pos0 = pos0;
-    a.mag = cfg->magnitude != 0.f ? cfg->magnitude : 1.f;
+    a.mag = cfg->magnitude != 0.0 ? (float)cfg->magnitude : 1.f;
     CK(launch_rope(a, t, (cudaStream_t)stream));
     return AF_OK;
 }

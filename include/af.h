@@ -390,11 +390,11 @@ typedef struct af_rope_config {
     int32_t layout;     /* af_rope_layout */
     int32_t scaling;    /* af_rope_scaling */
     int32_t native_ctx; /* AF_ROPE_YARN */
-    float base;         /* > 1 */
-    float factor;       /* > 0 (ignored by AF_ROPE_NONE) */
-    float turns_low;    /* AF_ROPE_YARN: 0 <= turns_low < turns_high (1 and 32 in the method's paper) */
-    float turns_high;
-    float magnitude;    /* m; 0 = 1 (AF_ROPE_YARN's paper: 0.1 ln(factor) + 1) */
+    double base;        /* > 1; in 64 bits, as what the angles of far positions depend on */
+    double factor;      /* > 0 (ignored by AF_ROPE_NONE) */
+    double turns_low;   /* AF_ROPE_YARN: 0 <= turns_low < turns_high (1 and 32 in the method's paper) */
+    double turns_high;
+    double magnitude;   /* m; 0 = 1 (AF_ROPE_YARN's paper: 0.1 ln(factor) + 1) */
 } af_rope_config;
 
 /*
@@ -403,8 +403,8 @@ typedef struct af_rope_config {
  *           are one call; the heads of a cache are one row each with n_heads = 1)
  *   y_dev   the result, rows ldy values apart; may be x_dev itself with ldy == ldx, and overlaps it in no other way
  *   pos_dev int32 [n], any value (a negative one rotates back); NULL: row r is at pos0 + r (pos0 + n - 1 < 2^31)
- * The angle is exact modulo a turn to 2^-33 of a turn at a million positions (2^-22 at 2^31).  Asynchronous on `stream`, allocates
- * nothing, can be captured.  Vectors of 16 bytes are moved where rows, rot_dim and pointers allow it.
+ * The angle is exact modulo a turn to 2^-33 of a turn at a million positions (2^-22 at 2^31; with a factor below 1, that
+ * divided by the factor).  Asynchronous on `stream`, allocates nothing, can be captured.  Vectors of 16 bytes are moved where rows, rot_dim and pointers allow it.
  * n = 0 does nothing.  Errors: AF_EINVAL, AF_ERANGE, AF_ENOTIMPL (head_dim > 256), AF_ECUDA.
  */
 int af_rope(const af_rope_config* cfg, const void* x_dev, int64_t ldx, void* y_dev, int64_t ldy, int32_t dtype,

@@ -120,6 +120,27 @@ def test_rope_counted_positions_and_inverse(af, dtype):
     assert (z.float() - x.float()).abs().max().item() <= tol
 
 
+@pytest.mark.parametrize("scaling,factor,base", [("none", 1.0, 1234567.9), ("linear", 7.3, 10000.0), ("ntk", 3.7, 10000.0)])
+def test_rope_parameters_keep_their_precision(af, scaling, factor, base):
+    """Base and factor are taken in 64 bits: in 32, a factor of 7.3 would turn the first pair by 4e-4 at position 100,000."""
+    d, pos = 64, [100003, 1 << 20, -777777]
+    one, D = 10 ** 40, decimal.Decimal
+    decimal.getcontext().prec = 60
+    two_pi = 2 * D("3.14159265358979323846264338327950288419716939937510582097494")
+    b, s = D(base), D(factor)
+    if scaling == "ntk":
+        b *= (s.ln() * d / (d - 2)).exp()
+    f = [(b.ln() * (-2 * i) / d).exp() / (s if scaling == "linear" else 1) for i in range(d // 2)]
+    x = np.random.default_rng(4).standard_normal((len(pos), 1, d)).astype(np.float32)
+    cfg = af.rope_config(d, d, "half", base, scaling, factor, 8192)
+    y = torch.empty(len(pos), d, device="cuda")
+    af.af_rope(cfg, _dev(x), d, y, d, af.AF_F32, len(pos), 1, _dev(np.array(pos, np.int32)))
+    ref = rope_ref(x.astype(np.float64), pos, d, "half", [int(v / two_pi * one) for v in f], 1.0)
+    # as test_rope's: sines, products and their sum, and the angle's 2^-53 of a turn a position
+    tol = 2 * np.abs(x).max() * (2.0 ** -21 + 2 * np.pi * max(map(abs, pos)) * 2.0 ** -53)
+    assert np.abs(y.cpu().numpy().reshape(ref.shape) - ref).max() <= tol
+
+
 def test_rope_equals_the_models_rotation(af):
     """AF_ROPE_INTERLEAVED with linear scaling is the rotation the model's QKV epilogue applies."""
     import oracle
