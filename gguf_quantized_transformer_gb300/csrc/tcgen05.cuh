@@ -1,14 +1,24 @@
-// 5th-generation tensor-core building blocks (inline PTX): shared-memory
+// 5th-generation tensor-core building blocks (inline PTX): tiled TMA copies, shared-memory
 // operand descriptors for the SWIZZLE_128B K-major layout, kind::f16 MMA with
 // an fp32 TMEM accumulator, commit to an mbarrier, TMEM loads, fences, and the
 // fp32 -> fp16 hi + lo split used for near-fp32 products.
 #pragma once
+#include <cuda.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
 
 #include "tma.cuh"
 
 namespace af {
+
+// Tiled copy of a 2-D tensor map's box at (x, y); x times the element size a multiple of 16 bytes.
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
+            "r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+        : "memory");
+}
 
 // UMMA shared-memory descriptor, K-major, SWIZZLE_128B: start address, stride
 // between 8-row groups (1024 B), fixed version bits, swizzle mode.  The

@@ -7,7 +7,6 @@
 // the CTA exits (drain with wait_bounded on every barrier that has copies
 // outstanding).
 #pragma once
-#include <cuda.h>
 #include <stdint.h>
 
 namespace af {
@@ -55,15 +54,6 @@ __device__ __forceinline__ void bulk_g2s_evict_first(void* dst, const void* src,
         "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], "
         "%4;" ::"r"(smem_u32(dst)),
         "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
-        : "memory");
-}
-
-// Tiled copy of a 2-D tensor map's box at (x, y); x times the element size a multiple of 16 bytes.
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
-            "r"(smem_u32(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
         : "memory");
 }
 

@@ -67,3 +67,8 @@ def test_prefill_flops(idx, tokens, tflop):
 
 def test_gemm_flops_per_token_8b():
     assert bench.gemm_flops(synth.CONFIGS[3], 1) == 2.0 * 32 * LAYER_W_8B
+
+
+def test_gemv_traffic_is_of_these_sources():
+    """The DRAM bytes that bench.py reports for a gate/up GEMV launch were captured with the sources as they are."""
+    assert bench.gemv_traffic("q4_0", 28672, 4096) == bench.GEMV_TRAFFIC["bytes"]
