@@ -123,3 +123,47 @@ def test_tree_pasts_at_the_end_of_the_integers():
                                            None) == af.AF_ERANGE
                 assert af.af_attention_tree_workspace(t, 1, 1, 64, past, n) == 0
     assert af.af_attention_tree_workspace(af.AF_F32, 1, 1, 64, big - 2048, 1024) <= 256 << 20
+
+
+# The binding's calls, whose arguments go over as one packed record: every argument with a value that only it can be refused
+# for, so that a member that lies elsewhere in the record than in the call is seen.  (stream is passed on unread.)
+GOOD = {
+    "af_rope": dict(cfg=None, x=P, ldx=1024, y=2 * P, ldy=1024, dtype=0, n=4, n_heads=8, pos=None, pos0=0),
+    "af_kv_write": dict(k=P, v=P, ld=1024, n=4, slots=None, slot0=0, kc=P, ks=P, vc=P, vs=P, t=2, kvh=8, d=128, ctx=64),
+    "af_kv_read": dict(kc=P, ks=P, vc=P, vs=P, t=2, kvh=8, d=128, ctx=64, n=4, slots=None, slot0=0, k=P, v=P, ld=1024),
+    "af_tree_mask": dict(parent=P, n=4, pos0=0, mask=P, pos=None),
+    "af_attention_tree": dict(q=P, ldq=4096, kc=P, ks=P, vc=P, vs=P, t=2, h=32, kvh=8, d=128, ctx=64, past=10, n=4, mask=P,
+                              ws=P, wsb=1 << 40, out=P, ldo=4096),
+}
+BAD = {
+    "af_rope": dict(x=P + 1, ldx=1000, y=P + 3, ldy=1001, dtype=3, n=-7, n_heads=-5, pos=P + 2, pos0=2 ** 31 - 2),
+    "af_kv_write": dict(k=P + 4, v=None, ld=1022, n=77, slots=P + 1, slot0=-9, kc=None, ks=None, vc=P + 8, vs=P + 2, t=9, kvh=0,
+                        d=96 * 3, ctx=-2),
+    "af_kv_read": dict(kc=None, ks=None, vc=P + 8, vs=P + 2, t=9, kvh=0, d=96 * 3, ctx=-2, n=77, slots=P + 1, slot0=-9, k=P + 4,
+                       v=None, ld=1022),
+    "af_tree_mask": dict(parent=None, n=1031, pos0=-11, mask=P + 1, pos=P + 2),
+    "af_attention_tree": dict(q=P + 4, ldq=4095, kc=None, ks=None, vc=P + 8, vs=P + 2, t=9, h=31, kvh=-1, d=96, ctx=13, past=-3,
+                              n=1029, mask=P + 1, out=P + 8, ldo=4094),
+}
+
+
+@pytest.mark.parametrize("name", list(GOOD))
+def test_packed_calls_refuse_what_the_calls_refuse(name):
+    af = _af()
+    cfg = af.rope_config(128, 128)
+    for arg, bad in BAD[name].items():
+        args = {**GOOD[name], arg: bad}
+        if "cfg" in args:
+            args["cfg"] = cfg
+        with pytest.raises(Exception) as refused:
+            getattr(af, name)(*args.values(), stream=0)
+        packed = af.af_last_error()
+        args = [ctypes.byref(cfg) if a is cfg else a for a in args.values()]
+        rc = getattr(af.lib(), name)(*args, None)
+        assert rc not in (af.AF_OK, af.AF_ECUDA), arg
+        assert packed == af.af_last_error() and af.STATUS_NAMES[rc] in str(refused.value), arg
+
+
+def test_packed_call_refuses_what_is_no_call():
+    L = _af().lib()
+    assert L.af_packed_call(5, b"\0" * 256) == 1 and L.af_packed_call(-1, b"\0" * 256) == 1 and L.af_packed_call(0, None) == 1
