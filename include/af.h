@@ -404,8 +404,8 @@ typedef struct af_rope_config {
  *   y_dev   the result, rows ldy values apart; may be x_dev itself with ldy == ldx, and overlaps it in no other way
  *   pos_dev int32 [n], any value (a negative one rotates back); NULL: row r is at pos0 + r (pos0 + n - 1 < 2^31)
  * The angle is exact modulo a turn to 2^-33 of a turn at a million positions (2^-22 at 2^31; with a factor below 1, that
- * divided by the factor).  Asynchronous on `stream`, allocates nothing, can be captured.  Vectors of 16 bytes are moved where rows, rot_dim and pointers allow it.
- * n = 0 does nothing.  Errors: AF_EINVAL, AF_ERANGE, AF_ENOTIMPL (head_dim > 256), AF_ECUDA.
+ * divided by the factor).  Asynchronous on `stream`, allocates nothing, can be captured.  Vectors of 16 bytes are moved
+ * where rows, rot_dim and pointers allow it.  n = 0 does nothing.  Errors: AF_EINVAL, AF_ERANGE, AF_ENOTIMPL (head_dim > 256), AF_ECUDA.
  */
 int af_rope(const af_rope_config* cfg, const void* x_dev, int64_t ldx, void* y_dev, int64_t ldy, int32_t dtype,
             int32_t n, int32_t n_heads, const int32_t* pos_dev, int32_t pos0, void* stream);
@@ -416,10 +416,11 @@ int af_rope(const af_rope_config* cfg, const void* x_dev, int64_t ldx, void* y_d
  *   AF_F32, AF_F16          [n_kv_heads][ctx][head_dim] values; k_scales = v_scales = NULL
  *   AF_KV_Q8_0, AF_KV_Q4_0  codes [n_kv_heads][ctx][head_dim or head_dim / 2 bytes] and fp16 scales
  *                           [n_kv_heads][ctx][head_dim / 32], as af_model_kv_store's: every slot is quantized at
- *                           once from the fp32 values given here (no fp16 window)
+ *                           once from the fp32 values given here (no fp16 window; a model's own store holds only
+ *                           the slots that have left its window, so it is not a whole cache for these calls)
  * The decisions of the quantizers are those of exact arithmetic on the fp32 values.  A block of 32 that holds a NaN,
- * or whose scale overflows fp16, reads back as NaN.  Slots written from values that af_kv_read returned hold the same
- * values again (scales below fp16's normal range excepted), so a read and a write move slots.
+ * or whose scale overflows fp16, reads back as NaN.  What af_kv_write has written and af_kv_read returned gives the same
+ * values when it is written again (scales below fp16's normal range excepted), so a read and a write move slots.
  *   k_dev, v_dev  fp32 rows [n] of n_kv_heads * head_dim values, ld apart (16-byte aligned, ld a multiple of 4)
  *   slots_dev     int32 [n]: the slot of each row; a row whose slot is outside [0, ctx) is skipped (af_kv_read
  *                 leaves its output row as it was).  Of rows with the same slot the last is written.  NULL: row r
@@ -453,17 +454,21 @@ int af_tree_mask(const int32_t* parent_dev, int32_t n, int32_t pos0, uint32_t* m
  *   q_dev     fp32 [n] rows of n_heads * head_dim values (rotated), ldq apart
  *   cache     as af_kv_write's; slots from n_past + n on are not read
  *   mask_dev  uint32 [n][(n + 31) / 32] as af_tree_mask writes it, or any other: a row that sees nothing (n_past = 0
- *             and no bit set) gives zeros, and what a hidden slot holds (NaN, infinities) reaches no row it is
- *             hidden from
+ *             and no bit set) gives zeros, and what a hidden slot holds (NaN, infinities, numbers of any size) reaches
+ *             no row it is hidden from
  *   ws_dev    scratch of at least af_attention_tree_workspace bytes (NULL where that is 0), 256-byte aligned, of any
- *             contents; calls that may overlap in time need scratch of their own
+ *             contents; calls that may overlap in time need scratch of their own.  A call of fewer nodes or slots may
+ *             need more than a larger one (it has more splits); none needs more than
+ *             512 * (the device's SMs) * (head_dim + 2) bytes, 10.1 MB with head_dim 128 on 152 SMs
  *   out_dev   fp32 [n] rows, ldo apart
- * Results keep fp32's precision (2^-20 of the row's score sums and values), and their bits do not change from call to
- * call.  A row that sees a NaN or an infinity gets what the formula gives or NaN in its place, in any of its values.  The
- * kernels' waits are bounded: rows of a call whose wait gave up (copies that never arrive) are NaN.
- * 1 <= n <= 1024, 0 <= n_past <= 2^31 - 2049, n_past + n <= ctx, n_kv_heads * ctx < 2^31; head_dim 64 or 128, any whole group up to 64.  Pointers are 16-byte
- * aligned (mask_dev: 4), ldq and ldo multiples of 4.  Asynchronous on `stream`, allocates nothing, can be captured
- * (the first call on a device loads the kernels: make it before a capture).
+ * Results keep fp32's precision: a slot's score 2^-20 of the sum of |q| times the slot's largest |k|, over sqrt(head_dim),
+ * and a row's result 2^-20 of the largest weight times |v| that it sees (fp32 values above 2^110 may give infinities).
+ * The bits do not change from call to call.  A row that sees a NaN or an infinity, or whose scores are all -infinity, gets
+ * what the formula gives or NaN in its place, in any of its values.  The kernels' waits are bounded: rows of a block whose
+ * wait gave up (copies that never arrive) are NaN.
+ * 1 <= n <= 1024, 0 <= n_past <= 2^31 - 2049, n_past + n <= ctx, n_kv_heads * ctx < 2^31; head_dim 64 or 128, any whole
+ * group up to 64.  Pointers are 16-byte aligned (mask_dev: 4), ldq and ldo multiples of 4.  Asynchronous on `stream`,
+ * allocates nothing, can be captured (the first call on a device loads the kernels: make it before a capture).
  * Errors: AF_EINVAL, AF_ERANGE, AF_ENOTIMPL, AF_ECUDA.
  */
 uint64_t af_attention_tree_workspace(int32_t kv_dtype, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,

@@ -920,6 +920,31 @@ def test_attention_tree_rows_that_see_only_minus_infinity(af, t, qv, kv, past, n
     assert (got[:blind] == 0).all()
 
 
+def test_attention_tree_workspace_has_a_bound(af):
+    """Smaller calls may need more scratch than larger ones, but none more than 512 * SMs * (head_dim + 2) bytes."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    shapes = [(1, 1, 64), (8, 4, 64), (32, 8, 128), (64, 1, 128), (40, 5, 128), (32, 32, 64), (96, 96, 128), (128, 2, 64),
+              (300, 150, 64)]
+    for t in KV:
+        for H, KVH, D in shapes:
+            need = [af.af_attention_tree_workspace(af.KVTYPE[t], H, KVH, D, past, n)
+                    for past in (0, 100, 700, 1500, 1600, 4096, 9000, 30000, 1 << 20) for n in range(1, 1025)]
+            assert max(need) <= 512 * sms * (D + 2), (t, H, KVH, D)
+            assert max(need) > 0 or KVH > sms // 2  # (one split a head fills the SMs)
+    H, KVH, D, past = 32, 8, 128, 4096
+    ws = torch.empty(512 * sms * (D + 2), dtype=torch.uint8, device="cuda")
+    rng = np.random.default_rng(25)
+    cache, k, v = filled(af, "f16", rng, KVH, D, past + 40, past + 40)
+    for n in (1, 8, 32, 33, 40):  # 32 nodes need more than 33
+        q = rng.standard_normal((n, H, D)).astype(np.float32)
+        see = np.tril(np.ones((n, n), bool))
+        out = torch.empty(n, H * D, device="cuda")
+        af.af_attention_tree(_dev(q.reshape(n, H * D)), H * D, *cache, af.AF_F16, H, KVH, D, past + 40, past, n, _dev(pack(see)),
+                             ws, ws.numel(), out, H * D)
+        ref = attn_ref(q.astype(np.float64), k[:, :past + n], v[:, :past + n], see, past)
+        assert np.abs(out.cpu().numpy().reshape(n, H, D) - ref).max() <= attn_tol(q, k, v)
+
+
 # ---------------------------------------------------------------- together
 
 @pytest.mark.parametrize("t", KV)
