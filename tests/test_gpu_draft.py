@@ -141,6 +141,30 @@ def test_rope_parameters_keep_their_precision(af, scaling, factor, base):
     assert np.abs(y.cpu().numpy().reshape(ref.shape) - ref).max() <= tol
 
 
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_rope_many_rows(af, layout, dtype):
+    """Blocks that walk many rows each, with the positions of every row its own."""
+    n, heads, D, rot = 6001, 5, 128, 96
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(n, heads, D, generator=g, device="cuda").to(torch.float32 if dtype == "f32" else torch.float16)
+    pos = torch.randint(-(1 << 17), 1 << 17, (n,), generator=g, device="cuda", dtype=torch.int32)
+    y = torch.empty_like(x)
+    af.af_rope(af.rope_config(D, rot, layout, 500000.0), x, heads * D, y, heads * D, af.AF_F32 if dtype == "f32" else af.AF_F16, n,
+               heads, pos)
+    f = 500000.0 ** (-torch.arange(0, rot, 2, device="cuda", dtype=torch.float64) / rot)
+    th = (pos.double()[:, None] * f)[:, None]
+    a, b = ([slice(0, rot, 2), slice(1, rot, 2)] if layout == "interleaved" else [slice(0, rot // 2), slice(rot // 2, rot)])
+    ref = x.double()
+    ref[..., a], ref[..., b] = (x[..., a].double() * th.cos() - x[..., b].double() * th.sin(),
+                                x[..., a].double() * th.sin() + x[..., b].double() * th.cos())
+    # as test_rope's (2^-21, the angle's 2^-53 of a turn a position), and the reference's own angle, 2^-53 of it
+    tol = 2 * x.abs().max().item() * (2.0 ** -21 + (2 * np.pi + 2) * 2.0 ** (17 - 53))
+    if dtype == "f16":
+        tol = tol + ref.abs() * 2.0 ** -11 + 2.0 ** -25
+    assert ((y.double() - ref).abs() <= tol).all()
+
+
 def test_rope_equals_the_models_rotation(af):
     """AF_ROPE_INTERLEAVED with linear scaling is the rotation the model's QKV epilogue applies."""
     import oracle
@@ -946,6 +970,59 @@ def test_attention_tree_workspace_has_a_bound(af):
 
 
 # ---------------------------------------------------------------- together
+
+@pytest.mark.parametrize("t", KV)
+@pytest.mark.parametrize("n", [5, 40])
+def test_draft_step_in_one_graph(af, t, n):
+    """Mask, rotation, write, attention and read of a drafted tree, captured together and replayed over other inputs, give
+    the bits of the calls one by one."""
+    H, KVH, D, past, ctx = 32, 8, 128, 700, 800
+    rng = np.random.default_rng(26)
+    start, _, _ = filled(af, t, rng, KVH, D, ctx, past)
+    w = (H + 2 * KVH) * D
+    inputs = [(_dev(rng.standard_normal((n, w)).astype(np.float32)), _dev(random_parents(rng, n).astype(np.int32))) for _ in range(3)]
+    cfg = af.rope_config(D, D, "half", 500000.0)
+    need = max(256, af.af_attention_tree_workspace(af.KVTYPE[t], H, KVH, D, past, n))
+    cache = [None if x is None else x.clone() for x in start]
+    rows, parent = inputs[0][0].clone(), inputs[0][1].clone()
+    rot, pos = torch.zeros(n, w, device="cuda"), torch.zeros(n, dtype=torch.int32, device="cuda")
+    mask = torch.zeros(n, (n + 31) // 32, dtype=torch.int32, device="cuda")
+    ws, out = torch.empty(need, dtype=torch.uint8, device="cuda"), torch.zeros(n, H * D, device="cuda")
+    kr, vr = torch.zeros(n, KVH * D, device="cuda"), torch.zeros(n, KVH * D, device="cuda")
+
+    def step(pause):
+        for call in (lambda: af.af_tree_mask(parent, n, past, mask, pos),
+                     lambda: af.af_rope(cfg, rows, w, rot, w, af.AF_F32, n, H + KVH, pos),
+                     lambda: af.af_kv_write(rot[:, H * D:], rows[:, (H + KVH) * D:], w, n, None, past, *cache, af.KVTYPE[t], KVH, D, ctx),
+                     lambda: af.af_attention_tree(rot, w, *cache, af.KVTYPE[t], H, KVH, D, ctx, past, n, mask, ws, need, out, H * D),
+                     lambda: af.af_kv_read(*cache, af.KVTYPE[t], KVH, D, ctx, n, None, past, kr, vr, KVH * D)):
+            call()
+            if pause:
+                torch.cuda.synchronize()
+
+    def put(i):
+        rows.copy_(inputs[i][0])
+        parent.copy_(inputs[i][1])
+        for x in (rot, pos, mask, out, kr, vr):
+            x.zero_()
+
+    want = []
+    for i in range(3):
+        put(i)
+        step(True)
+        want.append([x.clone() for x in (rot[:, :(H + KVH) * D], pos, mask, out, kr, vr)])
+    assert not torch.equal(want[0][3], want[1][3])
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        step(False)
+    for i in (2, 0, 1, 1, 2):
+        put(i)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [rot[:, :(H + KVH) * D], pos, mask, out, kr, vr]
+        assert all(torch.equal(x, y) for x, y in zip(got, want[i]))
+
 
 @pytest.mark.parametrize("t", KV)
 def test_draft_verify_and_move(af, t):
