@@ -27,8 +27,8 @@
 // carries a factor 2^8 so that small p keep their low part above fp16's subnormal step.  Sums are fp32.
 //
 // A call of up to 8 rows (MT = 0) puts the hi parts of q and p into rows 0-7 of the 16-row tile and the lo parts into rows
-// 8-15: one product instead of two, whose halves are added (one token over 30000 Q8_0 slots: 28.2 us with two products,
-// 22.6 with one; fp32 63.4 and 55.4).
+// 8-15: one product instead of two, whose halves are added (one token over 30000 Q8_0 slots: 28.4 us with two products,
+// 23.0 with one; fp32 64.9 and 48.7).
 //
 // Hidden slots: a masked score is -inf (a select, so NaN does not survive); in the groups of slots that hold nodes,
 // non-finite values are taken out of the product and added element by element to the rows that see them.

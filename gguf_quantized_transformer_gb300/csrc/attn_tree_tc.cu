@@ -11,8 +11,8 @@
 //                           p's fp16 hi and lo parts (16 columns each)
 // The tensor cores' fp32 sums are cut, not rounded: every product added to a sum takes up to 2^-23 of it, always towards
 // zero.  So the small lo products come first, before the sum has its size, and the output is added to the older tiles'
-// by the softmax warps, rounded, every kFlush tiles (64 nodes over 30720 fp32 slots were off by 1.3e-5 of the result's
-// norm with one sum of 53 tiles, in 103 us; sums of 4, 2 and 1 tiles: 1.2e-6 in 106, 8.2e-7 in 107, 6.7e-7 in 111).
+// by the softmax warps, rounded, every kFlush tiles (64 nodes over 30720 fp32 slots are off by 1.2e-5 of the result's
+// norm with one sum of 53 tiles, in 108.7 us; sums of 4, 2 and 1 tiles: 1.2e-6 in 109.9, 8.1e-7 in 111.3, 6.5e-7 in 113.8).
 // Both products take their A operand (q, p) from tensor memory and B from shared memory: K rows [slot][dim] are
 // K-major, V rows [slot][dim] MN-major, so neither is transposed and both have the cache's own order:
 //   fp16 cache    TMA copies 64 slots x 64 dims boxes into the SWIZZLE_128B layout; two products (hi, lo of q or p)
@@ -23,11 +23,11 @@
 //                 by its own (one large key, hidden or not, would leave its neighbours few bits).  K's power goes into
 //                 the scores; V's into p, relative to a reference exponent of the row's output, which is rescaled when
 //                 p times V, over the slots that the row sees, outgrows it.
-//                 (Rows read through registers instead, three tiles ahead: 192 us where this took 107 at 64 nodes
-//                 over 30720 fp32 slots; the warp's loads of several tiles share its few scoreboards.)
+//                 (Rows read through registers instead, three tiles ahead: 1.8 times as long at 64 nodes over 30720
+//                 fp32 slots; the warp's loads of several tiles share its few scoreboards.)
 // Warps 0-7 are the softmax: a thread owns a row and 32 of a tile's slots (its scores in registers: maximum, p, sum), the
 // two of a row exchange their maxima tile by tile.  (One thread for all 64 slots was the longest chain of the pipeline:
-// some 500 instructions a tile and a warp beside eight converting warps: 25 nodes over 30011 Q8_0 slots 50.3 us, 47.5 so.)
+// some 500 instructions a tile and a warp beside eight converting warps: 25 nodes over 30011 Q8_0 slots took 6% longer.)
 // One warp issues the MMAs, scores two (D = 64: three) tiles ahead of the outputs.
 // The reference maximum moves lazily, as in attn_tree.cu, with the same factor 2^8 in p.
 // Tiles that hold nodes (the last ones): a hidden slot's score is -inf by a select; non-finite keys and values and the
@@ -436,7 +436,8 @@ __device__ __forceinline__ void store_tile(uint8_t* dst, const uint8_t* st, cons
 // Half of a tile (32 slots a thread) where keys or values differ too much for one exponent in 16 or 64 slots.  Its scores in
 // tensor memory become scores plus V's exponent (-infinity for zero values), so that the common code weighs them as if all
 // exponents were 0; the largest score and the sum of 2^(score - that) come back.  Rare, and out of line: among the
-// common tiles' code it cost them 3 to 8%.
+// common tiles' code it cost them 3 to 8%.  (64 nodes over 30720 slots with every tile of this kind: fp32 210 us where
+// others take 111, Q8_0 164 and 91.)
 __device__ __noinline__ float2 own_scores(uint32_t s_addr, const int8_t* ek, const int8_t* ev, float rowf, unsigned see, unsigned bad) {
     float m = -CUDART_INF_F, l = 0.f;
     for (int c = 0; c < 32; c += 16) {

@@ -10,10 +10,11 @@
 // gives zero codes.  A block that holds a NaN, or whose scale overflows fp16, gets a NaN as its scale: nothing
 // non-finite is turned into a number.
 //
-// Both are bound by HBM.  A CTA takes a few rows at a time, all loads before the first use (writing: a thread holds eight
-// values of a block, two float4 64 bytes apart, so that four lanes share a block's scale); the grid is a few CTAs per
-// SM.  Data of earlier kernels is read through L2 (the kernels are
-// launched with programmatic serialization).
+// A CTA takes a few rows at a time, all loads before the first use (writing: a thread holds eight values of a block, two
+// float4 64 bytes apart, so that four lanes share a block's scale); the grid is a few CTAs per SM.  Data of earlier kernels
+// is read through L2 (the kernels are launched with programmatic serialization).
+// 30720 rows of 8 x 128, written and read: fp32 81 and 76 us, fp16 58 and 62, Q8_0 71 and 55, Q4_0 92 and 51, that is 5.7
+// to 6.6 TB/s but for the quantizers' 4.5 and 3.1: those are bound by their instructions (issue slots 72% busy).
 #include <algorithm>
 #include <type_traits>
 
@@ -42,8 +43,8 @@ __device__ __forceinline__ unsigned cta_or(unsigned x) {
 }
 
 // Four lanes (an aligned group of the warp) hold the 32 values of a block: lane i of them quads i and 4 + i.  Every lane of
-// the warp takes part in the exchanges (with a mask per group the warp would run group by group: 113 us where this
-// takes 88 for 30720 rows of 8 x 128 values into Q4_0).
+// the warp takes part in the exchanges (with a mask per group the warp would run group by group: a quarter
+// longer for 30720 rows of 8 x 128 values into Q4_0).
 template <int TYPE>
 __device__ __forceinline__ void quantize_group(const float (&x)[8], int lane, int (&q)[8], __half& dh) {
     unsigned amax = 0;  // magnitudes order like their bits, NaNs above infinity

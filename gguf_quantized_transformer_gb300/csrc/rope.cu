@@ -12,8 +12,10 @@
 // Sine and cosine on [-pi / 4, pi / 4] are their Taylor series (remainders below 2^-28 and 2^-33), two pairs at a time
 // in packed fp32.
 //
-// Bound by HBM: every value is read and written once.  A thread keeps one unit of the head (its frequencies in registers)
-// and walks rows with it, and the heads of a row with the sines of that row.
+// Every value is read and written once.  A thread keeps one unit of the head (its frequencies in registers) and walks rows
+// with it, and the heads of a row with the sines of that row.  4096 rows x 40 x 128: fp32 32.8 us (half) and 36.2
+// (interleaved), fp16 26.3 and 20.9; 245760 rows x 128 of one position: 45.5, 49.4, 34.5 and 37.7: 3.2 to 5.5 TB/s, bound
+// by each thread's wait for its own loads (16 to 24 warps an SM).
 #include "draft.cuh"
 #include "tma.cuh"
 
