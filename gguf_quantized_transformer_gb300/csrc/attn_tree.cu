@@ -636,7 +636,7 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT_>::NW * 32, 1) attn_tree_k
                 }
                 if (big > 0.f) {  // (2^-ev is an fp16 number)
                     const int e = min(max((int)(__float_as_uint(big) >> 23) - 127, -15), 14);
-                    const float f = ex2t((float)e - ev);
+                    const float f = __uint_as_float((unsigned)(127 + e - (int)ev) << 23);  // (exactly: stages may take turns)
                     ev = (float)e;
                     vlim = __uint_as_float((unsigned)(e + 129) << 23);
 #pragma unroll

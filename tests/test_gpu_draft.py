@@ -924,6 +924,40 @@ def test_attention_tree_few_rows_long_sums(af, t, D, n):
     assert err <= 12 * 2.0 ** -23 + 2.0 ** -20
 
 
+@pytest.mark.parametrize("t", KV)
+@pytest.mark.parametrize("D,n", [(128, 1), (128, 16), (64, 32), (128, 70)])
+@pytest.mark.parametrize("run", [16, 384])
+def test_attention_tree_sizes_of_values_that_take_turns(af, t, D, n, run):
+    """Values of one sign whose size changes 64-fold every few slots: the powers of two that follow them lose nothing.  The
+    bound of the long sums (tcgen05: 24 products over two tiles)."""
+    H = KVH = 32
+    past = 12000
+    m = past + n
+    g = torch.Generator(device="cuda").manual_seed(n)
+    turn = (torch.arange(m, device="cuda") // run % 2 * 6 - 3).float().exp2()[:, None, None]
+    k = torch.randn(m, KVH, D, generator=g, device="cuda")
+    v = (torch.rand(m, KVH, D, generator=g, device="cuda") + 0.5) * turn
+    q = torch.randn(n, H, D, generator=g, device="cuda").cpu().numpy()
+    cache, kh, vh = on_gpu(af, t, k, v, KVH, D)
+    see = np.tril(np.ones((n, n), bool))
+    got = attend(af, t, cache, q, H, KVH, D, m, past, see).double().view(n, H, D)
+    ref = attn_ref_gpu(q, kh, vh, see, past)
+    err = ((got - ref).norm() / ref.norm()).item()
+    print(f"err {err:.2e}")
+    assert err <= 24 * 2.0 ** -23 + 2.0 ** -20
+
+
+@pytest.mark.parametrize("t", KV)
+@pytest.mark.parametrize("H,KVH,D,n", [(1, 1, 64, 33), (4, 1, 128, 9), (40, 1, 64, 1), (64, 1, 128, 40)])
+def test_attention_tree_of_a_cache_smaller_than_a_tile(af, t, H, KVH, D, n):
+    rng = np.random.default_rng(27)
+    cache, k, v = filled(af, t, rng, KVH, D, n, n)
+    q = rng.standard_normal((n, H, D)).astype(np.float32)
+    see, _ = closure(random_parents(rng, n))
+    got = attend(af, t, cache, q, H, KVH, D, n, 0, see).cpu().numpy().reshape(n, H, D)
+    assert np.abs(got - attn_ref(q.astype(np.float64), k, v, see, 0)).max() <= attn_tol(q, k, v)
+
+
 @pytest.mark.parametrize("t,qv,kv", [("f32", 0.5, -np.inf), ("f16", 0.5, -np.inf), ("f32", 2.0 ** 68, -2.0 ** 68)])
 @pytest.mark.parametrize("past,n", [(0, 2), (40, 3), (600, 3), (0, 70), (600, 70)])
 def test_attention_tree_rows_that_see_only_minus_infinity(af, t, qv, kv, past, n):
