@@ -1115,12 +1115,14 @@ cudaError_t go_type(const TreeArgs& a, const TreeTcPlan& p, cudaStream_t s) {
 TreeTcPlan tree_tc_plan(int H, int KVH, int D, int type, int past, int n) {
     TreeTcPlan p;
     const int R = n * (H / KVH);
-    // More than 32 rows; of fp32 caches, whose mma.sync kernel needs three tf32 products, more than 16 over a long past.
-    // 32 rows x 128 over fp32 slots, there and here: 1100 slots 13.4 and 14.7 us, 2000 19.3 and 17.2, 30000 104 and 62;
-    // x 64: 1100 11.3 and 12.2, 4000 15.9 and 19.7, 30000 64.6 and 49.1.  16 rows x 128: 4000 16.4 and 22.7, 30000 65.8 and
-    // 61.5.  32 rows x 128 of the other types: 4000 fp16 slots 13.8 and 17.5, 30000 36.2 and 38.6; 30000 Q8_0 42.4 and
-    // 51.4, Q4_0 40.5 and 51.1.
-    if (R <= (type == AF_F32 && past + n >= (D == 128 ? 1536 : 8192) ? 16 : 32)) return p;
+    // More than 32 rows; of fp32 caches, whose mma.sync kernel needs three tf32 products, more than 16 over a long past and
+    // more than 8 over a longer one.  32 rows x 128 over fp32 slots, there and here: 1100 slots 13.4 and 14.7 us, 2000 19.3
+    // and 17.2, 30000 104 and 62; x 64: 1100 11.3 and 12.2, 4000 15.9 and 19.7, 30000 64.6 and 49.1.  16 rows x 128: 4000
+    // 16.4 and 22.7, 20400 49.0 and 47.9, 30000 65.8 and 61.8; x 64: 30000 34.6 and 49.4.  32 rows x 128 of the other types:
+    // 4000 fp16 slots 13.8 and 17.5, 30000 36.2 and 38.6; 30000 Q8_0 42.4 and 51.4, Q4_0 40.5 and 51.1.
+    int most = 32;
+    if (type == AF_F32 && past + n >= (D == 128 ? 1536 : 8192)) most = D == 128 && past + n >= 20480 ? 8 : 16;
+    if (R <= most) return p;
     p.tiles = (past + n + BK - 1) / BK;
     const int64_t ctas = (int64_t)KVH * ((R + kRows - 1) / kRows);
     // one CTA per SM, two tiles each or more (64 nodes over 448 fp16 slots: 11.4 us, 12.9 with four), but a few tiles are
