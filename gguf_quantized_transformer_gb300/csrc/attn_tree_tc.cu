@@ -1125,8 +1125,9 @@ TreeTcPlan tree_tc_plan(int H, int KVH, int D, int type, int past, int n) {
     if (R <= most) return p;
     p.tiles = (past + n + BK - 1) / BK;
     const int64_t ctas = (int64_t)KVH * ((R + kRows - 1) / kRows);
-    // one CTA per SM, two tiles each or more (64 nodes over 448 fp16 slots: 11.4 us, 12.9 with four), but a few tiles are
-    // not worth a merge (64 nodes, 256 slots: fp16 9.9 us in one split, 10.1 in two; fp32 13.2 and 12.1)
+    // one CTA per SM, two tiles each or more (64 nodes over 448 fp16 slots: 10.6 us, 12.3 with four), but a few tiles are
+    // not worth a merge (64 nodes over 192 slots: fp16 10.1 us in one split, 10.2 in two; fp32 14.2 and 13.0, Q8_0 12.5 and
+    // 11.7)
     p.splits = p.tiles <= 4 ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(num_sms() / ctas, p.tiles / 2));
     return p;
 }
