@@ -925,6 +925,30 @@ def test_attention_tree_few_rows_long_sums(af, t, D, n):
 
 
 @pytest.mark.parametrize("t", KV)
+@pytest.mark.parametrize("H,KVH,D,past,n", [(8, 8, 128, 1000, 1), (32, 8, 128, 6000, 3), (8, 2, 128, 6000, 3), (32, 8, 64, 6000, 3),
+                                            (32, 8, 128, 1000, 8), (8, 2, 128, 6000, 40)])
+def test_attention_tree_scores_are_not_cut_over_the_whole_head(af, t, H, KVH, D, past, n):
+    """Scores summed 32 dims at a time: 12 products, each cut by half of 2^-23 of the sum so far on average, and that grows
+    evenly, so together by 6.5 * 2^-24 of the block's score, which moves the slot's weight by as much; and 2^-21 of the
+    result's norm for all else (parts, exponential and row sum are off by 2^-22 at random).  tcgen05 sums the small lo
+    products first, then 8 over the head."""
+    m = past + n
+    g = torch.Generator(device="cuda").manual_seed(past)
+    q = torch.randn(n, H, D, generator=g, device="cuda")
+    k = torch.randn(m, KVH, D, generator=g, device="cuda") * torch.exp(0.5 * torch.randn(1, KVH, D, generator=g, device="cuda"))
+    v = torch.randn(m, KVH, D, generator=g, device="cuda")
+    cache, kh, vh = on_gpu(af, t, k, v, KVH, D)
+    see = np.tril(np.ones((n, n), bool))
+    got = attend(af, t, cache, q.cpu().numpy(), H, KVH, D, m, past, see).double().view(n, H, D)
+    ref = attn_ref_gpu(q.cpu().numpy(), kh, vh, see, past)
+    blocks = torch.einsum("nhbd,hmbd->nhmb", q.double().view(n, H, -1, 32),
+                          kh.repeat_interleave(H // KVH, 0).view(H, m, -1, 32)).abs().sum(-1).mean().item() * D ** -0.5
+    err = ((got - ref).norm() / ref.norm()).item()
+    print(f"err {err:.2e} bound {6.5 * 2.0 ** -24 * blocks + 2.0 ** -21:.2e}")
+    assert err <= 6.5 * 2.0 ** -24 * blocks + 2.0 ** -21
+
+
+@pytest.mark.parametrize("t", KV)
 @pytest.mark.parametrize("D,n", [(128, 1), (128, 16), (64, 32), (128, 70)])
 @pytest.mark.parametrize("run", [16, 384])
 def test_attention_tree_sizes_of_values_that_take_turns(af, t, D, n, run):
