@@ -23,7 +23,7 @@
 // The tensor cores cut their fp32 sums (every product takes up to 2^-23 of the sum, towards zero: one sum over a warp's 80
 // stages of fp32 slots was off by 1.1e-5 of the result's norm), so a stage's output starts from zero and is added,
 // rounded, to the walk's: 1.2e-7.  (fp32, 1 and 4 tokens over 30000 slots: 48.3 and 65.9 us, 45.2 and 55.7 with one sum.)
-// So do scores every 32 dims (3 nodes over 6000 fp32 slots: 6.1e-7, 2.1e-6 with one sum over the head).
+// So do scores every 32 dims, small lo products first (3 nodes over 6000 fp32 slots: 4e-7, 2.1e-6 with one sum over the head).
 // The reference maximum of the softmax moves only when a score exceeds it by more than 4 (in powers of two); p
 // carries a factor 2^8 so that small p keep their low part above fp16's subnormal step.  Sums are fp32.
 //
@@ -569,15 +569,20 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT_>::NW * 32, 1) attn_tree_k
                 for (int mt = 0; mt < MT; mt++) {
                     float p[GT][4] = {};
 #pragma unroll
-                    for (int e = 0; e < 4; e++) {
+                    for (int e = 0; e < 4; e++) {  // the small lo products first: what they are cut by is small
                         const uint4 qh = lds128(sq + ((4 * b + e) * MT + mt) * QP * 512 + lane * 16);
                         const uint4 ql = PACK ? qh : lds128(sq + ((4 * b + e) * MT + mt) * 1024 + 512 + lane * 16);
 #pragma unroll
                         for (int t = 0; t < GT; t++) {
                             mma8(p[t], qh, kl[t][2 * e], kl[t][2 * e + 1]);
                             if (!PACK) mma8(p[t], ql, kh[t][2 * e], kh[t][2 * e + 1]);
-                            mma8(p[t], qh, kh[t][2 * e], kh[t][2 * e + 1]);
                         }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const uint4 qh = lds128(sq + ((4 * b + e) * MT + mt) * QP * 512 + lane * 16);
+#pragma unroll
+                        for (int t = 0; t < GT; t++) mma8(p[t], qh, kh[t][2 * e], kh[t][2 * e + 1]);
                     }
 #pragma unroll
                     for (int t = 0; t < GT; t++) add4(s[mt][t], p[t]);

@@ -1116,10 +1116,10 @@ TreeTcPlan tree_tc_plan(int H, int KVH, int D, int type, int past, int n) {
     TreeTcPlan p;
     const int R = n * (H / KVH);
     // More than 32 rows; of fp32 caches, whose mma.sync kernel needs three tf32 products, more than 16 over a long past and
-    // more than 8 over a longer one.  32 rows x 128 over fp32 slots, there and here: 1100 slots 13.4 and 14.7 us, 2000 19.3
-    // and 17.2, 30000 104 and 62; x 64: 1100 11.3 and 12.2, 4000 15.9 and 19.7, 30000 64.6 and 49.1.  16 rows x 128: 4000
-    // 16.4 and 22.7, 20400 49.0 and 47.9, 30000 65.8 and 61.8; x 64: 30000 34.6 and 49.4.  32 rows x 128 of the other types:
-    // 4000 fp16 slots 13.8 and 17.5, 30000 36.2 and 38.6; 30000 Q8_0 42.4 and 51.4, Q4_0 40.5 and 51.1.
+    // more than 8 over a longer one.  32 rows x 128 over fp32 slots, there and here: 1100 slots 13.9 and 14.6 us, 2000 20.0
+    // and 17.4, 30000 108 and 62; x 64: 4000 15.6 and 19.6, 8192 22.1 and 23.8, 30000 63.8 and 48.6.  16 rows x 128: 4000
+    // 16.5 and 22.9, 20400 49.6 and 47.7, 30000 67.0 and 61.9; x 64: 30000 34.4 and 49.0.  32 rows x 128 of the other types:
+    // 4000 fp16 slots 14.1 and 17.4, 30000 38.1 and 39.0, 60000 62.0 and 61.2; 30000 Q8_0 42.6 and 51.5, Q4_0 40.5 and 51.1.
     int most = 32;
     if (type == AF_F32 && past + n >= (D == 128 ? 1536 : 8192)) most = D == 128 && past + n >= 20480 ? 8 : 16;
     if (R <= most) return p;
