@@ -507,14 +507,11 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT_>::NW * 32, 1) attn_tree_k
                 for (int mt = 0; mt < MT; mt++) {
                     float p[GT][4] = {};
 #pragma unroll
-                    for (int e = 0; e < 2; e++) {
-                        const uint4 qh = lds128(sq + ((2 * b + e) * MT + mt) * QP * 512 + lane * 16);
-                        const uint4 ql = PACK ? qh : lds128(sq + ((2 * b + e) * MT + mt) * 1024 + 512 + lane * 16);
+                    for (int i = PACK ? 2 : 0; i < 4; i++) {  // q's lo parts (steps 0 and 1), then its hi parts
+                        const int e = i & 1;
+                        const uint4 q = lds128(sq + ((2 * b + e) * MT + mt) * QP * 512 + (i < 2 ? 512 : 0) + lane * 16);
 #pragma unroll
-                        for (int t = 0; t < GT; t++) {
-                            mma16(p[t], qh, kw[t][2 * e], kw[t][2 * e + 1]);
-                            if (!PACK) mma16(p[t], ql, kw[t][2 * e], kw[t][2 * e + 1]);
-                        }
+                        for (int t = 0; t < GT; t++) mma16(p[t], q, kw[t][2 * e], kw[t][2 * e + 1]);
                     }
 #pragma unroll
                     for (int t = 0; t < GT; t++) {
@@ -538,14 +535,11 @@ __global__ void __launch_bounds__(TreeCfg<TYPE, D, MT_>::NW * 32, 1) attn_tree_k
                 for (int mt = 0; mt < MT; mt++) {
                     float p[GT][4] = {};  // of the block: its sum starts from zero, as the output's does
 #pragma unroll
-                    for (int e = 0; e < 2; e++) {
-                        const uint4 qh = lds128(sq + ((2 * b + e) * MT + mt) * QP * 512 + lane * 16);
-                        const uint4 ql = PACK ? qh : lds128(sq + ((2 * b + e) * MT + mt) * 1024 + 512 + lane * 16);
+                    for (int i = PACK ? 2 : 0; i < 4; i++) {  // q's lo parts (steps 0 and 1), then its hi parts
+                        const int e = i & 1;
+                        const uint4 q = lds128(sq + ((2 * b + e) * MT + mt) * QP * 512 + (i < 2 ? 512 : 0) + lane * 16);
 #pragma unroll
-                        for (int t = 0; t < GT; t++) {
-                            if (!PACK) mma16(p[t], ql, e ? kw[t].z : kw[t].x, e ? kw[t].w : kw[t].y);
-                            mma16(p[t], qh, e ? kw[t].z : kw[t].x, e ? kw[t].w : kw[t].y);
-                        }
+                        for (int t = 0; t < GT; t++) mma16(p[t], q, e ? kw[t].z : kw[t].x, e ? kw[t].w : kw[t].y);
                     }
 #pragma unroll
                     for (int t = 0; t < GT; t++) add4(s[mt][t], p[t]);

@@ -926,7 +926,7 @@ def test_attention_tree_few_rows_long_sums(af, t, D, n):
 
 @pytest.mark.parametrize("t", KV)
 @pytest.mark.parametrize("H,KVH,D,past,n", [(8, 8, 128, 1000, 1), (32, 8, 128, 6000, 3), (8, 2, 128, 6000, 3), (32, 8, 64, 6000, 3),
-                                            (32, 8, 128, 1000, 8), (8, 2, 128, 6000, 40)])
+                                            (32, 8, 128, 1000, 8), (8, 2, 128, 6000, 40), (8, 8, 64, 3454, 14)])
 def test_attention_tree_scores_are_not_cut_over_the_whole_head(af, t, H, KVH, D, past, n):
     """Scores summed 32 dims at a time: 12 products, each cut by half of 2^-23 of the sum so far on average, and that grows
     evenly, so together by 6.5 * 2^-24 of the block's score, which moves the slot's weight by as much; and 2^-21 of the
