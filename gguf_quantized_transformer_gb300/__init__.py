@@ -105,6 +105,18 @@ def lib():
         L.af_attention_tree_workspace.argtypes = [i32] * 6
         L.af_attention_tree_workspace.restype = u64
         L.af_attention_tree.argtypes = [vp, i64, vp, vp, vp, vp] + [i32] * 7 + [vp, vp, u64, vp, i64, vp]
+        L.af_kv_pages_workspace.argtypes = [i32]
+        L.af_kv_pages_workspace.restype = u64
+        L.af_kv_pages.argtypes = [vp, vp, i32, i32, i32, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, i32, vp, u64, vp]
+        L.af_attention_paged_workspace.argtypes = [i32] * 3
+        L.af_attention_paged_workspace.restype = u64
+        L.af_attention_paged.argtypes = [vp, i64, vp, vp, vp, vp] + [i32] * 6 + [vp, i32, i32, vp, vp, i32, vp, u64, vp, i64, vp]
+        L.af_lora_plan_bytes.argtypes = [i32] * 2
+        L.af_lora_plan_bytes.restype = u64
+        L.af_lora_plan.argtypes = [vp, i32, i32, vp, u64, vp]
+        L.af_lora_workspace.argtypes = [i32] * 5
+        L.af_lora_workspace.restype = u64
+        L.af_lora.argtypes = [vp, i64, i32, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, vp, i64, vp, i64, vp, u64, vp]
         L.af_packed_call.argtypes = [ctypes.c_int, ctypes.c_char_p]
         _lib = L
     return _lib
@@ -322,6 +334,10 @@ _KV_WRITE = struct.Struct("@PPqiPiPPPPiiiiP").pack
 _KV_READ = struct.Struct("@PPPPiiiiiPiPPqP").pack
 _TREE_MASK = struct.Struct("@PiiPPP").pack
 _TREE = struct.Struct("@PqPPPPiiiiiiiPPQPqP").pack
+_PAGES = struct.Struct("@PPiiiPPPiPPPPPPiPQP").pack
+_PAGED = struct.Struct("@PqPPPPiiiiiiPiiPPiPQPqP").pack
+_LORA_PLAN = struct.Struct("@PiiPQP").pack
+_LORA = struct.Struct("@PqiPPPiPPiiiiPqPqPQP").pack
 
 
 def _addr(t):
@@ -368,6 +384,50 @@ def af_attention_tree(q_dev, ldq: int, k_cache, k_scales, v_cache, v_scales, kv_
     return _packed(4, _TREE(_addr(q_dev), ldq, _addr(k_cache), _addr(k_scales), _addr(v_cache), _addr(v_scales),
                             kv_dtype, n_heads, n_kv_heads, head_dim, ctx, n_past, n, _addr(mask_dev), _addr(ws_dev),
                             ws_bytes, _addr(out_dev), ldo, _stream(stream)))
+
+
+def af_kv_pages_workspace(n_seqs: int) -> int:
+    return int(lib().af_kv_pages_workspace(n_seqs))
+
+
+def af_kv_pages(len_dev, new_dev, n_seqs: int, page_size: int, n_pages: int, pool_dev, free_dev, table_dev, table_width: int,
+                len_out_dev, pool_out_dev, start_dev, slots_dev, pos_dev, seq_dev, max_rows: int, ws_dev, ws_bytes: int,
+                stream=None):
+    return _packed(5, _PAGES(_addr(len_dev), _addr(new_dev), n_seqs, page_size, n_pages, _addr(pool_dev), _addr(free_dev),
+                             _addr(table_dev), table_width, _addr(len_out_dev), _addr(pool_out_dev), _addr(start_dev),
+                             _addr(slots_dev), _addr(pos_dev), _addr(seq_dev), max_rows, _addr(ws_dev), ws_bytes,
+                             _stream(stream)))
+
+
+def af_attention_paged_workspace(n_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    return int(lib().af_attention_paged_workspace(n_heads, n_kv_heads, head_dim))
+
+
+def af_attention_paged(q_dev, ldq: int, k_cache, k_scales, v_cache, v_scales, kv_dtype: int, n_heads: int, n_kv_heads: int,
+                       head_dim: int, page_size: int, n_pages: int, table_dev, table_width: int, n_seqs: int, seq_dev, pos_dev,
+                       n: int, ws_dev, ws_bytes: int, out_dev, ldo: int, stream=None):
+    return _packed(6, _PAGED(_addr(q_dev), ldq, _addr(k_cache), _addr(k_scales), _addr(v_cache), _addr(v_scales), kv_dtype,
+                             n_heads, n_kv_heads, head_dim, page_size, n_pages, _addr(table_dev), table_width, n_seqs,
+                             _addr(seq_dev), _addr(pos_dev), n, _addr(ws_dev), ws_bytes, _addr(out_dev), ldo, _stream(stream)))
+
+
+def af_lora_plan_bytes(n: int, n_adapters: int) -> int:
+    return int(lib().af_lora_plan_bytes(n, n_adapters))
+
+
+def af_lora_plan(ids_dev, n: int, n_adapters: int, plan_dev, plan_bytes: int, stream=None):
+    return _packed(7, _LORA_PLAN(_addr(ids_dev), n, n_adapters, _addr(plan_dev), plan_bytes, _stream(stream)))
+
+
+def af_lora_workspace(n: int, n_adapters: int, rank: int, K: int, N: int) -> int:
+    return int(lib().af_lora_workspace(n, n_adapters, rank, K, N))
+
+
+def af_lora(x_dev, ldx: int, n: int, plan_dev, a_dev, b_dev, dtype: int, scale_dev, rank_dev, n_adapters: int, rank: int, K: int,
+            N: int, base_dev, ldb: int, y_dev, ldy: int, ws_dev, ws_bytes: int, stream=None):
+    return _packed(8, _LORA(_addr(x_dev), ldx, n, _addr(plan_dev), _addr(a_dev), _addr(b_dev), dtype, _addr(scale_dev),
+                            _addr(rank_dev), n_adapters, rank, K, N, _addr(base_dev), ldb, _addr(y_dev), ldy, _addr(ws_dev),
+                            ws_bytes, _stream(stream)))
 
 
 def af_last_error() -> str:

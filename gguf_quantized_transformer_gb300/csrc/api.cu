@@ -23,6 +23,7 @@
 
 #include "common.cuh"
 #include "draft.cuh"
+#include "serve.cuh"
 
 using namespace af;
 
@@ -1238,6 +1239,193 @@ int af_attention_tree(const float* q_dev, int64_t ldq, const void* k_cache, cons
     return AF_OK;
 }
 
+}  // extern "C"
+
+// ---------------------------------------------------------------- serving many requests: pages, paged attention, adapters
+
+namespace {
+
+// Sizes of a paged cache and its table; slot numbers and positions (with a tile's more) are 32-bit
+int check_pages(int32_t n_seqs, int32_t page, int32_t n_pages, int32_t width) {
+    if (page < 1 || n_pages < 1 || width < 1) return fail(AF_EINVAL, "page_size, n_pages and table_width must be positive");
+    if ((int64_t)n_pages * page >= INT32_MAX - 64 || (int64_t)width * page >= INT32_MAX - 64)
+        return fail(AF_ERANGE, "n_pages * page_size and table_width * page_size must be below 2^31 - 64");
+    if (n_seqs < 1 || n_seqs > kPagesMaxSeqs) return fail(AF_ERANGE, "n_seqs=%d outside [1, %d]", n_seqs, kPagesMaxSeqs);
+    return AF_OK;
+}
+
+int check_paged_heads(int32_t H, int32_t KVH, int32_t D) {
+    if (H <= 0 || KVH <= 0 || D <= 0) return fail(AF_EINVAL, "sizes must be positive");
+    if (H % KVH) return fail(AF_EINVAL, "n_heads must be a multiple of n_kv_heads");
+    if ((D != 64 && D != 128) || H / KVH > 64 || H > 65535)
+        return fail(AF_ENOTIMPL, "paged attention supports head_dim 64 / 128 and groups up to 64");
+    return AF_OK;
+}
+
+int check_lora(int32_t n, int32_t adapters) {
+    if (n < 1 || n > kLoraMaxRows) return fail(AF_ERANGE, "n=%d outside [1, %d]", n, kLoraMaxRows);
+    if (adapters < 1 || adapters > kLoraMaxAdapters)
+        return fail(AF_ERANGE, "n_adapters=%d outside [1, %d]", adapters, kLoraMaxAdapters);
+    return AF_OK;
+}
+
+int check_lora_sizes(int32_t rank, int32_t K, int32_t N) {
+    if (rank <= 0 || K <= 0 || N <= 0) return fail(AF_EINVAL, "sizes must be positive");
+    if (rank % 8 || rank > kLoraMaxRank) return fail(AF_ENOTIMPL, "rank %d must be a multiple of 8 up to %d", rank, kLoraMaxRank);
+    if (K % 32) return fail(AF_ENOTIMPL, "K %d must be a multiple of 32", K);
+    return AF_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+uint64_t af_kv_pages_workspace(int32_t n_seqs) {
+    return n_seqs < 1 || n_seqs > kPagesMaxSeqs ? 0 : 16 * ((uint64_t)n_seqs + 1);
+}
+
+int af_kv_pages(const int32_t* len_dev, const int32_t* new_dev, int32_t n_seqs, int32_t page_size, int32_t n_pages,
+                const int32_t* pool_dev, int32_t* free_dev, int32_t* table_dev, int32_t table_width, int32_t* len_out_dev,
+                int32_t* pool_out_dev, int32_t* start_dev, int32_t* slots_dev, int32_t* pos_dev, int32_t* seq_dev,
+                int32_t max_rows, void* ws_dev, uint64_t ws_bytes, void* stream) {
+    if (!len_dev || !new_dev || !pool_dev || !free_dev || !table_dev || !len_out_dev || !pool_out_dev || !start_dev || !slots_dev ||
+        !pos_dev || !seq_dev)
+        return fail(AF_EINVAL, "null argument");
+    if (((uintptr_t)len_dev | (uintptr_t)new_dev | (uintptr_t)pool_dev | (uintptr_t)free_dev | (uintptr_t)table_dev |
+         (uintptr_t)len_out_dev | (uintptr_t)pool_out_dev | (uintptr_t)start_dev | (uintptr_t)slots_dev | (uintptr_t)pos_dev |
+         (uintptr_t)seq_dev) & 3)
+        return fail(AF_EINVAL, "unaligned pointer");
+    if (int rc = check_pages(n_seqs, page_size, n_pages, table_width)) return rc;
+    if (max_rows < 0) return fail(AF_ERANGE, "max_rows=%d", max_rows);
+    const uint64_t need = af_kv_pages_workspace(n_seqs);
+    if (!ws_dev || (uintptr_t)ws_dev & 15 || ws_bytes < need)
+        return fail(AF_EINVAL, "needs a 16-byte aligned workspace of %llu bytes", (unsigned long long)need);
+    PagesArgs a;
+    a.len = len_dev;
+    a.fresh = new_dev;
+    a.n = n_seqs;
+    a.page = page_size;
+    a.n_pages = n_pages;
+    a.width = table_width;
+    a.rows = max_rows;
+    a.pool = pool_dev;
+    a.free = free_dev;
+    a.table = table_dev;
+    a.len_out = len_out_dev;
+    a.pool_out = pool_out_dev;
+    a.start = start_dev;
+    a.slots = slots_dev;
+    a.pos = pos_dev;
+    a.seq = seq_dev;
+    a.ws = (int4*)ws_dev;
+    CK(launch_kv_pages(a, (cudaStream_t)stream));
+    return AF_OK;
+}
+
+uint64_t af_attention_paged_workspace(int32_t H, int32_t KVH, int32_t D) {
+    if (check_paged_heads(H, KVH, D)) return 0;
+    return attn_paged_ws_bytes(D);
+}
+
+int af_attention_paged(const float* q_dev, int64_t ldq, const void* k_cache, const void* k_scales, const void* v_cache,
+                       const void* v_scales, int32_t kv_dtype, int32_t H, int32_t KVH, int32_t D, int32_t page_size,
+                       int32_t n_pages, const int32_t* table_dev, int32_t table_width, int32_t n_seqs, const int32_t* seq_dev,
+                       const int32_t* pos_dev, int32_t n, void* ws_dev, uint64_t ws_bytes, float* out_dev, int64_t ldo,
+                       void* stream) {
+    if (!q_dev || !table_dev || !pos_dev || !out_dev) return fail(AF_EINVAL, "null argument");
+    if (int rc = check_paged_heads(H, KVH, D)) return rc;
+    if (int rc = check_pages(n_seqs, page_size, n_pages, table_width)) return rc;
+    PagedArgs a;
+    if (int rc = check_cache(k_cache, k_scales, v_cache, v_scales, kv_dtype, KVH, D, n_pages * page_size, a.c)) return rc;
+    if ((int64_t)KVH * a.c.ctx > INT32_MAX) return fail(AF_ENOTIMPL, "n_kv_heads * n_pages * page_size above 2^31 - 1");
+    if (n < 1 || n > kPagedMaxRows) return fail(AF_ERANGE, "n=%d outside [1, %d]", n, kPagedMaxRows);
+    if (!seq_dev && n > n_seqs) return fail(AF_ERANGE, "%d rows for %d requests", n, n_seqs);
+    if (((uintptr_t)q_dev | (uintptr_t)out_dev) & 15 || ((uintptr_t)table_dev | (uintptr_t)seq_dev | (uintptr_t)pos_dev) & 3)
+        return fail(AF_EINVAL, "unaligned pointer");
+    if (ldq < (int64_t)H * D || ldo < (int64_t)H * D || ldq % 4 || ldo % 4)
+        return fail(AF_EINVAL, "ldq and ldo must be multiples of 4 >= n_heads * head_dim");
+    const size_t need = attn_paged_ws_bytes(D);
+    if (!ws_dev || (uintptr_t)ws_dev & 255 || ws_bytes < need)
+        return fail(AF_EINVAL, "needs a 256-byte aligned workspace of %zu bytes", need);
+    a.q = q_dev;
+    a.ldq = ldq;
+    a.H = H;
+    a.page = page_size;
+    a.n_pages = n_pages;
+    a.width = table_width;
+    a.n_seqs = n_seqs;
+    a.n = n;
+    if (page_size > 1) {  // exact for slots below 2^31: the multiplier is 2^(31 + l) / page_size rounded up, 2^l >= page_size
+        int l = 1;
+        while ((1LL << l) < page_size) l++;
+        a.page_mul = (unsigned)(((1ULL << (31 + l)) + page_size - 1) / page_size);
+        a.page_shift = l - 1;
+    }
+    a.table = table_dev;
+    a.seq = seq_dev;
+    a.pos = pos_dev;
+    a.out = out_dev;
+    a.ldo = ldo;
+    a.ws = (float*)ws_dev;
+    CK(launch_attn_paged(a, (cudaStream_t)stream));
+    return AF_OK;
+}
+
+uint64_t af_lora_plan_bytes(int32_t n, int32_t n_adapters) { return check_lora(n, n_adapters) ? 0 : lora_plan_bytes(n, n_adapters); }
+
+int af_lora_plan(const int32_t* ids_dev, int32_t n, int32_t n_adapters, void* plan_dev, uint64_t plan_bytes, void* stream) {
+    if (!ids_dev || !plan_dev) return fail(AF_EINVAL, "null argument");
+    if (int rc = check_lora(n, n_adapters)) return rc;
+    if ((uintptr_t)ids_dev & 3 || (uintptr_t)plan_dev & 15) return fail(AF_EINVAL, "unaligned pointer");
+    if (plan_bytes < lora_plan_bytes(n, n_adapters))
+        return fail(AF_EINVAL, "the plan needs %zu bytes", lora_plan_bytes(n, n_adapters));
+    CK(launch_lora_plan(ids_dev, n, n_adapters, plan_dev, (cudaStream_t)stream));
+    return AF_OK;
+}
+
+uint64_t af_lora_workspace(int32_t n, int32_t n_adapters, int32_t rank, int32_t K, int32_t N) {
+    return check_lora(n, n_adapters) || check_lora_sizes(rank, K, N) ? 0 : lora_ws_bytes(n, rank);
+}
+
+int af_lora(const float* x_dev, int64_t ldx, int32_t n, const void* plan_dev, const void* a_dev, const void* b_dev, int32_t dtype,
+            const float* scale_dev, const int32_t* rank_dev, int32_t n_adapters, int32_t rank, int32_t K, int32_t N,
+            const float* base_dev, int64_t ldb, float* y_dev, int64_t ldy, void* ws_dev, uint64_t ws_bytes, void* stream) {
+    if (!x_dev || !plan_dev || !a_dev || !b_dev || !y_dev) return fail(AF_EINVAL, "null argument");
+    if (int rc = check_lora(n, n_adapters)) return rc;
+    if (int rc = check_lora_sizes(rank, K, N)) return rc;
+    if (dtype != AF_F32 && dtype != AF_F16) return fail(AF_EINVAL, "dtype must be AF_F32 or AF_F16");
+    if (ldx < K || ldx % 4) return fail(AF_EINVAL, "ldx must be a multiple of 4 >= K");
+    if (ldy < N || (base_dev && ldb < N)) return fail(AF_EINVAL, "ldb and ldy must be at least N");
+    if (base_dev == y_dev && ldb != ldy) return fail(AF_EINVAL, "in place needs ldb == ldy");
+    if (((uintptr_t)x_dev | (uintptr_t)a_dev | (uintptr_t)b_dev | (uintptr_t)plan_dev) & 15 ||
+        ((uintptr_t)base_dev | (uintptr_t)y_dev | (uintptr_t)scale_dev | (uintptr_t)rank_dev) & 3)
+        return fail(AF_EINVAL, "unaligned pointer");
+    const size_t need = lora_ws_bytes(n, rank);
+    if (!ws_dev || (uintptr_t)ws_dev & 255 || ws_bytes < need)
+        return fail(AF_EINVAL, "needs a 256-byte aligned workspace of %zu bytes", need);
+    LoraArgs a;
+    a.x = x_dev;
+    a.ldx = ldx;
+    a.n = n;
+    a.plan = plan_dev;
+    a.a = a_dev;
+    a.b = b_dev;
+    a.f16 = dtype == AF_F16;
+    a.scale = scale_dev;
+    a.ranks = rank_dev;
+    a.adapters = n_adapters;
+    a.rank = rank;
+    a.K = K;
+    a.N = N;
+    a.base = base_dev;
+    a.ldb = ldb;
+    a.y = y_dev;
+    a.ldy = ldy;
+    a.ws = (float*)ws_dev;
+    CK(launch_lora(a, (cudaStream_t)stream));
+    return AF_OK;
+}
+
 // The calls above with their arguments as one record in C layout (members in the order of the arguments): what the
 // Python binding makes, since converting nineteen arguments one by one takes longer than the launch.
 __attribute__((visibility("default"))) int af_packed_call(int op, const void* record) {
@@ -1314,6 +1502,76 @@ __attribute__((visibility("default"))) int af_packed_call(int op, const void* re
             memcpy(&r, record, sizeof r);
             return af_attention_tree(r.q, r.ldq, r.kc, r.ks, r.vc, r.vs, r.type, r.h, r.kvh, r.d, r.ctx, r.past, r.n, r.mask,
                                      r.ws, r.ws_bytes, r.out, r.ldo, r.stream);
+        }
+        case 5: {
+            struct R {
+                const int32_t *len, *fresh;
+                int32_t n_seqs, page, n_pages;
+                const int32_t* pool;
+                int32_t *free, *table;
+                int32_t width;
+                int32_t *len_out, *pool_out, *start, *slots, *pos, *seq;
+                int32_t max_rows;
+                void* ws;
+                uint64_t ws_bytes;
+                void* stream;
+            } r;
+            memcpy(&r, record, sizeof r);
+            return af_kv_pages(r.len, r.fresh, r.n_seqs, r.page, r.n_pages, r.pool, r.free, r.table, r.width, r.len_out,
+                               r.pool_out, r.start, r.slots, r.pos, r.seq, r.max_rows, r.ws, r.ws_bytes, r.stream);
+        }
+        case 6: {
+            struct R {
+                const float* q;
+                int64_t ldq;
+                const void *kc, *ks, *vc, *vs;
+                int32_t type, h, kvh, d, page, n_pages;
+                const int32_t* table;
+                int32_t width, n_seqs;
+                const int32_t *seq, *pos;
+                int32_t n;
+                void* ws;
+                uint64_t ws_bytes;
+                float* out;
+                int64_t ldo;
+                void* stream;
+            } r;
+            memcpy(&r, record, sizeof r);
+            return af_attention_paged(r.q, r.ldq, r.kc, r.ks, r.vc, r.vs, r.type, r.h, r.kvh, r.d, r.page, r.n_pages, r.table,
+                                      r.width, r.n_seqs, r.seq, r.pos, r.n, r.ws, r.ws_bytes, r.out, r.ldo, r.stream);
+        }
+        case 7: {
+            struct R {
+                const int32_t* ids;
+                int32_t n, adapters;
+                void* plan;
+                uint64_t bytes;
+                void* stream;
+            } r;
+            memcpy(&r, record, sizeof r);
+            return af_lora_plan(r.ids, r.n, r.adapters, r.plan, r.bytes, r.stream);
+        }
+        case 8: {
+            struct R {
+                const float* x;
+                int64_t ldx;
+                int32_t n;
+                const void *plan, *a, *b;
+                int32_t dtype;
+                const float* scale;
+                const int32_t* ranks;
+                int32_t adapters, rank, k, n_out;
+                const float* base;
+                int64_t ldb;
+                float* y;
+                int64_t ldy;
+                void* ws;
+                uint64_t ws_bytes;
+                void* stream;
+            } r;
+            memcpy(&r, record, sizeof r);
+            return af_lora(r.x, r.ldx, r.n, r.plan, r.a, r.b, r.dtype, r.scale, r.ranks, r.adapters, r.rank, r.k, r.n_out, r.base,
+                           r.ldb, r.y, r.ldy, r.ws, r.ws_bytes, r.stream);
         }
         default: return fail(AF_EINVAL, "unknown record");
     }

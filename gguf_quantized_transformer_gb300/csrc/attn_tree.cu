@@ -39,6 +39,7 @@
 #include <type_traits>
 
 #include "draft.cuh"
+#include "mma_sync.cuh"
 #include "tma.cuh"
 
 namespace af {
@@ -74,11 +75,6 @@ constexpr float kLazyT = 4.f;  // powers of two by which a score may exceed the 
 constexpr float kBiasT = 8.f;  // p = 2^(s - m + kBiasT): at most 2^12
 constexpr float kNoRefT = -1000.f;  // a row's exponent of the output before it has one
 
-__device__ __forceinline__ float ex2t(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool in) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
@@ -113,69 +109,6 @@ __device__ __forceinline__ uint4 ldsm4t(uint32_t a) {
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "r"(a));
     return v;
-}
-__device__ __forceinline__ void mma16(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma8(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
-}
-// The same onto zero
-__device__ __forceinline__ void mma16z(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
-        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.f));
-}
-__device__ __forceinline__ void mma8z(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
-        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.f));
-}
-// o += c, rounded: a stage's sum joins the walk's
-__device__ __forceinline__ void add4(float (&o)[4], const float (&c)[4]) {
-#pragma unroll
-    for (int i = 0; i < 4; i += 2) {
-        const float2 x = add2(make_float2(o[i], o[i + 1]), make_float2(c[i], c[i + 1]));
-        o[i] = x.x, o[i + 1] = x.y;
-    }
-}
-__device__ __forceinline__ uint32_t tf32_of(float x) {
-    uint32_t r;
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
-    return r;
-}
-// x = hi + lo in two tf32 parts
-__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-    hi = tf32_of(x);
-    lo = tf32_of(x - __uint_as_float(hi));
-}
-// The same for a value of the cache, whose hi part is cut, not rounded: rounded, fp32's largest numbers would be infinities,
-// which times a zero weight are NaN.  lo is then up to 2^-10 of x and off by 2^-22.  (One token over 30000 fp32 slots
-// 45.2 us, 51.9 with rounded parts: the cut is a plain logic instruction.)
-__device__ __forceinline__ void cut_tf32(float x, uint32_t& hi, uint32_t& lo) {
-    hi = __float_as_uint(x) & 0xFFFFE000u;
-    lo = tf32_of(x - __uint_as_float(hi));
-}
-// (a, b) = hi + lo in two fp16 parts each
-__device__ __forceinline__ void split_h2(float a, float b, uint32_t& hi, uint32_t& lo) {
-    const __half2 h = __floats2half2_rn(a, b);
-    const float2 r = fma2(__half22float2(h), both(-1.f), make_float2(a, b));
-    const __half2 l = __floats2half2_rn(r.x, r.y);
-    hi = *reinterpret_cast<const uint32_t*>(&h);
-    lo = *reinterpret_cast<const uint32_t*>(&l);
-}
-// two halves of `magic + code` minus `off`: the codes as fp16
-__device__ __forceinline__ uint32_t hsub2u(uint32_t x, uint32_t off) {
-    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&off));
-    return *reinterpret_cast<const uint32_t*>(&r);
 }
 // non-finite halves of x become 0; `bad` is set if there were any
 __device__ __forceinline__ uint32_t finite_h2(uint32_t x, bool& bad) {

@@ -1,0 +1,178 @@
+// The step of a serving loop that maps new tokens to slots of a paged cache: request i holds len_i tokens in the pages
+// that its table row names, page_size to a page.  Its new tokens get the rows start_i .. of the batch; a token at position p
+// lies in slot page * page_size + p % page_size.  Pages come from the head of a ring of free ones, in the requests' order,
+// and those of ended requests go behind its last one, so that no entry that is read here is written here.
+//
+// Three prefix sums over the requests (rows; then pages taken and pages given back, which need the first), one CTA; then one
+// thread per row of the batch, which finds its request by a binary search over the rows' starts.  A new page begins with a
+// new token, so the thread of the page's first token writes the table.  Small steps do both in the one CTA, larger ones the
+// second part in a grid of their own.
+#include <algorithm>
+
+#include "serve.cuh"
+#include "tma.cuh"
+
+namespace af {
+
+namespace {
+
+constexpr int kScan = 1024;             // threads of the scanning CTA
+constexpr int kFillRows = 4, kFill = 256;  // rows of a thread, threads of a CTA of the second part
+
+// A request as the second part sees it: .x the first page it takes (an index behind the ring's head), kRefused or kEnded;
+// .y its tokens before the step, .z its pages before the step, .w pages given back by earlier requests
+constexpr int kRefused = -1, kEnded = -2;
+
+__device__ __forceinline__ int64_t clamp_int(int64_t x) { return x < INT32_MAX ? x : INT32_MAX; }
+
+// Inclusive prefix sums over the CTA of two values a thread; `total` receives the CTA's.
+__device__ __forceinline__ void cta_scan2(int64_t& x, int64_t& y, int64_t (&total)[2]) {
+    __shared__ int64_t part[2][kScan / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int64_t a = __shfl_up_sync(0xffffffffu, x, o), b = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) x += a, y += b;
+    }
+    __syncthreads();  // (the previous call's parts have been read)
+    if (lane == 31) part[0][warp] = x, part[1][warp] = y;
+    __syncthreads();
+    if (warp == 0) {
+        int64_t u = part[0][lane], v = part[1][lane];
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const int64_t a = __shfl_up_sync(0xffffffffu, u, o), b = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) u += a, v += b;
+        }
+        part[0][lane] = u, part[1][lane] = v;
+    }
+    __syncthreads();
+    if (warp) x += part[0][warp - 1], y += part[1][warp - 1];
+    total[0] = part[0][kScan / 32 - 1], total[1] = part[1][kScan / 32 - 1];
+}
+
+// The last i of [0, n) with key(i) <= x; key(0) <= x
+template <typename F>
+__device__ __forceinline__ int last_le(int n, int x, F key) {
+    int lo = 0, hi = n;  // key(lo) <= x < key(hi)
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (key(mid) <= x)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// Rows and returned pages of thread t of nt.  start(i), back(i): the prefix sums; head, count: the ring before the step.
+template <typename S, typename B>
+__device__ __forceinline__ void fill(const PagesArgs& a, int64_t t, int64_t nt, int total, int returned, int head, int count, S start,
+                                     B back) {
+    for (int64_t r = t; r < a.rows; r += nt) {
+        int slot = -1, pos = -1, seq = -1;
+        if (r < total) {
+            const int i = last_le(a.n, (int)r, start);
+            const int4 q = __ldcg(a.ws + i);
+            if (q.x >= 0) {
+                pos = q.y + ((int)r - start(i));
+                const int at = pos / a.page, off = pos - at * a.page;
+                int page;
+                if (at < q.z) {
+                    page = __ldcg(a.table + (int64_t)i * a.width + at);
+                } else {
+                    page = __ldcg(a.free + ((int64_t)head + q.x + (at - q.z)) % a.n_pages);
+                    if (off == 0) a.table[(int64_t)i * a.width + at] = page;
+                }
+                slot = page >= 0 && page < a.n_pages ? page * a.page + off : -1;
+                seq = i;
+            }
+        }
+        a.slots[r] = slot;
+        a.pos[r] = pos;
+        a.seq[r] = seq;
+    }
+    for (int64_t e = t; e < returned; e += nt) {
+        const int i = last_le(a.n, (int)e, back);
+        a.free[((int64_t)head + count + e) % a.n_pages] = __ldcg(a.table + (int64_t)i * a.width + ((int)e - back(i)));
+    }
+}
+
+// FILL: both parts.
+template <bool FILL>
+__global__ void __launch_bounds__(kScan) kv_pages_scan_kernel(PagesArgs a) {
+    __shared__ int sm_start[FILL ? kScan : 1], sm_back[FILL ? kScan : 1];
+    __shared__ int sm_taken, sm_returned, sm_refused;
+    const int t = threadIdx.x;
+    pdl_launch_dependents();
+    pdl_wait();
+    int head = __ldcg(a.pool), count = __ldcg(a.pool + 1);
+    head = head >= 0 && head < a.n_pages ? head : 0;
+    count = min(max(count, 0), a.n_pages);
+    if (t == 0) sm_taken = sm_returned = sm_refused = 0;
+    int64_t rows0 = 0, take0 = 0, back0 = 0;  // sums of the requests before this round of kScan
+    const int64_t most = (int64_t)a.width * a.page;
+    for (int i0 = 0; i0 < a.n; i0 += kScan) {
+        const int i = i0 + t;
+        const bool in = i < a.n;
+        const int len = in ? __ldcg(a.len + i) : 0, fresh = in ? __ldcg(a.fresh + i) : 0;
+        const bool ends = fresh < 0, sound = len >= 0 && len <= most;
+        const int64_t grow = ends ? 0 : fresh;
+        int64_t rows = grow, unused = 0, total[2];
+        cta_scan2(rows, unused, total);
+        rows += rows0;
+        rows0 += total[0];
+        const int have = sound ? (int)(((int64_t)len + a.page - 1) / a.page) : 0;
+        const bool fits = in && !ends && sound && rows <= a.rows && len + grow <= most;
+        const int64_t need = fits ? (len + grow + a.page - 1) / a.page - have : 0, back = in && ends ? have : 0;
+        int64_t taken = need, returned = back;
+        cta_scan2(taken, returned, total);
+        taken += take0, returned += back0;
+        take0 += total[0], back0 += total[1];
+        const bool served = fits && (need == 0 || taken <= count);
+        const bool ended = in && ends && sound && (int64_t)count + returned <= a.n_pages;
+        if (in) {
+            const int start = (int)clamp_int(rows - grow);
+            a.start[i] = start;
+            a.ws[i] = make_int4(served ? (int)(need ? taken - need : 0) : ended ? kEnded : kRefused, len, have,
+                                (int)clamp_int(returned - back));
+            a.len_out[i] = served ? (int)(len + grow) : ended ? 0 : len;
+            if (FILL) sm_start[i] = start, sm_back[i] = (int)clamp_int(returned - back);
+            if (served && need) atomicMax(&sm_taken, (int)taken);
+            if (ended) atomicMax(&sm_returned, (int)returned);
+            if (!served && !ended) atomicAdd(&sm_refused, 1);
+        }
+        __syncthreads();
+    }
+    const int total = (int)clamp_int(rows0), taken = sm_taken, returned = sm_returned;
+    if (t == 0) {
+        a.start[a.n] = total;
+        a.ws[a.n] = make_int4(head, count, total, returned);
+        a.pool_out[0] = (int)(((int64_t)head + taken) % a.n_pages);
+        a.pool_out[1] = count - taken + returned;
+        a.pool_out[2] = sm_refused;
+        a.pool_out[3] = total;
+    }
+    if (FILL) fill(a, t, kScan, total, returned, head, count, [&](int i) { return sm_start[i]; }, [&](int i) { return sm_back[i]; });
+}
+
+__global__ void __launch_bounds__(kFill) kv_pages_fill_kernel(PagesArgs a) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int4 h = __ldcg(a.ws + a.n);
+    fill(a, (int64_t)blockIdx.x * kFill + threadIdx.x, (int64_t)gridDim.x * kFill, h.z, h.w, h.x, h.y,
+         [&](int i) { return __ldcg(a.start + i); }, [&](int i) { return __ldcg(&a.ws[i].w); });
+}
+
+}  // namespace
+
+cudaError_t launch_kv_pages(const PagesArgs& a, cudaStream_t s) {
+    if (a.n <= kScan && a.rows <= 4 * kScan) return launch_chained(kv_pages_scan_kernel<true>, dim3(1), kScan, 0, s, a);
+    cudaError_t e = launch_chained(kv_pages_scan_kernel<false>, dim3(1), kScan, 0, s, a);
+    if (e) return e;
+    const int64_t work = std::max<int64_t>(a.rows, a.n);
+    const int ctas = (int)std::min<int64_t>((work + kFill * kFillRows - 1) / (kFill * kFillRows), 8 * (int64_t)num_sms());
+    return launch_chained(kv_pages_fill_kernel, dim3(std::max(ctas, 1)), kFill, 0, s, a);
+}
+
+}  // namespace af

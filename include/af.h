@@ -478,6 +478,107 @@ int af_attention_tree(const float* q_dev, int64_t ldq, const void* k_cache, cons
                       int32_t ctx, int32_t n_past, int32_t n, const uint32_t* mask_dev, void* ws_dev, uint64_t ws_bytes,
                       float* out_dev, int64_t ldo, void* stream);
 
+/*
+ * A paged cache of many requests: a cache as af_kv_write's with ctx = n_pages * page_size slots, in which page p is the
+ * slots p * page_size .. + page_size - 1 (of every kv head) and a request's tokens lie in the pages that its row of the
+ * block table names, in order: the token at position t in slot table[t / page_size] * page_size + t % page_size.
+ * af_kv_write and af_kv_read move its rows by those slots.
+ *
+ * af_kv_pages: one step of the loop that serves the requests, on the device, so that a captured step needs no host: slots
+ * for the new tokens of all requests, pages for them from the free ones, and the pages of ended requests back.
+ *   len_dev     int32 [n_seqs]: tokens that each request has in the cache
+ *   new_dev     int32 [n_seqs]: tokens that the step adds to it; negative: the request has ended
+ *   pool_dev    int32 [4]: head and count of the ring of free pages (two more are ignored)
+ *   free_dev    int32 [n_pages]: the ring: free page i is free_dev[(head + i) % n_pages].  Pages are taken at the head, in
+ *               the requests' order, and returned behind the last one
+ *   table_dev   int32 [n_seqs][table_width]: the entries of pages taken are written, all others stay
+ *   len_out_dev  int32 [n_seqs]: tokens after the step (ended: 0); may be len_dev
+ *   pool_out_dev int32 [4]: the ring after the step, the number of requests refused, and the rows that the step wants; may
+ *               be pool_dev
+ *   start_dev   int32 [n_seqs + 1]: the batch's first row of each request, and the number of rows (2^31 - 1 for more)
+ *   slots_dev, pos_dev, seq_dev  int32 [max_rows]: of each row (a request's new tokens in order, the requests in theirs)
+ *               its slot, its position and its request; -1 in all three for the rows behind the last one and those of
+ *               refused requests, which af_kv_write skips and af_attention_paged answers with zeros.  (A slot alone is -1
+ *               where the table or the ring names no page of the cache.)
+ * A request is refused, and stays as it is, if its length is negative or more than its table row holds, if the step would
+ * make it so, if its rows do not end within max_rows, if it needs more pages than the requests before it (refused ones for
+ * want of pages among them) have left, or if it returns more pages than the ring has room for.
+ * A page belongs to one request; the ring never holds more than n_pages.  No entry of a page outside [0, n_pages) leads to
+ * memory outside the cache, here or in af_attention_paged.
+ *   ws_dev      scratch of af_kv_pages_workspace(n_seqs) bytes, 16-byte aligned, of any contents
+ * 1 <= n_seqs <= 65536, 0 <= max_rows, page_size and table_width at least 1, n_pages * page_size and table_width *
+ * page_size below 2^31 - 64.  Apart from the two pairs named, no two buffers overlap.  Asynchronous on `stream`, allocates
+ * nothing, can be captured.  Errors: AF_EINVAL, AF_ERANGE, AF_ECUDA.
+ */
+uint64_t af_kv_pages_workspace(int32_t n_seqs);
+int af_kv_pages(const int32_t* len_dev, const int32_t* new_dev, int32_t n_seqs, int32_t page_size, int32_t n_pages,
+                const int32_t* pool_dev, int32_t* free_dev, int32_t* table_dev, int32_t table_width, int32_t* len_out_dev,
+                int32_t* pool_out_dev, int32_t* start_dev, int32_t* slots_dev, int32_t* pos_dev, int32_t* seq_dev,
+                int32_t max_rows, void* ws_dev, uint64_t ws_bytes, void* stream);
+
+/*
+ * Attention of single tokens over a paged cache (a decode step of many requests): row r of n attends to the positions
+ * 0..pos_dev[r] of request seq_dev[r], its own among them (so its key and value are written first);
+ * softmax(q K^T / sqrt(head_dim)) V, GQA group = n_heads / n_kv_heads.
+ *   q_dev     fp32 [n] rows of n_heads * head_dim values (rotated), ldq apart
+ *   cache     as af_kv_write's, with n_pages * page_size slots
+ *   table_dev int32 [n_seqs][table_width], as af_kv_pages writes it
+ *   seq_dev   int32 [n]: the table's row of each batch row, any order, the same one more than once if need be (several new
+ *             tokens of a request are rows with positions of their own); NULL: row r is request r (n <= n_seqs)
+ *   pos_dev   int32 [n].  A row with a negative position or a request outside [0, n_seqs) gives zeros; a position behind
+ *             the table's last slot sees the slots that the table has.  Slots of pages outside [0, n_pages) are hidden: they
+ *             are not read, and a row that sees no other slot gives zeros
+ *   ws_dev    scratch of at least af_attention_paged_workspace bytes, 256-byte aligned, of any contents (1.3 MB with
+ *             head_dim 128 on 152 SMs, whatever the rows); calls that may overlap in time need scratch of their own
+ *   out_dev   fp32 [n] rows, ldo apart
+ * The work is split by the slots that the rows see, found on the device: lengths may differ as they like, and a captured
+ * call serves any lengths.  Precision, bits from call to call, and rows that see a NaN or an infinity: as
+ * af_attention_tree's.  What slots hold that a row does not see reaches nothing.
+ * 1 <= n <= 4096; head_dim 64 or 128, any whole group up to 64; n_kv_heads * n_pages * page_size below 2^31, page_size and
+ * table_width at least 1, table_width * page_size below 2^31 - 64.  Pointers are 16-byte aligned (table_dev, seq_dev,
+ * pos_dev: 4), ldq and ldo multiples of 4.  Asynchronous on `stream`, allocates nothing, can be captured (the first call on
+ * a device loads the kernels: make it before a capture).  Errors: AF_EINVAL, AF_ERANGE, AF_ENOTIMPL, AF_ECUDA.
+ */
+uint64_t af_attention_paged_workspace(int32_t n_heads, int32_t n_kv_heads, int32_t head_dim);
+int af_attention_paged(const float* q_dev, int64_t ldq, const void* k_cache, const void* k_scales, const void* v_cache,
+                       const void* v_scales, int32_t kv_dtype, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                       int32_t page_size, int32_t n_pages, const int32_t* table_dev, int32_t table_width, int32_t n_seqs,
+                       const int32_t* seq_dev, const int32_t* pos_dev, int32_t n, void* ws_dev, uint64_t ws_bytes,
+                       float* out_dev, int64_t ldo, void* stream);
+
+/*
+ * Low-rank adapters of many requests beside a shared projection (af_qgemm, af_qgemv): for row i of a batch, whose adapter
+ * is a = ids_dev[i],   y_i = base_i + scale_a B_a (A_a x_i).
+ * af_lora_plan puts the rows in the order of their adapters, once a step for all layers and projections:
+ *   ids_dev   int32 [n]; a value outside [0, n_adapters) is a row without an adapter
+ *   plan_dev  af_lora_plan_bytes(n, n_adapters) bytes, 16-byte aligned
+ * af_lora, with the n and n_adapters of its plan:
+ *   x_dev     fp32 [n] rows of K values, ldx apart
+ *   a_dev     [n_adapters][rank][K], b_dev [n_adapters][N][rank] of dtype AF_F16 or AF_F32
+ *   scale_dev fp32 [n_adapters]; NULL: 1
+ *   rank_dev  int32 [n_adapters]: ranks of adapters that have fewer than `rank` (taken into [0, rank]); what lies behind
+ *             them in a_dev and b_dev reaches nothing.  NULL: all have `rank`
+ *   base_dev  fp32 [n] rows of N values, ldb apart: the projection's; may be y_dev with ldb == ldy, and overlaps it in no
+ *             other way; NULL: zeros
+ *   y_dev     fp32 [n] rows, ldy apart.  Rows without an adapter are the base's
+ *   ws_dev    scratch of af_lora_workspace(n, n_adapters, rank, K, N) bytes, 256-byte aligned, of any contents; calls that
+ *             may overlap in time need scratch of their own
+ * Precision: products of two parts of 11 bits each (2^-20 of the sum of the products' magnitudes), sums in fp32.  A row's
+ * result does not depend on the other rows but for the order in which K's sums are joined; its bits do not change from call
+ * to call with the same plan.
+ * 1 <= n <= 65536, 1 <= n_adapters <= 4096; rank a multiple of 8 up to 128 (pad with rank_dev); K a multiple of 32, N any.
+ * x_dev, a_dev, b_dev are 16-byte aligned and ldx a multiple of 4; base_dev and y_dev 4-byte aligned (vectors of 16 bytes
+ * are moved where they, N, ldb and ldy allow it).  Asynchronous on `stream`, allocate nothing, can be captured (the first
+ * call on a device loads the kernels: make it before a capture).  Errors: AF_EINVAL, AF_ERANGE, AF_ENOTIMPL, AF_ECUDA.
+ */
+uint64_t af_lora_plan_bytes(int32_t n, int32_t n_adapters);
+int af_lora_plan(const int32_t* ids_dev, int32_t n, int32_t n_adapters, void* plan_dev, uint64_t plan_bytes, void* stream);
+uint64_t af_lora_workspace(int32_t n, int32_t n_adapters, int32_t rank, int32_t K, int32_t N);
+int af_lora(const float* x_dev, int64_t ldx, int32_t n, const void* plan_dev, const void* a_dev, const void* b_dev,
+            int32_t dtype, const float* scale_dev, const int32_t* rank_dev, int32_t n_adapters, int32_t rank, int32_t K,
+            int32_t N, const float* base_dev, int64_t ldb, float* y_dev, int64_t ldy, void* ws_dev, uint64_t ws_bytes,
+            void* stream);
+
 /* Thread-local message for the last failed call on this thread ("" if none). */
 const char* af_last_error(void);
 
