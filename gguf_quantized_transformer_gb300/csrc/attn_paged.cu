@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(PagedArgs a
 }  // namespace
 
 size_t attn_paged_ws_bytes(int D) {
-    return (size_t)num_sms() * 2 * (paged_piece_floats(D) * sizeof(float) + sizeof(PagedPiece));
+    return paged_ws_floats(num_sms(), D) * sizeof(float);
 }
 
 cudaError_t launch_attn_paged(const PagedArgs& a, cudaStream_t s) {

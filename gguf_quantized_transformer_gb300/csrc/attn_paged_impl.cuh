@@ -43,42 +43,84 @@ struct PagedPiece {
 };
 constexpr int kPagedHeads = 8;  // heads of a piece at most
 __host__ __device__ constexpr size_t paged_piece_floats(int D) { return (size_t)kPagedHeads * (D + 2); }
-// ws: [ctas][2] pieces of paged_piece_floats (outputs [8][D], then [8] (m, l)), then [ctas][2] PagedPiece
+// ws: [ctas][2] pieces of paged_piece_floats (outputs [8][D], then [8] (m, l)), [ctas][2] PagedPiece, then the pieces of warps
+// that end before the warp does: 16 warps of 4 heads or 8 of 8
+__host__ __device__ constexpr size_t paged_far(int ctas, int D) {
+    return (size_t)ctas * 2 * (paged_piece_floats(D) + sizeof(PagedPiece) / 4);
+}
+__host__ __device__ constexpr size_t paged_ws_floats(int ctas, int D) {
+    return paged_far(ctas, D) + (size_t)ctas * 8 * paged_piece_floats(D);
+}
+
+// Stages of a warp's ring in flight, and warps of a CTA (one to an SM)
+__host__ __device__ constexpr int paged_warps(int type, int D, int nt) {
+    return type == AF_F32 ? (D == 128 ? 6 : 8) : type == AF_F16 ? 8 : nt == 1 ? 12 : 8;
+}
+__host__ __device__ constexpr int paged_stages(int stage, int warps) {
+    return 216 * 1024 / (stage * warps) < 6 ? 216 * 1024 / (stage * warps) : 6;
+}
 
 template <int TYPE, int D, int NT>
 struct PagedCfg {
     static constexpr bool QUANT = TYPE == AF_KV_Q8_0 || TYPE == AF_KV_Q4_0;
     static constexpr int NB = D / 32;
     static constexpr int RB = TYPE == AF_F32 ? 4 * D : TYPE == AF_F16 ? 2 * D : TYPE == AF_KV_Q8_0 ? D : D / 2;  // row bytes
-    static constexpr int SB = QUANT ? 2 * NB : 0;
-    static constexpr int SUB = QUANT ? 2 : 1;  // 16-slot tiles of a stage
+    static constexpr int SB = QUANT ? 2 * NB : 0;  // scale bytes of a row
+    static constexpr int SUB = QUANT ? 2 : 1;      // 16-slot tiles of a stage
     static constexpr int KS = 16 * SUB;
-    static constexpr int KW = RB / 16;  // 32-bit words of K per thread, slot row and 16-slot tile (a quarter of a row)
-    static constexpr int VW = RB / 32;  // of V (an eighth)
     static constexpr int STEPS = TYPE == AF_F32 ? D / 8 : D / 16;  // matrix steps along a head
     static constexpr int MT = D / 16;                              // row tiles of the output
     static constexpr int HEADS = 4 * NT;
-    static constexpr int NW = TYPE == AF_F32 ? 8 : NT == 1 ? 12 : 8;  // warps
-    static constexpr bool QSMEM = TYPE == AF_F32;  // q's operands in shared memory
-    static constexpr int QBYTES = QSMEM ? NW * NT * STEPS * 32 * 8 : 0;
+    static constexpr int NW = paged_warps(TYPE, D, NT);
+    // a stage: K rows, V rows, and the 16 bytes around each slot's K and V scales
+    static constexpr int OV = KS * RB, OKS = 2 * KS * RB, OVS = OKS + (QUANT ? 16 * KS : 0);
+    static constexpr int STAGE = OVS + (QUANT ? 16 * KS : 0);
+    static constexpr int NST = paged_stages(STAGE, NW);
+    static_assert(NST >= 2, "a stage in flight while one is read");
     static constexpr int PIECE = HEADS * (D + 2);  // floats of a warp's piece
-    static constexpr int JOIN = NW * 2 * PIECE * 4;
-    // first of the dims that lane c of a K row owns in block b (8 in a row)
-    static __device__ __forceinline__ int kdim(int b, int c) {
-        return TYPE == AF_KV_Q4_0 ? 32 * b + 8 * ((c & 1) * 2 + (c >> 1)) : 32 * b + 8 * c;
+    static_assert(PIECE * 4 <= NST * STAGE, "a piece fits the ring");
+    // 16-byte chunk permutations within 128 bytes, by row, so that the reads of a warp meet all banks
+    static __device__ __forceinline__ int swk(int r) {
+        if (TYPE == AF_F32 || TYPE == AF_F16) return (r & 1) << 2;
+        if (TYPE == AF_KV_Q8_0) return D == 128 ? (r & 3) << 1 : (r & 2);
+        return D == 128 ? (r >> 1) & 3 : (r >> 2) & 1;
     }
+    static __device__ __forceinline__ int swv(int r) {
+        if (TYPE == AF_F32) return (r & 3) << 1;
+        if (TYPE == AF_F16 || TYPE == AF_KV_Q8_0) return ((r >> 1) & 3) << 1;
+        return D == 128 ? (r >> 1) & 3 : (r >> 2) & 1;
+    }
+    // where byte `at` of row r lies
+    static __device__ __forceinline__ int kbyte(int r, int at) { return (r * RB + at) ^ (swk(r) << 4); }
+    static __device__ __forceinline__ int vbyte(int r, int at) { return OV + ((r * RB + at) ^ (swv(r) << 4)); }
 };
 
-// ---- loads through L2: what earlier kernels of the chain have written may be stale in L1
-__device__ __forceinline__ void ldg16(const void* p, uint32_t* w) {
-    const uint4 x = __ldcg(reinterpret_cast<const uint4*>(p));
-    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+// 16 bytes from global to shared memory through L2 (what earlier kernels of the chain have written may be stale in L1), of
+// which the first `bytes` are read and the others zeros
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void ldg8(const void* p, uint32_t* w) {
-    const uint2 x = __ldcg(reinterpret_cast<const uint2*>(p));
-    w[0] = x.x, w[1] = x.y;
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ uint32_t ldg4(const void* p) { return __ldcg(reinterpret_cast<const unsigned*>(p)); }
+__device__ __forceinline__ void shared128(uint32_t a, uint32_t* w) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a));
+}
+__device__ __forceinline__ void shared64(uint32_t a, uint32_t* w) {
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a));
+}
+__device__ __forceinline__ uint32_t shared32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t shared16(uint32_t a) {
+    unsigned short v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+    return v;
+}
 
 // 8x8 of 16 bits, transposed across the warp
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -118,33 +160,40 @@ struct PagedAt {
 template <int TYPE, int D, int NT>
 __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_kernel(PagedArgs a) {
     using C = PagedCfg<TYPE, D, NT>;
-    constexpr int NW = C::NW, KS = C::KS, SUB = C::SUB, NB = C::NB;
-    extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ int64_t sm_part[NW];
-    __shared__ int4 sm_piece[NW][2];  // row, gi, used, ends
-    uint32_t* const sq = reinterpret_cast<uint32_t*>(smem);
-    float* const sjoin = reinterpret_cast<float*>(smem + C::QBYTES);
-    int64_t* const first = reinterpret_cast<int64_t*>(smem + C::QBYTES + C::JOIN);  // [n + 1] stages of the rows before
-    int2* const rows = reinterpret_cast<int2*>(first + a.n + 1);                     // [n] request, position
+    constexpr int NW = C::NW, KS = C::KS, SUB = C::SUB, NB = C::NB, NST = C::NST;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int64_t sm_part[NW], sm_base;
+    __shared__ int4 sm_piece[NW][2];   // row, gi, used (1: in the ring, 2: in the workspace), ends
+    __shared__ uint4 sm_head[NW][NST];  // of a stage in flight: the slots that are seen, and two bits of where their scales lie
+    unsigned* const first = reinterpret_cast<unsigned*>(smem + NW * NST * C::STAGE);  // [n + 1] stages before each row
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = lane & 3, j = lane >> 2;
     const int KVH = a.c.KVH, G = a.H / KVH, HT = (G + C::HEADS - 1) / C::HEADS, GI = KVH * HT;
+    const uint32_t ring = smem_u32(smem) + warp * NST * C::STAGE;
+    float* const my_piece = reinterpret_cast<float*>(smem + warp * NST * C::STAGE);
+    float* const far = a.ws + paged_far(gridDim.x, D);  // pieces of warps whose ring goes on
 
     pdl_wait();  // positions, tables, q and the cache are written by earlier kernels
     pdl_launch_dependents();  // (after the wait: the join may then read what they have written)
-    // ---- stages of the rows and their prefix sums
+    // request and last position of a row; -1: it sees nothing
+    auto row_of = [&](int r) {
+        const int who = a.seq ? __ldcg(a.seq + r) : r;
+        int pos = __ldcg(a.pos + r);
+        if (who < 0 || who >= a.n_seqs || pos < 0) pos = -1;
+        return make_int2(who, min(pos, a.width * a.page - 1));
+    };
+    // ---- stages of the rows and their prefix sums, from the row on with which this CTA begins
+    int64_t u, u1;
     {
+        for (int r = tid; r < a.n; r += NW * 32) first[r] = (unsigned)((row_of(r).y + KS) / KS);
+        if (lane < 2) sm_piece[warp][lane] = make_int4(0, 0, 0, 0);
+        __syncthreads();
+        for (int r = blockIdx.x; r < a.n; r += gridDim.x)  // rows that see nothing
+            if (first[r] == 0)
+                for (int d = tid; d < a.H * D / 4; d += NW * 32)
+                    *reinterpret_cast<float4*>(a.out + (int64_t)r * a.ldo + 4 * d) = make_float4(0.f, 0.f, 0.f, 0.f);
         const int per = (a.n + NW * 32 - 1) / (NW * 32), r0 = min(a.n, tid * per), r1 = min(a.n, r0 + per);
-        const int64_t most = (int64_t)a.width * a.page;
         int64_t sum = 0;
-        for (int r = r0; r < r1; r++) {
-            const int who = a.seq ? __ldcg(a.seq + r) : r;
-            int pos = __ldcg(a.pos + r);
-            if (who < 0 || who >= a.n_seqs || pos < 0) pos = -1;
-            if (pos >= most) pos = (int)(most - 1);
-            rows[r] = make_int2(who, pos);
-            first[r] = sum;
-            sum += (pos + KS) / KS;
-        }
+        for (int r = r0; r < r1; r++) sum += first[r];
         int64_t x = sum;
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
@@ -152,7 +201,6 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
             if (lane >= o) x += y;
         }
         if (lane == 31) sm_part[warp] = x;
-        if (lane < 2) sm_piece[warp][lane] = make_int4(0, 0, 0, 0);
         __syncthreads();
         int64_t before = x - sum, total = 0;
 #pragma unroll
@@ -160,27 +208,34 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
             if (w < warp) before += sm_part[w];
             total += sm_part[w];
         }
-        for (int r = r0; r < r1; r++) first[r] += before;
-        if (tid == 0) first[a.n] = total;
+        const int64_t units = total * GI, warps = (int64_t)gridDim.x * NW, me = (int64_t)blockIdx.x * NW;
+        auto cut = [&](int64_t w) { return units / warps * w + units % warps * w / warps; };
+        u = cut(me + warp);
+        u1 = cut(me + warp + 1);
+        const int64_t begin = cut(me) / GI;  // a stage of the row with which the CTA begins
+        int64_t at = before;
+        for (int r = r0; r < r1; r++) {
+            const int64_t next = at + first[r];
+            if (at <= begin && begin < next) sm_base = at;
+            at = next;
+        }
+        __syncthreads();
+        const int64_t base = sm_base;  // (unset where there is no stage at all: nothing is read then)
+        at = before;
+        for (int r = r0; r < r1; r++) {
+            const unsigned mine = first[r];
+            first[r] = (unsigned)min(max(at - base, (int64_t)0), (int64_t)UINT32_MAX);
+            at += mine;
+        }
+        if (tid == 0) first[a.n] = (unsigned)min(max(total - base, (int64_t)0), (int64_t)UINT32_MAX);
+        u -= base * GI, u1 -= base * GI;
         __syncthreads();
     }
-    const int64_t units = first[a.n] * GI, warps = (int64_t)gridDim.x * NW, me = (int64_t)blockIdx.x * NW + warp;
-    // (units < 2^12 rows * 2^27 stages * 2^16 heads, so the product with the warps' number stays below 2^63 for units
-    // below 2^51: above, the quotient comes first)
-    auto cut = [&](int64_t w) { return units / warps * w + units % warps * w / warps; };
-    int64_t u = cut(me);
-    const int64_t u1 = cut(me + 1);
-
-    // ---- rows that see nothing
-    for (int r = blockIdx.x; r < a.n; r += gridDim.x)
-        if (rows[r].y < 0)
-            for (int d = tid; d < a.H * D / 4; d += NW * 32)
-                *reinterpret_cast<float4*>(a.out + (int64_t)r * a.ldo + 4 * d) = make_float4(0.f, 0.f, 0.f, 0.f);
 
     if (u < u1) {
         PagedAt at;  // of the current stage
         {
-            const int64_t x = u / GI;
+            const unsigned x = (unsigned)(u / GI);
             int lo = 0, hi = a.n;  // first[lo] <= x < first[hi]
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
@@ -191,125 +246,131 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
             }
             at.row = lo;
             at.nst = (int)(first[lo + 1] - first[lo]);
-            const int64_t y = u - first[lo] * GI;
+            const int64_t y = u - (int64_t)first[lo] * GI;
             at.gi = (int)(y / at.nst);
             at.st = (int)(y - (int64_t)at.gi * at.nst);
         }
-        auto advance = [&](PagedAt& p) {  // (behind the last stage: stays there)
-            if (++p.st < p.nst) return;
-            if (p.gi + 1 < GI) {
-                p.st = 0;
-                p.gi++;
-                return;
+        auto next_row = [&](int r) {
+            for (r++; r < a.n && first[r + 1] == first[r]; r++) {
             }
-            int r = p.row + 1;
-            while (r < a.n && first[r + 1] == first[r]) r++;
-            if (r >= a.n) {
-                p.st--;
-                return;
-            }
-            p.row = r, p.gi = 0, p.st = 0, p.nst = (int)(first[r + 1] - first[r]);
+            return r;
         };
-        // The table's entry for this lane's slot of a stage; -1 where it sees none
-        auto look = [&](const PagedAt& p) -> int {
-            const int2 w = rows[p.row];
-            const int slot = p.st * KS + (KS == 32 ? lane : lane & 15);
-            if (slot > w.y) return -1;
-            const int pg = a.page_mul ? (int)(__umulhi((unsigned)slot, a.page_mul) >> a.page_shift) : slot;
-            return __ldcg(a.table + (int64_t)w.x * a.width + pg);
+        int left = (int)min(u1 - u, (int64_t)INT32_MAX);  // stages of this warp to compute, and to fetch (more are as good)
+        int fetch = left;
+        // ---- the stage that is fetched next: its place, its row and the row after it, and the table's entries for its slots
+        PagedAt ahead = at;
+        int2 who = row_of(at.row), who1 = make_int2(0, -1);
+        int row1 = next_row(at.row);
+        if (row1 < a.n) who1 = row_of(row1);
+        auto split = [&](int st, int& pg, int& off) {
+            const int slot = st * KS + (KS == 32 ? lane : lane & 15);
+            pg = a.page_mul ? (int)(__umulhi((unsigned)slot, a.page_mul) >> a.page_shift) : slot;
+            off = slot - pg * a.page;
+            return slot <= who.y;
         };
-        // That entry as this lane's slot of the cache; -1 where it is hidden
-        auto place = [&](const PagedAt& p, int pg) -> int {
-            const int slot = p.st * KS + (KS == 32 ? lane : lane & 15);
-            const int off = a.page_mul ? slot - (int)(__umulhi((unsigned)slot, a.page_mul) >> a.page_shift) * a.page : 0;
-            return pg >= 0 && pg < a.n_pages ? pg * a.page + off : -1;
+        int entry = -1;
+        auto look = [&]() {  // -1 where the lane's slot is not seen
+            int pg, off;
+            entry = split(ahead.st, pg, off) ? __ldcg(a.table + (int64_t)who.x * a.width + pg) : -1;
         };
-        uint32_t kw[SUB][2][C::KW], vw[SUB][4][C::VW];
-        uint2 ks[SUB][2], vs[SUB][2];
-        // K of a stage: rows j and j + 8 of each 16, this lane's quarter of them.  Hidden slots read slot 0 of the pool.
-        auto load_k = [&](int g, int phys) {
-            const int64_t row0 = (int64_t)g * a.c.ctx;
-#pragma unroll
-            for (int s = 0; s < SUB; s++)
-#pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    const int64_t row = row0 + max(__shfl_sync(0xffffffffu, phys, 16 * s + 8 * h + j), 0);
-                    const uint8_t* p = (const uint8_t*)a.c.k + row * C::RB;
-                    if constexpr (TYPE == AF_F32 || TYPE == AF_F16) {
-#pragma unroll
-                        for (int i = 0; i < C::KW / 4; i++) ldg16(p + (4 * i + c) * 16, &kw[s][h][4 * i]);
-                    } else if constexpr (TYPE == AF_KV_Q8_0) {
-#pragma unroll
-                        for (int i = 0; i < NB; i++) ldg8(p + 32 * i + 8 * c, &kw[s][h][2 * i]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < NB / 2; i++) ldg8(p + 32 * i + 8 * c, &kw[s][h][2 * i]);
-                    }
-                    if constexpr (C::QUANT) {
-                        const uint8_t* q = (const uint8_t*)a.c.ks + row * C::SB;
-                        if (NB == 4)
-                            ks[s][h] = __ldcg(reinterpret_cast<const uint2*>(q));
-                        else
-                            ks[s][h].x = ldg4(q);
-                    }
-                }
-        };
-        // V: the four slots of each 16 that this lane has as an operand, its eighth of their rows
-        auto load_v = [&](int g, int phys) {
-            const int64_t row0 = (int64_t)g * a.c.ctx;
-#pragma unroll
-            for (int s = 0; s < SUB; s++) {
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const int k = TYPE == AF_F32 ? c + 4 * i : 2 * c + (i & 1) + 8 * (i >> 1);
-                    const int64_t row = row0 + max(__shfl_sync(0xffffffffu, phys, 16 * s + k), 0);
-                    const uint8_t* p = (const uint8_t*)a.c.v + row * C::RB;
-                    if constexpr (TYPE == AF_F32 || TYPE == AF_F16) {
-#pragma unroll
-                        for (int x = 0; x < C::VW / 4; x++) ldg16(p + (8 * x + j) * 16, &vw[s][i][4 * x]);
-                    } else {
-#pragma unroll
-                        for (int x = 0; x < C::VW; x++) vw[s][i][x] = ldg4(p + 32 * x + 4 * j);
-                    }
-                }
-                if constexpr (C::QUANT) {
-#pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        const int64_t row = row0 + max(__shfl_sync(0xffffffffu, phys, 16 * s + 8 * h + j), 0);
-                        const uint8_t* q = (const uint8_t*)a.c.vs + row * C::SB;
-                        if (NB == 4)
-                            vs[s][h] = __ldcg(reinterpret_cast<const uint2*>(q));
-                        else
-                            vs[s][h].x = ldg4(q);
+        look();
+        // the lane's slot of the cache in the stage `ahead` (-1: hidden) and its kv head; then on to the next stage
+        int g_ahead = 0;
+        auto place = [&]() {
+            int pg, off;
+            split(ahead.st, pg, off);
+            const int phys = entry >= 0 && entry < a.n_pages ? entry * a.page + off : -1;
+            g_ahead = ahead.gi / HT;
+            if (++ahead.st == ahead.nst) {
+                ahead.st = 0;
+                if (++ahead.gi == GI) {
+                    ahead.gi = 0;
+                    if (row1 < a.n) {
+                        ahead.row = row1;
+                        ahead.nst = (int)(first[row1 + 1] - first[row1]);
+                        who = who1;
+                        row1 = next_row(row1);
+                        if (row1 < a.n) who1 = row_of(row1);
                     }
                 }
             }
+            return phys;
         };
+        auto rows_in = [&](const void* base, int phys, uint32_t dst, bool isv) {
+            constexpr int CPR = C::RB / 16;
+            const uint8_t* src = (const uint8_t*)base + (int64_t)g_ahead * a.c.ctx * C::RB;
+#pragma unroll
+            for (int i = 0; i < KS * CPR / 32; i++) {
+                const int idx = i * 32 + lane, r = idx / CPR, at16 = idx % CPR * 16;
+                const int p = __shfl_sync(0xffffffffu, phys, r);
+                copy16(dst + (isv ? C::vbyte(r, at16) : C::kbyte(r, at16)), src + (int64_t)max(p, 0) * C::RB + at16, p >= 0 ? 16 : 0);
+            }
+        };
+        // the 16 bytes around the scales of the lane's slot (up to the last scale of the cache)
+        auto scales_in = [&](const __half* base, int phys, uint32_t dst) {
+            if constexpr (C::QUANT) {
+                const int64_t row = (int64_t)g_ahead * a.c.ctx + max(phys, 0), end = (int64_t)KVH * a.c.ctx * C::SB;
+                const int64_t from = row * C::SB & ~(int64_t)15;
+                copy16(dst + 16 * lane, (const uint8_t*)base + from, phys < 0 ? 0 : (int)min(end - from, (int64_t)16));
+            }
+        };
+        auto fetch_k = [&](int phys, int slot) {
+            const uint32_t dst = ring + slot * C::STAGE;
+            rows_in(a.c.k, phys, dst, false);
+            scales_in(a.c.ks, phys, dst + C::OKS);
+            const unsigned see = __ballot_sync(0xffffffffu, phys >= 0);
+            unsigned b0 = 0, b1 = 0;
+            if constexpr (C::QUANT) {
+                const unsigned row = (unsigned)g_ahead * (unsigned)a.c.ctx + (unsigned)phys;
+                b0 = __ballot_sync(0xffffffffu, row & 1);
+                if (NB == 2) b1 = __ballot_sync(0xffffffffu, row & 2);
+            }
+            if (lane == 0) sm_head[warp][slot] = make_uint4(see, b0, b1, 0u);
+        };
+        auto fetch_v = [&](int phys, int slot) {
+            const uint32_t dst = ring + slot * C::STAGE;
+            rows_in(a.c.v, phys, dst, true);
+            scales_in(a.c.vs, phys, dst + C::OVS);
+        };
+#pragma unroll
+        for (int i = 0; i < NST; i++) {
+            if (fetch > 0) {
+                fetch--;
+                const int phys = place();
+                look();
+                fetch_k(phys, i);
+                copy_commit();
+                fetch_v(phys, i);
+                copy_commit();
+            } else {
+                copy_commit();
+                copy_commit();
+            }
+        }
 
-        // ---- the first stage is on its way, and the table's entries of the second
-        PagedAt next = at;
-        int phys = place(at, look(at));
-        unsigned see = __ballot_sync(0xffffffffu, phys >= 0);
-        load_k(at.gi / HT, phys);
-        load_v(at.gi / HT, phys);
-        advance(next);
-        int entry = look(next);
-        PagedAt after = next;
-
-        uint32_t qf[C::QSMEM ? 1 : NT][C::QSMEM ? 1 : C::STEPS][2];  // q's operands
+        uint32_t qf[NT][C::STEPS][2];  // q's operands
         float rowf[NT];
         float o[NT][C::MT][4], m_ref[NT], l[NT];
         bool seen = false, begun = true;  // begun: the piece begins with its item
         bool fresh = true;
-
-        for (; u < u1; u++) {
+        int slot = 0;
+        for (; left > 0; left--) {
             const int g = at.gi / HT, ht = at.gi - g * HT;
-            // ---- where the next stage lies
-            const int phys1 = place(next, entry);
-            const unsigned see1 = __ballot_sync(0xffffffffu, phys1 >= 0);
-            after = next;
-            advance(after);
-            entry = look(after);
+            const uint32_t st = ring + slot * C::STAGE;
+            copy_wait<2 * NST - 1>();
+            __syncwarp();  // every lane's copies of this stage's K have landed
+            asm volatile("" ::: "memory");
+            const uint4 hd = sm_head[warp][slot];
+            const unsigned see = hd.x;
+            // scales of this lane's slot s (of 32): the words of blocks 0, 1 and 2, 3
+            auto scale = [&](uint32_t base, int s, uint32_t (&w)[2]) {
+                if (NB == 4) {
+                    shared64(base + 16 * s + (hd.y >> s & 1) * 8, w);
+                } else {
+                    w[0] = shared32(base + 16 * s + (hd.y >> s & 1) * 4 + (hd.z >> s & 1) * 8);
+                    w[1] = 0;
+                }
+            };
             // ---- a new item: q's operands
             if (fresh) {
                 fresh = false;
@@ -326,7 +387,7 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
                     const float* q = a.q + (int64_t)at.row * a.ldq + (int64_t)(g * G + head) * D;
 #pragma unroll
                     for (int i = 0; i < D / 16; i++) {
-                        const int d = TYPE == AF_F32 ? 16 * i + 4 * c : C::kdim(i >> 1, c) + 4 * (i & 1);
+                        const int d = TYPE == AF_F32 ? 16 * i + 4 * c : 32 * (i >> 1) + 8 * c + 4 * (i & 1);
                         const float4 v = head < G ? __ldcg(reinterpret_cast<const float4*>(q + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
                         x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
                     }
@@ -338,7 +399,7 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
                             for (int e = 0; e < 4; e++) {  // dims 4c .. + 3 of 16: the two values of steps 2i and 2i + 1
                                 uint32_t hi, lo;
                                 split_tf32(x[4 * i + e] * sc, hi, lo);
-                                sq[((warp * NT + t) * C::STEPS + 2 * i + (e >> 1)) * 64 + lane * 2 + (e & 1)] = part ? lo : hi;
+                                qf[t][2 * i + (e >> 1)][e & 1] = part ? lo : hi;
                             }
                         rowf[t] = 1.f;
                     } else {
@@ -369,7 +430,6 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
                         }
                     }
                 }
-                if (C::QSMEM) __syncwarp();
             }
             // ---- scores: s[t][16 s + ..]: this lane's slots j and j + 8 of each 16, head c of tile t
             float s[NT][SUB][2];
@@ -379,77 +439,63 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
                 for (int x = 0; x < SUB; x++) s[t][x][0] = s[t][x][1] = 0.f;
 #pragma unroll
             for (int x = 0; x < SUB; x++) {
-                if constexpr (TYPE == AF_F32) {
+                uint32_t dk[2][2];
+                if constexpr (C::QUANT) {
+                    scale(st + C::OKS, 16 * x + j, dk[0]);
+                    scale(st + C::OKS, 16 * x + 8 + j, dk[1]);
+                }
 #pragma unroll
-                    for (int b = 0; b < NB; b++) {
+                for (int b = 0; b < NB; b++) {
+                    if constexpr (TYPE == AF_F32) {
                         float p[NT][4] = {};
-                        uint32_t lo[2][8];
+                        uint32_t hi[2][8], lo[2][8];
 #pragma unroll
-                        for (int i = 0; i < 8; i++)
+                        for (int h = 0; h < 2; h++) {
+                            shared128(st + C::kbyte(8 * h + j, (8 * b + c) * 16), hi[h]);
+                            shared128(st + C::kbyte(8 * h + j, (8 * b + 4 + c) * 16), hi[h] + 4);
 #pragma unroll
-                            for (int h = 0; h < 2; h++) cut_tf32(__uint_as_float(kw[x][h][8 * b + i]), kw[x][h][8 * b + i], lo[h][i]);
+                            for (int i = 0; i < 8; i++) cut_tf32(__uint_as_float(hi[h][i]), hi[h][i], lo[h][i]);
+                        }
 #pragma unroll
                         for (int e = 0; e < 8; e++) {  // the small lo products first
                             const int i = 2 * (e & 3), step = 4 * b + (e & 3);
-                            const uint32_t *k0 = e < 4 ? lo[0] : &kw[x][0][8 * b], *k1 = e < 4 ? lo[1] : &kw[x][1][8 * b];
+                            const uint32_t *k0 = e < 4 ? lo[0] : hi[0], *k1 = e < 4 ? lo[1] : hi[1];
 #pragma unroll
-                            for (int t = 0; t < NT; t++) {
-                                const uint2 q = *reinterpret_cast<const uint2*>(sq + ((warp * NT + t) * C::STEPS + step) * 64 + lane * 2);
-                                mma8(p[t], make_uint4(k0[i], k1[i], k0[i + 1], k1[i + 1]), q.x, q.y);
-                            }
+                            for (int t = 0; t < NT; t++)
+                                mma8(p[t], make_uint4(k0[i], k1[i], k0[i + 1], k1[i + 1]), qf[t][step][0], qf[t][step][1]);
                         }
 #pragma unroll
                         for (int t = 0; t < NT; t++) s[t][x][0] += p[t][0] + p[t][1], s[t][x][1] += p[t][2] + p[t][3];
-                    }
-                } else {
-                    uint32_t k4[2][NB];  // Q4_0: a word of each block
-                    if constexpr (TYPE == AF_KV_Q4_0) {
+                    } else {
+                        uint32_t w[2][4];
 #pragma unroll
-                        for (int h = 0; h < 2; h++)
-#pragma unroll
-                            for (int i = 0; i < NB / 2; i++) {
-                                // lanes c < 2 have 8 bytes of block 2i, the others of 2i + 1: one word of each is exchanged
-                                const uint32_t w0 = kw[x][h][2 * i], w1 = kw[x][h][2 * i + 1];
-                                const uint32_t got = __shfl_xor_sync(0xffffffffu, c < 2 ? w1 : w0, 2);
-                                k4[h][2 * i] = c < 2 ? w0 : got;
-                                k4[h][2 * i + 1] = c < 2 ? got : w1;
-                            }
-                    }
-#pragma unroll
-                    for (int b = 0; b < NB; b++) {
-                        uint4 k[2];
-                        if constexpr (TYPE == AF_F16) {
-                            k[0] = make_uint4(kw[x][0][4 * b], kw[x][1][4 * b], kw[x][0][4 * b + 1], kw[x][1][4 * b + 1]);
-                            k[1] = make_uint4(kw[x][0][4 * b + 2], kw[x][1][4 * b + 2], kw[x][0][4 * b + 3], kw[x][1][4 * b + 3]);
-                        } else if constexpr (TYPE == AF_KV_Q8_0) {
-                            uint32_t w[2][4];
-#pragma unroll
-                            for (int h = 0; h < 2; h++)
+                        for (int h = 0; h < 2; h++) {
+                            const int r = 16 * x + 8 * h + j;
+                            if constexpr (TYPE == AF_F16) {
+                                shared128(st + C::kbyte(r, (4 * b + c) * 16), w[h]);
+                            } else if constexpr (TYPE == AF_KV_Q8_0) {
+                                uint32_t y[2];
+                                shared64(st + C::kbyte(r, 32 * b + 8 * c), y);
 #pragma unroll
                                 for (int i = 0; i < 2; i++) {
-                                    const uint32_t y = kw[x][h][2 * b + i] ^ 0x80808080u;
-                                    w[h][2 * i] = hsub2u(__byte_perm(y, 0x64646464u, 0x4140), 0x64806480u);
-                                    w[h][2 * i + 1] = hsub2u(__byte_perm(y, 0x64646464u, 0x4342), 0x64806480u);
+                                    y[i] ^= 0x80808080u;
+                                    w[h][2 * i] = hsub2u(__byte_perm(y[i], 0x64646464u, 0x4140), 0x64806480u);
+                                    w[h][2 * i + 1] = hsub2u(__byte_perm(y[i], 0x64646464u, 0x4342), 0x64806480u);
                                 }
-                            k[0] = make_uint4(w[0][0], w[1][0], w[0][1], w[1][1]);
-                            k[1] = make_uint4(w[0][2], w[1][2], w[0][3], w[1][3]);
-                        } else {
-                            uint32_t w[2][4];
-                            codes4(k4[0][b], w[0]);
-                            codes4(k4[1][b], w[1]);
-                            k[0] = make_uint4(w[0][0], w[1][0], w[0][1], w[1][1]);
-                            k[1] = make_uint4(w[0][2], w[1][2], w[0][3], w[1][3]);
+                            } else {
+                                codes4(shared32(st + C::kbyte(r, 16 * b + 4 * c)), w[h]);
+                            }
                         }
 #pragma unroll
                         for (int t = 0; t < NT; t++) {
                             float p[4];
-                            mma16z(p, k[0], qf[t][2 * b][0], qf[t][2 * b][1]);
-                            mma16(p, k[1], qf[t][2 * b + 1][0], qf[t][2 * b + 1][1]);
+                            mma16z(p, make_uint4(w[0][0], w[1][0], w[0][1], w[1][1]), qf[t][2 * b][0], qf[t][2 * b][1]);
+                            mma16(p, make_uint4(w[0][2], w[1][2], w[0][3], w[1][3]), qf[t][2 * b + 1][0], qf[t][2 * b + 1][1]);
                             const float s0 = p[0] + p[1], s1 = p[2] + p[3];
                             if constexpr (C::QUANT) {
-                                const uint32_t d0 = b < 2 ? ks[x][0].x : ks[x][0].y, d1 = b < 2 ? ks[x][1].x : ks[x][1].y;
-                                s[t][x][0] = fmaf(__half2float(b & 1 ? __high2half(u_h2(d0)) : __low2half(u_h2(d0))), s0, s[t][x][0]);
-                                s[t][x][1] = fmaf(__half2float(b & 1 ? __high2half(u_h2(d1)) : __low2half(u_h2(d1))), s1, s[t][x][1]);
+                                const __half2 d0 = u_h2(dk[0][b / 2]), d1 = u_h2(dk[1][b / 2]);
+                                s[t][x][0] = fmaf(__half2float(b & 1 ? __high2half(d0) : __low2half(d0)), s0, s[t][x][0]);
+                                s[t][x][1] = fmaf(__half2float(b & 1 ? __high2half(d1) : __low2half(d1)), s1, s[t][x][1]);
                             } else {
                                 s[t][x][0] += s0;
                                 s[t][x][1] += s1;
@@ -458,29 +504,36 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
                     }
                 }
             }
-            // ---- K's registers take the next stage
-            if (u + 1 < u1) load_k(next.gi / HT, phys1);
-            // ---- softmax
-            seen |= see != 0;
-            if (see != 0xffffffffu) {  // hidden slots: no score, no value
+            // ---- K's place in the ring takes the stage NST ahead
+            int phys = -1;
+            __syncwarp();
+            if (fetch > 0) {
+                phys = place();
+                look();
+                fetch_k(phys, slot);
+            }
+            copy_commit();
+            copy_wait<2 * NST - 1>();
+            __syncwarp();  // V has landed
+            asm volatile("" ::: "memory");
+            uint32_t vs[SUB][2][2];
+            if constexpr (C::QUANT) {
 #pragma unroll
-                for (int x = 0; x < SUB; x++) {
+                for (int x = 0; x < SUB; x++)
+#pragma unroll
+                    for (int h = 0; h < 2; h++) scale(st + C::OVS, 16 * x + 8 * h + j, vs[x][h]);
+            }
+            // ---- softmax; hidden slots have no score (and zeros as values)
+            seen |= see != 0;
+            if (see != 0xffffffffu) {
+#pragma unroll
+                for (int x = 0; x < SUB; x++)
 #pragma unroll
                     for (int h = 0; h < 2; h++)
                         if (!(see >> (16 * x + 8 * h + j) & 1)) {
 #pragma unroll
                             for (int t = 0; t < NT; t++) s[t][x][h] = -CUDART_INF_F;
-                            if (C::QUANT) vs[x][h] = make_uint2(0u, 0u);
                         }
-                    if (!C::QUANT)
-#pragma unroll
-                        for (int i = 0; i < 4; i++) {
-                            const int k = TYPE == AF_F32 ? c + 4 * i : 2 * c + (i & 1) + 8 * (i >> 1);
-                            if (!(see >> (16 * x + k) & 1))
-#pragma unroll
-                                for (int w = 0; w < C::VW; w++) vw[x][i][w] = 0u;
-                        }
-                }
             }
             float big[SUB][2];  // log2 of the slots' largest value scales
             if constexpr (C::QUANT) {
@@ -488,8 +541,8 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
                 for (int x = 0; x < SUB; x++)
 #pragma unroll
                     for (int h = 0; h < 2; h++) {
-                        __half2 m = __habs2(u_h2(vs[x][h].x));
-                        if (NB == 4) m = __hmax2(m, __habs2(u_h2(vs[x][h].y)));
+                        __half2 m = __habs2(u_h2(vs[x][h][0]));
+                        if (NB == 4) m = __hmax2(m, __habs2(u_h2(vs[x][h][1])));
                         big[x][h] = lg2a(fmaxf(fmaxf(__low2float(m), __high2float(m)), 0x1p-24f));
                     }
             }
@@ -551,21 +604,25 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
                             pb[t][v][h] = j & 1 ? lo : hi;
                         }
 #pragma unroll
-                for (int i = 0; i < C::VW; i += 2) {  // the row tile of dims i and i + 1 of this lane's eighth
-                    uint32_t lo[4][2], hi[4][2];
+                for (int y = 0; y < D / 32; y++) {  // dims 32 y + 4 j .. + 3: two row tiles
+                    uint32_t lo[4][4], hi[4][4];
 #pragma unroll
-                    for (int k = 0; k < 4; k++)
+                    for (int k = 0; k < 4; k++) {
+                        shared128(st + C::vbyte(c + 4 * k, (8 * y + j) * 16), hi[k]);
 #pragma unroll
-                        for (int e = 0; e < 2; e++) cut_tf32(__uint_as_float(vw[0][k][i + e]), hi[k][e], lo[k][e]);
-#pragma unroll
-                    for (int t = 0; t < NT; t++) {
-                        float sum[4];
-                        mma8z(sum, make_uint4(lo[0][0], lo[0][1], lo[1][0], lo[1][1]), pb[t][0][0], pb[t][0][1]);
-                        mma8(sum, make_uint4(lo[2][0], lo[2][1], lo[3][0], lo[3][1]), pb[t][1][0], pb[t][1][1]);
-                        mma8(sum, make_uint4(hi[0][0], hi[0][1], hi[1][0], hi[1][1]), pb[t][0][0], pb[t][0][1]);
-                        mma8(sum, make_uint4(hi[2][0], hi[2][1], hi[3][0], hi[3][1]), pb[t][1][0], pb[t][1][1]);
-                        add4(o[t][i / 2], sum);
+                        for (int e = 0; e < 4; e++) cut_tf32(__uint_as_float(hi[k][e]), hi[k][e], lo[k][e]);
                     }
+#pragma unroll
+                    for (int t = 0; t < NT; t++)
+#pragma unroll
+                        for (int e = 0; e < 4; e += 2) {
+                            float sum[4];
+                            mma8z(sum, make_uint4(lo[0][e], lo[0][e + 1], lo[1][e], lo[1][e + 1]), pb[t][0][0], pb[t][0][1]);
+                            mma8(sum, make_uint4(lo[2][e], lo[2][e + 1], lo[3][e], lo[3][e + 1]), pb[t][1][0], pb[t][1][1]);
+                            mma8(sum, make_uint4(hi[0][e], hi[0][e + 1], hi[1][e], hi[1][e + 1]), pb[t][0][0], pb[t][0][1]);
+                            mma8(sum, make_uint4(hi[2][e], hi[2][e + 1], hi[3][e], hi[3][e + 1]), pb[t][1][0], pb[t][1][1]);
+                            add4(o[t][2 * y + e / 2], sum);
+                        }
                 }
             } else if constexpr (TYPE == AF_F16) {
                 uint32_t pb[NT][2];
@@ -574,33 +631,23 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
 #pragma unroll
                     for (int h = 0; h < 2; h++) pb[t][h] = transpose8(hi_lo(s[t][0][h]));
 #pragma unroll
-                for (int i = 0; i < C::VW; i++) {  // a word of the lane's eighth: two dims, one row tile
-                    const uint4 v = make_uint4(__byte_perm(vw[0][0][i], vw[0][1][i], 0x5410), __byte_perm(vw[0][0][i], vw[0][1][i], 0x7632),
-                                               __byte_perm(vw[0][2][i], vw[0][3][i], 0x5410), __byte_perm(vw[0][2][i], vw[0][3][i], 0x7632));
+                for (int y = 0; y < D / 64; y++) {  // dims 64 y + 8 j .. + 7: four row tiles
+                    uint32_t w[4][4];
 #pragma unroll
-                    for (int t = 0; t < NT; t++) {
-                        float sum[4];
-                        mma16z(sum, v, pb[t][0], pb[t][1]);
-                        add4(o[t][i], sum);
+                    for (int k = 0; k < 4; k++) shared128(st + C::vbyte(2 * c + (k & 1) + 8 * (k >> 1), (8 * y + j) * 16), w[k]);
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const uint4 v = make_uint4(__byte_perm(w[0][i], w[1][i], 0x5410), __byte_perm(w[0][i], w[1][i], 0x7632),
+                                                   __byte_perm(w[2][i], w[3][i], 0x5410), __byte_perm(w[2][i], w[3][i], 0x7632));
+#pragma unroll
+                        for (int t = 0; t < NT; t++) {
+                            float sum[4];
+                            mma16z(sum, v, pb[t][0], pb[t][1]);
+                            add4(o[t][4 * y + i], sum);
+                        }
                     }
                 }
             } else {
-                uint32_t v4[SUB][2][NB];  // Q4_0: 16 bits of each of two slots, by pair of slots and block
-                if constexpr (TYPE == AF_KV_Q4_0) {
-#pragma unroll
-                    for (int x = 0; x < SUB; x++)
-#pragma unroll
-                        for (int h = 0; h < 2; h++)
-#pragma unroll
-                            for (int i = 0; i < NB / 2; i++) {
-                                // lanes j < 4 have 4 bytes of block 2i, the others of 2i + 1: half of them is exchanged
-                                const uint32_t lo = __byte_perm(vw[x][2 * h][i], vw[x][2 * h + 1][i], 0x5410);
-                                const uint32_t hi = __byte_perm(vw[x][2 * h][i], vw[x][2 * h + 1][i], 0x7632);
-                                const uint32_t got = __shfl_xor_sync(0xffffffffu, j < 4 ? hi : lo, 16);
-                                v4[x][h][2 * i] = j < 4 ? lo : got;
-                                v4[x][h][2 * i + 1] = j < 4 ? got : hi;
-                            }
-                }
 #pragma unroll
                 for (int b = 0; b < NB; b++) {
                     uint32_t pb[NT][SUB][2];
@@ -608,8 +655,8 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
                     for (int x = 0; x < SUB; x++)
 #pragma unroll
                         for (int h = 0; h < 2; h++) {
-                            const uint32_t w = b < 2 ? vs[x][h].x : vs[x][h].y;
-                            const float d = __half2float(b & 1 ? __high2half(u_h2(w)) : __low2half(u_h2(w)));
+                            const __half2 w = u_h2(vs[x][h][b / 2]);
+                            const float d = __half2float(b & 1 ? __high2half(w) : __low2half(w));
 #pragma unroll
                             for (int t = 0; t < NT; t++) pb[t][x][h] = transpose8(hi_lo(s[t][x][h] * d));
                         }
@@ -618,17 +665,20 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
                     for (int x = 0; x < SUB; x++) {
                         uint32_t v[2][4];  // pair of slots, dim
 #pragma unroll
-                        for (int h = 0; h < 2; h++)
+                        for (int h = 0; h < 2; h++) {
+                            const int r = 16 * x + 2 * c + 8 * h;
                             if constexpr (TYPE == AF_KV_Q8_0) {
-                                const uint32_t w0 = vw[x][2 * h][b] ^ 0x80808080u, w1 = vw[x][2 * h + 1][b] ^ 0x80808080u;
+                                const uint32_t w0 = shared32(st + C::vbyte(r, 32 * b + 4 * j)) ^ 0x80808080u;
+                                const uint32_t w1 = shared32(st + C::vbyte(r + 1, 32 * b + 4 * j)) ^ 0x80808080u;
                                 const uint32_t y = __byte_perm(w0, w1, 0x5140), z = __byte_perm(w0, w1, 0x7362);
                                 v[h][0] = hsub2u(__byte_perm(y, 0x64646464u, 0x4140), 0x64806480u);
                                 v[h][1] = hsub2u(__byte_perm(y, 0x64646464u, 0x4342), 0x64806480u);
                                 v[h][2] = hsub2u(__byte_perm(z, 0x64646464u, 0x4140), 0x64806480u);
                                 v[h][3] = hsub2u(__byte_perm(z, 0x64646464u, 0x4342), 0x64806480u);
                             } else {
-                                codes4(v4[x][h][b], v[h]);
+                                codes4(shared16(st + C::vbyte(r, 16 * b + 2 * j)) | shared16(st + C::vbyte(r + 1, 16 * b + 2 * j)) << 16, v[h]);
                             }
+                        }
 #pragma unroll
                         for (int t = 0; t < NT; t++)
 #pragma unroll
@@ -646,17 +696,23 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
                         for (int i = 0; i < 2; i++) add4(o[t][2 * b + i], sum[t][i]);
                 }
             }
-            // ---- V's registers take the next stage
-            if (u + 1 < u1) load_v(next.gi / HT, phys1);
+            // ---- V's place in the ring takes the stage NST ahead
+            __syncwarp();
+            if (fetch > 0) {
+                fetch--;
+                fetch_v(phys, slot);
+            }
+            copy_commit();
+            slot = slot + 1 == NST ? 0 : slot + 1;
 
             // ---- the end of the item, or of this warp's range
             const bool ends = at.st + 1 == at.nst;
-            if (ends || u + 1 == u1) {
+            if (ends || left == 1) {
                 fresh = true;
                 const bool done = begun && ends;
-                const int slot = begun ? 1 : 0;
-                float* piece = sjoin + (warp * 2 + slot) * C::PIECE;
-                if (!done && lane == 0) sm_piece[warp][slot] = make_int4(at.row, at.gi, 1, ends);
+                const int which = begun ? 1 : 0;
+                float* piece = left == 1 ? my_piece : far + ((size_t)blockIdx.x * NW + warp) * C::PIECE;  // (all copies are done)
+                if (!done && lane == 0) sm_piece[warp][which] = make_int4(at.row, at.gi, left == 1 ? 1 : 2, ends);
 #pragma unroll
                 for (int t = 0; t < NT; t++) {
                     float x = l[t];
@@ -674,9 +730,7 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
                         for (int i = 0; i < C::MT; i += 2) {
                             const int d = TYPE == AF_F16   ? 64 * (i >> 2) + 8 * j + 2 * (i & 3)
                                           : TYPE == AF_F32 ? 32 * (i >> 1) + 4 * j
-                                          : TYPE == AF_KV_Q8_0
-                                              ? 16 * i + 4 * j
-                                              : 16 * i + (j < 4 ? 8 * j : 8 * (j - 4) + 4);
+                                                           : 16 * i + 4 * j;
                             *reinterpret_cast<float4*>(dst + d) =
                                 make_float4((o[t][i][0] + o[t][i][1]) * inv, (o[t][i][2] + o[t][i][3]) * inv,
                                             (o[t][i + 1][0] + o[t][i + 1][1]) * inv, (o[t][i + 1][2] + o[t][i + 1][3]) * inv);
@@ -684,9 +738,18 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
                     }
                 }
             }
-            at = next;
-            next = after;
-            see = see1;
+            if (ends) {
+                at.st = 0;
+                if (++at.gi == GI) {
+                    at.gi = 0;
+                    if (left > 1) {
+                        at.row = next_row(at.row);
+                        at.nst = (int)(first[at.row + 1] - first[at.row]);
+                    }
+                }
+            } else {
+                at.st++;
+            }
         }
     }
 
@@ -714,7 +777,10 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
             const int g = p.y / HT, ht = p.y - g * HT;
             for (int hh = 0; hh < C::HEADS; hh++, job++) {
                 if (job % NW != warp || ht * C::HEADS + hh >= G) continue;
-                auto piece = [&](int x) { return sjoin + (x * 2 + (x == w ? slot : 0)) * C::PIECE; };
+                auto piece = [&](int x) -> const float* {
+                    return sm_piece[x][x == w ? slot : 0].z == 1 ? reinterpret_cast<const float*>(smem + x * NST * C::STAGE)
+                                                                 : far + ((size_t)blockIdx.x * NW + x) * C::PIECE;
+                };
                 auto stat = [&](int x) { return reinterpret_cast<const float2*>(piece(x) + C::HEADS * D)[hh]; };
                 float m = -CUDART_INF_F;
                 for (int x = w; x <= last; x++)
@@ -760,13 +826,14 @@ cudaError_t launch_attn_paged_type(const PagedArgs& a, int ctas, cudaStream_t s)
 template <int TYPE, int D, int NT>
 cudaError_t paged_go(const PagedArgs& a, int ctas, cudaStream_t s) {
     using C = PagedCfg<TYPE, D, NT>;
-    constexpr int fixed = C::QBYTES + C::JOIN;
-    static_assert(fixed + (kPagedMaxRows + 1) * 8 + kPagedMaxRows * 8 <= 220 * 1024, "shared memory");
+    constexpr int ring = C::NW * C::NST * C::STAGE;
+    static_assert(ring + (kPagedMaxRows + 1) * 4 <= 227 * 1024 - 256 - C::NW * (32 + 16 * C::NST + 8), "shared memory");
+    static_assert(C::NW * C::PIECE <= 8 * paged_piece_floats(D), "workspace");
     auto k = attn_paged_kernel<TYPE, D, NT>;
     static SmemOptIn opt;
-    cudaError_t e = opt((const void*)k, fixed + (kPagedMaxRows + 1) * 8 + kPagedMaxRows * 8);
+    cudaError_t e = opt((const void*)k, ring + (kPagedMaxRows + 1) * 4);
     if (e) return e;
-    return launch_chained(k, dim3(ctas), C::NW * 32, fixed + (a.n + 1) * 8 + a.n * 8, s, a);
+    return launch_chained(k, dim3(ctas), C::NW * 32, ring + (a.n + 1) * 4, s, a);
 }
 
 #define AF_PAGED_INSTANTIATE(TYPE)                                                                    \

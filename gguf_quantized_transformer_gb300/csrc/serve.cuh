@@ -22,7 +22,7 @@ struct PagesArgs {
 cudaError_t launch_kv_pages(const PagesArgs& a, cudaStream_t s);
 
 // ---- attention of single tokens over a paged cache (attn_paged.cu)
-constexpr int kPagedMaxRows = 4096;
+constexpr int kPagedMaxRows = 2048;
 struct PagedArgs {
     const float* q = nullptr;
     int64_t ldq = 0;

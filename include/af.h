@@ -528,13 +528,13 @@ int af_kv_pages(const int32_t* len_dev, const int32_t* new_dev, int32_t n_seqs, 
  *   pos_dev   int32 [n].  A row with a negative position or a request outside [0, n_seqs) gives zeros; a position behind
  *             the table's last slot sees the slots that the table has.  Slots of pages outside [0, n_pages) are hidden: they
  *             are not read, and a row that sees no other slot gives zeros
- *   ws_dev    scratch of at least af_attention_paged_workspace bytes, 256-byte aligned, of any contents (1.3 MB with
+ *   ws_dev    scratch of at least af_attention_paged_workspace bytes, 256-byte aligned, of any contents (6.4 MB with
  *             head_dim 128 on 152 SMs, whatever the rows); calls that may overlap in time need scratch of their own
  *   out_dev   fp32 [n] rows, ldo apart
  * The work is split by the slots that the rows see, found on the device: lengths may differ as they like, and a captured
  * call serves any lengths.  Precision, bits from call to call, and rows that see a NaN or an infinity: as
  * af_attention_tree's.  What slots hold that a row does not see reaches nothing.
- * 1 <= n <= 4096; head_dim 64 or 128, any whole group up to 64; n_kv_heads * n_pages * page_size below 2^31, page_size and
+ * 1 <= n <= 2048; head_dim 64 or 128, any whole group up to 64; n_kv_heads * n_pages * page_size below 2^31, page_size and
  * table_width at least 1, table_width * page_size below 2^31 - 64.  Pointers are 16-byte aligned (table_dev, seq_dev,
  * pos_dev: 4), ldq and ldo multiples of 4.  Asynchronous on `stream`, allocates nothing, can be captured (the first call on
  * a device loads the kernels: make it before a capture).  Errors: AF_EINVAL, AF_ERANGE, AF_ENOTIMPL, AF_ECUDA.

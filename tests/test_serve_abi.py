@@ -33,7 +33,7 @@ BAD = {
                            ("h", 8 * 65, N), ("kvh", 0, E), ("d", 96, N), ("d", -64, E), ("page", 0, E), ("page", 2 ** 26, R),
                            ("n_pages", 0, E), ("n_pages", 2 ** 24, N), ("table", None, E), ("table", P + 1, E), ("width", 0, E),
                            ("width", 2 ** 27, R), ("n_seqs", 0, R), ("n_seqs", 3, R), ("n_seqs", 65537, R), ("seq", P + 2, E),
-                           ("pos", None, E), ("pos", P + 3, E), ("n", 0, R), ("n", 5, R), ("n", 4097, R), ("ws", None, E),
+                           ("pos", None, E), ("pos", P + 3, E), ("n", 0, R), ("n", 5, R), ("n", 2049, R), ("ws", None, E),
                            ("ws", P + 16, E), ("out", None, E), ("out", P + 4, E), ("ldo", 4092, E), ("ldo", 4097, E)],
     "af_lora_plan": [("ids", None, E), ("ids", P + 1, E), ("n", 0, R), ("n", 65537, R), ("adapters", 0, R), ("adapters", 4097, R),
                      ("plan", None, E), ("plan", P + 4, E), ("bytes", 15, E)],
