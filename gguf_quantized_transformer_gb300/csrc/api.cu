@@ -1254,6 +1254,15 @@ int check_pages(int32_t n_seqs, int32_t page, int32_t n_pages, int32_t width) {
     return AF_OK;
 }
 
+// x / page = umulhi(x, mul) >> shift, exactly for x below 2^31: mul is 2^(31 + l) / page rounded up, 2^l >= page
+void page_divisor(int32_t page, unsigned& mul, int& shift) {
+    if (page == 1) return;  // (mul stays 0)
+    int l = 1;
+    while ((1LL << l) < page) l++;
+    mul = (unsigned)(((1ULL << (31 + l)) + page - 1) / page);
+    shift = l - 1;
+}
+
 int check_paged_heads(int32_t H, int32_t KVH, int32_t D) {
     if (H <= 0 || KVH <= 0 || D <= 0) return fail(AF_EINVAL, "sizes must be positive");
     if (H % KVH) return fail(AF_EINVAL, "n_heads must be a multiple of n_kv_heads");
@@ -1318,6 +1327,8 @@ int af_kv_pages(const int32_t* len_dev, const int32_t* new_dev, int32_t n_seqs, 
     a.pos = pos_dev;
     a.seq = seq_dev;
     a.ws = (int4*)ws_dev;
+    page_divisor(page_size, a.page_mul, a.page_shift);
+    a.vec = !(((uintptr_t)slots_dev | (uintptr_t)pos_dev | (uintptr_t)seq_dev) & 15);
     CK(launch_kv_pages(a, (cudaStream_t)stream));
     return AF_OK;
 }
@@ -1355,12 +1366,7 @@ int af_attention_paged(const float* q_dev, int64_t ldq, const void* k_cache, con
     a.width = table_width;
     a.n_seqs = n_seqs;
     a.n = n;
-    if (page_size > 1) {  // exact for slots below 2^31: the multiplier is 2^(31 + l) / page_size rounded up, 2^l >= page_size
-        int l = 1;
-        while ((1LL << l) < page_size) l++;
-        a.page_mul = (unsigned)(((1ULL << (31 + l)) + page_size - 1) / page_size);
-        a.page_shift = l - 1;
-    }
+    page_divisor(page_size, a.page_mul, a.page_shift);
     a.table = table_dev;
     a.seq = seq_dev;
     a.pos = pos_dev;

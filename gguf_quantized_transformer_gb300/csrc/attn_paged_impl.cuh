@@ -22,7 +22,8 @@
 //  - Tensor cores cut fp32 sums instead of rounding them: a stage's output and a block's score start from zero and are added
 //    in fp32.
 // Pieces of an item that several warps hold are joined through shared memory at the end of the CTA, those of several CTAs
-// by paged_join_kernel, each in order: the bits do not change from call to call.
+// by the last of them to leave its own (a second kernel took 4 to 5 us more), each in order: the bits do not change from
+// call to call.
 #pragma once
 #include <math_constants.h>
 
@@ -36,18 +37,14 @@ constexpr float kLog2eP = 1.4426950408889634f;
 constexpr float kLazyP = 4.f;   // powers of two by which the reference may be exceeded
 constexpr float kBiasP = 10.f;  // p = 2^(s - m + kBiasP)
 
-// What a CTA leaves for the join: its pieces 0 (an item that begins before it) and 1 (one that ends after it).
-struct PagedPiece {
-    int row, gi;    // gi = kv head * head tiles + head tile
-    int used, ends;  // piece 0: whether the item ends in this CTA
-};
-constexpr int kPagedHeads = 8;  // heads of a piece at most
+constexpr int kPagedKept = 512;  // rows whose request and position a CTA keeps
+constexpr int kPagedHeads = 8;   // heads of a piece at most
+// The workspace: a counter per CTA (of the CTAs that have left their part of the item that begins in it); each CTA's pieces
+// 0 (of an item that begins before it) and 1 (of one that goes on after it), outputs [8][D] and then [8] (m, l); the pieces
+// of warps that go on after them: 16 warps of 4 heads or 8 of 8.
 __host__ __device__ constexpr size_t paged_piece_floats(int D) { return (size_t)kPagedHeads * (D + 2); }
-// ws: [ctas][2] pieces of paged_piece_floats (outputs [8][D], then [8] (m, l)), [ctas][2] PagedPiece, then the pieces of warps
-// that end before the warp does: 16 warps of 4 heads or 8 of 8
-__host__ __device__ constexpr size_t paged_far(int ctas, int D) {
-    return (size_t)ctas * 2 * (paged_piece_floats(D) + sizeof(PagedPiece) / 4);
-}
+__host__ __device__ constexpr size_t paged_pieces(int ctas) { return ((size_t)ctas * 2 + 63) / 64 * 64; }
+__host__ __device__ constexpr size_t paged_far(int ctas, int D) { return paged_pieces(ctas) + (size_t)ctas * 2 * paged_piece_floats(D); }
 __host__ __device__ constexpr size_t paged_ws_floats(int ctas, int D) {
     return paged_far(ctas, D) + (size_t)ctas * 8 * paged_piece_floats(D);
 }
@@ -162,10 +159,11 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
     using C = PagedCfg<TYPE, D, NT>;
     constexpr int NW = C::NW, KS = C::KS, SUB = C::SUB, NB = C::NB, NST = C::NST;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t sm_part[NW], sm_base;
+    __shared__ int64_t sm_part[NW];  // (32 or 64 bits)
     __shared__ int4 sm_piece[NW][2];   // row, gi, used (1: in the ring, 2: in the workspace), ends
     __shared__ uint4 sm_head[NW][NST];  // of a stage in flight: the slots that are seen, and two bits of where their scales lie
-    unsigned* const first = reinterpret_cast<unsigned*>(smem + NW * NST * C::STAGE);  // [n + 1] stages before each row
+    int2* const rows = reinterpret_cast<int2*>(smem + NW * NST * C::STAGE);  // [n] request and position, for up to kPagedKept rows
+    int* const first = reinterpret_cast<int*>(rows + (a.n <= kPagedKept ? a.n : 0));  // [n + 1] stages before each row
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = lane & 3, j = lane >> 2;
     const int KVH = a.c.KVH, G = a.H / KVH, HT = (G + C::HEADS - 1) / C::HEADS, GI = KVH * HT;
     const uint32_t ring = smem_u32(smem) + warp * NST * C::STAGE;
@@ -173,7 +171,7 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
     float* const far = a.ws + paged_far(gridDim.x, D);  // pieces of warps whose ring goes on
 
     pdl_wait();  // positions, tables, q and the cache are written by earlier kernels
-    pdl_launch_dependents();  // (after the wait: the join may then read what they have written)
+    pdl_launch_dependents();
     // request and last position of a row; -1: it sees nothing
     auto row_of = [&](int r) {
         const int who = a.seq ? __ldcg(a.seq + r) : r;
@@ -181,61 +179,79 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
         if (who < 0 || who >= a.n_seqs || pos < 0) pos = -1;
         return make_int2(who, min(pos, a.width * a.page - 1));
     };
-    // ---- stages of the rows and their prefix sums, from the row on with which this CTA begins
-    int64_t u, u1;
-    {
-        for (int r = tid; r < a.n; r += NW * 32) first[r] = (unsigned)((row_of(r).y + KS) / KS);
-        if (lane < 2) sm_piece[warp][lane] = make_int4(0, 0, 0, 0);
-        __syncthreads();
-        for (int r = blockIdx.x; r < a.n; r += gridDim.x)  // rows that see nothing
-            if (first[r] == 0)
-                for (int d = tid; d < a.H * D / 4; d += NW * 32)
-                    *reinterpret_cast<float4*>(a.out + (int64_t)r * a.ldo + 4 * d) = make_float4(0.f, 0.f, 0.f, 0.f);
-        const int per = (a.n + NW * 32 - 1) / (NW * 32), r0 = min(a.n, tid * per), r1 = min(a.n, r0 + per);
-        int64_t sum = 0;
-        for (int r = r0; r < r1; r++) sum += first[r];
-        int64_t x = sum;
+    const bool kept = a.n <= kPagedKept;
+    auto row_at = [&](int r) { return kept ? rows[r] : row_of(r); };
+    // ---- stages of the rows and their prefix sums, counted from the stage with which this CTA begins; each warp's range.
+    // (I: 32 bits where they hold all stages of all items)
+    const int per = (a.n + NW * 32 - 1) / (NW * 32), r0 = min(a.n, tid * per), r1 = min(a.n, r0 + per);
+    int64_t u, u1, begin_unit, units_each, units_rest;
+    auto plan = [&](auto zero, int64_t* parts) {
+        using I = decltype(zero);
+        I* const part = reinterpret_cast<I*>(parts);
+        I sum = 0;
+#pragma unroll 1
+        for (int r = r0; r < r1; r++) {
+            const int2 w = row_of(r);
+            if (kept) rows[r] = w;
+            first[r] = (w.y + KS) / KS;
+            sum += first[r];
+        }
+        I x = sum;
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+            const I y = __shfl_up_sync(0xffffffffu, x, o);
             if (lane >= o) x += y;
         }
-        if (lane == 31) sm_part[warp] = x;
+        if (lane == 31) part[warp] = x;
+        if (lane < 2) sm_piece[warp][lane] = make_int4(0, 0, 0, 0);
         __syncthreads();
-        int64_t before = x - sum, total = 0;
+        x -= sum;
+        I total = 0;
 #pragma unroll
         for (int w = 0; w < NW; w++) {
-            if (w < warp) before += sm_part[w];
-            total += sm_part[w];
+            const I y = part[w];
+            if (w < warp) x += y;
+            total += y;
         }
-        const int64_t units = total * GI, warps = (int64_t)gridDim.x * NW, me = (int64_t)blockIdx.x * NW;
-        auto cut = [&](int64_t w) { return units / warps * w + units % warps * w / warps; };
-        u = cut(me + warp);
-        u1 = cut(me + warp + 1);
-        const int64_t begin = cut(me) / GI;  // a stage of the row with which the CTA begins
-        int64_t at = before;
+        // the first `rest` warps have a stage more than the others
+        const I units = total * GI, warps = gridDim.x * NW, each = units / warps, rest = units - each * warps;
+        auto cut = [&](I w) { return each * w + min(w, rest); };
+        const I me = blockIdx.x * NW, begin = cut(me) / GI;
+        begin_unit = (int64_t)begin * GI, units_each = each, units_rest = rest;
+        u = cut(me + warp) - begin * GI;
+        u1 = cut(me + warp + 1) - begin * GI;
+        // (2048 rows of at most 2^27 stages over 152 CTAs: a CTA's own fit 31 bits)
+        auto from_here = [&](I at) { return (int)max(min((int64_t)at - begin, (int64_t)INT32_MAX), (int64_t)INT32_MIN); };
+#pragma unroll 1
         for (int r = r0; r < r1; r++) {
-            const int64_t next = at + first[r];
-            if (at <= begin && begin < next) sm_base = at;
-            at = next;
+            const int stages = first[r];
+            first[r] = from_here(x);
+            x += stages;
         }
+        if (tid == 0) first[a.n] = from_here(total);
         __syncthreads();
-        const int64_t base = sm_base;  // (unset where there is no stage at all: nothing is read then)
-        at = before;
-        for (int r = r0; r < r1; r++) {
-            const unsigned mine = first[r];
-            first[r] = (unsigned)min(max(at - base, (int64_t)0), (int64_t)UINT32_MAX);
-            at += mine;
-        }
-        if (tid == 0) first[a.n] = (unsigned)min(max(total - base, (int64_t)0), (int64_t)UINT32_MAX);
-        u -= base * GI, u1 -= base * GI;
-        __syncthreads();
-    }
-
-    if (u < u1) {
-        PagedAt at;  // of the current stage
+    };
+    if (a.wide)
+        plan((int64_t)0, sm_part);
+    else
+        plan((int)0, sm_part);
+    for (int r = blockIdx.x; r < a.n; r += gridDim.x)  // rows that see nothing
+        if (row_at(r).y < 0)
+            for (int d = tid; d < a.H * D / 4; d += NW * 32)
+                *reinterpret_cast<float4*>(a.out + (int64_t)r * a.ldo + 4 * d) = make_float4(0.f, 0.f, 0.f, 0.f);
+    unsigned long long* const counters = reinterpret_cast<unsigned long long*>(a.ws);
+    auto cta_of = [&](int64_t unit) {
+        const int64_t more = units_rest * (units_each + 1);
+        if (!a.wide)
+            return (int)((unit < more ? (unsigned)unit / (unsigned)(units_each + 1)
+                                      : (unsigned)units_rest + (unsigned)(unit - more) / max((unsigned)units_each, 1u)) / NW);
+        return (int)((unit < more ? unit / (units_each + 1) : units_rest + (unit - more) / max(units_each, (int64_t)1)) / NW);
+    };
+    const bool any = u < u1;
+    if (any) {
+        PagedAt at;  // the stage that is computed
         {
-            const unsigned x = (unsigned)(u / GI);
+            const int x = u <= INT32_MAX ? (int)u / GI : (int)(u / GI);
             int lo = 0, hi = a.n;  // first[lo] <= x < first[hi]
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
@@ -245,9 +261,9 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
                     hi = mid;
             }
             at.row = lo;
-            at.nst = (int)(first[lo + 1] - first[lo]);
+            at.nst = first[lo + 1] - first[lo];
             const int64_t y = u - (int64_t)first[lo] * GI;
-            at.gi = (int)(y / at.nst);
+            at.gi = y <= INT32_MAX ? (int)y / at.nst : (int)(y / at.nst);
             at.st = (int)(y - (int64_t)at.gi * at.nst);
         }
         auto next_row = [&](int r) {
@@ -255,42 +271,51 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
             }
             return r;
         };
+        auto page_of = [&](int slot) { return a.page_mul ? (int)(__umulhi((unsigned)slot, a.page_mul) >> a.page_shift) : slot; };
         int left = (int)min(u1 - u, (int64_t)INT32_MAX);  // stages of this warp to compute, and to fetch (more are as good)
         int fetch = left;
-        // ---- the stage that is fetched next: its place, its row and the row after it, and the table's entries for its slots
+        // ---- the stage that is fetched next and its row; 64 entries of the row's table, two to a lane, from entry 32 `win`
         PagedAt ahead = at;
-        int2 who = row_of(at.row), who1 = make_int2(0, -1);
-        int row1 = next_row(at.row);
-        if (row1 < a.n) who1 = row_of(row1);
-        auto split = [&](int st, int& pg, int& off) {
-            const int slot = st * KS + (KS == 32 ? lane : lane & 15);
-            pg = a.page_mul ? (int)(__umulhi((unsigned)slot, a.page_mul) >> a.page_shift) : slot;
-            off = slot - pg * a.page;
-            return slot <= who.y;
+        int2 who = row_at(at.row);
+        int win, ent0, ent1;
+        auto entries = [&](int w) {
+            const int e = 32 * w + lane;
+            return e < a.width ? __ldcg(a.table + (int64_t)who.x * a.width + e) : -1;
         };
-        int entry = -1;
-        auto look = [&]() {  // -1 where the lane's slot is not seen
-            int pg, off;
-            entry = split(ahead.st, pg, off) ? __ldcg(a.table + (int64_t)who.x * a.width + pg) : -1;
+        auto open = [&](int w) {
+            win = w;
+            ent0 = entries(w);
+            ent1 = entries(w + 1);
         };
-        look();
+        open(page_of(at.st * KS) >> 5);
         // the lane's slot of the cache in the stage `ahead` (-1: hidden) and its kv head; then on to the next stage
         int g_ahead = 0;
         auto place = [&]() {
-            int pg, off;
-            split(ahead.st, pg, off);
-            const int phys = entry >= 0 && entry < a.n_pages ? entry * a.page + off : -1;
+            const int slot = ahead.st * KS + (KS == 32 ? lane : lane & 15), pg = page_of(slot), off = slot - pg * a.page;
+            const int w = __shfl_sync(0xffffffffu, pg, 0) >> 5;
+            if (w != win) {  // (a stage has at most 32 pages)
+                if (w == win + 1) {
+                    win = w;
+                    ent0 = ent1;
+                    ent1 = entries(w + 1);
+                } else {
+                    open(w);
+                }
+            }
+            const int e0 = __shfl_sync(0xffffffffu, ent0, pg & 31), e1 = __shfl_sync(0xffffffffu, ent1, pg & 31);
+            const int entry = (pg >> 5) == win ? e0 : e1;
+            const int phys = slot <= who.y && entry >= 0 && entry < a.n_pages ? entry * a.page + off : -1;
             g_ahead = ahead.gi / HT;
             if (++ahead.st == ahead.nst) {
                 ahead.st = 0;
                 if (++ahead.gi == GI) {
                     ahead.gi = 0;
-                    if (row1 < a.n) {
-                        ahead.row = row1;
-                        ahead.nst = (int)(first[row1 + 1] - first[row1]);
-                        who = who1;
-                        row1 = next_row(row1);
-                        if (row1 < a.n) who1 = row_of(row1);
+                    const int r = next_row(ahead.row);
+                    if (r < a.n && fetch > 1) {
+                        ahead.row = r;
+                        ahead.nst = first[r + 1] - first[r];
+                        who = row_at(r);
+                        open(0);
                     }
                 }
             }
@@ -332,21 +357,11 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
             rows_in(a.c.v, phys, dst, true);
             scales_in(a.c.vs, phys, dst + C::OVS);
         };
-#pragma unroll
-        for (int i = 0; i < NST; i++) {
-            if (fetch > 0) {
-                fetch--;
-                const int phys = place();
-                look();
-                fetch_k(phys, i);
-                copy_commit();
-                fetch_v(phys, i);
-                copy_commit();
-            } else {
-                copy_commit();
-                copy_commit();
-            }
-        }
+        // The counters of the items that this CTA may hold a part of: that of its first stage and the one that begins in it.
+        // A counter holds the call's mark and the number of pieces left; what has another mark is nothing (below).
+        unsigned long long* const mine = counters + (lane ? (int)blockIdx.x : cta_of(begin_unit + u - at.st));
+        unsigned long long found = 0;
+        if (warp == 0 && lane < 2) found = __ldcg(mine);
 
         uint32_t qf[NT][C::STEPS][2];  // q's operands
         float rowf[NT];
@@ -354,23 +369,23 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
         bool seen = false, begun = true;  // begun: the piece begins with its item
         bool fresh = true;
         int slot = 0;
-        for (; left > 0; left--) {
+        // The first NST rounds only fetch; after them a stage is computed before its place takes the stage NST ahead.
+        for (int round = -NST;; round++) {
+            const bool work = round >= 0;
             const int g = at.gi / HT, ht = at.gi - g * HT;
             const uint32_t st = ring + slot * C::STAGE;
-            copy_wait<2 * NST - 1>();
-            __syncwarp();  // every lane's copies of this stage's K have landed
-            asm volatile("" ::: "memory");
-            const uint4 hd = sm_head[warp][slot];
-            const unsigned see = hd.x;
-            // scales of this lane's slot s (of 32): the words of blocks 0, 1 and 2, 3
-            auto scale = [&](uint32_t base, int s, uint32_t (&w)[2]) {
+            unsigned see = 0, b0 = 0, b1 = 0;  // the stage's slots that are seen, and where their scales lie
+            float s[NT][SUB][2];  // scores: this lane's slots j and j + 8 of each 16, head c of tile t
+            // scales of this lane's slot i (of 32): the words of blocks 0, 1 and 2, 3
+            auto scale = [&](uint32_t base, int i, uint32_t (&w)[2]) {
                 if (NB == 4) {
-                    shared64(base + 16 * s + (hd.y >> s & 1) * 8, w);
+                    shared64(base + 16 * i + (b0 >> i & 1) * 8, w);
                 } else {
-                    w[0] = shared32(base + 16 * s + (hd.y >> s & 1) * 4 + (hd.z >> s & 1) * 8);
+                    w[0] = shared32(base + 16 * i + (b0 >> i & 1) * 4 + (b1 >> i & 1) * 8);
                     w[1] = 0;
                 }
             };
+            if (work) {
             // ---- a new item: q's operands
             if (fresh) {
                 fresh = false;
@@ -431,8 +446,14 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
                     }
                 }
             }
-            // ---- scores: s[t][16 s + ..]: this lane's slots j and j + 8 of each 16, head c of tile t
-            float s[NT][SUB][2];
+            copy_wait<2 * NST - 1>();
+            __syncwarp();  // every lane's copies of this stage's K have landed
+            asm volatile("" ::: "memory");
+            {
+                const uint4 hd = sm_head[warp][slot];
+                see = hd.x, b0 = hd.y, b1 = hd.z;
+            }
+            // ---- scores
 #pragma unroll
             for (int t = 0; t < NT; t++)
 #pragma unroll
@@ -504,15 +525,16 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
                     }
                 }
             }
+            }
             // ---- K's place in the ring takes the stage NST ahead
             int phys = -1;
             __syncwarp();
             if (fetch > 0) {
                 phys = place();
-                look();
                 fetch_k(phys, slot);
             }
             copy_commit();
+            if (work) {
             copy_wait<2 * NST - 1>();
             __syncwarp();  // V has landed
             asm volatile("" ::: "memory");
@@ -696,6 +718,7 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
                         for (int i = 0; i < 2; i++) add4(o[t][2 * b + i], sum[t][i]);
                 }
             }
+            }
             // ---- V's place in the ring takes the stage NST ahead
             __syncwarp();
             if (fetch > 0) {
@@ -704,6 +727,11 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
             }
             copy_commit();
             slot = slot + 1 == NST ? 0 : slot + 1;
+            if (!work) {
+                // (one try: where it fails, another CTA of the item has set the mark)
+                if (round == -1 && warp == 0 && lane < 2 && found >> 16 != a.mark) atomicCAS(mine, found, a.mark << 16);
+                continue;
+            }
 
             // ---- the end of the item, or of this warp's range
             const bool ends = at.st + 1 == at.nst;
@@ -744,78 +772,167 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
                     at.gi = 0;
                     if (left > 1) {
                         at.row = next_row(at.row);
-                        at.nst = (int)(first[at.row + 1] - first[at.row]);
+                        at.nst = first[at.row + 1] - first[at.row];
                     }
                 }
             } else {
                 at.st++;
             }
+            if (--left == 0) break;
         }
     }
 
     // ---- join: chains of pieces in the order of the warps; a warp takes every NW-th head of all chains
     __syncthreads();
-    PagedPiece* const info = reinterpret_cast<PagedPiece*>(a.ws + (size_t)gridDim.x * 2 * paged_piece_floats(D));
+    float* const pieces = a.ws + paged_pieces(gridDim.x);
+    int4 p0 = make_int4(0, 0, 0, 0), p1 = p0;
+    if (lane < NW) p0 = sm_piece[lane][0], p1 = sm_piece[lane][1];
+    const unsigned used0 = __ballot_sync(0xffffffffu, p0.z != 0), ends0 = __ballot_sync(0xffffffffu, p0.z && p0.w);
+    unsigned heads1 = __ballot_sync(0xffffffffu, p1.z != 0);  // warps in which a chain begins
     int job = 0;
-    bool head0 = false, tail1 = false;  // the CTA's own pieces
-    int covered = -1;                    // the last warp whose piece 0 belongs to a chain
-    for (int w = 0; w < NW; w++)
-        for (int slot = 0; slot < 2; slot++) {
-            const int4 p = sm_piece[w][slot];
-            if (!p.z || (slot == 0 && w <= covered)) continue;
-            // where the chain ends
-            bool ends = p.w;
-            int last = w;
-            for (int x = w + 1; x < NW && !ends; x++) {
-                const int4 y = sm_piece[x][0];
-                if (y.z) last = x, ends = y.w;
+    int4 own0 = make_int4(0, 0, 0, 0), own1 = own0;  // items of which the CTA leaves pieces 0 and 1 (.z: it does)
+    // A piece 0 goes on with an earlier warp's item; the CTA's first one goes on with another CTA's.
+    const unsigned cta0 = used0 & -used0 & (heads1 ? (heads1 & -heads1) * 2 - 1 : ~0u);
+    for (int step = cta0 ? 0 : 1; step == 0 || heads1; step = 1) {
+        const int slot = step, w = __ffs(slot ? heads1 : cta0) - 1;
+        if (slot) heads1 &= heads1 - 1;
+        const int4 p = sm_piece[w][slot];
+        const unsigned above = used0 & ~((2u << w) - 1), stop = ends0 & above;
+        const bool here = slot == 0 && p.w;  // it ends where it begins
+        const unsigned more = here ? 0 : stop ? above & ((stop & -stop) * 2 - 1) : above;  // the other warps of the chain
+        const int last = more ? 31 - __clz(more) : w;
+        const bool ends = here || (more && stop);
+        const bool out = slot == 1 && ends;
+        if (!out) (slot ? own1 : own0) = p;
+        const int g = p.y / HT, ht = p.y - g * HT;
+        for (int hh = 0; hh < C::HEADS; hh++, job++) {
+            if (job % NW != warp || ht * C::HEADS + hh >= G) continue;
+            auto piece = [&](int x) -> const float* {
+                return sm_piece[x][x == w ? slot : 0].z == 1 ? reinterpret_cast<const float*>(smem + x * NST * C::STAGE)
+                                                             : far + ((size_t)blockIdx.x * NW + x) * C::PIECE;
+            };
+            auto stat = [&](int x) { return reinterpret_cast<const float2*>(piece(x) + C::HEADS * D)[hh]; };
+            float m = -CUDART_INF_F;
+            for (int x = w; x <= last; x++)
+                if (x == w || more >> x & 1) m = fmaxf(m, stat(x).x);
+            float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+            float den = 0.f;
+            bool saw = false;
+            for (int x = w; x <= last; x++) {
+                if (x != w && !(more >> x & 1)) continue;
+                const float2 ml = stat(x);
+                saw |= __float_as_uint(ml.y) != 0;
+                if (ml.x == -CUDART_INF_F && ml.y == 0.f) continue;
+                const float f = ex2t(ml.x - m);
+                den += f * ml.y;
+                if (4 * lane < D) {
+                    const float4 v = *reinterpret_cast<const float4*>(piece(x) + hh * D + 4 * lane);
+                    num.x += f * v.x, num.y += f * v.y, num.z += f * v.z, num.w += f * v.w;
+                }
             }
-            covered = last;
-            const bool out = slot == 1 && ends;
-            if (!out && tid == 0) info[blockIdx.x * 2 + slot] = PagedPiece{p.x, p.y, 1, ends};
-            if (!out) (slot ? tail1 : head0) = true;
-            const int g = p.y / HT, ht = p.y - g * HT;
-            for (int hh = 0; hh < C::HEADS; hh++, job++) {
-                if (job % NW != warp || ht * C::HEADS + hh >= G) continue;
-                auto piece = [&](int x) -> const float* {
-                    return sm_piece[x][x == w ? slot : 0].z == 1 ? reinterpret_cast<const float*>(smem + x * NST * C::STAGE)
-                                                                 : far + ((size_t)blockIdx.x * NW + x) * C::PIECE;
-                };
-                auto stat = [&](int x) { return reinterpret_cast<const float2*>(piece(x) + C::HEADS * D)[hh]; };
-                float m = -CUDART_INF_F;
-                for (int x = w; x <= last; x++)
-                    if (x == w || sm_piece[x][0].z) m = fmaxf(m, stat(x).x);
-                float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-                float den = 0.f;
-                bool saw = false;
-                for (int x = w; x <= last; x++) {
-                    if (x != w && !sm_piece[x][0].z) continue;
-                    const float2 ml = stat(x);
-                    saw |= __float_as_uint(ml.y) != 0;
-                    if (ml.x == -CUDART_INF_F && ml.y == 0.f) continue;
-                    const float f = ex2t(ml.x - m);
-                    den += f * ml.y;
-                    if (4 * lane < D) {
-                        const float4 v = *reinterpret_cast<const float4*>(piece(x) + hh * D + 4 * lane);
-                        num.x += f * v.x, num.y += f * v.y, num.z += f * v.z, num.w += f * v.w;
-                    }
-                }
-                if (out) {
-                    const float inv = den != 0.f ? 1.f / den : saw ? CUDART_NAN_F : 0.f;
-                    if (4 * lane < D)
-                        *reinterpret_cast<float4*>(a.out + (int64_t)p.x * a.ldo + (int64_t)(g * G + ht * C::HEADS + hh) * D + 4 * lane) =
-                            make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
-                } else {
-                    float* dst = a.ws + (size_t)(blockIdx.x * 2 + slot) * paged_piece_floats(D);
-                    if (4 * lane < D) *reinterpret_cast<float4*>(dst + hh * D + 4 * lane) = num;
-                    if (den == 0.f && saw) den = -0.f;
-                    if (lane == 0) reinterpret_cast<float2*>(dst + kPagedHeads * D)[hh] = make_float2(m, den);
-                }
+            if (out) {
+                const float inv = den != 0.f ? 1.f / den : saw ? CUDART_NAN_F : 0.f;
+                if (4 * lane < D)
+                    *reinterpret_cast<float4*>(a.out + (int64_t)p.x * a.ldo + (int64_t)(g * G + ht * C::HEADS + hh) * D + 4 * lane) =
+                        make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
+            } else {
+                float* dst = pieces + (size_t)(blockIdx.x * 2 + slot) * paged_piece_floats(D);
+                if (4 * lane < D) *reinterpret_cast<float4*>(dst + hh * D + 4 * lane) = num;
+                if (den == 0.f && saw) den = -0.f;
+                if (lane == 0) reinterpret_cast<float2*>(dst + kPagedHeads * D)[hh] = make_float2(m, den);
             }
         }
-    if (tid == 0) {
-        if (!head0) info[blockIdx.x * 2] = PagedPiece{0, 0, 0, 0};
-        if (!tail1) info[blockIdx.x * 2 + 1] = PagedPiece{0, 0, 0, 0};
+    }
+    if (!own0.z && !own1.z) return;
+    // ---- items of several CTAs: the last CTA to leave its piece joins them, in order
+    __shared__ int2 sm_chain[2];  // first and last CTA of an item that this one joins; first < 0: it does not
+    __threadfence();
+    __syncthreads();
+    if (tid < 2) {
+        const int4 p = tid ? own1 : own0;
+        int2 chain = make_int2(-1, -1);
+        if (p.z) {
+            const int64_t nst = first[p.x + 1] - first[p.x], from = begin_unit + (int64_t)first[p.x] * GI + p.y * nst;
+            const int b = cta_of(from), e = cta_of(from + nst - 1);
+            if ((int)(atomicAdd(counters + b, 1ull) & 0xFFFF) == e - b) {
+                counters[b] = 0;
+                chain = make_int2(b, e);
+            }
+        }
+        sm_chain[tid] = chain;
+        __threadfence();
+    }
+    __syncthreads();
+    constexpr int PER = NW >= C::HEADS ? NW / C::HEADS : 1, AT_ONCE = NW / PER;  // warps of a head, heads at once
+    float4* const sm_num = reinterpret_cast<float4*>(smem);
+    float* const sm_den = reinterpret_cast<float*>(sm_num + NW * 32);
+#pragma unroll 1
+    for (int which = 0; which < 2; which++) {
+        const int2 chain = sm_chain[which];
+        if (chain.x < 0) continue;
+        const int4 p = which ? own1 : own0;
+        const int n = chain.y - chain.x + 1, g = p.y / HT, h0 = (p.y - g * HT) * C::HEADS, sub = warp % PER;
+#pragma unroll 1
+        for (int hb = 0; hb < C::HEADS; hb += AT_ONCE) {
+            const int hh = hb + warp / PER, head = h0 + hh, d = 4 * lane < D ? 4 * lane : 0;
+            const bool in = hh < C::HEADS && head < G;
+            auto piece = [&](int i) { return pieces + (size_t)(2 * (chain.x + i) + (i ? 0 : 1)) * paged_piece_floats(D); };
+            auto stat = [&](int i) { return __ldcg(reinterpret_cast<const float2*>(piece(i) + kPagedHeads * D) + hh); };
+            float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+            float m = -CUDART_INF_F, den = 0.f;
+            bool saw = false;
+            if (in) {
+                for (int i = lane; i < n; i += 32) {
+                    const float2 ml = stat(i);
+                    m = fmaxf(m, ml.x);
+                    saw |= __float_as_uint(ml.y) != 0;
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                saw = __any_sync(0xffffffffu, saw);
+                for (int i0 = 0; i0 * PER + sub < n; i0 += 32) {  // this warp's pieces: every PER-th from `sub` on
+                    const int mine = (i0 + lane) * PER + sub;
+                    const float2 ml = mine < n ? stat(mine) : make_float2(-CUDART_INF_F, 0.f);
+                    const bool none = ml.x == -CUDART_INF_F && ml.y == 0.f;
+                    const float f = none ? 0.f : ex2t(ml.x - m);
+                    den += none ? 0.f : f * ml.y;
+                    const unsigned live = __ballot_sync(0xffffffffu, !none);
+                    for (int k0 = 0; k0 < 32 && (i0 + k0) * PER + sub < n; k0 += 8) {
+                        float4 v[8];
+#pragma unroll
+                        for (int k = 0; k < 8; k++)
+                            v[k] = live >> (k0 + k) & 1
+                                       ? __ldcg(reinterpret_cast<const float4*>(piece((i0 + k0 + k) * PER + sub) + hh * D + d))
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                        for (int k = 0; k < 8; k++) {
+                            const float w = __shfl_sync(0xffffffffu, f, k0 + k);
+                            num.x += w * v[k].x, num.y += w * v[k].y, num.z += w * v[k].z, num.w += w * v[k].w;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+            }
+            if (PER > 1) {
+                __syncthreads();  // (the previous item's sums have been read)
+                sm_num[warp * 32 + lane] = num;
+                if (lane == 0) sm_den[warp] = den;
+                __syncthreads();
+                if (in && sub == 0)
+#pragma unroll
+                    for (int i = 1; i < PER; i++) {
+                        const float4 y = sm_num[(warp + i) * 32 + lane];
+                        num.x += y.x, num.y += y.y, num.z += y.z, num.w += y.w;
+                        den += sm_den[warp + i];
+                    }
+            }
+            if (in && sub == 0 && 4 * lane < D) {
+                const float inv = den != 0.f ? 1.f / den : saw ? CUDART_NAN_F : 0.f;
+                *reinterpret_cast<float4*>(a.out + (int64_t)p.x * a.ldo + (int64_t)(g * G + head) * D + 4 * lane) =
+                    make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
+            }
+        }
     }
 }
 
@@ -833,7 +950,7 @@ cudaError_t paged_go(const PagedArgs& a, int ctas, cudaStream_t s) {
     static SmemOptIn opt;
     cudaError_t e = opt((const void*)k, ring + (kPagedMaxRows + 1) * 4);
     if (e) return e;
-    return launch_chained(k, dim3(ctas), C::NW * 32, ring + (a.n + 1) * 4, s, a);
+    return launch_chained(k, dim3(ctas), C::NW * 32, ring + (a.n + 1) * 4 + (a.n <= kPagedKept ? a.n * 8 : 0), s, a);
 }
 
 #define AF_PAGED_INSTANTIATE(TYPE)                                                                    \

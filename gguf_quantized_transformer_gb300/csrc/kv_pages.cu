@@ -17,7 +17,8 @@ namespace af {
 namespace {
 
 constexpr int kScan = 1024;             // threads of the scanning CTA
-constexpr int kFillRows = 4, kFill = 256;  // rows of a thread, threads of a CTA of the second part
+constexpr int kFillRows = 4, kFill = 256;  // rows of a thread at a time, threads of a CTA of the second part
+constexpr int kKept = 2048;                // requests whose prefix sums a CTA of the second part keeps
 
 // A request as the second part sees it: .x the first page it takes (an index behind the ring's head), kRefused or kEnded;
 // .y its tokens before the step, .z its pages before the step, .w pages given back by earlier requests
@@ -65,36 +66,70 @@ __device__ __forceinline__ int last_le(int n, int x, F key) {
     return lo;
 }
 
-// Rows and returned pages of thread t of nt.  start(i), back(i): the prefix sums; head, count: the ring before the step.
-template <typename S, typename B>
+__device__ __forceinline__ int page_of(const PagesArgs& a, int pos) {
+    return a.page_mul ? (int)(__umulhi((unsigned)pos, a.page_mul) >> a.page_shift) : pos;
+}
+// Pages that hold x tokens
+__device__ __forceinline__ int pages_for(const PagesArgs& a, int x) {
+    const int e = page_of(a, x);
+    return e + (e * a.page != x ? 1 : 0);
+}
+
+// x modulo n, for x < 2 n
+__device__ __forceinline__ int wrap(unsigned x, int n) { return (int)(x >= (unsigned)n ? x - (unsigned)n : x); }
+
+// Rows and returned pages of thread t of nt: ROWS neighbours at a time.  start(i), back(i): the prefix sums; head, count: the
+// ring before the step.
+template <int ROWS, typename S, typename B>
 __device__ __forceinline__ void fill(const PagesArgs& a, int64_t t, int64_t nt, int total, int returned, int head, int count, S start,
                                      B back) {
-    for (int64_t r = t; r < a.rows; r += nt) {
-        int slot = -1, pos = -1, seq = -1;
-        if (r < total) {
-            const int i = last_le(a.n, (int)r, start);
-            const int4 q = __ldcg(a.ws + i);
-            if (q.x >= 0) {
-                pos = q.y + ((int)r - start(i));
-                const int at = pos / a.page, off = pos - at * a.page;
-                int page;
-                if (at < q.z) {
-                    page = __ldcg(a.table + (int64_t)i * a.width + at);
-                } else {
-                    page = __ldcg(a.free + ((int64_t)head + q.x + (at - q.z)) % a.n_pages);
-                    if (off == 0) a.table[(int64_t)i * a.width + at] = page;
+    for (int64_t at = t * ROWS; at < a.rows; at += nt * ROWS) {
+        const int r0 = (int)at;
+        int slot[ROWS], pos[ROWS], seq[ROWS];
+        int i = r0 < total ? last_le(a.n, r0, start) : 0, begin = 0, end = -1;  // rows [begin, end) of request i
+        int4 q = make_int4(kRefused, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < ROWS; k++) {
+            const int r = r0 + k;
+            slot[k] = pos[k] = seq[k] = -1;
+            if (r >= total || at + k >= a.rows) continue;
+            if (r >= end) {
+                if (k) {
+                    do i++;
+                    while (i + 1 < a.n && start(i + 1) <= r);
                 }
-                slot = page >= 0 && page < a.n_pages ? page * a.page + off : -1;
-                seq = i;
+                begin = start(i);
+                end = i + 1 < a.n ? start(i + 1) : total;
+                q = __ldcg(a.ws + i);
             }
+            if (q.x < 0) continue;
+            const int p = q.y + (r - begin), e = page_of(a, p);
+            const int off = p - e * a.page;
+            int page;
+            if (e < q.z) {
+                page = __ldcg(a.table + (int64_t)i * a.width + e);
+            } else {
+                page = __ldcg(a.free + wrap((unsigned)head + (unsigned)(q.x + (e - q.z)), a.n_pages));
+                if (off == 0) a.table[(int64_t)i * a.width + e] = page;
+            }
+            slot[k] = page >= 0 && page < a.n_pages ? page * a.page + off : -1;
+            pos[k] = p;
+            seq[k] = i;
         }
-        a.slots[r] = slot;
-        a.pos[r] = pos;
-        a.seq[r] = seq;
+        if (ROWS == 4 && at + ROWS <= a.rows && a.vec) {
+            *reinterpret_cast<int4*>(a.slots + r0) = make_int4(slot[0], slot[1 % ROWS], slot[2 % ROWS], slot[3 % ROWS]);
+            *reinterpret_cast<int4*>(a.pos + r0) = make_int4(pos[0], pos[1 % ROWS], pos[2 % ROWS], pos[3 % ROWS]);
+            *reinterpret_cast<int4*>(a.seq + r0) = make_int4(seq[0], seq[1 % ROWS], seq[2 % ROWS], seq[3 % ROWS]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < ROWS; k++)
+                if (at + k < a.rows) a.slots[r0 + k] = slot[k], a.pos[r0 + k] = pos[k], a.seq[r0 + k] = seq[k];
+        }
     }
     for (int64_t e = t; e < returned; e += nt) {
         const int i = last_le(a.n, (int)e, back);
-        a.free[((int64_t)head + count + e) % a.n_pages] = __ldcg(a.table + (int64_t)i * a.width + ((int)e - back(i)));
+        a.free[wrap((unsigned)head + (unsigned)count + (unsigned)e, a.n_pages)] =  // (count + e < n_pages)
+            __ldcg(a.table + (int64_t)i * a.width + ((int)e - back(i)));
     }
 }
 
@@ -122,9 +157,9 @@ __global__ void __launch_bounds__(kScan) kv_pages_scan_kernel(PagesArgs a) {
         cta_scan2(rows, unused, total);
         rows += rows0;
         rows0 += total[0];
-        const int have = sound ? (int)(((int64_t)len + a.page - 1) / a.page) : 0;
+        const int have = sound ? pages_for(a, len) : 0;
         const bool fits = in && !ends && sound && rows <= a.rows && len + grow <= most;
-        const int64_t need = fits ? (len + grow + a.page - 1) / a.page - have : 0, back = in && ends ? have : 0;
+        const int64_t need = fits ? pages_for(a, (int)(len + grow)) - have : 0, back = in && ends ? have : 0;
         int64_t taken = need, returned = back;
         cta_scan2(taken, returned, total);
         taken += take0, returned += back0;
@@ -148,20 +183,30 @@ __global__ void __launch_bounds__(kScan) kv_pages_scan_kernel(PagesArgs a) {
     if (t == 0) {
         a.start[a.n] = total;
         a.ws[a.n] = make_int4(head, count, total, returned);
-        a.pool_out[0] = (int)(((int64_t)head + taken) % a.n_pages);
+        a.pool_out[0] = wrap((unsigned)head + (unsigned)taken, a.n_pages);
         a.pool_out[1] = count - taken + returned;
         a.pool_out[2] = sm_refused;
         a.pool_out[3] = total;
     }
-    if (FILL) fill(a, t, kScan, total, returned, head, count, [&](int i) { return sm_start[i]; }, [&](int i) { return sm_back[i]; });
+    if (FILL) fill<1>(a, t, kScan, total, returned, head, count, [&](int i) { return sm_start[i]; }, [&](int i) { return sm_back[i]; });
 }
 
+// KEPT: the prefix sums in shared memory, so that the searches do not wait for L2.
+template <bool KEPT>
 __global__ void __launch_bounds__(kFill) kv_pages_fill_kernel(PagesArgs a) {
+    extern __shared__ int sm_sums[];  // [n] starts, [n] pages given back
     pdl_launch_dependents();
     pdl_wait();
     const int4 h = __ldcg(a.ws + a.n);
-    fill(a, (int64_t)blockIdx.x * kFill + threadIdx.x, (int64_t)gridDim.x * kFill, h.z, h.w, h.x, h.y,
-         [&](int i) { return __ldcg(a.start + i); }, [&](int i) { return __ldcg(&a.ws[i].w); });
+    if (KEPT) {
+        for (int i = threadIdx.x; i < a.n; i += kFill) sm_sums[i] = __ldcg(a.start + i), sm_sums[a.n + i] = __ldcg(&a.ws[i].w);
+        __syncthreads();
+    }
+    const int64_t t = (int64_t)blockIdx.x * kFill + threadIdx.x, nt = (int64_t)gridDim.x * kFill;
+    if (KEPT)
+        fill<kFillRows>(a, t, nt, h.z, h.w, h.x, h.y, [&](int i) { return sm_sums[i]; }, [&](int i) { return sm_sums[a.n + i]; });
+    else
+        fill<kFillRows>(a, t, nt, h.z, h.w, h.x, h.y, [&](int i) { return __ldcg(a.start + i); }, [&](int i) { return __ldcg(&a.ws[i].w); });
 }
 
 }  // namespace
@@ -172,7 +217,8 @@ cudaError_t launch_kv_pages(const PagesArgs& a, cudaStream_t s) {
     if (e) return e;
     const int64_t work = std::max<int64_t>(a.rows, a.n);
     const int ctas = (int)std::min<int64_t>((work + kFill * kFillRows - 1) / (kFill * kFillRows), 8 * (int64_t)num_sms());
-    return launch_chained(kv_pages_fill_kernel, dim3(std::max(ctas, 1)), kFill, 0, s, a);
+    if (a.n <= kKept) return launch_chained(kv_pages_fill_kernel<true>, dim3(std::max(ctas, 1)), kFill, 8 * a.n, s, a);
+    return launch_chained(kv_pages_fill_kernel<false>, dim3(std::max(ctas, 1)), kFill, 0, s, a);
 }
 
 }  // namespace af

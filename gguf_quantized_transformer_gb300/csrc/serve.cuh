@@ -18,6 +18,9 @@ struct PagesArgs {
     int* start = nullptr;  // [n + 1]
     int *slots = nullptr, *pos = nullptr, *seq = nullptr;
     int4* ws = nullptr;  // [n + 1]
+    unsigned page_mul = 0;  // position / page = umulhi(position, page_mul) >> page_shift; 0: page is 1
+    int page_shift = 0;
+    bool vec = false;  // slots, pos and seq are 16-byte aligned
 };
 cudaError_t launch_kv_pages(const PagesArgs& a, cudaStream_t s);
 
@@ -30,12 +33,14 @@ struct PagedArgs {
     int H = 0, page = 1, n_pages = 0, width = 0, n_seqs = 0, n = 0;
     unsigned page_mul = 0;  // slot / page = umulhi(slot, page_mul) >> page_shift; 0: page is 1
     int page_shift = 0;
+    bool wide = false;  // the stages of all rows and heads may pass 31 bits
     const int* table = nullptr;
     const int* seq = nullptr;  // nullable: row r is request r
     const int* pos = nullptr;
     float* out = nullptr;
     int64_t ldo = 0;
     float* ws = nullptr;
+    unsigned long long mark = 0;  // 48 bits that a counter in a workspace of any contents does not hold
 };
 size_t attn_paged_ws_bytes(int D);
 cudaError_t launch_attn_paged(const PagedArgs& a, cudaStream_t s);
