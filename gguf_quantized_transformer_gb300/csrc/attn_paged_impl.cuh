@@ -213,9 +213,12 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
             if (w < warp) x += y;
             total += y;
         }
-        // the first `rest` warps have a stage more than the others
-        const I units = total * GI, warps = gridDim.x * NW, each = units / warps, rest = units - each * warps;
-        auto cut = [&](I w) { return each * w + min(w, rest); };
+        // the first `rest` warps have a stage more than the others; a warp has at least 32 slots, so that short items of a
+        // small call need no joining
+        const I units = total * GI, warps = gridDim.x * NW, least = 32 / KS;
+        I each = units / warps, rest = units - each * warps;
+        if (each < least) each = least, rest = 0;
+        auto cut = [&](I w) { return min(each * w + min(w, rest), units); };
         const I me = blockIdx.x * NW, begin = cut(me) / GI;
         begin_unit = (int64_t)begin * GI, units_each = each, units_rest = rest;
         u = cut(me + warp) - begin * GI;
@@ -785,55 +788,69 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
     // ---- join: chains of pieces in the order of the warps; a warp takes every NW-th head of all chains
     __syncthreads();
     float* const pieces = a.ws + paged_pieces(gridDim.x);
-    int4 p0 = make_int4(0, 0, 0, 0), p1 = p0;
+    int4 p0 = make_int4(0, 0, 0, 0), p1 = p0;  // lane x: the pieces of warp x
     if (lane < NW) p0 = sm_piece[lane][0], p1 = sm_piece[lane][1];
     const unsigned used0 = __ballot_sync(0xffffffffu, p0.z != 0), ends0 = __ballot_sync(0xffffffffu, p0.z && p0.w);
     unsigned heads1 = __ballot_sync(0xffffffffu, p1.z != 0);  // warps in which a chain begins
-    int job = 0;
+    const float* const near_by = reinterpret_cast<const float*>(smem + min(lane, NW - 1) * NST * C::STAGE);
+    const float* const far_off = far + ((size_t)blockIdx.x * NW + min(lane, NW - 1)) * C::PIECE;
+    int job = warp;                                             // heads before this warp's next one
     int4 own0 = make_int4(0, 0, 0, 0), own1 = own0;  // items of which the CTA leaves pieces 0 and 1 (.z: it does)
     // A piece 0 goes on with an earlier warp's item; the CTA's first one goes on with another CTA's.
     const unsigned cta0 = used0 & -used0 & (heads1 ? (heads1 & -heads1) * 2 - 1 : ~0u);
-    for (int step = cta0 ? 0 : 1; step == 0 || heads1; step = 1) {
-        const int slot = step, w = __ffs(slot ? heads1 : cta0) - 1;
+#pragma unroll 1
+    for (int slot = cta0 ? 0 : 1; slot == 0 || heads1; slot = 1) {
+        const int w = __ffs(slot ? heads1 : cta0) - 1;
         if (slot) heads1 &= heads1 - 1;
-        const int4 p = sm_piece[w][slot];
+        const int4 pw = slot ? p1 : p0;
+        const int4 p = make_int4(__shfl_sync(0xffffffffu, pw.x, w), __shfl_sync(0xffffffffu, pw.y, w), __shfl_sync(0xffffffffu, pw.z, w),
+                                 __shfl_sync(0xffffffffu, pw.w, w));
         const unsigned above = used0 & ~((2u << w) - 1), stop = ends0 & above;
         const bool here = slot == 0 && p.w;  // it ends where it begins
         const unsigned more = here ? 0 : stop ? above & ((stop & -stop) * 2 - 1) : above;  // the other warps of the chain
-        const int last = more ? 31 - __clz(more) : w;
-        const bool ends = here || (more && stop);
-        const bool out = slot == 1 && ends;
+        const bool out = slot == 1 && more && stop;
         if (!out) (slot ? own1 : own0) = p;
         const int g = p.y / HT, ht = p.y - g * HT;
-        for (int hh = 0; hh < C::HEADS; hh++, job++) {
-            if (job % NW != warp || ht * C::HEADS + hh >= G) continue;
-            auto piece = [&](int x) -> const float* {
-                return sm_piece[x][x == w ? slot : 0].z == 1 ? reinterpret_cast<const float*>(smem + x * NST * C::STAGE)
-                                                             : far + ((size_t)blockIdx.x * NW + x) * C::PIECE;
-            };
-            auto stat = [&](int x) { return reinterpret_cast<const float2*>(piece(x) + C::HEADS * D)[hh]; };
-            float m = -CUDART_INF_F;
-            for (int x = w; x <= last; x++)
-                if (x == w || more >> x & 1) m = fmaxf(m, stat(x).x);
+        const float* const mine = (lane == w ? pw.z : p0.z) == 1 ? near_by : far_off;
+        const unsigned chain = more | 1u << w;
+#pragma unroll 1
+        for (; job < C::HEADS; job += NW) {
+            const int hh = job, head = ht * C::HEADS + hh;
+            if (head >= G) continue;
+            float2 ml = make_float2(-CUDART_INF_F, 0.f);
+            if (chain >> lane & 1) ml = reinterpret_cast<const float2*>(mine + C::HEADS * D)[hh];
+            float m = ml.x;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const bool none = ml.x == -CUDART_INF_F && ml.y == 0.f;  // it adds nothing
+            const float f = none ? 0.f : ex2t(ml.x - m);
+            float den = none ? 0.f : f * ml.y;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+            const bool saw = __any_sync(0xffffffffu, __float_as_uint(ml.y) != 0);
+            const unsigned adds = __ballot_sync(0xffffffffu, !none);
             float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-            float den = 0.f;
-            bool saw = false;
-            for (int x = w; x <= last; x++) {
-                if (x != w && !(more >> x & 1)) continue;
-                const float2 ml = stat(x);
-                saw |= __float_as_uint(ml.y) != 0;
-                if (ml.x == -CUDART_INF_F && ml.y == 0.f) continue;
-                const float f = ex2t(ml.x - m);
-                den += f * ml.y;
-                if (4 * lane < D) {
-                    const float4 v = *reinterpret_cast<const float4*>(piece(x) + hh * D + 4 * lane);
-                    num.x += f * v.x, num.y += f * v.y, num.z += f * v.z, num.w += f * v.w;
+            float4 v[4];
+            float fx[4];
+            for (unsigned rest = adds; rest;) {  // four pieces' loads at a time
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int x = rest ? __ffs(rest) - 1 : 0;
+                    const float* src = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, (unsigned long long)mine, x));
+                    const float fs = __shfl_sync(0xffffffffu, f, x);
+                    const bool in = rest != 0;
+                    fx[i] = in ? fs : 0.f;
+                    v[i] = in && 4 * lane < D ? *reinterpret_cast<const float4*>(src + hh * D + 4 * lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    rest &= rest - 1;
                 }
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    num.x += fx[i] * v[i].x, num.y += fx[i] * v[i].y, num.z += fx[i] * v[i].z, num.w += fx[i] * v[i].w;
             }
             if (out) {
                 const float inv = den != 0.f ? 1.f / den : saw ? CUDART_NAN_F : 0.f;
                 if (4 * lane < D)
-                    *reinterpret_cast<float4*>(a.out + (int64_t)p.x * a.ldo + (int64_t)(g * G + ht * C::HEADS + hh) * D + 4 * lane) =
+                    *reinterpret_cast<float4*>(a.out + (int64_t)p.x * a.ldo + (int64_t)(g * G + head) * D + 4 * lane) =
                         make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
             } else {
                 float* dst = pieces + (size_t)(blockIdx.x * 2 + slot) * paged_piece_floats(D);
@@ -842,11 +859,11 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
                 if (lane == 0) reinterpret_cast<float2*>(dst + kPagedHeads * D)[hh] = make_float2(m, den);
             }
         }
+        job -= C::HEADS;
     }
     if (!own0.z && !own1.z) return;
     // ---- items of several CTAs: the last CTA to leave its piece joins them, in order
     __shared__ int2 sm_chain[2];  // first and last CTA of an item that this one joins; first < 0: it does not
-    __threadfence();
     __syncthreads();
     if (tid < 2) {
         const int4 p = tid ? own1 : own0;
@@ -854,85 +871,69 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
         if (p.z) {
             const int64_t nst = first[p.x + 1] - first[p.x], from = begin_unit + (int64_t)first[p.x] * GI + p.y * nst;
             const int b = cta_of(from), e = cta_of(from + nst - 1);
+            __threadfence();  // (the CTA's pieces, which the barrier has put before this thread)
             if ((int)(atomicAdd(counters + b, 1ull) & 0xFFFF) == e - b) {
                 counters[b] = 0;
                 chain = make_int2(b, e);
             }
+            __threadfence();
         }
         sm_chain[tid] = chain;
-        __threadfence();
     }
     __syncthreads();
-    constexpr int PER = NW >= C::HEADS ? NW / C::HEADS : 1, AT_ONCE = NW / PER;  // warps of a head, heads at once
-    float4* const sm_num = reinterpret_cast<float4*>(smem);
-    float* const sm_den = reinterpret_cast<float*>(sm_num + NW * 32);
+    // a warp takes every NW-th head of one or two items; sums over 32 pieces at a time
 #pragma unroll 1
-    for (int which = 0; which < 2; which++) {
+    for (int x = warp; x < 2 * C::HEADS; x += NW) {
+        const int which = x / C::HEADS, hh = x % C::HEADS;
         const int2 chain = sm_chain[which];
-        if (chain.x < 0) continue;
         const int4 p = which ? own1 : own0;
-        const int n = chain.y - chain.x + 1, g = p.y / HT, h0 = (p.y - g * HT) * C::HEADS, sub = warp % PER;
+        const int n = chain.y - chain.x + 1, g = p.y / HT, head = (p.y - g * HT) * C::HEADS + hh, d = 4 * lane < D ? 4 * lane : 0;
+        if (chain.x < 0 || head >= G) continue;
+        auto piece = [&](int i) { return pieces + (size_t)(2 * (chain.x + i) + (i ? 0 : 1)) * paged_piece_floats(D); };
+        float m = -CUDART_INF_F, den = 0.f;
+        float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+        bool saw = false;
 #pragma unroll 1
-        for (int hb = 0; hb < C::HEADS; hb += AT_ONCE) {
-            const int hh = hb + warp / PER, head = h0 + hh, d = 4 * lane < D ? 4 * lane : 0;
-            const bool in = hh < C::HEADS && head < G;
-            auto piece = [&](int i) { return pieces + (size_t)(2 * (chain.x + i) + (i ? 0 : 1)) * paged_piece_floats(D); };
-            auto stat = [&](int i) { return __ldcg(reinterpret_cast<const float2*>(piece(i) + kPagedHeads * D) + hh); };
-            float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-            float m = -CUDART_INF_F, den = 0.f;
-            bool saw = false;
-            if (in) {
-                for (int i = lane; i < n; i += 32) {
-                    const float2 ml = stat(i);
-                    m = fmaxf(m, ml.x);
-                    saw |= __float_as_uint(ml.y) != 0;
-                }
+        for (int i0 = 0; i0 < n; i0 += 32) {
+            float2 ml = make_float2(-CUDART_INF_F, 0.f);
+            if (i0 + lane < n) ml = __ldcg(reinterpret_cast<const float2*>(piece(i0 + lane) + kPagedHeads * D) + hh);
+            float4 v[8];
+            auto load = [&](int k0) {
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                saw = __any_sync(0xffffffffu, saw);
-                for (int i0 = 0; i0 * PER + sub < n; i0 += 32) {  // this warp's pieces: every PER-th from `sub` on
-                    const int mine = (i0 + lane) * PER + sub;
-                    const float2 ml = mine < n ? stat(mine) : make_float2(-CUDART_INF_F, 0.f);
-                    const bool none = ml.x == -CUDART_INF_F && ml.y == 0.f;
-                    const float f = none ? 0.f : ex2t(ml.x - m);
-                    den += none ? 0.f : f * ml.y;
-                    const unsigned live = __ballot_sync(0xffffffffu, !none);
-                    for (int k0 = 0; k0 < 32 && (i0 + k0) * PER + sub < n; k0 += 8) {
-                        float4 v[8];
+                for (int k = 0; k < 8; k++)
+                    if (i0 + k0 + k < n) v[k] = __ldcg(reinterpret_cast<const float4*>(piece(i0 + k0 + k) + hh * D + d));
+            };
+            load(0);
+            float top = fmaxf(m, ml.x);
 #pragma unroll
-                        for (int k = 0; k < 8; k++)
-                            v[k] = live >> (k0 + k) & 1
-                                       ? __ldcg(reinterpret_cast<const float4*>(piece((i0 + k0 + k) * PER + sub) + hh * D + d))
-                                       : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                        for (int k = 0; k < 8; k++) {
-                            const float w = __shfl_sync(0xffffffffu, f, k0 + k);
-                            num.x += w * v[k].x, num.y += w * v[k].y, num.z += w * v[k].z, num.w += w * v[k].w;
-                        }
-                    }
-                }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (top > m) {
+                const float f = ex2t(m - top);
+                m = top;
+                den *= f, num.x *= f, num.y *= f, num.z *= f, num.w *= f;
             }
-            if (PER > 1) {
-                __syncthreads();  // (the previous item's sums have been read)
-                sm_num[warp * 32 + lane] = num;
-                if (lane == 0) sm_den[warp] = den;
-                __syncthreads();
-                if (in && sub == 0)
+            const bool none = ml.x == -CUDART_INF_F && ml.y == 0.f;
+            const float f = none ? 0.f : ex2t(ml.x - m);
+            float sum = none ? 0.f : f * ml.y;
 #pragma unroll
-                    for (int i = 1; i < PER; i++) {
-                        const float4 y = sm_num[(warp + i) * 32 + lane];
-                        num.x += y.x, num.y += y.y, num.z += y.z, num.w += y.w;
-                        den += sm_den[warp + i];
-                    }
-            }
-            if (in && sub == 0 && 4 * lane < D) {
-                const float inv = den != 0.f ? 1.f / den : saw ? CUDART_NAN_F : 0.f;
-                *reinterpret_cast<float4*>(a.out + (int64_t)p.x * a.ldo + (int64_t)(g * G + head) * D + 4 * lane) =
-                    make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            den += sum;
+            saw |= __any_sync(0xffffffffu, __float_as_uint(ml.y) != 0);
+            const unsigned adds = __ballot_sync(0xffffffffu, !none);
+#pragma unroll 1
+            for (int k0 = 0; k0 < 32 && i0 + k0 < n; k0 += 8) {
+                if (k0) load(k0);
+#pragma unroll
+                for (int k = 0; k < 8; k++) {
+                    const float w = __shfl_sync(0xffffffffu, f, k0 + k);
+                    if (adds >> (k0 + k) & 1) num.x += w * v[k].x, num.y += w * v[k].y, num.z += w * v[k].z, num.w += w * v[k].w;
+                }
             }
         }
+        const float inv = den != 0.f ? 1.f / den : saw ? CUDART_NAN_F : 0.f;
+        if (4 * lane < D)
+            *reinterpret_cast<float4*>(a.out + (int64_t)p.x * a.ldo + (int64_t)(g * G + head) * D + 4 * lane) =
+                make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
     }
 }
 
