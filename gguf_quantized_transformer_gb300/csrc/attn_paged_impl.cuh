@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
                             const uint32_t *k0 = e < 4 ? lo[0] : hi[0], *k1 = e < 4 ? lo[1] : hi[1];
 #pragma unroll
                             for (int t = 0; t < NT; t++)
-                                mma8(p[t], make_uint4(k0[i], k1[i], k0[i + 1], k1[i + 1]), qf[t][step][0], qf[t][step][1]);
+                                dot8(p[t], make_uint4(k0[i], k1[i], k0[i + 1], k1[i + 1]), qf[t][step][0], qf[t][step][1]);
                         }
 #pragma unroll
                         for (int t = 0; t < NT; t++) s[t][x][0] += p[t][0] + p[t][1], s[t][x][1] += p[t][2] + p[t][3];
@@ -513,8 +513,8 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
 #pragma unroll
                         for (int t = 0; t < NT; t++) {
                             float p[4];
-                            mma16z(p, make_uint4(w[0][0], w[1][0], w[0][1], w[1][1]), qf[t][2 * b][0], qf[t][2 * b][1]);
-                            mma16(p, make_uint4(w[0][2], w[1][2], w[0][3], w[1][3]), qf[t][2 * b + 1][0], qf[t][2 * b + 1][1]);
+                            dot16z(p, make_uint4(w[0][0], w[1][0], w[0][1], w[1][1]), qf[t][2 * b][0], qf[t][2 * b][1]);
+                            dot16(p, make_uint4(w[0][2], w[1][2], w[0][3], w[1][3]), qf[t][2 * b + 1][0], qf[t][2 * b + 1][1]);
                             const float s0 = p[0] + p[1], s1 = p[2] + p[3];
                             if constexpr (C::QUANT) {
                                 const __half2 d0 = u_h2(dk[0][b / 2]), d1 = u_h2(dk[1][b / 2]);
@@ -642,10 +642,10 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
 #pragma unroll
                         for (int e = 0; e < 4; e += 2) {
                             float sum[4];
-                            mma8z(sum, make_uint4(lo[0][e], lo[0][e + 1], lo[1][e], lo[1][e + 1]), pb[t][0][0], pb[t][0][1]);
-                            mma8(sum, make_uint4(lo[2][e], lo[2][e + 1], lo[3][e], lo[3][e + 1]), pb[t][1][0], pb[t][1][1]);
-                            mma8(sum, make_uint4(hi[0][e], hi[0][e + 1], hi[1][e], hi[1][e + 1]), pb[t][0][0], pb[t][0][1]);
-                            mma8(sum, make_uint4(hi[2][e], hi[2][e + 1], hi[3][e], hi[3][e + 1]), pb[t][1][0], pb[t][1][1]);
+                            dot8z(sum, make_uint4(lo[0][e], lo[0][e + 1], lo[1][e], lo[1][e + 1]), pb[t][0][0], pb[t][0][1]);
+                            dot8(sum, make_uint4(lo[2][e], lo[2][e + 1], lo[3][e], lo[3][e + 1]), pb[t][1][0], pb[t][1][1]);
+                            dot8(sum, make_uint4(hi[0][e], hi[0][e + 1], hi[1][e], hi[1][e + 1]), pb[t][0][0], pb[t][0][1]);
+                            dot8(sum, make_uint4(hi[2][e], hi[2][e + 1], hi[3][e], hi[3][e + 1]), pb[t][1][0], pb[t][1][1]);
                             add4(o[t][2 * y + e / 2], sum);
                         }
                 }
@@ -667,7 +667,7 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
 #pragma unroll
                         for (int t = 0; t < NT; t++) {
                             float sum[4];
-                            mma16z(sum, v, pb[t][0], pb[t][1]);
+                            dot16z(sum, v, pb[t][0], pb[t][1]);
                             add4(o[t][4 * y + i], sum);
                         }
                     }
@@ -710,9 +710,9 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
                             for (int i = 0; i < 2; i++) {
                                 const uint4 w = make_uint4(v[0][2 * i], v[0][2 * i + 1], v[1][2 * i], v[1][2 * i + 1]);
                                 if (x == 0)
-                                    mma16z(sum[t][i], w, pb[t][x][0], pb[t][x][1]);
+                                    dot16z(sum[t][i], w, pb[t][x][0], pb[t][x][1]);
                                 else
-                                    mma16(sum[t][i], w, pb[t][x][0], pb[t][x][1]);
+                                    dot16(sum[t][i], w, pb[t][x][0], pb[t][x][1]);
                             }
                     }
 #pragma unroll

@@ -114,110 +114,130 @@ __global__ void __launch_bounds__(kPlanThreads) lora_plan_kernel(const int* __re
     }
 }
 
-// ---------------------------------------------------------------- shrink
+// ---------------------------------------------------------------- rings
 
-// Ranges of K: as many as two CTAs on every SM take at once, of at least 8 chunks of 32
-__device__ __forceinline__ int lora_splits(int items, int K, int sms) {
-    return max(1, min(min(2 * sms / max(items, 1), kMaxSplit), K / 32 / kWarps));
+// 16 bytes through L2 into a shared-memory ring, of which the first `bytes` are read and the others zeros
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 shared16(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
 }
 
 __device__ __forceinline__ int rank_of(const LoraArgs& a, int adapter) {
     return a.ranks ? min(max(__ldcg(a.ranks + adapter), 0), a.rank) : a.rank;
 }
-__device__ __forceinline__ float4 ldcg4(const float* p) { return __ldcg(reinterpret_cast<const float4*>(p)); }
 
-// 8 weights of a row as tf32 parts; lo only of fp32 weights
-template <bool F16>
-struct Weights8 {
-    uint4 w[F16 ? 1 : 2];
-    __device__ __forceinline__ void load(const void* p, bool in) {
-#pragma unroll
-        for (int i = 0; i < (F16 ? 1 : 2); i++)
-            w[i] = in ? __ldcg(reinterpret_cast<const uint4*>(p) + i) : make_uint4(0u, 0u, 0u, 0u);
-    }
-    __device__ __forceinline__ void parts(uint32_t (&hi)[8], uint32_t (&lo)[8]) const {
-        if constexpr (F16) {
-            const uint32_t x[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x[i]));
-                hi[2 * i] = __float_as_uint(f.x), hi[2 * i + 1] = __float_as_uint(f.y);
-            }
-        } else {
-            const uint32_t x[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
-#pragma unroll
-            for (int i = 0; i < 8; i++) cut_tf32(__uint_as_float(x[i]), hi[i], lo[i]);
-        }
-    }
-};
+// ---------------------------------------------------------------- shrink
 
-// The sums of chunks k0, k0 + kWarps .. below k1 for 16 MT ranks and 8 NT rows, U chunks on their way at once.
-// wp: this lane's weights of rank j; in: the ranks that there are, from j on; xp: this lane's values of the rows 8 t + j, null
-// where there is none.
-template <bool F16, int MT, int NT, int U>
-__device__ __forceinline__ void shrink_chunks(const uint8_t* wp, int in, int K, const float* const (&xp)[NT], int k0, int k1,
-                                              float (&acc)[MT][NT][4]) {
-    constexpr size_t es = F16 ? 2 : 4;
-#pragma unroll 1
-    for (int k = k0; k < k1; k += U * kWarps) {
-        Weights8<F16> w[U][MT][2];
-        float4 x[U][NT][2];
-#pragma unroll
-        for (int u = 0; u < U; u++) {
-            const int ku = k + u * kWarps;
-#pragma unroll
-            for (int m = 0; m < MT; m++)
-#pragma unroll
-                for (int h = 0; h < 2; h++)
-                    w[u][m][h].load(wp + ((int64_t)(16 * m + 8 * h) * K + 32 * ku) * es, ku < k1 && 16 * m + 8 * h < in);
-#pragma unroll
-            for (int t = 0; t < NT; t++)
-#pragma unroll
-                for (int i = 0; i < 2; i++)
-                    x[u][t][i] = ku < k1 && xp[t] ? ldcg4(xp[t] + 32 * ku + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-#pragma unroll
-        for (int u = 0; u < U; u++) {
-            if (u && k + u * kWarps >= k1) break;
-#pragma unroll
-            for (int m = 0; m < MT; m++) {
-                uint32_t h0[8], l0[8], h1[8], l1[8];
-                w[u][m][0].parts(h0, l0);
-                w[u][m][1].parts(h1, l1);
-#pragma unroll
-                for (int t = 0; t < NT; t++) {
-                    const float4 a = x[u][t][0], b = x[u][t][1];
-                    const float xs[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-                    uint32_t xh[8], xl[8];
-#pragma unroll
-                    for (int i = 0; i < 8; i++) cut_tf32(xs[i], xh[i], xl[i]);
-                    float sum[4];
-                    mma8z(sum, make_uint4(h0[0], h1[0], h0[1], h1[1]), xl[0], xl[1]);
-#pragma unroll
-                    for (int e = 2; e < 8; e += 2) mma8(sum, make_uint4(h0[e], h1[e], h0[e + 1], h1[e + 1]), xl[e], xl[e + 1]);
-                    if constexpr (!F16) {
-#pragma unroll
-                        for (int e = 0; e < 8; e += 2) mma8(sum, make_uint4(l0[e], l1[e], l0[e + 1], l1[e + 1]), xh[e], xh[e + 1]);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 8; e += 2) mma8(sum, make_uint4(h0[e], h1[e], h0[e + 1], h1[e + 1]), xh[e], xh[e + 1]);
-                    add4(acc[m][t], sum);
-                }
-            }
-        }
-    }
+// Ranges of K: as many as every SM takes one of at once, of at least 8 chunks of 32
+__device__ __forceinline__ int lora_splits(int items, int K, int sms) {
+    return max(1, min(min(sms / max(items, 1), kMaxSplit), K / 32 / kWarps));
 }
 
-// The tile's rows' 16 MT ranks, summed over the warps, in `sum`: [warps][16 MT][PAD]
-template <bool F16, int MT, int NT, int U>
+constexpr int kRing = 24 * 1024;  // of a warp of shrink
+
+// The sums of chunks k0 + warp, + kWarps .. below k1 for 16 MT ranks and 8 NT rows, in `sum`: [warps][16 MT][pad].  Weights and
+// x go through a ring in which every lane has places of its own, so that no lane waits for another.
+// wp: this lane's weights of rank j; in: the ranks that there are, from j on.
+template <bool F16, int MT, int NT>
 __device__ __forceinline__ void shrink_tile(const LoraArgs& a, const int* row, int count, const uint8_t* wp, int in, int k0, int k1,
-                                            float* sum, int pad) {
+                                            uint32_t ring, float* sum, int pad) {
+    constexpr int WC = F16 ? 1 : 2, COPIES = 2 * MT * WC + 2 * NT, STAGE = COPIES * 512, NST = kRing / STAGE < 8 ? kRing / STAGE : 8;
+    constexpr int es = F16 ? 2 : 4;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 3, j = lane >> 2;
     const float* xp[NT];
 #pragma unroll
-    for (int t = 0; t < NT; t++) xp[t] = 8 * t + j < count ? a.x + (int64_t)row[8 * t + j] * a.ldx + 8 * c : nullptr;
+    for (int t = 0; t < NT; t++) xp[t] = a.x + (8 * t + j < count ? (int64_t)row[8 * t + j] * a.ldx : 0) + 8 * c;
+    ring += lane * 16;
+    auto fetch = [&](int k, int slot) {
+        const uint32_t dst = ring + slot * STAGE;
+#pragma unroll
+        for (int i = 0; i < 2 * MT; i++) {
+            const bool is = 8 * i < in;
+            const uint8_t* p = is ? wp + ((int64_t)8 * i * a.K + 32 * k) * es : (const uint8_t*)a.a;
+#pragma unroll
+            for (int h = 0; h < WC; h++) copy16(dst + (i * WC + h) * 512, p + 16 * h, is ? 16 : 0);
+        }
+#pragma unroll
+        for (int t = 0; t < NT; t++) {
+            const int bytes = 8 * t + j < count ? 16 : 0;
+#pragma unroll
+            for (int h = 0; h < 2; h++) copy16(dst + (2 * MT * WC + 2 * t + h) * 512, xp[t] + 32 * k + 4 * h, bytes);
+        }
+    };
     float acc[MT][NT][4] = {};
-    shrink_chunks<F16, MT, NT, U>(wp, in, a.K, xp, k0 + warp, k1, acc);
+    int ahead = k0 + warp;
+#pragma unroll 1
+    for (int i = 0; i < NST; i++, ahead += kWarps) {
+        if (ahead < k1) fetch(ahead, i);
+        copy_commit();
+    }
+    int slot = 0;
+#pragma unroll 1
+    for (int k = k0 + warp; k < k1; k += kWarps, ahead += kWarps) {
+        copy_wait<NST - 1>();
+        const uint32_t at = ring + slot * STAGE;
+        uint32_t xh[NT][8], xl[NT][8];
+#pragma unroll
+        for (int t = 0; t < NT; t++) {
+            const uint4 v = shared16(at + (2 * MT * WC + 2 * t) * 512), w = shared16(at + (2 * MT * WC + 2 * t + 1) * 512);
+            const uint32_t y[8] = {v.x, v.y, v.z, v.w, w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int i = 0; i < 8; i++) cut_tf32(__uint_as_float(y[i]), xh[t][i], xl[t][i]);
+        }
+#pragma unroll
+        for (int m = 0; m < MT; m++) {
+            uint32_t hi[2][8], lo[2][8];
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                if constexpr (F16) {
+                    const uint4 v = shared16(at + (2 * m + h) * 512);
+                    const uint32_t y[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&y[i]));
+                        hi[h][2 * i] = __float_as_uint(f.x), hi[h][2 * i + 1] = __float_as_uint(f.y);
+                    }
+                } else {
+                    const uint4 v = shared16(at + (4 * m + 2 * h) * 512), w = shared16(at + (4 * m + 2 * h + 1) * 512);
+                    const uint32_t y[8] = {v.x, v.y, v.z, v.w, w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int i = 0; i < 8; i++) cut_tf32(__uint_as_float(y[i]), hi[h][i], lo[h][i]);
+                }
+            }
+            float s[NT][4] = {};
+#pragma unroll
+            for (int e = 0; e < 8; e += 2)
+#pragma unroll
+                for (int t = 0; t < NT; t++) dot8(s[t], make_uint4(hi[0][e], hi[1][e], hi[0][e + 1], hi[1][e + 1]), xl[t][e], xl[t][e + 1]);
+            if constexpr (!F16) {
+#pragma unroll
+                for (int e = 0; e < 8; e += 2)
+#pragma unroll
+                    for (int t = 0; t < NT; t++)
+                        dot8(s[t], make_uint4(lo[0][e], lo[1][e], lo[0][e + 1], lo[1][e + 1]), xh[t][e], xh[t][e + 1]);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; e += 2)
+#pragma unroll
+                for (int t = 0; t < NT; t++) dot8(s[t], make_uint4(hi[0][e], hi[1][e], hi[0][e + 1], hi[1][e + 1]), xh[t][e], xh[t][e + 1]);
+#pragma unroll
+            for (int t = 0; t < NT; t++) add4(acc[m][t], s[t]);
+        }
+        if (ahead < k1) fetch(ahead, slot);
+        copy_commit();
+        slot = slot + 1 == NST ? 0 : slot + 1;
+    }
+    copy_wait<0>();
+    __syncthreads();  // (the sums take the rings' place)
 #pragma unroll
     for (int m = 0; m < MT; m++)
 #pragma unroll
@@ -229,18 +249,18 @@ __device__ __forceinline__ void shrink_tile(const LoraArgs& a, const int* row, i
 }
 
 template <bool F16, int MT>
-__global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(LoraArgs a, int max_tiles, int sms) {
-    constexpr int RR = 16 * MT, PAD = kLoraTile + 2;
-    extern __shared__ __align__(16) float sm_sum[];  // [warps][RR][PAD]
+__global__ void __launch_bounds__(kThreads, 1) lora_shrink_kernel(LoraArgs a, int max_tiles, int sms) {
+    constexpr int RR = 16 * MT, PAD = kLoraTile + 2, es = F16 ? 2 : 4;
+    static_assert(kWarps * RR * PAD * 4 <= kWarps * kRing, "the sums fit the rings");
+    extern __shared__ __align__(16) float sm_sum[];  // the warps' rings, then [warps][RR][PAD]
     __shared__ int sm_row[kLoraTile];
-    const int tid = threadIdx.x, lane = tid & 31, c = lane & 3, j = lane >> 2;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = lane & 3, j = lane >> 2;
     const int* plan = (const int*)a.plan;
     pdl_launch_dependents();
     pdl_wait();
     const int4 head = __ldcg(reinterpret_cast<const int4*>(plan));
     const int tiles = head.y, rows = head.z, rt = (a.rank + RR - 1) / RR;
     const int splits = lora_splits(tiles * rt, a.K, sms), chunks = a.K / 32;
-    const size_t es = F16 ? 2 : 4;
     for (int item = blockIdx.x; item < tiles * rt * splits; item += gridDim.x) {
         const int split = item % splits, rest = item / splits, r0 = rest % rt * RR;
         const int4 tile = __ldcg(reinterpret_cast<const int4*>(plan) + 1 + rest / rt);
@@ -248,12 +268,13 @@ __global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(LoraArgs a, in
         if (tid < tile.z) sm_row[tid] = __ldcg(plan + plan_order(max_tiles) + tile.y + tid);
         const int rank = rank_of(a, tile.x);
         __syncthreads();
-        const uint8_t* wp = (const uint8_t*)a.a + ((int64_t)tile.x * a.rank + r0 + j) * a.K * es + 8 * c * es;
+        const uint8_t* wp = (const uint8_t*)a.a + (((int64_t)tile.x * a.rank + r0 + j) * a.K + 8 * c) * es;
         const int c0 = (int)((int64_t)chunks * split / splits), c1 = (int)((int64_t)chunks * (split + 1) / splits);
+        const uint32_t ring = smem_u32(sm_sum) + warp * kRing;
         if (tile.z <= 8)
-            shrink_tile<F16, MT, 1, F16 && MT == 1 ? 4 : 2>(a, sm_row, tile.z, wp, rank - r0 - j, c0, c1, sm_sum, PAD);
+            shrink_tile<F16, MT, 1>(a, sm_row, tile.z, wp, rank - r0 - j, c0, c1, ring, sm_sum, PAD);
         else
-            shrink_tile<F16, MT, 4, 1>(a, sm_row, tile.z, wp, rank - r0 - j, c0, c1, sm_sum, PAD);
+            shrink_tile<F16, MT, 4>(a, sm_row, tile.z, wp, rank - r0 - j, c0, c1, ring, sm_sum, PAD);
         __syncthreads();
         for (int i = tid; i < RR * tile.z; i += kThreads) {
             const int r = i % RR, row = i / RR;
@@ -267,77 +288,92 @@ __global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(LoraArgs a, in
 
 // ---------------------------------------------------------------- expand
 
-// 2 V values of a row of B from p on, as tf32 parts.  left: how many of them the adapter's rank has.
+// 2 V values of a row of B from shared memory, as tf32 parts (lo only of fp32 weights).  left: how many the adapter's rank has.
 template <bool F16, int V>
-struct WeightsV {
-    static constexpr int W = F16 ? V : 2 * V;  // words
+__device__ __forceinline__ void weights(uint32_t at, int left, uint32_t (&hi)[2 * V], uint32_t (&lo)[2 * V]) {
+    constexpr int W = F16 ? V : 2 * V;  // words
     uint32_t w[W];
-    __device__ __forceinline__ void load(const void* p, bool in) {
-        const uint32_t* q = reinterpret_cast<const uint32_t*>(p);
-        if constexpr (W >= 4) {
+    if constexpr (W >= 4) {
 #pragma unroll
-            for (int i = 0; i < W; i += 4) {
-                const uint4 x = in ? __ldcg(reinterpret_cast<const uint4*>(q + i)) : make_uint4(0u, 0u, 0u, 0u);
-                w[i] = x.x, w[i + 1] = x.y, w[i + 2] = x.z, w[i + 3] = x.w;
-            }
-        } else if constexpr (W == 2) {
-            const uint2 x = in ? __ldcg(reinterpret_cast<const uint2*>(q)) : make_uint2(0u, 0u);
-            w[0] = x.x, w[1] = x.y;
-        } else {
-            w[0] = in ? __ldcg(q) : 0u;
+        for (int i = 0; i < W; i += 4) {
+            const uint4 x = shared16(at + 4 * i);
+            w[i] = x.x, w[i + 1] = x.y, w[i + 2] = x.z, w[i + 3] = x.w;
         }
+    } else if constexpr (W == 2) {
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
+    } else {
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(at));
     }
-    __device__ __forceinline__ void parts(uint32_t (&hi)[2 * V], uint32_t (&lo)[2 * V], int left) const {
 #pragma unroll
-        for (int i = 0; i < 2 * V; i++) {
-            float f;
-            if constexpr (F16)
-                f = __half2float(__ushort_as_half((unsigned short)(w[i / 2] >> (16 * (i & 1)))));
-            else
-                f = __uint_as_float(w[i]);
-            if (i >= left) f = 0.f;
-            if (F16)
-                hi[i] = __float_as_uint(f);
-            else
-                cut_tf32(f, hi[i], lo[i]);
-        }
+    for (int i = 0; i < 2 * V; i++) {
+        float f;
+        if constexpr (F16)
+            f = __half2float(__ushort_as_half((unsigned short)(w[i / 2] >> (16 * (i & 1)))));
+        else
+            f = __uint_as_float(w[i]);
+        if (i >= left) f = 0.f;
+        if (F16)
+            hi[i] = __float_as_uint(f);
+        else
+            cut_tf32(f, hi[i], lo[i]);
     }
-};
+}
 
-// V: units of 8 ranks whose values a lane loads at once.  VEC: columns and rows allow 16-byte pieces.
-// Block (x, y) takes runs of kCols columns of tile y: `runs` of them from x runs on.  The next run's base and the next weights
-// are on their way while this run's products are formed.
-template <bool F16, int V, bool VEC>
-__global__ void __launch_bounds__(kThreads, 2) lora_expand_kernel(LoraArgs a, int max_tiles, int sms, int rr, int runs) {
-    extern __shared__ __align__(16) uint4 sm_h[];  // [steps][2 row tiles][hi, lo][32 lanes]
+// V: units of 8 ranks whose values a lane takes at once.  VEC: columns and rows allow 16-byte pieces.  NST: runs of 128 columns
+// (16 of a warp) whose base and weights are on their way, in the warp's ring: a lane's own pieces of base, then the 16
+// columns' rows of B as they lie in memory.
+// A CTA takes an equal share of all (tile, run of columns), of one tile after another.
+template <bool F16, int V, bool VEC, int NST>
+__global__ void __launch_bounds__(kThreads, NST == 2 ? 1 : 2) lora_expand_kernel(LoraArgs a, int max_tiles, int sms, int rr) {
+    extern __shared__ __align__(16) uint4 sm_h[];  // [steps][2 row tiles][hi, lo][32 lanes], then the rings
     __shared__ int sm_row[kLoraTile];
-    constexpr size_t es = F16 ? 2 : 4;
+    constexpr int es = F16 ? 2 : 4;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = lane & 3, j = lane >> 2;
+    const int row_bytes = a.rank * es, stage = (VEC ? 2048 : 0) + 16 * row_bytes, steps = (a.rank + 8 * V - 1) / (8 * V) * V;
+    const uint32_t ring = smem_u32(sm_h) + steps * 2 * 64 * 16 + warp * NST * stage;
     const int* plan = (const int*)a.plan;
     pdl_launch_dependents();
     pdl_wait();
-    const int4 head = __ldcg(reinterpret_cast<const int4*>(plan)), tile = __ldcg(reinterpret_cast<const int4*>(plan) + 1 + blockIdx.y);
-    if ((int)blockIdx.y >= head.x || (tile.x < 0 && a.base == a.y)) return;  // (in place, rows without an adapter stay)
-    const int rank = tile.x < 0 ? 0 : rank_of(a, tile.x);
-    const int groups = (rank + 8 * V - 1) / (8 * V), mt = tile.z > 16 ? 2 : 1;
-    const int end = min(a.N, (int)(blockIdx.x + 1) * runs * kCols);
-    int n0 = blockIdx.x * runs * kCols + 16 * warp;
-    // column j of tile t is n0 + 4 (j / 2) + 2 t + j % 2, so that a lane's columns of both tiles are four neighbours
-    WeightsV<F16, V> w[2];
-    auto load_w = [&](int n, int g) {
+    const int4 head = __ldcg(reinterpret_cast<const int4*>(plan));
+    const int tiles = a.base && a.base == a.y ? head.y : head.x;  // in place, rows without an adapter stay as they are
+    const int rows = head.z, splits = lora_splits(head.y * ((a.rank + rr - 1) / rr), a.K, sms), cols = (a.N + kCols - 1) / kCols;
+    const int64_t items = (int64_t)tiles * cols, last = items * (blockIdx.x + 1) / gridDim.x;
+    for (int64_t item = items * blockIdx.x / gridDim.x; item < last;) {
+        const int which = (int)(item / cols), run0 = (int)(item - (int64_t)which * cols), run1 = (int)min((int64_t)cols, run0 + (last - item));
+        item += run1 - run0;
+        const int4 tile = __ldcg(reinterpret_cast<const int4*>(plan) + 1 + which);
+        __syncthreads();  // (the previous tile's rows and operands have been read)
+        if (tid < tile.z) sm_row[tid] = __ldcg(plan + plan_order(max_tiles) + tile.y + tid);
+        const int rank = tile.x < 0 ? 0 : rank_of(a, tile.x);
+        const float scale = tile.x >= 0 && a.scale ? __ldcg(a.scale + tile.x) : 1.f;
+        const int groups = (rank + 8 * V - 1) / (8 * V), mt = tile.z > 16 ? 2 : 1, rank_bytes = rank * es;
+        __syncthreads();
+        int64_t at[4];  // rows j + 8 i
 #pragma unroll
-        for (int t = 0; t < 2; t++) {
-            const int col = n + 4 * (j >> 1) + 2 * t + (j & 1);
-            const bool in = g < groups && col < end;
-            w[t].load((const uint8_t*)a.b + (((int64_t)tile.x * a.N + (in ? col : 0)) * a.rank + 8 * V * g + 2 * V * c) * es, in);
+        for (int i = 0; i < 4; i++) at[i] = 8 * i + j < tile.z ? sm_row[8 * i + j] : -1;
+        auto fetch = [&](int run, int slot) {
+            const uint32_t dst = ring + slot * stage;
+            const int n0 = run * kCols + 16 * warp, n = n0 + 4 * c;
+            if (VEC && a.base)
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    if (at[i] >= 0 && n < a.N) copy16(dst + i * 512 + lane * 16, a.base + at[i] * a.ldb + n, 16);
+            if (rank) {
+                const uint8_t* src = (const uint8_t*)a.b + ((int64_t)tile.x * a.N + n0) * row_bytes;
+                for (int x = lane * 16; x < 16 * row_bytes; x += 512) {
+                    const int col = x / row_bytes;
+                    const bool in = n0 + col < a.N && x - col * row_bytes < rank_bytes;
+                    copy16(dst + (VEC ? 2048 : 0) + x, in ? src + x : (const uint8_t*)a.b, in ? 16 : 0);
+                }
+            }
+        };
+#pragma unroll 1
+        for (int i = 0; i < NST; i++) {
+            if (run0 + i < run1) fetch(run0 + i, i);
+            copy_commit();
         }
-    };
-    if (groups) load_w(n0, 0);
-    if (tid < tile.z) sm_row[tid] = __ldcg(plan + plan_order(max_tiles) + tile.y + tid);
-    // h as operands: value i of lane cc's 2 V in group g is rank 8 V g + 2 V cc + i
-    if (groups) {
-        const float scale = a.scale ? __ldcg(a.scale + tile.x) : 1.f;
-        const int rows = head.z, splits = lora_splits(head.y * ((a.rank + rr - 1) / rr), a.K, sms), held = groups * 8 * V;
+        // h as operands: value i of lane cc's 2 V in group g is rank 8 V g + 2 V cc + i
+        const int held = groups * 8 * V;
         const int64_t stride = (int64_t)rows * a.rank;
         for (int i = tid; i < held * 16 * mt; i += kThreads) {
             const int row = i / held, r = i - row * held;
@@ -356,81 +392,65 @@ __global__ void __launch_bounds__(kThreads, 2) lora_expand_kernel(LoraArgs a, in
             dst[0] = hi;
             dst[32 * 4] = lo;
         }
-    }
-    __syncthreads();
-    // base: rows j + 8 i, columns n0 + 4 c ..
-    int64_t at[4];
-#pragma unroll
-    for (int i = 0; i < 4; i++) at[i] = 8 * i + j < tile.z ? sm_row[8 * i + j] : -1;
-    float4 y[4];
-    auto load_base = [&](int n) {
-        n += 4 * c;
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (!a.base || at[i] < 0 || n >= end) continue;
-            const float* p = a.base + at[i] * a.ldb + n;
-            if (VEC) {
-                y[i] = ldcg4(p);
-            } else {
-                y[i].x = __ldcg(p);
-                if (n + 1 < end) y[i].y = __ldcg(p + 1);
-                if (n + 2 < end) y[i].z = __ldcg(p + 2);
-                if (n + 3 < end) y[i].w = __ldcg(p + 3);
-            }
-        }
-    };
-    load_base(n0);
+        __syncthreads();
+        int slot = 0;
 #pragma unroll 1
-    for (; n0 < end; n0 += kCols) {
-        float4 z[4];
-#pragma unroll
-        for (int i = 0; i < 4; i++) z[i] = y[i];
-        if (n0 + kCols < end) load_base(n0 + kCols);
-        float acc[2][2][4] = {};
+        for (int run = run0; run < run1; run++) {
+            copy_wait<NST - 1>();
+            __syncwarp();  // the other lanes' pieces of B have landed
+            const uint32_t st = ring + slot * stage;
+            // column j of tile t is n0 + 4 (j / 2) + 2 t + j % 2, so that a lane's columns of both tiles are four neighbours
+            const uint32_t wb = st + (VEC ? 2048 : 0) + (4 * (j >> 1) + (j & 1)) * row_bytes + 2 * V * c * es;
+            float acc[2][2][4] = {};
 #pragma unroll 1
-        for (int g = 0; g < groups; g++) {
-            uint32_t hi[2][2 * V], lo[2][2 * V];
+            for (int g = 0; g < groups; g++) {
+                uint32_t hi[2][2 * V], lo[2][2 * V];
 #pragma unroll
-            for (int t = 0; t < 2; t++) w[t].parts(hi[t], lo[t], rank - (8 * V * g + 2 * V * c));
-            if (g + 1 < groups)
-                load_w(n0, g + 1);
-            else if (n0 + kCols < end)
-                load_w(n0 + kCols, 0);
-#pragma unroll
-            for (int m = 0; m < 2; m++) {
-                if (m >= mt) break;
-                float sum[2][4] = {};
+                for (int t = 0; t < 2; t++) weights<F16, V>(wb + 2 * t * row_bytes + g * 8 * V * es, rank - (8 * V * g + 2 * V * c), hi[t], lo[t]);
+                float sum[2][2][4] = {};
 #pragma unroll
                 for (int part = 1; part >= 0; part--)
 #pragma unroll
-                    for (int e = 0; e < V; e++) {
-                        const uint4 h = sm_h[((g * V + e) * 2 + m) * 64 + part * 32 + lane];
+                    for (int e = 0; e < V; e++)
 #pragma unroll
-                        for (int t = 0; t < 2; t++) {
-                            if (!F16 && part == 0) mma8(sum[t], h, lo[t][2 * e], lo[t][2 * e + 1]);
-                            mma8(sum[t], h, hi[t][2 * e], hi[t][2 * e + 1]);
+                        for (int m = 0; m < 2; m++) {
+                            if (m >= mt) break;
+                            const uint4 h = sm_h[((g * V + e) * 2 + m) * 64 + part * 32 + lane];
+#pragma unroll
+                            for (int t = 0; t < 2; t++) {
+                                if (!F16 && part == 0) dot8(sum[m][t], h, lo[t][2 * e], lo[t][2 * e + 1]);
+                                dot8(sum[m][t], h, hi[t][2 * e], hi[t][2 * e + 1]);
+                            }
                         }
+#pragma unroll
+                for (int m = 0; m < 2; m++)
+#pragma unroll
+                    for (int t = 0; t < 2; t++) add4(acc[m][t], sum[m][t]);
+            }
+            const int n = run * kCols + 16 * warp + 4 * c;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                if (at[i] < 0 || n >= a.N) continue;
+                const int m = i / 2, h = 2 * (i & 1);
+                float4 v = make_float4(acc[m][0][h], acc[m][0][h + 1], acc[m][1][h], acc[m][1][h + 1]);
+                float* p = a.y + at[i] * a.ldy + n;
+                if (VEC) {
+                    if (a.base) {
+                        const uint4 z = shared16(st + i * 512 + lane * 16);
+                        v.x += __uint_as_float(z.x), v.y += __uint_as_float(z.y), v.z += __uint_as_float(z.z), v.w += __uint_as_float(z.w);
                     }
+                    *reinterpret_cast<float4*>(p) = v;
+                } else {
+                    const float x[4] = {v.x, v.y, v.z, v.w}, *q = a.base + at[i] * a.ldb + n;
 #pragma unroll
-                for (int t = 0; t < 2; t++) add4(acc[m][t], sum[t]);
+                    for (int k = 0; k < 4; k++)
+                        if (n + k < a.N) p[k] = a.base ? __ldcg(q + k) + x[k] : x[k];
+                }
             }
-        }
-        const int n = n0 + 4 * c;
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            if (at[i] < 0 || n >= end) continue;
-            const int m = i / 2, h = 2 * (i & 1);
-            float* p = a.y + at[i] * a.ldy + n;
-            const float4 v = make_float4(z[i].x + acc[m][0][h], z[i].y + acc[m][0][h + 1], z[i].z + acc[m][1][h], z[i].w + acc[m][1][h + 1]);
-            if (VEC) {
-                *reinterpret_cast<float4*>(p) = v;
-            } else {
-                p[0] = v.x;
-                if (n + 1 < end) p[1] = v.y;
-                if (n + 2 < end) p[2] = v.z;
-                if (n + 3 < end) p[3] = v.w;
-            }
+            __syncwarp();
+            if (run + NST < run1) fetch(run + NST, slot);
+            copy_commit();
+            slot = slot + 1 == NST ? 0 : slot + 1;
         }
     }
 }
@@ -440,22 +460,30 @@ int shrink_ranks(int rank) { return rank <= 16 ? 16 : 32; }
 
 template <bool F16, int MT>
 cudaError_t shrink(const LoraArgs& a, int max_tiles, cudaStream_t s) {
-    constexpr int smem = kWarps * 16 * MT * (kLoraTile + 2) * 4;
     auto k = lora_shrink_kernel<F16, MT>;
     static SmemOptIn opt;
-    if (cudaError_t e = opt((const void*)k, smem)) return e;
-    return launch_chained(k, dim3(2 * num_sms()), kThreads, smem, s, a, max_tiles, num_sms());
+    if (cudaError_t e = opt((const void*)k, kWarps * kRing)) return e;
+    return launch_chained(k, dim3(num_sms()), kThreads, kWarps * kRing, s, a, max_tiles, num_sms());
 }
 
+template <bool F16, int V, bool VEC, int NST>
+cudaError_t expand_go(const LoraArgs& a, int max_tiles, int smem, cudaStream_t s) {
+    auto k = lora_expand_kernel<F16, V, VEC, NST>;
+    static SmemOptIn opt;
+    if (cudaError_t e = opt((const void*)k, NST == 2 ? 220 * 1024 : 112 * 1024)) return e;
+    return launch_chained(k, dim3((NST == 2 ? 1 : 2) * num_sms()), kThreads, smem, s, a, max_tiles, num_sms(), shrink_ranks(a.rank));
+}
+
+// Four runs on their way where two CTAs' rings fit an SM; two of one CTA's fit for every rank (128 fp32: 192 KB).
+template <bool F16, int V, bool VEC>
+cudaError_t expand(const LoraArgs& a, int max_tiles, cudaStream_t s) {
+    const int operands = (a.rank + 8 * V - 1) / (8 * V) * V * 2 * 64 * 16, stage = (VEC ? 2048 : 0) + 16 * a.rank * (F16 ? 2 : 4);
+    if (operands + 4 * kWarps * stage <= 112 * 1024) return expand_go<F16, V, VEC, 4>(a, max_tiles, operands + 4 * kWarps * stage, s);
+    return expand_go<F16, V, VEC, 2>(a, max_tiles, operands + 2 * kWarps * stage, s);
+}
 template <bool F16, int V>
 cudaError_t expand(const LoraArgs& a, int max_tiles, bool vec, cudaStream_t s) {
-    const int smem = (a.rank + 8 * V - 1) / (8 * V) * V * 2 * 64 * 16;  // at most 32 KB
-    // runs of columns for a CTA: four where that leaves two CTAs for every SM
-    const int64_t cols = (a.N + kCols - 1) / kCols;
-    const int runs = (cols + 3) / 4 * ((a.n + kLoraTile - 1) / kLoraTile) >= 2 * num_sms() ? 4 : 1;
-    const dim3 grid((unsigned)((cols + runs - 1) / runs), max_tiles);
-    auto go = [&](auto k) { return launch_chained(k, grid, kThreads, smem, s, a, max_tiles, num_sms(), shrink_ranks(a.rank), runs); };
-    return vec ? go(lora_expand_kernel<F16, V, true>) : go(lora_expand_kernel<F16, V, false>);
+    return vec ? expand<F16, V, true>(a, max_tiles, s) : expand<F16, V, false>(a, max_tiles, s);
 }
 
 template <bool F16>
@@ -477,9 +505,9 @@ cudaError_t launch_lora_plan(const int* ids, int n, int adapters, void* plan, cu
     return launch_chained(lora_plan_kernel, dim3(1), kPlanThreads, 0, s, ids, n, adapters, lora_max_tiles(n, adapters), (int*)plan);
 }
 
-// A range's sums of every row.  With t tiles there are at most 2 SMs / t ranges, or one, and at most 32 t rows.
+// A range's sums of every row.  With t tiles there are at most SMs / t ranges, or one, and at most 32 t rows.
 size_t lora_ws_bytes(int n, int rank) {
-    return (size_t)std::min<int64_t>((int64_t)kMaxSplit * n, 2 * (int64_t)num_sms() * kLoraTile + n) * rank * sizeof(float);
+    return (size_t)std::min<int64_t>((int64_t)kMaxSplit * n, (int64_t)num_sms() * kLoraTile + n) * rank * sizeof(float);
 }
 
 cudaError_t launch_lora(const LoraArgs& a, cudaStream_t s) { return a.f16 ? lora<true>(a, s) : lora<false>(a, s); }
