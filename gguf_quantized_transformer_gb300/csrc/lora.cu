@@ -9,9 +9,11 @@
 //  - expand: y = base + B (scale h).  A CTA takes a tile and runs of 128 columns; h's parts lie in shared memory as operands,
 //    a warp's 16 columns of B come straight into operands, and y is moved in 16-byte pieces.
 // Bound by the bytes of base, y and x for many rows, by those of the weights for few, and by two launches for one.
-// Precision: tf32 products of parts.  fp16 weights are tf32 numbers; x, h and fp32 weights are cut into two parts of 11 bits
-// (x = hi + lo to 2^-22), and the product of two lo parts is left out.  Tensor cores cut their sums: those of a chunk start
-// from zero, small products first, and are added in fp32.
+// Precision: fp16 products of two parts of 11 bits (x, h and fp32 weights; fp16 weights are operands as they are), after a power
+// of two has brought the largest of a row's 32 values (of a chunk; of h all) to [2^13, 2^14), which leaves the low part 24
+// bits below fp16's smallest normal number: 2^-22 of a value, 2^-38 of the largest.  The product of two low parts is left
+// out.  Tensor cores cut their sums: those of a chunk start from zero, small products first, and are added in fp32.  (tf32
+// needs no scaling, but mma.sync does 128 of its multiplications a cycle and SM.)
 #include <algorithm>
 
 #include "mma_sync.cuh"
@@ -23,7 +25,8 @@ namespace af {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 256, kWarps = kThreads / 32;  // of expand
+constexpr int kShrinkWarps = 12;
 constexpr int kMaxSplit = 16;
 constexpr int kCols = 16 * kWarps;  // columns that a CTA of expand takes at once
 
@@ -131,107 +134,149 @@ __device__ __forceinline__ uint4 shared16(uint32_t a) {
     return v;
 }
 
+// Tile i; the first 32, a lane each, come with the header
+__device__ __forceinline__ int4 first_tiles(const int* plan, int lane, int max_tiles) {
+    return __ldcg(reinterpret_cast<const int4*>(plan) + 1 + min(lane, max_tiles - 1));
+}
+__device__ __forceinline__ int4 tile_of(const int* plan, int i, const int4& early) {
+    if (i >= 32) return __ldcg(reinterpret_cast<const int4*>(plan) + 1 + i);
+    return make_int4(__shfl_sync(0xffffffffu, early.x, i), __shfl_sync(0xffffffffu, early.y, i), __shfl_sync(0xffffffffu, early.z, i), 0);
+}
+
 __device__ __forceinline__ int rank_of(const LoraArgs& a, int adapter) {
     return a.ranks ? min(max(__ldcg(a.ranks + adapter), 0), a.rank) : a.rank;
 }
 
 // ---------------------------------------------------------------- shrink
 
-// Ranges of K: as many as every SM takes one of at once, of at least 8 chunks of 32
+// Ranges of K: as many as every SM takes one of at once, of at least a chunk of 32 for each warp
 __device__ __forceinline__ int lora_splits(int items, int K, int sms) {
-    return max(1, min(min(sms / max(items, 1), kMaxSplit), K / 32 / kWarps));
+    return max(1, min(min(sms / max(items, 1), kMaxSplit), K / 32 / kShrinkWarps));
 }
 
-constexpr int kRing = 24 * 1024;  // of a warp of shrink
+constexpr int kRing = 16 * 1024;  // of a warp of shrink
 
-// The sums of chunks k0 + warp, + kWarps .. below k1 for 16 MT ranks and 8 NT rows, in `sum`: [warps][16 MT][pad].  Weights and
-// x go through a ring in which every lane has places of its own, so that no lane waits for another.
-// wp: this lane's weights of rank j; in: the ranks that there are, from j on.
-template <bool F16, int MT, int NT>
-__device__ __forceinline__ void shrink_tile(const LoraArgs& a, const int* row, int count, const uint8_t* wp, int in, int k0, int k1,
-                                            uint32_t ring, float* sum, int pad) {
-    constexpr int WC = F16 ? 1 : 2, COPIES = 2 * MT * WC + 2 * NT, STAGE = COPIES * 512, NST = kRing / STAGE < 8 ? kRing / STAGE : 8;
-    constexpr int es = F16 ? 2 : 4;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 3, j = lane >> 2;
-    const float* xp[NT];
+// 2^k that brings a largest magnitude m to [2^13, 2^14), and 2^-k.  (Below 2^-112 it comes no nearer; infinities and NaNs
+// stay what they are.)
+__device__ __forceinline__ void powers(float m, float& down, float& up) {
+    int e = (int)(__float_as_uint(m) >> 23) - 127;
+    e = min(max(e, -112), 127);
+    down = __uint_as_float((unsigned)(127 + 13 - e) << 23);
+    up = __uint_as_float((unsigned)(127 - 13 + e) << 23);
+}
+// 8 values of lanes c = 0..3 (32 of one row) as scaled parts, in pairs; the power that takes the sums back
+__device__ __forceinline__ float parts8(const uint4& v, const uint4& w, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+    float x[8] = {__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w),
+                  __uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w)};
+    float m = 0.f, down, up;
 #pragma unroll
-    for (int t = 0; t < NT; t++) xp[t] = a.x + (8 * t + j < count ? (int64_t)row[8 * t + j] * a.ldx : 0) + 8 * c;
-    ring += lane * 16;
+    for (int i = 0; i < 8; i++) m = fmaxf(m, fabsf(x[i]));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    powers(m, down, up);
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const float2 y = mul2(make_float2(x[2 * i], x[2 * i + 1]), both(down));
+        split_h2(y.x, y.y, hi[i], lo[i]);
+    }
+    return up;
+}
+
+// The sums of chunks k0 + warp, + kShrinkWarps .. below k1 for 16 MT ranks and 8 NT rows, in `sum`: [warps][16 MT][pad].
+// Weights and x go through the warp's ring, whole lines of 128 bytes a row (64 of fp16 weights); in it odd rows have
+// neighbouring 16-byte pieces exchanged, so that the reads meet all banks.
+// w: the adapter's weights from the tile's first rank on; in: the ranks that there are from it on.
+template <bool F16, int MT, int NT>
+__device__ __forceinline__ void shrink_tile(const LoraArgs& a, const int* row, int count, const uint8_t* w, int in, int k0, int k1,
+                                            uint32_t ring, float* sum, int pad) {
+    constexpr int WB = 16 * MT * (F16 ? 64 : 128), STAGE = WB + 8 * NT * 128, NST = kRing / STAGE < 8 ? kRing / STAGE : 8;
+    static_assert(NST >= 2, "a stage in flight while one is read");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 3, j = lane >> 2, q = lane >> 3, e16 = lane & 7;
     auto fetch = [&](int k, int slot) {
         const uint32_t dst = ring + slot * STAGE;
+        if constexpr (F16) {
 #pragma unroll
-        for (int i = 0; i < 2 * MT; i++) {
-            const bool is = 8 * i < in;
-            const uint8_t* p = is ? wp + ((int64_t)8 * i * a.K + 32 * k) * es : (const uint8_t*)a.a;
+            for (int i = 0; i < 2 * MT; i++) {
+                const bool is = 8 * i + j < in;
+                copy16(dst + i * 512 + lane * 16, is ? w + ((int64_t)(8 * i + j) * a.K + 32 * k + 8 * c) * 2 : (const uint8_t*)a.a, is ? 16 : 0);
+            }
+        } else {
 #pragma unroll
-            for (int h = 0; h < WC; h++) copy16(dst + (i * WC + h) * 512, p + 16 * h, is ? 16 : 0);
+            for (int i = 0; i < 4 * MT; i++) {
+                const bool is = 4 * i + q < in;
+                copy16(dst + (4 * i + q) * 128 + ((e16 ^ (q & 1)) << 4),
+                       is ? w + ((int64_t)(4 * i + q) * a.K + 32 * k + 4 * e16) * 4 : (const uint8_t*)a.a, is ? 16 : 0);
+            }
         }
 #pragma unroll
-        for (int t = 0; t < NT; t++) {
-            const int bytes = 8 * t + j < count ? 16 : 0;
-#pragma unroll
-            for (int h = 0; h < 2; h++) copy16(dst + (2 * MT * WC + 2 * t + h) * 512, xp[t] + 32 * k + 4 * h, bytes);
+        for (int i = 0; i < 2 * NT; i++) {
+            const int r = 4 * i + q;
+            const float* p = a.x + (r < count ? (int64_t)row[r] * a.ldx : 0) + 32 * k + 4 * e16;
+            copy16(dst + WB + r * 128 + ((e16 ^ (q & 1)) << 4), p, r < count ? 16 : 0);
         }
     };
+    // half h of the 8 values of row j of eight that lie in lines of 128 bytes
+    auto line8 = [&](uint32_t at, int h) { return shared16(at + j * 128 + (((2 * c + h) ^ (j & 1)) << 4)); };
     float acc[MT][NT][4] = {};
     int ahead = k0 + warp;
 #pragma unroll 1
-    for (int i = 0; i < NST; i++, ahead += kWarps) {
+    for (int i = 0; i < NST; i++, ahead += kShrinkWarps) {
         if (ahead < k1) fetch(ahead, i);
         copy_commit();
     }
     int slot = 0;
 #pragma unroll 1
-    for (int k = k0 + warp; k < k1; k += kWarps, ahead += kWarps) {
+    for (int k = k0 + warp; k < k1; k += kShrinkWarps, ahead += kShrinkWarps) {
         copy_wait<NST - 1>();
+        __syncwarp();  // the other lanes' pieces have landed
         const uint32_t at = ring + slot * STAGE;
-        uint32_t xh[NT][8], xl[NT][8];
+        uint32_t xh[NT][4], xl[NT][4];
+        float2 up[NT];  // of rows 2c and 2c + 1 of each 8
 #pragma unroll
         for (int t = 0; t < NT; t++) {
-            const uint4 v = shared16(at + (2 * MT * WC + 2 * t) * 512), w = shared16(at + (2 * MT * WC + 2 * t + 1) * 512);
-            const uint32_t y[8] = {v.x, v.y, v.z, v.w, w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int i = 0; i < 8; i++) cut_tf32(__uint_as_float(y[i]), xh[t][i], xl[t][i]);
+            const float u = parts8(line8(at + WB + 1024 * t, 0), line8(at + WB + 1024 * t, 1), xh[t], xl[t]);
+            up[t] = make_float2(__shfl_sync(0xffffffffu, u, 8 * c), __shfl_sync(0xffffffffu, u, 8 * c + 4));
         }
 #pragma unroll
         for (int m = 0; m < MT; m++) {
-            uint32_t hi[2][8], lo[2][8];
+            uint32_t hi[2][4], lo[2][4];
+            float wup[2] = {1.f, 1.f};
 #pragma unroll
             for (int h = 0; h < 2; h++) {
                 if constexpr (F16) {
-                    const uint4 v = shared16(at + (2 * m + h) * 512);
-                    const uint32_t y[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&y[i]));
-                        hi[h][2 * i] = __float_as_uint(f.x), hi[h][2 * i + 1] = __float_as_uint(f.y);
-                    }
+                    const uint4 v = shared16(at + (2 * m + h) * 512 + lane * 16);
+                    hi[h][0] = v.x, hi[h][1] = v.y, hi[h][2] = v.z, hi[h][3] = v.w;
                 } else {
-                    const uint4 v = shared16(at + (4 * m + 2 * h) * 512), w = shared16(at + (4 * m + 2 * h + 1) * 512);
-                    const uint32_t y[8] = {v.x, v.y, v.z, v.w, w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int i = 0; i < 8; i++) cut_tf32(__uint_as_float(y[i]), hi[h][i], lo[h][i]);
+                    wup[h] = parts8(line8(at + 1024 * (2 * m + h), 0), line8(at + 1024 * (2 * m + h), 1), hi[h], lo[h]);
                 }
             }
-            float s[NT][4] = {};
+            float s[NT][4];
 #pragma unroll
-            for (int e = 0; e < 8; e += 2)
+            for (int t = 0; t < NT; t++) dot16z(s[t], make_uint4(hi[0][0], hi[1][0], hi[0][1], hi[1][1]), xl[t][0], xl[t][1]);
 #pragma unroll
-                for (int t = 0; t < NT; t++) dot8(s[t], make_uint4(hi[0][e], hi[1][e], hi[0][e + 1], hi[1][e + 1]), xl[t][e], xl[t][e + 1]);
+            for (int t = 0; t < NT; t++) dot16(s[t], make_uint4(hi[0][2], hi[1][2], hi[0][3], hi[1][3]), xl[t][2], xl[t][3]);
             if constexpr (!F16) {
 #pragma unroll
-                for (int e = 0; e < 8; e += 2)
+                for (int e = 0; e < 4; e += 2)
 #pragma unroll
                     for (int t = 0; t < NT; t++)
-                        dot8(s[t], make_uint4(lo[0][e], lo[1][e], lo[0][e + 1], lo[1][e + 1]), xh[t][e], xh[t][e + 1]);
+                        dot16(s[t], make_uint4(lo[0][e], lo[1][e], lo[0][e + 1], lo[1][e + 1]), xh[t][e], xh[t][e + 1]);
             }
 #pragma unroll
-            for (int e = 0; e < 8; e += 2)
+            for (int e = 0; e < 4; e += 2)
 #pragma unroll
-                for (int t = 0; t < NT; t++) dot8(s[t], make_uint4(hi[0][e], hi[1][e], hi[0][e + 1], hi[1][e + 1]), xh[t][e], xh[t][e + 1]);
+                for (int t = 0; t < NT; t++) dot16(s[t], make_uint4(hi[0][e], hi[1][e], hi[0][e + 1], hi[1][e + 1]), xh[t][e], xh[t][e + 1]);
 #pragma unroll
-            for (int t = 0; t < NT; t++) add4(acc[m][t], s[t]);
+            for (int t = 0; t < NT; t++)
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    float2 v = make_float2(s[t][2 * h], s[t][2 * h + 1]);
+                    if (!F16) v = mul2(v, both(wup[h]));
+                    const float2 y = fma2(v, up[t], make_float2(acc[m][t][2 * h], acc[m][t][2 * h + 1]));
+                    acc[m][t][2 * h] = y.x, acc[m][t][2 * h + 1] = y.y;
+                }
         }
+        __syncwarp();
         if (ahead < k1) fetch(ahead, slot);
         copy_commit();
         slot = slot + 1 == NST ? 0 : slot + 1;
@@ -249,38 +294,39 @@ __device__ __forceinline__ void shrink_tile(const LoraArgs& a, const int* row, i
 }
 
 template <bool F16, int MT>
-__global__ void __launch_bounds__(kThreads, 1) lora_shrink_kernel(LoraArgs a, int max_tiles, int sms) {
+__global__ void __launch_bounds__(kShrinkWarps * 32, 1) lora_shrink_kernel(LoraArgs a, int max_tiles, int sms) {
     constexpr int RR = 16 * MT, PAD = kLoraTile + 2, es = F16 ? 2 : 4;
-    static_assert(kWarps * RR * PAD * 4 <= kWarps * kRing, "the sums fit the rings");
+    static_assert(RR * PAD * 4 <= kRing, "the sums fit the rings");
     extern __shared__ __align__(16) float sm_sum[];  // the warps' rings, then [warps][RR][PAD]
     __shared__ int sm_row[kLoraTile];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = lane & 3, j = lane >> 2;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int* plan = (const int*)a.plan;
     pdl_launch_dependents();
     pdl_wait();
     const int4 head = __ldcg(reinterpret_cast<const int4*>(plan));
+    const int4 early = first_tiles(plan, lane, max_tiles);
     const int tiles = head.y, rows = head.z, rt = (a.rank + RR - 1) / RR;
     const int splits = lora_splits(tiles * rt, a.K, sms), chunks = a.K / 32;
     for (int item = blockIdx.x; item < tiles * rt * splits; item += gridDim.x) {
         const int split = item % splits, rest = item / splits, r0 = rest % rt * RR;
-        const int4 tile = __ldcg(reinterpret_cast<const int4*>(plan) + 1 + rest / rt);
+        const int4 tile = tile_of(plan, rest / rt, early);
         __syncthreads();  // (the previous item's sums and rows have been read)
         if (tid < tile.z) sm_row[tid] = __ldcg(plan + plan_order(max_tiles) + tile.y + tid);
         const int rank = rank_of(a, tile.x);
         __syncthreads();
-        const uint8_t* wp = (const uint8_t*)a.a + (((int64_t)tile.x * a.rank + r0 + j) * a.K + 8 * c) * es;
+        const uint8_t* w = (const uint8_t*)a.a + ((int64_t)tile.x * a.rank + r0) * a.K * es;
         const int c0 = (int)((int64_t)chunks * split / splits), c1 = (int)((int64_t)chunks * (split + 1) / splits);
         const uint32_t ring = smem_u32(sm_sum) + warp * kRing;
         if (tile.z <= 8)
-            shrink_tile<F16, MT, 1>(a, sm_row, tile.z, wp, rank - r0 - j, c0, c1, ring, sm_sum, PAD);
+            shrink_tile<F16, MT, 1>(a, sm_row, tile.z, w, rank - r0, c0, c1, ring, sm_sum, PAD);
         else
-            shrink_tile<F16, MT, 4>(a, sm_row, tile.z, wp, rank - r0 - j, c0, c1, ring, sm_sum, PAD);
+            shrink_tile<F16, MT, 4>(a, sm_row, tile.z, w, rank - r0, c0, c1, ring, sm_sum, PAD);
         __syncthreads();
-        for (int i = tid; i < RR * tile.z; i += kThreads) {
+        for (int i = tid; i < RR * tile.z; i += kShrinkWarps * 32) {
             const int r = i % RR, row = i / RR;
             float sum = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; w++) sum += sm_sum[(w * RR + r) * PAD + row];
+            for (int w = 0; w < kShrinkWarps; w++) sum += sm_sum[(w * RR + r) * PAD + row];
             if (r0 + r < a.rank) a.ws[((int64_t)split * rows + tile.y + row) * a.rank + r0 + r] = sum;
         }
     }
@@ -288,9 +334,10 @@ __global__ void __launch_bounds__(kThreads, 1) lora_shrink_kernel(LoraArgs a, in
 
 // ---------------------------------------------------------------- expand
 
-// 2 V values of a row of B from shared memory, as tf32 parts (lo only of fp32 weights).  left: how many the adapter's rank has.
+// 2 V values of a row of B from shared memory in pairs (of fp32 weights as scaled parts, of the 8 V of four lanes; the power that
+// takes sums back).  left: how many the adapter's rank has from this lane's first on.
 template <bool F16, int V>
-__device__ __forceinline__ void weights(uint32_t at, int left, uint32_t (&hi)[2 * V], uint32_t (&lo)[2 * V]) {
+__device__ __forceinline__ float weights(uint32_t at, int left, uint32_t (&hi)[V], uint32_t (&lo)[V]) {
     constexpr int W = F16 ? V : 2 * V;  // words
     uint32_t w[W];
     if constexpr (W >= 4) {
@@ -304,18 +351,23 @@ __device__ __forceinline__ void weights(uint32_t at, int left, uint32_t (&hi)[2 
     } else {
         asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(at));
     }
+    if constexpr (F16) {
 #pragma unroll
-    for (int i = 0; i < 2 * V; i++) {
-        float f;
-        if constexpr (F16)
-            f = __half2float(__ushort_as_half((unsigned short)(w[i / 2] >> (16 * (i & 1)))));
-        else
-            f = __uint_as_float(w[i]);
-        if (i >= left) f = 0.f;
-        if (F16)
-            hi[i] = __float_as_uint(f);
-        else
-            cut_tf32(f, hi[i], lo[i]);
+        for (int i = 0; i < V; i++) hi[i] = w[i] & ((2 * i < left ? 0xFFFFu : 0u) | (2 * i + 1 < left ? 0xFFFF0000u : 0u));
+        return 1.f;
+    } else {
+        float x[2 * V], m = 0.f, down, up;
+#pragma unroll
+        for (int i = 0; i < 2 * V; i++) x[i] = i < left ? __uint_as_float(w[i]) : 0.f, m = fmaxf(m, fabsf(x[i]));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        powers(m, down, up);
+#pragma unroll
+        for (int i = 0; i < V; i++) {
+            const float2 y = mul2(make_float2(x[2 * i], x[2 * i + 1]), both(down));
+            split_h2(y.x, y.y, hi[i], lo[i]);
+        }
+        return up;
     }
 }
 
@@ -327,26 +379,49 @@ template <bool F16, int V, bool VEC, int NST>
 __global__ void __launch_bounds__(kThreads, NST == 2 ? 1 : 2) lora_expand_kernel(LoraArgs a, int max_tiles, int sms, int rr) {
     extern __shared__ __align__(16) uint4 sm_h[];  // [steps][2 row tiles][hi, lo][32 lanes], then the rings
     __shared__ int sm_row[kLoraTile];
+    __shared__ float sm_up[kLoraTile];  // the powers of two that take the rows of h back
+    constexpr int SG = (V + 1) / 2;     // matrix steps of a group of 8 V ranks
+    constexpr int HQ = kLoraMaxRank / 32;
     constexpr int es = F16 ? 2 : 4;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = lane & 3, j = lane >> 2;
-    const int row_bytes = a.rank * es, stage = (VEC ? 2048 : 0) + 16 * row_bytes, steps = (a.rank + 8 * V - 1) / (8 * V) * V;
+    const int row_bytes = a.rank * es, stage = (VEC ? 2048 : 0) + 16 * row_bytes, steps = (a.rank + 8 * V - 1) / (8 * V) * SG;
     const uint32_t ring = smem_u32(sm_h) + steps * 2 * 64 * 16 + warp * NST * stage;
     const int* plan = (const int*)a.plan;
     pdl_launch_dependents();
     pdl_wait();
     const int4 head = __ldcg(reinterpret_cast<const int4*>(plan));
+    const int4 early = first_tiles(plan, lane, max_tiles);
     const int tiles = a.base && a.base == a.y ? head.y : head.x;  // in place, rows without an adapter stay as they are
     const int rows = head.z, splits = lora_splits(head.y * ((a.rank + rr - 1) / rr), a.K, sms), cols = (a.N + kCols - 1) / kCols;
     const int64_t items = (int64_t)tiles * cols, last = items * (blockIdx.x + 1) / gridDim.x;
     for (int64_t item = items * blockIdx.x / gridDim.x; item < last;) {
         const int which = (int)(item / cols), run0 = (int)(item - (int64_t)which * cols), run1 = (int)min((int64_t)cols, run0 + (last - item));
         item += run1 - run0;
-        const int4 tile = __ldcg(reinterpret_cast<const int4*>(plan) + 1 + which);
-        __syncthreads();  // (the previous tile's rows and operands have been read)
-        if (tid < tile.z) sm_row[tid] = __ldcg(plan + plan_order(max_tiles) + tile.y + tid);
+        const int4 tile = tile_of(plan, which, early);
+        // everything that depends on the tile alone, at once: its rows, rank and scale, and the warp's first row of h
+        int my_row = 0;
+        if (tid < tile.z) my_row = __ldcg(plan + plan_order(max_tiles) + tile.y + tid);
         const int rank = tile.x < 0 ? 0 : rank_of(a, tile.x);
         const float scale = tile.x >= 0 && a.scale ? __ldcg(a.scale + tile.x) : 1.f;
-        const int groups = (rank + 8 * V - 1) / (8 * V), mt = tile.z > 16 ? 2 : 1, rank_bytes = rank * es;
+        const int mt = tile.z > 16 ? 2 : 1;
+        // ranks lane, lane + 32 .. of a row of h
+        float h[HQ];
+        auto load_h = [&](int row) {
+#pragma unroll
+            for (int q = 0; q < HQ; q++) {
+                h[q] = 0.f;
+                if (32 * q >= a.rank) break;
+                if (lane + 32 * q < a.rank && row < tile.z && tile.x >= 0) {
+                    const float* p = a.ws + ((int64_t)tile.y + row) * a.rank + lane + 32 * q;
+#pragma unroll 4
+                    for (int s = 0; s < splits; s++, p += (int64_t)rows * a.rank) h[q] += __ldcg(p);
+                }
+            }
+        };
+        load_h(warp);
+        __syncthreads();  // (the previous tile's rows and operands have been read)
+        if (tid < tile.z) sm_row[tid] = my_row;
+        const int groups = (rank + 8 * V - 1) / (8 * V), rank_bytes = rank * es;
         __syncthreads();
         int64_t at[4];  // rows j + 8 i
 #pragma unroll
@@ -372,27 +447,39 @@ __global__ void __launch_bounds__(kThreads, NST == 2 ? 1 : 2) lora_expand_kernel
             if (run0 + i < run1) fetch(run0 + i, i);
             copy_commit();
         }
-        // h as operands: value i of lane cc's 2 V in group g is rank 8 V g + 2 V cc + i
+        // h as operands: value i of lane cc's 2 V in group g is rank 8 V g + 2 V cc + i, its pairs those of steps 0, 0, 1, 1
         const int held = groups * 8 * V;
-        const int64_t stride = (int64_t)rows * a.rank;
-        for (int i = tid; i < held * 16 * mt; i += kThreads) {
-            const int row = i / held, r = i - row * held;
-            float h = 0.f;
-            if (r < rank && row < tile.z) {
-                const float* p = a.ws + ((int64_t)tile.y + row) * a.rank + r;
-#pragma unroll 4
-                for (int s = 0; s < splits; s++) h += __ldcg(p + s * stride);
-                h *= scale;
+#pragma unroll 1
+        for (int row = warp; row < 16 * mt; row += kWarps) {
+            if (row != warp) load_h(row);
+            float m = 0.f, down, up;
+#pragma unroll
+            for (int q = 0; q < HQ; q++) {
+                h[q] = lane + 32 * q < rank ? h[q] * scale : 0.f;
+                m = fmaxf(m, fabsf(h[q]));
             }
-            uint32_t hi, lo;
-            cut_tf32(h, hi, lo);
-            const int g = r / (8 * V), cc = r % (8 * V) / (2 * V), k = r % (2 * V);
-            uint32_t* dst = reinterpret_cast<uint32_t*>(sm_h + ((g * V + k / 2) * 2 + row / 16) * 64 + (row & 7) * 4 + cc) +
-                            (row >> 3 & 1) + 2 * (k & 1);
-            dst[0] = hi;
-            dst[32 * 4] = lo;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            powers(m, down, up);
+            if (lane == 0) sm_up[row] = up;
+#pragma unroll
+            for (int q = 0; q < HQ; q++) {
+                const int r = lane + 32 * q;
+                if (r >= held) break;
+                uint32_t hi, lo;
+                split_h2(h[q] * down, 0.f, hi, lo);
+                const int g = r / (8 * V), cc = r % (8 * V) / (2 * V), i = r % (2 * V);
+                unsigned short* dst = reinterpret_cast<unsigned short*>(sm_h + ((g * SG + i / 4) * 2 + row / 16) * 64 + (row & 7) * 4 + cc) +
+                                      2 * (2 * (i / 2 & 1) + (row >> 3 & 1)) + (i & 1);
+                dst[0] = (unsigned short)hi;
+                dst[32 * 8] = (unsigned short)lo;
+                if (V == 1) dst[4] = dst[32 * 8 + 4] = 0;  // (the step's other pairs)
+            }
         }
         __syncthreads();
+        float up[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) up[i] = sm_up[min(8 * i, 16 * mt - 8) + j];
         int slot = 0;
 #pragma unroll 1
         for (int run = run0; run < run1; run++) {
@@ -404,35 +491,51 @@ __global__ void __launch_bounds__(kThreads, NST == 2 ? 1 : 2) lora_expand_kernel
             float acc[2][2][4] = {};
 #pragma unroll 1
             for (int g = 0; g < groups; g++) {
-                uint32_t hi[2][2 * V], lo[2][2 * V];
+                uint32_t hi[2][V], lo[2][V];
+                float2 back[2];  // of the lane's columns
 #pragma unroll
-                for (int t = 0; t < 2; t++) weights<F16, V>(wb + 2 * t * row_bytes + g * 8 * V * es, rank - (8 * V * g + 2 * V * c), hi[t], lo[t]);
+                for (int t = 0; t < 2; t++) {
+                    const float u = weights<F16, V>(wb + 2 * t * row_bytes + g * 8 * V * es, rank - (8 * V * g + 2 * V * c), hi[t], lo[t]);
+                    if (!F16) back[t] = make_float2(__shfl_sync(0xffffffffu, u, 8 * c), __shfl_sync(0xffffffffu, u, 8 * c + 4));
+                }
                 float sum[2][2][4] = {};
 #pragma unroll
                 for (int part = 1; part >= 0; part--)
 #pragma unroll
-                    for (int e = 0; e < V; e++)
+                    for (int e = 0; e < SG; e++)
 #pragma unroll
                         for (int m = 0; m < 2; m++) {
                             if (m >= mt) break;
-                            const uint4 h = sm_h[((g * V + e) * 2 + m) * 64 + part * 32 + lane];
+                            const uint4 h = sm_h[((g * SG + e) * 2 + m) * 64 + part * 32 + lane];
 #pragma unroll
                             for (int t = 0; t < 2; t++) {
-                                if (!F16 && part == 0) dot8(sum[m][t], h, lo[t][2 * e], lo[t][2 * e + 1]);
-                                dot8(sum[m][t], h, hi[t][2 * e], hi[t][2 * e + 1]);
+                                const int x = 2 * e, y = V == 1 ? 0 : 2 * e + 1;  // (V = 1: h's second pairs are zeros)
+                                if constexpr (!F16)
+                                    if (part == 0) dot16(sum[m][t], h, lo[t][x], lo[t][y]);
+                                dot16(sum[m][t], h, hi[t][x], hi[t][y]);
                             }
                         }
 #pragma unroll
                 for (int m = 0; m < 2; m++)
 #pragma unroll
-                    for (int t = 0; t < 2; t++) add4(acc[m][t], sum[m][t]);
+                    for (int t = 0; t < 2; t++)
+                        if constexpr (F16) {
+                            add4(acc[m][t], sum[m][t]);
+                        } else {
+#pragma unroll
+                            for (int h = 0; h < 4; h += 2) {
+                                const float2 z = fma2(make_float2(sum[m][t][h], sum[m][t][h + 1]), back[t],
+                                                      make_float2(acc[m][t][h], acc[m][t][h + 1]));
+                                acc[m][t][h] = z.x, acc[m][t][h + 1] = z.y;
+                            }
+                        }
             }
             const int n = run * kCols + 16 * warp + 4 * c;
 #pragma unroll
             for (int i = 0; i < 4; i++) {
                 if (at[i] < 0 || n >= a.N) continue;
                 const int m = i / 2, h = 2 * (i & 1);
-                float4 v = make_float4(acc[m][0][h], acc[m][0][h + 1], acc[m][1][h], acc[m][1][h + 1]);
+                float4 v = make_float4(acc[m][0][h] * up[i], acc[m][0][h + 1] * up[i], acc[m][1][h] * up[i], acc[m][1][h + 1] * up[i]);
                 float* p = a.y + at[i] * a.ldy + n;
                 if (VEC) {
                     if (a.base) {
@@ -462,8 +565,8 @@ template <bool F16, int MT>
 cudaError_t shrink(const LoraArgs& a, int max_tiles, cudaStream_t s) {
     auto k = lora_shrink_kernel<F16, MT>;
     static SmemOptIn opt;
-    if (cudaError_t e = opt((const void*)k, kWarps * kRing)) return e;
-    return launch_chained(k, dim3(num_sms()), kThreads, kWarps * kRing, s, a, max_tiles, num_sms());
+    if (cudaError_t e = opt((const void*)k, kShrinkWarps * kRing)) return e;
+    return launch_chained(k, dim3(num_sms()), kShrinkWarps * 32, kShrinkWarps * kRing, s, a, max_tiles, num_sms());
 }
 
 template <bool F16, int V, bool VEC, int NST>
@@ -474,10 +577,10 @@ cudaError_t expand_go(const LoraArgs& a, int max_tiles, int smem, cudaStream_t s
     return launch_chained(k, dim3((NST == 2 ? 1 : 2) * num_sms()), kThreads, smem, s, a, max_tiles, num_sms(), shrink_ranks(a.rank));
 }
 
-// Four runs on their way where two CTAs' rings fit an SM; two of one CTA's fit for every rank (128 fp32: 192 KB).
+// Four runs on their way where two CTAs' rings fit an SM; two of one CTA's fit for every rank (128 fp32: 176 KB).
 template <bool F16, int V, bool VEC>
 cudaError_t expand(const LoraArgs& a, int max_tiles, cudaStream_t s) {
-    const int operands = (a.rank + 8 * V - 1) / (8 * V) * V * 2 * 64 * 16, stage = (VEC ? 2048 : 0) + 16 * a.rank * (F16 ? 2 : 4);
+    const int operands = (a.rank + 8 * V - 1) / (8 * V) * ((V + 1) / 2) * 2 * 64 * 16, stage = (VEC ? 2048 : 0) + 16 * a.rank * (F16 ? 2 : 4);
     if (operands + 4 * kWarps * stage <= 112 * 1024) return expand_go<F16, V, VEC, 4>(a, max_tiles, operands + 4 * kWarps * stage, s);
     return expand_go<F16, V, VEC, 2>(a, max_tiles, operands + 2 * kWarps * stage, s);
 }
