@@ -28,6 +28,7 @@ constexpr int kPlanThreads = 1024;
 constexpr int kThreads = 256, kWarps = kThreads / 32;  // of expand
 constexpr int kShrinkWarps = 12;
 constexpr int kMaxSplit = 16;
+constexpr int kSetup = 6;
 constexpr int kCols = 16 * kWarps;  // columns that a CTA of expand takes at once
 
 __host__ __device__ inline int64_t plan_order(int max_tiles) { return 4 * (int64_t)(1 + max_tiles); }  // in ints
@@ -149,9 +150,10 @@ __device__ __forceinline__ int rank_of(const LoraArgs& a, int adapter) {
 
 // ---------------------------------------------------------------- shrink
 
-// Ranges of K: as many as every SM takes one of at once, of at least a chunk of 32 for each warp
+// Ranges of K: as many as every SM takes one of at once, of at least three chunks of 32 for each warp (shorter ones take as long
+// here, and every range is a round of loads in expand: 64 rows of 4 rank-64 adapters 31 us with 10 ranges, 23 with 3)
 __device__ __forceinline__ int lora_splits(int items, int K, int sms) {
-    return max(1, min(min(sms / max(items, 1), kMaxSplit), K / 32 / kShrinkWarps));
+    return max(1, min(min(sms / max(items, 1), kMaxSplit), K / 32 / (3 * kShrinkWarps)));
 }
 
 constexpr int kRing = 16 * 1024;  // of a warp of shrink
@@ -353,7 +355,11 @@ __device__ __forceinline__ float weights(uint32_t at, int left, uint32_t (&hi)[V
     }
     if constexpr (F16) {
 #pragma unroll
-        for (int i = 0; i < V; i++) hi[i] = w[i] & ((2 * i < left ? 0xFFFFu : 0u) | (2 * i + 1 < left ? 0xFFFF0000u : 0u));
+        for (int i = 0; i < V; i++) hi[i] = w[i];
+        if (__any_sync(0xffffffffu, left < 2 * V)) {
+#pragma unroll
+            for (int i = 0; i < V; i++) hi[i] &= (2 * i < left ? 0xFFFFu : 0u) | (2 * i + 1 < left ? 0xFFFF0000u : 0u);
+        }
         return 1.f;
     } else {
         float x[2 * V], m = 0.f, down, up;
@@ -381,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, NST == 2 ? 1 : 2) lora_expand_kernel
     __shared__ int sm_row[kLoraTile];
     __shared__ float sm_up[kLoraTile];  // the powers of two that take the rows of h back
     constexpr int SG = (V + 1) / 2;     // matrix steps of a group of 8 V ranks
-    constexpr int HQ = kLoraMaxRank / 32;
+    constexpr int HR = kLoraTile / kWarps, HQ = kLoraMaxRank / 32;
     constexpr int es = F16 ? 2 : 4;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = lane & 3, j = lane >> 2;
     const int row_bytes = a.rank * es, stage = (VEC ? 2048 : 0) + 16 * row_bytes, steps = (a.rank + 8 * V - 1) / (8 * V) * SG;
@@ -393,70 +399,110 @@ __global__ void __launch_bounds__(kThreads, NST == 2 ? 1 : 2) lora_expand_kernel
     const int4 early = first_tiles(plan, lane, max_tiles);
     const int tiles = a.base && a.base == a.y ? head.y : head.x;  // in place, rows without an adapter stay as they are
     const int rows = head.z, splits = lora_splits(head.y * ((a.rank + rr - 1) / rr), a.K, sms), cols = (a.N + kCols - 1) / kCols;
-    const int64_t items = (int64_t)tiles * cols, last = items * (blockIdx.x + 1) / gridDim.x;
-    for (int64_t item = items * blockIdx.x / gridDim.x; item < last;) {
-        const int which = (int)(item / cols), run0 = (int)(item - (int64_t)which * cols), run1 = (int)min((int64_t)cols, run0 + (last - item));
+    // The CTA's share: an equal one of all runs, or, where that is not much less, of one tile's, since a tile's preparation takes
+    // as long as some kSetup runs (64 rows of 40 adapters beside 4096 -> 6144: 7 runs of one tile in place of 6.6 of 1.2)
+    const int64_t items = (int64_t)tiles * cols;
+    const int ctas = gridDim.x, each_tile = ctas / max(tiles, 1), me = blockIdx.x;
+    int64_t item, last;
+    if (each_tile && (int64_t)((cols + each_tile - 1) / each_tile) * ctas <= items + (int64_t)kSetup * ctas) {
+        const int which = me / each_tile, part = me - which * each_tile;
+        if (which >= tiles) return;
+        item = (int64_t)which * cols + (unsigned)cols * (unsigned)part / (unsigned)each_tile;
+        last = (int64_t)which * cols + (unsigned)cols * (unsigned)(part + 1) / (unsigned)each_tile;
+    } else {
+        const int64_t each = items <= INT32_MAX ? (int64_t)((unsigned)items / (unsigned)ctas) : items / ctas, rest = items - each * ctas;
+        item = each * me + min((int64_t)me, rest);
+        last = each * (me + 1) + min((int64_t)me + 1, rest);
+    }
+    // this lane's first piece of 16 columns' weights: its column and byte within the row; and how far 512 bytes on is
+    const int col0 = lane * 16 / row_bytes, byte0 = lane * 16 - col0 * row_bytes, col_step = 512 / row_bytes, byte_step = 512 - col_step * row_bytes;
+    while (item < last) {
+        const int which = items <= INT32_MAX ? (int)((unsigned)item / (unsigned)cols) : (int)(item / cols);
+        const int run0 = (int)(item - (int64_t)which * cols), run1 = (int)min((int64_t)cols, run0 + (last - item));
         item += run1 - run0;
         const int4 tile = tile_of(plan, which, early);
-        // everything that depends on the tile alone, at once: its rows, rank and scale, and the warp's first row of h
+        // what depends on the tile alone, all at once: its rows, rank and scale, h (a warp takes every eighth row, a lane every 32nd
+        // rank) and the first weights
         int my_row = 0;
         if (tid < tile.z) my_row = __ldcg(plan + plan_order(max_tiles) + tile.y + tid);
         const int rank = tile.x < 0 ? 0 : rank_of(a, tile.x);
         const float scale = tile.x >= 0 && a.scale ? __ldcg(a.scale + tile.x) : 1.f;
         const int mt = tile.z > 16 ? 2 : 1;
-        // ranks lane, lane + 32 .. of a row of h
-        float h[HQ];
-        auto load_h = [&](int row) {
+        float h[HR][HQ];
 #pragma unroll
-            for (int q = 0; q < HQ; q++) {
-                h[q] = 0.f;
-                if (32 * q >= a.rank) break;
-                if (lane + 32 * q < a.rank && row < tile.z && tile.x >= 0) {
-                    const float* p = a.ws + ((int64_t)tile.y + row) * a.rank + lane + 32 * q;
+        for (int i = 0; i < HR; i++)
+#pragma unroll
+            for (int q = 0; q < HQ; q++) h[i][q] = 0.f;
+        if (tile.x >= 0 && warp < tile.z) {
+            const float* p = a.ws + ((int64_t)tile.y + warp) * a.rank + lane;
+            const int64_t stride = (int64_t)rows * a.rank;
+            if (tile.z <= kWarps && a.rank <= 32) {  // (one value a lane: four ranges on their way)
+                if (lane < a.rank)
 #pragma unroll 4
-                    for (int s = 0; s < splits; s++, p += (int64_t)rows * a.rank) h[q] += __ldcg(p);
-                }
+                    for (int s = 0; s < splits; s++) h[0][0] += __ldcg(p + s * stride);
+            } else {
+#pragma unroll 1
+                for (int s = 0; s < splits; s++, p += stride)
+#pragma unroll
+                    for (int i = 0; i < HR; i++) {
+                        if (warp + kWarps * i >= tile.z) break;
+#pragma unroll
+                        for (int q = 0; q < HQ; q++) {
+                            if (32 * q >= a.rank) break;
+                            if (lane + 32 * q < a.rank) h[i][q] += __ldcg(p + (int64_t)kWarps * i * a.rank + 32 * q);
+                        }
+                    }
+            }
+        }
+        const int groups = (rank + 8 * V - 1) / (8 * V), rank_bytes = rank * es;
+        auto fetch_b = [&](int run, int slot) {
+            const uint32_t dst = ring + slot * stage + (VEC ? 2048 : 0);
+            const int n0 = run * kCols + 16 * warp;
+            const uint8_t* src = (const uint8_t*)a.b + ((int64_t)tile.x * a.N + n0) * row_bytes;
+#pragma unroll 1
+            for (int x = lane * 16, col = col0, byte = byte0; x < 16 * row_bytes; x += 512) {
+                const bool in = n0 + col < a.N && byte < rank_bytes;
+                copy16(dst + x, in ? src + x : (const uint8_t*)a.b, in ? 16 : 0);
+                col += col_step, byte += byte_step;
+                if (byte >= row_bytes) col++, byte -= row_bytes;
             }
         };
-        load_h(warp);
         __syncthreads();  // (the previous tile's rows and operands have been read)
         if (tid < tile.z) sm_row[tid] = my_row;
-        const int groups = (rank + 8 * V - 1) / (8 * V), rank_bytes = rank * es;
+        if (rank)
+#pragma unroll 1
+            for (int i = 0; i < NST; i++)
+                if (run0 + i < run1) fetch_b(run0 + i, i);
         __syncthreads();
         int64_t at[4];  // rows j + 8 i
 #pragma unroll
         for (int i = 0; i < 4; i++) at[i] = 8 * i + j < tile.z ? sm_row[8 * i + j] : -1;
-        auto fetch = [&](int run, int slot) {
+        auto fetch_base = [&](int run, int slot) {
             const uint32_t dst = ring + slot * stage;
-            const int n0 = run * kCols + 16 * warp, n = n0 + 4 * c;
+            const int n = run * kCols + 16 * warp + 4 * c;
             if (VEC && a.base)
 #pragma unroll
-                for (int i = 0; i < 4; i++)
+                for (int i = 0; i < 4; i++) {
+                    if (8 * i >= tile.z) break;
                     if (at[i] >= 0 && n < a.N) copy16(dst + i * 512 + lane * 16, a.base + at[i] * a.ldb + n, 16);
-            if (rank) {
-                const uint8_t* src = (const uint8_t*)a.b + ((int64_t)tile.x * a.N + n0) * row_bytes;
-                for (int x = lane * 16; x < 16 * row_bytes; x += 512) {
-                    const int col = x / row_bytes;
-                    const bool in = n0 + col < a.N && x - col * row_bytes < rank_bytes;
-                    copy16(dst + (VEC ? 2048 : 0) + x, in ? src + x : (const uint8_t*)a.b, in ? 16 : 0);
                 }
-            }
         };
 #pragma unroll 1
         for (int i = 0; i < NST; i++) {
-            if (run0 + i < run1) fetch(run0 + i, i);
+            if (run0 + i < run1) fetch_base(run0 + i, i);
             copy_commit();
         }
         // h as operands: value i of lane cc's 2 V in group g is rank 8 V g + 2 V cc + i, its pairs those of steps 0, 0, 1, 1
         const int held = groups * 8 * V;
-#pragma unroll 1
-        for (int row = warp; row < 16 * mt; row += kWarps) {
-            if (row != warp) load_h(row);
+#pragma unroll
+        for (int x = 0; x < HR; x++) {
+            const int row = warp + kWarps * x;
+            if (row >= 16 * mt) break;
             float m = 0.f, down, up;
 #pragma unroll
             for (int q = 0; q < HQ; q++) {
-                h[q] = lane + 32 * q < rank ? h[q] * scale : 0.f;
-                m = fmaxf(m, fabsf(h[q]));
+                h[x][q] = lane + 32 * q < rank ? h[x][q] * scale : 0.f;
+                m = fmaxf(m, fabsf(h[x][q]));
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -465,15 +511,17 @@ __global__ void __launch_bounds__(kThreads, NST == 2 ? 1 : 2) lora_expand_kernel
 #pragma unroll
             for (int q = 0; q < HQ; q++) {
                 const int r = lane + 32 * q;
-                if (r >= held) break;
+                if (32 * q >= held) break;
                 uint32_t hi, lo;
-                split_h2(h[q] * down, 0.f, hi, lo);
+                split_h2(h[x][q] * down, 0.f, hi, lo);
                 const int g = r / (8 * V), cc = r % (8 * V) / (2 * V), i = r % (2 * V);
                 unsigned short* dst = reinterpret_cast<unsigned short*>(sm_h + ((g * SG + i / 4) * 2 + row / 16) * 64 + (row & 7) * 4 + cc) +
                                       2 * (2 * (i / 2 & 1) + (row >> 3 & 1)) + (i & 1);
-                dst[0] = (unsigned short)hi;
-                dst[32 * 8] = (unsigned short)lo;
-                if (V == 1) dst[4] = dst[32 * 8 + 4] = 0;  // (the step's other pairs)
+                if (r < held) {
+                    dst[0] = (unsigned short)hi;
+                    dst[32 * 8] = (unsigned short)lo;
+                    if (V == 1) dst[4] = dst[32 * 8 + 4] = 0;  // (the step's other pairs)
+                }
             }
         }
         __syncthreads();
@@ -533,6 +581,7 @@ __global__ void __launch_bounds__(kThreads, NST == 2 ? 1 : 2) lora_expand_kernel
             const int n = run * kCols + 16 * warp + 4 * c;
 #pragma unroll
             for (int i = 0; i < 4; i++) {
+                if (8 * i >= tile.z) break;
                 if (at[i] < 0 || n >= a.N) continue;
                 const int m = i / 2, h = 2 * (i & 1);
                 float4 v = make_float4(acc[m][0][h] * up[i], acc[m][0][h + 1] * up[i], acc[m][1][h] * up[i], acc[m][1][h + 1] * up[i]);
@@ -551,7 +600,10 @@ __global__ void __launch_bounds__(kThreads, NST == 2 ? 1 : 2) lora_expand_kernel
                 }
             }
             __syncwarp();
-            if (run + NST < run1) fetch(run + NST, slot);
+            if (run + NST < run1) {
+                if (rank) fetch_b(run + NST, slot);
+                fetch_base(run + NST, slot);
+            }
             copy_commit();
             slot = slot + 1 == NST ? 0 : slot + 1;
         }
