@@ -76,20 +76,26 @@ struct PagedCfg {
     static_assert(NST >= 2, "a stage in flight while one is read");
     static constexpr int PIECE = HEADS * (D + 2);  // floats of a warp's piece
     static_assert(PIECE * 4 <= NST * STAGE, "a piece fits the ring");
-    // 16-byte chunk permutations within 128 bytes, by row, so that the reads of a warp meet all banks
-    static __device__ __forceinline__ int swk(int r) {
-        if (TYPE == AF_F32 || TYPE == AF_F16) return (r & 1) << 2;
-        if (TYPE == AF_KV_Q8_0) return D == 128 ? (r & 3) << 1 : (r & 2);
-        return D == 128 ? (r >> 1) & 3 : (r >> 2) & 1;
+    // 16-byte chunk permutations within 128 bytes, by row, so that the reads of a warp meet all banks (codes: eight rows in a
+    // row)
+    static __device__ __forceinline__ constexpr int swk(int r) {
+        if (!QUANT) return (r & 1) << 2;
+        return RB == 128 ? r & 7 : RB == 64 ? (r >> 1) & 3 : (r >> 2) & 1;
     }
-    static __device__ __forceinline__ int swv(int r) {
+    static __device__ __forceinline__ constexpr int swv(int r) {
         if (TYPE == AF_F32) return (r & 3) << 1;
-        if (TYPE == AF_F16 || TYPE == AF_KV_Q8_0) return ((r >> 1) & 3) << 1;
-        return D == 128 ? (r >> 1) & 3 : (r >> 2) & 1;
+        if (TYPE == AF_F16) return ((r >> 1) & 3) << 1;
+        return swk(r);
     }
     // where byte `at` of row r lies
     static __device__ __forceinline__ int kbyte(int r, int at) { return (r * RB + at) ^ (swk(r) << 4); }
     static __device__ __forceinline__ int vbyte(int r, int at) { return OV + ((r * RB + at) ^ (swv(r) << 4)); }
+    // Slot of K's row r of 16, and of row j of half h of a matrix operand: transposed bytes give a lane four slots in a row of V,
+    // so the operands' 16 are those of lanes c = 0..3, pairs (4c, 4c + 1) and then (4c + 2, 4c + 3).
+    static __device__ __forceinline__ constexpr int kslot(int r) {
+        return QUANT ? 4 * ((r & 7) >> 1) + (r & 1) + 2 * (r >> 3) : r;
+    }
+    static __device__ __forceinline__ int slot(int h, int j) { return kslot(8 * h + j); }
 };
 
 // 16 bytes from global to shared memory through L2 (what earlier kernels of the chain have written may be stale in L1), of
@@ -139,6 +145,25 @@ __device__ __forceinline__ uint32_t hi_lo(float x) {
 __device__ __forceinline__ __half2 u_h2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
 __device__ __forceinline__ uint32_t h2_u(__half2 x) { return *reinterpret_cast<const uint32_t*>(&x); }
 
+// Four 8x8 matrices of 16 bits: lane (j, c) gets the 4 bytes at 4c of each one's row j.  Lanes 8i.. give matrix i's rows.
+__device__ __forceinline__ void rows4(uint32_t a, uint32_t* w) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(a));
+}
+// Two 16x16 matrices of bytes, transposed: lane (j, c) gets columns j and j + 8 of each, of rows 4c .. 4c + 3.  Lanes 16i.. give
+// matrix i's rows.
+__device__ __forceinline__ void columns4(uint32_t a, uint32_t* w) {
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(a));
+}
+// Four signed bytes as fp16 pairs
+__device__ __forceinline__ void codes2(uint32_t w, uint32_t& a, uint32_t& b) {
+    w ^= 0x80808080u;
+    a = hsub2u(__byte_perm(w, 0x64646464u, 0x4140), 0x64806480u);
+    b = hsub2u(__byte_perm(w, 0x64646464u, 0x4342), 0x64806480u);
+}
 // The nibbles of both halves of a word as fp16 codes -8..7: place 0 of each half in r[0] and so on
 __device__ __forceinline__ void codes4(uint32_t w, uint32_t (&r)[4]) {
     const __half2 f = __float2half2_rn(0.0625f), m72 = __float2half2_rn(-72.f);  // (1024 + 16 n) / 16 - 72
@@ -324,14 +349,31 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
             }
             return phys;
         };
-        auto rows_in = [&](const void* base, int phys, uint32_t dst, bool isv) {
-            constexpr int CPR = C::RB / 16;
-            const uint8_t* src = (const uint8_t*)base + (int64_t)g_ahead * a.c.ctx * C::RB;
+        auto rows_in = [&](const void* base, int phys, bool whole, uint32_t dst, bool isv) {
+            constexpr int CPR = C::RB / 16, RPI = CPR <= 32 ? 32 / CPR : 1, N = 16 / RPI;  // rows of an instruction, instructions of 16
+            static_assert(CPR <= 32 && N * RPI == 16, "");
+            const uint8_t* src = (const uint8_t*)base + (int64_t)g_ahead * a.c.ctx * C::RB + lane % CPR * 16;
+            const int r0 = lane / CPR;
+            dst += (isv ? C::vbyte(r0, lane % CPR * 16) : C::kbyte(r0, lane % CPR * 16));
+            auto to = [&](int x, int i) {  // (swizzles are linear in the bits of the row)
+                const int sw = isv ? C::swv(i * RPI) : C::swk(i * RPI);
+                return (dst ^ (sw << 4)) + (16 * x + i * RPI) * C::RB;
+            };
+            if (whole) {  // 16 slots are neighbours in memory
 #pragma unroll
-            for (int i = 0; i < KS * CPR / 32; i++) {
-                const int idx = i * 32 + lane, r = idx / CPR, at16 = idx % CPR * 16;
-                const int p = __shfl_sync(0xffffffffu, phys, r);
-                copy16(dst + (isv ? C::vbyte(r, at16) : C::kbyte(r, at16)), src + (int64_t)max(p, 0) * C::RB + at16, p >= 0 ? 16 : 0);
+                for (int x = 0; x < SUB; x++) {
+                    const uint8_t* p = src + ((int64_t)__shfl_sync(0xffffffffu, phys, 16 * x) + (isv ? r0 : C::kslot(r0))) * C::RB;
+#pragma unroll
+                    for (int i = 0; i < N; i++) copy16(to(x, i), p + (isv ? i * RPI : C::kslot(i * RPI)) * C::RB, 16);
+                }
+            } else {
+#pragma unroll
+                for (int x = 0; x < SUB; x++)
+#pragma unroll
+                    for (int i = 0; i < N; i++) {
+                        const int p = __shfl_sync(0xffffffffu, phys, 16 * x + (isv ? r0 + i * RPI : C::kslot(r0) + C::kslot(i * RPI)));
+                        copy16(to(x, i), src + (int64_t)max(p, 0) * C::RB, p >= 0 ? 16 : 0);
+                    }
             }
         };
         // the 16 bytes around the scales of the lane's slot (up to the last scale of the cache)
@@ -342,11 +384,13 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
                 copy16(dst + 16 * lane, (const uint8_t*)base + from, phys < 0 ? 0 : (int)min(end - from, (int64_t)16));
             }
         };
+        bool whole = false;  // of the stage: all slots are seen, and pages hold 16 at a time
         auto fetch_k = [&](int phys, int slot) {
             const uint32_t dst = ring + slot * C::STAGE;
-            rows_in(a.c.k, phys, dst, false);
-            scales_in(a.c.ks, phys, dst + C::OKS);
             const unsigned see = __ballot_sync(0xffffffffu, phys >= 0);
+            whole = see == 0xffffffffu && a.page % 16 == 0;
+            rows_in(a.c.k, phys, whole, dst, false);
+            scales_in(a.c.ks, phys, dst + C::OKS);
             unsigned b0 = 0, b1 = 0;
             if constexpr (C::QUANT) {
                 const unsigned row = (unsigned)g_ahead * (unsigned)a.c.ctx + (unsigned)phys;
@@ -357,9 +401,14 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
         };
         auto fetch_v = [&](int phys, int slot) {
             const uint32_t dst = ring + slot * C::STAGE;
-            rows_in(a.c.v, phys, dst, true);
+            rows_in(a.c.v, phys, whole, dst, true);
             scales_in(a.c.vs, phys, dst + C::OVS);
         };
+        // codes: where this lane's rows of the matrices of K and V begin
+        constexpr int CPR = C::RB / 16;
+        const int kaddr = CPR >= 4 ? C::kbyte(lane & 7, (lane >> 3) * 16) : C::kbyte((lane & 7) + 8 * (lane >> 4), (lane >> 3 & 1) * 16);
+        const int vaddr = C::vbyte(lane & 15, (lane >> 4) * 16) - C::OV;
+
         // The counters of the items that this CTA may hold a part of: that of its first stage and the one that begins in it.
         // A counter holds the call's mark and the number of pieces left; what has another mark is nothing (below).
         unsigned long long* const mine = counters + (lane ? (int)blockIdx.x : cta_of(begin_unit + u - at.st));
@@ -405,7 +454,7 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
                     const float* q = a.q + (int64_t)at.row * a.ldq + (int64_t)(g * G + head) * D;
 #pragma unroll
                     for (int i = 0; i < D / 16; i++) {
-                        const int d = TYPE == AF_F32 ? 16 * i + 4 * c : 32 * (i >> 1) + 8 * c + 4 * (i & 1);
+                        const int d = TYPE == AF_F32 || TYPE == AF_KV_Q8_0 ? 16 * i + 4 * c : 32 * (i >> 1) + 8 * c + 4 * (i & 1);
                         const float4 v = head < G ? __ldcg(reinterpret_cast<const float4*>(q + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
                         x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
                     }
@@ -464,9 +513,22 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
 #pragma unroll
             for (int x = 0; x < SUB; x++) {
                 uint32_t dk[2][2];
+                uint32_t kc[2][2 * NB];  // codes: a word of each 16 bytes of the rows j of both halves
                 if constexpr (C::QUANT) {
-                    scale(st + C::OKS, 16 * x + j, dk[0]);
-                    scale(st + C::OKS, 16 * x + 8 + j, dk[1]);
+                    scale(st + C::OKS, 16 * x + C::slot(0, j), dk[0]);
+                    scale(st + C::OKS, 16 * x + C::slot(1, j), dk[1]);
+                    constexpr int CPR = C::RB / 16;
+                    if constexpr (CPR >= 4) {
+#pragma unroll
+                        for (int h = 0; h < 2; h++)
+#pragma unroll
+                            for (int g4 = 0; g4 < CPR; g4 += 4)
+                                rows4(st + (kaddr ^ (g4 << 4)) + (16 * x + 8 * h) * C::RB, &kc[h][g4]);
+                    } else {  // (both halves' two chunks)
+                        uint32_t y[4];
+                        rows4(st + kaddr + 16 * x * C::RB, y);
+                        kc[0][0] = y[0], kc[0][1] = y[1], kc[1][0] = y[2], kc[1][1] = y[3];
+                    }
                 }
 #pragma unroll
                 for (int b = 0; b < NB; b++) {
@@ -494,20 +556,13 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
                         uint32_t w[2][4];
 #pragma unroll
                         for (int h = 0; h < 2; h++) {
-                            const int r = 16 * x + 8 * h + j;
                             if constexpr (TYPE == AF_F16) {
-                                shared128(st + C::kbyte(r, (4 * b + c) * 16), w[h]);
+                                shared128(st + C::kbyte(16 * x + 8 * h + j, (4 * b + c) * 16), w[h]);
                             } else if constexpr (TYPE == AF_KV_Q8_0) {
-                                uint32_t y[2];
-                                shared64(st + C::kbyte(r, 32 * b + 8 * c), y);
 #pragma unroll
-                                for (int i = 0; i < 2; i++) {
-                                    y[i] ^= 0x80808080u;
-                                    w[h][2 * i] = hsub2u(__byte_perm(y[i], 0x64646464u, 0x4140), 0x64806480u);
-                                    w[h][2 * i + 1] = hsub2u(__byte_perm(y[i], 0x64646464u, 0x4342), 0x64806480u);
-                                }
+                                for (int i = 0; i < 2; i++) codes2(kc[h][2 * b + i], w[h][2 * i], w[h][2 * i + 1]);
                             } else {
-                                codes4(shared32(st + C::kbyte(r, 16 * b + 4 * c)), w[h]);
+                                codes4(kc[h][b], w[h]);
                             }
                         }
 #pragma unroll
@@ -546,7 +601,7 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
 #pragma unroll
                 for (int x = 0; x < SUB; x++)
 #pragma unroll
-                    for (int h = 0; h < 2; h++) scale(st + C::OVS, 16 * x + 8 * h + j, vs[x][h]);
+                    for (int h = 0; h < 2; h++) scale(st + C::OVS, 16 * x + C::slot(h, j), vs[x][h]);
             }
             // ---- softmax; hidden slots have no score (and zeros as values)
             seen |= see != 0;
@@ -555,7 +610,7 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
                 for (int x = 0; x < SUB; x++)
 #pragma unroll
                     for (int h = 0; h < 2; h++)
-                        if (!(see >> (16 * x + 8 * h + j) & 1)) {
+                        if (!(see >> (16 * x + C::slot(h, j)) & 1)) {
 #pragma unroll
                             for (int t = 0; t < NT; t++) s[t][x][h] = -CUDART_INF_F;
                         }
@@ -673,35 +728,46 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
                     }
                 }
             } else {
+                uint32_t vc[SUB][4];
 #pragma unroll
                 for (int b = 0; b < NB; b++) {
                     uint32_t pb[NT][SUB][2];
 #pragma unroll
-                    for (int x = 0; x < SUB; x++)
+                    for (int x = 0; x < SUB; x++) {
+                        float d[2];
 #pragma unroll
                         for (int h = 0; h < 2; h++) {
                             const __half2 w = u_h2(vs[x][h][b / 2]);
-                            const float d = __half2float(b & 1 ? __high2half(w) : __low2half(w));
-#pragma unroll
-                            for (int t = 0; t < NT; t++) pb[t][x][h] = transpose8(hi_lo(s[t][x][h] * d));
+                            d[h] = __half2float(b & 1 ? __high2half(w) : __low2half(w));
                         }
+#pragma unroll
+                        for (int t = 0; t < NT; t++) {  // p d in two parts, of two slots at a time
+                            const float2 y = mul2(make_float2(s[t][x][0], s[t][x][1]), make_float2(d[0], d[1]));
+                            const float2 hi = make_float2(__uint_as_float(__float_as_uint(y.x) & 0xFFFFE000u), __uint_as_float(__float_as_uint(y.y) & 0xFFFFE000u));
+                            const float2 lo = fma2(hi, both(-1.f), y);
+                            pb[t][x][0] = transpose8(h2_u(__floats2half2_rn(hi.x, lo.x)));
+                            pb[t][x][1] = transpose8(h2_u(__floats2half2_rn(hi.y, lo.y)));
+                        }
+                    }
                     float sum[NT][2][4];
 #pragma unroll
                     for (int x = 0; x < SUB; x++) {
-                        uint32_t v[2][4];  // pair of slots, dim
+                        uint32_t v[2][4];  // pair of slots, row of the two row tiles
+                        if constexpr (TYPE == AF_KV_Q8_0) {
+                            uint32_t y[4];  // dims j, j + 8, j + 16, j + 24 of four slots
+                            columns4(st + C::OV + (vaddr ^ (b << 5)) + 16 * x * C::RB, y);
 #pragma unroll
-                        for (int h = 0; h < 2; h++) {
-                            const int r = 16 * x + 2 * c + 8 * h;
-                            if constexpr (TYPE == AF_KV_Q8_0) {
-                                const uint32_t w0 = shared32(st + C::vbyte(r, 32 * b + 4 * j)) ^ 0x80808080u;
-                                const uint32_t w1 = shared32(st + C::vbyte(r + 1, 32 * b + 4 * j)) ^ 0x80808080u;
-                                const uint32_t y = __byte_perm(w0, w1, 0x5140), z = __byte_perm(w0, w1, 0x7362);
-                                v[h][0] = hsub2u(__byte_perm(y, 0x64646464u, 0x4140), 0x64806480u);
-                                v[h][1] = hsub2u(__byte_perm(y, 0x64646464u, 0x4342), 0x64806480u);
-                                v[h][2] = hsub2u(__byte_perm(z, 0x64646464u, 0x4140), 0x64806480u);
-                                v[h][3] = hsub2u(__byte_perm(z, 0x64646464u, 0x4342), 0x64806480u);
-                            } else {
-                                codes4(shared16(st + C::vbyte(r, 16 * b + 2 * j)) | shared16(st + C::vbyte(r + 1, 16 * b + 2 * j)) << 16, v[h]);
+                            for (int i = 0; i < 4; i++) codes2(y[i], v[0][i], v[1][i]);
+                        } else {
+                            if (b % 2 == 0) columns4(st + C::OV + (vaddr ^ (b << 4)) + 16 * x * C::RB, vc[x]);  // two blocks' bytes
+#pragma unroll
+                            for (int i = 0; i < 2; i++) {  // bytes j and j + 8 of the block: dims 2j, 2j + 1 and 16 more
+                                const uint32_t y = vc[x][2 * (b & 1) + i], lo = y & 0x0F0F0F0Fu, hi = y & 0xF0F0F0F0u;
+                                const __half2 f = __float2half2_rn(0.0625f), m72 = __float2half2_rn(-72.f);  // (1024 + 16 n) / 16 - 72
+                                v[0][2 * i] = hsub2u(__byte_perm(lo, 0x64646464u, 0x4140), 0x64086408u);
+                                v[1][2 * i] = hsub2u(__byte_perm(lo, 0x64646464u, 0x4342), 0x64086408u);
+                                v[0][2 * i + 1] = h2_u(__hfma2(u_h2(__byte_perm(hi, 0x64646464u, 0x4140)), f, m72));
+                                v[1][2 * i + 1] = h2_u(__hfma2(u_h2(__byte_perm(hi, 0x64646464u, 0x4342)), f, m72));
                             }
                         }
 #pragma unroll
@@ -756,15 +822,26 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
                     float* dst = done ? a.out + (int64_t)at.row * a.ldo + (int64_t)(g * G + head) * D : piece + hh * D;
                     if (!done && j == 0) reinterpret_cast<float2*>(piece + C::HEADS * D)[hh] = make_float2(m_ref[t], x);
                     if (!done || head < G) {
-                        // row tile i: dims (j) and (j + 8) of its output are neighbours, i and i + 1 make four
+                        if constexpr (C::QUANT) {
 #pragma unroll
-                        for (int i = 0; i < C::MT; i += 2) {
-                            const int d = TYPE == AF_F16   ? 64 * (i >> 2) + 8 * j + 2 * (i & 3)
-                                          : TYPE == AF_F32 ? 32 * (i >> 1) + 4 * j
-                                                           : 16 * i + 4 * j;
-                            *reinterpret_cast<float4*>(dst + d) =
-                                make_float4((o[t][i][0] + o[t][i][1]) * inv, (o[t][i][2] + o[t][i][3]) * inv,
-                                            (o[t][i + 1][0] + o[t][i + 1][1]) * inv, (o[t][i + 1][2] + o[t][i + 1][3]) * inv);
+                            for (int i = 0; i < C::MT; i++) {
+                                const float y = (o[t][i][0] + o[t][i][1]) * inv, z = (o[t][i][2] + o[t][i][3]) * inv;
+                                if (TYPE == AF_KV_Q8_0) {  // rows j and j + 8 are dims 16 i + j and 8 on
+                                    dst[16 * i + j] = y;
+                                    dst[16 * i + 8 + j] = z;
+                                } else {
+                                    *reinterpret_cast<float2*>(dst + 16 * i + 2 * j) = make_float2(y, z);
+                                }
+                            }
+                        } else {
+                            // row tile i: dims (j) and (j + 8) of its output are neighbours, i and i + 1 make four
+#pragma unroll
+                            for (int i = 0; i < C::MT; i += 2) {
+                                const int d = TYPE == AF_F16 ? 64 * (i >> 2) + 8 * j + 2 * (i & 3) : 32 * (i >> 1) + 4 * j;
+                                *reinterpret_cast<float4*>(dst + d) =
+                                    make_float4((o[t][i][0] + o[t][i][1]) * inv, (o[t][i][2] + o[t][i][3]) * inv,
+                                                (o[t][i + 1][0] + o[t][i + 1][1]) * inv, (o[t][i + 1][2] + o[t][i + 1][3]) * inv);
+                            }
                         }
                     }
                 }
