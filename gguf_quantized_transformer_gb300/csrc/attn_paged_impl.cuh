@@ -941,20 +941,21 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
     if (!own0.z && !own1.z) return;
     // ---- items of several CTAs: the last CTA to leave its piece joins them, in order
     __shared__ int2 sm_chain[2];  // first and last CTA of an item that this one joins; first < 0: it does not
+    const int4 mine_of = tid ? own1 : own0;
+    int2 chain = make_int2(0, 0);
+    if (tid < 2 && mine_of.z) {
+        const int64_t nst = first[mine_of.x + 1] - first[mine_of.x], from = begin_unit + (int64_t)first[mine_of.x] * GI + mine_of.y * nst;
+        chain = make_int2(cta_of(from), cta_of(from + nst - 1));
+    }
     __syncthreads();
     if (tid < 2) {
-        const int4 p = tid ? own1 : own0;
-        int2 chain = make_int2(-1, -1);
-        if (p.z) {
-            const int64_t nst = first[p.x + 1] - first[p.x], from = begin_unit + (int64_t)first[p.x] * GI + p.y * nst;
-            const int b = cta_of(from), e = cta_of(from + nst - 1);
-            __threadfence();  // (the CTA's pieces, which the barrier has put before this thread)
-            if ((int)(atomicAdd(counters + b, 1ull) & 0xFFFF) == e - b) {
-                counters[b] = 0;
-                chain = make_int2(b, e);
-            }
-            __threadfence();
-        }
+        unsigned long long left = ~0ull;
+        if (mine_of.z)  // (the barrier has put the CTA's pieces before this thread, the release puts them before the count)
+            asm volatile("atom.acq_rel.gpu.global.add.u64 %0, [%1], 1;" : "=l"(left) : "l"(counters + chain.x) : "memory");
+        if ((int)(left & 0xFFFF) == chain.y - chain.x)
+            counters[chain.x] = 0;
+        else
+            chain = make_int2(-1, -1);
         sm_chain[tid] = chain;
     }
     __syncthreads();

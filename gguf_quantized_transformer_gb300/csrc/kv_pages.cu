@@ -3,7 +3,7 @@
 // lies in slot page * page_size + p % page_size.  Pages come from the head of a ring of free ones, in the requests' order,
 // and those of ended requests go behind its last one, so that no entry that is read here is written here.
 //
-// Three prefix sums over the requests (rows; then pages taken and pages given back, which need the first), one CTA; then one
+// Three prefix sums over the requests (rows, pages taken, pages given back), one CTA; then one
 // thread per row of the batch, which finds its request by a binary search over the rows' starts.  A new page begins with a
 // new token, so the thread of the page's first token writes the table.  Small steps do both in the one CTA, larger ones the
 // second part in a grid of their own.
@@ -26,44 +26,45 @@ constexpr int kRefused = -1, kEnded = -2;
 
 __device__ __forceinline__ int64_t clamp_int(int64_t x) { return x < INT32_MAX ? x : INT32_MAX; }
 
-// Inclusive prefix sums over the CTA of two values a thread; `total` receives the CTA's.
-__device__ __forceinline__ void cta_scan2(int64_t& x, int64_t& y, int64_t (&total)[2]) {
-    __shared__ int64_t part[2][kScan / 32];
+// Inclusive prefix sums over the CTA of three values a thread; `total` receives the CTA's.
+__device__ __forceinline__ void cta_scan(int64_t (&x)[3], int64_t (&total)[3]) {
+    __shared__ int64_t part[kScan / 32][3];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-        const int64_t a = __shfl_up_sync(0xffffffffu, x, o), b = __shfl_up_sync(0xffffffffu, y, o);
-        if (lane >= o) x += a, y += b;
-    }
-    __syncthreads();  // (the previous call's parts have been read)
-    if (lane == 31) part[0][warp] = x, part[1][warp] = y;
-    __syncthreads();
-    if (warp == 0) {
-        int64_t u = part[0][lane], v = part[1][lane];
+    for (int o = 1; o < 32; o *= 2)
 #pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-            const int64_t a = __shfl_up_sync(0xffffffffu, u, o), b = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) u += a, v += b;
+        for (int k = 0; k < 3; k++) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x[k], o);
+            if (lane >= o) x[k] += y;
         }
-        part[0][lane] = u, part[1][lane] = v;
-    }
+    __syncthreads();  // (the previous call's parts have been read)
+    if (lane == 31)
+#pragma unroll
+        for (int k = 0; k < 3; k++) part[warp][k] = x[k];
     __syncthreads();
-    if (warp) x += part[0][warp - 1], y += part[1][warp - 1];
-    total[0] = part[0][kScan / 32 - 1], total[1] = part[1][kScan / 32 - 1];
+    // every warp sums the others' parts, lane by lane
+#pragma unroll
+    for (int k = 0; k < 3; k++) {
+        int64_t y = part[lane][k], before = lane < warp ? y : 0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            y += __shfl_xor_sync(0xffffffffu, y, o);
+            before += __shfl_xor_sync(0xffffffffu, before, o);
+        }
+        total[k] = y;
+        x[k] += before;
+    }
 }
 
-// The last i of [0, n) with key(i) <= x; key(0) <= x
-template <typename F>
-__device__ __forceinline__ int last_le(int n, int x, F key) {
-    int lo = 0, hi = n;  // key(lo) <= x < key(hi)
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (key(mid) <= x)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    return lo;
+// For N numbers x: the last i of [0, n) with key(i) <= x; key(0) <= x
+template <int N, typename F>
+__device__ __forceinline__ void last_le(int n, const int (&x)[N], int (&i)[N], F key) {
+#pragma unroll
+    for (int k = 0; k < N; k++) i[k] = 0;
+    for (int w = n > 1 ? 1 << (31 - __clz(n - 1)) : 0; w; w >>= 1)
+#pragma unroll
+        for (int k = 0; k < N; k++)
+            if (i[k] + w < n && key(i[k] + w) <= x[k]) i[k] += w;
 }
 
 __device__ __forceinline__ int page_of(const PagesArgs& a, int pos) {
@@ -80,13 +81,19 @@ __device__ __forceinline__ int wrap(unsigned x, int n) { return (int)(x >= (unsi
 
 // Rows and returned pages of thread t of nt: ROWS neighbours at a time.  start(i), back(i): the prefix sums; head, count: the
 // ring before the step.
-template <int ROWS, typename S, typename B>
+template <int ROWS, typename S, typename B, typename Q>
 __device__ __forceinline__ void fill(const PagesArgs& a, int64_t t, int64_t nt, int total, int returned, int head, int count, S start,
-                                     B back) {
+                                     B back, Q request) {
     for (int64_t at = t * ROWS; at < a.rows; at += nt * ROWS) {
         const int r0 = (int)at;
         int slot[ROWS], pos[ROWS], seq[ROWS];
-        int i = r0 < total ? last_le(a.n, r0, start) : 0, begin = 0, end = -1;  // rows [begin, end) of request i
+        int i = 0, begin = 0, end = -1;  // rows [begin, end) of request i
+        if (r0 < total) {
+            const int x[1] = {r0};
+            int y[1];
+            last_le<1>(a.n, x, y, start);
+            i = y[0];
+        }
         int4 q = make_int4(kRefused, 0, 0, 0);
 #pragma unroll
         for (int k = 0; k < ROWS; k++) {
@@ -100,7 +107,7 @@ __device__ __forceinline__ void fill(const PagesArgs& a, int64_t t, int64_t nt, 
                 }
                 begin = start(i);
                 end = i + 1 < a.n ? start(i + 1) : total;
-                q = __ldcg(a.ws + i);
+                q = request(i);
             }
             if (q.x < 0) continue;
             const int p = q.y + (r - begin), e = page_of(a, p);
@@ -126,10 +133,17 @@ __device__ __forceinline__ void fill(const PagesArgs& a, int64_t t, int64_t nt, 
                 if (at + k < a.rows) a.slots[r0 + k] = slot[k], a.pos[r0 + k] = pos[k], a.seq[r0 + k] = seq[k];
         }
     }
-    for (int64_t e = t; e < returned; e += nt) {
-        const int i = last_le(a.n, (int)e, back);
-        a.free[wrap((unsigned)head + (unsigned)count + (unsigned)e, a.n_pages)] =  // (count + e < n_pages)
-            __ldcg(a.table + (int64_t)i * a.width + ((int)e - back(i)));
+    // four pages given back at a time, a grid apart
+    for (int64_t e0 = t; e0 < returned; e0 += 4 * nt) {
+        int e[4], i[4], page[4];
+#pragma unroll
+        for (int k = 0; k < 4; k++) e[k] = (int)min(e0 + k * nt, (int64_t)returned - 1);
+        last_le<4>(a.n, e, i, back);
+#pragma unroll
+        for (int k = 0; k < 4; k++) page[k] = __ldcg(a.table + (int64_t)i[k] * a.width + (e[k] - back(i[k])));
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+            if (e0 + k * nt < returned) a.free[wrap((unsigned)head + (unsigned)count + (unsigned)e[k], a.n_pages)] = page[k];  // (count + e < n_pages)
     }
 }
 
@@ -137,58 +151,67 @@ __device__ __forceinline__ void fill(const PagesArgs& a, int64_t t, int64_t nt, 
 template <bool FILL>
 __global__ void __launch_bounds__(kScan) kv_pages_scan_kernel(PagesArgs a) {
     __shared__ int sm_start[FILL ? kScan : 1], sm_back[FILL ? kScan : 1];
+    __shared__ int4 sm_request[FILL ? kScan : 1];
     __shared__ int sm_taken, sm_returned, sm_refused;
     const int t = threadIdx.x;
     pdl_launch_dependents();
     pdl_wait();
     int head = __ldcg(a.pool), count = __ldcg(a.pool + 1);
-    head = head >= 0 && head < a.n_pages ? head : 0;
-    count = min(max(count, 0), a.n_pages);
     if (t == 0) sm_taken = sm_returned = sm_refused = 0;
-    int64_t rows0 = 0, take0 = 0, back0 = 0;  // sums of the requests before this round of kScan
+    int64_t before[3] = {0, 0, 0};  // rows, pages taken and pages given back by the requests before this round of kScan
     const int64_t most = (int64_t)a.width * a.page;
     for (int i0 = 0; i0 < a.n; i0 += kScan) {
         const int i = i0 + t;
         const bool in = i < a.n;
         const int len = in ? __ldcg(a.len + i) : 0, fresh = in ? __ldcg(a.fresh + i) : 0;
+        if (i0 == 0) {
+            head = head >= 0 && head < a.n_pages ? head : 0;
+            count = min(max(count, 0), a.n_pages);
+        }
         const bool ends = fresh < 0, sound = len >= 0 && len <= most;
-        const int64_t grow = ends ? 0 : fresh;
-        int64_t rows = grow, unused = 0, total[2];
-        cta_scan2(rows, unused, total);
-        rows += rows0;
-        rows0 += total[0];
+        const int64_t grow = ends ? 0 : fresh, back = in && ends && sound ? pages_for(a, len) : 0;
         const int have = sound ? pages_for(a, len) : 0;
-        const bool fits = in && !ends && sound && rows <= a.rows && len + grow <= most;
-        const int64_t need = fits ? pages_for(a, (int)(len + grow)) - have : 0, back = in && ends ? have : 0;
-        int64_t taken = need, returned = back;
-        cta_scan2(taken, returned, total);
-        taken += take0, returned += back0;
-        take0 += total[0], back0 += total[1];
+        bool fits = in && !ends && sound && len + grow <= most;
+        int64_t need = fits ? pages_for(a, (int)(len + grow)) - have : 0, sums[3] = {grow, need, back}, total[3];
+        cta_scan(sums, total);
+        if (before[0] + total[0] > a.rows) {  // some requests' rows do not fit: they take no pages
+            if (before[0] + sums[0] > a.rows) fits = false, need = 0;
+            sums[0] = grow, sums[1] = need, sums[2] = back;
+            cta_scan(sums, total);
+        }
+        const int64_t rows = before[0] + sums[0], taken = before[1] + sums[1], returned = before[2] + sums[2];
+#pragma unroll
+        for (int k = 0; k < 3; k++) before[k] += total[k];
         const bool served = fits && (need == 0 || taken <= count);
         const bool ended = in && ends && sound && (int64_t)count + returned <= a.n_pages;
         if (in) {
             const int start = (int)clamp_int(rows - grow);
+            const int4 q = make_int4(served ? (int)(need ? taken - need : 0) : ended ? kEnded : kRefused, len, have,
+                                     (int)clamp_int(returned - back));
             a.start[i] = start;
-            a.ws[i] = make_int4(served ? (int)(need ? taken - need : 0) : ended ? kEnded : kRefused, len, have,
-                                (int)clamp_int(returned - back));
             a.len_out[i] = served ? (int)(len + grow) : ended ? 0 : len;
-            if (FILL) sm_start[i] = start, sm_back[i] = (int)clamp_int(returned - back);
+            if (FILL)
+                sm_start[i] = start, sm_back[i] = q.w, sm_request[i] = q;
+            else
+                a.ws[i] = q;
             if (served && need) atomicMax(&sm_taken, (int)taken);
             if (ended) atomicMax(&sm_returned, (int)returned);
             if (!served && !ended) atomicAdd(&sm_refused, 1);
         }
         __syncthreads();
     }
-    const int total = (int)clamp_int(rows0), taken = sm_taken, returned = sm_returned;
+    const int total = (int)clamp_int(before[0]), taken = sm_taken, returned = sm_returned;
     if (t == 0) {
         a.start[a.n] = total;
-        a.ws[a.n] = make_int4(head, count, total, returned);
+        if (!FILL) a.ws[a.n] = make_int4(head, count, total, returned);
         a.pool_out[0] = wrap((unsigned)head + (unsigned)taken, a.n_pages);
         a.pool_out[1] = count - taken + returned;
         a.pool_out[2] = sm_refused;
         a.pool_out[3] = total;
     }
-    if (FILL) fill<1>(a, t, kScan, total, returned, head, count, [&](int i) { return sm_start[i]; }, [&](int i) { return sm_back[i]; });
+    if (FILL)
+        fill<1>(a, t, kScan, total, returned, head, count, [&](int i) { return sm_start[i]; }, [&](int i) { return sm_back[i]; },
+                [&](int i) { return sm_request[i]; });
 }
 
 // KEPT: the prefix sums in shared memory, so that the searches do not wait for L2.
@@ -203,10 +226,12 @@ __global__ void __launch_bounds__(kFill) kv_pages_fill_kernel(PagesArgs a) {
         __syncthreads();
     }
     const int64_t t = (int64_t)blockIdx.x * kFill + threadIdx.x, nt = (int64_t)gridDim.x * kFill;
+    auto request = [&](int i) { return __ldcg(a.ws + i); };
     if (KEPT)
-        fill<kFillRows>(a, t, nt, h.z, h.w, h.x, h.y, [&](int i) { return sm_sums[i]; }, [&](int i) { return sm_sums[a.n + i]; });
+        fill<kFillRows>(a, t, nt, h.z, h.w, h.x, h.y, [&](int i) { return sm_sums[i]; }, [&](int i) { return sm_sums[a.n + i]; }, request);
     else
-        fill<kFillRows>(a, t, nt, h.z, h.w, h.x, h.y, [&](int i) { return __ldcg(a.start + i); }, [&](int i) { return __ldcg(&a.ws[i].w); });
+        fill<kFillRows>(a, t, nt, h.z, h.w, h.x, h.y, [&](int i) { return __ldcg(a.start + i); }, [&](int i) { return __ldcg(&a.ws[i].w); },
+                        request);
 }
 
 }  // namespace
