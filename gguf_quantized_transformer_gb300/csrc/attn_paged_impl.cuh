@@ -2,19 +2,24 @@
 //   out = sum_j p_j v_j / sum_j p_j,   p_j = exp(q . k_j / sqrt(D)),   k_j, v_j at slot table[seq][j / page] page + j % page.
 // A row that sees no slot gives zeros; one whose scores are all -infinity has no softmax and gives NaN.
 //
-// Bound by the bytes of the cache: everything is arranged so that a warp does nothing but stream them.
+// Bound by the bytes of the cache (fp32 and fp16: 0.92 to 1.0 of the measured copy rate for long batches; Q8_0 0.87), with
+// codes by the instructions that unpack them (Q4_0 0.5), for few slots by its chain of dependent loads:
 //  - A work item is a row, a kv head and up to 4 NT heads of its group.  All items' stages of KS slots in a row are cut into
 //    equal ranges, one per warp: no warp waits for another whatever the lengths are, one long request is spread over the
-//    whole GPU and many short ones need no joining.  The ranges come from prefix sums of the rows' stages, which each
+//    whole GPU and many short ones need little joining.  The ranges come from prefix sums of the rows' stages, which each
 //    CTA forms from pos (at most kPagedMaxRows rows).
-//  - K and V go from memory straight into the registers from which the matrix products take them: a stage's K is on its way
-//    while the previous stage's softmax and output run, its V during the scores.  No shared memory and no barrier in the loop.
+//  - A warp streams its range through a ring of its own, two stages of K and V by 16-byte asynchronous copies, K's part
+//    refilled while the softmax runs and V's during the next scores; no barrier but __syncwarp in the loop.  (Loads straight
+//    into operand registers, the first design, took 236 us where this takes 173: 64 fp16 requests of up to 8192 x 128.)
+//    A lane holds two entries of the table's row, so that 64 pages' addresses are shuffles; 16 neighbouring slots
+//    (pages of a multiple of 16) are copied from one address.
 //  - Products have the slots as rows: S^T = K q^T with the columns (head 0 hi, head 0 lo, head 1 hi ..), q split into two
 //    parts of 11 bits, so that a thread's two columns add up to one head's score; out^T = V^T p^T likewise, with p brought
 //    into the operand's layout by 8x8 transposes (fp32: shuffles).  Four heads fill the 8 columns (a group of 8 takes two
 //    column tiles).
 //  - fp16: K and V are operands as they are.  Codes become fp16 integers: a key's scale multiplies its block's partial
-//    score, a value's scale multiplies p in fp32 before p is split.
+//    score, a value's scale multiplies p in fp32 before p is split.  (Codes with their offset left in, which saves a third of
+//    the unpacking, lose three bits of a score: 1.3e-6 of the result's norm in place of 4e-7.)
 //  - fp32: K and V are cut into tf32 parts, three of the four products matter (the fourth comes with the columns).
 //  - The reference of the softmax follows score + log2(the value's largest scale), so that what goes into the fp16 operand
 //    (p times scale) stays below 2^14 and its low part above fp16's subnormal step whatever the scales; it moves only when
@@ -26,6 +31,8 @@
 // call to call.
 #pragma once
 #include <math_constants.h>
+
+#include <type_traits>
 
 #include "mma_sync.cuh"
 #include "serve.cuh"
@@ -49,12 +56,11 @@ __host__ __device__ constexpr size_t paged_ws_floats(int ctas, int D) {
     return paged_far(ctas, D) + (size_t)ctas * 8 * paged_piece_floats(D);
 }
 
-// Stages of a warp's ring in flight, and warps of a CTA (one to an SM)
+// Warps of a CTA (one to an SM): as many as their registers and rings allow, but for fp16 rows of 128 and fp32 ones, where more
+// only lengthen the joins (fp16, one token over 30720 slots 28.6 us with 8 warps, 29.7 with 12; fp32 rows of 64 312 and 329
+// with 8 and 12; fp16 rows of 64 190 and 168 with 8 and 12, Q8_0 ones 133 and 121 with 12 and 16).
 __host__ __device__ constexpr int paged_warps(int type, int D, int nt) {
-    return type == AF_F32 ? (D == 128 ? 6 : 8) : type == AF_F16 ? 8 : nt == 1 ? 12 : 8;
-}
-__host__ __device__ constexpr int paged_stages(int stage, int warps) {
-    return 216 * 1024 / (stage * warps) < 6 ? 216 * 1024 / (stage * warps) : 6;
+    return type == AF_F32 ? (D == 128 ? 6 : 8) : nt == 2 ? 8 : D == 64 ? (type == AF_F16 ? 12 : 16) : (type == AF_F16 ? 8 : 12);
 }
 
 template <int TYPE, int D, int NT>
@@ -72,10 +78,13 @@ struct PagedCfg {
     // a stage: K rows, V rows, and the 16 bytes around each slot's K and V scales
     static constexpr int OV = KS * RB, OKS = 2 * KS * RB, OVS = OKS + (QUANT ? 16 * KS : 0);
     static constexpr int STAGE = OVS + (QUANT ? 16 * KS : 0);
-    static constexpr int NST = paged_stages(STAGE, NW);
-    static_assert(NST >= 2, "a stage in flight while one is read");
+    static constexpr int NST = 2;  // stages of a warp's ring (three measured 1 to 2% slower, in every type)
     static constexpr int PIECE = HEADS * (D + 2);  // floats of a warp's piece
     static_assert(PIECE * 4 <= NST * STAGE, "a piece fits the ring");
+    static constexpr int RING = NW * NST * STAGE, ROWS = (kPagedMaxRows + 1) * 4, STATIC = NW * (32 + 16 * NST + 8) + 256;
+    static constexpr bool NEAR = RING + ROWS + STATIC + NW * PIECE * 4 <= 227 * 1024;  // pieces of warps that go on fit beside it
+    static constexpr int FIXED = RING + (NEAR ? NW * PIECE * 4 : 0);
+    static_assert(FIXED + ROWS + STATIC <= 227 * 1024, "shared memory");
     // 16-byte chunk permutations within 128 bytes, by row, so that the reads of a warp meet all banks (codes: eight rows in a
     // row)
     static __device__ __forceinline__ constexpr int swk(int r) {
@@ -90,8 +99,9 @@ struct PagedCfg {
     // where byte `at` of row r lies
     static __device__ __forceinline__ int kbyte(int r, int at) { return (r * RB + at) ^ (swk(r) << 4); }
     static __device__ __forceinline__ int vbyte(int r, int at) { return OV + ((r * RB + at) ^ (swv(r) << 4)); }
-    // Slot of K's row r of 16, and of row j of half h of a matrix operand: transposed bytes give a lane four slots in a row of V,
-    // so the operands' 16 are those of lanes c = 0..3, pairs (4c, 4c + 1) and then (4c + 2, 4c + 3).
+    // Slot of K's row r of 16, and of row j of half h of a matrix operand: transposed bytes give a lane c four slots in a row of V,
+    // and its operands' pairs are what takes the fewest instructions: (4c, 4c + 1) and (4c + 2, 4c + 3), of nibbles (4c, 4c + 2)
+    // and (4c + 1, 4c + 3).
     static __device__ __forceinline__ constexpr int kslot(int r) {
         return QUANT ? 4 * ((r & 7) >> 1) + (r & 1) + 2 * (r >> 3) : r;
     }
@@ -187,13 +197,14 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
     __shared__ int64_t sm_part[NW];  // (32 or 64 bits)
     __shared__ int4 sm_piece[NW][2];   // row, gi, used (1: in the ring, 2: in the workspace), ends
     __shared__ uint4 sm_head[NW][NST];  // of a stage in flight: the slots that are seen, and two bits of where their scales lie
-    int2* const rows = reinterpret_cast<int2*>(smem + NW * NST * C::STAGE);  // [n] request and position, for up to kPagedKept rows
+    int2* const rows = reinterpret_cast<int2*>(smem + C::FIXED);  // [n] request and position, for up to kPagedKept rows
     int* const first = reinterpret_cast<int*>(rows + (a.n <= kPagedKept ? a.n : 0));  // [n + 1] stages before each row
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = lane & 3, j = lane >> 2;
     const int KVH = a.c.KVH, G = a.H / KVH, HT = (G + C::HEADS - 1) / C::HEADS, GI = KVH * HT;
     const uint32_t ring = smem_u32(smem) + warp * NST * C::STAGE;
     float* const my_piece = reinterpret_cast<float*>(smem + warp * NST * C::STAGE);
-    float* const far = a.ws + paged_far(gridDim.x, D);  // pieces of warps whose ring goes on
+    // pieces of warps whose ring goes on
+    float* const far = C::NEAR ? reinterpret_cast<float*>(smem + C::RING) : a.ws + paged_far(gridDim.x, D) + (size_t)blockIdx.x * NW * C::PIECE;
 
     pdl_wait();  // positions, tables, q and the cache are written by earlier kernels
     pdl_launch_dependents();
@@ -426,163 +437,170 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
             const bool work = round >= 0;
             const int g = at.gi / HT, ht = at.gi - g * HT;
             const uint32_t st = ring + slot * C::STAGE;
-            unsigned see = 0, b0 = 0, b1 = 0;  // the stage's slots that are seen, and where their scales lie
+            unsigned see = 0;  // the stage's slots that are seen
             float s[NT][SUB][2];  // scores: this lane's slots j and j + 8 of each 16, head c of tile t
-            // scales of this lane's slot i (of 32): the words of blocks 0, 1 and 2, 3
-            auto scale = [&](uint32_t base, int i, uint32_t (&w)[2]) {
+            int so[SUB][2];  // where the scales of this lane's slots lie
+            auto scale = [&](uint32_t base, int x, int h, uint32_t (&w)[2]) {  // the words of blocks 0, 1 and 2, 3
                 if (NB == 4) {
-                    shared64(base + 16 * i + (b0 >> i & 1) * 8, w);
+                    shared64(base + so[x][h], w);
                 } else {
-                    w[0] = shared32(base + 16 * i + (b0 >> i & 1) * 4 + (b1 >> i & 1) * 8);
+                    w[0] = shared32(base + so[x][h]);
                     w[1] = 0;
                 }
             };
             if (work) {
-            // ---- a new item: q's operands
-            if (fresh) {
-                fresh = false;
-                begun = at.st == 0;
-                seen = false;
+                // ---- a new item: q's operands
+                if (fresh) {
+                    fresh = false;
+                    begun = at.st == 0;
+                    seen = false;
 #pragma unroll
-                for (int t = 0; t < NT; t++) {
-                    m_ref[t] = -CUDART_INF_F;
-                    l[t] = 0.f;
+                    for (int t = 0; t < NT; t++) {
+                        m_ref[t] = -CUDART_INF_F;
+                        l[t] = 0.f;
 #pragma unroll
-                    for (int i = 0; i < C::MT; i++) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
-                    const int head = ht * C::HEADS + 4 * t + (j >> 1), part = j & 1;
-                    float x[D / 4];  // this lane's quarter of the head
-                    const float* q = a.q + (int64_t)at.row * a.ldq + (int64_t)(g * G + head) * D;
+                        for (int i = 0; i < C::MT; i++) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
+                        const int head = ht * C::HEADS + 4 * t + (j >> 1), part = j & 1;
+                        float x[D / 4];  // this lane's quarter of the head
+                        const float* q = a.q + (int64_t)at.row * a.ldq + (int64_t)(g * G + head) * D;
 #pragma unroll
-                    for (int i = 0; i < D / 16; i++) {
-                        const int d = TYPE == AF_F32 || TYPE == AF_KV_Q8_0 ? 16 * i + 4 * c : 32 * (i >> 1) + 8 * c + 4 * (i & 1);
-                        const float4 v = head < G ? __ldcg(reinterpret_cast<const float4*>(q + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
-                        x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
-                    }
-                    const float sc = rsqrtf((float)D) * kLog2eP;
-                    if constexpr (TYPE == AF_F32) {
-#pragma unroll
-                        for (int i = 0; i < D / 16; i++)
-#pragma unroll
-                            for (int e = 0; e < 4; e++) {  // dims 4c .. + 3 of 16: the two values of steps 2i and 2i + 1
-                                uint32_t hi, lo;
-                                split_tf32(x[4 * i + e] * sc, hi, lo);
-                                qf[t][2 * i + (e >> 1)][e & 1] = part ? lo : hi;
-                            }
-                        rowf[t] = 1.f;
-                    } else {
-                        // a power of two brings the head's largest value to [2^12, 2^13)
-                        float mx = 0.f;
-#pragma unroll
-                        for (int i = 0; i < D / 4; i++) x[i] *= sc, mx = fmaxf(mx, fabsf(x[i]));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                        int e = (int)(__float_as_uint(mx) >> 23) - 127 - 12;
-                        e = e < -100 ? -100 : (e > 114 ? 114 : e);  // (0, subnormal; infinite: the row becomes NaN either way)
-                        const float down = __uint_as_float((unsigned)(127 - e) << 23);
-                        const float up = __uint_as_float((unsigned)(127 + e) << 23);
-                        rowf[t] = __shfl_sync(0xffffffffu, up, 8 * c);  // of head c
-#pragma unroll
-                        for (int i = 0; i < D / 4; i++) {
-                            x[i] *= down;
-                            const uint32_t w = hi_lo(x[i]);
-                            x[i] = __half2float(__ushort_as_half((unsigned short)(part ? w >> 16 : w)));  // this column's part
+                        for (int i = 0; i < D / 16; i++) {
+                            const int d = TYPE == AF_F32 || TYPE == AF_KV_Q8_0 ? 16 * i + 4 * c : 32 * (i >> 1) + 8 * c + 4 * (i & 1);
+                            const float4 v = head < G ? __ldcg(reinterpret_cast<const float4*>(q + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                            x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
                         }
+                        const float sc = rsqrtf((float)D) * kLog2eP;
+                        if constexpr (TYPE == AF_F32) {
 #pragma unroll
-                        for (int b = 0; b < NB; b++) {
-                            const float* y = x + 8 * b;
+                            for (int i = 0; i < D / 16; i++)
 #pragma unroll
-                            for (int i = 0; i < 4; i++)  // Q4_0: nibble i of a word's halves is dims i and i + 4
-                                qf[t][2 * b + (i >> 1)][i & 1] = TYPE == AF_KV_Q4_0 ? h2_u(__floats2half2_rn(y[i], y[i + 4]))
-                                                                                    : h2_u(__floats2half2_rn(y[2 * i], y[2 * i + 1]));
+                                for (int e = 0; e < 4; e++) {  // dims 4c .. + 3 of 16: the two values of steps 2i and 2i + 1
+                                    uint32_t hi, lo;
+                                    split_tf32(x[4 * i + e] * sc, hi, lo);
+                                    qf[t][2 * i + (e >> 1)][e & 1] = part ? lo : hi;
+                                }
+                            rowf[t] = 1.f;
+                        } else {
+                            // a power of two brings the head's largest value to [2^12, 2^13)
+                            float mx = 0.f;
+#pragma unroll
+                            for (int i = 0; i < D / 4; i++) x[i] *= sc, mx = fmaxf(mx, fabsf(x[i]));
+                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                            int e = (int)(__float_as_uint(mx) >> 23) - 127 - 12;
+                            e = e < -100 ? -100 : (e > 114 ? 114 : e);  // (0, subnormal; infinite: the row becomes NaN either way)
+                            const float down = __uint_as_float((unsigned)(127 - e) << 23);
+                            const float up = __uint_as_float((unsigned)(127 + e) << 23);
+                            rowf[t] = __shfl_sync(0xffffffffu, up, 8 * c);  // of head c
+#pragma unroll
+                            for (int i = 0; i < D / 4; i++) {
+                                x[i] *= down;
+                                const uint32_t w = hi_lo(x[i]);
+                                x[i] = __half2float(__ushort_as_half((unsigned short)(part ? w >> 16 : w)));  // this column's part
+                            }
+#pragma unroll
+                            for (int b = 0; b < NB; b++) {
+                                const float* y = x + 8 * b;
+#pragma unroll
+                                for (int i = 0; i < 4; i++)  // Q4_0: nibble i of a word's halves is dims i and i + 4
+                                    qf[t][2 * b + (i >> 1)][i & 1] = TYPE == AF_KV_Q4_0 ? h2_u(__floats2half2_rn(y[i], y[i + 4]))
+                                                                                        : h2_u(__floats2half2_rn(y[2 * i], y[2 * i + 1]));
+                            }
                         }
                     }
                 }
-            }
-            copy_wait<2 * NST - 1>();
-            __syncwarp();  // every lane's copies of this stage's K have landed
-            asm volatile("" ::: "memory");
-            {
+                copy_wait<2 * NST - 1>();
+                __syncwarp();  // every lane's copies of this stage's K have landed
+                asm volatile("" ::: "memory");
                 const uint4 hd = sm_head[warp][slot];
-                see = hd.x, b0 = hd.y, b1 = hd.z;
-            }
-            // ---- scores
-#pragma unroll
-            for (int t = 0; t < NT; t++)
-#pragma unroll
-                for (int x = 0; x < SUB; x++) s[t][x][0] = s[t][x][1] = 0.f;
-#pragma unroll
-            for (int x = 0; x < SUB; x++) {
-                uint32_t dk[2][2];
-                uint32_t kc[2][2 * NB];  // codes: a word of each 16 bytes of the rows j of both halves
+                see = hd.x;
                 if constexpr (C::QUANT) {
-                    scale(st + C::OKS, 16 * x + C::slot(0, j), dk[0]);
-                    scale(st + C::OKS, 16 * x + C::slot(1, j), dk[1]);
-                    constexpr int CPR = C::RB / 16;
-                    if constexpr (CPR >= 4) {
 #pragma unroll
-                        for (int h = 0; h < 2; h++)
-#pragma unroll
-                            for (int g4 = 0; g4 < CPR; g4 += 4)
-                                rows4(st + (kaddr ^ (g4 << 4)) + (16 * x + 8 * h) * C::RB, &kc[h][g4]);
-                    } else {  // (both halves' two chunks)
-                        uint32_t y[4];
-                        rows4(st + kaddr + 16 * x * C::RB, y);
-                        kc[0][0] = y[0], kc[0][1] = y[1], kc[1][0] = y[2], kc[1][1] = y[3];
-                    }
-                }
-#pragma unroll
-                for (int b = 0; b < NB; b++) {
-                    if constexpr (TYPE == AF_F32) {
-                        float p[NT][4] = {};
-                        uint32_t hi[2][8], lo[2][8];
+                    for (int x = 0; x < SUB; x++)
 #pragma unroll
                         for (int h = 0; h < 2; h++) {
-                            shared128(st + C::kbyte(8 * h + j, (8 * b + c) * 16), hi[h]);
-                            shared128(st + C::kbyte(8 * h + j, (8 * b + 4 + c) * 16), hi[h] + 4);
-#pragma unroll
-                            for (int i = 0; i < 8; i++) cut_tf32(__uint_as_float(hi[h][i]), hi[h][i], lo[h][i]);
+                            const int i = 16 * x + C::slot(h, j);
+                            so[x][h] = st + 16 * i + (NB == 4 ? (hd.y >> i & 1) * 8 : (hd.y >> i & 1) * 4 + (hd.z >> i & 1) * 8);
                         }
+                }
+                // ---- scores
 #pragma unroll
-                        for (int e = 0; e < 8; e++) {  // the small lo products first
-                            const int i = 2 * (e & 3), step = 4 * b + (e & 3);
-                            const uint32_t *k0 = e < 4 ? lo[0] : hi[0], *k1 = e < 4 ? lo[1] : hi[1];
+                for (int t = 0; t < NT; t++)
 #pragma unroll
-                            for (int t = 0; t < NT; t++)
-                                dot8(p[t], make_uint4(k0[i], k1[i], k0[i + 1], k1[i + 1]), qf[t][step][0], qf[t][step][1]);
+                    for (int x = 0; x < SUB; x++) s[t][x][0] = s[t][x][1] = 0.f;
+#pragma unroll
+                for (int x = 0; x < SUB; x++) {
+                    uint32_t dk[2][2];
+                    uint32_t kc[2][2 * NB];  // codes: a word of each 16 bytes of the rows j of both halves
+                    if constexpr (C::QUANT) {
+                        scale(C::OKS, x, 0, dk[0]);
+                        scale(C::OKS, x, 1, dk[1]);
+                        constexpr int CPR = C::RB / 16;
+                        if constexpr (CPR >= 4) {
+#pragma unroll
+                            for (int h = 0; h < 2; h++)
+#pragma unroll
+                                for (int g4 = 0; g4 < CPR; g4 += 4)
+                                    rows4(st + (kaddr ^ (g4 << 4)) + (16 * x + 8 * h) * C::RB, &kc[h][g4]);
+                        } else {  // (both halves' two chunks)
+                            uint32_t y[4];
+                            rows4(st + kaddr + 16 * x * C::RB, y);
+                            kc[0][0] = y[0], kc[0][1] = y[1], kc[1][0] = y[2], kc[1][1] = y[3];
                         }
+                    }
 #pragma unroll
-                        for (int t = 0; t < NT; t++) s[t][x][0] += p[t][0] + p[t][1], s[t][x][1] += p[t][2] + p[t][3];
-                    } else {
-                        uint32_t w[2][4];
+                    for (int b = 0; b < NB; b++) {
+                        if constexpr (TYPE == AF_F32) {
+                            float p[NT][4] = {};
+                            uint32_t hi[2][8], lo[2][8];
 #pragma unroll
-                        for (int h = 0; h < 2; h++) {
-                            if constexpr (TYPE == AF_F16) {
-                                shared128(st + C::kbyte(16 * x + 8 * h + j, (4 * b + c) * 16), w[h]);
-                            } else if constexpr (TYPE == AF_KV_Q8_0) {
+                            for (int h = 0; h < 2; h++) {
+                                shared128(st + C::kbyte(8 * h + j, (8 * b + c) * 16), hi[h]);
+                                shared128(st + C::kbyte(8 * h + j, (8 * b + 4 + c) * 16), hi[h] + 4);
 #pragma unroll
-                                for (int i = 0; i < 2; i++) codes2(kc[h][2 * b + i], w[h][2 * i], w[h][2 * i + 1]);
-                            } else {
-                                codes4(kc[h][b], w[h]);
+                                for (int i = 0; i < 8; i++) cut_tf32(__uint_as_float(hi[h][i]), hi[h][i], lo[h][i]);
                             }
-                        }
 #pragma unroll
-                        for (int t = 0; t < NT; t++) {
-                            float p[4];
-                            dot16z(p, make_uint4(w[0][0], w[1][0], w[0][1], w[1][1]), qf[t][2 * b][0], qf[t][2 * b][1]);
-                            dot16(p, make_uint4(w[0][2], w[1][2], w[0][3], w[1][3]), qf[t][2 * b + 1][0], qf[t][2 * b + 1][1]);
-                            const float s0 = p[0] + p[1], s1 = p[2] + p[3];
-                            if constexpr (C::QUANT) {
-                                const __half2 d0 = u_h2(dk[0][b / 2]), d1 = u_h2(dk[1][b / 2]);
-                                s[t][x][0] = fmaf(__half2float(b & 1 ? __high2half(d0) : __low2half(d0)), s0, s[t][x][0]);
-                                s[t][x][1] = fmaf(__half2float(b & 1 ? __high2half(d1) : __low2half(d1)), s1, s[t][x][1]);
-                            } else {
-                                s[t][x][0] += s0;
-                                s[t][x][1] += s1;
+                            for (int e = 0; e < 8; e++) {  // the small lo products first
+                                const int i = 2 * (e & 3), step = 4 * b + (e & 3);
+                                const uint32_t *k0 = e < 4 ? lo[0] : hi[0], *k1 = e < 4 ? lo[1] : hi[1];
+#pragma unroll
+                                for (int t = 0; t < NT; t++)
+                                    dot8(p[t], make_uint4(k0[i], k1[i], k0[i + 1], k1[i + 1]), qf[t][step][0], qf[t][step][1]);
+                            }
+#pragma unroll
+                            for (int t = 0; t < NT; t++) s[t][x][0] += p[t][0] + p[t][1], s[t][x][1] += p[t][2] + p[t][3];
+                        } else {
+                            uint32_t w[2][4];
+#pragma unroll
+                            for (int h = 0; h < 2; h++) {
+                                if constexpr (TYPE == AF_F16) {
+                                    shared128(st + C::kbyte(16 * x + 8 * h + j, (4 * b + c) * 16), w[h]);
+                                } else if constexpr (TYPE == AF_KV_Q8_0) {
+#pragma unroll
+                                    for (int i = 0; i < 2; i++) codes2(kc[h][2 * b + i], w[h][2 * i], w[h][2 * i + 1]);
+                                } else {
+                                    codes4(kc[h][b], w[h]);
+                                }
+                            }
+#pragma unroll
+                            for (int t = 0; t < NT; t++) {
+                                float p[4];
+                                dot16z(p, make_uint4(w[0][0], w[1][0], w[0][1], w[1][1]), qf[t][2 * b][0], qf[t][2 * b][1]);
+                                dot16(p, make_uint4(w[0][2], w[1][2], w[0][3], w[1][3]), qf[t][2 * b + 1][0], qf[t][2 * b + 1][1]);
+                                const float s0 = p[0] + p[1], s1 = p[2] + p[3];
+                                if constexpr (C::QUANT) {
+                                    const __half2 d0 = u_h2(dk[0][b / 2]), d1 = u_h2(dk[1][b / 2]);
+                                    s[t][x][0] = fmaf(__half2float(b & 1 ? __high2half(d0) : __low2half(d0)), s0, s[t][x][0]);
+                                    s[t][x][1] = fmaf(__half2float(b & 1 ? __high2half(d1) : __low2half(d1)), s1, s[t][x][1]);
+                                } else {
+                                    s[t][x][0] += s0;
+                                    s[t][x][1] += s1;
+                                }
                             }
                         }
                     }
                 }
-            }
             }
             // ---- K's place in the ring takes the stage NST ahead
             int phys = -1;
@@ -593,200 +611,200 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
             }
             copy_commit();
             if (work) {
-            copy_wait<2 * NST - 1>();
-            __syncwarp();  // V has landed
-            asm volatile("" ::: "memory");
-            uint32_t vs[SUB][2][2];
-            if constexpr (C::QUANT) {
+                copy_wait<2 * NST - 1>();
+                __syncwarp();  // V has landed
+                asm volatile("" ::: "memory");
+                uint32_t vs[SUB][2][2];
+                if constexpr (C::QUANT) {
 #pragma unroll
-                for (int x = 0; x < SUB; x++)
+                    for (int x = 0; x < SUB; x++)
 #pragma unroll
-                    for (int h = 0; h < 2; h++) scale(st + C::OVS, 16 * x + C::slot(h, j), vs[x][h]);
-            }
-            // ---- softmax; hidden slots have no score (and zeros as values)
-            seen |= see != 0;
-            if (see != 0xffffffffu) {
-#pragma unroll
-                for (int x = 0; x < SUB; x++)
-#pragma unroll
-                    for (int h = 0; h < 2; h++)
-                        if (!(see >> (16 * x + C::slot(h, j)) & 1)) {
-#pragma unroll
-                            for (int t = 0; t < NT; t++) s[t][x][h] = -CUDART_INF_F;
-                        }
-            }
-            float big[SUB][2];  // log2 of the slots' largest value scales
-            if constexpr (C::QUANT) {
-#pragma unroll
-                for (int x = 0; x < SUB; x++)
-#pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        __half2 m = __habs2(u_h2(vs[x][h][0]));
-                        if (NB == 4) m = __hmax2(m, __habs2(u_h2(vs[x][h][1])));
-                        big[x][h] = lg2a(fmaxf(fmaxf(__low2float(m), __high2float(m)), 0x1p-24f));
-                    }
-            }
-            bool move = false;
-            float mx[NT];
-#pragma unroll
-            for (int t = 0; t < NT; t++) {
-                mx[t] = -CUDART_INF_F;
-#pragma unroll
-                for (int x = 0; x < SUB; x++)
-#pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        if (TYPE != AF_F32) s[t][x][h] *= rowf[t];
-                        mx[t] = fmaxf(mx[t], C::QUANT ? s[t][x][h] + big[x][h] : s[t][x][h]);
-                    }
-                move |= mx[t] > m_ref[t] + kLazyP;
-            }
-            if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-                for (int t = 0; t < NT; t++) {
-                    float m = mx[t];
-                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                    if (m > m_ref[t]) {
-                        const float f = ex2t(m_ref[t] - m);
-                        m_ref[t] = m;
-                        l[t] *= f;
-#pragma unroll
-                        for (int i = 0; i < C::MT; i++)
-#pragma unroll
-                            for (int e = 0; e < 4; e++) o[t][i][e] *= f;
-                    }
+                        for (int h = 0; h < 2; h++) scale(C::OVS, x, h, vs[x][h]);
                 }
-            }
+                // ---- softmax; hidden slots have no score (and zeros as values)
+                seen |= see != 0;
+                if (see != 0xffffffffu) {
 #pragma unroll
-            for (int t = 0; t < NT; t++) {
-                const float mb = (m_ref[t] == -CUDART_INF_F ? 0.f : m_ref[t]) - kBiasP;
+                    for (int x = 0; x < SUB; x++)
 #pragma unroll
-                for (int x = 0; x < SUB; x++)
+                        for (int h = 0; h < 2; h++)
+                            if (!(see >> (16 * x + C::slot(h, j)) & 1)) {
 #pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        s[t][x][h] = ex2t(s[t][x][h] - mb);
-                        l[t] += s[t][x][h];
-                    }
-            }
-            // ---- output
-            if constexpr (TYPE == AF_F32) {
-                uint32_t pb[NT][2][2];  // p of slots c + 8 u and c + 4 + 8 u for column j: its head's hi or lo part
+                                for (int t = 0; t < NT; t++) s[t][x][h] = -CUDART_INF_F;
+                            }
+                }
+                float big[SUB][2];  // log2 of the slots' largest value scales
+                if constexpr (C::QUANT) {
 #pragma unroll
-                for (int t = 0; t < NT; t++)
-#pragma unroll
-                    for (int v = 0; v < 2; v++)
+                    for (int x = 0; x < SUB; x++)
 #pragma unroll
                         for (int h = 0; h < 2; h++) {
-                            const float p = __shfl_sync(0xffffffffu, s[t][0][v], 4 * (c + 4 * h) + (j >> 1));
-                            uint32_t hi, lo;
-                            split_tf32(p, hi, lo);
-                            pb[t][v][h] = j & 1 ? lo : hi;
+                            __half2 m = __habs2(u_h2(vs[x][h][0]));
+                            if (NB == 4) m = __hmax2(m, __habs2(u_h2(vs[x][h][1])));
+                            big[x][h] = lg2a(fmaxf(fmaxf(__low2float(m), __high2float(m)), 0x1p-24f));
                         }
+                }
+                bool move = false;
+                float mx[NT];
 #pragma unroll
-                for (int y = 0; y < D / 32; y++) {  // dims 32 y + 4 j .. + 3: two row tiles
-                    uint32_t lo[4][4], hi[4][4];
+                for (int t = 0; t < NT; t++) {
+                    mx[t] = -CUDART_INF_F;
 #pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        shared128(st + C::vbyte(c + 4 * k, (8 * y + j) * 16), hi[k]);
+                    for (int x = 0; x < SUB; x++)
 #pragma unroll
-                        for (int e = 0; e < 4; e++) cut_tf32(__uint_as_float(hi[k][e]), hi[k][e], lo[k][e]);
+                        for (int h = 0; h < 2; h++) {
+                            if (TYPE != AF_F32) s[t][x][h] *= rowf[t];
+                            mx[t] = fmaxf(mx[t], C::QUANT ? s[t][x][h] + big[x][h] : s[t][x][h]);
+                        }
+                    move |= mx[t] > m_ref[t] + kLazyP;
+                }
+                if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+                    for (int t = 0; t < NT; t++) {
+                        float m = mx[t];
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                        if (m > m_ref[t]) {
+                            const float f = ex2t(m_ref[t] - m);
+                            m_ref[t] = m;
+                            l[t] *= f;
+#pragma unroll
+                            for (int i = 0; i < C::MT; i++)
+#pragma unroll
+                                for (int e = 0; e < 4; e++) o[t][i][e] *= f;
+                        }
                     }
+                }
+#pragma unroll
+                for (int t = 0; t < NT; t++) {
+                    const float mb = (m_ref[t] == -CUDART_INF_F ? 0.f : m_ref[t]) - kBiasP;
+#pragma unroll
+                    for (int x = 0; x < SUB; x++)
+#pragma unroll
+                        for (int h = 0; h < 2; h++) {
+                            s[t][x][h] = ex2t(s[t][x][h] - mb);
+                            l[t] += s[t][x][h];
+                        }
+                }
+                // ---- output
+                if constexpr (TYPE == AF_F32) {
+                    uint32_t pb[NT][2][2];  // p of slots c + 8 u and c + 4 + 8 u for column j: its head's hi or lo part
 #pragma unroll
                     for (int t = 0; t < NT; t++)
 #pragma unroll
-                        for (int e = 0; e < 4; e += 2) {
-                            float sum[4];
-                            dot8z(sum, make_uint4(lo[0][e], lo[0][e + 1], lo[1][e], lo[1][e + 1]), pb[t][0][0], pb[t][0][1]);
-                            dot8(sum, make_uint4(lo[2][e], lo[2][e + 1], lo[3][e], lo[3][e + 1]), pb[t][1][0], pb[t][1][1]);
-                            dot8(sum, make_uint4(hi[0][e], hi[0][e + 1], hi[1][e], hi[1][e + 1]), pb[t][0][0], pb[t][0][1]);
-                            dot8(sum, make_uint4(hi[2][e], hi[2][e + 1], hi[3][e], hi[3][e + 1]), pb[t][1][0], pb[t][1][1]);
-                            add4(o[t][2 * y + e / 2], sum);
-                        }
-                }
-            } else if constexpr (TYPE == AF_F16) {
-                uint32_t pb[NT][2];
+                        for (int v = 0; v < 2; v++)
 #pragma unroll
-                for (int t = 0; t < NT; t++)
-#pragma unroll
-                    for (int h = 0; h < 2; h++) pb[t][h] = transpose8(hi_lo(s[t][0][h]));
-#pragma unroll
-                for (int y = 0; y < D / 64; y++) {  // dims 64 y + 8 j .. + 7: four row tiles
-                    uint32_t w[4][4];
-#pragma unroll
-                    for (int k = 0; k < 4; k++) shared128(st + C::vbyte(2 * c + (k & 1) + 8 * (k >> 1), (8 * y + j) * 16), w[k]);
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const uint4 v = make_uint4(__byte_perm(w[0][i], w[1][i], 0x5410), __byte_perm(w[0][i], w[1][i], 0x7632),
-                                                   __byte_perm(w[2][i], w[3][i], 0x5410), __byte_perm(w[2][i], w[3][i], 0x7632));
-#pragma unroll
-                        for (int t = 0; t < NT; t++) {
-                            float sum[4];
-                            dot16z(sum, v, pb[t][0], pb[t][1]);
-                            add4(o[t][4 * y + i], sum);
-                        }
-                    }
-                }
-            } else {
-                uint32_t vc[SUB][4];
-#pragma unroll
-                for (int b = 0; b < NB; b++) {
-                    uint32_t pb[NT][SUB][2];
-#pragma unroll
-                    for (int x = 0; x < SUB; x++) {
-                        float d[2];
-#pragma unroll
-                        for (int h = 0; h < 2; h++) {
-                            const __half2 w = u_h2(vs[x][h][b / 2]);
-                            d[h] = __half2float(b & 1 ? __high2half(w) : __low2half(w));
-                        }
-#pragma unroll
-                        for (int t = 0; t < NT; t++) {  // p d in two parts, of two slots at a time
-                            const float2 y = mul2(make_float2(s[t][x][0], s[t][x][1]), make_float2(d[0], d[1]));
-                            const float2 hi = make_float2(__uint_as_float(__float_as_uint(y.x) & 0xFFFFE000u), __uint_as_float(__float_as_uint(y.y) & 0xFFFFE000u));
-                            const float2 lo = fma2(hi, both(-1.f), y);
-                            pb[t][x][0] = transpose8(h2_u(__floats2half2_rn(hi.x, lo.x)));
-                            pb[t][x][1] = transpose8(h2_u(__floats2half2_rn(hi.y, lo.y)));
-                        }
-                    }
-                    float sum[NT][2][4];
-#pragma unroll
-                    for (int x = 0; x < SUB; x++) {
-                        uint32_t v[2][4];  // pair of slots, row of the two row tiles
-                        if constexpr (TYPE == AF_KV_Q8_0) {
-                            uint32_t y[4];  // dims j, j + 8, j + 16, j + 24 of four slots
-                            columns4(st + C::OV + (vaddr ^ (b << 5)) + 16 * x * C::RB, y);
-#pragma unroll
-                            for (int i = 0; i < 4; i++) codes2(y[i], v[0][i], v[1][i]);
-                        } else {
-                            if (b % 2 == 0) columns4(st + C::OV + (vaddr ^ (b << 4)) + 16 * x * C::RB, vc[x]);  // two blocks' bytes
-#pragma unroll
-                            for (int i = 0; i < 2; i++) {  // bytes j and j + 8 of the block: dims 2j, 2j + 1 and 16 more
-                                const uint32_t y = vc[x][2 * (b & 1) + i], lo = y & 0x0F0F0F0Fu, hi = y & 0xF0F0F0F0u;
-                                const __half2 f = __float2half2_rn(0.0625f), m72 = __float2half2_rn(-72.f);  // (1024 + 16 n) / 16 - 72
-                                v[0][2 * i] = hsub2u(__byte_perm(lo, 0x64646464u, 0x4140), 0x64086408u);
-                                v[1][2 * i] = hsub2u(__byte_perm(lo, 0x64646464u, 0x4342), 0x64086408u);
-                                v[0][2 * i + 1] = h2_u(__hfma2(u_h2(__byte_perm(hi, 0x64646464u, 0x4140)), f, m72));
-                                v[1][2 * i + 1] = h2_u(__hfma2(u_h2(__byte_perm(hi, 0x64646464u, 0x4342)), f, m72));
+                            for (int h = 0; h < 2; h++) {
+                                const float p = __shfl_sync(0xffffffffu, s[t][0][v], 4 * (c + 4 * h) + (j >> 1));
+                                uint32_t hi, lo;
+                                split_tf32(p, hi, lo);
+                                pb[t][v][h] = j & 1 ? lo : hi;
                             }
+#pragma unroll
+                    for (int y = 0; y < D / 32; y++) {  // dims 32 y + 4 j .. + 3: two row tiles
+                        uint32_t lo[4][4], hi[4][4];
+#pragma unroll
+                        for (int k = 0; k < 4; k++) {
+                            shared128(st + C::vbyte(c + 4 * k, (8 * y + j) * 16), hi[k]);
+#pragma unroll
+                            for (int e = 0; e < 4; e++) cut_tf32(__uint_as_float(hi[k][e]), hi[k][e], lo[k][e]);
                         }
 #pragma unroll
                         for (int t = 0; t < NT; t++)
 #pragma unroll
-                            for (int i = 0; i < 2; i++) {
-                                const uint4 w = make_uint4(v[0][2 * i], v[0][2 * i + 1], v[1][2 * i], v[1][2 * i + 1]);
-                                if (x == 0)
-                                    dot16z(sum[t][i], w, pb[t][x][0], pb[t][x][1]);
-                                else
-                                    dot16(sum[t][i], w, pb[t][x][0], pb[t][x][1]);
+                            for (int e = 0; e < 4; e += 2) {
+                                float sum[4];
+                                dot8z(sum, make_uint4(lo[0][e], lo[0][e + 1], lo[1][e], lo[1][e + 1]), pb[t][0][0], pb[t][0][1]);
+                                dot8(sum, make_uint4(lo[2][e], lo[2][e + 1], lo[3][e], lo[3][e + 1]), pb[t][1][0], pb[t][1][1]);
+                                dot8(sum, make_uint4(hi[0][e], hi[0][e + 1], hi[1][e], hi[1][e + 1]), pb[t][0][0], pb[t][0][1]);
+                                dot8(sum, make_uint4(hi[2][e], hi[2][e + 1], hi[3][e], hi[3][e + 1]), pb[t][1][0], pb[t][1][1]);
+                                add4(o[t][2 * y + e / 2], sum);
                             }
                     }
+                } else if constexpr (TYPE == AF_F16) {
+                    uint32_t pb[NT][2];
 #pragma unroll
                     for (int t = 0; t < NT; t++)
 #pragma unroll
-                        for (int i = 0; i < 2; i++) add4(o[t][2 * b + i], sum[t][i]);
+                        for (int h = 0; h < 2; h++) pb[t][h] = transpose8(hi_lo(s[t][0][h]));
+#pragma unroll
+                    for (int y = 0; y < D / 64; y++) {  // dims 64 y + 8 j .. + 7: four row tiles
+                        uint32_t w[4][4];
+#pragma unroll
+                        for (int k = 0; k < 4; k++) shared128(st + C::vbyte(2 * c + (k & 1) + 8 * (k >> 1), (8 * y + j) * 16), w[k]);
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            const uint4 v = make_uint4(__byte_perm(w[0][i], w[1][i], 0x5410), __byte_perm(w[0][i], w[1][i], 0x7632),
+                                                       __byte_perm(w[2][i], w[3][i], 0x5410), __byte_perm(w[2][i], w[3][i], 0x7632));
+#pragma unroll
+                            for (int t = 0; t < NT; t++) {
+                                float sum[4];
+                                dot16z(sum, v, pb[t][0], pb[t][1]);
+                                add4(o[t][4 * y + i], sum);
+                            }
+                        }
+                    }
+                } else {
+                    uint32_t vc[SUB][4];
+#pragma unroll
+                    for (int b = 0; b < NB; b++) {
+                        uint32_t pb[NT][SUB][2];
+#pragma unroll
+                        for (int x = 0; x < SUB; x++) {
+                            float d[2];
+#pragma unroll
+                            for (int h = 0; h < 2; h++) {
+                                const __half2 w = u_h2(vs[x][h][b / 2]);
+                                d[h] = __half2float(b & 1 ? __high2half(w) : __low2half(w));
+                            }
+#pragma unroll
+                            for (int t = 0; t < NT; t++) {  // p d in two parts, of two slots at a time
+                                const float2 y = mul2(make_float2(s[t][x][0], s[t][x][1]), make_float2(d[0], d[1]));
+                                const float2 hi = make_float2(__uint_as_float(__float_as_uint(y.x) & 0xFFFFE000u), __uint_as_float(__float_as_uint(y.y) & 0xFFFFE000u));
+                                const float2 lo = fma2(hi, both(-1.f), y);
+                                pb[t][x][0] = transpose8(h2_u(__floats2half2_rn(hi.x, lo.x)));
+                                pb[t][x][1] = transpose8(h2_u(__floats2half2_rn(hi.y, lo.y)));
+                            }
+                        }
+                        float sum[NT][2][4];
+#pragma unroll
+                        for (int x = 0; x < SUB; x++) {
+                            uint32_t v[2][4];  // pair of slots, row of the two row tiles
+                            if constexpr (TYPE == AF_KV_Q8_0) {
+                                uint32_t y[4];  // dims j, j + 8, j + 16, j + 24 of four slots
+                                columns4(st + C::OV + (vaddr ^ (b << 5)) + 16 * x * C::RB, y);
+#pragma unroll
+                                for (int i = 0; i < 4; i++) codes2(y[i], v[0][i], v[1][i]);
+                            } else {
+                                if (b % 2 == 0) columns4(st + C::OV + (vaddr ^ (b << 4)) + 16 * x * C::RB, vc[x]);  // two blocks' bytes
+#pragma unroll
+                                for (int i = 0; i < 2; i++) {  // bytes j and j + 8 of the block: dims 2j, 2j + 1 and 16 more
+                                    const uint32_t y = vc[x][2 * (b & 1) + i], lo = y & 0x0F0F0F0Fu, hi = y & 0xF0F0F0F0u;
+                                    const __half2 f = __float2half2_rn(0.0625f), m72 = __float2half2_rn(-72.f);  // (1024 + 16 n) / 16 - 72
+                                    v[0][2 * i] = hsub2u(__byte_perm(lo, 0x64646464u, 0x4140), 0x64086408u);
+                                    v[1][2 * i] = hsub2u(__byte_perm(lo, 0x64646464u, 0x4342), 0x64086408u);
+                                    v[0][2 * i + 1] = h2_u(__hfma2(u_h2(__byte_perm(hi, 0x64646464u, 0x4140)), f, m72));
+                                    v[1][2 * i + 1] = h2_u(__hfma2(u_h2(__byte_perm(hi, 0x64646464u, 0x4342)), f, m72));
+                                }
+                            }
+#pragma unroll
+                            for (int t = 0; t < NT; t++)
+#pragma unroll
+                                for (int i = 0; i < 2; i++) {
+                                    const uint4 w = make_uint4(v[0][2 * i], v[0][2 * i + 1], v[1][2 * i], v[1][2 * i + 1]);
+                                    if (x == 0)
+                                        dot16z(sum[t][i], w, pb[t][x][0], pb[t][x][1]);
+                                    else
+                                        dot16(sum[t][i], w, pb[t][x][0], pb[t][x][1]);
+                                }
+                        }
+#pragma unroll
+                        for (int t = 0; t < NT; t++)
+#pragma unroll
+                            for (int i = 0; i < 2; i++) add4(o[t][2 * b + i], sum[t][i]);
+                    }
                 }
-            }
             }
             // ---- V's place in the ring takes the stage NST ahead
             __syncwarp();
@@ -808,7 +826,7 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
                 fresh = true;
                 const bool done = begun && ends;
                 const int which = begun ? 1 : 0;
-                float* piece = left == 1 ? my_piece : far + ((size_t)blockIdx.x * NW + warp) * C::PIECE;  // (all copies are done)
+                float* piece = left == 1 ? my_piece : far + warp * C::PIECE;  // (all copies are done)
                 if (!done && lane == 0) sm_piece[warp][which] = make_int4(at.row, at.gi, left == 1 ? 1 : 2, ends);
 #pragma unroll
                 for (int t = 0; t < NT; t++) {
@@ -870,7 +888,7 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
     const unsigned used0 = __ballot_sync(0xffffffffu, p0.z != 0), ends0 = __ballot_sync(0xffffffffu, p0.z && p0.w);
     unsigned heads1 = __ballot_sync(0xffffffffu, p1.z != 0);  // warps in which a chain begins
     const float* const near_by = reinterpret_cast<const float*>(smem + min(lane, NW - 1) * NST * C::STAGE);
-    const float* const far_off = far + ((size_t)blockIdx.x * NW + min(lane, NW - 1)) * C::PIECE;
+    const float* const far_off = far + min(lane, NW - 1) * C::PIECE;
     int job = warp;                                             // heads before this warp's next one
     int4 own0 = make_int4(0, 0, 0, 0), own1 = own0;  // items of which the CTA leaves pieces 0 and 1 (.z: it does)
     // A piece 0 goes on with an earlier warp's item; the CTA's first one goes on with another CTA's.
@@ -1022,14 +1040,12 @@ cudaError_t launch_attn_paged_type(const PagedArgs& a, int ctas, cudaStream_t s)
 template <int TYPE, int D, int NT>
 cudaError_t paged_go(const PagedArgs& a, int ctas, cudaStream_t s) {
     using C = PagedCfg<TYPE, D, NT>;
-    constexpr int ring = C::NW * C::NST * C::STAGE;
-    static_assert(ring + (kPagedMaxRows + 1) * 4 <= 227 * 1024 - 256 - C::NW * (32 + 16 * C::NST + 8), "shared memory");
     static_assert(C::NW * C::PIECE <= 8 * paged_piece_floats(D), "workspace");
     auto k = attn_paged_kernel<TYPE, D, NT>;
     static SmemOptIn opt;
-    cudaError_t e = opt((const void*)k, ring + (kPagedMaxRows + 1) * 4);
+    cudaError_t e = opt((const void*)k, C::FIXED + C::ROWS);
     if (e) return e;
-    return launch_chained(k, dim3(ctas), C::NW * 32, ring + (a.n + 1) * 4 + (a.n <= kPagedKept ? a.n * 8 : 0), s, a);
+    return launch_chained(k, dim3(ctas), C::NW * 32, C::FIXED + (a.n + 1) * 4 + (a.n <= kPagedKept ? a.n * 8 : 0), s, a);
 }
 
 #define AF_PAGED_INSTANTIATE(TYPE)                                                                    \

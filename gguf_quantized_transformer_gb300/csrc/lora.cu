@@ -436,10 +436,14 @@ __global__ void __launch_bounds__(kThreads, NST == 2 ? 1 : 2) lora_expand_kernel
         if (tile.x >= 0 && warp < tile.z) {
             const float* p = a.ws + ((int64_t)tile.y + warp) * a.rank + lane;
             const int64_t stride = (int64_t)rows * a.rank;
-            if (tile.z <= kWarps && a.rank <= 32) {  // (one value a lane: four ranges on their way)
-                if (lane < a.rank)
+            if (tile.z <= kWarps) {  // (a row a warp: four ranges on their way)
 #pragma unroll 4
-                    for (int s = 0; s < splits; s++) h[0][0] += __ldcg(p + s * stride);
+                for (int s = 0; s < splits; s++)
+#pragma unroll
+                    for (int q = 0; q < HQ; q++) {
+                        if (32 * q >= a.rank) break;
+                        if (lane + 32 * q < a.rank) h[0][q] += __ldcg(p + s * stride + 32 * q);
+                    }
             } else {
 #pragma unroll 1
                 for (int s = 0; s < splits; s++, p += stride)
