@@ -1282,6 +1282,7 @@ int check_lora_sizes(int32_t rank, int32_t K, int32_t N) {
     if (rank <= 0 || K <= 0 || N <= 0) return fail(AF_EINVAL, "sizes must be positive");
     if (rank % 8 || rank > kLoraMaxRank) return fail(AF_ENOTIMPL, "rank %d must be a multiple of 8 up to %d", rank, kLoraMaxRank);
     if (K % 32) return fail(AF_ENOTIMPL, "K %d must be a multiple of 32", K);
+    if (K > (1 << 24) || N > (1 << 24)) return fail(AF_ENOTIMPL, "K and N up to 2^24");  // (runs of columns are counted in 32 bits)
     return AF_OK;
 }
 

@@ -563,10 +563,11 @@ int af_attention_paged(const float* q_dev, int64_t ldq, const void* k_cache, con
  *   y_dev     fp32 [n] rows, ldy apart.  Rows without an adapter are the base's
  *   ws_dev    scratch of af_lora_workspace(n, n_adapters, rank, K, N) bytes, 256-byte aligned, of any contents; calls that
  *             may overlap in time need scratch of their own
- * Precision: products of two parts of 11 bits each (2^-20 of the sum of the products' magnitudes), sums in fp32.  A row's
- * result does not depend on the other rows but for the order in which K's sums are joined; its bits do not change from call
- * to call with the same plan.
- * 1 <= n <= 65536, 1 <= n_adapters <= 4096; rank a multiple of 8 up to 128 (pad with rank_dev); K a multiple of 32, N any.
+ * Precision: x, fp32 weights and A x keep 2^-22 of each value, or 2^-38 of the largest of 32 neighbours along K (of a row of
+ * A x) where that is more; sums are fp32's.  A row's result depends on the other rows only through the order in which K's
+ * sums are joined; its bits do not change from call to call with the same plan.
+ * 1 <= n <= 65536, 1 <= n_adapters <= 4096; rank a multiple of 8 up to 128 (pad with rank_dev); K a multiple of 32, N any,
+ * both up to 2^24.
  * x_dev, a_dev, b_dev are 16-byte aligned and ldx a multiple of 4; base_dev and y_dev 4-byte aligned (vectors of 16 bytes
  * are moved where they, N, ldb and ldy allow it).  Asynchronous on `stream`, allocate nothing, can be captured (the first
  * call on a device loads the kernels: make it before a capture).  Errors: AF_EINVAL, AF_ERANGE, AF_ENOTIMPL, AF_ECUDA.

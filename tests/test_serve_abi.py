@@ -37,10 +37,10 @@ BAD = {
                            ("ws", P + 16, E), ("out", None, E), ("out", P + 4, E), ("ldo", 4092, E), ("ldo", 4097, E)],
     "af_lora_plan": [("ids", None, E), ("ids", P + 1, E), ("n", 0, R), ("n", 65537, R), ("adapters", 0, R), ("adapters", 4097, R),
                      ("plan", None, E), ("plan", P + 4, E), ("bytes", 15, E)],
-    "af_lora": [("x", None, E), ("x", P + 4, E), ("ldx", 511, E), ("ldx", 514, E), ("n", 0, R), ("n", 65537, R), ("plan", None, E),
+    "af_lora": [("x", None, E), ("x", P + 4, E), ("ldx", 508, E), ("ldx", 514, E), ("n", 0, R), ("n", 65537, R), ("plan", None, E),
                 ("plan", P + 8, E), ("a", None, E), ("a", P + 2, E), ("b", None, E), ("b", P + 8, E), ("dtype", 2, E),
                 ("scale", P + 1, E), ("ranks", P + 2, E), ("adapters", 0, R), ("adapters", 4097, R), ("rank", 0, E), ("rank", 12, N),
-                ("rank", 136, N), ("K", 0, E), ("K", 500, N), ("N", 0, E), ("N", 97, E), ("base", P + 2, E), ("ldb", 95, E),
+                ("rank", 136, N), ("K", 0, E), ("K", 2 ** 24 + 32, N), ("N", 2 ** 24 + 1, N), ("K", 500, N), ("N", 0, E), ("N", 97, E), ("base", P + 2, E), ("ldb", 95, E),
                 ("y", None, E), ("y", P + 1, E), ("ldy", 95, E), ("ws", None, E), ("ws", P + 16, E), ("wsb", 100, E)],
 }
 
