@@ -172,6 +172,24 @@ def test_kv_pages_bad_page_numbers_lead_nowhere(af):
     assert (got[0] == -1).sum() >= 5 and got[0].max() < n_pages * P
 
 
+@pytest.mark.parametrize("shift", [0, 1])
+def test_kv_pages_of_many_requests_and_unaligned_rows(af, shift):
+    """The most requests a call takes, no rows at all, and row arrays that begin at any int."""
+    rng = np.random.default_rng(13)
+    for n, P, rows in ((65536, 16, 70001), (2049, 8, 3000), (9, 4, 0), (700, 16, 701)):
+        ln = rng.integers(0, 40, n)
+        new = np.where(rng.random(n) < 0.1, -1, 1) if rows else np.zeros(n, int)
+        n_pages, table, free, pool = random_pool(rng, ln, P, 12, n)
+        want = pages_ref(ln, new, P, n_pages, 12, pool, free, table, rows)
+        d = [i32(v) for v in (ln, new, pool, free, table)]
+        start, outs = i32(np.zeros(n + 1)), [i32(np.full(rows + 9, 77)) for _ in range(3)]
+        ws = torch.full((af.af_kv_pages_workspace(n),), 0xFF, dtype=torch.uint8, device="cuda")
+        af.af_kv_pages(d[0], d[1], n, P, n_pages, d[2], d[3], d[4], 12, d[0], d[2], start, *[t[shift:] for t in outs], rows, ws, ws.numel())
+        got = [t.cpu().numpy() for t in outs]
+        assert all((g[:shift] == 77).all() and (g[shift + rows:] == 77).all() for g in got)
+        same([g[shift:shift + rows] for g in got] + [t.cpu().numpy() for t in (start, d[0], d[2], d[4], d[3])], want)
+
+
 def test_kv_pages_many_steps(af):
     """A loop that serves requests: pages are never lost, shared or outside the pool; captured once and replayed."""
     rng = np.random.default_rng(3)
@@ -413,6 +431,73 @@ def test_attention_paged_long_and_many(af, t, H, KVH, D, P, lens):
     assert err <= tol
 
 
+@pytest.mark.parametrize("t", ["f32", "q4_0"])
+@pytest.mark.parametrize("n,width", [(2048, 4), (64, 600000), (1, 1 << 26)])
+def test_attention_paged_most_rows_and_widest_tables(af, t, n, width):
+    """The most rows of a call, of a few requests, and tables so wide that stages are counted in 64 bits."""
+    rng = np.random.default_rng(14)
+    kvh, H, D, P, lens = 1, 64, 64, 16, [40, 64, 7]
+    c = Paged(af, t, rng, kvh, D, P, lens, extra=0)
+    reqs = min(3, max(1, (1 << 27) // width))
+    table = torch.full((reqs, width), -1, dtype=torch.int32, device="cuda")
+    table[:, :c.table.shape[1]] = i32(c.table[:reqs])
+    seq = rng.integers(0, reqs, n)
+    pos = np.array([rng.integers(-1, lens[s]) for s in seq])
+    q = rng.standard_normal((n, H, D)).astype(np.float32)
+    qd, out = _dev(q.reshape(n, -1)), torch.full((n, H * D), 9.0, device="cuda")
+    ws = torch.full((af.af_attention_paged_workspace(H, kvh, D),), 0xFF, dtype=torch.uint8, device="cuda")
+    af.af_attention_paged(qd, H * D, *c.cache, af.KVTYPE[t], H, kvh, D, P, c.n_pages, table, width, reqs, i32(seq), i32(pos), n, ws,
+                          ws.numel(), out, H * D)
+    ref = attn_ref_gpu(q, c, [c.slots[s][:p + 1] for s, p in zip(seq, pos)])
+    assert np.abs(out.cpu().numpy().reshape(ref.shape) - ref).max() <= attn_tol(q, c.k, c.v)
+
+
+@pytest.mark.parametrize("t,D,slots", [("f32", 128, 1 << 21), ("f16", 64, 1 << 24), ("q8_0", 128, 1 << 24), ("q4_0", 64, 1 << 26)])
+def test_attention_paged_far_into_a_large_cache(af, t, D, slots):
+    """Pages whose bytes lie past 32 bits."""
+    rng = np.random.default_rng(15)
+    kvh, H, P, m = 5 if t == "f32" else 4, 20 if t == "f32" else 16, 16, 100
+    size = {"f32": 4 * D, "f16": 2 * D, "q8_0": D, "q4_0": D // 2}[t]
+    assert kvh * slots * size > 1 << 32
+    if t in ("f32", "f16"):
+        cache = [x for _ in range(2) for x in (torch.empty(kvh, slots, D, dtype=torch.float32 if t == "f32" else torch.float16,
+                                                           device="cuda"), None)]
+    else:
+        cache = [x for _ in range(2) for x in (torch.empty(kvh, slots, size, dtype=torch.uint8, device="cuda"),
+                                               torch.empty(kvh, slots, D // 32, dtype=torch.float16, device="cuda"))]
+    n_pages = slots // P
+    pages = np.array([[n_pages - 1, 0, n_pages - 3, n_pages // 2, n_pages - 2, 1, n_pages - 9]])
+    at = (pages[0, np.arange(m) // P] * P + np.arange(m) % P).astype(np.int32)
+    k, v = (rng.standard_normal((m, kvh * D)).astype(np.float32) for _ in range(2))
+    write(af, t, cache, _dev(k), _dev(v), kvh, D, slots, _dev(at))
+    q = rng.standard_normal((1, H, D)).astype(np.float32)
+    got = attend(af, t, cache, q, kvh, P, n_pages, pages, [m - 1]).cpu().numpy().reshape(1, H, D)
+    kh, vh = (held(x.reshape(m, kvh, D), t).transpose(1, 0, 2) for x in (k, v))
+    ref = attn_ref(q.astype(np.float64), kh, vh, [np.arange(m)])
+    assert np.abs(got - ref).max() <= attn_tol(q, kh, vh)
+
+
+@pytest.mark.parametrize("t", KV)
+def test_attention_paged_queries_that_are_not_finite(af, t):
+    """A row's query with a NaN, an infinity or fp32's extremes does nothing to the other rows and heads."""
+    rng = np.random.default_rng(16)
+    P, kvh, H, D, lens = 16, 2, 8, 64, [300, 40, 500, 33]
+    c = Paged(af, t, rng, kvh, D, P, lens)
+    q = rng.standard_normal((4, H, D)).astype(np.float32)
+    pos = np.array(lens) - 1
+    clean = attend(af, t, c.cache, q, kvh, P, c.n_pages, c.table, pos).cpu().numpy().reshape(q.shape)
+    bad = q.copy()
+    bad[0, 3, 5], bad[2, 0, 0], bad[3, 7] = np.nan, np.inf, 0
+    bad[1, 2] *= np.float32(1e-41)
+    got = attend(af, t, c.cache, bad, kvh, P, c.n_pages, c.table, pos).cpu().numpy().reshape(q.shape)
+    same_q = (bad == q).all(-1)
+    assert np.array_equal(got[same_q], clean[same_q])
+    assert not np.isfinite(got[0, 3]).any() and not np.isfinite(got[2, 0]).any()
+    for r, h in ((1, 2), (3, 7)):  # scores of zero: the mean of the values
+        want = c.v[h // 4][c.slots[r]].mean(0)
+        assert np.abs(got[r, h] - want).max() <= 2.0 ** -19 * np.abs(c.v).max()
+
+
 @pytest.mark.parametrize("t", KV)
 @pytest.mark.parametrize("D,m", [(128, 30000), (64, 8000)])
 def test_attention_paged_long_sums(af, t, D, m):
@@ -635,6 +720,27 @@ def test_lora_sizes_of_values(af, dtype):
     hit[[7, 22]] = True
     hit |= ids == 4
     assert torch.equal(y[~hit], clean[~hit]) and not torch.isfinite(y[hit]).any()
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+def test_lora_values_far_apart(af, dtype):
+    """One value of x, of A or of A x that is far larger than its neighbours costs them no bits that the sums would keep: the others
+    are down to 2^-30 of it, and only they meet weights that are not zero."""
+    n, m, r, K, N = 3, 1, 16, 64, 40
+    g = torch.Generator(device="cuda").manual_seed(9)
+    x = torch.randn(n, K, generator=g, device="cuda")
+    a = torch.randn(m, r, K, generator=g, device="cuda")
+    b = torch.randn(m, N, r, generator=g, device="cuda")
+    x[:, ::32] *= 2.0 ** 15
+    a[:, :, ::32] = 0
+    a[:, 3] *= 2.0 ** 10  # a rank of h far above the others, which B does not use
+    b[:, :, 3] = 0
+    a, b = a.to(dtype), b.to(dtype)
+    y = torch.empty(n, N, device="cuda")
+    ids = torch.zeros(n, dtype=torch.int32, device="cuda")
+    lora_call(af, x, ids, a, b, None, None, None, y, N)
+    ref, tol = lora_ref(x, ids, a, b, None, None, torch.zeros(n, N, device="cuda"))
+    assert ((y.double() - ref).abs() <= tol).all()
 
 
 @pytest.mark.parametrize("n,m", [(1, 1), (5000, 1), (5000, 4096), (65536, 3), (4097, 900), (1023, 4)])
