@@ -1,5 +1,7 @@
 // Paged attention: the dispatch by cache type (attn_paged_impl.cuh).
 #include <atomic>
+#include <chrono>
+#include <exception>
 #include <random>
 
 #include "attn_paged_impl.cuh"
@@ -23,8 +25,13 @@ namespace {
 // 2^-48.
 unsigned long long next_mark() {
     static std::atomic<unsigned long long> at([] {
-        std::random_device r;
-        return ((unsigned long long)r() << 32 | r()) * 0x9E3779B97F4A7C15ull;
+        unsigned long long seed = (unsigned long long)std::chrono::steady_clock::now().time_since_epoch().count();
+        try {
+            std::random_device r;
+            seed ^= (unsigned long long)r() << 32 | r();
+        } catch (const std::exception&) {  // (no source of randomness: the clock's count stands)
+        }
+        return seed * 0x9E3779B97F4A7C15ull;
     }());
     return at.fetch_add(0x9E3779B97F4Bull) & 0xFFFFFFFFFFFFull;
 }

@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kScan) kv_pages_scan_kernel(PagesArgs a) {
 #pragma unroll
         for (int k = 0; k < 3; k++) before[k] += total[k];
         const bool served = fits && (need == 0 || taken <= count);
-        const bool ended = in && ends && sound && (int64_t)count + returned <= a.n_pages;
+        const bool ended = in && ends && sound && (back == 0 || (int64_t)count + returned <= a.n_pages);
         if (in) {
             const int start = (int)clamp_int(rows - grow);
             const int4 q = make_int4(served ? (int)(need ? taken - need : 0) : ended ? kEnded : kRefused, len, have,
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kScan) kv_pages_scan_kernel(PagesArgs a) {
             else
                 a.ws[i] = q;
             if (served && need) atomicMax(&sm_taken, (int)taken);
-            if (ended) atomicMax(&sm_returned, (int)returned);
+            if (ended && back) atomicMax(&sm_returned, (int)returned);
             if (!served && !ended) atomicAdd(&sm_refused, 1);
         }
         __syncthreads();

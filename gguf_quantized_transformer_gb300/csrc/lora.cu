@@ -35,25 +35,24 @@ __host__ __device__ inline int64_t plan_order(int max_tiles) { return 4 * (int64
 
 // ---------------------------------------------------------------- plan
 
-__device__ __forceinline__ int cta_scan(int x, int& total) {  // inclusive
-    __shared__ int part[kPlanThreads / 32];
+constexpr int kTileBits = 14;  // rows and tiles are summed in one word: 17 bits of rows, 13 of tiles
+constexpr unsigned kTileMask = (1u << kTileBits) - 1;
+static_assert(kLoraMaxRows / kLoraTile + kLoraMaxAdapters + 1 <= (int)kTileMask && kLoraMaxRows < 1 << (32 - kTileBits), "");
+
+__device__ __forceinline__ unsigned cta_scan(unsigned x, unsigned& total) {  // inclusive
+    __shared__ unsigned part[kPlanThreads / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        const unsigned y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
     __syncthreads();
     if (lane == 31) part[warp] = x;
     __syncthreads();
-    int before = 0, sum = 0;
-#pragma unroll
-    for (int w = 0; w < kPlanThreads / 32; w++) {
-        if (w < warp) before += part[w];
-        sum += part[w];
-    }
-    total = sum;
-    return x + before;
+    const unsigned y = part[lane];
+    total = __reduce_add_sync(0xffffffffu, y);
+    return x + __reduce_add_sync(0xffffffffu, lane < warp ? y : 0u);
 }
 
 __global__ void __launch_bounds__(kPlanThreads) lora_plan_kernel(const int* __restrict__ ids, int n, int adapters, int max_tiles,
@@ -62,15 +61,17 @@ __global__ void __launch_bounds__(kPlanThreads) lora_plan_kernel(const int* __re
     const int t = threadIdx.x, lane = t & 31;
     pdl_launch_dependents();
     pdl_wait();
+    // a row's adapter; those without one count as the last, -1 behind the last row
+    auto bucket = [&](int i) {
+        const int id = i < n ? __ldcg(ids + i) : 0;
+        return i >= n ? -1 : id >= 0 && id < adapters ? id : adapters;
+    };
+    const int mine = bucket(t);
     for (int i = t; i <= adapters; i += kPlanThreads) count[i] = 0;
     __syncthreads();
-    // rows of each adapter (those without one count as the last), a warp's equal ones at once
-    auto bucket = [&](int i) {
-        const int id = __ldcg(ids + i);
-        return id >= 0 && id < adapters ? id : adapters;
-    };
+    // rows of each adapter, a warp's equal ones at once
     for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
-        const int i = i0 + t, b = i < n ? bucket(i) : -1;
+        const int b = i0 ? bucket(i0 + t) : mine;
         const unsigned same = __match_any_sync(0xffffffffu, b);
         if (b >= 0 && lane == __ffs(same) - 1) atomicAdd(&count[b], __popc(same));
     }
@@ -78,14 +79,12 @@ __global__ void __launch_bounds__(kPlanThreads) lora_plan_kernel(const int* __re
     int rows = 0, tiles = 0;
     const int bare = count[adapters];
     for (int i0 = 0; i0 <= adapters; i0 += kPlanThreads) {
-        const int i = i0 + t, c = i <= adapters ? count[i] : 0;
-        int total;
-        const int r = cta_scan(c, total) + rows;
-        rows += total;
-        const int k = (c + kLoraTile - 1) / kLoraTile, f = cta_scan(k, total) + tiles;
-        tiles += total;
-        __syncthreads();
-        if (i <= adapters) count[i] = r - c, first[i] = f - k;  // the adapter's first row and tile
+        const int i = i0 + t, c = i <= adapters ? count[i] : 0, k = (c + kLoraTile - 1) / kLoraTile;
+        unsigned total;
+        const unsigned both = cta_scan((unsigned)c << kTileBits | (unsigned)k, total);
+        if (i <= adapters) count[i] = rows + (int)(both >> kTileBits) - c, first[i] = tiles + (int)(both & kTileMask) - k;
+        rows += (int)(total >> kTileBits);
+        tiles += (int)(total & kTileMask);
     }
     if (t == 0) {
         first[adapters + 1] = tiles;
@@ -108,7 +107,7 @@ __global__ void __launch_bounds__(kPlanThreads) lora_plan_kernel(const int* __re
     __syncthreads();
     int* const order = plan + plan_order(max_tiles);
     for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
-        const int i = i0 + t, b = i < n ? bucket(i) : -1;
+        const int i = i0 + t, b = i0 ? bucket(i) : mine;
         const unsigned same = __match_any_sync(0xffffffffu, b);
         const int lead = __ffs(same) - 1;
         int at = 0;
@@ -300,11 +299,13 @@ __global__ void __launch_bounds__(kShrinkWarps * 32, 1) lora_shrink_kernel(LoraA
     constexpr int RR = 16 * MT, PAD = kLoraTile + 2, es = F16 ? 2 : 4;
     static_assert(RR * PAD * 4 <= kRing, "the sums fit the rings");
     extern __shared__ __align__(16) float sm_sum[];  // the warps' rings, then [warps][RR][PAD]
-    __shared__ int sm_row[kLoraTile];
+    __shared__ int sm_row[kLoraTile], sm_order[kShrinkWarps * 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int* plan = (const int*)a.plan;
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();  // (behind the wait: expand reads what is older than this kernel before its own)
+    const int* const order = plan + plan_order(max_tiles);
+    const int early_row = tid < a.n ? __ldcg(order + tid) : 0;
     const int4 head = __ldcg(reinterpret_cast<const int4*>(plan));
     const int4 early = first_tiles(plan, lane, max_tiles);
     const int tiles = head.y, rows = head.z, rt = (a.rank + RR - 1) / RR;
@@ -313,23 +314,25 @@ __global__ void __launch_bounds__(kShrinkWarps * 32, 1) lora_shrink_kernel(LoraA
         const int split = item % splits, rest = item / splits, r0 = rest % rt * RR;
         const int4 tile = tile_of(plan, rest / rt, early);
         __syncthreads();  // (the previous item's sums and rows have been read)
-        if (tid < tile.z) sm_row[tid] = __ldcg(plan + plan_order(max_tiles) + tile.y + tid);
+        sm_order[tid] = early_row;
+        const int* const row = tile.y + tile.z <= kShrinkWarps * 32 ? sm_order + tile.y : sm_row;
+        if (row == sm_row && tid < tile.z) sm_row[tid] = __ldcg(order + tile.y + tid);
         const int rank = rank_of(a, tile.x);
         __syncthreads();
         const uint8_t* w = (const uint8_t*)a.a + ((int64_t)tile.x * a.rank + r0) * a.K * es;
         const int c0 = (int)((int64_t)chunks * split / splits), c1 = (int)((int64_t)chunks * (split + 1) / splits);
         const uint32_t ring = smem_u32(sm_sum) + warp * kRing;
         if (tile.z <= 8)
-            shrink_tile<F16, MT, 1>(a, sm_row, tile.z, w, rank - r0, c0, c1, ring, sm_sum, PAD);
+            shrink_tile<F16, MT, 1>(a, row, tile.z, w, rank - r0, c0, c1, ring, sm_sum, PAD);
         else
-            shrink_tile<F16, MT, 4>(a, sm_row, tile.z, w, rank - r0, c0, c1, ring, sm_sum, PAD);
+            shrink_tile<F16, MT, 4>(a, row, tile.z, w, rank - r0, c0, c1, ring, sm_sum, PAD);
         __syncthreads();
         for (int i = tid; i < RR * tile.z; i += kShrinkWarps * 32) {
-            const int r = i % RR, row = i / RR;
+            const int r = i % RR, x = i / RR;
             float sum = 0.f;
 #pragma unroll
-            for (int w = 0; w < kShrinkWarps; w++) sum += sm_sum[(w * RR + r) * PAD + row];
-            if (r0 + r < a.rank) a.ws[((int64_t)split * rows + tile.y + row) * a.rank + r0 + r] = sum;
+            for (int w = 0; w < kShrinkWarps; w++) sum += sm_sum[(w * RR + r) * PAD + x];
+            if (r0 + r < a.rank) a.ws[((int64_t)split * rows + tile.y + x) * a.rank + r0 + r] = sum;
         }
     }
 }
@@ -394,7 +397,6 @@ __global__ void __launch_bounds__(kThreads, NST == 2 ? 1 : 2) lora_expand_kernel
     const uint32_t ring = smem_u32(sm_h) + steps * 2 * 64 * 16 + warp * NST * stage;
     const int* plan = (const int*)a.plan;
     pdl_launch_dependents();
-    pdl_wait();
     const int4 head = __ldcg(reinterpret_cast<const int4*>(plan));
     const int4 early = first_tiles(plan, lane, max_tiles);
     const int tiles = a.base && a.base == a.y ? head.y : head.x;  // in place, rows without an adapter stay as they are
@@ -406,7 +408,10 @@ __global__ void __launch_bounds__(kThreads, NST == 2 ? 1 : 2) lora_expand_kernel
     int64_t item, last;
     if (each_tile && (int64_t)((cols + each_tile - 1) / each_tile) * ctas <= items + (int64_t)kSetup * ctas) {
         const int which = me / each_tile, part = me - which * each_tile;
-        if (which >= tiles) return;
+        if (which >= tiles) {
+            pdl_wait();  // (the kernel does not end before shrink)
+            return;
+        }
         item = (int64_t)which * cols + (unsigned)cols * (unsigned)part / (unsigned)each_tile;
         last = (int64_t)which * cols + (unsigned)cols * (unsigned)(part + 1) / (unsigned)each_tile;
     } else {
@@ -421,43 +426,12 @@ __global__ void __launch_bounds__(kThreads, NST == 2 ? 1 : 2) lora_expand_kernel
         const int run0 = (int)(item - (int64_t)which * cols), run1 = (int)min((int64_t)cols, run0 + (last - item));
         item += run1 - run0;
         const int4 tile = tile_of(plan, which, early);
-        // what depends on the tile alone, all at once: its rows, rank and scale, h (a warp takes every eighth row, a lane every 32nd
-        // rank) and the first weights
+        // what shrink does not write comes before the wait: the tile's rows, rank and scale, the first weights and the base's rows
         int my_row = 0;
         if (tid < tile.z) my_row = __ldcg(plan + plan_order(max_tiles) + tile.y + tid);
         const int rank = tile.x < 0 ? 0 : rank_of(a, tile.x);
         const float scale = tile.x >= 0 && a.scale ? __ldcg(a.scale + tile.x) : 1.f;
         const int mt = tile.z > 16 ? 2 : 1;
-        float h[HR][HQ];
-#pragma unroll
-        for (int i = 0; i < HR; i++)
-#pragma unroll
-            for (int q = 0; q < HQ; q++) h[i][q] = 0.f;
-        if (tile.x >= 0 && warp < tile.z) {
-            const float* p = a.ws + ((int64_t)tile.y + warp) * a.rank + lane;
-            const int64_t stride = (int64_t)rows * a.rank;
-            if (tile.z <= kWarps) {  // (a row a warp: four ranges on their way)
-#pragma unroll 4
-                for (int s = 0; s < splits; s++)
-#pragma unroll
-                    for (int q = 0; q < HQ; q++) {
-                        if (32 * q >= a.rank) break;
-                        if (lane + 32 * q < a.rank) h[0][q] += __ldcg(p + s * stride + 32 * q);
-                    }
-            } else {
-#pragma unroll 1
-                for (int s = 0; s < splits; s++, p += stride)
-#pragma unroll
-                    for (int i = 0; i < HR; i++) {
-                        if (warp + kWarps * i >= tile.z) break;
-#pragma unroll
-                        for (int q = 0; q < HQ; q++) {
-                            if (32 * q >= a.rank) break;
-                            if (lane + 32 * q < a.rank) h[i][q] += __ldcg(p + (int64_t)kWarps * i * a.rank + 32 * q);
-                        }
-                    }
-            }
-        }
         const int groups = (rank + 8 * V - 1) / (8 * V), rank_bytes = rank * es;
         auto fetch_b = [&](int run, int slot) {
             const uint32_t dst = ring + slot * stage + (VEC ? 2048 : 0);
@@ -495,6 +469,38 @@ __global__ void __launch_bounds__(kThreads, NST == 2 ? 1 : 2) lora_expand_kernel
         for (int i = 0; i < NST; i++) {
             if (run0 + i < run1) fetch_base(run0 + i, i);
             copy_commit();
+        }
+        // h: a warp takes every eighth row, a lane every 32nd rank
+        pdl_wait();
+        float h[HR][HQ];
+#pragma unroll
+        for (int i = 0; i < HR; i++)
+#pragma unroll
+            for (int q = 0; q < HQ; q++) h[i][q] = 0.f;
+        if (tile.x >= 0 && warp < tile.z) {
+            const float* p = a.ws + ((int64_t)tile.y + warp) * a.rank + lane;
+            const int64_t stride = (int64_t)rows * a.rank;
+            if (tile.z <= kWarps) {  // (a row a warp: four ranges on their way)
+#pragma unroll 4
+                for (int s = 0; s < splits; s++)
+#pragma unroll
+                    for (int q = 0; q < HQ; q++) {
+                        if (32 * q >= a.rank) break;
+                        if (lane + 32 * q < a.rank) h[0][q] += __ldcg(p + s * stride + 32 * q);
+                    }
+            } else {
+#pragma unroll 1
+                for (int s = 0; s < splits; s++, p += stride)
+#pragma unroll
+                    for (int i = 0; i < HR; i++) {
+                        if (warp + kWarps * i >= tile.z) break;
+#pragma unroll
+                        for (int q = 0; q < HQ; q++) {
+                            if (32 * q >= a.rank) break;
+                            if (lane + 32 * q < a.rank) h[i][q] += __ldcg(p + (int64_t)kWarps * i * a.rank + 32 * q);
+                        }
+                    }
+            }
         }
         // h as operands: value i of lane cc's 2 V in group g is rank 8 V g + 2 V cc + i, its pairs those of steps 0, 0, 1, 1
         const int held = groups * 8 * V;
@@ -612,6 +618,7 @@ __global__ void __launch_bounds__(kThreads, NST == 2 ? 1 : 2) lora_expand_kernel
             slot = slot + 1 == NST ? 0 : slot + 1;
         }
     }
+    pdl_wait();  // (also where there was nothing to do)
 }
 
 // ranks of a shrink item

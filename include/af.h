@@ -502,7 +502,7 @@ int af_attention_tree(const float* q_dev, int64_t ldq, const void* k_cache, cons
  *               where the table or the ring names no page of the cache.)
  * A request is refused, and stays as it is, if its length is negative or more than its table row holds, if the step would
  * make it so, if its rows do not end within max_rows, if it needs more pages than the requests before it (refused ones for
- * want of pages among them) have left, or if it returns more pages than the ring has room for.
+ * want of pages among them) have left, or if the ring has no room for the pages that it and those before it return.
  * A page belongs to one request; the ring never holds more than n_pages.  No entry of a page outside [0, n_pages) leads to
  * memory outside the cache, here or in af_attention_paged.
  *   ws_dev      scratch of af_kv_pages_workspace(n_seqs) bytes, 16-byte aligned, of any contents

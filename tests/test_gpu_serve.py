@@ -49,12 +49,12 @@ def pages_ref(ln, new, P, n_pages, width, pool, free, table, max_rows):
         ok = False
         if x < 0:
             back += have
-            ok = sound and count + back <= n_pages
+            ok = sound and (have == 0 or count + back <= n_pages)
             if ok:
                 out[i] = 0
                 for k in range(have):
                     free[(head + count + back - have + k) % n_pages] = before[i, k]
-                returned = max(returned, back)
+                returned = max(returned, back if have else 0)
         elif sound and rows <= max_rows and ln[i] + grow <= width * P:
             need = -(-(ln[i] + grow) // P) - have
             wanted += need
