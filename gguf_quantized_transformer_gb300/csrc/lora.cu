@@ -29,6 +29,7 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;  // of expand
 constexpr int kShrinkWarps = 12;
 constexpr int kMaxSplit = 16;
 constexpr int kSetup = 6;
+constexpr int kHalf = 112 * 1024;  // shared memory of a CTA of expand that shares its SM with another
 constexpr int kCols = 16 * kWarps;  // columns that a CTA of expand takes at once
 
 __host__ __device__ inline int64_t plan_order(int max_tiles) { return 4 * (int64_t)(1 + max_tiles); }  // in ints
@@ -384,8 +385,8 @@ __device__ __forceinline__ float weights(uint32_t at, int left, uint32_t (&hi)[V
 // (16 of a warp) whose base and weights are on their way, in the warp's ring: a lane's own pieces of base, then the 16
 // columns' rows of B as they lie in memory.
 // A CTA takes an equal share of all (tile, run of columns), of one tile after another.
-template <bool F16, int V, bool VEC, int NST>
-__global__ void __launch_bounds__(kThreads, NST == 2 ? 1 : 2) lora_expand_kernel(LoraArgs a, int max_tiles, int sms, int rr) {
+template <bool F16, int V, bool VEC, int NST, int CTAS>
+__global__ void __launch_bounds__(kThreads, CTAS) lora_expand_kernel(LoraArgs a, int max_tiles, int sms, int rr) {
     extern __shared__ __align__(16) uint4 sm_h[];  // [steps][2 row tiles][hi, lo][32 lanes], then the rings
     __shared__ int sm_row[kLoraTile];
     __shared__ float sm_up[kLoraTile];  // the powers of two that take the rows of h back
@@ -632,20 +633,24 @@ cudaError_t shrink(const LoraArgs& a, int max_tiles, cudaStream_t s) {
     return launch_chained(k, dim3(num_sms()), kShrinkWarps * 32, kShrinkWarps * kRing, s, a, max_tiles, num_sms());
 }
 
-template <bool F16, int V, bool VEC, int NST>
+template <bool F16, int V, bool VEC, int NST, int CTAS>
 cudaError_t expand_go(const LoraArgs& a, int max_tiles, int smem, cudaStream_t s) {
-    auto k = lora_expand_kernel<F16, V, VEC, NST>;
+    auto k = lora_expand_kernel<F16, V, VEC, NST, CTAS>;
     static SmemOptIn opt;
-    if (cudaError_t e = opt((const void*)k, NST == 2 ? 220 * 1024 : 112 * 1024)) return e;
-    return launch_chained(k, dim3((NST == 2 ? 1 : 2) * num_sms()), kThreads, smem, s, a, max_tiles, num_sms(), shrink_ranks(a.rank));
+    if (cudaError_t e = opt((const void*)k, CTAS == 2 ? kHalf : 220 * 1024)) return e;
+    return launch_chained(k, dim3(CTAS * num_sms()), kThreads, smem, s, a, max_tiles, num_sms(), shrink_ranks(a.rank));
 }
 
-// Four runs on their way where two CTAs' rings fit an SM; two of one CTA's fit for every rank (128 fp32: 176 KB).
+// Two CTAs to an SM where their rings fit it, with three runs on their way if those fit, else with two (64 rows of 4 fp16
+// adapters of rank 64 beside 4096 -> 28672: 19.7 us; one CTA with two 22.0; four runs where they fit are no faster).  Two of
+// one CTA's fit for every rank (128 fp32: 176 KB).
 template <bool F16, int V, bool VEC>
 cudaError_t expand(const LoraArgs& a, int max_tiles, cudaStream_t s) {
     const int operands = (a.rank + 8 * V - 1) / (8 * V) * ((V + 1) / 2) * 2 * 64 * 16, stage = (VEC ? 2048 : 0) + 16 * a.rank * (F16 ? 2 : 4);
-    if (operands + 4 * kWarps * stage <= 112 * 1024) return expand_go<F16, V, VEC, 4>(a, max_tiles, operands + 4 * kWarps * stage, s);
-    return expand_go<F16, V, VEC, 2>(a, max_tiles, operands + 2 * kWarps * stage, s);
+    const int two = operands + 2 * kWarps * stage, three = two + kWarps * stage;
+    if (three <= kHalf) return expand_go<F16, V, VEC, 3, 2>(a, max_tiles, three, s);
+    if (two <= kHalf) return expand_go<F16, V, VEC, 2, 2>(a, max_tiles, two, s);
+    return expand_go<F16, V, VEC, 2, 1>(a, max_tiles, two, s);
 }
 template <bool F16, int V>
 cudaError_t expand(const LoraArgs& a, int max_tiles, bool vec, cudaStream_t s) {
