@@ -15,6 +15,7 @@
 // out.  Tensor cores cut their sums: those of a chunk start from zero, small products first, and are added in fp32.  (tf32
 // needs no scaling, but mma.sync does 128 of its multiplications a cycle and SM.)
 #include <algorithm>
+#include <type_traits>
 
 #include "mma_sync.cuh"
 #include "serve.cuh"
@@ -26,7 +27,13 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kThreads = 256, kWarps = kThreads / 32;  // of expand
-constexpr int kShrinkWarps = 12;
+// Warps of a CTA of shrink and the bytes of a warp's ring.  (fp16 of rank 16: as little shared memory as lets expand's CTAs in
+// beside it: one row, 4096 -> 4096, 6.3 us; with 12 warps of 16 KB 6.9.  Higher ranks: as much as there is, 2048 rows of fp32
+// adapters of rank 64 101 us, with 8 warps 107.)
+template <bool F16, int MT>
+constexpr int kShrinkWarps = F16 && MT == 1 ? 8 : 12;
+template <bool F16, int MT>
+constexpr int kRing = (F16 && MT == 1 ? 10 : 16) * 1024;
 constexpr int kMaxSplit = 16;
 constexpr int kSetup = 6;
 constexpr int kHalf = 112 * 1024;  // shared memory of a CTA of expand that shares its SM with another
@@ -150,13 +157,12 @@ __device__ __forceinline__ int rank_of(const LoraArgs& a, int adapter) {
 
 // ---------------------------------------------------------------- shrink
 
-// Ranges of K: as many as every SM takes one of at once, of at least three chunks of 32 for each warp (shorter ones take as long
-// here, and every range is a round of loads in expand: 64 rows of 4 rank-64 adapters 31 us with 10 ranges, 23 with 3)
-__device__ __forceinline__ int lora_splits(int items, int K, int sms) {
-    return max(1, min(min(sms / max(items, 1), kMaxSplit), K / 32 / (3 * kShrinkWarps)));
+// Ranges of K: as many as every SM takes one of at once, of at least two chunks of 32 for each warp (64 rows of 4 fp16
+// adapters of rank 64 beside 4096 -> 28672: 16.6 us; with three 17.6, with one, more to add up in expand, 16.8)
+__device__ __forceinline__ int lora_splits(int items, int K, int sms, int warps) {
+    return max(1, min(min(sms / max(items, 1), kMaxSplit), K / 32 / (2 * warps)));
 }
 
-constexpr int kRing = 16 * 1024;  // of a warp of shrink
 
 // 2^k that brings a largest magnitude m to [2^13, 2^14), and 2^-k.  (Below 2^-112 it comes no nearer; infinities and NaNs
 // stay what they are.)
@@ -184,14 +190,14 @@ __device__ __forceinline__ float parts8(const uint4& v, const uint4& w, uint32_t
     return up;
 }
 
-// The sums of chunks k0 + warp, + kShrinkWarps .. below k1 for 16 MT ranks and 8 NT rows, in `sum`: [warps][16 MT][pad].
+// The sums of chunks k0 + warp, + NW .. below k1 for 16 MT ranks and 8 NT rows, in `sum`: [warps][16 MT][pad].
 // Weights and x go through the warp's ring, whole lines of 128 bytes a row (64 of fp16 weights); in it odd rows have
 // neighbouring 16-byte pieces exchanged, so that the reads meet all banks.
 // w: the adapter's weights from the tile's first rank on; in: the ranks that there are from it on.
 template <bool F16, int MT, int NT>
 __device__ __forceinline__ void shrink_tile(const LoraArgs& a, const int* row, int count, const uint8_t* w, int in, int k0, int k1,
                                             uint32_t ring, float* sum, int pad) {
-    constexpr int WB = 16 * MT * (F16 ? 64 : 128), STAGE = WB + 8 * NT * 128, NST = kRing / STAGE < 8 ? kRing / STAGE : 8;
+    constexpr int WB = 16 * MT * (F16 ? 64 : 128), STAGE = WB + 8 * NT * 128, NST = kRing<F16, MT> / STAGE < 8 ? kRing<F16, MT> / STAGE : 8, NW = kShrinkWarps<F16, MT>;
     static_assert(NST >= 2, "a stage in flight while one is read");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 3, j = lane >> 2, q = lane >> 3, e16 = lane & 7;
     auto fetch = [&](int k, int slot) {
@@ -222,13 +228,13 @@ __device__ __forceinline__ void shrink_tile(const LoraArgs& a, const int* row, i
     float acc[MT][NT][4] = {};
     int ahead = k0 + warp;
 #pragma unroll 1
-    for (int i = 0; i < NST; i++, ahead += kShrinkWarps) {
+    for (int i = 0; i < NST; i++, ahead += NW) {
         if (ahead < k1) fetch(ahead, i);
         copy_commit();
     }
     int slot = 0;
 #pragma unroll 1
-    for (int k = k0 + warp; k < k1; k += kShrinkWarps, ahead += kShrinkWarps) {
+    for (int k = k0 + warp; k < k1; k += NW, ahead += NW) {
         copy_wait<NST - 1>();
         __syncwarp();  // the other lanes' pieces have landed
         const uint32_t at = ring + slot * STAGE;
@@ -296,11 +302,11 @@ __device__ __forceinline__ void shrink_tile(const LoraArgs& a, const int* row, i
 }
 
 template <bool F16, int MT>
-__global__ void __launch_bounds__(kShrinkWarps * 32, 1) lora_shrink_kernel(LoraArgs a, int max_tiles, int sms) {
-    constexpr int RR = 16 * MT, PAD = kLoraTile + 2, es = F16 ? 2 : 4;
-    static_assert(RR * PAD * 4 <= kRing, "the sums fit the rings");
+__global__ void __launch_bounds__(kShrinkWarps<F16, MT> * 32, 1) lora_shrink_kernel(LoraArgs a, int max_tiles, int sms) {
+    constexpr int NW = kShrinkWarps<F16, MT>, RING = kRing<F16, MT>, RR = 16 * MT, PAD = kLoraTile + 2, es = F16 ? 2 : 4;
+    static_assert(RR * PAD * 4 <= RING, "the sums fit the rings");
     extern __shared__ __align__(16) float sm_sum[];  // the warps' rings, then [warps][RR][PAD]
-    __shared__ int sm_row[kLoraTile], sm_order[kShrinkWarps * 32];
+    __shared__ int sm_row[kLoraTile], sm_order[NW * 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int* plan = (const int*)a.plan;
     pdl_wait();
@@ -310,29 +316,29 @@ __global__ void __launch_bounds__(kShrinkWarps * 32, 1) lora_shrink_kernel(LoraA
     const int4 head = __ldcg(reinterpret_cast<const int4*>(plan));
     const int4 early = first_tiles(plan, lane, max_tiles);
     const int tiles = head.y, rows = head.z, rt = (a.rank + RR - 1) / RR;
-    const int splits = lora_splits(tiles * rt, a.K, sms), chunks = a.K / 32;
+    const int splits = lora_splits(tiles * rt, a.K, sms, NW), chunks = a.K / 32;
     for (int item = blockIdx.x; item < tiles * rt * splits; item += gridDim.x) {
         const int split = item % splits, rest = item / splits, r0 = rest % rt * RR;
         const int4 tile = tile_of(plan, rest / rt, early);
         __syncthreads();  // (the previous item's sums and rows have been read)
         sm_order[tid] = early_row;
-        const int* const row = tile.y + tile.z <= kShrinkWarps * 32 ? sm_order + tile.y : sm_row;
+        const int* const row = tile.y + tile.z <= NW * 32 ? sm_order + tile.y : sm_row;
         if (row == sm_row && tid < tile.z) sm_row[tid] = __ldcg(order + tile.y + tid);
         const int rank = rank_of(a, tile.x);
         __syncthreads();
         const uint8_t* w = (const uint8_t*)a.a + ((int64_t)tile.x * a.rank + r0) * a.K * es;
         const int c0 = (int)((int64_t)chunks * split / splits), c1 = (int)((int64_t)chunks * (split + 1) / splits);
-        const uint32_t ring = smem_u32(sm_sum) + warp * kRing;
+        const uint32_t ring = smem_u32(sm_sum) + warp * RING;
         if (tile.z <= 8)
             shrink_tile<F16, MT, 1>(a, row, tile.z, w, rank - r0, c0, c1, ring, sm_sum, PAD);
         else
             shrink_tile<F16, MT, 4>(a, row, tile.z, w, rank - r0, c0, c1, ring, sm_sum, PAD);
         __syncthreads();
-        for (int i = tid; i < RR * tile.z; i += kShrinkWarps * 32) {
+        for (int i = tid; i < RR * tile.z; i += NW * 32) {
             const int r = i % RR, x = i / RR;
             float sum = 0.f;
 #pragma unroll
-            for (int w = 0; w < kShrinkWarps; w++) sum += sm_sum[(w * RR + r) * PAD + x];
+            for (int w = 0; w < NW; w++) sum += sm_sum[(w * RR + r) * PAD + x];
             if (r0 + r < a.rank) a.ws[((int64_t)split * rows + tile.y + x) * a.rank + r0 + r] = sum;
         }
     }
@@ -401,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) lora_expand_kernel(LoraArgs a,
     const int4 head = __ldcg(reinterpret_cast<const int4*>(plan));
     const int4 early = first_tiles(plan, lane, max_tiles);
     const int tiles = a.base && a.base == a.y ? head.y : head.x;  // in place, rows without an adapter stay as they are
-    const int rows = head.z, splits = lora_splits(head.y * ((a.rank + rr - 1) / rr), a.K, sms), cols = (a.N + kCols - 1) / kCols;
+    const int rows = head.z, splits = lora_splits(head.y * ((a.rank + rr - 1) / rr), a.K, sms, rr == 16 ? kShrinkWarps<F16, 1> : kShrinkWarps<F16, 2>), cols = (a.N + kCols - 1) / kCols;
     // The CTA's share: an equal one of all runs, or, where that is not much less, of one tile's, since a tile's preparation takes
     // as long as some kSetup runs (64 rows of 40 adapters beside 4096 -> 6144: 7 runs of one tile in place of 6.6 of 1.2)
     const int64_t items = (int64_t)tiles * cols;
@@ -481,27 +487,34 @@ __global__ void __launch_bounds__(kThreads, CTAS) lora_expand_kernel(LoraArgs a,
         if (tile.x >= 0 && warp < tile.z) {
             const float* p = a.ws + ((int64_t)tile.y + warp) * a.rank + lane;
             const int64_t stride = (int64_t)rows * a.rank;
-            if (tile.z <= kWarps) {  // (a row a warp: four ranges on their way)
-#pragma unroll 4
-                for (int s = 0; s < splits; s++)
-#pragma unroll
-                    for (int q = 0; q < HQ; q++) {
-                        if (32 * q >= a.rank) break;
-                        if (lane + 32 * q < a.rank) h[0][q] += __ldcg(p + s * stride + 32 * q);
-                    }
-            } else {
+            // ranges on their way: eight of a row, two of four rows
+            auto take = [&](auto in_flight, auto row_groups) {
+                constexpr int S = decltype(in_flight)::value, R = decltype(row_groups)::value;
 #pragma unroll 1
-                for (int s = 0; s < splits; s++, p += stride)
+                for (int s0 = 0; s0 < splits; s0 += S, p += S * stride) {
+                    float v[S][R][HQ];
 #pragma unroll
-                    for (int i = 0; i < HR; i++) {
-                        if (warp + kWarps * i >= tile.z) break;
+                    for (int s = 0; s < S; s++)
 #pragma unroll
-                        for (int q = 0; q < HQ; q++) {
-                            if (32 * q >= a.rank) break;
-                            if (lane + 32 * q < a.rank) h[i][q] += __ldcg(p + (int64_t)kWarps * i * a.rank + 32 * q);
-                        }
-                    }
-            }
+                        for (int i = 0; i < R; i++)
+#pragma unroll
+                            for (int q = 0; q < HQ; q++) {
+                                v[s][i][q] = 0.f;
+                                if (s0 + s < splits && warp + kWarps * i < tile.z && lane + 32 * q < a.rank)
+                                    v[s][i][q] = __ldcg(p + s * stride + (int64_t)kWarps * i * a.rank + 32 * q);
+                            }
+#pragma unroll
+                    for (int s = 0; s < S; s++)
+#pragma unroll
+                        for (int i = 0; i < R; i++)
+#pragma unroll
+                            for (int q = 0; q < HQ; q++) h[i][q] += v[s][i][q];
+                }
+            };
+            if (tile.z <= kWarps)
+                take(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
+            else
+                take(std::integral_constant<int, 2>{}, std::integral_constant<int, HR>{});
         }
         // h as operands: value i of lane cc's 2 V in group g is rank 8 V g + 2 V cc + i, its pairs those of steps 0, 0, 1, 1
         const int held = groups * 8 * V;
@@ -627,10 +640,11 @@ int shrink_ranks(int rank) { return rank <= 16 ? 16 : 32; }
 
 template <bool F16, int MT>
 cudaError_t shrink(const LoraArgs& a, int max_tiles, cudaStream_t s) {
+    constexpr int NW = kShrinkWarps<F16, MT>, RING = kRing<F16, MT>;
     auto k = lora_shrink_kernel<F16, MT>;
     static SmemOptIn opt;
-    if (cudaError_t e = opt((const void*)k, kShrinkWarps * kRing)) return e;
-    return launch_chained(k, dim3(num_sms()), kShrinkWarps * 32, kShrinkWarps * kRing, s, a, max_tiles, num_sms());
+    if (cudaError_t e = opt((const void*)k, NW * RING)) return e;
+    return launch_chained(k, dim3(num_sms()), NW * 32, NW * RING, s, a, max_tiles, num_sms());
 }
 
 template <bool F16, int V, bool VEC, int NST, int CTAS>
