@@ -439,11 +439,14 @@ __global__ void __launch_bounds__(kThreads, CTAS) lora_expand_kernel(LoraArgs a,
         const int rank = tile.x < 0 ? 0 : rank_of(a, tile.x);
         const float scale = tile.x >= 0 && a.scale ? __ldcg(a.scale + tile.x) : 1.f;
         const int mt = tile.z > 16 ? 2 : 1;
+        const bool few = tile.z <= 8;
         const int groups = (rank + 8 * V - 1) / (8 * V), rank_bytes = rank * es;
+        const uint8_t* const tile_b = (const uint8_t*)a.b + ((int64_t)tile.x * a.N + 16 * warp) * row_bytes;
+        const unsigned run_bytes = kCols * row_bytes;
         auto fetch_b = [&](int run, int slot) {
             const uint32_t dst = ring + slot * stage + (VEC ? 2048 : 0);
             const int n0 = run * kCols + 16 * warp;
-            const uint8_t* src = (const uint8_t*)a.b + ((int64_t)tile.x * a.N + n0) * row_bytes;
+            const uint8_t* src = tile_b + (uint64_t)(unsigned)run * run_bytes;
 #pragma unroll 1
             for (int x = lane * 16, col = col0, byte = byte0; x < 16 * row_bytes; x += 512) {
                 const bool in = n0 + col < a.N && byte < rank_bytes;
@@ -487,18 +490,18 @@ __global__ void __launch_bounds__(kThreads, CTAS) lora_expand_kernel(LoraArgs a,
         if (tile.x >= 0 && warp < tile.z) {
             const float* p = a.ws + ((int64_t)tile.y + warp) * a.rank + lane;
             const int64_t stride = (int64_t)rows * a.rank;
-            // ranges on their way: eight of a row, two of four rows
-            auto take = [&](auto in_flight, auto row_groups) {
-                constexpr int S = decltype(in_flight)::value, R = decltype(row_groups)::value;
+            // ranges on their way: eight of a row, two or four of four rows
+            auto take = [&](auto in_flight, auto row_groups, auto rank_groups) {
+                constexpr int S = decltype(in_flight)::value, R = decltype(row_groups)::value, Q = decltype(rank_groups)::value;
 #pragma unroll 1
                 for (int s0 = 0; s0 < splits; s0 += S, p += S * stride) {
-                    float v[S][R][HQ];
+                    float v[S][R][Q];
 #pragma unroll
                     for (int s = 0; s < S; s++)
 #pragma unroll
                         for (int i = 0; i < R; i++)
 #pragma unroll
-                            for (int q = 0; q < HQ; q++) {
+                            for (int q = 0; q < Q; q++) {
                                 v[s][i][q] = 0.f;
                                 if (s0 + s < splits && warp + kWarps * i < tile.z && lane + 32 * q < a.rank)
                                     v[s][i][q] = __ldcg(p + s * stride + (int64_t)kWarps * i * a.rank + 32 * q);
@@ -508,13 +511,18 @@ __global__ void __launch_bounds__(kThreads, CTAS) lora_expand_kernel(LoraArgs a,
 #pragma unroll
                         for (int i = 0; i < R; i++)
 #pragma unroll
-                            for (int q = 0; q < HQ; q++) h[i][q] += v[s][i][q];
+                            for (int q = 0; q < Q; q++) h[i][q] += v[s][i][q];
                 }
             };
-            if (tile.z <= kWarps)
-                take(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
+            const auto i1 = std::integral_constant<int, 1>{};
+            if (few && a.rank <= 32)
+                take(std::integral_constant<int, 8>{}, i1, i1);
+            else if (few)
+                take(std::integral_constant<int, 8>{}, i1, std::integral_constant<int, HQ>{});
+            else if (a.rank <= 32)
+                take(std::integral_constant<int, 4>{}, std::integral_constant<int, HR>{}, i1);
             else
-                take(std::integral_constant<int, 2>{}, std::integral_constant<int, HR>{});
+                take(std::integral_constant<int, 2>{}, std::integral_constant<int, HR>{}, std::integral_constant<int, HQ>{});
         }
         // h as operands: value i of lane cc's 2 V in group g is rank 8 V g + 2 V cc + i, its pairs those of steps 0, 0, 1, 1
         const int held = groups * 8 * V;
