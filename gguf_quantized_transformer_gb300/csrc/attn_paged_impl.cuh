@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
     float* const far = C::NEAR ? reinterpret_cast<float*>(smem + C::RING) : a.ws + paged_far(gridDim.x, D) + (size_t)blockIdx.x * NW * C::PIECE;
 
     pdl_wait();  // positions, tables, q and the cache are written by earlier kernels
-    pdl_launch_dependents();
+    if (a.ldo > kCacheRow) pdl_launch_dependents();
     // request and last position of a row; -1: it sees nothing
     auto row_of = [&](int r) {
         const int who = a.seq ? __ldcg(a.seq + r) : r;

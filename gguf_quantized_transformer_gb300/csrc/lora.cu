@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) lora_expand_kernel(LoraArgs a,
     const int row_bytes = a.rank * es, stage = (VEC ? 2048 : 0) + 16 * row_bytes, steps = (a.rank + 8 * V - 1) / (8 * V) * SG;
     const uint32_t ring = smem_u32(sm_h) + steps * 2 * 64 * 16 + warp * NST * stage;
     const int* plan = (const int*)a.plan;
-    pdl_launch_dependents();
+    if (a.ldy > kCacheRow) pdl_launch_dependents();
     const int4 head = __ldcg(reinterpret_cast<const int4*>(plan));
     const int4 early = first_tiles(plan, lane, max_tiles);
     const int tiles = a.base && a.base == a.y ? head.y : head.x;  // in place, rows without an adapter stay as they are

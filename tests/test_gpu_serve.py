@@ -722,6 +722,39 @@ def test_lora_sizes_of_values(af, dtype):
     assert torch.equal(y[~hit], clean[~hit]) and not torch.isfinite(y[hit]).any()
 
 
+@pytest.mark.parametrize("ctx", [1024, 6000])
+def test_decode_attention_sees_keys_that_an_adapter_wrote_just_before(af, ctx):
+    """Rows of one kv head are slots of an fp32 cache, in which the decode attention reads ahead."""
+    H, KVH, D, K, r = 32, 8, 128, 64, 16
+    g = torch.Generator(device="cuda").manual_seed(ctx)
+    def normal(*s):
+        return torch.randn(*s, generator=g, device="cuda")
+    x, q = [normal(ctx, K) * 2.0 ** i for i in (0, 1)], normal(H * D)
+    a, b = (normal(1, r, K) / 8).half(), [(normal(1, D, r) / 4).half() for _ in range(KVH)]
+    k, v = torch.zeros(KVH, ctx, D, device="cuda"), normal(KVH, ctx, D)
+    plan = torch.empty(af.af_lora_plan_bytes(ctx, 1), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(af.af_lora_workspace(ctx, 1, r, K, D), dtype=torch.uint8, device="cuda")
+    af.af_lora_plan(torch.zeros(ctx, dtype=torch.int32, device="cuda"), ctx, 1, plan, plan.numel())
+    heads = [k[h] for h in range(KVH)]
+
+    def step(i, out):
+        for h in range(KVH):
+            af.af_lora(x[i], K, ctx, plan, a, b[h], af.AF_F16, None, None, 1, r, K, D, None, 0, heads[h], D, ws, ws.numel())
+        af.af_attention_decode_static(q, k, v, af.AF_F32, H, KVH, D, ctx, ctx - 1, out)
+
+    want = [torch.zeros(H * D, device="cuda") for _ in range(2)]
+    for i in (0, 1):
+        torch.cuda.synchronize()
+        step(i, want[i])
+    outs = [torch.zeros(H * D, device="cuda") for _ in range(20)]
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        step(i % 2, out)
+    torch.cuda.synchronize()
+    assert not torch.equal(want[0], want[1])
+    assert all(torch.equal(y, want[i % 2]) for i, y in enumerate(outs))
+
+
 @pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
 def test_lora_values_far_apart(af, dtype):
     """One value of x, of A or of A x that is far larger than its neighbours costs them no bits that the sums would keep: the others
