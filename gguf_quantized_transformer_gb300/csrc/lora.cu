@@ -8,7 +8,11 @@
 //    free).  The warps' sums join in shared memory, the ranges' sums by their reader, both in order.
 //  - expand: y = base + B (scale h).  A CTA takes a tile and runs of 128 columns; h's parts lie in shared memory as operands,
 //    a warp's 16 columns of B come straight into operands, and y is moved in 16-byte pieces.
-// Bound by the bytes of base, y and x for many rows, by those of the weights for few, and by two launches for one.
+// Bound by the bytes of base, y and x for many rows (2048 rows of 5 fp16 adapters of rank 32 beside 4096 -> 28672 98 us, 5.2
+// TB/s), by two rounds of loads and a join in each kernel for few (one row of rank 16 beside 4096 -> 4096 4.5 us; 40 rows of 12
+// fp32 adapters of rank 64 beside 14336 -> 4096 17.0 us for 39 MB; 64 rows of 40 of rank 16 beside 4096 -> 6144 12.3 us, in
+// expand by its instructions: runs of 16 columns a warp for one or two rows).  Expand starts while shrink runs: what shrink does
+// not write (the plan, B, the base) is fetched before its wait, which takes 0.7 us of a row's time.
 // Precision: fp16 products of two parts of 11 bits (x, h and fp32 weights; fp16 weights are operands as they are), after a power
 // of two has brought the largest of a row's 32 values (of a chunk; of h all) to [2^13, 2^14), which leaves the low part 24
 // bits below fp16's smallest normal number: 2^-22 of a value, 2^-38 of the largest.  The product of two low parts is left
@@ -35,7 +39,6 @@ constexpr int kShrinkWarps = F16 && MT == 1 ? 8 : 12;
 template <bool F16, int MT>
 constexpr int kRing = (F16 && MT == 1 ? 10 : 16) * 1024;
 constexpr int kMaxSplit = 16;
-constexpr int kSetup = 6;
 constexpr int kHalf = 112 * 1024;  // shared memory of a CTA of expand that shares its SM with another
 constexpr int kCols = 16 * kWarps;  // columns that a CTA of expand takes at once
 
@@ -329,6 +332,7 @@ __global__ void __launch_bounds__(kShrinkWarps<F16, MT> * 32, 1) lora_shrink_ker
         const uint8_t* w = (const uint8_t*)a.a + ((int64_t)tile.x * a.rank + r0) * a.K * es;
         const int c0 = (int)((int64_t)chunks * split / splits), c1 = (int)((int64_t)chunks * (split + 1) / splits);
         const uint32_t ring = smem_u32(sm_sum) + warp * RING;
+        // (few rows as 32: 40 rows of 12 fp32 adapters 25.3 us in place of 17.8)
         if (tile.z <= 8)
             shrink_tile<F16, MT, 1>(a, row, tile.z, w, rank - r0, c0, c1, ring, sm_sum, PAD);
         else
@@ -408,24 +412,14 @@ __global__ void __launch_bounds__(kThreads, CTAS) lora_expand_kernel(LoraArgs a,
     const int4 early = first_tiles(plan, lane, max_tiles);
     const int tiles = a.base && a.base == a.y ? head.y : head.x;  // in place, rows without an adapter stay as they are
     const int rows = head.z, splits = lora_splits(head.y * ((a.rank + rr - 1) / rr), a.K, sms, rr == 16 ? kShrinkWarps<F16, 1> : kShrinkWarps<F16, 2>), cols = (a.N + kCols - 1) / kCols;
-    // The CTA's share: an equal one of all runs, or, where that is not much less, of one tile's, since a tile's preparation takes
-    // as long as some kSetup runs (64 rows of 40 adapters beside 4096 -> 6144: 7 runs of one tile in place of 6.6 of 1.2)
+    // The CTA's share: an equal one of all runs, the first CTAs one more, since they start first.  (Shares of one tile each save a
+    // second preparation but not the time: 64 rows of 40 adapters 15.2 us in place of 14.7, 40 rows of 12 17.7 in place of 17.0,
+    // though 512 rows of one adapter 35.3 in place of 36.8.)
     const int64_t items = (int64_t)tiles * cols;
-    const int ctas = gridDim.x, each_tile = ctas / max(tiles, 1), me = blockIdx.x;
-    int64_t item, last;
-    if (each_tile && (int64_t)((cols + each_tile - 1) / each_tile) * ctas <= items + (int64_t)kSetup * ctas) {
-        const int which = me / each_tile, part = me - which * each_tile;
-        if (which >= tiles) {
-            pdl_wait();  // (the kernel does not end before shrink)
-            return;
-        }
-        item = (int64_t)which * cols + (unsigned)cols * (unsigned)part / (unsigned)each_tile;
-        last = (int64_t)which * cols + (unsigned)cols * (unsigned)(part + 1) / (unsigned)each_tile;
-    } else {
-        const int64_t each = items <= INT32_MAX ? (int64_t)((unsigned)items / (unsigned)ctas) : items / ctas, rest = items - each * ctas;
-        item = each * me + min((int64_t)me, rest);
-        last = each * (me + 1) + min((int64_t)me + 1, rest);
-    }
+    const int ctas = gridDim.x, me = blockIdx.x;
+    const int64_t each = items <= INT32_MAX ? (int64_t)((unsigned)items / (unsigned)ctas) : items / ctas, rest = items - each * ctas;
+    int64_t item = each * me + min((int64_t)me, rest);
+    const int64_t last = each * (me + 1) + min((int64_t)me + 1, rest);
     // this lane's first piece of 16 columns' weights: its column and byte within the row; and how far 512 bytes on is
     const int col0 = lane * 16 / row_bytes, byte0 = lane * 16 - col0 * row_bytes, col_step = 512 / row_bytes, byte_step = 512 - col_step * row_bytes;
     while (item < last) {
@@ -643,7 +637,8 @@ __global__ void __launch_bounds__(kThreads, CTAS) lora_expand_kernel(LoraArgs a,
     pdl_wait();  // (also where there was nothing to do)
 }
 
-// ranks of a shrink item
+// Ranks of an item of shrink.  (2048 rows of fp32 adapters of rank 64 101 us, in items of 16 129: x is read once an item; one row of
+// rank 16 in items of 32 0.9 us more.)
 int shrink_ranks(int rank) { return rank <= 16 ? 16 : 32; }
 
 template <bool F16, int MT>
@@ -685,6 +680,7 @@ cudaError_t lora(const LoraArgs& a, cudaStream_t s) {
     cudaError_t e = rr == 16 ? shrink<F16, 1>(a, tiles, s) : shrink<F16, 2>(a, tiles, s);
     if (e) return e;
     const bool vec = a.N % 4 == 0 && a.ldy % 4 == 0 && (uintptr_t)a.y % 16 == 0 && (!a.base || (a.ldb % 4 == 0 && (uintptr_t)a.base % 16 == 0));
+    // as many ranks a step as divide the rank (rank 64 by 8: 40 rows of 12 fp32 adapters 20.6 us in place of 17.8)
     if (a.rank % 32 == 0) return expand<F16, 4>(a, tiles, vec, s);
     if (a.rank % 16 == 0) return expand<F16, 2>(a, tiles, vec, s);
     return expand<F16, 1>(a, tiles, vec, s);
