@@ -19,7 +19,9 @@ namespace af {
 
 namespace {
 
-constexpr int kScan = 1024;             // threads of the scanning CTA
+// Threads of the scanning CTA, for up to 512 requests and for more.  (64 requests 3.2 us with 512, 4.2 with 1024, which issue twice
+// the instructions; 2000 requests 12.8 and 12.1.)
+constexpr int kFewSeqs = 512, kScan = 1024;
 constexpr int kFillRows = 4, kFill = 256;  // rows of a thread at a time, threads of a CTA of the second part
 constexpr int kKept = 2048;                // requests whose prefix sums a CTA of the second part keeps
 
@@ -29,17 +31,26 @@ constexpr int kRefused = -1, kEnded = -2;
 
 __device__ __forceinline__ int64_t clamp_int(int64_t x) { return x < INT32_MAX ? x : INT32_MAX; }
 
-// Inclusive prefix sums over the CTA of three values a thread; `total` receives the CTA's.
-__device__ __forceinline__ void cta_scan(int64_t (&x)[3], int64_t (&total)[3]) {
-    __shared__ int64_t part[kScan / 32][3];
+// Sum over the warp of values below 2^40
+__device__ __forceinline__ int64_t warp_sum(int64_t x) {
+    return ((int64_t)__reduce_add_sync(0xffffffffu, (unsigned)(x >> 24)) << 24) + __reduce_add_sync(0xffffffffu, (unsigned)x & 0xFFFFFFu);
+}
+
+// Inclusive prefix sums over the CTA of three values a thread, each below 2^31; `total` receives the CTA's.  live: the warp's may be
+// other than zeros.
+template <int T>
+__device__ __forceinline__ void cta_scan(bool live, int64_t (&x)[3], int64_t (&total)[3]) {
+    __shared__ int64_t part[T / 32][3];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (live) {
 #pragma unroll
-    for (int o = 1; o < 32; o *= 2)
+        for (int o = 1; o < 32; o *= 2)
 #pragma unroll
-        for (int k = 0; k < 3; k++) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x[k], o);
-            if (lane >= o) x[k] += y;
-        }
+            for (int k = 0; k < 3; k++) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, x[k], o);
+                if (lane >= o) x[k] += y;
+            }
+    }
     __syncthreads();  // (the previous call's parts have been read)
     if (lane == 31)
 #pragma unroll
@@ -48,14 +59,9 @@ __device__ __forceinline__ void cta_scan(int64_t (&x)[3], int64_t (&total)[3]) {
     // every warp sums the others' parts, lane by lane
 #pragma unroll
     for (int k = 0; k < 3; k++) {
-        int64_t y = part[lane][k], before = lane < warp ? y : 0;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            y += __shfl_xor_sync(0xffffffffu, y, o);
-            before += __shfl_xor_sync(0xffffffffu, before, o);
-        }
-        total[k] = y;
-        x[k] += before;
+        const int64_t y = lane < T / 32 ? part[lane][k] : 0;
+        total[k] = warp_sum(y);
+        if (live) x[k] += warp_sum(lane < warp ? y : 0);
     }
 }
 
@@ -150,22 +156,22 @@ __device__ __forceinline__ void fill(const PagesArgs& a, int64_t t, int64_t nt, 
     }
 }
 
-// FILL: both parts.
-template <bool FILL>
-__global__ void __launch_bounds__(kScan) kv_pages_scan_kernel(PagesArgs a) {
-    __shared__ int sm_start[FILL ? kScan : 1], sm_back[FILL ? kScan : 1];
-    __shared__ int4 sm_request[FILL ? kScan : 1];
+// T threads.  FILL: both parts.
+template <bool FILL, int T>
+__global__ void __launch_bounds__(T) kv_pages_scan_kernel(PagesArgs a) {
+    __shared__ int sm_start[FILL ? T : 1], sm_back[FILL ? T : 1];
+    __shared__ int4 sm_request[FILL ? T : 1];
     __shared__ int sm_taken, sm_returned, sm_refused;
     const int t = threadIdx.x;
     pdl_launch_dependents();
     pdl_wait();
     int head = __ldcg(a.pool), count = __ldcg(a.pool + 1);
     if (t == 0) sm_taken = sm_returned = sm_refused = 0;
-    int64_t before[3] = {0, 0, 0};  // rows, pages taken and pages given back by the requests before this round of kScan
+    int64_t before[3] = {0, 0, 0};  // rows, pages taken and pages given back by the requests before this round of T
     const int64_t most = (int64_t)a.width * a.page;
-    for (int i0 = 0; i0 < a.n; i0 += kScan) {
+    for (int i0 = 0; i0 < a.n; i0 += T) {
         const int i = i0 + t;
-        const bool in = i < a.n;
+        const bool in = i < a.n, live = i0 + (t & ~31) < a.n;
         const int len = in ? __ldcg(a.len + i) : 0, fresh = in ? __ldcg(a.fresh + i) : 0;
         if (i0 == 0) {
             head = head >= 0 && head < a.n_pages ? head : 0;
@@ -176,11 +182,11 @@ __global__ void __launch_bounds__(kScan) kv_pages_scan_kernel(PagesArgs a) {
         const int have = sound ? pages_for(a, len) : 0;
         bool fits = in && !ends && sound && len + grow <= most;
         int64_t need = fits ? pages_for(a, (int)(len + grow)) - have : 0, sums[3] = {grow, need, back}, total[3];
-        cta_scan(sums, total);
+        cta_scan<T>(live, sums, total);
         if (before[0] + total[0] > a.rows) {  // some requests' rows do not fit: they take no pages
             if (before[0] + sums[0] > a.rows) fits = false, need = 0;
             sums[0] = grow, sums[1] = need, sums[2] = back;
-            cta_scan(sums, total);
+            cta_scan<T>(live, sums, total);
         }
         const int64_t rows = before[0] + sums[0], taken = before[1] + sums[1], returned = before[2] + sums[2];
 #pragma unroll
@@ -213,7 +219,7 @@ __global__ void __launch_bounds__(kScan) kv_pages_scan_kernel(PagesArgs a) {
         a.pool_out[3] = total;
     }
     if (FILL)
-        fill<1>(a, t, kScan, total, returned, head, count, [&](int i) { return sm_start[i]; }, [&](int i) { return sm_back[i]; },
+        fill<1>(a, t, T, total, returned, head, count, [&](int i) { return sm_start[i]; }, [&](int i) { return sm_back[i]; },
                 [&](int i) { return sm_request[i]; });
 }
 
@@ -243,8 +249,13 @@ __global__ void __launch_bounds__(kFill) kv_pages_fill_kernel(PagesArgs a) {
 // 7.2); in two, the sums in shared memory while they fit it beside 7 other CTAs' (7856 rows 7.2 us, without 8.4; 2000 requests
 // 12.1 and 13.6).
 cudaError_t launch_kv_pages(const PagesArgs& a, cudaStream_t s) {
-    if (a.n <= kScan && a.rows <= 4 * kScan) return launch_chained(kv_pages_scan_kernel<true>, dim3(1), kScan, 0, s, a);
-    cudaError_t e = launch_chained(kv_pages_scan_kernel<false>, dim3(1), kScan, 0, s, a);
+    const bool few = a.n <= kFewSeqs;
+    if (a.n <= kScan && a.rows <= 4 * (few ? kFewSeqs : kScan)) {
+        if (few) return launch_chained(kv_pages_scan_kernel<true, kFewSeqs>, dim3(1), kFewSeqs, 0, s, a);
+        return launch_chained(kv_pages_scan_kernel<true, kScan>, dim3(1), kScan, 0, s, a);
+    }
+    cudaError_t e = few ? launch_chained(kv_pages_scan_kernel<false, kFewSeqs>, dim3(1), kFewSeqs, 0, s, a)
+                        : launch_chained(kv_pages_scan_kernel<false, kScan>, dim3(1), kScan, 0, s, a);
     if (e) return e;
     const int64_t work = std::max<int64_t>(a.rows, a.n);
     const int ctas = (int)std::min<int64_t>((work + kFill * kFillRows - 1) / (kFill * kFillRows), 8 * (int64_t)num_sms());
