@@ -8,8 +8,8 @@
 // new token, so the thread of the page's first token writes the table.  Small steps do both in the one CTA, larger ones the
 // second part in a grid of their own.
 // Latency-bound: one or two launches, three rounds of dependent loads (lengths; requests; pages), the barriers of the sums.  In
-// one CTA a step of 256 requests takes 7.0 us (5.0 with 8 requests), 24 prompts of 370,000 tokens in two launches 8.5 us, of
-// which 4.4 MB of slots are 0.7.
+// one CTA 64 requests take 3.0 us and a step of 256 in which 16 end and give back 4000 pages 6.3; 24 prompts with 414,896 rows, in two
+// launches, 7.7, of which the 5 MB of slots, positions and requests are 0.7.
 #include <algorithm>
 
 #include "serve.cuh"
@@ -19,8 +19,9 @@ namespace af {
 
 namespace {
 
-// Threads of the scanning CTA, for up to 512 requests and for more.  (64 requests 3.2 us with 512, 4.2 with 1024, which issue twice
-// the instructions; 2000 requests 12.8 and 12.1.)
+// Threads of the scanning CTA: fewer where it does both parts for up to 512 requests.  (64 requests 3.2 us with 512, 4.2 with 1024,
+// which issue twice the instructions.  Before a second launch 512 are slower, outside a graph: 124 requests 9.9 and 7.9 us; 2000
+// requests 12.8 and 12.1.)
 constexpr int kFewSeqs = 512, kScan = 1024;
 constexpr int kFillRows = 4, kFill = 256;  // rows of a thread at a time, threads of a CTA of the second part
 constexpr int kKept = 2048;                // requests whose prefix sums a CTA of the second part keeps
@@ -245,17 +246,16 @@ __global__ void __launch_bounds__(kFill) kv_pages_fill_kernel(PagesArgs a) {
 
 }  // namespace
 
-// One launch while a thread has few rows (64 requests with 2656 rows 6.6 us, in two 7.2; 3952 rows 7.5 and 7.2, 7856 rows 11.5 and
-// 7.2); in two, the sums in shared memory while they fit it beside 7 other CTAs' (7856 rows 7.2 us, without 8.4; 2000 requests
-// 12.1 and 13.6).
+// One launch while a thread has few rows (64 requests with 704 rows 4.0 us, in two 5.8; 1024 threads with 2656 rows 6.6 and 7.2, 7856
+// rows 11.5 and 7.2); in two, the sums in shared memory while they fit it beside 7 other CTAs' (7856 rows 7.2 us, without 8.4;
+// 2000 requests 12.1 and 13.6).
 cudaError_t launch_kv_pages(const PagesArgs& a, cudaStream_t s) {
     const bool few = a.n <= kFewSeqs;
     if (a.n <= kScan && a.rows <= 4 * (few ? kFewSeqs : kScan)) {
         if (few) return launch_chained(kv_pages_scan_kernel<true, kFewSeqs>, dim3(1), kFewSeqs, 0, s, a);
         return launch_chained(kv_pages_scan_kernel<true, kScan>, dim3(1), kScan, 0, s, a);
     }
-    cudaError_t e = few ? launch_chained(kv_pages_scan_kernel<false, kFewSeqs>, dim3(1), kFewSeqs, 0, s, a)
-                        : launch_chained(kv_pages_scan_kernel<false, kScan>, dim3(1), kScan, 0, s, a);
+    cudaError_t e = launch_chained(kv_pages_scan_kernel<false, kScan>, dim3(1), kScan, 0, s, a);
     if (e) return e;
     const int64_t work = std::max<int64_t>(a.rows, a.n);
     const int ctas = (int)std::min<int64_t>((work + kFill * kFillRows - 1) / (kFill * kFillRows), 8 * (int64_t)num_sms());
