@@ -560,7 +560,7 @@ int af_attention_paged(const float* q_dev, int64_t ldq, const void* k_cache, con
  *             them in a_dev and b_dev reaches nothing.  NULL: all have `rank`
  *   base_dev  fp32 [n] rows of N values, ldb apart: the projection's; may be y_dev with ldb == ldy, and overlaps it in no
  *             other way; NULL: zeros
- *   y_dev     fp32 [n] rows, ldy apart.  Rows without an adapter are the base's
+ *   y_dev     fp32 [n] rows, ldy apart.  Rows without an adapter are the base's.  (May overlap x_dev, which is read first)
  *   ws_dev    scratch of af_lora_workspace(n, n_adapters, rank, K, N) bytes, 256-byte aligned, of any contents; calls that
  *             may overlap in time need scratch of their own
  * Precision: x, fp32 weights and A x keep 2^-22 of each value, or 2^-38 of the largest of 32 neighbours along K (of a row of

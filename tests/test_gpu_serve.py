@@ -722,6 +722,43 @@ def test_lora_sizes_of_values(af, dtype):
     assert torch.equal(y[~hit], clean[~hit]) and not torch.isfinite(y[hit]).any()
 
 
+@pytest.mark.parametrize("n,r,K,N", [(3, 16, 4096, 512), (40, 8, 256, 4100), (300, 64, 96, 1030)])
+def test_lora_chain_of_calls(af, n, r, K, N):
+    """Calls behind one another, each on what the last one wrote (its base, its x, the plan in the same buffer): as with a
+    synchronisation between them, since a call reads ahead only what is older than its first kernel."""
+    g = torch.Generator(device="cuda").manual_seed(n)
+    def normal(*s):
+        return torch.randn(*s, generator=g, device="cuda")
+    m, calls = 5, 8
+    a, b = [(normal(m, r, K) * K ** -0.5).half() for _ in range(calls)], [(normal(m, N, r) * r ** -0.5).half() for _ in range(calls)]
+    back = [(normal(m, K, r) * r ** -0.5).half() for _ in range(calls)]
+    ids = [torch.randint(-1, m, (n,), generator=g, device="cuda", dtype=torch.int32) for _ in range(calls)]
+    x0, y0 = normal(n, K), normal(n, N)
+    ldn = -(-N // 4) * 4
+    plan = torch.empty(af.af_lora_plan_bytes(n, m), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(max(af.af_lora_workspace(n, m, r, K, N), af.af_lora_workspace(n, m, r, K, K)), dtype=torch.uint8, device="cuda")
+
+    def run(wait):
+        x, y = x0.clone(), torch.zeros(n, ldn, device="cuda")
+        y[:, :N] = y0
+        torch.cuda.synchronize()
+        for i in range(calls):
+            for call in (lambda: af.af_lora_plan(ids[i], n, m, plan, plan.numel()),
+                         lambda: af.af_lora(x, K, n, plan, a[i], b[i], af.AF_F16, None, None, m, r, K, N, y, ldn, y, ldn, ws, ws.numel()),
+                         lambda: af.af_lora(x, K, n, plan, a[i], back[i], af.AF_F16, None, None, m, r, K, K, x, K, x, K, ws, ws.numel())):
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return x, y
+
+    want = run(True)
+    assert all(torch.isfinite(t).all() for t in want) and not torch.equal(want[0], x0)
+    for _ in range(5):
+        got = run(False)
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
 @pytest.mark.parametrize("ctx", [1024, 6000])
 def test_decode_attention_sees_keys_that_an_adapter_wrote_just_before(af, ctx):
     """Rows of one kv head are slots of an fp32 cache, in which the decode attention reads ahead."""
