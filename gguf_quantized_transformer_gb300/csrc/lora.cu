@@ -3,19 +3,19 @@
 //
 // The rows are put in the order of their adapters once a step (lora_plan_kernel: a counting sort), in tiles of up to 32 rows
 // of one adapter, so that an adapter's weights are read once for all of them.  Then two kernels:
-//  - shrink: h = A x.  A CTA takes a tile and a range of K, its warps chunks of 32 of that range in turn; weights and x go
-//    from memory straight into operands (lane c of 4 owns 8 values of a chunk, on both sides, so the order within it is
-//    free).  The warps' sums join in shared memory, the ranges' sums by their reader, both in order.
-//  - expand: y = base + B (scale h).  A CTA takes a tile and runs of 128 columns; h's parts lie in shared memory as operands,
-//    a warp's 16 columns of B come straight into operands, and y is moved in 16-byte pieces.
+//  - shrink: h = A x.  A CTA takes a tile, 16 or 32 ranks and a range of K, its warps chunks of 32 of that range in turn, each
+//    through a ring of its own (lane c of 4 owns 8 values of a chunk, on both sides, so the order within it is free).  The
+//    warps' sums join in shared memory, the ranges' sums by their reader, both in order.
+//  - expand: y = base + B (scale h).  A CTA takes runs of 128 columns of one tile after another; h's parts lie in shared memory as
+//    operands, a warp's 16 columns of B and their part of the base come through its ring, y is written in 16-byte pieces.
 // Bound by the bytes of base, y and x for many rows (2048 rows of 5 fp16 adapters of rank 32 beside 4096 -> 28672 98 us, 5.2
 // TB/s), by two rounds of loads and a join in each kernel for few (one row of rank 16 beside 4096 -> 4096 4.5 us; 40 rows of 12
 // fp32 adapters of rank 64 beside 14336 -> 4096 17.0 us for 39 MB; 64 rows of 40 of rank 16 beside 4096 -> 6144 12.3 us, in
 // expand by its instructions: runs of 16 columns a warp for one or two rows).  Expand starts while shrink runs: what shrink does
 // not write (the plan, B, the base) is fetched before its wait, which takes 0.7 us of a row's time.
 // Precision: fp16 products of two parts of 11 bits (x, h and fp32 weights; fp16 weights are operands as they are), after a power
-// of two has brought the largest of a row's 32 values (of a chunk; of h all) to [2^13, 2^14), which leaves the low part 24
-// bits below fp16's smallest normal number: 2^-22 of a value, 2^-38 of the largest.  The product of two low parts is left
+// of two has brought the largest of a row's 32 values (of a chunk; of h all) to [2^13, 2^14): 2^-22 of a value or fp16's
+// smallest step of 2^-24, which is 2^-38 of the largest, stays.  The product of two low parts is left
 // out.  Tensor cores cut their sums: those of a chunk start from zero, small products first, and are added in fp32.  (tf32
 // needs no scaling, but mma.sync does 128 of its multiplications a cycle and SM.)
 #include <algorithm>
