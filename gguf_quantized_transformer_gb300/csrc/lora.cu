@@ -14,9 +14,9 @@
 // expand by its instructions: runs of 16 columns a warp for one or two rows).  Expand starts while shrink runs: what shrink does
 // not write (the plan, B, the base) is fetched before its wait, which takes 0.7 us of a row's time.
 // Precision: fp16 products of two parts of 11 bits (x, h and fp32 weights; fp16 weights are operands as they are), after a power
-// of two has brought the largest of a row's 32 values (of a chunk; of h all) to [2^13, 2^14): 2^-22 of a value or fp16's
-// smallest step of 2^-24, which is 2^-38 of the largest, stays.  The product of two low parts is left
-// out.  Tensor cores cut their sums: those of a chunk start from zero, small products first, and are added in fp32.  (tf32
+// of two has brought the largest of a row's 32 values (of a chunk; of h all) to [2^13, 2^14), or [2^13, 2^15] with fp32 weights:
+// 2^-22 of a value or half of fp16's smallest step of 2^-24, which is 2^-38 of the largest, stays.  The product of two low parts
+// is left out.  Tensor cores cut their sums: those of a chunk start from zero, small products first, and are added in fp32.  (tf32
 // needs no scaling, but mma.sync does 128 of its multiplications a cycle and SM.)
 #include <algorithm>
 #include <type_traits>
@@ -175,16 +175,32 @@ __device__ __forceinline__ void powers(float m, float& down, float& up) {
     down = __uint_as_float((unsigned)(127 + 13 - e) << 23);
     up = __uint_as_float((unsigned)(127 - 13 + e) << 23);
 }
-// 8 values of lanes c = 0..3 (32 of one row) as scaled parts, in pairs; the power that takes the sums back
+// The same for fp32 weights and what meets them, for m >= kLeast: 2^k with k even brings it to [2^13, 2^15]; and 2^(-k / 2).  A sum
+// of products is taken back by the product of two such roots, twice: that product is in [2^-126, 2^114], so that nothing on the
+// way leaves fp32's range where the result does not.  (The sum times the weights' whole power alone is infinite for weights of
+// 1e36, though x of 1e-36 brings it back.)
+constexpr float kLeast = 0x1p-112f;
+__device__ __forceinline__ void power_root(float m, float& down, float& root) {
+    const int k = (int)(0x47000000u - __float_as_uint(m)) & ~0xFFFFFF;  // k 2^23: 15 less the exponent, the mantissa too, down to even
+    down = __int_as_float(0x3F800000 + k);
+    root = __int_as_float(0x3F800000 - (k >> 1));
+}
+// s p^2 + acc
+__device__ __forceinline__ float2 back_from(const float2& s, const float2& p, const float2& acc) { return fma2(mul2(s, p), p, acc); }
+// 8 values of lanes c = 0..3 (32 of one row) as scaled parts, in pairs; the power, or its ROOT, that takes the sums back
+template <bool ROOT>
 __device__ __forceinline__ float parts8(const uint4& v, const uint4& w, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
     float x[8] = {__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w),
                   __uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w)};
-    float m = 0.f, down, up;
+    float m = ROOT ? kLeast : 0.f, down, up;
 #pragma unroll
     for (int i = 0; i < 8; i++) m = fmaxf(m, fabsf(x[i]));
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    powers(m, down, up);
+    if (ROOT)
+        power_root(m, down, up);
+    else
+        powers(m, down, up);
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         const float2 y = mul2(make_float2(x[2 * i], x[2 * i + 1]), both(down));
@@ -242,10 +258,10 @@ __device__ __forceinline__ void shrink_tile(const LoraArgs& a, const int* row, i
         __syncwarp();  // the other lanes' pieces have landed
         const uint32_t at = ring + slot * STAGE;
         uint32_t xh[NT][4], xl[NT][4];
-        float2 up[NT];  // of rows 2c and 2c + 1 of each 8
+        float2 up[NT];  // of rows 2c and 2c + 1 of each 8 (fp32 weights: its root)
 #pragma unroll
         for (int t = 0; t < NT; t++) {
-            const float u = parts8(line8(at + WB + 1024 * t, 0), line8(at + WB + 1024 * t, 1), xh[t], xl[t]);
+            const float u = parts8<!F16>(line8(at + WB + 1024 * t, 0), line8(at + WB + 1024 * t, 1), xh[t], xl[t]);
             up[t] = make_float2(__shfl_sync(0xffffffffu, u, 8 * c), __shfl_sync(0xffffffffu, u, 8 * c + 4));
         }
 #pragma unroll
@@ -258,7 +274,7 @@ __device__ __forceinline__ void shrink_tile(const LoraArgs& a, const int* row, i
                     const uint4 v = shared16(at + (2 * m + h) * 512 + lane * 16);
                     hi[h][0] = v.x, hi[h][1] = v.y, hi[h][2] = v.z, hi[h][3] = v.w;
                 } else {
-                    wup[h] = parts8(line8(at + 1024 * (2 * m + h), 0), line8(at + 1024 * (2 * m + h), 1), hi[h], lo[h]);
+                    wup[h] = parts8<true>(line8(at + 1024 * (2 * m + h), 0), line8(at + 1024 * (2 * m + h), 1), hi[h], lo[h]);
                 }
             }
             float s[NT][4];
@@ -281,9 +297,8 @@ __device__ __forceinline__ void shrink_tile(const LoraArgs& a, const int* row, i
             for (int t = 0; t < NT; t++)
 #pragma unroll
                 for (int h = 0; h < 2; h++) {
-                    float2 v = make_float2(s[t][2 * h], s[t][2 * h + 1]);
-                    if (!F16) v = mul2(v, both(wup[h]));
-                    const float2 y = fma2(v, up[t], make_float2(acc[m][t][2 * h], acc[m][t][2 * h + 1]));
+                    const float2 v = make_float2(s[t][2 * h], s[t][2 * h + 1]), z = make_float2(acc[m][t][2 * h], acc[m][t][2 * h + 1]);
+                    const float2 y = F16 ? fma2(v, up[t], z) : back_from(v, mul2(up[t], both(wup[h])), z);
                     acc[m][t][2 * h] = y.x, acc[m][t][2 * h + 1] = y.y;
                 }
         }
@@ -350,8 +365,8 @@ __global__ void __launch_bounds__(kShrinkWarps<F16, MT> * 32, 1) lora_shrink_ker
 
 // ---------------------------------------------------------------- expand
 
-// 2 V values of a row of B from shared memory in pairs (of fp32 weights as scaled parts, of the 8 V of four lanes; the power that
-// takes sums back).  left: how many the adapter's rank has from this lane's first on.
+// 2 V values of a row of B from shared memory in pairs (of fp32 weights as scaled parts, of the 8 V of four lanes; the root of the
+// power that takes sums back).  left: how many the adapter's rank has from this lane's first on.
 template <bool F16, int V>
 __device__ __forceinline__ float weights(uint32_t at, int left, uint32_t (&hi)[V], uint32_t (&lo)[V]) {
     constexpr int W = F16 ? V : 2 * V;  // words
@@ -376,12 +391,12 @@ __device__ __forceinline__ float weights(uint32_t at, int left, uint32_t (&hi)[V
         }
         return 1.f;
     } else {
-        float x[2 * V], m = 0.f, down, up;
+        float x[2 * V], m = kLeast, down, up;
 #pragma unroll
         for (int i = 0; i < 2 * V; i++) x[i] = i < left ? __uint_as_float(w[i]) : 0.f, m = fmaxf(m, fabsf(x[i]));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        powers(m, down, up);
+        power_root(m, down, up);
 #pragma unroll
         for (int i = 0; i < V; i++) {
             const float2 y = mul2(make_float2(x[2 * i], x[2 * i + 1]), both(down));
@@ -399,7 +414,7 @@ template <bool F16, int V, bool VEC, int NST, int CTAS>
 __global__ void __launch_bounds__(kThreads, CTAS) lora_expand_kernel(LoraArgs a, int max_tiles, int sms, int rr) {
     extern __shared__ __align__(16) uint4 sm_h[];  // [steps][2 row tiles][hi, lo][32 lanes], then the rings
     __shared__ int sm_row[kLoraTile];
-    __shared__ float sm_up[kLoraTile];  // the powers of two that take the rows of h back
+    __shared__ float sm_up[kLoraTile];  // the powers of two that take the rows of h back (fp32 weights: their roots)
     constexpr int SG = (V + 1) / 2;     // matrix steps of a group of 8 V ranks
     constexpr int HR = kLoraTile / kWarps, HQ = kLoraMaxRank / 32;
     constexpr int es = F16 ? 2 : 4;
@@ -524,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) lora_expand_kernel(LoraArgs a,
         for (int x = 0; x < HR; x++) {
             const int row = warp + kWarps * x;
             if (row >= 16 * mt) break;
-            float m = 0.f, down, up;
+            float m = F16 ? 0.f : kLeast, down, up;
 #pragma unroll
             for (int q = 0; q < HQ; q++) {
                 h[x][q] = lane + 32 * q < rank ? h[x][q] * scale : 0.f;
@@ -532,7 +547,10 @@ __global__ void __launch_bounds__(kThreads, CTAS) lora_expand_kernel(LoraArgs a,
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            powers(m, down, up);
+            if (F16)
+                powers(m, down, up);
+            else
+                power_root(m, down, up);
             if (lane == 0) sm_up[row] = up;
 #pragma unroll
             for (int q = 0; q < HQ; q++) {
@@ -598,8 +616,8 @@ __global__ void __launch_bounds__(kThreads, CTAS) lora_expand_kernel(LoraArgs a,
                         } else {
 #pragma unroll
                             for (int h = 0; h < 4; h += 2) {
-                                const float2 z = fma2(make_float2(sum[m][t][h], sum[m][t][h + 1]), back[t],
-                                                      make_float2(acc[m][t][h], acc[m][t][h + 1]));
+                                const float2 z = back_from(make_float2(sum[m][t][h], sum[m][t][h + 1]), mul2(back[t], both(up[2 * m + h / 2])),
+                                                           make_float2(acc[m][t][h], acc[m][t][h + 1]));
                                 acc[m][t][h] = z.x, acc[m][t][h + 1] = z.y;
                             }
                         }
@@ -610,7 +628,8 @@ __global__ void __launch_bounds__(kThreads, CTAS) lora_expand_kernel(LoraArgs a,
                 if (8 * i >= tile.z) break;
                 if (at[i] < 0 || n >= a.N) continue;
                 const int m = i / 2, h = 2 * (i & 1);
-                float4 v = make_float4(acc[m][0][h] * up[i], acc[m][0][h + 1] * up[i], acc[m][1][h] * up[i], acc[m][1][h + 1] * up[i]);
+                float4 v = make_float4(acc[m][0][h], acc[m][0][h + 1], acc[m][1][h], acc[m][1][h + 1]);
+                if (F16) v.x *= up[i], v.y *= up[i], v.z *= up[i], v.w *= up[i];
                 float* p = a.y + at[i] * a.ldy + n;
                 if (VEC) {
                     if (a.base) {
