@@ -917,9 +917,11 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
             float m = ml.x;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const bool none = ml.x == -CUDART_INF_F && ml.y == 0.f;  // it adds nothing
-            const float f = none ? 0.f : ex2t(ml.x - m);
-            float den = none ? 0.f : f * ml.y;
+            // A piece that saw nothing adds nothing; one that saw only scores of -infinity has weights of zero, which a value that is
+            // not finite turns into NaN.
+            const bool none = __float_as_uint(ml.y) == 0;
+            const float f = ml.x == -CUDART_INF_F ? 0.f : ex2t(ml.x - m);
+            float den = f * ml.y;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
             const bool saw = __any_sync(0xffffffffu, __float_as_uint(ml.y) != 0);
@@ -1008,9 +1010,9 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
                 m = top;
                 den *= f, num.x *= f, num.y *= f, num.z *= f, num.w *= f;
             }
-            const bool none = ml.x == -CUDART_INF_F && ml.y == 0.f;
-            const float f = none ? 0.f : ex2t(ml.x - m);
-            float sum = none ? 0.f : f * ml.y;
+            const bool none = __float_as_uint(ml.y) == 0;  // (as above)
+            const float f = ml.x == -CUDART_INF_F ? 0.f : ex2t(ml.x - m);
+            float sum = f * ml.y;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             den += sum;

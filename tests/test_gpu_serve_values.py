@@ -1,7 +1,9 @@
 """The operators of a serving step at values and in orders where a mistake would be small or rare."""
+import numpy as np
 import pytest
 
-from test_gpu_serve import af, lora_call, lora_ref  # noqa: F401
+from test_gpu_draft import new_cache, write
+from test_gpu_serve import af, attend, lora_call, lora_ref  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -38,3 +40,31 @@ def test_lora_large_factors_that_do_not_meet(af):
     y = torch.empty(n, N, device="cuda")
     lora_call(af, x, torch.zeros(n, dtype=torch.int32, device="cuda"), a, b, None, None, None, y, N)
     assert torch.isfinite(y).all()
+
+
+# ---------------------------------------------------------------- attention: values that are not finite where work is cut
+
+@pytest.mark.parametrize("what", [np.inf, -np.inf, np.nan])
+@pytest.mark.parametrize("lo,hi,at", [(0, 10000, 5000), (9000, 19900, 9900), (64, 128, 100), (19984, 20000, 19990), (3000, 3400, 3100)])
+@pytest.mark.parametrize("G", [4, 8])
+def test_attention_paged_values_behind_scores_of_minus_infinity(af, what, lo, hi, at, G):
+    """Slots lo..hi have scores of -infinity (fp32 products out of range), one of them a value that is not finite: its weight of
+    zero times it is NaN wherever the work on the row is cut; the other dims are finite."""
+    kvh, D, P, m, dim = 1, 64, 16, 20000, 5
+    cache = new_cache("f32", kvh, m, D, 0)
+    k, v = torch.zeros(m, D, device="cuda"), torch.randn(m, D, device="cuda")
+    k[lo:hi] = -2.0 ** 68
+    v[at, dim] = float(what)
+    write(af, "f32", cache, k, v, kvh, D, m, slot0=0)
+    q = np.full((3, G, D), 2.0 ** 68, np.float32)
+    q[1] = 1.0  # finite scores, but so large that the slots' weights are 0 too
+    pos = [m - 1, m - 1, lo + 3 if lo else 3]
+    table = np.tile(np.arange(m // P), (3, 1))
+    got = attend(af, "f32", cache, q, kvh, P, m // P, table, pos).cpu().numpy().reshape(3, G, D)
+    assert np.isnan(got[:2, :, dim]).all()
+    keep = np.r_[0:lo, hi:m]
+    others = np.arange(D) != dim
+    want = v[keep].double().mean(0).cpu().numpy()
+    assert np.abs(got[:2, :, others] - want[others]).max() <= 2.0 ** -19 * float(v[torch.isfinite(v)].abs().max())
+    # a row that does not see the value is as it was: finite where some of its scores are, NaN where all are -infinity
+    assert np.isnan(got[2]).all() if lo == 0 else np.isfinite(got[2]).all()
