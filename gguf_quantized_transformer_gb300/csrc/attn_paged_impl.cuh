@@ -958,7 +958,11 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
         }
         job -= C::HEADS;
     }
-    if (!own0.z && !own1.z) return;
+    // (rows that may be a cache are visible before the CTA ends: see launch_chained)
+    if (!own0.z && !own1.z) {
+        if (a.ldo <= kCacheRow) __threadfence();
+        return;
+    }
     // ---- items of several CTAs: the last CTA to leave its piece joins them, in order
     __shared__ int2 sm_chain[2];  // first and last CTA of an item that this one joins; first < 0: it does not
     const int4 mine_of = tid ? own1 : own0;
@@ -1033,6 +1037,7 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
             *reinterpret_cast<float4*>(a.out + (int64_t)p.x * a.ldo + (int64_t)(g * G + head) * D + 4 * lane) =
                 make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
     }
+    if (a.ldo <= kCacheRow) __threadfence();
 }
 
 // One translation unit per cache type.

@@ -654,6 +654,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) lora_expand_kernel(LoraArgs a,
         }
     }
     pdl_wait();  // (also where there was nothing to do)
+    if (a.ldy <= kCacheRow) __threadfence();  // what may be a cache is visible before the CTA ends: see launch_chained
 }
 
 // Ranks of an item of shrink.  (2048 rows of fp32 adapters of rank 64 101 us, in items of 16 129: x is read once an item; one row of

@@ -68,3 +68,70 @@ def test_attention_paged_values_behind_scores_of_minus_infinity(af, what, lo, hi
     assert np.abs(got[:2, :, others] - want[others]).max() <= 2.0 ** -19 * float(v[torch.isfinite(v)].abs().max())
     # a row that does not see the value is as it was: finite where some of its scores are, NaN where all are -infinity
     assert np.isnan(got[2]).all() if lo == 0 else np.isfinite(got[2]).all()
+
+
+# ---------------------------------------------------------------- calls that write a cache just before the decode attention
+
+class Chain:
+    """One kv head's fp32 cache of `ctx` slots, whose keys are written by adapters just before the decode attention, which reads
+    ahead: two sets of keys in turn, each with the result that a synchronisation in between gives."""
+    D, K, r, H = 128, 64, 16, 4
+
+    def __init__(self, af, ctx, seed):
+        self.af, self.ctx = af, ctx
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.normal = lambda *s: torch.randn(*s, generator=g, device="cuda")
+        self.q, self.k, self.v = self.normal(self.H * self.D), torch.zeros(1, ctx, self.D, device="cuda"), self.normal(1, ctx, self.D)
+        self.a = (self.normal(1, self.r, self.K) / 8).half()
+
+    def adapters(self, n, N):
+        """What af_lora needs for n rows of N: two inputs and the rest."""
+        af = self.af
+        plan = torch.empty(af.af_lora_plan_bytes(n, 1), dtype=torch.uint8, device="cuda")
+        ws = torch.empty(af.af_lora_workspace(n, 1, self.r, self.K, N), dtype=torch.uint8, device="cuda")
+        af.af_lora_plan(torch.zeros(n, dtype=torch.int32, device="cuda"), n, 1, plan, plan.numel())
+        x = [self.normal(n, self.K) * 2.0 ** i for i in (0, 1)]
+        b = (self.normal(1, N, self.r) / 4).half()
+        return lambda i, y, ldy: af.af_lora(x[i], self.K, n, plan, self.a, b, af.AF_F16, None, None, 1, self.r, self.K, N, None, 0, y, ldy,
+                                            ws, ws.numel())
+
+    def attend(self, out):
+        self.af.af_attention_decode_static(self.q, self.k, self.v, self.af.AF_F32, self.H, 1, self.D, self.ctx, self.ctx - 1, out)
+
+    def check(self, step):
+        """step(i) writes keys i; the attention directly behind it has to see them."""
+        want = [torch.zeros(self.H * self.D, device="cuda") for _ in range(2)]
+        for i in (0, 1):
+            step(i)
+            torch.cuda.synchronize()
+            self.attend(want[i])
+            torch.cuda.synchronize()
+        outs = [torch.zeros(self.H * self.D, device="cuda") for _ in range(30)]
+        torch.cuda.synchronize()
+        for i, out in enumerate(outs):
+            step(i % 2)
+            self.attend(out)
+        torch.cuda.synchronize()
+        assert not torch.equal(want[0], want[1])
+        assert all(torch.equal(y, want[i % 2]) for i, y in enumerate(outs))
+
+
+@pytest.mark.parametrize("ctx", [640, 6000])
+@pytest.mark.parametrize("between", ["nothing", "plan", "pages"])
+def test_decode_attention_sees_an_adapters_keys_behind_other_calls(af, ctx, between):
+    """A call in between that lets the next kernel start before its own wait, and touches nothing of the cache."""
+    c = Chain(af, ctx, 3)
+    keys = c.adapters(ctx, c.D)
+    plan = torch.empty(af.af_lora_plan_bytes(64, 4), dtype=torch.uint8, device="cuda")
+    ids = torch.zeros(64, dtype=torch.int32, device="cuda")
+    zeros = [torch.zeros(k, dtype=torch.int32, device="cuda") for k in (4, 4, 4, 64, 4 * 8, 4, 4, 5, 16, 16, 16)]
+    ws = torch.empty(af.af_kv_pages_workspace(4), dtype=torch.uint8, device="cuda")
+    ln, new, pool, free, table, ln_out, pool_out, start, slots, pos, seq = zeros
+
+    def step(i):
+        keys(i, c.k, c.D)
+        if between == "plan":
+            af.af_lora_plan(ids, 64, 4, plan, plan.numel())
+        elif between == "pages":
+            af.af_kv_pages(ln, new, 4, 16, 64, pool, free, table, 8, ln_out, pool_out, start, slots, pos, seq, 16, ws, ws.numel())
+    c.check(step)
