@@ -207,7 +207,6 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
     float* const far = C::NEAR ? reinterpret_cast<float*>(smem + C::RING) : a.ws + paged_far(gridDim.x, D) + (size_t)blockIdx.x * NW * C::PIECE;
 
     pdl_wait();  // positions, tables, q and the cache are written by earlier kernels
-    if (a.ldo > kCacheRow) pdl_launch_dependents();
     // request and last position of a row; -1: it sees nothing
     auto row_of = [&](int r) {
         const int who = a.seq ? __ldcg(a.seq + r) : r;
@@ -958,9 +957,8 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
         }
         job -= C::HEADS;
     }
-    // (rows that may be a cache are visible before the CTA ends: see launch_chained)
     if (!own0.z && !own1.z) {
-        if (a.ldo <= kCacheRow) __threadfence();
+        __threadfence();
         return;
     }
     // ---- items of several CTAs: the last CTA to leave its piece joins them, in order
@@ -1037,7 +1035,7 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
             *reinterpret_cast<float4*>(a.out + (int64_t)p.x * a.ldo + (int64_t)(g * G + head) * D + 4 * lane) =
                 make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
     }
-    if (a.ldo <= kCacheRow) __threadfence();
+    __threadfence();  // (and no early launch of the next kernel: the rows may be a cache, see launch_chained)
 }
 
 // One translation unit per cache type.

@@ -422,7 +422,6 @@ __global__ void __launch_bounds__(kThreads, CTAS) lora_expand_kernel(LoraArgs a,
     const int row_bytes = a.rank * es, stage = (VEC ? 2048 : 0) + 16 * row_bytes, steps = (a.rank + 8 * V - 1) / (8 * V) * SG;
     const uint32_t ring = smem_u32(sm_h) + steps * 2 * 64 * 16 + warp * NST * stage;
     const int* plan = (const int*)a.plan;
-    if (a.ldy > kCacheRow) pdl_launch_dependents();
     const int4 head = __ldcg(reinterpret_cast<const int4*>(plan));
     const int4 early = first_tiles(plan, lane, max_tiles);
     const int tiles = a.base && a.base == a.y ? head.y : head.x;  // in place, rows without an adapter stay as they are
@@ -654,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) lora_expand_kernel(LoraArgs a,
         }
     }
     pdl_wait();  // (also where there was nothing to do)
-    if (a.ldy <= kCacheRow) __threadfence();  // what may be a cache is visible before the CTA ends: see launch_chained
+    __threadfence();  // (and no early launch of the next kernel: y may be a cache, see launch_chained)
 }
 
 // Ranks of an item of shrink.  (2048 rows of fp32 adapters of rank 64 101 us, in items of 16 129: x is read once an item; one row of

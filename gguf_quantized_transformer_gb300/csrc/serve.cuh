@@ -4,10 +4,6 @@
 
 namespace af {
 
-// Rows of a result this close together may be a kv head's slots of an fp32 cache, which the decode attention reads before its
-// wait: the next kernel does not start early
-constexpr int kCacheRow = 256;
-
 // ---- pages and slots (kv_pages.cu)
 constexpr int kPagesMaxSeqs = 1 << 16;
 struct PagesArgs {

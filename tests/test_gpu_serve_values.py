@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 
 from test_gpu_draft import new_cache, write
-from test_gpu_serve import af, attend, lora_call, lora_ref  # noqa: F401
+from test_gpu_serve import Paged, af, attend, i32, lora_call, lora_ref  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -135,3 +135,32 @@ def test_decode_attention_sees_an_adapters_keys_behind_other_calls(af, ctx, betw
         elif between == "pages":
             af.af_kv_pages(ln, new, 4, 16, 64, pool, free, table, 8, ln_out, pool_out, start, slots, pos, seq, 16, ws, ws.numel())
     c.check(step)
+
+
+def test_decode_attention_sees_an_adapters_keys_at_any_stride(af):
+    """Rows of an adapter call that are every fourth slot, eight neighbouring slots each, or one row of all slots."""
+    c = Chain(af, 6000, 4)
+    fourth, eight, one = c.adapters(1500, c.D), c.adapters(750, 8 * c.D), c.adapters(1, 6000 * c.D)
+    rows = [c.k[0, i:] for i in range(4)]
+
+    def every_fourth(i):
+        for y in rows:
+            fourth(i, y, 4 * c.D)
+    c.check(every_fourth)
+    c.check(lambda i: eight(i, c.k, 8 * c.D))
+    c.check(lambda i: one(i, c.k, 6000 * c.D + 4))
+
+
+@pytest.mark.parametrize("lens", ["short", "long"])
+def test_decode_attention_sees_keys_that_the_paged_attention_wrote(af, lens):
+    """The paged attention's rows, of eight heads, as eight neighbouring slots each."""
+    H, D, P, n = 8, 128, 16, 200
+    rng = np.random.default_rng(5)
+    lens = rng.integers(1, 40, n) if lens == "short" else rng.integers(1, 400, n)
+    lens[::9] = 0  # rows of zeros
+    p = Paged(af, "f16", rng, 2, D, P, lens)
+    c = Chain(af, n * H, 6)
+    q, table, pos = [c.normal(n, H * D) * (i + 1) for i in (0, 1)], i32(p.table), i32(lens - 1)
+    ws = torch.empty(af.af_attention_paged_workspace(H, 2, D), dtype=torch.uint8, device="cuda")
+    c.check(lambda i: af.af_attention_paged(q[i], H * D, *p.cache, af.KVTYPE["f16"], H, 2, D, P, p.n_pages, table, table.shape[1], n, None,
+                                            pos, n, ws, ws.numel(), c.k, H * D))
