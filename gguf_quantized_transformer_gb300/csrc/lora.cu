@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kPlanThreads) lora_plan_kernel(const int* __re
     if (t == 0) {
         first[adapters + 1] = tiles;
         const int bare_tiles = (bare + kLoraTile - 1) / kLoraTile;
-        *reinterpret_cast<int4*>(plan) = make_int4(tiles, tiles - bare_tiles, n - bare, 0);
+        *reinterpret_cast<int4*>(plan) = make_int4(tiles, tiles - bare_tiles, n - bare, lora_plan_sizes(n, adapters));
     }
     __syncthreads();
     for (int i = t; i < tiles; i += kPlanThreads) {
@@ -333,7 +333,8 @@ __global__ void __launch_bounds__(kShrinkWarps<F16, MT> * 32, 1) lora_shrink_ker
     const int early_row = tid < a.n ? __ldcg(order + tid) : 0;
     const int4 head = __ldcg(reinterpret_cast<const int4*>(plan));
     const int4 early = first_tiles(plan, lane, max_tiles);
-    const int tiles = head.y, rows = head.z, rt = (a.rank + RR - 1) / RR;
+    const int tiles = head.w == lora_plan_sizes(a.n, a.adapters) ? head.y : 0;  // (another call's plan: nothing, see expand)
+    const int rows = head.z, rt = (a.rank + RR - 1) / RR;
     const int splits = lora_splits(tiles * rt, a.K, sms, NW), chunks = a.K / 32;
     for (int item = blockIdx.x; item < tiles * rt * splits; item += gridDim.x) {
         const int split = item % splits, rest = item / splits, r0 = rest % rt * RR;
@@ -424,7 +425,8 @@ __global__ void __launch_bounds__(kThreads, CTAS) lora_expand_kernel(LoraArgs a,
     const int* plan = (const int*)a.plan;
     const int4 head = __ldcg(reinterpret_cast<const int4*>(plan));
     const int4 early = first_tiles(plan, lane, max_tiles);
-    const int tiles = a.base && a.base == a.y ? head.y : head.x;  // in place, rows without an adapter stay as they are
+    const bool fits = head.w == lora_plan_sizes(a.n, a.adapters);
+    const int tiles = !fits ? 0 : a.base && a.base == a.y ? head.y : head.x;  // in place, rows without an adapter stay as they are
     const int rows = head.z, splits = lora_splits(head.y * ((a.rank + rr - 1) / rr), a.K, sms, rr == 16 ? kShrinkWarps<F16, 1> : kShrinkWarps<F16, 2>), cols = (a.N + kCols - 1) / kCols;
     // The CTA's share: an equal one of all runs, the first CTAs one more, since they start first.  (Shares of one tile each save a
     // second preparation but not the time: 64 rows of 40 adapters 15.2 us in place of 14.7, 40 rows of 12 17.7 in place of 17.0,
@@ -653,6 +655,10 @@ __global__ void __launch_bounds__(kThreads, CTAS) lora_expand_kernel(LoraArgs a,
         }
     }
     pdl_wait();  // (also where there was nothing to do)
+    if (!fits) {  // what the plan names may not be rows and adapters of this call: NaN, and no address is formed from it
+        for (int64_t i = (int64_t)me * kThreads + tid; i < (int64_t)a.n * a.N; i += (int64_t)ctas * kThreads)
+            a.y[i / a.N * a.ldy + i % a.N] = __int_as_float(0x7FC00000);
+    }
     __threadfence();  // (and no early launch of the next kernel: y may be a cache, see launch_chained)
 }
 

@@ -48,8 +48,10 @@ cudaError_t launch_attn_paged(const PagedArgs& a, cudaStream_t s);
 // ---- low-rank adapters (lora.cu)
 constexpr int kLoraMaxRows = 1 << 16, kLoraMaxAdapters = 4096, kLoraMaxRank = 128;
 constexpr int kLoraTile = 32;  // rows of one adapter that a CTA takes at once
-// A plan: header {tiles, tiles of adapters, rows of adapters, 0}, the tiles {adapter or -1, first, count, 0}, then the rows in
-// their order
+// A plan: header {tiles, tiles of adapters, rows of adapters, lora_plan_sizes}, the tiles {adapter or -1, first, count, 0}, then the
+// rows in their order
+__host__ __device__ constexpr int lora_plan_sizes(int n, int adapters) { return n | adapters << 17; }
+static_assert(kLoraMaxRows < 1 << 17 && kLoraMaxAdapters < 1 << 13, "");
 inline int lora_max_tiles(int n, int adapters) { return n / kLoraTile + (n < adapters + 1 ? n : adapters + 1); }
 size_t lora_plan_bytes(int n, int adapters);
 cudaError_t launch_lora_plan(const int* ids, int n, int adapters, void* plan, cudaStream_t s);

@@ -552,7 +552,7 @@ int af_attention_paged(const float* q_dev, int64_t ldq, const void* k_cache, con
  * af_lora_plan puts the rows in the order of their adapters, once a step for all layers and projections:
  *   ids_dev   int32 [n]; a value outside [0, n_adapters) is a row without an adapter
  *   plan_dev  af_lora_plan_bytes(n, n_adapters) bytes, 16-byte aligned
- * af_lora, with the n and n_adapters of its plan:
+ * af_lora, with the n and n_adapters of its plan (a plan of others, in a buffer of this call's size, gives rows of NaN):
  *   x_dev     fp32 [n] rows of K values, ldx apart
  *   a_dev     [n_adapters][rank][K], b_dev [n_adapters][N][rank] of dtype AF_F16 or AF_F32
  *   scale_dev fp32 [n_adapters]; NULL: 1

@@ -42,6 +42,35 @@ def test_lora_large_factors_that_do_not_meet(af):
     assert torch.isfinite(y).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+@pytest.mark.parametrize("n,m,N", [(40, 6, 260), (7, 300, 33)])
+def test_lora_with_a_plan_of_other_sizes(af, dtype, n, m, N):
+    """Rows of NaN, whether the plan was made for more or fewer rows or adapters or never; the next call with its own plan is right."""
+    K, r = 64, 16
+    g = torch.Generator(device="cuda").manual_seed(1)
+    def normal(*s):
+        return torch.randn(*s, generator=g, device="cuda")
+    x, a, b, base = normal(n, K), normal(m, r, K).to(dtype), normal(m, N, r).to(dtype), normal(n, N)
+    ids = torch.randint(0, 1 << 30, (5000,), generator=g, device="cuda", dtype=torch.int32)
+    plan = torch.zeros(max(af.af_lora_plan_bytes(*s) for s in ((n, m), (5000, 4096))), dtype=torch.uint8, device="cuda")
+    right = torch.randint(-1, m, (n,), generator=g, device="cuda", dtype=torch.int32)
+    ref, tol = lora_ref(x, right, a, b, None, None, base)
+    for other in (0, 0xFF, (n + 1, m), (n - 1, m), (n, m + 1), (n, m - 1), (5000, m), (n, 4096), (5000, 4096), (1, 1)):
+        if isinstance(other, int):
+            plan.fill_(other)
+        else:
+            af.af_lora_plan(ids % other[1], *other, plan, plan.numel())
+        y = torch.full((n, N + 3), 9.0, device="cuda")
+        lora_call(af, x, None, a, b, None, None, base, y, N, plan=plan)
+        assert torch.isnan(y[:, :N]).all() and (y[:, N:] == 9.0).all()
+        y[:, :N] = base
+        lora_call(af, x, None, a, b, None, None, y, y, N, plan=plan)
+        assert torch.isnan(y[:, :N]).all() and (y[:, N:] == 9.0).all()
+        af.af_lora_plan(right, n, m, plan, plan.numel())
+        lora_call(af, x, None, a, b, None, None, base, y, N, plan=plan)
+        assert ((y[:, :N].double() - ref).abs() <= tol).all()
+
+
 # ---------------------------------------------------------------- attention: values that are not finite where work is cut
 
 @pytest.mark.parametrize("what", [np.inf, -np.inf, np.nan])
