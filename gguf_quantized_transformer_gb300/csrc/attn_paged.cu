@@ -20,8 +20,8 @@ cudaError_t launch_attn_paged_type<AF_KV_Q4_0>(const PagedArgs&, int, cudaStream
 namespace {
 
 // A mark for the counters of one call.  A workspace may hold anything, so the counters do not start at a known number: what
-// does not carry the call's mark counts as zero.  A call leaves its counters zero, so that a captured one, whose mark is
-// the same in every replay, finds them so.  The start is random: contents that this process did not write match with
+// does not carry the call's mark counts as zero.  A call leaves each of its counters zero or with its mark and a count of zero,
+// so that a captured one, whose mark is the same in every replay, finds them so.  The start is random: contents that this process did not write match with
 // 2^-48.
 unsigned long long next_mark() {
     static std::atomic<unsigned long long> at([] {

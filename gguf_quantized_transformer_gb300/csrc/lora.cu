@@ -46,7 +46,7 @@ __host__ __device__ inline int64_t plan_order(int max_tiles) { return 4 * (int64
 
 // ---------------------------------------------------------------- plan
 
-constexpr int kTileBits = 14;  // rows and tiles are summed in one word: 17 bits of rows, 13 of tiles
+constexpr int kTileBits = 14;  // rows and tiles are summed in one word: 18 bits of rows, 14 of tiles
 constexpr unsigned kTileMask = (1u << kTileBits) - 1;
 static_assert(kLoraMaxRows / kLoraTile + kLoraMaxAdapters + 1 <= (int)kTileMask && kLoraMaxRows < 1 << (32 - kTileBits), "");
 
@@ -167,8 +167,8 @@ __device__ __forceinline__ int lora_splits(int items, int K, int sms, int warps)
 }
 
 
-// 2^k that brings a largest magnitude m to [2^13, 2^14), and 2^-k.  (Below 2^-112 it comes no nearer; infinities and NaNs
-// stay what they are.)
+// 2^k that brings a largest magnitude m to [2^13, 2^14), and 2^-k.  (Below 2^-112 it comes no nearer.  An infinity stays one, and
+// its low part is NaN: what it meets is NaN.)
 __device__ __forceinline__ void powers(float m, float& down, float& up) {
     int e = (int)(__float_as_uint(m) >> 23) - 127;
     e = min(max(e, -112), 127);

@@ -563,9 +563,11 @@ int af_attention_paged(const float* q_dev, int64_t ldq, const void* k_cache, con
  *   y_dev     fp32 [n] rows, ldy apart.  Rows without an adapter are the base's.  (May overlap x_dev, which is read first)
  *   ws_dev    scratch of af_lora_workspace(n, n_adapters, rank, K, N) bytes, 256-byte aligned, of any contents; calls that
  *             may overlap in time need scratch of their own
- * Precision: x, fp32 weights and A x keep 2^-22 of each value, or 2^-38 of the largest of 32 neighbours along K (of a row of
- * A x) where that is more; sums are fp32's.  A row's result depends on the other rows only through the order in which K's
- * sums are joined; its bits do not change from call to call with the same plan.
+ * Precision: x, fp32 weights and A x keep 2^-22 of each value, or 2^-38 of the largest of 32 neighbours along K or the rank (of
+ * a row of A x; 2^-150 where that is more still); sums are fp32's.  Where a value of the formula is not finite (a NaN or an infinity in a
+ * row of x, in A for all rows of its adapter, in a row of B for their values of that column), or a sum leaves fp32's range, the
+ * result is NaN or an infinity; no other row or value is touched.  A row's result depends on the other rows only through the
+ * order in which K's sums are joined; its bits do not change from call to call with the same plan.
  * 1 <= n <= 65536, 1 <= n_adapters <= 4096; rank a multiple of 8 up to 128 (pad with rank_dev); K a multiple of 32, N any,
  * both up to 2^24.
  * x_dev, a_dev, b_dev are 16-byte aligned and ldx a multiple of 4; base_dev and y_dev 4-byte aligned (vectors of 16 bytes

@@ -43,6 +43,36 @@ def test_lora_large_factors_that_do_not_meet(af):
 
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+@pytest.mark.parametrize("what", [np.inf, -np.inf, np.nan])
+@pytest.mark.parametrize("n,m,r,K,N", [(3, 2, 8, 64, 40), (50, 4, 64, 512, 300)])
+def test_lora_values_that_are_not_finite(af, dtype, what, n, m, r, K, N):
+    """They reach the rows and columns that the formula takes them to, and no others."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    def normal(*s):
+        return torch.randn(*s, generator=g, device="cuda")
+    x, a, b, base = normal(n, K), normal(m, r, K).to(dtype), normal(m, N, r).to(dtype), normal(n, N)
+    ids = (torch.arange(n, device="cuda") % m).to(torch.int32)
+    clean = torch.empty(n, N, device="cuda")
+    lora_call(af, x, ids, a, b, None, None, base, clean, N)
+    hit = torch.zeros(n, N, dtype=torch.bool, device="cuda")
+    for kind in ("x", "a", "b"):
+        xs, as_, bs, want = x.clone(), a.clone(), b.clone(), hit.clone()
+        if kind == "x":
+            xs[n // 2, K // 3] = float(what)
+            want[n // 2] = True
+        elif kind == "a":
+            as_[1, r - 1, K - 1] = float(what)
+            want[ids == 1] = True
+        else:
+            bs[1, N // 2, 3] = float(what)
+            want[ids == 1, N // 2] = True
+        y = torch.empty(n, N, device="cuda")
+        lora_call(af, xs, ids, as_, bs, None, None, base, y, N)
+        assert torch.equal(~torch.isfinite(y), want)
+        assert torch.equal(y[~want], clean[~want])
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
 @pytest.mark.parametrize("n,m,N", [(40, 6, 260), (7, 300, 33)])
 def test_lora_with_a_plan_of_other_sizes(af, dtype, n, m, N):
     """Rows of NaN, whether the plan was made for more or fewer rows or adapters or never; the next call with its own plan is right."""
