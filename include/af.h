@@ -534,10 +534,10 @@ int af_kv_pages(const int32_t* len_dev, const int32_t* new_dev, int32_t n_seqs, 
  * The work is split by the slots that the rows see, found on the device: lengths may differ as they like, and a captured
  * call serves any lengths.  Precision, bits from call to call, and rows that see a NaN or an infinity: as
  * af_attention_tree's.  What slots hold that a row does not see reaches nothing.
- * 1 <= n <= 2048; head_dim 64 or 128, any whole group up to 64; n_kv_heads * n_pages * page_size below 2^31, page_size and
- * table_width at least 1, table_width * page_size below 2^31 - 64.  Pointers are 16-byte aligned (table_dev, seq_dev,
- * pos_dev: 4), ldq and ldo multiples of 4.  Asynchronous on `stream`, allocates nothing, can be captured (the first call on
- * a device loads the kernels: make it before a capture).  Errors: AF_EINVAL, AF_ERANGE, AF_ENOTIMPL, AF_ECUDA.
+ * 1 <= n <= 2048, 1 <= n_seqs <= 65536; head_dim 64 or 128, any whole group up to 64; n_kv_heads * n_pages * page_size below
+ * 2^31, page_size and table_width at least 1, table_width * page_size below 2^31 - 64.  Pointers are 16-byte aligned
+ * (table_dev, seq_dev, pos_dev: 4), ldq and ldo multiples of 4.  Asynchronous on `stream`, allocates nothing, can be captured
+ * (the first call on a device loads the kernels: make it before a capture).  Errors: AF_EINVAL, AF_ERANGE, AF_ENOTIMPL, AF_ECUDA.
  */
 uint64_t af_attention_paged_workspace(int32_t n_heads, int32_t n_kv_heads, int32_t head_dim);
 int af_attention_paged(const float* q_dev, int64_t ldq, const void* k_cache, const void* k_scales, const void* v_cache,
