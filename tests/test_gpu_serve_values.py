@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 
 from test_gpu_draft import new_cache, write
-from test_gpu_serve import Paged, af, attend, i32, lora_call, lora_ref  # noqa: F401
+from test_gpu_serve import ATTN, KV, LONG, Paged, af, attend, attn_ref_gpu, i32, lora_call, lora_ref  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -99,6 +99,65 @@ def test_lora_with_a_plan_of_other_sizes(af, dtype, n, m, N):
         af.af_lora_plan(right, n, m, plan, plan.numel())
         lora_call(af, x, None, a, b, None, None, base, y, N, plan=plan)
         assert ((y[:, :N].double() - ref).abs() <= tol).all()
+
+
+# ---------------------------------------------------------------- attention: precision
+
+@pytest.mark.parametrize("t", KV)
+@pytest.mark.parametrize("H,KVH,D,P,lens", ATTN + LONG)
+def test_attention_paged_precision_of_rows(af, t, H, KVH, D, P, lens):
+    """Each row's error against its own norm, with queries, keys and values of unit size: a slot left out or counted twice at a cut,
+    or a low part that is lost, shows in rows of any length.  q's parts and p's leave 2^-21 of a value each, the exponential
+    2^-22, and scores, up to 8 in powers of two, are rounded by 2^-22 a few times.  These errors differ from slot to slot, so a
+    weighted mean of independent values moves by as much of its norm as they do themselves: 2^-19 holds all of them at their
+    largest.  (Half the bits of q lost: 2^-12; a slot of 20011 left out: 6e-3 of the row.)"""
+    rng = np.random.default_rng(H * D + P + 1)
+    c = Paged(af, t, rng, KVH, D, P, lens)
+    q = rng.standard_normal((len(lens), H, D)).astype(np.float32)
+    got = attend(af, t, c.cache, q, KVH, P, c.n_pages, c.table, np.array(lens) - 1).cpu().numpy().reshape(len(lens), -1)
+    ref = attn_ref_gpu(q, c, c.slots).reshape(len(lens), -1)
+    size = np.linalg.norm(ref, axis=1)
+    err = np.linalg.norm(got - ref, axis=1)
+    print(f"largest {(err[size > 0] / size[size > 0]).max():.2e}")
+    assert (err <= 2.0 ** -19 * size).all()
+
+
+def score_bound(t, q, k, v, slots):
+    """Per value of the result: scores off by at most d_j = 2^-20 sum |q| max |k_j| / sqrt(D) change the weights by factors of
+    exp(+-d_j), which moves the mean by at most sum p_j (exp(d_j) - 1) |v_j - out| / sum p_j exp(-d_j); parts of p and v and the
+    sums leave 2^-19 of the weighted mean of |v|.  For fp16 and the codes p, times a value's scale, is held in fp16 parts whose
+    smallest step is 2^-24, while the row's largest is at least 2^9 (p = 2^10 at the reference, which is at most the largest; the
+    slot's largest scale, to a factor of 2): half a step is 2^-34 of the largest p |v|, of each slot.  (It is all that is left
+    of a dim in which the slots that count hold zeros.)"""
+    n, H, D = q.shape
+    G = H // k.shape[0]
+    out, tol = np.zeros((n, H, D)), np.zeros((n, H, D))
+    for i in range(n):
+        for h in range(H):
+            kk, vv = k[h // G, slots[i]], v[h // G, slots[i]]
+            s = kk @ q[i, h] / np.sqrt(D)
+            d = 2.0 ** -20 * np.abs(q[i, h]).sum() * np.abs(kk).max(1) / np.sqrt(D)
+            p = np.exp(s - s.max())
+            p /= p.sum()
+            out[i, h] = p @ vv
+            tol[i, h] = (p * np.expm1(d)) @ np.abs(vv - out[i, h]) / (p @ np.exp(-d)) + 2.0 ** -19 * (p @ np.abs(vv))
+            if t != "f32":
+                tol[i, h] += len(p) * 2.0 ** -34 * (p * np.abs(vv).max(1)).max()
+    return out, tol
+
+
+@pytest.mark.parametrize("t", KV)
+@pytest.mark.parametrize("H,D,spread,qs", [(8, 64, 8.0, 4.0), (16, 64, 30.0, 0.01), (8, 64, 1e-3, 1e4), (4, 128, 3.0, 1.0), (16, 128, 1.0, 8.0)])
+def test_attention_paged_precision_of_wide_scores(af, t, H, D, spread, qs):
+    """Scores far apart, each value against what its own row's scores allow."""
+    rng = np.random.default_rng(17)
+    lens = [900, 50, 1, 3000, 333]
+    c = Paged(af, t, rng, 2, D, 16, lens, spread=spread)
+    q = (rng.standard_normal((5, H, D)) * qs).astype(np.float32)
+    got = attend(af, t, c.cache, q, 2, 16, c.n_pages, c.table, np.array(lens) - 1).cpu().numpy().reshape(q.shape)
+    ref, tol = score_bound(t, q.astype(np.float64), c.k, c.v, c.slots)
+    print(f"largest {(np.abs(got - ref)[tol > 0] / tol[tol > 0]).max():.2f} of the bound")
+    assert (np.abs(got - ref) <= tol).all()
 
 
 # ---------------------------------------------------------------- attention: values that are not finite where work is cut
