@@ -2,9 +2,15 @@
 //   out = sum_j p_j v_j / sum_j p_j,   p_j = exp(q . k_j / sqrt(D)),   k_j, v_j at slot table[seq][j / page] page + j % page.
 // A row that sees no slot gives zeros; one whose scores are all -infinity has no softmax and gives NaN.
 //
-// Bound by the bytes of the cache (fp32 and fp16: 0.92 to 1.0 of the measured copy rate for long batches; Q8_0 0.87), with
-// codes by the instructions that unpack them (Q4_0 0.5), for few slots by its chain of dependent loads:
-//  - A work item is a row, a kv head and up to 4 NT heads of its group.  All items' stages of KS slots in a row are cut into
+// Bound by the bytes of the cache (of the measured copy rate, for long batches with groups of 4: fp32 0.92 to 1.0, fp16 0.93 to
+// 0.97, Q8_0 with heads of 128 0.84 to 0.90), for few slots by its chain of dependent loads.  Q4_0 (0.51), heads of 64 with codes
+// (Q8_0 0.70, Q4_0 0.37) and fp32 with groups of 8 (0.78, the tf32 rate of mma.sync) are bound in the SM: for Q4_0 issue is 65%
+// full and the ALU pipe 59%, next to nothing waits for memory, and a scheduler's three warps mostly wait for their own last
+// results.  How it is laid out:
+//  - A work item is a row, a kv head and up to 4 NT heads of its group.  (A group above 8 is several items, each of which copies and
+//    unpacks K and V: 16 rows of 8000 fp16 slots 51 us with groups of 8, 88 with 16, 162 with 32.  A group of 5 costs what one of
+//    8 does.  New tokens of one request are items of their own too: 8 requests with 8 each over 4096 slots take 119 us, with one
+//    each 29.)  All items' stages of KS slots in a row are cut into
 //    equal ranges, one per warp: no warp waits for another whatever the lengths are, one long request is spread over the
 //    whole GPU and many short ones need little joining.  The ranges come from prefix sums of the rows' stages, which each
 //    CTA forms from pos (at most kPagedMaxRows rows).
@@ -78,7 +84,7 @@ struct PagedCfg {
     // a stage: K rows, V rows, and the 16 bytes around each slot's K and V scales
     static constexpr int OV = KS * RB, OKS = 2 * KS * RB, OVS = OKS + (QUANT ? 16 * KS : 0);
     static constexpr int STAGE = OVS + (QUANT ? 16 * KS : 0);
-    static constexpr int NST = 2;  // stages of a warp's ring (three measured 1 to 2% slower, in every type)
+    static constexpr int NST = 2;  // stages of a warp's ring (three, which no longer fit, were 1 to 2% slower)
     static constexpr int PIECE = HEADS * (D + 2);  // floats of a warp's piece
     static_assert(PIECE * 4 <= NST * STAGE, "a piece fits the ring");
     static constexpr int RING = NW * NST * STAGE, ROWS = (kPagedMaxRows + 1) * 4, STATIC = NW * (32 + 16 * NST + 8) + 256;
@@ -249,7 +255,7 @@ __global__ void __launch_bounds__(PagedCfg<TYPE, D, NT>::NW * 32, 1) attn_paged_
             total += y;
         }
         // the first `rest` warps have a stage more than the others; a warp has at least 32 slots, so that short items of a
-        // small call need no joining
+        // small call need no joining (chosen by calls with groups of 4 and 8)
         const I units = total * GI, warps = gridDim.x * NW, least = 32 / KS;
         I each = units / warps, rest = units - each * warps;
         if (each < least) each = least, rest = 0;

@@ -8,8 +8,9 @@
 // new token, so the thread of the page's first token writes the table.  Small steps do both in the one CTA, larger ones the
 // second part in a grid of their own.
 // Latency-bound: one or two launches, three rounds of dependent loads (lengths; requests; pages), the barriers of the sums.  In
-// one CTA 64 requests take 3.0 us and a step of 256 in which 16 end and give back 4000 pages 6.3; 24 prompts with 414,896 rows, in two
-// launches, 7.7, of which the 5 MB of slots, positions and requests are 0.7.
+// one CTA 64 requests take 3.0 us and a step of 256 in which 16 end and give back 4000 pages 6.2; 24 prompts with 414,896 rows, in
+// two launches, 7.3, of which the 5 MB of slots, positions and requests are 0.7.  (In a graph of such calls; launched one by one 4.5,
+// 6.3 and 7.7 to 10.)
 #include <algorithm>
 
 #include "serve.cuh"
@@ -19,9 +20,10 @@ namespace af {
 
 namespace {
 
-// Threads of the scanning CTA: fewer where it does both parts for up to 512 requests.  (64 requests 3.2 us with 512, 4.2 with 1024,
-// which issue twice the instructions.  Before a second launch 512 are slower, outside a graph: 124 requests 9.9 and 7.9 us; 2000
-// requests 12.8 and 12.1.)
+// Threads of the scanning CTA: fewer where it does both parts for up to 512 requests.  (64 requests with a token
+// each 3.0 us with 512, 3.4 with 1024, which issue twice the instructions; with 11 tokens each 4.0 and 3.5.  Before a second launch
+// 512 are slower outside a graph: 124 requests 9.1 and 7.6 us, 2000 requests 12.6 and 11.5; in a graph 64 requests with 2656 rows
+// take 5.8 and 6.2, 2000 requests 12.0 and 11.0.)
 constexpr int kFewSeqs = 512, kScan = 1024;
 constexpr int kFillRows = 4, kFill = 256;  // rows of a thread at a time, threads of a CTA of the second part
 constexpr int kKept = 2048;                // requests whose prefix sums a CTA of the second part keeps
@@ -246,9 +248,9 @@ __global__ void __launch_bounds__(kFill) kv_pages_fill_kernel(PagesArgs a) {
 
 }  // namespace
 
-// One launch while a thread has few rows (64 requests with 704 rows 4.0 us, in two 5.8; 1024 threads with 2656 rows 6.6 and 7.2, 7856
-// rows 11.5 and 7.2); in two, the sums in shared memory while they fit it beside 7 other CTAs' (7856 rows 7.2 us, without 8.4;
-// 2000 requests 12.1 and 13.6).
+// One launch while a thread has few rows (64 requests with 704 rows 4.0 us, in two 6.3; with 2656 rows 7.3 in one and 6.2 in two, with
+// 7856 15.6 and 6.3); in two, the sums in shared memory while they fit it beside 7 other CTAs' (7856 rows 6.3 us, without 7.4;
+// 2000 requests 11.0 and 12.5).
 cudaError_t launch_kv_pages(const PagesArgs& a, cudaStream_t s) {
     const bool few = a.n <= kFewSeqs;
     if (a.n <= kScan && a.rows <= 4 * (few ? kFewSeqs : kScan)) {

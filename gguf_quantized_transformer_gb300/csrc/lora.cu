@@ -8,11 +8,14 @@
 //    warps' sums join in shared memory, the ranges' sums by their reader, both in order.
 //  - expand: y = base + B (scale h).  A CTA takes runs of 128 columns of one tile after another; h's parts lie in shared memory as
 //    operands, a warp's 16 columns of B and their part of the base come through its ring, y is written in 16-byte pieces.
-// Bound by the bytes of base, y and x for many rows (2048 rows of 5 fp16 adapters of rank 32 beside 4096 -> 28672 98 us, 5.2
-// TB/s), by two rounds of loads and a join in each kernel for few (one row of rank 16 beside 4096 -> 4096 4.5 us; 40 rows of 12
-// fp32 adapters of rank 64 beside 14336 -> 4096 17.0 us for 39 MB; 64 rows of 40 of rank 16 beside 4096 -> 6144 12.3 us, in
-// expand by its instructions: runs of 16 columns a warp for one or two rows).  Expand starts while shrink runs: what shrink does
-// not write (the plan, B, the base) is fetched before its wait, which takes 0.7 us of a row's time.
+// Bound by the bytes of base, y and x for many rows of low rank (2048 rows of 5 fp16 adapters of rank 32 beside 4096 -> 28672 97 us,
+// 5.3 TB/s), by two rounds of loads and a join in each kernel for few (one row of rank 16 beside 4096 -> 4096 4.9 us; 40 rows of
+// 12 fp32 adapters of ranks 16 to 64 beside 14336 -> 4096 17.6 us for 39 MB; 64 rows of 40 of rank 16 beside 4096 -> 6144 12.6 us,
+// in expand by its instructions: runs of 16 columns a warp for one or two rows).  Many rows of high rank or fp32 weights are bound
+// by the weights, which are fetched from L2 and split again for every 32 rows (512 rows of one fp16 adapter of rank 128 beside
+// 4096 -> 14336 37 us, 10.6 of them bytes; 2048 rows of 5 fp32 adapters of rank 64 beside 14336 -> 4096 100 us, 31 of them).
+// Expand starts while shrink runs: what shrink does not write (the plan, B, the base) is fetched before its wait.  (All figures
+// here and below are of calls in a graph.)
 // Precision: fp16 products of two parts of 11 bits (x, h and fp32 weights; fp16 weights are operands as they are), after a power
 // of two has brought the largest of a row's 32 values (of a chunk; of h all) to [2^13, 2^14), or [2^13, 2^15] with fp32 weights:
 // 2^-22 of a value or half of fp16's smallest step of 2^-24, which is 2^-38 of the largest, stays.  The product of two low parts
@@ -32,8 +35,8 @@ namespace {
 constexpr int kPlanThreads = 1024;
 constexpr int kThreads = 256, kWarps = kThreads / 32;  // of expand
 // Warps of a CTA of shrink and the bytes of a warp's ring.  (fp16 of rank 16: as little shared memory as lets expand's CTAs in
-// beside it: one row, 4096 -> 4096, 6.3 us; with 12 warps of 16 KB 6.9.  Higher ranks: as much as there is, 2048 rows of fp32
-// adapters of rank 64 101 us, with 8 warps 107.)
+// beside it: one row, 4096 -> 4096, 4.8 us; with 12 warps of 16 KB 5.6.  Higher ranks: as much as there is, 2048 rows of fp32
+// adapters of rank 64 100 us, with 8 warps 104; 64 rows of 4 fp16 adapters of rank 64 go the other way, 17.1 and 16.0.)
 template <bool F16, int MT>
 constexpr int kShrinkWarps = F16 && MT == 1 ? 8 : 12;
 template <bool F16, int MT>
@@ -161,7 +164,8 @@ __device__ __forceinline__ int rank_of(const LoraArgs& a, int adapter) {
 // ---------------------------------------------------------------- shrink
 
 // Ranges of K: as many as every SM takes one of at once, of at least two chunks of 32 for each warp (64 rows of 4 fp16
-// adapters of rank 64 beside 4096 -> 28672: 16.6 us; with three 17.6, with one, more to add up in expand, 16.8)
+// adapters of rank 64 beside 4096 -> 28672: 17.1 us; with three 18.2, with one, more to add up in expand, 18.1; one row 4.8, 5.3
+// and 5.1)
 __device__ __forceinline__ int lora_splits(int items, int K, int sms, int warps) {
     return max(1, min(min(sms / max(items, 1), kMaxSplit), K / 32 / (2 * warps)));
 }
@@ -348,7 +352,7 @@ __global__ void __launch_bounds__(kShrinkWarps<F16, MT> * 32, 1) lora_shrink_ker
         const uint8_t* w = (const uint8_t*)a.a + ((int64_t)tile.x * a.rank + r0) * a.K * es;
         const int c0 = (int)((int64_t)chunks * split / splits), c1 = (int)((int64_t)chunks * (split + 1) / splits);
         const uint32_t ring = smem_u32(sm_sum) + warp * RING;
-        // (few rows as 32: 40 rows of 12 fp32 adapters 25.3 us in place of 17.8)
+        // (few rows as 32: 40 rows of 12 fp32 adapters 24.7 us in place of 17.7, one row 6.0 in place of 4.8)
         if (tile.z <= 8)
             shrink_tile<F16, MT, 1>(a, row, tile.z, w, rank - r0, c0, c1, ring, sm_sum, PAD);
         else
@@ -429,8 +433,8 @@ __global__ void __launch_bounds__(kThreads, CTAS) lora_expand_kernel(LoraArgs a,
     const int tiles = !fits ? 0 : a.base && a.base == a.y ? head.y : head.x;  // in place, rows without an adapter stay as they are
     const int rows = head.z, splits = lora_splits(head.y * ((a.rank + rr - 1) / rr), a.K, sms, rr == 16 ? kShrinkWarps<F16, 1> : kShrinkWarps<F16, 2>), cols = (a.N + kCols - 1) / kCols;
     // The CTA's share: an equal one of all runs, the first CTAs one more, since they start first.  (Shares of one tile each save a
-    // second preparation but not the time: 64 rows of 40 adapters 15.2 us in place of 14.7, 40 rows of 12 17.7 in place of 17.0,
-    // though 512 rows of one adapter 35.3 in place of 36.8.)
+    // second preparation but not the time: 64 rows of 40 adapters took 0.5 us more, 40 rows of 12 0.7, 512 rows of one adapter 1.5
+    // less.)
     const int64_t items = (int64_t)tiles * cols;
     const int ctas = gridDim.x, me = blockIdx.x;
     const int64_t each = items <= INT32_MAX ? (int64_t)((unsigned)items / (unsigned)ctas) : items / ctas, rest = items - each * ctas;
@@ -662,8 +666,8 @@ __global__ void __launch_bounds__(kThreads, CTAS) lora_expand_kernel(LoraArgs a,
     __threadfence();  // (and no early launch of the next kernel: y may be a cache, see launch_chained)
 }
 
-// Ranks of an item of shrink.  (2048 rows of fp32 adapters of rank 64 101 us, in items of 16 129: x is read once an item; one row of
-// rank 16 in items of 32 0.9 us more.)
+// Ranks of an item of shrink.  (2048 rows of fp32 adapters of rank 64 100 us, in items of 16 132: x is read once an item; one row of
+// rank 16 4.8 us, in items of 32 5.9.)
 int shrink_ranks(int rank) { return rank <= 16 ? 16 : 32; }
 
 template <bool F16, int MT>
@@ -684,7 +688,9 @@ cudaError_t expand_go(const LoraArgs& a, int max_tiles, int smem, cudaStream_t s
 }
 
 // Two CTAs to an SM where their rings fit it, with three runs on their way if those fit, else with two (64 rows of 4 fp16
-// adapters of rank 64 beside 4096 -> 28672: 19.7 us; one CTA with two 22.0; four runs where they fit are no faster).  Two of
+// adapters of rank 64 beside 4096 -> 28672: 17.1 us; one CTA with two runs 19.0; 2048 rows of 5 of rank 32 97 and 117.  Four runs
+// where they fit are no faster; two everywhere give 92.6 for those 2048 rows, 38.0 in place of 37.5 for 512 of rank 128, and the
+// same for the others).  Two of
 // one CTA's fit for every rank (128 fp32: 176 KB).
 template <bool F16, int V, bool VEC>
 cudaError_t expand(const LoraArgs& a, int max_tiles, cudaStream_t s) {
@@ -705,7 +711,7 @@ cudaError_t lora(const LoraArgs& a, cudaStream_t s) {
     cudaError_t e = rr == 16 ? shrink<F16, 1>(a, tiles, s) : shrink<F16, 2>(a, tiles, s);
     if (e) return e;
     const bool vec = a.N % 4 == 0 && a.ldy % 4 == 0 && (uintptr_t)a.y % 16 == 0 && (!a.base || (a.ldb % 4 == 0 && (uintptr_t)a.base % 16 == 0));
-    // as many ranks a step as divide the rank (rank 64 by 8: 40 rows of 12 fp32 adapters 20.6 us in place of 17.8)
+    // as many ranks a step as divide the rank (rank 64 by 8: 40 rows of 12 fp32 adapters 21.7 us in place of 17.7)
     if (a.rank % 32 == 0) return expand<F16, 4>(a, tiles, vec, s);
     if (a.rank % 16 == 0) return expand<F16, 2>(a, tiles, vec, s);
     return expand<F16, 1>(a, tiles, vec, s);
