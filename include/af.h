@@ -291,7 +291,10 @@ int af_attention_decode(const float* q_dev, const void* k_dev, const void* v_dev
  * serving loop that cannot take the device-wide synchronisation of cudaFree,
  * or one whose memory is all handed to its own pool).  Same arguments, same
  * kernel and same result as af_attention_decode, but stream-ordered: it does
- * not synchronise `stream`.
+ * not synchronise `stream`.  Slots before pos are read ahead of the end of the
+ * kernel before it: what af_kv_write, af_kv_read, af_rope, af_lora and
+ * af_attention_paged have written into the cache is seen; a result of another
+ * call of this header that lies in those slots may not be.
  * Scratch: one file-scope device array of this library (4 MiB of split
  * partials + 1024 arrival counters + an error word), used only when ctx >
  * 2048 (shorter caches take the cluster path, which merges in distributed
